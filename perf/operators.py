@@ -1,0 +1,496 @@
+"""Work that the 8-bit KV cache and the eviction of COLD tokens do, as cases to be timed and compared.
+
+Four operators over a cache whose rows are packed in 8 bits (e4m3 codes of all KV heads, then one
+fp32 scale for each head, the row padded to 16 bytes) or held in 16 bits:
+
+  write   K/V of new tokens into the 8-bit cache: a prefix slab (one scale for each block of 64
+          tokens and head) or single tokens at their COLD slots (one scale for each token and head)
+  decode  decode-step attention over the 8-bit cache: shared prefix slabs, then each request's
+          COLD tokens through its token table; o and lse
+  weigh   the attention weight that each COLD token of a request received in a step, summed over
+          the query heads
+  evict   the least weighted tokens leave the token table: the rest close up, and the slots of
+          those that left are returned
+
+``run`` computes them from elementary torch operations in fp32, or with the library's calls where
+``own`` is true.
+"""
+
+import math
+import random
+
+import torch
+
+own = False
+
+BLOCK = 64            # tokens of a slab block that share a head's scale
+E4M3_MAX = 448.0
+AMAX_MIN = 2.0 ** -96  # smallest amax a scale is made for
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+# ---- cases ------------------------------------------------------------------------------------
+
+def listed():
+    head = {"n_q": 32, "n_kv": 8, "d": 128, "dtype": "bf16"}
+    return [
+        # a 16K shared prefix admitted to its slab, one layer
+        {"name": "write_prefix_16k", "op": "write", "kind": "slab", "tokens": 16384, **head},
+        # the new tokens of one decode step of 64 requests
+        {"name": "write_step_64", "op": "write", "kind": "cold", "tokens": 64, **head},
+        # an fp32 prefix of odd length with 64-dim heads
+        {"name": "write_prefix_f32", "op": "write", "kind": "slab", "tokens": 1501, "n_q": 8, "n_kv": 2, "d": 64, "dtype": "f32"},
+        # one agent alone on a long prefix: latency
+        {"name": "decode_one", "op": "decode", "prefixes": "8192", "B": 1, "suffix": "uniform", "lo": 200, "hi": 300, **head},
+        # 64 agents on one 16K prefix, chat-like suffixes
+        {"name": "decode_one_prefix_64", "op": "decode", "prefixes": "16384", "B": 64, "suffix": "lognormal", "lo": 32, "hi": 2048, **head},
+        # 128 agents on one 16K prefix, five query heads a KV head
+        {"name": "decode_one_prefix_128", "op": "decode", "prefixes": "16384", "B": 128, "suffix": "uniform", "lo": 64, "hi": 1024, **head, "n_q": 40},
+        # eight ragged prefixes, 160 agents
+        {"name": "decode_eight_prefixes", "op": "decode", "prefixes": "2048,3001,5000,7777,9216,11111,14000,16384", "B": 160, "suffix": "lognormal", "lo": 32, "hi": 2048, **head},
+        # fp32, small heads, a ragged prefix
+        {"name": "decode_f32", "op": "decode", "prefixes": "1500", "B": 48, "suffix": "uniform", "lo": 1, "hi": 80, "n_q": 8, "n_kv": 2, "d": 64, "dtype": "f32"},
+        # chat-like suffixes of 64 agents, 16-bit cache
+        {"name": "weigh_64", "op": "weigh", "cache": "bf16", "B": 64, "suffix": "lognormal", "lo": 32, "hi": 2048, "keep": 1.0, **head},
+        # a prefix that found no slab: long COLD rows, 8-bit cache
+        {"name": "weigh_long", "op": "weigh", "cache": "kv8", "B": 16, "suffix": "uniform", "lo": 12000, "hi": 16000, "keep": 0.0, **head},
+        # 64 agents over budget, a quarter of their tokens leaves
+        {"name": "evict_64", "op": "evict", "B": 64, "lo": 512, "hi": 2048, "share": 0.25, "first": 4, "last": 32, "cap": 4096},
+        # a few long rows
+        {"name": "evict_long", "op": "evict", "B": 4, "lo": 40000, "hi": 65536, "share": 0.5, "first": 16, "last": 256, "cap": 65536},
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["write", "decode", "decode", "weigh", "evict"])
+    heads = rng.choice([(1, 1), (8, 2), (16, 8), (32, 8), (40, 8), (16, 4), (24, 8), (64, 8)])
+    head = {"n_q": heads[0], "n_kv": heads[1], "d": 128, "dtype": "bf16"}
+    if op == "write":
+        kind = rng.choice(["slab", "cold"])
+        if rng.random() < 0.3:
+            head = {"n_q": 8, "n_kv": 2, "d": rng.choice([32, 64, 96]), "dtype": "f32"}
+        return {"op": op, "kind": kind, "tokens": _log(rng, 1, 16384 if kind == "slab" else 4096), **head}
+    if op == "decode":
+        if rng.random() < 0.2:
+            head = {"n_q": 8, "n_kv": 2, "d": rng.choice([32, 64, 128]), "dtype": "f32"}
+            n = rng.choice([1, 2])
+            top, many, tail = 3000, 64, 300
+        else:
+            n = rng.choice([0, 1, 1, 2, 3, 6])
+            top, many, tail = 16384, 160, 2048
+        prefixes = ",".join(str(_log(rng, 16, top // max(1, n // 2))) for _ in range(n))
+        hi = _log(rng, 1, tail)
+        return {"op": op, "prefixes": prefixes, "B": _log(rng, max(1, n), many), "suffix": "uniform", "lo": rng.choice([0 if n else 1, 1, max(1, hi // 2)]), "hi": hi, **head}
+    if op == "weigh":
+        hi = _log(rng, 1, 16000)
+        return {"op": op, "cache": rng.choice(["bf16", "kv8"]), "B": _log(rng, 1, max(1, min(128, 200000 // hi))), "suffix": "uniform", "lo": max(1, hi // 3), "hi": hi, "keep": rng.choice([0.0, 1.0, 0.9]), **head}
+    hi = _log(rng, 8, 65536)
+    return {"op": op, "B": _log(rng, 1, max(1, min(256, 260000 // hi))), "lo": max(1, hi // 4), "hi": hi, "share": rng.choice([0.01, 0.1, 0.25, 0.5, 0.9]), "first": rng.choice([0, 1, 4, 16]), "last": rng.choice([0, 1, 32, 256]), "cap": hi + rng.choice([0, 1, 500])}
+
+
+def _row_bytes(case):
+    """Bytes of one slot of the 8-bit cache: codes, scales, padding to 16."""
+    return (case["n_kv"] * (case["d"] + 4) + 15) // 16 * 16
+
+
+def _layout(case):
+    """The lengths of a case, the same for every seed: (prefix lengths, prefix of each request, COLD tokens of each)."""
+    rng = random.Random("lengths of %s" % sorted((k, v) for k, v in case.items() if k != "name"))
+    prefixes = [int(x) for x in str(case.get("prefixes", "")).split(",") if x]
+    B = case["B"]
+    of = [b % len(prefixes) if prefixes else -1 for b in range(B)]
+    lens = []
+    for _ in range(B):
+        if case.get("suffix") == "lognormal":
+            n = int(round(math.exp(rng.gauss(math.log(300.0), 1.0))))
+            n = min(max(n, case["lo"]), case["hi"])
+        else:
+            n = rng.randint(case["lo"], case["hi"])
+        lens.append(n)
+    return prefixes, of, lens
+
+
+def _leaving(case):
+    """(tokens of each row, tokens that leave it, tokens kept at its start)."""
+    _, _, lens = _layout(case)
+    first = [min(case["first"], n) for n in lens]
+    free = [max(0, n - f - case["last"]) for n, f in zip(lens, first)]
+    return lens, [min(m, int(n * case["share"])) for n, m in zip(lens, free)], first
+
+
+def work(case):
+    op = case["op"]
+    if op == "write":
+        n = case["tokens"] * case["n_kv"] * case["d"]
+        width = 2 if case["dtype"] == "bf16" else 4
+        scales = case["n_kv"] * 4 * (case["tokens"] if case["kind"] == "cold" else -(-case["tokens"] // BLOCK))
+        return {"bytes": 2 * (n * width + n + scales), "flops": 2 * 3 * n}
+    if op == "evict":
+        lens, out, _ = _leaving(case)
+        return {"bytes": sum(4 * n + 12 * (n - e) + 8 * e for n, e in zip(lens, out)), "flops": sum(lens)}
+    prefixes, of, lens = _layout(case)
+    q = case["B"] * case["n_q"] * case["d"] * (2 if case["dtype"] == "bf16" else 4)
+    lse = case["B"] * case["n_q"] * 4
+    if op == "decode":
+        row = case["n_kv"] * case["d"]
+        slab = sum(2 * L * row + 2 * -(-L // BLOCK) * 4 * case["n_kv"] for L in prefixes)
+        cold = sum(lens) * (2 * (row + 4 * case["n_kv"]) + 4)
+        keys = sum(n + (prefixes[p] if p >= 0 else 0) for n, p in zip(lens, of))
+        return {"bytes": slab + cold + 2 * q + lse, "flops": 4 * case["d"] * case["n_q"] * keys}
+    row = case["n_kv"] * (2 * case["d"] if case["cache"] == "bf16" else case["d"] + 4)
+    return {"bytes": sum(lens) * (row + 4 + 4 + (4 if case["keep"] else 0)) + q + lse, "flops": 2 * case["d"] * case["n_q"] * sum(lens)}
+
+
+# ---- inputs -----------------------------------------------------------------------------------
+
+def _normal(gen, *shape, dtype=torch.float32, scale=1.0):
+    return (torch.randn(*shape, generator=gen, device="cuda") * scale).to(dtype)
+
+
+def _heads_apart(gen, n, n_kv, d, dtype):
+    """K or V as projections give them: a few channels of each head far larger than the rest."""
+    x = torch.randn(n, n_kv, d, generator=gen, device="cuda")
+    channel = torch.exp(0.5 * torch.randn(n_kv, d, generator=gen, device="cuda"))
+    return (x * channel).to(dtype)
+
+
+def _codes(pool, n_kv, d):
+    return pool[..., : n_kv * d].view(torch.float8_e4m3fn)
+
+
+def _scales(pool, n_kv, d):
+    return pool[..., n_kv * d : n_kv * (d + 4)].view(torch.float32)
+
+
+def _write_plain(x, per_block):
+    """Codes [n, n_kv, d] and scales [n, n_kv] of K or V rows: the scale is the largest finite magnitude over 448."""
+    n, n_kv, d = x.shape
+    x = x.float()
+    size = x.abs()
+    amax = torch.where(torch.isfinite(size), size, torch.zeros_like(size)).amax(dim=2)
+    if per_block:
+        blocks = -(-n // BLOCK)
+        full = torch.zeros(blocks * BLOCK, n_kv, device=x.device)
+        full[:n] = amax
+        amax = full.view(blocks, BLOCK, n_kv).amax(dim=1).repeat_interleave(BLOCK, dim=0)[:n]
+    amax = amax.clamp(min=AMAX_MIN)
+    codes = (x * (E4M3_MAX / amax)[..., None]).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
+    return codes, amax / E4M3_MAX
+
+
+def _store(pool, at, x, per_block):
+    """Writes the rows of x to the pool's slots `at` (a slice or slot ids)."""
+    n, n_kv, d = x.shape
+    codes, scales = _write_plain(x, per_block)
+    pool[at, : n_kv * d] = codes.view(torch.uint8).reshape(n, n_kv * d)
+    pool[at, n_kv * d : n_kv * (d + 4)] = scales.view(torch.uint8).reshape(n, n_kv * 4)
+
+
+def prepare(case, seed):
+    gen = torch.Generator("cuda").manual_seed(int(seed))
+    s = {"case": case}
+    if case["op"] == "evict":
+        return _prepare_evict(case, gen, s)
+    n_q, n_kv, d, dtype = case["n_q"], case["n_kv"], case["d"], DTYPES[case["dtype"]]
+    if case["op"] == "write":
+        n = case["tokens"]
+        n_hot = n if case["kind"] == "slab" else 0
+        n_slots = n + 2 if case["kind"] == "slab" else 4 * n + 2
+        s["k"], s["v"] = _heads_apart(gen, n, n_kv, d, dtype), _heads_apart(gen, n, n_kv, d, dtype)
+        s["slots"] = torch.randperm(n_slots, generator=gen, device="cuda")[:n].to(torch.int32)
+        kv8 = True
+        k_pool, v_pool = (torch.zeros(n_slots, _row_bytes(case), dtype=torch.uint8, device="cuda") for _ in range(2))
+        lens, n_hot_lens = [], [n] if n_hot else []
+    else:
+        prefixes, of, lens = _layout(case)
+        kv8 = case["op"] == "decode" or case["cache"] == "kv8"
+        n_hot = sum(prefixes)
+        cold = sum(lens)
+        n_slots = n_hot + cold + 2
+        n_hot_lens = prefixes
+        shape = (n_slots, _row_bytes(case)) if kv8 else (n_slots, n_kv, d)
+        k_pool, v_pool = (torch.zeros(shape, dtype=torch.uint8 if kv8 else dtype, device="cuda") for _ in range(2))
+        for pool in (k_pool, v_pool):
+            at = 0
+            for L in prefixes:
+                _store(pool, slice(at, at + L), _heads_apart(gen, L, n_kv, d, dtype), True)
+                at += L
+            for i in range(0, cold, 16384):
+                x = _heads_apart(gen, min(16384, cold - i), n_kv, d, dtype)
+                if kv8:
+                    _store(pool, slice(n_hot + i, n_hot + i + x.shape[0]), x, False)
+                else:
+                    pool[n_hot + i : n_hot + i + x.shape[0]] = x
+        cap = max(max(lens), 1)
+        order = (n_hot + torch.randperm(cold, generator=gen, device="cuda")).to(torch.int32)
+        s["lens"] = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        s["table"] = torch.zeros(case["B"], cap, dtype=torch.int32, device="cuda")
+        live = torch.arange(cap, device="cuda")[None] < s["lens"][:, None]
+        s["table"][live] = order
+        s["of"], s["prefixes"] = of, prefixes
+        s["q"] = _normal(gen, case["B"], n_q, d, dtype=dtype, scale=1.0 / math.sqrt(d))
+        if case["op"] == "weigh":
+            k, own_keys = _gathered(s, k_pool, kv8)
+            scores = _scores(s["q"].float(), k) / math.sqrt(d)
+            s["lse"] = torch.logsumexp(scores.masked_fill(~own_keys[:, None], -math.inf), dim=2)
+            del k, scores
+            s["before"] = torch.rand(case["B"], cap, generator=gen, device="cuda")
+            s["weight"] = s["before"].clone()
+        else:
+            s["o"] = torch.empty_like(s["q"])
+            s["lse"] = torch.empty(case["B"], n_q, dtype=torch.float32, device="cuda")
+            s["members"] = [torch.tensor([b for b, p in enumerate(of) if p == i], device="cuda") for i in range(len(prefixes))]
+    s["k_pool"], s["v_pool"], s["kv8"] = k_pool, v_pool, kv8
+    if own:
+        import shared_prefix_kv_decode_gb300 as G
+
+        ctx = s["ctx"] = G.Context(
+            n_layers=1, n_q=n_q, n_kv=n_kv, head_dim=d, dtype=G.DTYPE_BF16 if case["dtype"] == "bf16" else G.DTYPE_F32,
+            n_slots=n_slots, k_pools=[k_pool], v_pools=[v_pool], hot_fraction=(n_hot + 0.5) / n_slots, max_batch=max(1, case.get("B", 1)),
+            device=torch.cuda.current_device(), kv8=kv8)
+        s["slabs"] = [ctx.hot_alloc(L)[0] for L in n_hot_lens]
+        if lens:
+            s["batch"] = G.Batch([s["slabs"][p] if p >= 0 else -1 for p in of], lens, s["table"], s["table"].shape[1], s["lens"])
+        if case["op"] == "decode":
+            s["plan"] = ctx.dispatch(s["batch"])
+            s["ws"] = torch.empty(ctx.workspace_size(s["plan"]), dtype=torch.uint8, device="cuda")
+    return s
+
+
+def _prepare_evict(case, gen, s):
+    lens, out, first = _leaving(case)
+    B, cap = case["B"], case["cap"]
+    s["lens"] = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    s["out"] = torch.tensor(out, dtype=torch.int32, device="cuda")
+    s["first"] = torch.tensor(first, dtype=torch.int32, device="cuda")
+    # weights as a softmax leaves them, summed over steps: a few tokens hold most, and some are equal
+    w = torch.exp(2.5 * torch.randn(B, cap, generator=gen, device="cuda") - 6.0)
+    some = torch.rand(B, cap, generator=gen, device="cuda") < 0.05
+    s["weight0"] = torch.where(some, torch.zeros_like(w), w)
+    s["table0"] = torch.randint(2, 1 << 30, (B, cap), generator=gen, device="cuda", dtype=torch.int32)
+    s["table"], s["weight"] = s["table0"].clone(), s["weight0"].clone()
+    s["len"] = s["lens"].clone()
+    s["slots"] = torch.zeros(max(1, sum(out)), dtype=torch.int32, device="cuda")
+    if own:
+        import shared_prefix_kv_decode_gb300 as G
+
+        pool = s["pool"] = torch.zeros(64, dtype=torch.uint8, device="cuda")
+        s["ctx"] = G.Context(
+            n_layers=1, n_q=1, n_kv=1, head_dim=32, dtype=G.DTYPE_BF16, n_slots=2, k_pools=[pool], v_pools=[pool], hot_fraction=0.25, max_batch=B,
+            device=torch.cuda.current_device())
+        s["counts"] = (G.int32_array(lens), G.int32_array(out), G.int32_array(first))
+    return s
+
+
+# ---- one pass ---------------------------------------------------------------------------------
+
+def run(state):
+    return (_run_own if own else _run_plain)[state["case"]["op"]](state)
+
+
+def _own_write(s):
+    c = s["case"]
+    stream = torch.cuda.current_stream()
+    if c["kind"] == "slab":
+        s["ctx"].hot_fill(0, s["slabs"][0], s["k"], s["v"], stream)
+    else:
+        s["ctx"].cold_append(0, s["k"], s["v"], s["slots"], c["tokens"], stream)
+    return _pools_out(s)
+
+
+def _own_decode(s):
+    s["ctx"].decode_attention(0, s["q"], s["batch"], s["plan"], s["o"], s["lse"], s["ws"], s["ws"].numel(), torch.cuda.current_stream())
+    return s["o"], s["lse"]
+
+
+def _own_weigh(s):
+    if s["case"]["keep"]:
+        s["weight"].copy_(s["before"])
+    s["ctx"].cold_weigh(0, s["q"], s["lse"], s["batch"], s["weight"], s["case"]["keep"], torch.cuda.current_stream())
+    return s["weight"]
+
+
+def _own_evict(s):
+    s["table"].copy_(s["table0"])
+    s["weight"].copy_(s["weight0"])
+    lens, out, first = s["counts"]
+    s["ctx"].cold_evict(lens, out, first, s["case"]["last"], s["table"], s["len"], s["weight"], s["case"]["cap"], s["slots"], torch.cuda.current_stream())
+    return s["table"], s["weight"], s["len"], s["slots"]
+
+
+def _pools_out(s):
+    c = s["case"]
+    return {
+        "k": _codes(s["k_pool"], c["n_kv"], c["d"]), "k_scale": _scales(s["k_pool"], c["n_kv"], c["d"]),
+        "v": _codes(s["v_pool"], c["n_kv"], c["d"]), "v_scale": _scales(s["v_pool"], c["n_kv"], c["d"])}
+
+
+def _plain_write(s):
+    c = s["case"]
+    slab = c["kind"] == "slab"
+    at = slice(0, c["tokens"]) if slab else s["slots"].long()
+    _store(s["k_pool"], at, s["k"], slab)
+    _store(s["v_pool"], at, s["v"], slab)
+    return _pools_out(s)
+
+
+def _values(rows, n_kv, d):
+    """fp32 values of packed 8-bit rows [..., row bytes] -> [..., n_kv, d]."""
+    rows = rows.contiguous()
+    lead = rows.shape[:-1]
+    return _codes(rows, n_kv, d).float().reshape(*lead, n_kv, d) * _scales(rows, n_kv, d).reshape(*lead, n_kv, 1)
+
+
+def _gathered(s, pool, kv8):
+    """Each request's COLD rows [B, cap, n_kv, d] in fp32, and which of them it owns [B, cap]."""
+    c = s["case"]
+    live = torch.arange(s["table"].shape[1], device="cuda")[None] < s["lens"][:, None]
+    rows = pool[torch.where(live, s["table"], s["table"].new_zeros(())).long()]
+    return (_values(rows, c["n_kv"], c["d"]) if kv8 else rows.float()), live
+
+
+def _scores(q, k):
+    """q [B, n_q, d], k [B, L, n_kv, d] -> [B, n_q, L]."""
+    B, n_q, d = q.shape
+    n_kv = k.shape[2]
+    x = torch.matmul(q.view(B, n_kv, n_q // n_kv, d), k.permute(0, 2, 3, 1))
+    return x.reshape(B, n_q, -1)
+
+
+def _plain_decode(s):
+    c = s["case"]
+    n_q, n_kv, d, B = c["n_q"], c["n_kv"], c["d"], c["B"]
+    g = n_q // n_kv
+    q = s["q"].float()
+    # the COLD tokens
+    k, live = _gathered(s, s["k_pool"], True)
+    x = (_scores(q, k) / math.sqrt(d)).masked_fill(~live[:, None], -math.inf)
+    top = x.amax(dim=2)
+    at = 0
+    parts = []
+    for L, who in zip(s["prefixes"], s["members"]):
+        rows = slice(at, at + L)
+        at += L
+        if who.numel():
+            kp = _values(s["k_pool"][rows], n_kv, d)
+            qg = q[who].view(-1, n_kv, g, d).transpose(0, 1).reshape(n_kv, -1, d)
+            xp = torch.matmul(qg, kp.permute(1, 2, 0)) / math.sqrt(d)
+            peak = xp.amax(dim=2).view(n_kv, -1, g).transpose(0, 1).reshape(-1, n_q)
+            top[who] = torch.maximum(top[who], peak)
+            parts.append((rows, who, xp))
+    x = torch.exp(x - top[..., None])
+    total = x.sum(dim=2)
+    v, _ = _gathered(s, s["v_pool"], True)
+    o = torch.matmul(x.view(B, n_kv, g, -1), v.permute(0, 2, 1, 3)).reshape(B, n_q, d)
+    for rows, who, xp in parts:
+        m = top[who].view(-1, n_kv, g).transpose(0, 1).reshape(n_kv, -1, 1)
+        w = torch.exp(xp - m)
+        vp = _values(s["v_pool"][rows], n_kv, d)
+        total[who] += w.sum(dim=2).view(n_kv, -1, g).transpose(0, 1).reshape(-1, n_q)
+        o[who] += torch.matmul(w, vp.permute(1, 0, 2)).view(n_kv, -1, g, d).transpose(0, 1).reshape(-1, n_q, d)
+    s["o"].copy_(o / total[..., None])
+    s["lse"].copy_(top + torch.log(total))
+    return s["o"], s["lse"]
+
+
+def _plain_weigh(s):
+    c = s["case"]
+    k, live = _gathered(s, s["k_pool"], s["kv8"])
+    p = torch.exp(_scores(s["q"].float(), k) / math.sqrt(c["d"]) - s["lse"][..., None]).sum(dim=1)
+    before = s["before"]
+    return torch.where(live, c["keep"] * before + p if c["keep"] else p, before)
+
+
+def _plain_evict(s):
+    c = s["case"]
+    table, weight, n = s["table0"], s["weight0"], s["lens"][:, None]
+    pos = torch.arange(c["cap"], device="cuda")[None].expand_as(table)
+    free = (pos >= s["first"][:, None]) & (pos < n - c["last"])
+    # the lightest first, those that may not leave behind all others; equal ones by position
+    order = torch.argsort(torch.where(free, weight, torch.full_like(weight, math.inf)), dim=1, stable=True)
+    rank = torch.empty_like(order).scatter_(1, order, pos)
+    leaves = rank < s["out"][:, None]
+    stays = (pos < n) & ~leaves
+    to = torch.cumsum(stays, dim=1) - 1
+    new_table, new_weight = table.clone(), weight.clone()
+    r = torch.arange(c["B"], device="cuda")[:, None].expand_as(table)
+    new_table[r[stays], to[stays]] = table[stays]
+    new_weight[r[stays], to[stays]] = weight[stays]
+    gone = table[leaves]
+    if not gone.numel():
+        gone = s["slots"]
+    return new_table, new_weight, s["lens"] - s["out"], gone
+
+
+_run_own = {"write": _own_write, "decode": _own_decode, "weigh": _own_weigh, "evict": _own_evict}
+_run_plain = {"write": _plain_write, "decode": _plain_decode, "weigh": _plain_weigh, "evict": _plain_evict}
+
+
+# ---- 64-bit values ----------------------------------------------------------------------------
+
+def _e4m3_64(y):
+    """The nearest e4m3 value (ties to even) of finite doubles, saturated at 448."""
+    _, e = torch.frexp(y)
+    step = torch.ldexp(torch.ones_like(y), (e - 1).clamp(min=-6) - 3)
+    return (torch.round(y / step) * step).clamp(-E4M3_MAX, E4M3_MAX)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    op = case["op"]
+    if op == "evict":
+        weight = s["weight0"].double()
+        for b, (n, e, f) in enumerate(zip(*_leaving(case))):
+            w = weight[b, :n].tolist()
+            out = set(sorted(range(f, max(f, n - case["last"])), key=lambda i: (w[i], i))[:e])
+            weight[b, : n - e] = torch.tensor([x for i, x in enumerate(w) if i not in out], dtype=torch.float64, device="cuda")
+        return None, weight, None, None
+    n_q, n_kv, d = case["n_q"], case["n_kv"], case["d"]
+    if op == "write":
+        out = {}
+        for name in ("k", "v"):
+            x = s[name].double()
+            amax = x.abs().amax(dim=2)
+            if case["kind"] == "slab":
+                amax = torch.cat([part.amax(dim=0, keepdim=True).expand_as(part) for part in amax.split(BLOCK)])
+            scale = amax.clamp(min=AMAX_MIN) / E4M3_MAX
+            codes = torch.zeros(s["k_pool"].shape[0], n_kv * d, dtype=torch.float64, device="cuda")
+            scales = torch.zeros(s["k_pool"].shape[0], n_kv, dtype=torch.float64, device="cuda")
+            at = torch.arange(case["tokens"], device="cuda") if case["kind"] == "slab" else s["slots"].long()
+            codes[at] = _e4m3_64(x / scale[..., None]).flatten(1)
+            scales[at] = scale
+            out[name], out[name + "_scale"] = codes, scales
+        return out
+    start = [0]
+    for L in s["prefixes"]:
+        start.append(start[-1] + L)
+
+    def keys(pool, slots):
+        rows = pool[slots]
+        if not s["kv8"]:
+            return rows.double()
+        codes = rows[:, : n_kv * d].contiguous().view(torch.float8_e4m3fn).double().view(-1, n_kv, d)
+        return codes * rows[:, n_kv * d : n_kv * (d + 4)].contiguous().view(torch.float32).double()[..., None]
+
+    lens = s["lens"].tolist()
+    o = torch.zeros(case["B"], n_q, d, dtype=torch.float64, device="cuda")
+    lse = torch.zeros(case["B"], n_q, dtype=torch.float64, device="cuda")
+    weight = s["before"].double() if op == "weigh" else None
+    for b in range(case["B"]):
+        slots = s["table"][b, : lens[b]].long()
+        p = s["of"][b]
+        if op == "decode" and p >= 0:
+            slots = torch.cat([torch.arange(start[p], start[p + 1], device="cuda"), slots])
+        qb = s["q"][b].double().view(n_kv, n_q // n_kv, d)
+        x = torch.einsum("hgd,lhd->hgl", qb, keys(s["k_pool"], slots)) * d ** -0.5
+        if op == "weigh":
+            mass = torch.exp(x - s["lse"][b].double().view(n_kv, -1, 1)).sum(dim=(0, 1))
+            weight[b, : lens[b]] = case["keep"] * weight[b, : lens[b]] + mass
+            continue
+        lse[b] = torch.logsumexp(x, dim=2).flatten()
+        o[b] = torch.einsum("hgl,lhd->hgd", torch.softmax(x, dim=2), keys(s["v_pool"], slots)).reshape(n_q, d)
+    return weight if op == "weigh" else (o, lse)
