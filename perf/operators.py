@@ -420,6 +420,7 @@ def _plain_evict(s):
     r = torch.arange(c["B"], device="cuda")[:, None].expand_as(table)
     new_table[r[stays], to[stays]] = table[stays]
     new_weight[r[stays], to[stays]] = weight[stays]
+    new_weight[(pos < n) & (pos >= n - s["out"][:, None])] = 0.0  # the places left free start from nothing again
     gone = table[leaves]
     if not gone.numel():
         gone = s["slots"]
@@ -448,6 +449,7 @@ def exact(case, seed):
             w = weight[b, :n].tolist()
             out = set(sorted(range(f, max(f, n - case["last"])), key=lambda i: (w[i], i))[:e])
             weight[b, : n - e] = torch.tensor([x for i, x in enumerate(w) if i not in out], dtype=torch.float64, device="cuda")
+            weight[b, n - e : n] = 0.0
         return None, weight, None, None
     n_q, n_kv, d = case["n_q"], case["n_kv"], case["d"]
     if op == "write":
