@@ -125,6 +125,30 @@ int32_t granikv_version(void);
 granikv_status granikv_create(const granikv_config* cfg, granikv_ctx** out);
 granikv_status granikv_destroy(granikv_ctx* ctx);
 
+/* ---- 8-bit cache.  A context made by granikv_create_kv8 keeps K and V as e4m3 codes with an fp32
+ * scale for each block of tokens and KV head, in half the bytes of a bf16 pool.  (The paper keeps
+ * its cache in 16 bits; what is asked of the layout -- contiguous slabs, token-level COLD slots --
+ * is unchanged.)
+ *
+ * cfg->k_pool and v_pool are then byte pools [n_slots, row_bytes], row_bytes from
+ * granikv_kv8_row_bytes: one slot's row is n_kv * head_dim codes (head by head), n_kv float32
+ * scales, padding to a multiple of 16 bytes; value = code * scale.  cfg->dtype is the type of q, o
+ * and of the K/V rows given to granikv_hot_fill, granikv_cold_append and
+ * granikv_decode_attention_append, which quantise them:
+ *     scale = max(amax, 2^-96) / 448,   code = e4m3(x * (448 / max(amax, 2^-96))),
+ * both in float32, rounded to nearest even and saturated at +-448 (an infinity becomes +-448, a
+ * NaN stays one); amax is the largest finite magnitude of the head's elements over a block of
+ * tokens: 64 consecutive tokens of a slab, counted from its start (the last block may be
+ * shorter), whose rows all hold the block's scale, or one COLD token (page size 1).
+ * Those rows and q and o must start on 16-byte boundaries (GRANIKV_ERR_INVALID).
+ * granikv_dispatch, granikv_decode_attention (and its append and static forms),
+ * granikv_cold_weigh and the pool calls work on such a context as on any other;
+ * granikv_prefill_attention is GRANIKV_ERR_UNSUPPORTED (a prefix is prefilled in 16 bits and its
+ * K/V given to granikv_hot_fill), and granikv_set_fused_merge has no effect. ----------------- */
+granikv_status granikv_create_kv8(const granikv_config* cfg, granikv_ctx** out);
+/* Bytes of one slot's row; GRANIKV_ERR_UNSUPPORTED for a head_dim that granikv_create refuses. */
+granikv_status granikv_kv8_row_bytes(int32_t n_kv, int32_t head_dim, size_t* bytes);
+
 /* ---- HOT pool ("B.10 Cross-pool admission and promotion policy"; "B.8 Multi-prefix
  * sensitivity": first-fit packing of mixed slab sizes; card page: one slab per prefix node).
  * Host only, no device access. ------------------------------------------------------------- */
@@ -185,6 +209,43 @@ granikv_status granikv_cold_sync(granikv_ctx* ctx, granikv_stream_t stream);
 granikv_status granikv_cold_append(granikv_ctx* ctx, int32_t layer, const void* k_new,
                                    const void* v_new, const int32_t* slots, int32_t N,
                                    granikv_stream_t stream);
+
+/* ---- eviction of COLD tokens.  (No counterpart in the paper, whose COLD rows only grow; the
+ * token-level pool of "3 GraniKV", page size 1, is what lets single tokens leave.)  The caller
+ * keeps one weight per place of the token table, weight [B, cap] float32, zero for a new row;
+ * granikv_cold_weigh adds what each token received in a step, granikv_cold_evict takes the
+ * lightest tokens out, and granikv_cold_free takes the slots that it returns. -------------------- */
+
+/* weight[b, i] = keep * weight[b, i] + sum over the query heads h of exp(q[b,h].k_i * scale - lse[b,h])
+ * for i < min(seq_len[b], seq_len_dev[b]): the softmax weight of request b's COLD token i in one
+ * layer of the step that gave lse (granikv_decode_attention's, over prefix and COLD tokens),
+ * scale 1/sqrt(head_dim).  The other places are left as they are.  The sum is taken in a fixed
+ * order: the same inputs give the same bits.  keep = 1 accumulates over layers and steps; with
+ * keep = 0 the old weights are not read.  A head whose lse is -inf adds nothing.
+ *   q: device [B, n_q, head_dim] (dtype), 16-byte aligned;  lse: device [B, n_q] float32;
+ *   batch: seq_len_dev must be given (slab_id is not read);  weight: device [B, batch->cap].
+ * Safe to capture in a CUDA graph and replay.  GRANIKV_ERR_INVALID for keep < 0 or not finite.
+ * A slot outside [n_hot, n_slots) is a device check failure; its token's weight becomes keep * weight. */
+granikv_status granikv_cold_weigh(granikv_ctx* ctx, int32_t layer, const void* q, const float* lse,
+                                  const granikv_batch* batch, float* weight, float keep,
+                                  granikv_stream_t stream);
+/* Of row b's places [keep_first[b], seq_len[b] - keep_last) the n_evict[b] with the least weight
+ * leave: equal weights leave from the lowest place on, -0 and 0 are equal, a NaN counts as the
+ * largest.  The other tokens close up in order (req_to_slot and weight), the places
+ * [seq_len[b] - n_evict[b], seq_len[b]) get weight 0 (their table entries stay), and
+ * suffix_len[b] = seq_len[b] - n_evict[b].  slots_out receives the slots that left, row after row
+ * and in the rows' order, for granikv_cold_free (the shared slots of a prefix placed in COLD must
+ * lie below keep_first).  Rows B and beyond are not touched.
+ *   seq_len, n_evict: host [B];  keep_first: host [B] or NULL (0);  keep_last >= 0
+ *   req_to_slot: device [B, cap];  weight: device [B, cap] float32
+ *   suffix_len: device [B] or NULL;  slots_out: device [sum n_evict] (NULL if that is 0)
+ * GRANIKV_ERR_INVALID, with nothing changed, unless 0 <= seq_len[b] <= cap, keep_first[b] >= 0 and
+ * 0 <= n_evict[b] <= max(0, seq_len[b] - keep_first[b] - keep_last) for every row.  Captured in a
+ * CUDA graph, the call replays with the host arrays' values at capture. */
+granikv_status granikv_cold_evict(granikv_ctx* ctx, const int32_t* seq_len, const int32_t* n_evict,
+                                  const int32_t* keep_first, int32_t keep_last, int32_t B,
+                                  int32_t* req_to_slot, int32_t* suffix_len, float* weight, int32_t cap,
+                                  int32_t* slots_out, granikv_stream_t stream);
 
 /* ---- prefix index ("2 Related Work", prefix-aware serving: a radix tree over token-id
  * sequences with reference-counted nodes; card page: one HOT slab per radix-tree prefix node;

@@ -92,6 +92,8 @@ _SIGNATURES = [
     ("granikv_status_string", C.c_char_p, [C.c_int32]),
     ("granikv_version", C.c_int32, []),
     ("granikv_create", C.c_int32, [C.POINTER(_Config), C.POINTER(C.c_void_p)]),
+    ("granikv_create_kv8", C.c_int32, [C.POINTER(_Config), C.POINTER(C.c_void_p)]),
+    ("granikv_kv8_row_bytes", C.c_int32, [C.c_int32, C.c_int32, C.POINTER(C.c_size_t)]),
     ("granikv_destroy", C.c_int32, [C.c_void_p]),
     ("granikv_hot_alloc", C.c_int32, [C.c_void_p, C.c_int32, C.POINTER(C.c_int32), C.POINTER(C.c_int64)]),
     ("granikv_hot_free", C.c_int32, [C.c_void_p, C.c_int32]),
@@ -107,6 +109,11 @@ _SIGNATURES = [
     ("granikv_cold_sync", C.c_int32, [C.c_void_p, C.c_void_p]),
     ("granikv_cold_append", C.c_int32, [C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p,
                                         C.c_int32, C.c_void_p]),
+    ("granikv_cold_weigh", C.c_int32, [C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p, C.POINTER(_Batch),
+                                       C.c_void_p, C.c_float, C.c_void_p]),
+    ("granikv_cold_evict", C.c_int32, [C.c_void_p, C.POINTER(C.c_int32), C.POINTER(C.c_int32),
+                                       C.POINTER(C.c_int32), C.c_int32, C.c_int32, C.c_void_p, C.c_void_p,
+                                       C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p]),
     ("granikv_index_create", C.c_int32, [C.c_void_p, C.POINTER(C.c_void_p)]),
     ("granikv_index_destroy", C.c_int32, [C.c_void_p]),
     ("granikv_index_match", C.c_int32, [C.c_void_p, C.POINTER(C.c_int32), C.c_int32, C.c_int32,
@@ -211,8 +218,23 @@ def _stream(s) -> Optional[int]:
 
 
 def _i32_array(values: Sequence[int]):
+    if isinstance(values, C.Array) and values._type_ is C.c_int32:
+        return values
     arr = (C.c_int32 * len(values))(*[int(v) for v in values])
     return arr
+
+
+def int32_array(values: Sequence[int]):
+    """Host int32 array that the calls taking host counts accept as it is (a list is converted at
+    every call)."""
+    return _i32_array(values)
+
+
+def kv8_row_bytes(n_kv: int, head_dim: int) -> int:
+    """Bytes of one slot of an 8-bit pool (granikv_kv8_row_bytes)."""
+    n = C.c_size_t()
+    _check(load_library().granikv_kv8_row_bytes(n_kv, head_dim, C.byref(n)), "granikv_kv8_row_bytes")
+    return n.value
 
 
 class Batch:
@@ -232,6 +254,13 @@ class Batch:
     @property
     def B(self) -> int:
         return self.c.B
+
+    def with_live(self, seq_len_dev) -> "Batch":
+        """The same batch with the device token counts `seq_len_dev` (the host arrays are shared)."""
+        out = object.__new__(Batch)
+        out._slab, out._len, out._table, out._live = self._slab, self._len, self._table, seq_len_dev
+        out.c = _Batch(self.c.B, self.c.slab_id, self.c.seq_len, self.c.req_to_slot, self.c.cap, _ptr(seq_len_dev))
+        return out
 
 
 class Plan:
@@ -367,7 +396,9 @@ class Context:
     def __init__(self, *, n_layers: int, n_q: int, n_kv: int, head_dim: int, dtype: int,
                  n_slots: int, k_pools=(), v_pools=(), hot_fraction: float = 0.2,
                  cold_init_order: Optional[Sequence[int]] = None, m_sat: int = 0,
-                 max_slabs: int = 0, max_batch: int = 0, device: int = 0, host_only: bool = False):
+                 max_slabs: int = 0, max_batch: int = 0, device: int = 0, host_only: bool = False,
+                 kv8: bool = False):
+        """kv8: an 8-bit cache (granikv_create_kv8); the pools are then bytes [n_slots, kv8_row_bytes(...)]."""
         self._lib = load_library()
         self._kp = (C.c_void_p * max(1, n_layers))(*[_ptr(p) for p in k_pools]) if k_pools else None
         self._vp = (C.c_void_p * max(1, n_layers))(*[_ptr(p) for p in v_pools]) if v_pools else None
@@ -378,9 +409,12 @@ class Context:
                       C.cast(self._order, C.POINTER(C.c_int32)) if self._order else None,
                       m_sat, max_slabs, max_batch, 1 if host_only else 0)
         h = C.c_void_p()
-        _check(self._lib.granikv_create(C.byref(cfg), C.byref(h)), "granikv_create")
+        if kv8:
+            _check(self._lib.granikv_create_kv8(C.byref(cfg), C.byref(h)), "granikv_create_kv8")
+        else:
+            _check(self._lib.granikv_create(C.byref(cfg), C.byref(h)), "granikv_create")
         self.handle = h
-        self.n_q, self.n_kv, self.head_dim, self.dtype = n_q, n_kv, head_dim, dtype
+        self.n_q, self.n_kv, self.head_dim, self.dtype, self.kv8 = n_q, n_kv, head_dim, dtype, kv8
         self._indexes = []
 
     def index(self) -> Index:
@@ -449,6 +483,24 @@ class Context:
     def cold_append(self, layer: int, k_new, v_new, slots, N: int, stream=None):
         _check(self._lib.granikv_cold_append(self.handle, layer, _ptr(k_new), _ptr(v_new), _ptr(slots), N,
                                              _stream(stream)), "granikv_cold_append")
+
+    # eviction of COLD tokens
+    def cold_weigh(self, layer: int, q, lse, batch: Batch, weight, keep: float = 1.0, stream=None):
+        """weight[b, i] = keep * weight[b, i] + the softmax weight COLD token i of request b received
+        from q in this layer, summed over the query heads; batch needs seq_len_dev."""
+        _check(self._lib.granikv_cold_weigh(self.handle, layer, _ptr(q), _ptr(lse), C.byref(batch.c), _ptr(weight),
+                                            keep, _stream(stream)), "granikv_cold_weigh")
+
+    def cold_evict(self, seq_len: Sequence[int], n_evict: Sequence[int], keep_first: Optional[Sequence[int]],
+                   keep_last: int, req_to_slot, suffix_len, weight, cap: int, slots_out, stream=None):
+        """The n_evict[b] lightest tokens of row b's places [keep_first[b], seq_len[b] - keep_last) leave;
+        slots_out receives their slots (see granikv_cold_evict in include/granikv.h)."""
+        if len(seq_len) != len(n_evict) or (keep_first is not None and len(keep_first) != len(seq_len)):
+            raise ValueError("seq_len, n_evict and keep_first differ in length")
+        _check(self._lib.granikv_cold_evict(self.handle, _i32_array(seq_len), _i32_array(n_evict),
+                                            _i32_array(keep_first) if keep_first is not None else None, keep_last,
+                                            len(seq_len), _ptr(req_to_slot), _ptr(suffix_len), _ptr(weight), cap,
+                                            _ptr(slots_out), _stream(stream)), "granikv_cold_evict")
 
     # dispatch
     def plan(self) -> Plan:

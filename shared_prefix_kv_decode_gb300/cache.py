@@ -18,31 +18,38 @@ _TORCH_DTYPE = {gb.DTYPE_F32: torch.float32, gb.DTYPE_BF16: torch.bfloat16}
 
 
 class GraniKVCache:
-    """Per-layer K/V pools [n_slots, n_kv, d], per-request COLD token tables, and a context."""
+    """Per-layer K/V pools [n_slots, n_kv, d], per-request COLD token tables, and a context.
+
+    kv8: the pools hold e4m3 codes with fp32 scales, one packed row of bytes a slot
+    (granikv_create_kv8); K and V are still given in `dtype`."""
 
     def __init__(self, *, n_layers: int, n_q: int, n_kv: int, head_dim: int, dtype: int,
                  n_slots: int, max_batch: int, cap: int, hot_fraction: float = 0.2,
                  cold_init_order: Optional[Sequence[int]] = None, m_sat: int = 0,
-                 device: int = 0, max_slabs: int = 0):
+                 device: int = 0, max_slabs: int = 0, kv8: bool = False):
         if not torch.cuda.is_available():
             raise RuntimeError("GraniKVCache needs a CUDA device")
         self.device = torch.device("cuda", device)
         self.tdtype = _TORCH_DTYPE[dtype]
         self.n_layers, self.n_q, self.n_kv, self.head_dim = n_layers, n_q, n_kv, head_dim
         self.dtype, self.n_slots, self.cap, self.max_batch = dtype, n_slots, cap, max_batch
+        self.kv8 = kv8
+        shape = (n_slots, gb.kv8_row_bytes(n_kv, head_dim)) if kv8 else (n_slots, n_kv, head_dim)
+        pool_dtype = torch.uint8 if kv8 else self.tdtype
         self.k_pools: List[torch.Tensor] = []
         self.v_pools: List[torch.Tensor] = []
         for _ in range(n_layers):
-            self.k_pools.append(torch.zeros((n_slots, n_kv, head_dim), dtype=self.tdtype, device=self.device))
-            self.v_pools.append(torch.zeros((n_slots, n_kv, head_dim), dtype=self.tdtype, device=self.device))
+            self.k_pools.append(torch.zeros(shape, dtype=pool_dtype, device=self.device))
+            self.v_pools.append(torch.zeros(shape, dtype=pool_dtype, device=self.device))
         self.ctx = gb.Context(n_layers=n_layers, n_q=n_q, n_kv=n_kv, head_dim=head_dim, dtype=dtype,
                               n_slots=n_slots, k_pools=self.k_pools, v_pools=self.v_pools,
                               hot_fraction=hot_fraction, cold_init_order=cold_init_order,
-                              m_sat=m_sat, max_batch=max_batch, device=device, max_slabs=max_slabs)
+                              m_sat=m_sat, max_batch=max_batch, device=device, max_slabs=max_slabs, kv8=kv8)
         self.req_to_slot = torch.zeros((max_batch, cap), dtype=torch.int32, device=self.device)
         self.suffix_len = torch.zeros((max_batch,), dtype=torch.int32, device=self.device)
         self.seq_len_host = [0] * max_batch
         self._ws: Optional[torch.Tensor] = None
+        self._weight: Optional[torch.Tensor] = None
         self._index: Optional[gb.Index] = None
         self.cached: Dict[int, dict] = {}                      # prefixes written by admit()
         self.cold_prefix_slots: Dict[int, torch.Tensor] = {}  # COLD-placed prefix -> its slots
@@ -144,6 +151,7 @@ class GraniKVCache:
         self.row_prefix[b] = None
         self.seq_len_host[b] = 0
         self.suffix_len[b].zero_()
+        self.clear_weight(b)
 
     def remove_prefix(self, pid: int):
         """Drop an unreferenced cached prefix: a HOT slab returns to the pool, a COLD prefix's
@@ -160,6 +168,9 @@ class GraniKVCache:
             return
         self.req_to_slot[dst].copy_(self.req_to_slot[src])
         self.suffix_len[dst].copy_(self.suffix_len[src])
+        if self._weight is not None:
+            self._weight[dst].copy_(self._weight[src])
+            self.clear_weight(src)
         self.seq_len_host[dst] = self.seq_len_host[src]
         self.row_prefix[dst] = self.row_prefix[src]
         self.seq_len_host[src] = 0
@@ -184,6 +195,46 @@ class GraniKVCache:
                 self.ctx.cold_append(layer, k_layers[layer].contiguous(), v_layers[layer].contiguous(),
                                      slots_out, N, s)
         return slots_out[:N]
+
+    # eviction of COLD tokens --------------------------------------------------------------
+    @property
+    def weight(self) -> torch.Tensor:
+        """Accumulated attention weight of every place of the token table [max_batch, cap] (fp32),
+        made on first use; a new row's weights are 0."""
+        if self._weight is None:
+            self._weight = torch.zeros((self.max_batch, self.cap), dtype=torch.float32, device=self.device)
+        return self._weight
+
+    def clear_weight(self, b: int):
+        """Row b's weights start from 0 again."""
+        if self._weight is not None:
+            self._weight[b].zero_()
+
+    def weigh(self, layer: int, q: torch.Tensor, lse: torch.Tensor, batch: gb.Batch, keep: float = 1.0):
+        """Add the attention weight that each COLD token received in one layer of a step (q and the
+        lse decode() returned), summed over the query heads, to keep times its old weight."""
+        if batch._live is None:
+            batch = batch.with_live(self.suffix_len)
+        self.ctx.cold_weigh(layer, q.contiguous(), lse.contiguous(), batch, self.weight, keep, self.stream())
+
+    def evict(self, n_evict: Sequence[int], keep_last: int = 0, keep_first: Optional[Sequence[int]] = None):
+        """The n_evict[b] lightest COLD tokens of row b leave (b < len(n_evict)), but for its first
+        keep_first[b] and last keep_last ones and the slots it shares with a prefix placed in COLD;
+        the rest close up in order and the slots return to the free ring.  Returns those slots."""
+        B = len(n_evict)
+        first = [0] * B if keep_first is None else [int(x) for x in keep_first]
+        for b in range(B):
+            if self.row_prefix[b] is not None:
+                first[b] = max(first[b], min(self.row_prefix[b][1], self.seq_len_host[b]))
+        total = int(sum(n_evict))
+        slots = torch.empty((max(total, 1),), dtype=torch.int32, device=self.device)
+        self.ctx.cold_evict(self.seq_len_host[:B], list(n_evict), first, keep_last, self.req_to_slot, self.suffix_len,
+                            self.weight, self.cap, slots, self.stream())
+        if total:
+            self.ctx.cold_free(slots, total, self.stream())
+        for b in range(B):
+            self.seq_len_host[b] -= int(n_evict[b])
+        return slots[:total]
 
     # attention ----------------------------------------------------------------------------
     def batch(self, slab_ids: Sequence[int], seq_len: Optional[Sequence[int]] = None) -> gb.Batch:

@@ -84,6 +84,8 @@ struct granikv_ctx {
   // TMA descriptors of each layer's K and V pools (dense backend), valid when has_tmaps
   std::vector<CUtensorMap> tmap_k, tmap_v;
   bool has_tmaps = false;
+  // 8-bit cache (granikv_create_kv8): bytes of a slot's packed row, else 0
+  int64_t kv8_row = 0;
 };
 
 struct granikv_plan {
@@ -159,6 +161,7 @@ bool has_device(const granikv_ctx* c) { return c && !c->cfg.host_only && c->d_ri
 
 // Which prefix implementation serves a group of this shape and backend.
 int32_t prefix_impl_for(const granikv_ctx* c, int32_t backend) {
+  if (c->kv8_row) return kImplKv8Generic;
   if (c->cfg.dtype == GRANIKV_DTYPE_BF16 && c->cfg.head_dim == 128) {
     if (backend == GRANIKV_BACKEND_DENSE && (c->has_tmaps || c->cfg.host_only)) return kImplDenseTc;
     if (c->g <= kCascadeStreamCols * kCascadeStreamWarps) return kImplCascadeStream;
@@ -168,6 +171,16 @@ int32_t prefix_impl_for(const granikv_ctx* c, int32_t backend) {
       c->cfg.head_dim <= 128)
     return kImplDenseTf32;
   return kImplGeneric;
+}
+
+// Kernels outside the 16-bit tensor-core path: they take no part in the one grid, and their step
+// runs prefix, suffix and merge one after another.
+bool runs_alone(int32_t impl) { return impl == kImplGeneric || impl == kImplDenseTf32 || impl == kImplKv8Generic; }
+
+// Which kernel attends the COLD suffix.
+int32_t suffix_impl_for(const granikv_ctx* c) {
+  if (c->kv8_row) return kImplKv8Generic;
+  return c->cfg.dtype == GRANIKV_DTYPE_BF16 && c->cfg.head_dim == 128 && c->g <= 8 ? kImplSuffixMma : kImplGeneric;
 }
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no link-time libcuda).
@@ -438,7 +451,10 @@ const char* granikv_status_string(granikv_status s) {
 
 int32_t granikv_version(void) { return 100; }
 
-granikv_status granikv_create(const granikv_config* cfg, granikv_ctx** out) {
+}  // extern "C"
+
+namespace {
+granikv_status create_impl(const granikv_config* cfg, bool kv8, granikv_ctx** out) {
   if (!cfg || !out) return GRANIKV_ERR_INVALID;
   *out = nullptr;
   if (cfg->n_layers <= 0 || cfg->n_q <= 0 || cfg->n_kv <= 0 || cfg->n_q % cfg->n_kv)
@@ -464,6 +480,7 @@ granikv_status granikv_create(const granikv_config* cfg, granikv_ctx** out) {
     delete c;
     return GRANIKV_ERR_INVALID;
   }
+  if (kv8) c->kv8_row = kv8_row_bytes(cfg->n_kv, cfg->head_dim);
   if (c->n_hot > 0) c->free_ext.push_back({0, c->n_hot});
   c->slabs.resize(c->cfg.max_slabs);
   c->head = 0;
@@ -525,7 +542,7 @@ granikv_status granikv_create(const granikv_config* cfg, granikv_ctx** out) {
     if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&c->aux, cudaStreamNonBlocking);
     if (e == cudaSuccess) e = cudaEventCreateWithFlags(&c->ev_fork, cudaEventDisableTiming);
     if (e == cudaSuccess) e = cudaEventCreateWithFlags(&c->ev_join, cudaEventDisableTiming);
-    if (e == cudaSuccess && cfg->dtype == GRANIKV_DTYPE_BF16 && cfg->head_dim == 128 && c->cc_major == 10) {
+    if (e == cudaSuccess && !kv8 && cfg->dtype == GRANIKV_DTYPE_BF16 && cfg->head_dim == 128 && c->cc_major == 10) {
       c->tmap_k.resize(cfg->n_layers);
       c->tmap_v.resize(cfg->n_layers);
       bool ok = true;
@@ -549,6 +566,21 @@ granikv_status granikv_create(const granikv_config* cfg, granikv_ctx** out) {
     }
   }
   *out = c;
+  return GRANIKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+granikv_status granikv_create(const granikv_config* cfg, granikv_ctx** out) { return create_impl(cfg, false, out); }
+
+granikv_status granikv_create_kv8(const granikv_config* cfg, granikv_ctx** out) { return create_impl(cfg, true, out); }
+
+granikv_status granikv_kv8_row_bytes(int32_t n_kv, int32_t head_dim, size_t* bytes) {
+  if (!bytes || n_kv <= 0) return GRANIKV_ERR_INVALID;
+  if (head_dim <= 0 || head_dim % 32 || head_dim > 256) return GRANIKV_ERR_UNSUPPORTED;
+  *bytes = (size_t)kv8_row_bytes(n_kv, head_dim);
   return GRANIKV_OK;
 }
 
@@ -642,8 +674,15 @@ granikv_status granikv_hot_fill(granikv_ctx* c, int32_t layer, int32_t sid, cons
                                 const void* v, granikv_stream_t stream) {
   if (!c || !k || !v || layer < 0 || layer >= c->cfg.n_layers) return GRANIKV_ERR_INVALID;
   if (sid < 0 || sid >= (int32_t)c->slabs.size() || !c->slabs[sid].live) return GRANIKV_ERR_INVALID;
+  if (c->kv8_row && ((uintptr_t)k | (uintptr_t)v) % 16) return GRANIKV_ERR_INVALID;
   if (!has_device(c)) return GRANIKV_ERR_NO_DEVICE;
   DeviceGuard dg(c->cfg.device);
+  if (c->kv8_row) {
+    c->n_kernels += 1;
+    return cuda_status(launch_kv8_fill(c->cfg.dtype, k, v, c->slabs[sid].len, (uint8_t*)c->kpool[layer],
+                                       (uint8_t*)c->vpool[layer], c->slabs[sid].off, c->cfg.n_kv, c->cfg.head_dim,
+                                       (cudaStream_t)stream));
+  }
   size_t row = (size_t)c->cfg.n_kv * c->cfg.head_dim * elem_size(c->cfg.dtype);
   size_t off = (size_t)c->slabs[sid].off * row;
   size_t bytes = (size_t)c->slabs[sid].len * row;
@@ -742,14 +781,91 @@ granikv_status granikv_cold_append(granikv_ctx* c, int32_t layer, const void* k_
                                    granikv_stream_t stream) {
   if (!c || layer < 0 || layer >= c->cfg.n_layers || N < 0) return GRANIKV_ERR_INVALID;
   if (N > 0 && (!k_new || !v_new || !slots)) return GRANIKV_ERR_INVALID;
+  if (c->kv8_row && ((uintptr_t)k_new | (uintptr_t)v_new) % 16) return GRANIKV_ERR_INVALID;
   if (!has_device(c)) return GRANIKV_ERR_NO_DEVICE;
   if (N == 0) return GRANIKV_OK;
   DeviceGuard dg(c->cfg.device);
+  if (c->kv8_row) {
+    c->n_kernels += 1;
+    return cuda_status(launch_kv8_append(c->cfg.dtype, k_new, v_new, slots, N, (uint8_t*)c->kpool[layer],
+                                         (uint8_t*)c->vpool[layer], c->cfg.n_kv, c->cfg.head_dim, c->n_hot,
+                                         c->cfg.n_slots, c->d_err, (cudaStream_t)stream));
+  }
   cudaError_t e = launch_cold_append(c->cfg.dtype, k_new, v_new, slots, N, c->kpool[layer],
                                      c->vpool[layer], (int64_t)c->cfg.n_kv * c->cfg.head_dim,
                                      c->n_hot, c->cfg.n_slots, c->checks, c->d_err,
                                      (cudaStream_t)stream);
   if (e == cudaSuccess) c->n_kernels += 1;
+  return cuda_status(e);
+}
+
+// ---- eviction of COLD tokens ----------------------------------------------------------------
+
+granikv_status granikv_cold_weigh(granikv_ctx* c, int32_t layer, const void* q, const float* lse,
+                                  const granikv_batch* bt, float* weight, float keep, granikv_stream_t stream) {
+  if (!c || !q || !lse || !bt || !weight || layer < 0 || layer >= c->cfg.n_layers) return GRANIKV_ERR_INVALID;
+  if (bt->B <= 0 || bt->B > c->cfg.max_batch || !bt->seq_len || bt->cap < 0) return GRANIKV_ERR_INVALID;
+  if (!(keep >= 0.f) || std::isinf(keep) || (uintptr_t)q % 16) return GRANIKV_ERR_INVALID;
+  int32_t max_len = 0;
+  for (int32_t b = 0; b < bt->B; ++b) {
+    if (bt->seq_len[b] < 0 || bt->seq_len[b] > bt->cap) return GRANIKV_ERR_INVALID;
+    max_len = std::max(max_len, bt->seq_len[b]);
+  }
+  if (!bt->seq_len_dev || !bt->req_to_slot) return GRANIKV_ERR_INVALID;
+  if (!has_device(c)) return GRANIKV_ERR_NO_DEVICE;
+  if (max_len == 0) return GRANIKV_OK;
+  DeviceGuard dg(c->cfg.device);
+  WeighParams a{};
+  a.q = q;
+  a.lse = lse;
+  a.kpool = c->kpool[layer];
+  a.kv8_row = c->kv8_row;
+  a.req_to_slot = bt->req_to_slot;
+  a.live_len = bt->seq_len_dev;
+  a.weight = weight;
+  a.n_slots = c->cfg.n_slots;
+  a.n_hot = c->n_hot;
+  a.cap = bt->cap;
+  a.B = bt->B;
+  a.n_q = c->cfg.n_q;
+  a.n_kv = c->cfg.n_kv;
+  a.d = c->cfg.head_dim;
+  a.g = c->g;
+  a.keep = keep;
+  a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c->cfg.head_dim));
+  a.err = c->d_err;
+  c->n_kernels += 1;
+  return cuda_status(launch_cold_weigh(c->cfg.dtype, a, bt->seq_len, (cudaStream_t)stream));
+}
+
+granikv_status granikv_cold_evict(granikv_ctx* c, const int32_t* seq_len, const int32_t* n_evict,
+                                  const int32_t* keep_first, int32_t keep_last, int32_t B, int32_t* req_to_slot,
+                                  int32_t* suffix_len, float* weight, int32_t cap, int32_t* slots_out,
+                                  granikv_stream_t stream) {
+  if (!c || !seq_len || !n_evict || !req_to_slot || !weight || keep_last < 0 || cap <= 0) return GRANIKV_ERR_INVALID;
+  if (B <= 0 || B > c->cfg.max_batch) return GRANIKV_ERR_INVALID;
+  std::vector<EvictRow> rows;
+  try {
+    rows.resize((size_t)B);
+  } catch (const std::bad_alloc&) {
+    return GRANIKV_ERR_INVALID;
+  }
+  int64_t total = 0;
+  for (int32_t b = 0; b < B; ++b) {
+    const int64_t first = keep_first ? keep_first[b] : 0;
+    if (seq_len[b] < 0 || seq_len[b] > cap || first < 0 || n_evict[b] < 0) return GRANIKV_ERR_INVALID;
+    if (n_evict[b] > std::max<int64_t>(0, (int64_t)seq_len[b] - first - keep_last)) return GRANIKV_ERR_INVALID;
+    rows[b] = EvictRow{seq_len[b], n_evict[b], (int32_t)first, (int32_t)total};
+    total += n_evict[b];
+    if (total > (int64_t)INT32_MAX) return GRANIKV_ERR_INVALID;
+  }
+  if (total > 0 && !slots_out) return GRANIKV_ERR_INVALID;
+  if (!has_device(c)) return GRANIKV_ERR_NO_DEVICE;
+  if (total == 0 && !suffix_len) return GRANIKV_OK;
+  DeviceGuard dg(c->cfg.device);
+  cudaError_t e = launch_cold_evict(rows.data(), B, keep_last, req_to_slot, suffix_len, weight, cap, slots_out,
+                                    (cudaStream_t)stream);
+  c->n_kernels += 1;
   return cuda_status(e);
 }
 
@@ -871,13 +987,13 @@ granikv_status granikv_dispatch(granikv_ctx* c, const granikv_batch* bt, granikv
   }
   // Fused merge when every kernel of the step is a tensor-core kernel; then the suffix may run
   // next to the prefix on its own share of the SMs.
-  const bool fast_suffix_pre = c->cfg.dtype == GRANIKV_DTYPE_BF16 && c->cfg.head_dim == 128 && g <= 8;
+  const bool fast_suffix_pre = suffix_impl_for(c) == kImplSuffixMma;
   bool fused = c->fused_merge && (fast_suffix_pre || T_all == 0);
   for (int32_t i = 0; i < G; ++i)
-    if (groups[i].impl == kImplGeneric || groups[i].impl == kImplDenseTf32) fused = false;
+    if (runs_alone(groups[i].impl)) fused = false;
   bool fast_all = fast_suffix_pre || T_all == 0;
   for (int32_t i = 0; i < G; ++i)
-    if (groups[i].impl == kImplGeneric || groups[i].impl == kImplDenseTf32) fast_all = false;
+    if (runs_alone(groups[i].impl)) fast_all = false;
   bool concurrent = fast_all && c->concurrent && G > 0 && T_all > 0;
   const bool split_sms = concurrent && c->prefix_share < 0.999f;
   const bool auto_share = split_sms && c->prefix_share <= 0.f;
@@ -892,7 +1008,7 @@ granikv_status granikv_dispatch(granikv_ctx* c, const granikv_batch* bt, granikv
   //    kernels run one CTA per SM, so their target is one wave over their SMs.
   int64_t target = 2LL * c->num_sms;
   for (int32_t i = 0; i < G; ++i)
-    if (groups[i].impl != kImplGeneric) target = prefix_sms;
+    if (groups[i].impl != kImplGeneric && groups[i].impl != kImplKv8Generic) target = prefix_sms;
   {
     int64_t max_tiles = 1;
     for (int32_t i = 0; i < G; ++i) {
@@ -1098,8 +1214,7 @@ granikv_status granikv_dispatch(granikv_ctx* c, const granikv_batch* bt, granikv
   //    plus segments reach an equal share of what is left when it starts (cut_suffix_runs).
   static_assert(kSTile == 16, "the tile count above uses 16-token tiles");
   const int64_t T = T_tiles;
-  const bool fast_suffix = c->cfg.dtype == GRANIKV_DTYPE_BF16 && c->cfg.head_dim == 128 && g <= 8;
-  const int32_t suffix_impl = fast_suffix ? kImplSuffixMma : kImplGeneric;
+  const int32_t suffix_impl = suffix_impl_for(c);
   int32_t n_scta = 0;       // token-CTA runs
   int32_t n_tail = 0;       // of them, the last n_tail are run by the dense CTAs of one grid
   int64_t U = 0;            // tiles plus segment costs, with every cut counted as inside a request
@@ -1429,6 +1544,7 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
                                      float* lse, void* ws, size_t ws_bytes, granikv_stream_t stream) {
   if (!c || !bt || !q || !o || !lse || !ws) return GRANIKV_ERR_INVALID;
   if (layer < 0 || layer >= c->cfg.n_layers) return GRANIKV_ERR_INVALID;
+  if (c->kv8_row && ((uintptr_t)q | (uintptr_t)o) % 16) return GRANIKV_ERR_INVALID;
   if (!has_device(c)) return GRANIKV_ERR_NO_DEVICE;
   if ((uintptr_t)ws % 256) return GRANIKV_ERR_INVALID;
   if (!bt->req_to_slot) return GRANIKV_ERR_INVALID;
@@ -1502,6 +1618,7 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
   a.live_len = bt->seq_len_dev;
   a.k_new = k_new;
   a.v_new = v_new;
+  a.kv8_row = c->kv8_row;
   CUtensorMap tmq{};
   a.q_tma = 0;
   if (p->pitem_count[kImplDenseTc] > 0 && c->cfg.dtype == GRANIKV_DTYPE_BF16 && c->cfg.head_dim == 128)
@@ -1513,6 +1630,7 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
   auto launch_suffix = [&](cudaStream_t st, bool pdl) -> cudaError_t {
     if (p->n_sitems <= 0) return cudaSuccess;
     c->n_kernels += 1;
+    if (p->suffix_impl == kImplKv8Generic) return launch_kv8_suffix_generic(c->cfg.dtype, a, st);
     return p->suffix_impl == kImplSuffixMma ? launch_suffix_mma(a, a.scta_begin, p->n_scta, st, pdl)
                                             : launch_suffix_generic(c->cfg.dtype, a, st);
   };
@@ -1522,6 +1640,11 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
     cudaError_t r = cudaSuccess;
     if (p->pitem_count[kImplGeneric] > 0) {
       r = launch_prefix_generic(c->cfg.dtype, a, p->pitem_first[kImplGeneric], p->pitem_count[kImplGeneric], st);
+      c->n_kernels += 1;
+    }
+    if (r == cudaSuccess && p->pitem_count[kImplKv8Generic] > 0) {
+      r = launch_kv8_prefix_generic(c->cfg.dtype, a, p->pitem_first[kImplKv8Generic], p->pitem_count[kImplKv8Generic],
+                                    st);
       c->n_kernels += 1;
     }
     if (r == cudaSuccess && p->pitem_count[kImplDenseTf32] > 0) {
@@ -1552,6 +1675,12 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
     if (c->cfg.dtype == GRANIKV_DTYPE_BF16 && c->cfg.head_dim == 128) return launch_merge_rows(a, p->merge_warps, s, pdl);
     return launch_merge(c->cfg.dtype, a, s, pdl);
   };
+  // 8-bit cache: the newest rows are quantised into their slots before anything reads them
+  if (k_new && c->kv8_row) {
+    e = launch_kv8_append_newest(c->cfg.dtype, a, s);
+    c->n_kernels += 1;
+    if (e != cudaSuccess) return cuda_status(e);
+  }
   const int32_t n_dense = p->pitem_count[kImplDenseTc], n_casc = p->pitem_count[kImplCascadeStream];
   const bool one_launch = p->concurrent && p->n_pitems > 0 && n_dense + n_casc == p->n_pitems &&
                           (n_dense == 0 || c->has_tmaps) && p->suffix_impl == kImplSuffixMma && p->n_sitems > 0;

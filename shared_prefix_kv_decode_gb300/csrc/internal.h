@@ -33,6 +33,7 @@ enum Impl : int32_t {
   kImplSuffixMma = 3, // bf16, head_dim 128, g <= 8: warp-level tensor-core suffix kernel
   kImplCascadeStream = 4,  // bf16, head_dim 128, g <= 128: cascade over whole 2 KB slot rows
   kImplDenseTf32 = 5,      // f32, head_dim % 32 == 0 up to 128: tcgen05 kind::tf32 dense kernel
+  kImplKv8Generic = 6,     // 8-bit cache, any head_dim % 32 == 0 up to 256: CUDA-core kernel
 };
 
 // Geometry of each prefix kernel: query rows per CTA and tokens per tile.  The planner and the
@@ -127,6 +128,39 @@ struct AttnParams {
   const void* v_new;        // here (not the pool) and written to its slot by the suffix CTA
   const int32_t* live_len;  // [B] device token counts that end each request's suffix segments early
                             // (the plan may cover more tokens than exist yet); NULL: the plan's
+  int64_t kv8_row;          // 8-bit cache: bytes of a packed slot row (kv8_row_bytes), else 0
+};
+
+// ---- 8-bit cache ---------------------------------------------------------------------------
+// One slot of an 8-bit pool is one packed row: e4m3 codes [n_kv, d], then one fp32 scale a KV
+// head, padded to 16 bytes (value = code * scale).  Every row carries its own scales; the rows of
+// one 64-token block of a slab (kKv8Block, counted from the slab's start) hold the same ones.
+constexpr int kKv8Block = 64;
+constexpr float kE4m3Max = 448.0f;
+constexpr float kKv8AmaxMin = 1.2621774483536189e-29f;  // 2^-96: smallest amax a scale is made for
+__host__ __device__ inline int64_t kv8_row_bytes(int32_t n_kv, int32_t d) {
+  return ((int64_t)n_kv * (d + 4) + 15) / 16 * 16;
+}
+
+// Tokens and weights of one row for the eviction kernel, passed by value.
+struct EvictRow {
+  int32_t len, n_evict, first, out;  // tokens; how many leave; first position that may; first place in slots_out
+};
+
+// What the weighing of COLD tokens needs, passed by value.
+struct WeighParams {
+  const void* q;               // [B, n_q, d]
+  const float* lse;            // [B, n_q]
+  const void* kpool;           // 16/32-bit rows [n_slots, n_kv, d], or packed 8-bit rows
+  int64_t kv8_row;             // bytes of a packed row, 0 for the 16/32-bit pools
+  const int32_t* req_to_slot;  // [B, cap]
+  const int32_t* live_len;     // [B] device
+  float* weight;               // [B, cap]
+  int64_t n_slots, n_hot;
+  int32_t cap, B, n_q, n_kv, d, g;
+  float keep;                  // weight = keep * weight + this step's
+  float scale_log2;
+  int32_t* err;
 };
 
 // ---- launchers (kernels_*.cu) ------------------------------------------------------------
@@ -172,7 +206,25 @@ cudaError_t launch_prefix_suffix_tc(const AttnParams& p, int32_t first_dense, in
 // each row's records.
 cudaError_t launch_merge_rows(const AttnParams& p, int32_t warps_per_row, cudaStream_t s, bool pdl);
 
-constexpr int kNumImpl = 6;
+
+// 8-bit cache (kernels_kv8.cu): quantise L_p consecutive rows of a slab, N rows at slots[i], or
+// each request's newest row at its slot (k_new/v_new of AttnParams).
+cudaError_t launch_kv8_fill(int32_t dtype, const void* k, const void* v, int32_t L_p, uint8_t* kpool, uint8_t* vpool,
+                            int64_t first_slot, int32_t n_kv, int32_t d, cudaStream_t s);
+cudaError_t launch_kv8_append(int32_t dtype, const void* k_new, const void* v_new, const int32_t* slots, int32_t N,
+                              uint8_t* kpool, uint8_t* vpool, int32_t n_kv, int32_t d, int64_t n_hot,
+                              int64_t n_slots, int32_t* err, cudaStream_t s);
+cudaError_t launch_kv8_append_newest(int32_t dtype, const AttnParams& p, cudaStream_t s);
+cudaError_t launch_kv8_prefix_generic(int32_t dtype, const AttnParams& p, int32_t first_item, int32_t n_items,
+                                      cudaStream_t s);
+cudaError_t launch_kv8_suffix_generic(int32_t dtype, const AttnParams& p, cudaStream_t s);
+
+// Eviction (kernels_evict.cu)
+cudaError_t launch_cold_weigh(int32_t dtype, const WeighParams& p, const int32_t* seq_len /*host [B]*/, cudaStream_t s);
+cudaError_t launch_cold_evict(const EvictRow* rows, int32_t B, int32_t keep_last, int32_t* req_to_slot,
+                              int32_t* suffix_len, float* weight, int32_t cap, int32_t* slots_out, cudaStream_t s);
+
+constexpr int kNumImpl = 7;
 
 }  // namespace granikv
 

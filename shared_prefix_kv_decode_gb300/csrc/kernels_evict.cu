@@ -1,0 +1,493 @@
+// kernels_evict.cu -- eviction of COLD tokens by accumulated attention weight: the weight each
+// COLD token received in a step, and the selection and removal of the lightest tokens of a row.
+//
+// The token-level COLD pool (GraniKV, arXiv:2608.15584, "3 GraniKV": page size 1) lets single
+// tokens leave a request: their table entries close up and their slots go back to the free ring.
+#include "kv8_util.cuh"
+#include "launch_util.cuh"
+#include "mma_util.cuh"
+#include "tc_util.cuh"
+
+#include <type_traits>
+
+namespace granikv {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ void latch(int32_t* err, int32_t code) { atomicCAS(err, 0, code); }
+
+// ---- weighing ---------------------------------------------------------------------------------
+// The rows' token counts travel as a kernel parameter, with the number of chunks before each row,
+// so the grid has one CTA for each chunk of tokens that a row may hold and none for empty ones.
+template <int N>
+struct WeighRows {
+  int32_t first[N + 1];  // chunks of the rows before
+  int32_t len[N];
+  int32_t n, b0;         // rows here; row r is request b0 + r
+};
+
+// Chunk -> (row of the parameter, first token); a chunk that begins past the row's live tokens has n <= 0.
+template <int N>
+__device__ __forceinline__ void chunk_of(const WeighRows<N>& rows, const int32_t* live_len, int32_t chunk, int tokens,
+                                         int32_t& b, int32_t& t0, int32_t& n) {
+  int lo = 0, hi = rows.n;  // the last row with first <= chunk
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (rows.first[mid] <= chunk) lo = mid;
+    else hi = mid;
+  }
+  b = rows.b0 + lo;
+  t0 = (chunk - rows.first[lo]) * tokens;
+  n = min(min(live_len[b], rows.len[lo]) - t0, tokens);
+}
+
+// Any shape:
+// A CTA takes 32 tokens of a request: KV head by KV head the tokens' K rows go to shared memory in
+// fp32, each warp takes every eighth query head of the group, its lanes the tokens.  A lane sums
+// its heads in order, the warps' sums are added in warp order.
+constexpr int kTok = 32;
+
+template <typename T, bool KV8, int N>
+__global__ void __launch_bounds__(256) weigh_generic_kernel(WeighParams p, const __grid_constant__ WeighRows<N> rows) {
+  extern __shared__ float sm[];
+  float* sK = sm;                       // [kTok][d + 1]
+  float* sSum = sK + kTok * (p.d + 1);  // [8][kTok]
+  __shared__ int32_t s_slot[kTok];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t d = p.d;
+  int32_t b, t0, n;
+  chunk_of(rows, p.live_len, blockIdx.x, kTok, b, t0, n);
+  if (n > 0) {
+    if (threadIdx.x < kTok) {
+      int32_t slot = -1;
+      if (threadIdx.x < n) {
+        slot = p.req_to_slot[(int64_t)b * p.cap + t0 + threadIdx.x];
+        if (slot < p.n_hot || slot >= p.n_slots) {
+          latch(p.err, kDevBadSlot);
+          slot = -1;
+        }
+      }
+      s_slot[threadIdx.x] = slot;
+    }
+    float sum = 0.f;
+    for (int32_t j = 0; j < p.n_kv; ++j) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < kTok * (d / 4); i += blockDim.x) {
+        const int tok = i / (d / 4), c = i % (d / 4) * 4;
+        const int32_t slot = s_slot[tok];
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        if (slot >= 0) {
+          if constexpr (KV8) {
+            const uint8_t* row = (const uint8_t*)p.kpool + (int64_t)slot * p.kv8_row;
+            e4m3x4_to_f32x4(*reinterpret_cast<const uint32_t*>(row + (int64_t)j * d + c), x);
+            const float s = *reinterpret_cast<const float*>(row + (int64_t)p.n_kv * d + 4 * j);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[u] *= s;
+          } else {
+            const T* row = (const T*)p.kpool + ((int64_t)slot * p.n_kv + j) * d + c;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[u] = (float)row[u];
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sK[tok * (d + 1) + c + u] = x[u];
+      }
+      __syncthreads();
+      for (int32_t h = j * p.g + warp; h < (j + 1) * p.g; h += 8) {
+        const T* q = (const T*)p.q + ((int64_t)b * p.n_q + h) * d;
+        float s = 0.f;
+        for (int i = 0; i < d; ++i) s += (float)q[i] * sK[lane * (d + 1) + i];
+        const float lse = p.lse[(int64_t)b * p.n_q + h];
+        if (lse != -INFINITY) sum += exp2f(s * p.scale_log2 - lse * kLog2e);
+      }
+    }
+    sSum[warp * kTok + lane] = sum;
+    __syncthreads();
+    if (warp == 0 && lane < n) {
+      float w = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w += sSum[i * kTok + lane];
+      if (s_slot[lane] < 0) w = 0.f;
+      float* dst = p.weight + (int64_t)b * p.cap + t0 + lane;
+      *dst = p.keep != 0.f ? p.keep * *dst + w : w;
+    }
+  }
+}
+
+// bf16 q, head_dim 64 or 128: one unit is 16 tokens of one KV head, on warp-level tensor cores,
+//     S^T[16 tok x 8 heads] = K[16 tok x d] . Q^T[d x 8]     (d / 16 mma.m16n8k16 for each 8 query heads)
+// A warp takes its tokens' rows straight from global memory into the A operand: the sum over d may
+// be taken in any order, so the lanes of a row take 16-byte pieces of it (whole sectors), and Q^T is
+// loaded in the same order.  K is read once, no shared memory or barrier stands between HBM and the
+// MMAs, and each warp requests its next unit's rows before it computes the present one.
+// Of a 16-bit row lane c = lane % 4 holds dims 32 i + 8 c + 0..7 of load i; k-step 2 i + u takes its dims
+// 4 u + {0, 1} and 4 u + {2, 3}.  Of a packed 8-bit row it holds dims 64 i + 16 c + 0..15; k-step
+// 4 i + u takes dims 4 u + {0, 1} and 4 u + {2, 3}, converted to fp16 (exact); the row's scale
+// multiplies the scores, and q is brought into fp16's range by a power of two per query head
+// (exact but for elements 2^-28 below the row's largest).
+// The units' sums go to shared memory and are added in KV-head order: the result has one order.
+constexpr int kChunk = 64;          // tokens of a CTA
+constexpr int kMaxSums = 40 * 1024; // shared memory for the units' sums
+
+template <bool KV8, int D>
+struct KRows {
+  static constexpr int kLoads = KV8 ? D / 64 : D / 32;
+  uint4 a[kLoads], b[kLoads];  // rows lane / 4 and lane / 4 + 8
+  float sa, sb;                // their scales
+};
+
+template <bool KV8, int D, int N>
+__global__ void __launch_bounds__(256, 2) weigh_mma_kernel(WeighParams p, const __grid_constant__ WeighRows<N> rows) {
+  extern __shared__ float s_sum[];  // [n_kv][kChunk]
+  __shared__ int32_t s_slot[kChunk];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r = lane >> 2, c = lane & 3;
+  int32_t b, t0, n;
+  chunk_of(rows, p.live_len, blockIdx.x, kChunk, b, t0, n);
+  if (n <= 0) return;
+  if (tid < kChunk) {
+    int32_t slot = -1;
+    if (tid < n) {
+      slot = p.req_to_slot[(int64_t)b * p.cap + t0 + tid];
+      if (slot < p.n_hot || slot >= p.n_slots) {
+        latch(p.err, kDevBadSlot);
+        slot = -1;
+      }
+    }
+    s_slot[tid] = slot;
+  }
+  __syncthreads();
+  const int n_units = (n + 15) / 16 * p.n_kv;
+  using Rows = KRows<KV8, D>;
+  // the row of a slot (or, for a slot that does not count, zeros)
+  auto load_row = [&](int32_t slot, int32_t j, uint4 (&x)[Rows::kLoads], float& scale) {
+    scale = 1.f;
+    if (slot < 0) {
+#pragma unroll
+      for (int i = 0; i < Rows::kLoads; ++i) x[i] = make_uint4(0u, 0u, 0u, 0u);
+      return;
+    }
+    const uint8_t* row = (const uint8_t*)p.kpool + (int64_t)slot * (KV8 ? p.kv8_row : (int64_t)p.n_kv * D * 2);
+    const uint4* src = reinterpret_cast<const uint4*>(row + (int64_t)j * (KV8 ? D : 2 * D)) + c;
+#pragma unroll
+    for (int i = 0; i < Rows::kLoads; ++i) x[i] = __ldg(src + 4 * i);
+    if constexpr (KV8) scale = __ldg(reinterpret_cast<const float*>(row + (int64_t)p.n_kv * D) + j);
+  };
+  auto load_unit = [&](int u, Rows& k) {
+    if (u >= n_units) return;
+    const int32_t j = u % p.n_kv, tile = u / p.n_kv * 16;
+    load_row(s_slot[tile + r], j, k.a, k.sa);
+    load_row(s_slot[tile + r + 8], j, k.b, k.sb);
+  };
+  constexpr int kSteps = D / 16;
+  uint32_t qf[kSteps][2];
+  float c0 = 0.f, c1 = 0.f, e0 = -INFINITY, e1 = -INFINITY;  // heads 2 c and 2 c + 1: score factor, -lse in base 2
+  int32_t have = -1;                                          // the query heads whose q is in qf
+  // q of query heads h0 .. (at most 8, below h_end): column lane / 4
+  auto load_q = [&](int32_t h0, int32_t h_end) {
+    have = h0;
+    const bool mine = h0 + r < h_end;
+    const uint4* src = reinterpret_cast<const uint4*>((const __nv_bfloat16*)p.q + ((int64_t)b * p.n_q + h0 + r) * D);
+    float unit = 1.f;  // what one step of the scaled q stands for
+    if constexpr (!KV8) {
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint4 x = mine ? __ldg(src + 4 * i + c) : make_uint4(0u, 0u, 0u, 0u);
+        qf[2 * i][0] = x.x, qf[2 * i][1] = x.y, qf[2 * i + 1][0] = x.z, qf[2 * i + 1][1] = x.w;
+      }
+    } else {
+      uint32_t w[D / 64][8];
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint4 x = mine ? __ldg(src + 8 * i + 2 * c + u) : make_uint4(0u, 0u, 0u, 0u);
+          w[i][4 * u] = x.x, w[i][4 * u + 1] = x.y, w[i][4 * u + 2] = x.z, w[i][4 * u + 3] = x.w;
+        }
+      q_to_f16<D / 8>(&w[0][0], unit);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) qf[4 * i + u][0] = w[i][2 * u], qf[4 * i + u][1] = w[i][2 * u + 1];
+    }
+    const float lse = mine ? p.lse[(int64_t)b * p.n_q + h0 + r] : -INFINITY;
+    const float factor = unit * p.scale_log2, minus = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+    c0 = __shfl_sync(0xffffffffu, factor, 8 * c);
+    c1 = __shfl_sync(0xffffffffu, factor, 8 * c + 4);
+    e0 = __shfl_sync(0xffffffffu, minus, 8 * c);
+    e1 = __shfl_sync(0xffffffffu, minus, 8 * c + 4);
+  };
+  auto unit = [&](int u, const Rows& k) {
+    const int32_t j = u % p.n_kv, tile = u / p.n_kv * 16;
+    float w0 = 0.f, w1 = 0.f;
+    for (int32_t h0 = j * p.g; h0 < (j + 1) * p.g; h0 += 8) {
+      if (have != h0) load_q(h0, (j + 1) * p.g);
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < Rows::kLoads; ++i) {
+        const uint32_t a[4] = {k.a[i].x, k.a[i].y, k.a[i].z, k.a[i].w}, z[4] = {k.b[i].x, k.b[i].y, k.b[i].z, k.b[i].w};
+        if constexpr (KV8) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t a0, a2, b0, b2;
+            e4m3x4_to_f16x4(a[w], a0, a2);
+            e4m3x4_to_f16x4(z[w], b0, b2);
+            mma_f16_16816(s, a0, b0, a2, b2, qf[4 * i + w][0], qf[4 * i + w][1]);
+          }
+        } else {
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+            mma_bf16_16816(s, a[2 * w], z[2 * w], a[2 * w + 1], z[2 * w + 1], qf[2 * i + w][0], qf[2 * i + w][1]);
+        }
+      }
+      // a head without weight (lse -inf, or past the group) adds 2^-inf = 0, whatever its score
+      w0 += (e0 == -INFINITY ? 0.f : exp2f(s[0] * (c0 * k.sa) + e0)) + (e1 == -INFINITY ? 0.f : exp2f(s[1] * (c1 * k.sa) + e1));
+      w1 += (e0 == -INFINITY ? 0.f : exp2f(s[2] * (c0 * k.sb) + e0)) + (e1 == -INFINITY ? 0.f : exp2f(s[3] * (c1 * k.sb) + e1));
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      w0 += __shfl_xor_sync(0xffffffffu, w0, o);
+      w1 += __shfl_xor_sync(0xffffffffu, w1, o);
+    }
+    if (c == 0) {
+      s_sum[j * kChunk + tile + r] = w0;
+      s_sum[j * kChunk + tile + r + 8] = w1;
+    }
+  };
+  Rows k0, k1;
+  load_unit(warp, k0);
+  for (int u = warp; u < n_units; u += 16) {
+    load_unit(u + 8, k1);
+    unit(u, k0);
+    if (u + 8 < n_units) {
+      load_unit(u + 16, k0);
+      unit(u + 8, k1);
+    }
+  }
+  __syncthreads();
+  if (tid < n) {
+    float w = 0.f;
+    for (int32_t j = 0; j < p.n_kv; ++j) w += s_sum[j * kChunk + tid];
+    if (s_slot[tid] < 0) w = 0.f;
+    float* dst = p.weight + (int64_t)b * p.cap + t0 + tid;
+    *dst = p.keep != 0.f ? p.keep * *dst + w : w;
+  }
+}
+
+// ---- eviction ---------------------------------------------------------------------------------
+// Ordering key of a weight: unsigned order = float order, -0 equal to 0, NaN above everything.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  if (!(w == w)) return 0xffffffffu;
+  const uint32_t u = __float_as_uint(w + 0.0f);
+  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+template <int N>
+struct EvictRows {
+  EvictRow r[N];
+};
+
+constexpr int kEvictThreads = 1024;
+
+// One CTA per row: a radix selection (four passes of 8 bits) finds the key of the n_evict-th
+// lightest candidate; one pass in place then closes the row up, tile by tile.  A tile's places are
+// read before any is written, and tokens only move towards the row's start, so no place is
+// overwritten before it is read.
+template <int N>
+__global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_constant__ EvictRows<N> rows, int32_t row0,
+                                                              int32_t keep_last, int32_t* __restrict__ req_to_slot,
+                                                              int32_t* __restrict__ suffix_len,
+                                                              float* __restrict__ weight, int32_t cap,
+                                                              int32_t* __restrict__ slots_out) {
+  __shared__ int32_t s_hist[256];
+  __shared__ uint32_t s_prefix;
+  __shared__ int32_t s_left;
+  __shared__ uint32_t s_scan[32];
+  const EvictRow r = rows.r[blockIdx.x];
+  const int32_t b = row0 + blockIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0 && suffix_len) suffix_len[b] = r.len - r.n_evict;
+  if (r.n_evict <= 0) return;
+  int32_t* tab = req_to_slot + (int64_t)b * cap;
+  float* wt = weight + (int64_t)b * cap;
+  const int32_t c0 = r.first, c1 = r.len - keep_last;  // candidates
+  // the n_evict-th smallest key: after the pass of bits [sh, sh + 8) the key's bits above sh are
+  // `prefix`, and `left` of the candidates with those bits are still to leave
+  uint32_t prefix = 0;
+  int32_t left = r.n_evict;
+  for (int sh = 24; sh >= 0; sh -= 8) {
+    for (int i = tid; i < 256; i += kEvictThreads) s_hist[i] = 0;
+    __syncthreads();
+    for (int32_t t = c0 + tid; t < c1; t += kEvictThreads) {
+      const uint32_t key = weight_key(wt[t]);
+      if (sh == 24 || (key >> (sh + 8)) == (prefix >> (sh + 8))) atomicAdd(&s_hist[(key >> sh) & 255u], 1);
+    }
+    __syncthreads();
+    if (warp == 0) {  // lane: bins 8 * lane ..
+      int32_t c[8], mine = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mine += c[i] = s_hist[lane * 8 + i];
+      int32_t upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      int32_t before = upto - mine;
+      if (before < left && left <= upto) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (before < left && left <= before + c[i]) {
+            s_prefix = prefix | ((uint32_t)(lane * 8 + i) << sh);
+            s_left = left - before;
+          }
+          before += c[i];
+        }
+      }
+    }
+    __syncthreads();
+    prefix = s_prefix;
+    left = s_left;
+  }
+  // leavers: keys below `prefix`, and the first `left` with that key
+  int32_t below = 0, equal = 0;  // of the places before this tile
+  for (int32_t t0 = c0; t0 < r.len; t0 += kEvictThreads) {
+    const int32_t t = t0 + tid;
+    int32_t slot = 0;
+    float w = 0.f;
+    uint32_t flag = 0;  // 1: below, 1 << 16: equal
+    if (t < r.len) {
+      slot = tab[t];
+      w = wt[t];
+      if (t < c1) {
+        const uint32_t key = weight_key(w);
+        flag = key < prefix ? 1u : key == prefix ? 0x10000u : 0u;
+      }
+    }
+    uint32_t upto = flag;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    if (lane == 31) s_scan[warp] = upto;
+    __syncthreads();
+    uint32_t base = 0, total = 0;
+    {
+      uint32_t v = s_scan[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+      }
+      total = __shfl_sync(0xffffffffu, v, 31);
+      base = warp ? __shfl_sync(0xffffffffu, v, warp - 1) : 0u;
+    }
+    const uint32_t ex = base + upto - flag;
+    const int32_t nb = below + (int32_t)(ex & 0xffffu), ne = equal + (int32_t)(ex >> 16);
+    const int32_t gone = nb + min(ne, left);  // leavers before this place
+    if (t < r.len) {
+      const bool leaves = (flag & 1u) || ((flag >> 16) && ne < left);
+      if (leaves) {
+        slots_out[r.out + gone] = slot;
+      } else if (gone > 0) {
+        tab[t - gone] = slot;
+        wt[t - gone] = w;
+      }
+    }
+    below += (int32_t)(total & 0xffffu);
+    equal += (int32_t)(total >> 16);
+    __syncthreads();  // s_scan is read; the writes are done before the next tile's
+  }
+  for (int32_t t = r.len - r.n_evict + tid; t < r.len; t += kEvictThreads) wt[t] = 0.f;
+}
+
+template <int N>
+cudaError_t evict_n(const EvictRow* rows, int32_t row0, int32_t n, int32_t keep_last, int32_t* req_to_slot,
+                    int32_t* suffix_len, float* weight, int32_t cap, int32_t* slots_out, cudaStream_t s) {
+  EvictRows<N> a{};
+  for (int32_t i = 0; i < n; ++i) a.r[i] = rows[i];
+  evict_kernel<N><<<n, kEvictThreads, 0, s>>>(a, row0, keep_last, req_to_slot, suffix_len, weight, cap, slots_out);
+  return cudaGetLastError();
+}
+
+template <typename T, bool KV8, int N>
+cudaError_t weigh_launch(const WeighParams& p, const WeighRows<N>& rows, int32_t chunks, cudaStream_t s) {
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    const int smem = (int)sizeof(float) * p.n_kv * kChunk;
+    if (p.d == 128 && smem <= kMaxSums) {
+      weigh_mma_kernel<KV8, 128, N><<<chunks, 256, smem, s>>>(p, rows);
+      return cudaGetLastError();
+    }
+    if (p.d == 64 && smem <= kMaxSums) {
+      weigh_mma_kernel<KV8, 64, N><<<chunks, 256, smem, s>>>(p, rows);
+      return cudaGetLastError();
+    }
+  }
+  const int smem = (int)sizeof(float) * (kTok * (p.d + 1) + 8 * kTok);
+  weigh_generic_kernel<T, KV8, N><<<chunks, 256, smem, s>>>(p, rows);
+  return cudaGetLastError();
+}
+
+template <typename T, bool KV8>
+int weigh_tokens(const WeighParams& p) {
+  const bool mma = std::is_same_v<T, __nv_bfloat16> && (p.d == 128 || p.d == 64) &&
+                   (int)sizeof(float) * p.n_kv * kChunk <= kMaxSums;
+  return mma ? kChunk : kTok;
+}
+
+template <typename T, bool KV8, int N>
+cudaError_t weigh_rows(const WeighParams& p, const int32_t* seq_len, int32_t b0, int32_t n, int tokens, cudaStream_t s) {
+  WeighRows<N> rows;
+  int64_t chunks = 0;
+  for (int32_t r = 0; r < n; ++r) {
+    rows.first[r] = (int32_t)chunks;
+    rows.len[r] = seq_len[b0 + r];
+    chunks += (seq_len[b0 + r] + tokens - 1) / tokens;
+  }
+  if (chunks > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
+  rows.first[n] = (int32_t)chunks;
+  rows.n = n;
+  rows.b0 = b0;
+  return chunks ? weigh_launch<T, KV8, N>(p, rows, (int32_t)chunks, s) : cudaSuccess;
+}
+
+template <typename T, bool KV8>
+cudaError_t weigh_all(const WeighParams& p, const int32_t* seq_len, cudaStream_t s) {
+  constexpr int kSmall = 64, kLarge = 1024;
+  const int tokens = weigh_tokens<T, KV8>(p);
+  cudaError_t e = cudaSuccess;
+  for (int32_t b = 0; b < p.B && e == cudaSuccess;) {
+    const int32_t n = p.B - b < kLarge ? p.B - b : kLarge;
+    e = n <= kSmall ? weigh_rows<T, KV8, kSmall>(p, seq_len, b, n, tokens, s)
+                    : weigh_rows<T, KV8, kLarge>(p, seq_len, b, n, tokens, s);
+    b += n;
+  }
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_cold_weigh(int32_t dtype, const WeighParams& p, const int32_t* seq_len, cudaStream_t s) {
+  if (dtype == 1)
+    return p.kv8_row ? weigh_all<__nv_bfloat16, true>(p, seq_len, s) : weigh_all<__nv_bfloat16, false>(p, seq_len, s);
+  return p.kv8_row ? weigh_all<float, true>(p, seq_len, s) : weigh_all<float, false>(p, seq_len, s);
+}
+
+cudaError_t launch_cold_evict(const EvictRow* rows, int32_t B, int32_t keep_last, int32_t* req_to_slot,
+                              int32_t* suffix_len, float* weight, int32_t cap, int32_t* slots_out, cudaStream_t s) {
+  // the rows' counts travel as a kernel parameter: nothing is staged in memory that two calls (or
+  // a captured and an eager one) could share
+  constexpr int kSmall = 64, kLarge = 1024;
+  cudaError_t e = cudaSuccess;
+  for (int32_t b = 0; b < B && e == cudaSuccess;) {
+    const int32_t n = B - b < kLarge ? B - b : kLarge;
+    e = n <= kSmall ? evict_n<kSmall>(rows + b, b, n, keep_last, req_to_slot, suffix_len, weight, cap, slots_out, s)
+                    : evict_n<kLarge>(rows + b, b, n, keep_last, req_to_slot, suffix_len, weight, cap, slots_out, s);
+    b += n;
+  }
+  return e;
+}
+
+}  // namespace granikv

@@ -1,0 +1,397 @@
+// kernels_kv8.cu -- 8-bit cache: the kernels that quantise K/V rows into packed slots, and the
+// CUDA-core decode attention over such slots for any head_dim that is a multiple of 32 (up to
+// 256) and either type of q.
+#include "kv8_util.cuh"
+#include "launch_util.cuh"
+
+#include <cmath>
+
+namespace granikv {
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ void latch(int32_t* err, int32_t code) { atomicCAS(err, 0, code); }
+
+// 8 consecutive elements of a 16-byte aligned row.
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// One block of kKv8Block slab tokens of one KV head, of K (blockIdx.z = 0) or V: 256 threads hold
+// the block in registers (NCH chunks of 8 elements each), so the rows are read once.
+template <typename T, int NCH>
+__global__ void __launch_bounds__(256) kv8_fill_kernel(const T* __restrict__ k, const T* __restrict__ v, int32_t L_p,
+                                                       uint8_t* __restrict__ kpool, uint8_t* __restrict__ vpool,
+                                                       int64_t first_slot, int32_t n_kv, int32_t d, int64_t row) {
+  __shared__ float s_max[8];
+  const int32_t j = blockIdx.y;
+  const T* src = blockIdx.z ? v : k;
+  uint8_t* pool = blockIdx.z ? vpool : kpool;
+  const int32_t t0 = blockIdx.x * kKv8Block;
+  const int32_t n = min(kKv8Block, L_p - t0);
+  const int32_t per_row = d / 8;  // chunks of a head's row
+  float x[NCH][8];
+  float amax = 0.f;
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    const int32_t idx = threadIdx.x + c * 256;
+    const int32_t t = idx / per_row;
+    if (t < n) load8(src + ((int64_t)(t0 + t) * n_kv + j) * d + idx % per_row * 8, x[c]);
+    else
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[c][i] = 0.f;
+  }
+#pragma unroll
+  for (int c = 0; c < NCH; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, finite_abs(x[c][i]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = amax;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) amax = fmaxf(amax, s_max[w]);
+  const float inv = kv8_inverse(amax), scale = kv8_scale(amax);
+  uint8_t* dst = pool + (first_slot + t0) * row;
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    const int32_t idx = threadIdx.x + c * 256;
+    const int32_t t = idx / per_row;
+    if (t >= n) continue;
+    const uint32_t lo = f32x4_to_e4m3x4(x[c][0] * inv, x[c][1] * inv, x[c][2] * inv, x[c][3] * inv);
+    const uint32_t hi = f32x4_to_e4m3x4(x[c][4] * inv, x[c][5] * inv, x[c][6] * inv, x[c][7] * inv);
+    *reinterpret_cast<uint2*>(dst + (int64_t)t * row + (int64_t)j * d + idx % per_row * 8) = make_uint2(lo, hi);
+  }
+  for (int32_t t = threadIdx.x; t < n; t += 256)
+    *reinterpret_cast<float*>(dst + (int64_t)t * row + (int64_t)n_kv * d + 4 * j) = scale;
+}
+
+// One warp quantises head j of one K (or V) row into a packed slot: a lane holds VPL consecutive
+// elements, and stores VPL codes (VPL bytes, at a VPL-byte offset).
+template <typename T, int VPL>
+__device__ __forceinline__ void kv8_write_row(const T* __restrict__ src, uint8_t* __restrict__ slot_row, int32_t j,
+                                              int32_t n_kv, int32_t d, int lane) {
+  float x[VPL];
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    x[i] = (float)src[lane * VPL + i];
+    amax = fmaxf(amax, finite_abs(x[i]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const float inv = kv8_inverse(amax);
+  uint8_t* dst = slot_row + (int64_t)j * d + lane * VPL;
+  if constexpr (VPL % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < VPL; i += 4)
+      *reinterpret_cast<uint32_t*>(dst + i) =
+          f32x4_to_e4m3x4(x[i] * inv, x[i + 1] * inv, x[i + 2] * inv, x[i + 3] * inv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) dst[i] = (uint8_t)f32x2_to_e4m3x2(x[i] * inv, 0.f);
+  }
+  if (lane == 0) *reinterpret_cast<float*>(slot_row + (int64_t)n_kv * d + 4 * j) = kv8_scale(amax);
+}
+
+// Rows at slots[i] (one scale per token and head): one warp per (row, head), K and V.
+template <typename T, int VPL>
+__global__ void __launch_bounds__(256) kv8_append_kernel(const T* __restrict__ k_new, const T* __restrict__ v_new,
+                                                         const int32_t* __restrict__ slots, int32_t N,
+                                                         uint8_t* __restrict__ kpool, uint8_t* __restrict__ vpool,
+                                                         int32_t n_kv, int32_t d, int64_t row, int64_t n_hot,
+                                                         int64_t n_slots, int32_t* err) {
+  const int lane = threadIdx.x & 31;
+  const int64_t total = (int64_t)N * n_kv;
+  for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < total; w += (int64_t)gridDim.x * 8) {
+    const int32_t t = (int32_t)(w / n_kv), j = (int32_t)(w % n_kv);
+    const int32_t slot = slots[t];
+    if (slot < n_hot || slot >= n_slots) {
+      if (lane == 0) latch(err, kDevBadSlot);
+      continue;
+    }
+    kv8_write_row<T, VPL>(k_new + w * d, kpool + (int64_t)slot * row, j, n_kv, d, lane);
+    kv8_write_row<T, VPL>(v_new + w * d, vpool + (int64_t)slot * row, j, n_kv, d, lane);
+  }
+}
+
+// Row b of k_new/v_new at the slot of request b's newest token (the fused append's write).
+template <typename T, int VPL>
+__global__ void __launch_bounds__(256) kv8_append_newest_kernel(AttnParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (w >= (int64_t)p.B * p.n_kv) return;
+  const int32_t b = (int32_t)(w / p.n_kv), j = (int32_t)(w % p.n_kv);
+  int32_t n = p.reqs[b].seq_len;
+  if (p.live_len) n = min(n, p.live_len[b]);
+  if (n < 1) return;
+  const int32_t slot = p.req_to_slot[(int64_t)b * p.cap + n - 1];
+  if (slot < p.n_hot || slot >= p.n_slots) {
+    if (lane == 0) latch(p.err, kDevBadSlot);
+    return;
+  }
+  kv8_write_row<T, VPL>((const T*)p.k_new + w * p.d, (uint8_t*)p.kpool + (int64_t)slot * p.kv8_row, j, p.n_kv, p.d, lane);
+  kv8_write_row<T, VPL>((const T*)p.v_new + w * p.d, (uint8_t*)p.vpool + (int64_t)slot * p.kv8_row, j, p.n_kv, p.d, lane);
+}
+
+// ---- decode attention on CUDA cores -----------------------------------------------------------
+// A CTA takes up to kGenericRows query rows of one KV head and a run of tokens.  Tiles of 32
+// tokens are dequantised into shared memory once for all rows; a warp holds two rows, its lanes
+// are the tile's tokens for the scores and head_dim's columns for the weighted sum.
+constexpr int kTok = kGenericTile, kRows = kGenericRows;
+
+__host__ __device__ inline int generic_smem(int d) {
+  return (int)sizeof(float) * (kTok * (d + 1) + kTok * d + kRows * d);
+}
+
+// slot_of(t): the token's slot, or -1 for one that does not count.
+template <typename T, int VPL, typename SlotOf, typename RowOf, typename RecOf>
+__device__ __forceinline__ void kv8_generic_run(const AttnParams& p, int32_t j, int32_t t0, int32_t t1, int n_rows,
+                                                SlotOf slot_of, RowOf row_of, RecOf rec_of) {
+  constexpr int d = VPL * 32;
+  extern __shared__ float sm[];
+  float* sK = sm;                    // [kTok][d + 1]
+  float* sV = sK + kTok * (d + 1);   // [kTok][d]
+  float* sQ = sV + kTok * d;         // [kRows][d]
+  __shared__ int32_t s_slot[kTok];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < n_rows * d; i += blockDim.x)
+    sQ[i] = (float)((const T*)p.q)[row_of(i / d) * d + i % d] * p.scale_log2;
+  const int r0 = warp * 2;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, acc[2][VPL];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) acc[r][i] = 0.f;
+  for (int32_t t = t0; t < t1; t += kTok) {
+    __syncthreads();  // the tile before is read
+    if (threadIdx.x < kTok) s_slot[threadIdx.x] = t + threadIdx.x < t1 ? slot_of(t + threadIdx.x) : -1;
+    __syncthreads();
+    for (int i = threadIdx.x; i < kTok * (d / 4); i += blockDim.x) {
+      const int tok = i / (d / 4), c = i % (d / 4) * 4;
+      const int32_t slot = s_slot[tok];
+      float kx[4] = {0.f, 0.f, 0.f, 0.f}, vx[4] = {0.f, 0.f, 0.f, 0.f};
+      if (slot >= 0) {
+        const uint8_t* kr = (const uint8_t*)p.kpool + (int64_t)slot * p.kv8_row;
+        const uint8_t* vr = (const uint8_t*)p.vpool + (int64_t)slot * p.kv8_row;
+        const uint32_t kw = *reinterpret_cast<const uint32_t*>(kr + (int64_t)j * d + c);
+        const uint32_t vw = *reinterpret_cast<const uint32_t*>(vr + (int64_t)j * d + c);
+        const float ks = *reinterpret_cast<const float*>(kr + (int64_t)p.n_kv * d + 4 * j);
+        const float vs = *reinterpret_cast<const float*>(vr + (int64_t)p.n_kv * d + 4 * j);
+        e4m3x4_to_f32x4(kw, kx);
+        e4m3x4_to_f32x4(vw, vx);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          kx[u] *= ks;
+          vx[u] *= vs;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) sK[tok * (d + 1) + c + u] = kx[u];
+      *reinterpret_cast<float4*>(sV + tok * d + c) = make_float4(vx[0], vx[1], vx[2], vx[3]);
+    }
+    __syncthreads();
+    if (r0 >= n_rows) continue;
+    const bool live = s_slot[lane] >= 0;
+    const float* q0 = sQ + r0 * d;
+    const float* q1 = r0 + 1 < n_rows ? q0 + d : q0;
+    float s[2] = {0.f, 0.f};
+    const float* kr = sK + lane * (d + 1);
+#pragma unroll 8
+    for (int i = 0; i < d; ++i) {
+      const float kv = kr[i];
+      s[0] += q0[i] * kv;
+      s[1] += q1[i] * kv;
+    }
+    float w[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if (!live) s[r] = -INFINITY;
+      float mx = s[r];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float mn = fmaxf(m[r], mx);
+      const float base = mn == -INFINITY ? 0.f : mn;
+      const float a = exp2f(m[r] - base);
+      w[r] = exp2f(s[r] - base);
+      float sum = w[r];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      l[r] = l[r] * a + sum;
+      m[r] = mn;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) acc[r][i] *= a;
+    }
+    const int n_tok = min(kTok, t1 - t);
+    for (int tok = 0; tok < n_tok; ++tok) {
+      const float w0 = __shfl_sync(0xffffffffu, w[0], tok), w1 = __shfl_sync(0xffffffffu, w[1], tok);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const float v = sV[tok * d + lane + 32 * i];
+        acc[0][i] += w0 * v;
+        acc[1][i] += w1 * v;
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    if (r0 + r >= n_rows) break;
+    const int32_t rec = rec_of(r0 + r);
+    if (rec < 0 || rec >= p.n_records) {
+      if (lane == 0) latch(p.err, kDevBadRecord);
+      continue;
+    }
+    const int32_t h = (int32_t)(row_of(r0 + r) % p.n_q);
+    const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+    float* dst = p.rec_o + ((int64_t)rec * p.n_q + h) * d;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) dst[lane + 32 * i] = acc[r][i] * inv;
+    if (lane == 0) p.rec_lse[(int64_t)rec * p.n_q + h] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2;
+  }
+}
+
+template <typename T, int VPL>
+__global__ void __launch_bounds__(256) kv8_prefix_generic_kernel(AttnParams p, int32_t first_item) {
+  const DevPrefixItem it = p.pitems[first_item + blockIdx.x];
+  const DevGroup gr = p.groups[it.group];
+  if (gr.slab_off < 0 || gr.slab_off + gr.L_p > p.n_hot) {
+    if (threadIdx.x == 0) latch(p.err, kDevBadSlab);
+    return;
+  }
+  int32_t t0, t1;
+  piece_range(gr, it.split, t0, t1);
+  const int32_t r0 = it.row_block * gr.rows_per_cta;
+  const int n_rows = min(gr.n_req * p.g - r0, kRows);
+  auto req = [&](int r) { return p.group_req[gr.req_begin + (r0 + r) / p.g]; };
+  kv8_generic_run<T, VPL>(
+      p, it.kv_head, t0, t1, n_rows, [&](int32_t t) { return (int32_t)(gr.slab_off + t); },
+      [&](int r) { return (int64_t)req(r) * p.n_q + it.kv_head * p.g + (r0 + r) % p.g; },
+      [&](int r) { return p.reqs[req(r)].rec_base + it.split; });
+}
+
+// blockIdx.y: KV head and block of kRows of its query heads.
+template <typename T, int VPL>
+__global__ void __launch_bounds__(256) kv8_suffix_generic_kernel(AttnParams p) {
+  DevSuffixItem it = p.sitems[blockIdx.x];
+  if (p.live_len) it.t1 = max(it.t0, min(it.t1, p.live_len[it.b]));
+  const int blocks = (p.g + kRows - 1) / kRows;
+  const int32_t j = blockIdx.y / blocks, h0 = j * p.g + blockIdx.y % blocks * kRows;
+  const int n_rows = min(kRows, (j + 1) * p.g - h0);
+  kv8_generic_run<T, VPL>(
+      p, j, it.t0, it.t1, n_rows,
+      [&](int32_t t) {
+        const int32_t slot = p.req_to_slot[(int64_t)it.b * p.cap + t];
+        if (slot >= p.n_hot && slot < p.n_slots) return slot;
+        latch(p.err, kDevBadSlot);
+        return (int32_t)-1;
+      },
+      [&](int r) { return (int64_t)it.b * p.n_q + h0 + r; }, [&](int) { return it.rec; });
+}
+
+// Runs f with VPL = d / 32 as a compile-time constant.
+template <typename F>
+cudaError_t with_vpl(int32_t d, F f) {
+  switch (d / 32) {
+    case 1: return f(std::integral_constant<int, 1>{});
+    case 2: return f(std::integral_constant<int, 2>{});
+    case 3: return f(std::integral_constant<int, 3>{});
+    case 4: return f(std::integral_constant<int, 4>{});
+    case 5: return f(std::integral_constant<int, 5>{});
+    case 6: return f(std::integral_constant<int, 6>{});
+    case 7: return f(std::integral_constant<int, 7>{});
+    case 8: return f(std::integral_constant<int, 8>{});
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+template <typename T>
+cudaError_t fill_t(const T* k, const T* v, int32_t L_p, uint8_t* kpool, uint8_t* vpool, int64_t first_slot,
+                   int32_t n_kv, int32_t d, cudaStream_t s) {
+  const dim3 grid((L_p + kKv8Block - 1) / kKv8Block, n_kv, 2);
+  return with_vpl(d, [&](auto vpl) {
+    constexpr int nch = decltype(vpl)::value;  // kKv8Block * d / 8 chunks over 256 threads
+    static_assert(kKv8Block * 32 / 8 == 256, "chunks per thread");
+    kv8_fill_kernel<T, nch><<<grid, 256, 0, s>>>(k, v, L_p, kpool, vpool, first_slot, n_kv, d, kv8_row_bytes(n_kv, d));
+    return cudaGetLastError();
+  });
+}
+
+template <typename T>
+cudaError_t append_t(const T* k, const T* v, const int32_t* slots, int32_t N, uint8_t* kpool, uint8_t* vpool,
+                     int32_t n_kv, int32_t d, int64_t n_hot, int64_t n_slots, int32_t* err, cudaStream_t s) {
+  const int64_t ctas = ((int64_t)N * n_kv + 7) / 8;
+  const unsigned grid = (unsigned)(ctas < 16384 ? ctas : 16384);
+  return with_vpl(d, [&](auto vpl) {
+    kv8_append_kernel<T, decltype(vpl)::value><<<grid, 256, 0, s>>>(k, v, slots, N, kpool, vpool, n_kv, d,
+                                                                    kv8_row_bytes(n_kv, d), n_hot, n_slots, err);
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_fill(int32_t dtype, const void* k, const void* v, int32_t L_p, uint8_t* kpool, uint8_t* vpool,
+                            int64_t first_slot, int32_t n_kv, int32_t d, cudaStream_t s) {
+  return dtype == 1 ? fill_t((const __nv_bfloat16*)k, (const __nv_bfloat16*)v, L_p, kpool, vpool, first_slot, n_kv, d, s)
+                    : fill_t((const float*)k, (const float*)v, L_p, kpool, vpool, first_slot, n_kv, d, s);
+}
+
+cudaError_t launch_kv8_append(int32_t dtype, const void* k_new, const void* v_new, const int32_t* slots, int32_t N,
+                              uint8_t* kpool, uint8_t* vpool, int32_t n_kv, int32_t d, int64_t n_hot,
+                              int64_t n_slots, int32_t* err, cudaStream_t s) {
+  return dtype == 1 ? append_t((const __nv_bfloat16*)k_new, (const __nv_bfloat16*)v_new, slots, N, kpool, vpool, n_kv,
+                               d, n_hot, n_slots, err, s)
+                    : append_t((const float*)k_new, (const float*)v_new, slots, N, kpool, vpool, n_kv, d, n_hot,
+                               n_slots, err, s);
+}
+
+cudaError_t launch_kv8_append_newest(int32_t dtype, const AttnParams& p, cudaStream_t s) {
+  const unsigned grid = (unsigned)(((int64_t)p.B * p.n_kv + 7) / 8);
+  return with_vpl(p.d, [&](auto vpl) {
+    constexpr int n = decltype(vpl)::value;
+    if (dtype == 1) kv8_append_newest_kernel<__nv_bfloat16, n><<<grid, 256, 0, s>>>(p);
+    else kv8_append_newest_kernel<float, n><<<grid, 256, 0, s>>>(p);
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_kv8_prefix_generic(int32_t dtype, const AttnParams& p, int32_t first_item, int32_t n_items,
+                                      cudaStream_t s) {
+  if (n_items <= 0) return cudaSuccess;
+  const int smem = generic_smem(p.d);
+  return with_vpl(p.d, [&](auto vpl) {
+    constexpr int n = decltype(vpl)::value;
+    auto kernel = dtype == 1 ? kv8_prefix_generic_kernel<__nv_bfloat16, n> : kv8_prefix_generic_kernel<float, n>;
+    cudaError_t e = allow_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<n_items, 256, smem, s>>>(p, first_item);
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_kv8_suffix_generic(int32_t dtype, const AttnParams& p, cudaStream_t s) {
+  if (p.n_sitems <= 0) return cudaSuccess;
+  const int smem = generic_smem(p.d);
+  const dim3 grid(p.n_sitems, p.n_kv * ((p.g + kRows - 1) / kRows));
+  return with_vpl(p.d, [&](auto vpl) {
+    constexpr int n = decltype(vpl)::value;
+    auto kernel = dtype == 1 ? kv8_suffix_generic_kernel<__nv_bfloat16, n> : kv8_suffix_generic_kernel<float, n>;
+    cudaError_t e = allow_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, 256, smem, s>>>(p);
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace granikv

@@ -1,0 +1,81 @@
+// kv8_util.cuh -- the 8-bit cache's number format: quantising K/V rows to e4m3 codes, and reading
+// codes back.  Every e4m3 value is exact in fp16 (4 significant bits, exponents -9..8), so the
+// attention kernels convert codes to fp16 with one hardware conversion per pair and apply the
+// scales to the scores and weights in fp32.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cstdint>
+
+#include "internal.h"
+
+namespace granikv {
+
+// Two e4m3 codes (low byte first) -> fp16x2.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t w) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(w));
+  return r;
+}
+// Four e4m3 codes -> two fp16x2 (codes 0, 1 and 2, 3).
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ void e4m3x4_to_f32x4(uint32_t w, float (&x)[4]) {
+  uint32_t a, b;
+  e4m3x4_to_f16x4(w, a, b);
+  const float2 u = __half22float2(*reinterpret_cast<__half2*>(&a)), v = __half22float2(*reinterpret_cast<__half2*>(&b));
+  x[0] = u.x;
+  x[1] = u.y;
+  x[2] = v.x;
+  x[3] = v.y;
+}
+// Two floats -> two e4m3 codes (a in the low byte): nearest even, saturated at +-448, NaN kept.
+__device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t f32x4_to_e4m3x4(float a, float b, float c, float d) {
+  return (uint32_t)f32x2_to_e4m3x2(a, b) | ((uint32_t)f32x2_to_e4m3x2(c, d) << 16);
+}
+
+// A query row in fp16, scaled by a power of two so that its largest finite element lies in
+// [2^14, 2^15): W words of two bf16 a lane, the row spread over the four lanes of a quad.  bf16's 8
+// significant bits fit fp16's 11, so elements down to 2^-31 of the largest stay exact (fp16's last
+// subnormal is 2^-24), smaller ones are off by at most 2^-39 of it.  `unit` is the power of two
+// that undoes the scaling.
+template <int W>
+__device__ __forceinline__ void q_to_f16(uint32_t* w, float& unit) {
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const float a = fabsf(__uint_as_float(w[i] << 16)), b = fabsf(__uint_as_float(w[i] & 0xffff0000u));
+    amax = fmaxf(amax, fmaxf(a < INFINITY ? a : 0.f, b < INFINITY ? b : 0.f));
+  }
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  // 2^(14 - exponent of amax), kept within what fp32 holds together with its inverse
+  const int e = (int)((__float_as_uint(amax) >> 23) & 255u);
+  const int up = amax == 0.f ? 127 : min(141 + 127 - e, 253);
+  const float f = __uint_as_float((uint32_t)up << 23);
+  unit = __uint_as_float((uint32_t)(254 - up) << 23);
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const __half2 h = __floats2half2_rn(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// |x| for a block's amax: infinities and NaN do not count.
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = fabsf(x);
+  return a < INFINITY ? a : 0.f;
+}
+__device__ __forceinline__ float kv8_scale(float amax) { return fmaxf(amax, kKv8AmaxMin) / kE4m3Max; }
+__device__ __forceinline__ float kv8_inverse(float amax) { return kE4m3Max / fmaxf(amax, kKv8AmaxMin); }
+
+}  // namespace granikv

@@ -39,6 +39,14 @@ inline cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// Let a kernel be launched with `bytes` of dynamic shared memory on the current device (a no-op up
+// to the 48 KB that need no leave).
+template <typename K>
+inline cudaError_t allow_smem(K kernel, int bytes) {
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 // Ask for the largest shared-memory carveout, so that an SM switching between this kernel and
 // the tensor-core kernels (which need nearly all of it) does not reconfigure its L1/shared split.
 template <typename K>

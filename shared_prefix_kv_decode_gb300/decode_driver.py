@@ -26,7 +26,13 @@ requests' lengths plus a headroom and the kernels read the lengths that exist fr
 outgrow its planned length; then the step runs eagerly once (which also uploads the new plan)
 and is captured again.
 
+With a COLD budget, every step also weighs the requests' COLD tokens by the attention they
+received in each layer (granikv_cold_weigh, in the captured step too), and before a step a request
+that holds more than the budget gives up its lightest tokens (granikv_cold_evict, but for its last
+`keep_last`), whose slots return to the free ring.  kv8 keeps the pools in 8 bits.
+
   python -m shared_prefix_kv_decode_gb300.decode_driver [--steps 64] [--layers 2] [--seed 0] [--graph]
+      [--kv8] [--cold-budget N]
 """
 
 from __future__ import annotations
@@ -55,12 +61,16 @@ class DecodeDriver:
     def __init__(self, *, prefix_lens: Sequence[int], n_layers: int = 1, n_q: int = 32, n_kv: int = 8,
                  head_dim: int = 128, max_batch: int = 256, cap: int = 4096, n_slots: int = 1 << 17,
                  seed: int = 0, keep_logical: bool = False, device: int = 0, graph: bool = False,
-                 headroom: int = 16, fused_append: bool = True):
+                 headroom: int = 16, fused_append: bool = True, kv8: bool = False,
+                 cold_budget: Optional[int] = None, keep_last: int = 16):
+        if cold_budget is not None and not 0 < keep_last <= cold_budget:
+            raise ValueError("a COLD budget needs 0 < keep_last <= cold_budget")
+        self.cold_budget, self.keep_last = cold_budget, keep_last
         self.n_layers, self.n_q, self.n_kv, self.d = n_layers, n_q, n_kv, head_dim
         self.rng = np.random.default_rng(seed)
         self.keep = keep_logical
         self.cache = GraniKVCache(n_layers=n_layers, n_q=n_q, n_kv=n_kv, head_dim=head_dim, dtype=gb.DTYPE_BF16,
-                                  n_slots=n_slots, max_batch=max_batch, cap=cap, device=device)
+                                  n_slots=n_slots, max_batch=max_batch, cap=cap, device=device, kv8=kv8)
         self.dev = self.cache.device
         self.ctx = self.cache.ctx
         self.plan = self.ctx.plan()
@@ -166,9 +176,34 @@ class DecodeDriver:
             self.cache.suffix_len[b].copy_(self.cache.suffix_len[last])
             self.rows[b] = self.rows[last]
             self.cache.seq_len_host[b] = self.cache.seq_len_host[last]
+            if self.cold_budget is not None:
+                self.cache.weight[b].copy_(self.cache.weight[last])
+        self.cache.clear_weight(last)
         self.rows.pop()
         self.cache.seq_len_host[last] = 0
         self.cache.suffix_len[last].zero_()
+
+    # ---- the COLD budget -----------------------------------------------------------------
+    def _evict(self) -> int:
+        """Requests over the COLD budget give up their lightest tokens; returns how many left."""
+        if self.cold_budget is None:
+            return 0
+        n_evict = [max(0, r["len"] - self.cold_budget) for r in self.rows]
+        total = sum(n_evict)
+        if total == 0:
+            return 0
+        self._sync_cold()
+        before = [self.cache.req_to_slot[b, :r["len"]].tolist() for b, r in enumerate(self.rows)] if self.keep else None
+        self.cache.evict(n_evict, self.keep_last)
+        for b, r in enumerate(self.rows):
+            if self.keep and n_evict[b]:
+                left = set(self.cache.req_to_slot[b, :r["len"] - n_evict[b]].tolist())
+                stays = np.array([s in left for s in before[b]])
+                for layer in range(self.n_layers):
+                    r["k"][layer] = [np.concatenate(r["k"][layer], axis=0)[stays]]
+                    r["v"][layer] = [np.concatenate(r["v"][layer], axis=0)[stays]]
+            r["len"] -= n_evict[b]
+        return total
 
     # ---- one decode step -----------------------------------------------------------------
     def step(self):
@@ -177,6 +212,7 @@ class DecodeDriver:
         B = self.B
         if B == 0:
             return None
+        evicted = self._evict()
         for r in self.rows:
             r["len"] += 1
         slab_ids = [self.slabs[r["prefix"]] for r in self.rows]
@@ -207,13 +243,15 @@ class DecodeDriver:
             for layer in range(self.n_layers):
                 out = self.cache.decode(layer, q_dev[layer], batch, self.plan,
                                         k_new=kd[layer] if fused else None, v_new=vd[layer] if fused else None)
+                if self.cold_budget is not None:
+                    self.cache.weigh(layer, q_dev[layer], out[1], batch)
             t_host = time.perf_counter() - t_issue
             e1.record(s)
             rec = {"dispatch_us": t_disp * 1e6, "host_us": t_host * 1e6, "mode": "eager"}
         self._keep_new([1] * B, ks, vs)
         self._events.append((e0, e1))
         groups = self.plan.groups()
-        rec.update({"B": B, "concurrent": self.plan.schedule()["concurrent"], "groups": [{"m_eff": g["m_eff"], "backend": gb.BACKEND_NAMES[g["backend"]],
+        rec.update({"B": B, "evicted": evicted, "concurrent": self.plan.schedule()["concurrent"], "groups": [{"m_eff": g["m_eff"], "backend": gb.BACKEND_NAMES[g["backend"]],
                                         "n_splits": g["n_splits"]} for g in groups]})
         self.trace.append(rec)
         if self.keep:
@@ -253,6 +291,7 @@ class DecodeDriver:
         self.ctx.dispatch(batch, self.plan)
         t_disp = time.perf_counter() - t0
         ws = self.cache.workspace(self.plan)
+        weight = self.cache.weight if self.cold_budget is not None else None  # made before the capture
 
         fused = self.fused
 
@@ -271,6 +310,8 @@ class DecodeDriver:
                 else:
                     self.ctx.decode_attention(layer, self._q_buf[layer], batch, self.plan, self._o_buf[layer],
                                               self._lse_buf[layer], ws, ws.numel(), st)
+                if weight is not None:
+                    self.ctx.cold_weigh(layer, self._q_buf[layer], self._lse_buf[layer], batch, weight, 1.0, st)
 
         e0.record(s)
         t1 = time.perf_counter()
@@ -306,14 +347,15 @@ class DecodeDriver:
 
 def run(*, steps: int = 64, n_layers: int = 2, prefix_lens=(16384, 4096), start_batch: int = 48,
         p_arrive: float = 0.25, p_complete: float = 0.02, prompt=(64, 512), seed: int = 0,
-        max_batch: int = 256, graph: bool = False, headroom: int = 16, fused_append: bool = True) -> Dict:
+        max_batch: int = 256, graph: bool = False, headroom: int = 16, fused_append: bool = True,
+        kv8: bool = False, cold_budget: Optional[int] = None) -> Dict:
     """Seeded arrival/completion schedule: each step, with probability p_arrive a request arrives
     (uniform prefix, uniform prompt length in `prompt`), and every active request completes with
     probability p_complete."""
     sched = np.random.default_rng(seed + 1)
     drv = DecodeDriver(prefix_lens=prefix_lens, n_layers=n_layers, max_batch=max_batch,
                        cap=max(prompt) + steps + headroom + 64, seed=seed, graph=graph, headroom=headroom,
-                       fused_append=fused_append)
+                       fused_append=fused_append, kv8=kv8, cold_budget=cold_budget)
     for i in range(start_batch):
         drv.arrive(int(sched.integers(len(prefix_lens))), int(sched.integers(prompt[0], prompt[1] + 1)))
     for _ in range(steps):
@@ -330,7 +372,7 @@ def run(*, steps: int = 64, n_layers: int = 2, prefix_lens=(16384, 4096), start_
     disp = [t["dispatch_us"] for t in trace]
     host = [t["host_us"] for t in trace]
     out = {"steps": steps, "layers": n_layers, "graph": graph, "B_min": min(t["B"] for t in trace),
-           "B_max": max(t["B"] for t in trace), "dense_fraction": n_dense / max(1, n_groups),
+           "B_max": max(t["B"] for t in trace), "kv8": kv8, "evicted": sum(t["evicted"] for t in trace), "dense_fraction": n_dense / max(1, n_groups),
            "gpu_us_per_step_median": statistics.median(gpu),
            "host_us_per_step_median": statistics.median(host),
            "host_share_of_step": statistics.median(h / g for h, g in zip(host, gpu)),
@@ -356,9 +398,12 @@ def main(argv=None):
     ap.add_argument("--p-arrive", type=float, default=0.25, help="chance of an arrival per step")
     ap.add_argument("--p-complete", type=float, default=0.02, help="chance per request of completing per step")
     ap.add_argument("--no-fused-append", action="store_true", help="append new K/V with launches of their own")
+    ap.add_argument("--kv8", action="store_true", help="keep the pools in 8 bits")
+    ap.add_argument("--cold-budget", type=int, default=None, help="COLD tokens a request may hold before a step")
     a = ap.parse_args(argv)
     res = run(steps=a.steps, n_layers=a.layers, seed=a.seed, graph=a.graph, headroom=a.headroom,
-              p_arrive=a.p_arrive, p_complete=a.p_complete, fused_append=not a.no_fused_append)
+              p_arrive=a.p_arrive, p_complete=a.p_complete, fused_append=not a.no_fused_append,
+              kv8=a.kv8, cold_budget=a.cold_budget)
     trace = res.pop("trace")
     if a.trace:
         for i, t in enumerate(trace):
