@@ -33,6 +33,8 @@ constexpr int32_t kDefaultMaxBatch = 4096;
 // at M_eff <= 32 (both are bandwidth-bound there) and falls far behind above, where its
 // warp-level MMAs run out of throughput.
 constexpr int32_t kDefaultMsat = 4;
+// 8-bit cache: the cascade backend is the CUDA-core kernel, so every group goes to the dense one.
+constexpr int32_t kDefaultMsatKv8 = 1;
 
 struct Extent {
   int64_t off, len;
@@ -161,7 +163,11 @@ bool has_device(const granikv_ctx* c) { return c && !c->cfg.host_only && c->d_ri
 
 // Which prefix implementation serves a group of this shape and backend.
 int32_t prefix_impl_for(const granikv_ctx* c, int32_t backend) {
-  if (c->kv8_row) return kImplKv8Generic;
+  if (c->kv8_row) {
+    const bool dense = backend == GRANIKV_BACKEND_DENSE && c->cfg.dtype == GRANIKV_DTYPE_BF16 &&
+                       c->cfg.head_dim == 128 && (c->has_tmaps || c->cfg.host_only);
+    return dense ? kImplKv8Dense : kImplKv8Generic;
+  }
   if (c->cfg.dtype == GRANIKV_DTYPE_BF16 && c->cfg.head_dim == 128) {
     if (backend == GRANIKV_BACKEND_DENSE && (c->has_tmaps || c->cfg.host_only)) return kImplDenseTc;
     if (c->g <= kCascadeStreamCols * kCascadeStreamWarps) return kImplCascadeStream;
@@ -179,9 +185,16 @@ bool runs_alone(int32_t impl) { return impl == kImplGeneric || impl == kImplDens
 
 // Which kernel attends the COLD suffix.
 int32_t suffix_impl_for(const granikv_ctx* c) {
-  if (c->kv8_row) return kImplKv8Generic;
-  return c->cfg.dtype == GRANIKV_DTYPE_BF16 && c->cfg.head_dim == 128 && c->g <= 8 ? kImplSuffixMma : kImplGeneric;
+  const bool mma = c->cfg.dtype == GRANIKV_DTYPE_BF16 && c->cfg.head_dim == 128 && c->g <= 8;
+  if (c->kv8_row) return mma ? kImplKv8Suffix : kImplKv8Generic;
+  return mma ? kImplSuffixMma : kImplGeneric;
 }
+
+// The suffix kernels that run one token-CTA per run and group of eight KV heads.
+bool token_ctas(int32_t suffix_impl) { return suffix_impl == kImplSuffixMma || suffix_impl == kImplKv8Suffix; }
+
+// The dense prefix kernels of the tensor-core path (16-bit and 8-bit cache).
+bool dense_tc(int32_t impl) { return impl == kImplDenseTc || impl == kImplKv8Dense; }
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no link-time libcuda).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -214,6 +227,20 @@ bool encode_pool_map(CUtensorMap* m, void* base, int64_t n_slots, int32_t n_kv) 
   return r == CUDA_SUCCESS;
 }
 
+// An 8-bit pool [n_slots, row bytes] as a byte matrix of its codes (head j at byte 128 j) with boxes
+// of 128 slots x one head's 128 codes, stored one row after the other.
+bool encode_kv8_map(CUtensorMap* m, void* base, int64_t n_slots, int32_t n_kv, int64_t row) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)n_kv * 128, (cuuint64_t)n_slots};
+  cuuint64_t strides[1] = {(cuuint64_t)row};
+  cuuint32_t box[2] = {128, (cuuint32_t)kDenseTile};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // q [B, n_q, 128] bf16 as a 3-D tensor (dim, head, request) with (64, g, 128/g) boxes: one box
 // is a dense row block's q rows of one 64-dim half, in the layout the operand descriptors expect.
 bool encode_q_map(CUtensorMap* m, const void* q, int32_t B, int32_t n_q, int32_t g) {
@@ -243,7 +270,8 @@ int32_t stream_sub_for(int32_t n_req, int32_t g) {
 // the streaming cascade kernel takes whole requests, as many as fit its query columns.
 int32_t rows_per_cta_for(int32_t impl, int32_t g, int32_t sub) {
   switch (impl) {
-    case kImplDenseTc: return kDenseRows;
+    case kImplDenseTc:
+    case kImplKv8Dense: return kDenseRows;
     case kImplDenseTf32: return kDenseTf32Rows;
     case kImplCascadeMma: return kCascadeRows;
     case kImplCascadeStream: return (kCascadeStreamCols * sub / g) * g;
@@ -253,7 +281,8 @@ int32_t rows_per_cta_for(int32_t impl, int32_t g, int32_t sub) {
 
 int32_t tile_tokens_for(int32_t impl, int32_t sub) {
   switch (impl) {
-    case kImplDenseTc: return kDenseTile;
+    case kImplDenseTc:
+    case kImplKv8Dense: return kDenseTile;
     case kImplDenseTf32: return kDenseTf32Tile;
     case kImplCascadeMma: return kCascadeTile;
     case kImplCascadeStream: return kCascadeStreamTile * sub;
@@ -472,7 +501,7 @@ granikv_status create_impl(const granikv_config* cfg, bool kv8, granikv_ctx** ou
   c->cfg.hot_fraction = fp;
   if (c->cfg.max_slabs == 0) c->cfg.max_slabs = kDefaultMaxSlabs;
   if (c->cfg.max_batch == 0) c->cfg.max_batch = kDefaultMaxBatch;
-  c->m_sat = cfg->m_sat ? cfg->m_sat : kDefaultMsat;
+  c->m_sat = cfg->m_sat ? cfg->m_sat : kv8 ? kDefaultMsatKv8 : kDefaultMsat;
   c->g = cfg->n_q / cfg->n_kv;
   c->n_hot = (int64_t)std::floor(fp * (double)cfg->n_slots);
   c->n_cold = cfg->n_slots - c->n_hot;
@@ -542,11 +571,16 @@ granikv_status create_impl(const granikv_config* cfg, bool kv8, granikv_ctx** ou
     if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&c->aux, cudaStreamNonBlocking);
     if (e == cudaSuccess) e = cudaEventCreateWithFlags(&c->ev_fork, cudaEventDisableTiming);
     if (e == cudaSuccess) e = cudaEventCreateWithFlags(&c->ev_join, cudaEventDisableTiming);
-    if (e == cudaSuccess && !kv8 && cfg->dtype == GRANIKV_DTYPE_BF16 && cfg->head_dim == 128 && c->cc_major == 10) {
+    if (e == cudaSuccess && cfg->dtype == GRANIKV_DTYPE_BF16 && cfg->head_dim == 128 && c->cc_major == 10) {
       c->tmap_k.resize(cfg->n_layers);
       c->tmap_v.resize(cfg->n_layers);
       bool ok = true;
       for (int32_t l = 0; l < cfg->n_layers && ok; ++l) {
+        if (kv8) {
+          ok = encode_kv8_map(&c->tmap_k[l], c->kpool[l], cfg->n_slots, cfg->n_kv, c->kv8_row) &&
+               encode_kv8_map(&c->tmap_v[l], c->vpool[l], cfg->n_slots, cfg->n_kv, c->kv8_row);
+          continue;
+        }
         ok = ((uintptr_t)c->kpool[l] % 16 == 0) && ((uintptr_t)c->vpool[l] % 16 == 0) &&
              encode_pool_map(&c->tmap_k[l], c->kpool[l], cfg->n_slots, cfg->n_kv) &&
              encode_pool_map(&c->tmap_v[l], c->vpool[l], cfg->n_slots, cfg->n_kv);
@@ -987,8 +1021,8 @@ granikv_status granikv_dispatch(granikv_ctx* c, const granikv_batch* bt, granikv
   }
   // Fused merge when every kernel of the step is a tensor-core kernel; then the suffix may run
   // next to the prefix on its own share of the SMs.
-  const bool fast_suffix_pre = suffix_impl_for(c) == kImplSuffixMma;
-  bool fused = c->fused_merge && (fast_suffix_pre || T_all == 0);
+  const bool fast_suffix_pre = token_ctas(suffix_impl_for(c));
+  bool fused = c->fused_merge && !c->kv8_row && (fast_suffix_pre || T_all == 0);
   for (int32_t i = 0; i < G; ++i)
     if (runs_alone(groups[i].impl)) fused = false;
   bool fast_all = fast_suffix_pre || T_all == 0;
@@ -1042,15 +1076,17 @@ granikv_status granikv_dispatch(granikv_ctx* c, const granikv_batch* bt, granikv
       // the suffix then bound by the bandwidth HBM gives its random 2 KB row reads (about
       // 5.8 TB/s measured), and the step's bytes bounding either way at about 5.9 TB/s.
       const int64_t head_groups = (n_kv + 7) / 8;
-      const double w_s = 1.40 * (double)head_groups * (double)T_tiles;
-      const double suffix_bytes = 4.0 * n_kv * c->cfg.head_dim * (double)T_all;
+      const double w_s = (c->kv8_row ? 0.75 : 1.40) * (double)head_groups * (double)T_tiles;
+      const double token_bytes = c->kv8_row ? 2.0 * (double)c->kv8_row : 4.0 * n_kv * c->cfg.head_dim;
+      const double suffix_bytes = token_bytes * (double)T_all;
       double prefix_bytes = 0.0;
-      for (int32_t i = 0; i < G; ++i) prefix_bytes += 4.0 * n_kv * c->cfg.head_dim * (double)groups[i].L_p;
+      for (int32_t i = 0; i < G; ++i) prefix_bytes += token_bytes * (double)groups[i].L_p;
       auto prefix_time = [&](int64_t cand) {
         double t_p = 0.0;
         for (int32_t i = 0; i < G; ++i) {
           const int64_t tile = tile_tokens_for(groups[i].impl, groups[i].sub);
           const double per_token = groups[i].impl == kImplDenseTc ? 0.0078
+                                   : groups[i].impl == kImplKv8Dense ? 0.0078
                                    : groups[i].impl == kImplCascadeStream
                                        ? 0.09 * std::min(n_kv, stream_heads(groups[i].sub)) / 8.0
                                        : 0.02;
@@ -1086,7 +1122,7 @@ granikv_status granikv_dispatch(granikv_ctx* c, const granikv_batch* bt, granikv
       // that shape, which covers it; with 4 / 2 / 0 us set aside for it the call took 82.9 /
       // 81.0 / 80.3 us, and at 0 both sides end within 0.4 us of each other.
       bool all_dense = G > 0 && n_kv <= 8;
-      for (int32_t i = 0; i < G; ++i) all_dense = all_dense && groups[i].impl == kImplDenseTc;
+      for (int32_t i = 0; i < G; ++i) all_dense = all_dense && dense_tc(groups[i].impl);
       if (auto_found && all_dense) {
         const double n_d = (double)ctas_for(lo), n_s = (double)c->num_sms - n_d;
         const double x = (w_s / n_s - prefix_time(lo)) / (1.0 / n_s + 1.0 / n_d);
@@ -1130,7 +1166,7 @@ granikv_status granikv_dispatch(granikv_ctx* c, const granikv_batch* bt, granikv
     w.grp_tail.assign(G, 0);
     bool all_dense = G > 0;
     for (int32_t i = 0; i < G; ++i)
-      all_dense = all_dense && groups[i].impl == kImplDenseTc && groups[i].L_p == groups[0].L_p;
+      all_dense = all_dense && dense_tc(groups[i].impl) && groups[i].L_p == groups[0].L_p;
     if (!concurrent && all_dense) {
       constexpr int64_t kCtaFixedTiles = 7;
       std::vector<int64_t>& key = w.tail_key_now;
@@ -1377,7 +1413,7 @@ granikv_status granikv_dispatch(granikv_ctx* c, const granikv_batch* bt, granikv
     while (wpr > 1 && rows * wpr > 16LL * c->num_sms) wpr /= 2;
     p->merge_warps = wpr;
   }
-  p->fused = fused && (T == 0 || suffix_impl == kImplSuffixMma);
+  p->fused = fused && (T == 0 || token_ctas(suffix_impl));
   p->concurrent = concurrent;
   // The dense CTAs of a split whose prefix side is estimated to end last, next to a suffix side
   // that reads at least as many bytes, read two tiles ahead into L2: their per-tile chain keeps
@@ -1419,7 +1455,7 @@ granikv_status granikv_plan_group(const granikv_plan* p, int32_t i, granikv_grou
 
 granikv_status granikv_plan_suffix_runs(const granikv_plan* p, int32_t* runs, int32_t* tail_runs) {
   if (!p || !p->valid) return GRANIKV_ERR_INVALID;
-  if (runs) *runs = p->suffix_impl == kImplSuffixMma ? p->n_scta : p->n_sitems;
+  if (runs) *runs = token_ctas(p->suffix_impl) ? p->n_scta : p->n_sitems;
   if (tail_runs) *tail_runs = p->n_tail;
   return GRANIKV_OK;
 }
@@ -1437,7 +1473,7 @@ granikv_status granikv_plan_schedule(const granikv_plan* p, int32_t* concurrent,
   if (prefix_ctas) *prefix_ctas = p->n_pitems;
   if (suffix_ctas) {
     const int32_t head_groups = (p->ctx->cfg.n_kv + 7) / 8;
-    *suffix_ctas = p->suffix_impl == kImplSuffixMma ? (p->n_scta - p->n_tail) * head_groups : p->n_sitems;
+    *suffix_ctas = token_ctas(p->suffix_impl) ? (p->n_scta - p->n_tail) * head_groups : p->n_sitems;
   }
   return GRANIKV_OK;
 }
@@ -1630,6 +1666,7 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
   auto launch_suffix = [&](cudaStream_t st, bool pdl) -> cudaError_t {
     if (p->n_sitems <= 0) return cudaSuccess;
     c->n_kernels += 1;
+    if (p->suffix_impl == kImplKv8Suffix) return launch_kv8_suffix(a, a.scta_begin, p->n_scta, st, pdl);
     if (p->suffix_impl == kImplKv8Generic) return launch_kv8_suffix_generic(c->cfg.dtype, a, st);
     return p->suffix_impl == kImplSuffixMma ? launch_suffix_mma(a, a.scta_begin, p->n_scta, st, pdl)
                                             : launch_suffix_generic(c->cfg.dtype, a, st);
@@ -1645,6 +1682,12 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
     if (r == cudaSuccess && p->pitem_count[kImplKv8Generic] > 0) {
       r = launch_kv8_prefix_generic(c->cfg.dtype, a, p->pitem_first[kImplKv8Generic], p->pitem_count[kImplKv8Generic],
                                     st);
+      c->n_kernels += 1;
+    }
+    if (r == cudaSuccess && p->pitem_count[kImplKv8Dense] > 0) {
+      if (!c->has_tmaps) return cudaErrorNotSupported;
+      r = launch_kv8_step(a, p->pitem_first[kImplKv8Dense], p->pitem_count[kImplKv8Dense], c->tmap_k[layer],
+                          c->tmap_v[layer], a.scta_begin, 0, 0, st, p->pitem_count[kImplKv8Generic] == 0);
       c->n_kernels += 1;
     }
     if (r == cudaSuccess && p->pitem_count[kImplDenseTf32] > 0) {
@@ -1682,6 +1725,17 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
     if (e != cudaSuccess) return cuda_status(e);
   }
   const int32_t n_dense = p->pitem_count[kImplDenseTc], n_casc = p->pitem_count[kImplCascadeStream];
+  const int32_t n_dense8 = p->pitem_count[kImplKv8Dense];
+  if (p->concurrent && p->n_pitems > 0 && n_dense8 == p->n_pitems && c->has_tmaps &&
+      p->suffix_impl == kImplKv8Suffix && p->n_sitems > 0) {
+    // one grid, as below
+    const int32_t n_tail = p->n_tail <= n_dense8 ? p->n_tail : 0;
+    e = launch_kv8_step(a, p->pitem_first[kImplKv8Dense], n_dense8, c->tmap_k[layer], c->tmap_v[layer], a.scta_begin,
+                        p->n_scta - n_tail, n_tail, s, true);
+    c->n_kernels += 1;
+    if (e == cudaSuccess) e = launch_merge_k(true);
+    return e == cudaErrorNotSupported ? GRANIKV_ERR_UNSUPPORTED : cuda_status(e);
+  }
   const bool one_launch = p->concurrent && p->n_pitems > 0 && n_dense + n_casc == p->n_pitems &&
                           (n_dense == 0 || c->has_tmaps) && p->suffix_impl == kImplSuffixMma && p->n_sitems > 0;
   if (one_launch) {
@@ -1711,8 +1765,8 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
   } else {
     e = launch_prefix(s);
     // the suffix kernel follows a prefix kernel of this call, the merge the suffix kernel
-    const bool after_prefix = p->n_pitems > 0 && n_dense + n_casc > 0;
-    if (e == cudaSuccess) e = launch_suffix(s, after_prefix && p->suffix_impl == kImplSuffixMma);
+    const bool after_prefix = p->n_pitems > 0 && n_dense + n_casc + n_dense8 > 0;
+    if (e == cudaSuccess) e = launch_suffix(s, after_prefix && token_ctas(p->suffix_impl));
     if (e == cudaSuccess && !p->fused) {
       // the merge's stream predecessor is this call's suffix kernel, or its prefix kernel when
       // the step has no COLD tokens; the merge waits (griddepcontrol.wait) before it reads a
@@ -1784,7 +1838,8 @@ granikv_status granikv_prefill_attention(granikv_ctx* c, int32_t layer, int32_t 
   if ((k_new == nullptr) != (v_new == nullptr)) return GRANIKV_ERR_INVALID;
   if ((uintptr_t)ws % 256) return GRANIKV_ERR_INVALID;
   if (!has_device(c)) return GRANIKV_ERR_NO_DEVICE;
-  if (c->cfg.dtype != GRANIKV_DTYPE_BF16 || c->cfg.head_dim != 128 || !c->has_tmaps) return GRANIKV_ERR_UNSUPPORTED;
+  if (c->kv8_row || c->cfg.dtype != GRANIKV_DTYPE_BF16 || c->cfg.head_dim != 128 || !c->has_tmaps)
+    return GRANIKV_ERR_UNSUPPORTED;
   const int32_t L_p = c->slabs[sid].len;
   const PrefillLayout lay = prefill_layout(c, L_p);
   if (ws_bytes < lay.total) return GRANIKV_ERR_INVALID;

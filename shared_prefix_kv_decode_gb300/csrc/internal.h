@@ -34,6 +34,8 @@ enum Impl : int32_t {
   kImplCascadeStream = 4,  // bf16, head_dim 128, g <= 128: cascade over whole 2 KB slot rows
   kImplDenseTf32 = 5,      // f32, head_dim % 32 == 0 up to 128: tcgen05 kind::tf32 dense kernel
   kImplKv8Generic = 6,     // 8-bit cache, any head_dim % 32 == 0 up to 256: CUDA-core kernel
+  kImplKv8Dense = 7,       // 8-bit cache, bf16 q, head_dim 128: tcgen05/TMEM dense kernel
+  kImplKv8Suffix = 8,      // 8-bit cache, bf16 q, head_dim 128, g <= 8: warp-level tensor-core suffix kernel
 };
 
 // Geometry of each prefix kernel: query rows per CTA and tokens per tile.  The planner and the
@@ -218,13 +220,19 @@ cudaError_t launch_kv8_append_newest(int32_t dtype, const AttnParams& p, cudaStr
 cudaError_t launch_kv8_prefix_generic(int32_t dtype, const AttnParams& p, int32_t first_item, int32_t n_items,
                                       cudaStream_t s);
 cudaError_t launch_kv8_suffix_generic(int32_t dtype, const AttnParams& p, cudaStream_t s);
+// Tensor-core path of the 8-bit cache (kernels_kv8_tc.cu): dense prefix items and suffix token-CTAs in
+// one grid (either count may be 0; n_tail as for launch_prefix_suffix_tc), and the suffix alone.
+cudaError_t launch_kv8_step(const AttnParams& p, int32_t first_dense, int32_t n_dense, const CUtensorMap& tmk,
+                            const CUtensorMap& tmv, const int32_t* cta_begin, int32_t n_scta, int32_t n_tail,
+                            cudaStream_t s, bool pdl);
+cudaError_t launch_kv8_suffix(const AttnParams& p, const int32_t* cta_begin, int32_t n_scta, cudaStream_t s, bool pdl);
 
 // Eviction (kernels_evict.cu)
 cudaError_t launch_cold_weigh(int32_t dtype, const WeighParams& p, const int32_t* seq_len /*host [B]*/, cudaStream_t s);
 cudaError_t launch_cold_evict(const EvictRow* rows, int32_t B, int32_t keep_last, int32_t* req_to_slot,
                               int32_t* suffix_len, float* weight, int32_t cap, int32_t* slots_out, cudaStream_t s);
 
-constexpr int kNumImpl = 7;
+constexpr int kNumImpl = 8;  // that a prefix group can run on
 
 }  // namespace granikv
 

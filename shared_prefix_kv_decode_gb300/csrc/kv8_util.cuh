@@ -44,30 +44,35 @@ __device__ __forceinline__ uint32_t f32x4_to_e4m3x4(float a, float b, float c, f
 }
 
 // A query row in fp16, scaled by a power of two so that its largest finite element lies in
-// [2^14, 2^15): W words of two bf16 a lane, the row spread over the four lanes of a quad.  bf16's 8
-// significant bits fit fp16's 11, so elements down to 2^-31 of the largest stay exact (fp16's last
-// subnormal is 2^-24), smaller ones are off by at most 2^-39 of it.  `unit` is the power of two
-// that undoes the scaling.
+// [2^14, 2^15).  bf16's 8 significant bits fit fp16's 11, so elements down to 2^-31 of the largest stay
+// exact (fp16's last subnormal is 2^-24), smaller ones are off by at most 2^-39 of it.
+__device__ __forceinline__ float bf16x2_finite_max(uint32_t w) {
+  const float a = fabsf(__uint_as_float(w << 16)), b = fabsf(__uint_as_float(w & 0xffff0000u));
+  return fmaxf(a < INFINITY ? a : 0.f, b < INFINITY ? b : 0.f);
+}
+// The power of two for a row whose largest finite element is amax, and the one that undoes it; both
+// are kept within what fp32 holds.
+__device__ __forceinline__ float q_factor(float amax, float& unit) {
+  const int e = (int)((__float_as_uint(amax) >> 23) & 255u);
+  const int up = amax == 0.f ? 127 : min(141 + 127 - e, 253);  // 2^(14 - exponent of amax)
+  unit = __uint_as_float((uint32_t)(254 - up) << 23);
+  return __uint_as_float((uint32_t)up << 23);
+}
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float f) {
+  const __half2 h = __floats2half2_rn(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// The same for a row spread over the four lanes of a quad, W words of two bf16 a lane.
 template <int W>
 __device__ __forceinline__ void q_to_f16(uint32_t* w, float& unit) {
   float amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < W; ++i) {
-    const float a = fabsf(__uint_as_float(w[i] << 16)), b = fabsf(__uint_as_float(w[i] & 0xffff0000u));
-    amax = fmaxf(amax, fmaxf(a < INFINITY ? a : 0.f, b < INFINITY ? b : 0.f));
-  }
+  for (int i = 0; i < W; ++i) amax = fmaxf(amax, bf16x2_finite_max(w[i]));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  // 2^(14 - exponent of amax), kept within what fp32 holds together with its inverse
-  const int e = (int)((__float_as_uint(amax) >> 23) & 255u);
-  const int up = amax == 0.f ? 127 : min(141 + 127 - e, 253);
-  const float f = __uint_as_float((uint32_t)up << 23);
-  unit = __uint_as_float((uint32_t)(254 - up) << 23);
+  const float f = q_factor(amax, unit);
 #pragma unroll
-  for (int i = 0; i < W; ++i) {
-    const __half2 h = __floats2half2_rn(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
+  for (int i = 0; i < W; ++i) w[i] = bf16x2_to_f16x2(w[i], f);
 }
 
 // |x| for a block's amax: infinities and NaN do not count.
