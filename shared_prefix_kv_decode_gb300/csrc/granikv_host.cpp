@@ -228,16 +228,17 @@ bool encode_pool_map(CUtensorMap* m, void* base, int64_t n_slots, int32_t n_kv) 
 }
 
 // An 8-bit pool [n_slots, row bytes] as a byte matrix of its codes (head j at byte 128 j) with boxes
-// of 128 slots x one head's 128 codes, stored one row after the other.
-bool encode_kv8_map(CUtensorMap* m, void* base, int64_t n_slots, int32_t n_kv, int64_t row) {
+// of `slots` x one head's 128 codes: with the 128-byte swizzle the operand descriptors expect (K), or
+// stored one row after the other (V, converted before it is an operand).
+bool encode_kv8_map(CUtensorMap* m, void* base, int64_t n_slots, int32_t n_kv, int64_t row, int32_t slots, bool swizzle) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[2] = {(cuuint64_t)n_kv * 128, (cuuint64_t)n_slots};
   cuuint64_t strides[1] = {(cuuint64_t)row};
-  cuuint32_t box[2] = {128, (cuuint32_t)kDenseTile};
+  cuuint32_t box[2] = {128, (cuuint32_t)slots};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                   swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
@@ -577,8 +578,8 @@ granikv_status create_impl(const granikv_config* cfg, bool kv8, granikv_ctx** ou
       bool ok = true;
       for (int32_t l = 0; l < cfg->n_layers && ok; ++l) {
         if (kv8) {
-          ok = encode_kv8_map(&c->tmap_k[l], c->kpool[l], cfg->n_slots, cfg->n_kv, c->kv8_row) &&
-               encode_kv8_map(&c->tmap_v[l], c->vpool[l], cfg->n_slots, cfg->n_kv, c->kv8_row);
+          ok = encode_kv8_map(&c->tmap_k[l], c->kpool[l], cfg->n_slots, cfg->n_kv, c->kv8_row, kDenseTile, true) &&
+               encode_kv8_map(&c->tmap_v[l], c->vpool[l], cfg->n_slots, cfg->n_kv, c->kv8_row, kKv8VBox, false);
           continue;
         }
         ok = ((uintptr_t)c->kpool[l] % 16 == 0) && ((uintptr_t)c->vpool[l] % 16 == 0) &&

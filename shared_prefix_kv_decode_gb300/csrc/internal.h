@@ -138,6 +138,7 @@ struct AttnParams {
 // head, padded to 16 bytes (value = code * scale).  Every row carries its own scales; the rows of
 // one 64-token block of a slab (kKv8Block, counted from the slab's start) hold the same ones.
 constexpr int kKv8Block = 64;
+constexpr int kKv8VBox = 32;  // slots of one TMA box of V's codes (dense kernel)
 constexpr float kE4m3Max = 448.0f;
 constexpr float kKv8AmaxMin = 1.2621774483536189e-29f;  // 2^-96: smallest amax a scale is made for
 __host__ __device__ inline int64_t kv8_row_bytes(int32_t n_kv, int32_t d) {

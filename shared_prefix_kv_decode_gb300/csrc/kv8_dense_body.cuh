@@ -3,28 +3,34 @@
 //
 // One CTA takes one (prefix group, KV head j, 128-row block, L_p piece), as the 16-bit dense kernel:
 // rows are the group's (request, head-in-group) pairs of KV head j, and for each 128-token tile i
-//     S(i) = Q K(i)^T       (8 tcgen05.mma 128x128x16, fp16 codes of K from shared memory)
+//     S(i) = Q K(i)^T       (8 tcgen05.mma 128x128x32, kind::f8f6f4: the codes of K as they are)
 //     P(i) = 2^(z - m)      (softmax warps; fp16, written back over S(i) in TMEM)
-//     O   += P(i) V(i)      (8 tcgen05.mma with A = P(i) read from TMEM, fp16 codes of V)
-// Number format.  Codes become fp16 exactly; q is brought into fp16's range by a power of two per
-// row (exact but for elements 2^-31 below the row's largest).  The scales of a slab are those of
-// 64-token blocks counted from its start, so each half of a tile has one K scale ks and one V scale
-// vs: z = s ks + log2 vs (base 2) costs the FMA that the softmax needs anyway, P = 2^(z - m) is p times
-// vs, which is what meets the V codes, and the row sum adds each half's sum of P once, over vs.  The
-// running maximum m is taken over z.  P carries a factor of 2^7: it is at most 2^15 (m may lag the row's
-// maximum by 2^8, see below), and fp16 keeps its 11 bits down to 2^-21 of the largest weight.
-// Roles (13 warps):
+//     O   += P(i) V(i)      (8 tcgen05.mma 128x128x16, fp16, with A = P(i) read from TMEM)
+// Number format.  S takes K's codes straight from TMA and q as the sum of two e4m3 values: each row is
+// scaled by a power of two so that its largest element lies in [2^7, 2^8), hi = e4m3(q) and lo =
+// e4m3(q - hi).  bf16 has 8 significant bits and each part 4, so q = hi + lo exactly down to 2^-2, 2^-9
+// of the row's largest element at the least; smaller elements are off by at most 2^-10 there, 2^-17 of
+// the largest (bf16 itself rounds an element by 2^-9 of its own size).  Two passes at fp8's rate
+// take the time of one in fp16, and no conversion stands before S.  V's codes become fp16 exactly:
+// P in 8 bits would lose the weights.
+// The scales of a slab are those of 64-token blocks counted from its start, so each half of a tile
+// has one K scale ks and one V scale vs: z = s ks + log2 vs (base 2) costs the FMA that the softmax
+// needs anyway, P = 2^(z - m) is p times vs, which is what meets the V codes, and the row sum adds each
+// half's sum of P once, over vs.  The running maximum m is taken over z.  P carries a factor of 2^7: it
+// is at most 2^15 (m may lag the row's maximum by 2^8, see below), and fp16 keeps its 11 bits down to 2^-21
+// of the largest weight.
+// Roles (14 warps):
 //  * warps 0-7, softmax and epilogue: warp w serves TMEM lanes 32*(w%4).. (row r = lane r), all 128
 //    columns of the tiles i with i % 2 == w / 4; the two warps of a row quarter take turns, half a
 //    tile apart.  The running max is a chain over the tiles: the warp of tile i reads the max used
 //    for tile i-1 from shared memory, keeps it unless the tile's row max exceeds it by more than
 //    2^8 (then O is rescaled in TMEM), and publishes its own.
-//  * warps 8-9 (K) and 10-11 (V), conversion: the tile's codes arrive by TMA (a box of 128 tokens x
-//    128 bytes, two in flight for each of K and V); each thread turns 16 codes at a time into fp16
-//    and stores them in the 128-byte-swizzled layout that the MMA operands have.  Rows of V past
-//    the piece's end are stored as zeros.  The pair's first lane then refills the box.
+//  * warps 8-11, V conversion: each takes 32 tokens of every V tile.  It loads their codes by TMA into
+//    its own ring of three, turns 16 codes at a time into fp16 and stores them in the
+//    128-byte-swizzled layout that the MMA operand has (rows past the piece's end as zeros).
 //  * warp 12, the MMAs, issued as their inputs become ready: S(j) up to three tiles ahead of the PV
 //    products (three S/P buffers in TMEM).
+//  * warp 13, the TMA loads of K.
 // Every mbarrier wait is bounded in time; on expiry the CTA raises an abort flag, latches an error,
 // drains what it issued and frees its TMEM.
 #pragma once
@@ -48,32 +54,36 @@ using k8s::pack_f16;
 constexpr int kD = 128;
 constexpr int kM = kDenseRows;                // 128 query rows per CTA
 constexpr int kN = kDenseTile;                // 128 tokens per tile
+static_assert(kN / 4 == kKv8VBox, "a conversion warp's part of a V tile is one box");
 static_assert(kN == 2 * kKv8Block, "each half of a tile is one block of the slab");
-constexpr int kSlots = 2;                     // slots of each ring: fp16 K, fp16 V, codes of K, codes of V
+constexpr int kKSlots = 3;                    // slots of the K ring (codes)
+constexpr int kVSlots = 3;                    // slots of the V ring (fp16)
+constexpr int kCSlots = 3;                    // slots of each conversion warp's ring of V codes
 constexpr int kSBufs = 3;                     // S/P buffers in TMEM
 constexpr int kSoftmaxWarps = 8;
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
-constexpr int kWarpConv = 8, kConvThreads = 64;  // warps 8, 9: K; 10, 11: V
-constexpr int kWarpMma = 12;
-constexpr int kThreads = 416;
+constexpr int kWarpConv = 8, kConvWarps = 4;
+constexpr int kPart = kN / kConvWarps;        // tokens of a V tile that one warp converts
+constexpr int kWarpMma = 12, kWarpTmaK = 13;
+constexpr int kThreads = 448;
 constexpr int kHalf = kN * 128;               // one 64-dim half of an fp16 tile: 16 KB
 constexpr int kTile = 2 * kHalf;              // 32 KB
 constexpr int kCodes = kN * kD;               // a tile's codes: 16 KB
-constexpr int kQBytes = kM * kD * 2;          // 32 KB (two 64-dim K-blocks)
+constexpr int kPartCodes = kPart * kD;        // 4 KB
+constexpr int kQPart = kM * kD;               // hi (or lo) of the Q block: 16 KB
 constexpr int kOffQ = 0;
-constexpr int kOffK = kOffQ + kQBytes;
-constexpr int kOffV = kOffK + kSlots * kTile;
-constexpr int kOffCodes = kOffV + kSlots * kTile;  // codes of K: slots 0, 1; of V: slots 2, 3
-constexpr int kOffUnit = kOffCodes + 2 * kSlots * kCodes;  // [kM] power of two that undoes a row's scaling
-constexpr int kOffBar = kOffUnit + kM * 4;
-constexpr int kBarArea = 320;
-// [4 quarters][2 tile parities][32 rows] published maxima: in the unit array's place they would
-// have to wait for it to be read, so they have their own
-constexpr int kOffMPub = kOffBar + kBarArea;
-constexpr int kSmemBytes = kOffMPub + 4 * 2 * 32 * 4 + 1024;  // + alignment slack
+constexpr int kOffK = kOffQ + 2 * kQPart;
+constexpr int kOffV = kOffK + kKSlots * kCodes;
+constexpr int kOffCodes = kOffV + kVSlots * kTile;
+constexpr int kOffUnit = kOffCodes + kConvWarps * kCSlots * kPartCodes;  // [kM] power of two that undoes a row's scaling
+constexpr int kOffMPub = kOffUnit + kM * 4;   // [4 quarters][2 tile parities][32 rows] published maxima
+constexpr int kOffBar = kOffMPub + 4 * 2 * 32 * 4;
+constexpr int kBarArea = 448;
+constexpr int kSmemBytes = kOffBar + kBarArea + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-static_assert(kSlots * kTile >= kM * kD * 4, "the epilogue stages the fp32 record rows in the K ring");
-static_assert(kSlots * kTile >= kM * 8, "the epilogue keeps the rows' record offsets in the V ring");
+static_assert(kVSlots * kTile >= kM * kD * 4, "the epilogue stages the fp32 record rows in the V ring");
+static_assert(kKSlots * kCodes >= kM * 8, "the epilogue keeps the rows' record offsets in the K ring");
+static_assert(kConvWarps * kCSlots * kPartCodes >= 4 * kM * 4, "the epilogue's sums and maxima");
 constexpr uint32_t kTmemCols = 512;           // S/P buffers at 0, 128, 256; O at 384
 constexpr uint32_t kColO = 384;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -82,13 +92,12 @@ constexpr float kShift = 7.0f;                // log2 of the factor that P carri
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 enum : int {
-  kBarCFull = 0,                            // [2 * kSlots] TMA -> conversion (codes of K, then of V)
-  kBarCEmpty = kBarCFull + 2 * kSlots,      // [2 * kSlots] conversion has read the codes -> its first lane
-  kBarKFull = kBarCEmpty + 2 * kSlots,      // [kSlots] conversion -> MMA (kConvThreads arrivals)
-  kBarKEmpty = kBarKFull + kSlots,          // [kSlots] MMA (S done) -> conversion
-  kBarVFull = kBarKEmpty + kSlots,          // [kSlots]
-  kBarVEmpty = kBarVFull + kSlots,          // [kSlots] MMA (PV done) -> conversion
-  kBarSFull = kBarVEmpty + kSlots,          // [kSBufs] S(i) in TMEM -> softmax
+  kBarKFull = 0,                            // [kKSlots] TMA -> MMA
+  kBarKEmpty = kBarKFull + kKSlots,         // [kKSlots] MMA (S done) -> TMA
+  kBarCFull = kBarKEmpty + kKSlots,         // [kConvWarps][kCSlots] TMA -> conversion (codes of V)
+  kBarVFull = kBarCFull + kConvWarps * kCSlots,  // [kVSlots] conversion -> MMA (kConvWarps arrivals)
+  kBarVEmpty = kBarVFull + kVSlots,         // [kVSlots] MMA (PV done) -> conversion
+  kBarSFull = kBarVEmpty + kVSlots,         // [kSBufs] S(i) in TMEM -> softmax
   kBarPFull = kBarSFull + kSBufs,           // [kSBufs] P(i) in TMEM -> MMA (128 arrivals)
   kBarPvDone = kBarPFull + kSBufs,          // [kSBufs] PV(i) done -> softmax
   kBarDrain = kBarPvDone + kSBufs,          // all MMAs done -> teardown
@@ -98,8 +107,19 @@ enum : int {
 };
 static_assert(8 * kNumBars + 16 <= kBarArea, "barrier area");
 
-// Instruction descriptor of tcgen05.mma kind::f16 with fp16 A and B, fp32 accumulator, A K-major.
-__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
+// D[tmem] (+)= A[smem desc] * B[smem desc], kind::f8f6f4, issued by one thread
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor with A and B of the kind's format 0 (fp16 of kind::f16, e4m3 of
+// kind::f8f6f4), fp32 accumulator, A K-major.
+__host__ __device__ constexpr uint32_t idesc_fmt0_f32(int M, int N, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
@@ -112,12 +132,18 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int3
 __device__ __forceinline__ void tma_prefetch_l2_2d(const void* tmap, int32_t x, int32_t y) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(tmap), "r"(x), "r"(y) : "memory");
 }
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 x;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(a));
+  return x;
+}
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
 // Prefix work item `item` (one CTA) on `smem_raw` (at least kSmemBytes), run by kThreads threads.
-// tmk/tmv: the layer's K and V pools as byte matrices [n_slots, row bytes], boxes of 128 x 128.
+// tmk/tmv: the layer's K and V pools as byte matrices [n_slots, row bytes]: K in boxes of 128 slots x
+// 128 bytes with the 128-byte swizzle, V in boxes of 32 slots x 128 bytes, row after row.
 __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item, const CUtensorMap* tmk,
                                                const CUtensorMap* tmv, unsigned char* smem_raw) {
   // 1024-byte alignment for the 128-byte-swizzle atoms
@@ -148,20 +174,24 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
   const int32_t rbase = it.row_block * kM;
   const int64_t first_slot = gr.slab_off + t0;
 
-  // codes of tile i of K (which = 0) or V into slot i % kSlots
-  auto issue_codes = [&](int which, int i) {
-    const int c = which * kSlots + i % kSlots;
-    mbar_arrive_expect_tx(bar(kBarCFull + c), kCodes);
-    tma_load_2d(sC + c * kCodes, which ? tmv : tmk, j * kD, (int32_t)(first_slot + i * kN), bar(kBarCFull + c));
+  auto issue_k = [&](int i) {
+    const int st = i % kKSlots;
+    mbar_arrive_expect_tx(bar(kBarKFull + st), kCodes);
+    tma_load_2d(sK + st * kCodes, tmk, j * kD, (int32_t)(first_slot + (int64_t)i * kN), bar(kBarKFull + st));
+  };
+  // conversion warp w's part of V tile i
+  auto issue_v = [&](int w, int i) {
+    const int c = w * kCSlots + i % kCSlots;
+    mbar_arrive_expect_tx(bar(kBarCFull + c), kPartCodes);
+    tma_load_2d(sC + c * kPartCodes, tmv, j * kD, (int32_t)(first_slot + (int64_t)i * kN + w * kPart), bar(kBarCFull + c));
   };
   const int l2_ahead = p.l2_ahead;
-  if (warp == kWarpConv && lane == 0) {
+  if (warp == kWarpTmaK && lane == 0) {
     tma_prefetch_desc(tmk);
     tma_prefetch_desc(tmv);
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1u;
-      if (i >= kBarCEmpty && i < kBarCEmpty + 2 * kSlots) count = kConvThreads;
-      if ((i >= kBarKFull && i < kBarKFull + kSlots) || (i >= kBarVFull && i < kBarVFull + kSlots)) count = kConvThreads;
+      if (i >= kBarVFull && i < kBarVFull + kVSlots) count = kConvWarps;
       if (i >= kBarPFull && i < kBarPFull + kSBufs) count = kSoftmaxThreads / 2;
       if (i >= kBarPair && i < kBarPair + 4) count = 64u;
       if (i >= kBarMPub && i < kBarMPub + 8) count = 32u;
@@ -172,11 +202,11 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
     mbar_fence_init();
     fence_proxy_async_smem();
     grid_dep_wait();  // the slab may have been written by the work before this kernel
-    if (slab_ok)
-      for (int i = 0; i < min(n_tiles, kSlots); ++i) {
-        issue_codes(0, i);
-        issue_codes(1, i);
-      }
+    if (slab_ok) {
+      for (int i = 0; i < min(n_tiles, kKSlots); ++i) issue_k(i);
+      for (int i = 0; i < min(n_tiles, kCSlots); ++i)
+        for (int w = 0; w < kConvWarps; ++w) issue_v(w, i);
+    }
   }
   if (warp == 0) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
@@ -185,9 +215,9 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
   // q and the records are touched only after the previous kernel in the stream has completed
   grid_dep_wait();
   grid_dep_launch_dependents();
-  // Q rows of this block -> shared memory in fp16, K-major with 128-byte swizzle: row r, 16-byte
-  // chunk c lives in 64-dim block c/8 at r*128 + ((c%8) ^ (r%8))*16; rows past the group are 0.  The 16
-  // lanes that hold a row agree on its power of two.
+  // Q rows of this block -> shared memory as hi and lo, K-major with 128-byte swizzle: row r, 16-byte
+  // chunk c lives at r*128 + ((c%8) ^ (r%8))*16 of each; rows past the group are 0.  The 16 lanes that
+  // hold a row, 8 elements each, agree on its power of two.
   {
     constexpr int kQIters = (kM * 16 + kThreads - 1) / kThreads;
     int32_t qoff[kQIters];
@@ -218,12 +248,23 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
 #pragma unroll
       for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       float unit;
-      const float f = q_factor(amax, unit);
+      const float f = q_factor<7>(amax, unit);
+      uint32_t hi[2], lo[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = bf16x2_to_f16x2(w[i], f);
+      for (int i = 0; i < 2; ++i) {
+        const float a = __uint_as_float(w[2 * i] << 16) * f, b = __uint_as_float(w[2 * i] & 0xffff0000u) * f;
+        const float c = __uint_as_float(w[2 * i + 1] << 16) * f, d = __uint_as_float(w[2 * i + 1] & 0xffff0000u) * f;
+        // an infinity becomes NaN, as the scores it stands in would end
+        hi[i] = f32x4_to_e4m3x4(a + 0.f * a, b + 0.f * b, c + 0.f * c, d + 0.f * d);
+        float h[4];
+        e4m3x4_to_f32x4(hi[i], h);
+        lo[i] = f32x4_to_e4m3x4(a - h[0], b - h[1], c - h[2], d - h[3]);
+      }
       if (idx < kM * 16) {
         const int r = idx >> 4, c = idx & 15;
-        sts128(sQ + (c >> 3) * (kM * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
+        const uint32_t at = sQ + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
+        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + kQPart), "r"(lo[0]), "r"(lo[1]) : "memory");
         if (c == 0) units[r] = unit;
       }
     }
@@ -235,67 +276,99 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
   const uint32_t tmem = *tmem_slot;
 
   if (warp >= kWarpConv && warp < kWarpMma) {
-    // ---------------- conversion: codes -> fp16 operand tiles ----------------
-    const int which = (warp - kWarpConv) >> 1;  // 0: K, 1: V
-    const int ct = tid - (kWarpConv + 2 * which) * 32;
-    const uint32_t dst0 = which ? sV : sK;
-    const int full = which ? kBarVFull : kBarKFull, empty = which ? kBarVEmpty : kBarKEmpty;
-    int issued = slab_ok ? min(n_tiles, kSlots) : 0, seen = 0;
+    // ---------------- conversion: codes of V -> fp16 operand tiles ----------------
+    // lane: dims 16 * (lane % 8) .. of tokens lane / 8 + 4 n of the part, which become two 16-byte chunks
+    // of the token's row in 64-dim half lane % 8 / 4.  Lanes of the upper half store theirs in the other
+    // order, so a store instruction covers all banks.
+    constexpr int kPer = kPart / 4;
+    const int w = warp - kWarpConv;
+    const bool upper = (lane & 7) >= 4;
+    const int lt = lane >> 3;
+    const uint32_t src_off = (uint32_t)lt * kD + (lane & 7) * 16;
+    const uint32_t row_off = (uint32_t)w * kPart * 128 + (upper ? kHalf : 0) + (uint32_t)lt * 128;
+    const uint32_t ch = (lane & 3) * 2;
+    // tokens lt and lt + 4 modulo 8 have two swizzles
+    const uint32_t lo0 = row_off + ((ch ^ lt) << 4), hi0 = row_off + (((ch + 1) ^ lt) << 4);
+    const uint32_t lo1 = row_off + ((ch ^ (lt + 4)) << 4), hi1 = row_off + (((ch + 1) ^ (lt + 4)) << 4);
+    int issued = slab_ok ? min(n_tiles, kCSlots) : 0, seen = 0;
     for (int i = 0; slab_ok && i < n_tiles; ++i) {
-      const int st = i % kSlots, c = which * kSlots + st;
-      bool ok = mbar_wait_bounded(bar(kBarCFull + c), (i / kSlots) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
-      if (ok && i >= kSlots)
-        ok = mbar_wait_bounded(bar(empty + st), ((i / kSlots) - 1) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
+      const int c = w * kCSlots + i % kCSlots, st = i % kVSlots;
+      bool ok = mbar_wait_bounded(bar(kBarCFull + c), (i / kCSlots) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;  // the abort flag is up: every other role leaves as well
-      const int valid = t1 - t0 - i * kN;  // tokens of the tile in range (may exceed kN)
-      const uint32_t src = sC + c * kCodes, dst = dst0 + st * kTile;
-      // 16 codes at a time: chunk idx is token idx / 8, dims 16 * (idx % 8) ..; they become two 16-byte
-      // chunks of the token's row in 64-dim half idx % 8 / 4.  Lanes of the upper half store theirs
-      // in the other order, so a store instruction covers all banks.
-      const int k16 = ct & 7, half = k16 >> 2, ch = (k16 & 3) * 2;
-#pragma unroll 4
-      for (int n = 0; n < kN * 8 / kConvThreads; ++n) {
-        const int tok = (ct >> 3) + n * (kConvThreads / 8);
-        uint4 x;
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                     : "r"(src + tok * kD + k16 * 16));
-        if (which && tok >= valid) x = make_uint4(0u, 0u, 0u, 0u);  // 0 * whatever lies there must not reach O
-        uint32_t lo[4], hi[4];
-        e4m3x4_to_f16x4(x.x, lo[0], lo[1]);
-        e4m3x4_to_f16x4(x.y, lo[2], lo[3]);
-        e4m3x4_to_f16x4(x.z, hi[0], hi[1]);
-        e4m3x4_to_f16x4(x.w, hi[2], hi[3]);
-        const uint32_t row = dst + half * kHalf + tok * 128;
-        const uint32_t a = row + ((ch ^ (tok & 7)) << 4), b = row + (((ch + 1) ^ (tok & 7)) << 4);
-        if (half) {
-          sts128(b, hi[0], hi[1], hi[2], hi[3]);
-          sts128(a, lo[0], lo[1], lo[2], lo[3]);
+      seen = i + 1;
+      const uint32_t src = sC + c * kPartCodes + src_off, dst = sV + st * kTile;
+      uint4 x[kPer];
+#pragma unroll
+      for (int n = 0; n < kPer; ++n) x[n] = lds128(src + n * 4 * kD);
+      const int valid = t1 - t0 - i * kN - w * kPart;  // tokens of the part in range, or more
+      if (valid < kPart) {  // 0 * whatever lies past the piece must not reach O
+#pragma unroll
+        for (int n = 0; n < kPer; ++n)
+          if (lt + 4 * n >= valid) x[n] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (i >= kVSlots) {
+        ok = mbar_wait_bounded(bar(kBarVEmpty + st), ((i / kVSlots) - 1) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+      }
+#pragma unroll
+      for (int n = 0; n < kPer; ++n) {
+        uint32_t y[8];
+        e4m3x4_to_f16x4(x[n].x, y[0], y[1]);
+        e4m3x4_to_f16x4(x[n].y, y[2], y[3]);
+        e4m3x4_to_f16x4(x[n].z, y[4], y[5]);
+        e4m3x4_to_f16x4(x[n].w, y[6], y[7]);
+        const uint32_t lo = dst + n * 4 * 128 + (n & 1 ? lo1 : lo0), hi = dst + n * 4 * 128 + (n & 1 ? hi1 : hi0);
+        if (upper) {
+          sts128(hi, y[4], y[5], y[6], y[7]);
+          sts128(lo, y[0], y[1], y[2], y[3]);
         } else {
-          sts128(a, lo[0], lo[1], lo[2], lo[3]);
-          sts128(b, hi[0], hi[1], hi[2], hi[3]);
+          sts128(lo, y[0], y[1], y[2], y[3]);
+          sts128(hi, y[4], y[5], y[6], y[7]);
         }
       }
       fence_proxy_async_smem();
-      mbar_arrive(bar(full + st));
-      seen = i + 1;
-      if (i + kSlots < n_tiles) {
-        mbar_arrive(bar(kBarCEmpty + c));
-        if (ct == 0) {
-          // the pair has read the codes
-          if (!mbar_wait_bounded(bar(kBarCEmpty + c), (i / kSlots) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs))
-            break;
-          issue_codes(which, i + kSlots);
-          if (l2_ahead > 0 && i + kSlots + l2_ahead < n_tiles)
-            tma_prefetch_l2_2d(which ? tmv : tmk, j * kD, (int32_t)(first_slot + (int64_t)(i + kSlots + l2_ahead) * kN));
-          issued = i + kSlots + 1;
+      __syncwarp();  // the warp has stored its part, and read its codes
+      if (lane == 0) {
+        mbar_arrive(bar(kBarVFull + st));
+        if (i + kCSlots < n_tiles) {
+          issue_v(w, i + kCSlots);
+          if (l2_ahead > 0 && i + kCSlots + l2_ahead < n_tiles)
+            tma_prefetch_l2_2d(tmv, j * kD, (int32_t)(first_slot + (int64_t)(i + kCSlots + l2_ahead) * kN + w * kPart));
+          issued = i + kCSlots + 1;
         }
       }
     }
-    if (ct == 0) {
-      // never leave with a copy in flight
+    // never leave with a copy in flight
+    if (lane == 0) {
       for (int i = seen; i < issued; ++i) {
         const uint64_t t_start = globaltimer_ns();
-        while (!mbar_try_wait(bar(kBarCFull + which * kSlots + i % kSlots), (i / kSlots) & 1)) {
+        while (!mbar_try_wait(bar(kBarCFull + w * kCSlots + i % kCSlots), (i / kCSlots) & 1)) {
+          if (globaltimer_ns() - t_start > kWaitLimitNs) {
+            atomicCAS(p.err, 0, kDevTimeout);
+            break;
+          }
+        }
+      }
+    }
+  } else if (warp == kWarpTmaK) {
+    // ---------------- TMA loads of K ----------------
+    if (lane == 0) {
+      int issued = slab_ok ? min(n_tiles, kKSlots) : 0;
+      for (int i = issued; slab_ok && i < n_tiles; ++i) {
+        if (!mbar_wait_bounded(bar(kBarKEmpty + i % kKSlots), ((i / kKSlots) - 1) & 1, abort_flag, p.err, kDevTimeout,
+                               kWaitLimitNs))
+          break;
+        issue_k(i);
+        if (l2_ahead > 0 && i + l2_ahead < n_tiles)
+          tma_prefetch_l2_2d(tmk, j * kD, (int32_t)(first_slot + (int64_t)(i + l2_ahead) * kN));
+        issued = i + 1;
+      }
+      // never leave with a copy in flight
+      for (int i = max(0, issued - kKSlots); i < issued; ++i) {
+        const uint64_t t_start = globaltimer_ns();
+        while (!mbar_try_wait(bar(kBarKFull + i % kKSlots), (i / kKSlots) & 1)) {
           if (globaltimer_ns() - t_start > kWaitLimitNs) {
             atomicCAS(p.err, 0, kDevTimeout);
             break;
@@ -306,8 +379,8 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
   } else if (warp == kWarpMma) {
     // ---------------- MMA issuer ----------------
     if (lane == 0 && !*abort_flag) {
-      constexpr uint32_t idS = idesc_f16_f32(kM, kN, false);
-      constexpr uint32_t idO = idesc_f16_f32(kM, kD, true);
+      constexpr uint32_t idS = idesc_fmt0_f32(kM, kN, false);
+      constexpr uint32_t idO = idesc_fmt0_f32(kM, kD, true);
       const uint64_t dq0 = smem_desc_sw128(sQ, 16, 1024);
       const uint64_t dk0 = smem_desc_sw128(sK, 16, 1024);
       // V tile as an MN-major B operand: 16 tokens per step (2048 bytes), the two 64-dim halves
@@ -318,15 +391,16 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
       // free: S(j) overwrites S(j-3)/P(j-3), so it may go in once PV(j-3) has been issued (MMAs of one
       // thread execute in order; the softmax was done with S(j-3) before it produced P(j-3)).
       int next_s = 0, next_pv = 0;
-      uint64_t t_last = globaltimer_ns();
+      uint64_t t_last = 0;  // when it was first seen waiting
+      int idle = 0;
       while (next_pv < n_tiles) {
         bool progressed = false;
         if (next_pv < next_s) {
           const int i = next_pv;
-          const int st = i % kSlots;
+          const int st = i % kVSlots;
           const int sb = i % kSBufs;
           if (mbar_test_wait(bar(kBarPFull + sb), (i / kSBufs) & 1) &&
-              mbar_test_wait(bar(kBarVFull + st), (i / kSlots) & 1)) {
+              mbar_test_wait(bar(kBarVFull + st), (i / kVSlots) & 1)) {
             tc_fence_after();
             const uint32_t pa = tmem + (uint32_t)(sb * kN);  // P(i): 64 columns, two tokens per column
             const uint64_t dv = dv0 + (uint64_t)((st * kTile) >> 4);
@@ -343,17 +417,15 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
         }
         if (next_s < n_tiles && next_s < next_pv + kSBufs) {
           const int i = next_s;
-          const int st = i % kSlots;
-          if (mbar_test_wait(bar(kBarKFull + st), (i / kSlots) & 1)) {
+          const int st = i % kKSlots;
+          if (mbar_test_wait(bar(kBarKFull + st), (i / kKSlots) & 1)) {
             tc_fence_after();
             const uint32_t dS = tmem + (uint32_t)((i % kSBufs) * kN);
-            const uint64_t dk = dk0 + (uint64_t)((st * kTile) >> 4);
+            const uint64_t dk = dk0 + (uint64_t)((st * kCodes) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint64_t a = dq0 + (uint64_t)(((kk >> 2) * (kM * 128) + (kk & 3) * 32) >> 4);
-              const uint64_t b = dk + (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
-              umma_f16(dS, a, b, idS, kk > 0 ? 1u : 0u);
-            }
+            for (int kk = 0; kk < 8; ++kk)  // lo, the smaller, first
+              umma_f8(dS, dq0 + (uint64_t)(((kk < 4 ? kQPart : 0) + (kk & 3) * 32) >> 4), dk + (uint64_t)(((kk & 3) * 32) >> 4),
+                      idS, kk > 0 ? 1u : 0u);
             umma_commit(bar(kBarSFull + i % kSBufs));
             umma_commit(bar(kBarKEmpty + st));
             committed += 2;
@@ -361,14 +433,21 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
             progressed = true;
           }
         }
+        // the clock is read on every 64th idle round only
         if (progressed) {
-          t_last = globaltimer_ns();
+          idle = 0;
+          t_last = 0;
         } else if (*abort_flag) {
           break;
-        } else if (globaltimer_ns() - t_last > kWaitLimitNs) {
-          *abort_flag = 1;
-          atomicCAS(p.err, 0, (int32_t)kDevTimeout);
-          break;
+        } else if ((++idle & 63) == 0) {
+          const uint64_t now = globaltimer_ns();
+          if (t_last == 0) {
+            t_last = now;
+          } else if (now - t_last > kWaitLimitNs) {
+            *abort_flag = 1;
+            atomicCAS(p.err, 0, (int32_t)kDevTimeout);
+            break;
+          }
         }
       }
       // drain: every tcgen05 op this thread issued completes before the CTA frees TMEM
@@ -576,7 +655,7 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
       // has completed), 16-byte chunk c of row r at chunk c ^ (r % 32), so that a warp's 32
       // rows hit all banks; the pair then stores whole 512-byte rows, one per warp instruction.
       fence_proxy_async_smem();
-      unsigned char* stage = smem + kOffK;
+      unsigned char* stage = smem + kOffV;
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -589,7 +668,7 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
       if (half == 0) {
         const float m_fin = m_used == -INFINITY ? 0.f : m_used;
         const float lse_row = lt == 0.f ? -INFINITY : (m_fin - kShift + log2f(lt)) * kLn2;
-        reinterpret_cast<int64_t*>(smem + kOffV)[r] = rec >= 0 ? ((int64_t)rec * p.n_q + h) * kD : -1;
+        reinterpret_cast<int64_t*>(smem + kOffK)[r] = rec >= 0 ? ((int64_t)rec * p.n_q + h) * kD : -1;
         if (rec >= 0) st_record(p.rec_lse + (int64_t)rec * p.n_q + h, lse_row, l2_policy_keep());
       }
     }
@@ -600,8 +679,8 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
     ++pair_phase;
     staged = __all_sync(0xffffffffu, staged) && ok;
     if (staged) {
-      const unsigned char* stage = smem + kOffK;
-      const int64_t* sdst = reinterpret_cast<const int64_t*>(smem + kOffV);
+      const unsigned char* stage = smem + kOffV;
+      const int64_t* sdst = reinterpret_cast<const int64_t*>(smem + kOffK);
       const uint64_t keep = l2_policy_keep();
 #pragma unroll 4
       for (int i = 0; i < 16; ++i) {

@@ -18,7 +18,7 @@
 // tokens x two dims, which one byte permutation turns into the two A registers of O^T's dims 2 r
 // and 2 r + 1.
 //
-// Loads: the plan's token-CTA runs, as in the 16-bit kernel.  A producer warp streams 16-token
+// Loads: the plan's token-CTA runs, as in the 16-bit kernel.  Producer warps stream 16-token
 // tiles through a 6-stage shared-memory ring, one cp.async.bulk for each token's packed K and V row
 // (1,056 bytes for eight heads: codes and scales arrive together), so a CTA keeps up to 200 KB in
 // flight.  Rows are 1,072 bytes apart, which puts the eight rows an ldmatrix reads into eight
@@ -41,7 +41,9 @@ constexpr int kD = 128;
 constexpr int kTile = 16;                          // tokens per tile (MMA M)
 constexpr int kStages = 6;
 constexpr int kWarps = 8;                          // consumer warps: KV heads per CTA
-constexpr int kThreads = (kWarps + 1) * 32;        // + the producer warp
+constexpr int kProducers = 4;                      // producer warps: a quarter of a tile's rows each
+constexpr int kRowsEach = kTile / kProducers;
+constexpr int kThreads = (kWarps + kProducers) * 32;
 constexpr int kRowMax = kWarps * (kD + 4);         // packed row of eight heads: 1,056 B
 constexpr int kRowStride = kRowMax + 16;           // 1,072 B: 48 modulo 128
 constexpr int kTileBytes = kTile * kRowStride;
@@ -117,7 +119,7 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
   for (int k = threadIdx.x; k < min(n_seg, kSegSmem); k += blockDim.x) sseg[k] = item(k);
   if (threadIdx.x == 0) {
     for (int st = 0; st < kStages; ++st) {
-      mbar_init(full_bar(st), 1);
+      mbar_init(full_bar(st), kProducers);
       mbar_init(empty_bar(st), (uint32_t)nh);
     }
     *abort_flag = 0;
@@ -137,13 +139,15 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
   __syncthreads();
   if (n_tok > kSuffixMaxCtaTokens) return;
 
-  if (warp == kWarps) {
-    // ---------------- producer: one packed row per lane (lanes 0-15 K, 16-31 V) -----------
-    const bool is_v = lane >= kTile;
+  if (warp >= kWarps) {
+    // ---------------- producers: one packed row per lane (lanes 0-3 K, 4-7 V) -------------
+    const int part = warp - kWarps;
+    if (part >= kProducers) return;
+    const bool is_v = (lane & (2 * kRowsEach - 1)) >= kRowsEach;
     const uint8_t* pool = static_cast<const uint8_t*>(is_v ? p.vpool : p.kpool);
     const int64_t code_off = (int64_t)j0 * kD, scale_off = (int64_t)p.n_kv * kD + 4 * j0;
     const bool whole = p.n_kv <= kWarps;  // codes and scales are one run of bytes
-    const int r = lane & (kTile - 1);
+    const int r = part * kRowsEach + (lane & (kRowsEach - 1));
     int n = 0;    // tiles issued
     int pos = 0;  // position of the current segment's first token in sslot
     bool stop = false;
@@ -161,14 +165,15 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
           break;
         }
         const uint8_t* row = nullptr;
-        if (t + r < seg.t1) {
+        if (lane < 2 * kRowsEach && t + r < seg.t1) {
           const int32_t slot = sslot[pos + (t - seg.t0) + r];
           if (slot >= p.n_hot && slot < p.n_slots) row = pool + (int64_t)slot * p.kv8_row;
           else latch_err(p.err, kDevBadSlot);
         }
         if (skip0 && n == 0) continue;
-        if (lane == 0) mbar_arrive_expect_tx(full_bar(st), 2u * kTile * (code_bytes + scale_bytes));
+        if (lane == 0) mbar_arrive_expect_tx(full_bar(st), 2u * kRowsEach * (code_bytes + scale_bytes));
         __syncwarp();
+        if (lane >= 2 * kRowsEach) continue;
         const uint32_t dst = sbase + st * kStageBytes + (is_v ? kTileBytes : 0) + r * kRowStride;
         const uint8_t* zero = reinterpret_cast<const uint8_t*>(g_zero_row);
         if (whole) {
@@ -180,7 +185,8 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
       }
       pos += seg.t1 - seg.t0;
     }
-    // never leave with a copy in flight: wait for the last issued tiles to land
+    // never leave with a copy in flight: wait for the last issued tiles to land (every producer's
+    // part of a tile: they issue the same tiles unless one gave up, and then this gives up as well)
     if (lane == 0) {
       for (int i = max(skip0 ? 1 : 0, n - kStages); i < n; ++i) {
         const uint64_t t_start = globaltimer_ns();

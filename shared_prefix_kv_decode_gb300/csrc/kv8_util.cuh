@@ -43,8 +43,8 @@ __device__ __forceinline__ uint32_t f32x4_to_e4m3x4(float a, float b, float c, f
   return (uint32_t)f32x2_to_e4m3x2(a, b) | ((uint32_t)f32x2_to_e4m3x2(c, d) << 16);
 }
 
-// A query row in fp16, scaled by a power of two so that its largest finite element lies in
-// [2^14, 2^15).  bf16's 8 significant bits fit fp16's 11, so elements down to 2^-31 of the largest stay
+// A query row scaled by a power of two so that its largest finite element lies in [2^kTop, 2^(kTop+1)).
+// In fp16 with kTop = 14: bf16's 8 significant bits fit fp16's 11, so elements down to 2^-31 of the largest stay
 // exact (fp16's last subnormal is 2^-24), smaller ones are off by at most 2^-39 of it.
 __device__ __forceinline__ float bf16x2_finite_max(uint32_t w) {
   const float a = fabsf(__uint_as_float(w << 16)), b = fabsf(__uint_as_float(w & 0xffff0000u));
@@ -52,9 +52,10 @@ __device__ __forceinline__ float bf16x2_finite_max(uint32_t w) {
 }
 // The power of two for a row whose largest finite element is amax, and the one that undoes it; both
 // are kept within what fp32 holds.
+template <int kTop>
 __device__ __forceinline__ float q_factor(float amax, float& unit) {
   const int e = (int)((__float_as_uint(amax) >> 23) & 255u);
-  const int up = amax == 0.f ? 127 : min(141 + 127 - e, 253);  // 2^(14 - exponent of amax)
+  const int up = amax == 0.f ? 127 : min(kTop + 127 + 127 - e, 253);  // 2^(kTop - exponent of amax)
   unit = __uint_as_float((uint32_t)(254 - up) << 23);
   return __uint_as_float((uint32_t)up << 23);
 }
@@ -70,7 +71,7 @@ __device__ __forceinline__ void q_to_f16(uint32_t* w, float& unit) {
   for (int i = 0; i < W; ++i) amax = fmaxf(amax, bf16x2_finite_max(w[i]));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  const float f = q_factor(amax, unit);
+  const float f = q_factor<14>(amax, unit);
 #pragma unroll
   for (int i = 0; i < W; ++i) w[i] = bf16x2_to_f16x2(w[i], f);
 }

@@ -14,7 +14,10 @@ Tolerances.  With A = sum_t p_t |v_t| (64 bits) over a row's L keys:
        a code of at most 448.  With B_t = 448 vs_t, the largest |v| of the token's block and head, that is
        2^-32 max_t(p_t B_t) for each of the L tokens (it shows only where a column's result is
        that far below the row's largest possible one).
-  lse: a score q.k is a sum of d exact products in fp32: error at most d 2^-24 sum|q_i k_i| scale =: x;
+  lse: a score q.k is a sum of d exact products in fp32: error at most d 2^-24 sum|q_i k_i| scale; the
+       tensor-core prefix takes q as two e4m3 parts, exact but for elements below 2^-9 of the row's largest,
+       which are off by at most 2^-17 of that: 2^-17 max|q| sum|k_i| scale over those elements more.
+       x is the sum of the two;
        the exponential and logarithm add 2^-20, the sum of L weights L 2^-24.
 fp32 contexts keep the weights in fp32, and so have no 2^-11."""
 
@@ -135,6 +138,10 @@ class Kv8:
             q = self.q_host[b].reshape(self.n_kv, g, self.d)
             s = np.einsum("jgd,ljd->jgl", q, K) / math.sqrt(self.d)
             x = self.d * 2.0 ** -24 * (np.einsum("jgd,ljd->jgl", np.abs(q), np.abs(K)) / math.sqrt(self.d)).max(axis=2)
+            if self.of[b] >= 0 and self.dtype == "bf16" and self.d == 128:
+                top_q = np.abs(q).max(axis=2, keepdims=True)
+                small = np.where(np.abs(q) < 2.0 ** -9 * top_q, 2.0 ** -17 * top_q, 0.0)
+                x = x + (np.einsum("jgd,ljd->jgl", small, np.abs(K)) / math.sqrt(self.d)).max(axis=2)
             m = s.max(axis=2, keepdims=True)
             p = np.exp(s - m)
             ref_lse = (m[..., 0] + np.log(p.sum(axis=2))).reshape(self.n_q)
