@@ -19,7 +19,7 @@
 // half's sum of P once, over vs.  The running maximum m is taken over z.  P carries a factor of 2^7: it
 // is at most 2^15 (m may lag the row's maximum by 2^8, see below), and fp16 keeps its 11 bits down to 2^-21
 // of the largest weight.
-// Roles (14 warps):
+// Roles (15 warps):
 //  * warps 0-7, softmax and epilogue: warp w serves TMEM lanes 32*(w%4).. (row r = lane r), all 128
 //    columns of the tiles i with i % 2 == w / 4; the two warps of a row quarter take turns, half a
 //    tile apart.  The running max is a chain over the tiles: the warp of tile i reads the max used
@@ -28,9 +28,9 @@
 //  * warps 8-11, V conversion: each takes 32 tokens of every V tile.  It loads their codes by TMA into
 //    its own ring of three, turns 16 codes at a time into fp16 and stores them in the
 //    128-byte-swizzled layout that the MMA operand has (rows past the piece's end as zeros).
-//  * warp 12, the MMAs, issued as their inputs become ready: S(j) up to three tiles ahead of the PV
-//    products (three S/P buffers in TMEM).
-//  * warp 13, the TMA loads of K.
+//  * warps 12 and 13, the MMAs: one issues S(i), up to three tiles ahead (three S/P buffers in TMEM), the
+//    other PV(i), so that neither's waits hold up the other's products.
+//  * warp 14, the TMA loads of K.
 // Every mbarrier wait is bounded in time; on expiry the CTA raises an abort flag, latches an error,
 // drains what it issued and frees its TMEM.
 #pragma once
@@ -60,12 +60,13 @@ constexpr int kKSlots = 3;                    // slots of the K ring (codes)
 constexpr int kVSlots = 3;                    // slots of the V ring (fp16)
 constexpr int kCSlots = 3;                    // slots of each conversion warp's ring of V codes
 constexpr int kSBufs = 3;                     // S/P buffers in TMEM
+static_assert(kKSlots == kSBufs && kVSlots == kSBufs, "one commit tells both that a result is there and a slot free");
 constexpr int kSoftmaxWarps = 8;
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
 constexpr int kWarpConv = 8, kConvWarps = 4;
 constexpr int kPart = kN / kConvWarps;        // tokens of a V tile that one warp converts
-constexpr int kWarpMma = 12, kWarpTmaK = 13;
-constexpr int kThreads = 448;
+constexpr int kWarpS = 12, kWarpPv = 13, kWarpTmaK = 14;
+constexpr int kThreads = 480;
 constexpr int kHalf = kN * 128;               // one 64-dim half of an fp16 tile: 16 KB
 constexpr int kTile = 2 * kHalf;              // 32 KB
 constexpr int kCodes = kN * kD;               // a tile's codes: 16 KB
@@ -93,15 +94,13 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 enum : int {
   kBarKFull = 0,                            // [kKSlots] TMA -> MMA
-  kBarKEmpty = kBarKFull + kKSlots,         // [kKSlots] MMA (S done) -> TMA
-  kBarCFull = kBarKEmpty + kKSlots,         // [kConvWarps][kCSlots] TMA -> conversion (codes of V)
+  kBarCFull = kBarKFull + kKSlots,          // [kConvWarps][kCSlots] TMA -> conversion (codes of V)
   kBarVFull = kBarCFull + kConvWarps * kCSlots,  // [kVSlots] conversion -> MMA (kConvWarps arrivals)
-  kBarVEmpty = kBarVFull + kVSlots,         // [kVSlots] MMA (PV done) -> conversion
-  kBarSFull = kBarVEmpty + kVSlots,         // [kSBufs] S(i) in TMEM -> softmax
+  kBarSFull = kBarVFull + kVSlots,          // [kSBufs] S(i) in TMEM -> softmax; K slot free -> TMA
   kBarPFull = kBarSFull + kSBufs,           // [kSBufs] P(i) in TMEM -> MMA (128 arrivals)
-  kBarPvDone = kBarPFull + kSBufs,          // [kSBufs] PV(i) done -> softmax
-  kBarDrain = kBarPvDone + kSBufs,          // all MMAs done -> teardown
-  kBarPair = kBarDrain + 1,                 // [4] the two softmax warps of a row quarter, epilogue (64)
+  kBarPvDone = kBarPFull + kSBufs,          // [kSBufs] PV(i) done -> softmax; V slot free -> conversion
+  kBarDrain = kBarPvDone + kSBufs,          // [2] all S (all PV) products done -> teardown
+  kBarPair = kBarDrain + 2,                 // [4] the two softmax warps of a row quarter, epilogue (64)
   kBarMPub = kBarPair + 4,                  // [4 quarters][2 parities] max of a tile published (32)
   kNumBars = kBarMPub + 8
 };
@@ -275,7 +274,7 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp >= kWarpConv && warp < kWarpMma) {
+  if (warp >= kWarpConv && warp < kWarpConv + kConvWarps) {
     // ---------------- conversion: codes of V -> fp16 operand tiles ----------------
     // lane: dims 16 * (lane % 8) .. of tokens lane / 8 + 4 n of the part, which become two 16-byte chunks
     // of the token's row in 64-dim half lane % 8 / 4.  Lanes of the upper half store theirs in the other
@@ -308,7 +307,7 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
           if (lt + 4 * n >= valid) x[n] = make_uint4(0u, 0u, 0u, 0u);
       }
       if (i >= kVSlots) {
-        ok = mbar_wait_bounded(bar(kBarVEmpty + st), ((i / kVSlots) - 1) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
+        ok = mbar_wait_bounded(bar(kBarPvDone + st), ((i / kVSlots) - 1) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
       }
@@ -357,7 +356,7 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
     if (lane == 0) {
       int issued = slab_ok ? min(n_tiles, kKSlots) : 0;
       for (int i = issued; slab_ok && i < n_tiles; ++i) {
-        if (!mbar_wait_bounded(bar(kBarKEmpty + i % kKSlots), ((i / kKSlots) - 1) & 1, abort_flag, p.err, kDevTimeout,
+        if (!mbar_wait_bounded(bar(kBarSFull + i % kKSlots), ((i / kKSlots) - 1) & 1, abort_flag, p.err, kDevTimeout,
                                kWaitLimitNs))
           break;
         issue_k(i);
@@ -376,85 +375,54 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
         }
       }
     }
-  } else if (warp == kWarpMma) {
-    // ---------------- MMA issuer ----------------
+  } else if (warp == kWarpS || warp == kWarpPv) {
+    // ---------------- MMA issuers ----------------
     if (lane == 0 && !*abort_flag) {
       constexpr uint32_t idS = idesc_fmt0_f32(kM, kN, false);
       constexpr uint32_t idO = idesc_fmt0_f32(kM, kD, true);
-      const uint64_t dq0 = smem_desc_sw128(sQ, 16, 1024);
-      const uint64_t dk0 = smem_desc_sw128(sK, 16, 1024);
-      // V tile as an MN-major B operand: 16 tokens per step (2048 bytes), the two 64-dim halves
-      // kHalf apart (leading offset), 8-token groups 1024 bytes apart (stride)
-      const uint64_t dv0 = smem_desc_sw128(sV, kHalf, 1024);
+      auto wait = [&](int b, int i) {
+        return mbar_wait_bounded(bar(b + i % kSBufs), (i / kSBufs) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
+      };
       int committed = 0;
-      // PV(i) as soon as P(i) and V(i) are ready, S(j) as soon as K(j) is and its TMEM buffer is
-      // free: S(j) overwrites S(j-3)/P(j-3), so it may go in once PV(j-3) has been issued (MMAs of one
-      // thread execute in order; the softmax was done with S(j-3) before it produced P(j-3)).
-      int next_s = 0, next_pv = 0;
-      uint64_t t_last = 0;  // when it was first seen waiting
-      int idle = 0;
-      while (next_pv < n_tiles) {
-        bool progressed = false;
-        if (next_pv < next_s) {
-          const int i = next_pv;
-          const int st = i % kVSlots;
-          const int sb = i % kSBufs;
-          if (mbar_test_wait(bar(kBarPFull + sb), (i / kSBufs) & 1) &&
-              mbar_test_wait(bar(kBarVFull + st), (i / kVSlots) & 1)) {
-            tc_fence_after();
-            const uint32_t pa = tmem + (uint32_t)(sb * kN);  // P(i): 64 columns, two tokens per column
-            const uint64_t dv = dv0 + (uint64_t)((st * kTile) >> 4);
+      if (warp == kWarpS) {
+        const uint64_t dq0 = smem_desc_sw128(sQ, 16, 1024);
+        const uint64_t dk0 = smem_desc_sw128(sK, 16, 1024);
+        for (int i = 0; i < n_tiles; ++i) {
+          // S(i) overwrites S(i-3)/P(i-3), whose last reader is PV(i-3)
+          if (i >= kSBufs && !wait(kBarPvDone, i - kSBufs)) break;
+          if (!wait(kBarKFull, i)) break;
+          tc_fence_after();
+          const uint32_t dS = tmem + (uint32_t)((i % kSBufs) * kN);
+          const uint64_t dk = dk0 + (uint64_t)(((i % kKSlots) * kCodes) >> 4);
 #pragma unroll
-            for (int ks = 0; ks < kN / 16; ++ks)
-              umma_f16_ts(tmem + kColO, pa + (uint32_t)(ks * 8), dv + (uint64_t)((ks * 2048) >> 4), idO,
-                          (i > 0 || ks > 0) ? 1u : 0u);
-            umma_commit(bar(kBarVEmpty + st));
-            umma_commit(bar(kBarPvDone + sb));
-            committed += 2;
-            ++next_pv;
-            progressed = true;
-          }
+          for (int kk = 0; kk < 8; ++kk)  // lo, the smaller, first
+            umma_f8(dS, dq0 + (uint64_t)(((kk < 4 ? kQPart : 0) + (kk & 3) * 32) >> 4), dk + (uint64_t)(((kk & 3) * 32) >> 4),
+                    idS, kk > 0 ? 1u : 0u);
+          umma_commit(bar(kBarSFull + i % kSBufs));
+          committed += 1;
         }
-        if (next_s < n_tiles && next_s < next_pv + kSBufs) {
-          const int i = next_s;
-          const int st = i % kKSlots;
-          if (mbar_test_wait(bar(kBarKFull + st), (i / kKSlots) & 1)) {
-            tc_fence_after();
-            const uint32_t dS = tmem + (uint32_t)((i % kSBufs) * kN);
-            const uint64_t dk = dk0 + (uint64_t)((st * kCodes) >> 4);
+      } else {
+        // V tile as an MN-major B operand: 16 tokens per step (2048 bytes), the two 64-dim halves
+        // kHalf apart (leading offset), 8-token groups 1024 bytes apart (stride)
+        const uint64_t dv0 = smem_desc_sw128(sV, kHalf, 1024);
+        for (int i = 0; i < n_tiles; ++i) {
+          if (!wait(kBarVFull, i) || !wait(kBarPFull, i)) break;
+          tc_fence_after();
+          const uint32_t pa = tmem + (uint32_t)((i % kSBufs) * kN);  // P(i): 64 columns, two tokens per column
+          const uint64_t dv = dv0 + (uint64_t)(((i % kVSlots) * kTile) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)  // lo, the smaller, first
-              umma_f8(dS, dq0 + (uint64_t)(((kk < 4 ? kQPart : 0) + (kk & 3) * 32) >> 4), dk + (uint64_t)(((kk & 3) * 32) >> 4),
-                      idS, kk > 0 ? 1u : 0u);
-            umma_commit(bar(kBarSFull + i % kSBufs));
-            umma_commit(bar(kBarKEmpty + st));
-            committed += 2;
-            ++next_s;
-            progressed = true;
-          }
-        }
-        // the clock is read on every 64th idle round only
-        if (progressed) {
-          idle = 0;
-          t_last = 0;
-        } else if (*abort_flag) {
-          break;
-        } else if ((++idle & 63) == 0) {
-          const uint64_t now = globaltimer_ns();
-          if (t_last == 0) {
-            t_last = now;
-          } else if (now - t_last > kWaitLimitNs) {
-            *abort_flag = 1;
-            atomicCAS(p.err, 0, (int32_t)kDevTimeout);
-            break;
-          }
+          for (int ks = 0; ks < kN / 16; ++ks)
+            umma_f16_ts(tmem + kColO, pa + (uint32_t)(ks * 8), dv + (uint64_t)((ks * 2048) >> 4), idO, (i > 0 || ks > 0) ? 1u : 0u);
+          umma_commit(bar(kBarPvDone + i % kSBufs));
+          committed += 1;
         }
       }
       // drain: every tcgen05 op this thread issued completes before the CTA frees TMEM
       if (committed > 0) {
-        umma_commit(bar(kBarDrain));
+        const uint32_t drain = bar(kBarDrain + (warp == kWarpS ? 0 : 1));
+        umma_commit(drain);
         const uint64_t t_start = globaltimer_ns();
-        while (!mbar_try_wait(bar(kBarDrain), 0)) {
+        while (!mbar_try_wait(drain, 0)) {
           if (globaltimer_ns() - t_start > kWaitLimitNs) {
             atomicCAS(p.err, 0, kDevTimeout);
             break;
