@@ -132,6 +132,12 @@ struct granikv_plan {
     std::vector<int64_t> tail_key, tail_key_now, sim_heap;
     int64_t tail_len = 0;
     std::vector<char> grp_tail;           // group's last piece is a shorter remainder
+    std::vector<double> share;            // 8-bit cache: what each suffix run's CTA can take
+    struct Class {                        // dense CTAs that are done at t (us)
+      double t;
+      int64_t n;
+    };
+    std::vector<Class> classes;
   } scratch;
 };
 
@@ -351,6 +357,9 @@ void ws_forget(const void* ws) {
 // part of one token-CTA run) costs its CTA about one tile on top of its tiles.
 constexpr int64_t kSTile = 16;
 constexpr int64_t kSegTiles = 1;
+// 8-bit cache: a tile takes a token-CTA 0.56 us and a segment about 0.95 us more than that (its q, its
+// record, its odd last tile), measured on GB300 over the CTAs of three workloads
+constexpr int64_t kSegTilesKv8 = 3;
 
 struct SuffixCut {
   int32_t n_items = 0;         // suffix work items written
@@ -367,13 +376,15 @@ struct SuffixCut {
 // that fell between two requests (it added no segment), so that short requests, which most cuts
 // do not split, leave no run short at the end.  Writes every request's record layout
 // (np_of[rg[b]] prefix records, then one per segment), one suffix item per segment and each
-// run's first item (scta_begin[0..n_scta]).  Out of line so that its loop's counters stay in
+// run's first item (scta_begin[0..n_scta]).  With share (n_scta positive numbers), run k's part of
+// what is left is share[k] over the shares left, in place of an equal one, and n_tail and U_tail are
+// not used.  Out of line so that its loop's counters stay in
 // registers.
 __attribute__((noinline)) SuffixCut cut_suffix_runs(int32_t B, const int32_t* __restrict__ np_of,
                                                     const int32_t* __restrict__ rg,
                                                     const int32_t* __restrict__ seq_len, int32_t n_scta,
-                                                    int32_t n_tail, int64_t U, int64_t U_tail,
-                                                    DevReq* __restrict__ reqs, DevSuffixItem* __restrict__ si,
+                                                    int32_t n_tail, int64_t U, int64_t U_tail, int64_t seg_tiles,
+                                                    const double* __restrict__ share, DevReq* __restrict__ reqs, DevSuffixItem* __restrict__ si,
                                                     int32_t* __restrict__ scta_begin) {
   const int32_t n_main = n_scta - n_tail;
   int32_t n_si = 0;
@@ -383,8 +394,15 @@ __attribute__((noinline)) SuffixCut cut_suffix_runs(int32_t B, const int32_t* __
   int64_t whole_cuts = 0;   // cuts so far that fell between two requests
   bool cta_open = false;    // the current CTA has a segment
   // where run k (starting now, at `done`) ends: one division per run, not per segment
+  double shares_left = 0.0;
+  for (int32_t k = 0; share && k < n_scta; ++k) shares_left += share[k];
   auto run_end = [&](int64_t k) {
-    const int64_t left = U - done - whole_cuts;
+    const int64_t left = U - done - seg_tiles * whole_cuts;
+    if (share) {
+      const double part = shares_left > share[k] ? (double)left * share[k] / shares_left : (double)left;
+      shares_left -= share[k];
+      return done + (int64_t)part;
+    }
     if (k < n_main) return done + (left - U_tail) / (n_main - k);
     return done + left / (n_scta - k);
   };
@@ -403,13 +421,13 @@ __attribute__((noinline)) SuffixCut cut_suffix_runs(int32_t B, const int32_t* __
     const int64_t n_t = (L + kSTile - 1) / kSTile;
     // the common case: the whole request fits the current run with room to spare (the loop
     // below would take it in one segment and leave the run open)
-    if (n_t > 0 && (cta >= n_scta - 1 || end_cur - done - kSegTiles > n_t)) {
+    if (n_t > 0 && (cta >= n_scta - 1 || end_cur - done - seg_tiles > n_t)) {
       DevSuffixItem& it = si[n_si++];
       it.b = b;
       it.t0 = 0;
       it.t1 = L;
       it.rec = (int32_t)(rec + n_prefix);
-      done += kSegTiles + n_t;
+      done += seg_tiles + n_t;
       cta_open = true;
       r.n_parts = n_prefix + 1;
       max_parts = std::max(max_parts, r.n_parts);
@@ -418,7 +436,7 @@ __attribute__((noinline)) SuffixCut cut_suffix_runs(int32_t B, const int32_t* __
     }
     for (int64_t t = 0; t < n_t;) {
       const bool last_cta = cta >= n_scta - 1;
-      int64_t room = last_cta ? n_t - t : end_cur - done - kSegTiles;
+      int64_t room = last_cta ? n_t - t : end_cur - done - seg_tiles;
       if (room <= 0 && cta_open) {
         // no tile more fits in this CTA: the request goes on in the next one
         ++cta;
@@ -436,7 +454,7 @@ __attribute__((noinline)) SuffixCut cut_suffix_runs(int32_t B, const int32_t* __
       it.rec = (int32_t)(rec + n_prefix + k);
       ++k;
       t += take;
-      done += kSegTiles + take;
+      done += seg_tiles + take;
       cta_open = true;
       if (!last_cta && done >= end_cur) {
         ++cta;
@@ -1037,6 +1055,11 @@ granikv_status granikv_dispatch(granikv_ctx* c, const granikv_batch* bt, granikv
   int32_t suffix_sms = c->num_sms;  // set after the prefix pieces when the SMs are split
   bool read_ahead = false;          // the split's dense CTAs read ahead into L2 (see below)
   double tail_frac = 0.0;           // share of the suffix work the dense CTAs take after their piece
+  const int64_t seg_tiles = c->kv8_row ? kSegTilesKv8 : kSegTiles;
+  bool kv8_split = false;           // 8-bit cache: the split and its runs' shares as planned below
+  int32_t kv8_main = 0;             // its suffix CTAs
+  std::vector<double>& share = w.share;
+  share.clear();
 
   // 3. prefix pieces: the smallest piece length (in tiles, one length for all groups) whose
   //    CTA count fits the target, pieces balanced to within one tile.  The tensor-core
@@ -1066,7 +1089,88 @@ granikv_status granikv_dispatch(granikv_ctx* c, const granikv_batch* bt, granikv
       else lo = mid + 1;
     }
     bool auto_found = false;
-    if (auto_share) {
+    bool kv8_dense = auto_share && c->kv8_row && n_kv <= 8;
+    for (int32_t i = 0; i < G; ++i) kv8_dense = kv8_dense && groups[i].impl == kImplKv8Dense;
+    if (kv8_dense) {
+      // 8-bit cache: every SM works until the end.  With pieces of a given length, dense CTA k is done
+      // at t_k = 5.2 us + 7.3 ns a token and then takes suffix work (3 us for its set-up), the SMs
+      // without a prefix piece take suffix work from the start (4.5 us); a unit of it (16 tokens, or
+      // a third of a segment's cost) is 0.57 us.  The common end T makes the parts add up to
+      // the step's units; the length with the earliest end is taken, and every run's share is what
+      // its CTA can do by then.  Measured on GB300 (CTA end times): Llama shape 26.9 us for 21.3
+      // tiles, Qwen shape 65 us for 64.
+      constexpr double kDense = 5.2, kToken = 0.0073, kTail = 3.0, kMain = 4.5, kUnit = 0.57, kMinTail = 6.0;
+      const int64_t few = (T_tiles + 3) / 4;  // a run for every four tiles at most
+      const double units = (double)(T_tiles + seg_tiles * (n_sreq + std::min<int64_t>(few, c->num_sms)));
+      using Class = granikv_plan::Scratch::Class;
+      auto classes_of = [&](int64_t cand, std::vector<Class>& out) {
+        out.clear();
+        for (int32_t i = 0; i < G; ++i) {
+          const int64_t tiles = (groups[i].L_p + kDenseTile - 1) / kDenseTile;
+          const int64_t n = (tiles + cand - 1) / cand, per = ctas_per_piece(groups[i], n_kv), longer = tiles % n;
+          if (longer) out.push_back({kDense + kToken * kDenseTile * (double)(tiles / n + 1), per * longer});
+          out.push_back({kDense + kToken * kDenseTile * (double)(tiles / n), per * (n - longer)});
+        }
+      };
+      // the T by which the CTAs that start their suffix work at x.t (sorted) have done all units
+      auto end_of = [&](const std::vector<Class>& cl) {
+        double sum = units * kUnit, n = 0.0, T = 1e300;
+        for (size_t k = 0; k < cl.size() && T > cl[k].t; ++k) {
+          sum += (double)cl[k].n * cl[k].t;
+          n += (double)cl[k].n;
+          if (n > 0.0) T = sum / n;
+        }
+        return T;
+      };
+      auto starts_of = [&](int64_t cand, std::vector<Class>& out) {
+        classes_of(cand, out);
+        double t_p = 0.0;
+        for (Class& x : out) {
+          t_p = std::max(t_p, x.t);
+          x.t += kTail;
+        }
+        out.push_back({kMain, c->num_sms - ctas_for(cand)});
+        std::sort(out.begin(), out.end(), [](const Class& a, const Class& b) { return a.t < b.t; });
+        return t_p;  // the last dense CTA's end
+      };
+      std::vector<Class>& cl = w.classes;
+      double best = 1e300, best_T = 0.0;
+      int64_t best_len = 0;
+      for (int64_t n = 1; n <= max_tiles; ++n) {
+        const int64_t cand = (max_tiles + n - 1) / n;
+        if (n > 1 && cand == (max_tiles + n - 2) / (n - 1)) continue;
+        const int64_t ctas = ctas_for(cand);
+        if (ctas > c->num_sms) break;
+        const double t_p = starts_of(cand, cl), T = end_of(cl);
+        if (std::max(T, t_p) < best) {
+          best = std::max(T, t_p);
+          best_T = T;
+          best_len = cand;
+        }
+      }
+      if (best_len > 0) {
+        lo = best_len;
+        auto_found = true;
+        kv8_main = (int32_t)(c->num_sms - ctas_for(lo));
+        classes_of(lo, cl);
+        std::sort(cl.begin(), cl.end(), [](const Class& a, const Class& b) { return a.t < b.t; });
+        // few tiles: on the SMs without a prefix piece only
+        for (int32_t k = 0; k < kv8_main && k < few; ++k) share.push_back(std::max(1.0, (best_T - kMain) / kUnit));
+        kv8_main = (int32_t)share.size();
+        if (few > kv8_main)
+          for (const Class& x : cl)
+            for (int64_t k = 0; k < x.n; ++k)
+              if ((best_T - x.t - kTail) / kUnit >= kMinTail) share.push_back((best_T - x.t - kTail) / kUnit);
+        double sum = 0.0, top = 0.0;
+        for (const double s : share) {
+          sum += s;
+          top = std::max(top, s);
+        }
+        // a run's slot ids fit its shared memory; else the equal shares below, on the main CTAs
+        kv8_split = !share.empty() && top / sum * units < 0.9 * (double)(kSuffixMaxCtaTokens / kSTile);
+        if (!kv8_split) auto_found = ctas_for(lo) < c->num_sms;
+      }
+    } else if (auto_share) {
       // Automatic split: the piece length whose prefix time (one wave: the longest piece) and
       // suffix time (its work spread over the SMs the prefix CTAs leave) are most nearly equal,
       // i.e. the smallest max of the two.  Costs measured on GB300: a prefix CTA 5 us plus, per
@@ -1256,7 +1360,11 @@ granikv_status granikv_dispatch(granikv_ctx* c, const granikv_batch* bt, granikv
   int32_t n_tail = 0;       // of them, the last n_tail are run by the dense CTAs of one grid
   int64_t U = 0;            // tiles plus segment costs, with every cut counted as inside a request
   int64_t U_tail = 0;       // of U, the tail runs' share
-  if (T > 0) {
+  if (kv8_split) {
+    n_scta = (int32_t)share.size();
+    n_tail = n_scta - kv8_main;
+    U = T + seg_tiles * (n_sreq + n_scta - 1);
+  } else if (T > 0) {
     // one wave over the suffix's SMs, with at least kMinCtaTiles tiles per token-CTA (a CTA's
     // set-up and first-tile latency cost about as much as three tiles, and every CTA adds a
     // record per request it touches), unless a CTA would then stream more tokens than it can
@@ -1264,19 +1372,19 @@ granikv_status granikv_dispatch(granikv_ctx* c, const granikv_batch* bt, granikv
     constexpr int64_t kMinCtaTiles = 4;
     constexpr int64_t kMaxCtaTiles = kSuffixMaxCtaTokens / kSTile;
     n_scta = (int32_t)std::min<int64_t>(suffix_sms, (T + kMinCtaTiles - 1) / kMinCtaTiles);
-    n_scta = (int32_t)std::max<int64_t>(n_scta, (T + n_sreq + kMaxCtaTiles - 3) / (kMaxCtaTiles - 2));
+    n_scta = (int32_t)std::max<int64_t>(n_scta, (T + seg_tiles * n_sreq + kMaxCtaTiles - 3) / (kMaxCtaTiles - 2));
     const int32_t n_dense_ctas = (int32_t)(c->num_sms - suffix_sms);
     if (tail_frac > 0.0 && n_scta == suffix_sms && n_dense_ctas > 0) {
       n_tail = n_dense_ctas;
       n_scta += n_tail;
     }
-    U = T + kSegTiles * (n_sreq + n_scta - 1);
+    U = T + seg_tiles * (n_sreq + n_scta - 1);
     U_tail = n_tail > 0 ? (int64_t)(tail_frac * (double)U) : 0;
     if (U_tail < 3 * (int64_t)n_tail) {  // under about two tiles a run: not worth a run's set-up
       n_scta -= n_tail;
       n_tail = 0;
       U_tail = 0;
-      U = T + kSegTiles * (n_sreq + n_scta - 1);
+      U = T + seg_tiles * (n_sreq + n_scta - 1);
     }
   }
 
@@ -1307,8 +1415,9 @@ granikv_status granikv_dispatch(granikv_ctx* c, const granikv_batch* bt, granikv
   // the items depend on the groups' kernels and shapes only (and the KV heads)
   {
     std::vector<int32_t> key_now;
-    key_now.reserve((size_t)G * 6 + 1);
+    key_now.reserve((size_t)G * 7 + 2);
     key_now.push_back(n_kv);
+    key_now.push_back(kv8_split ? 1 : 0);
     for (int32_t i = 0; i < G; ++i) {
       const DevGroup& dg = groups[i];
       key_now.insert(key_now.end(), {dg.impl, dg.sub, dg.n_splits, dg.row_blocks, dg.split_len, dg.n_long, w.grp_tail[i]});
@@ -1337,6 +1446,16 @@ granikv_status granikv_dispatch(granikv_ctx* c, const granikv_batch* bt, granikv
       for (int32_t j = 0; j < n_kv; ++j)
         for (int32_t rb = 0; rb < dg.row_blocks; ++rb) pitems.push_back({i, j, rb, dg.n_splits - 1});
     }
+    // the 8-bit dense kernel's first CTAs are those that take suffix runs after their piece: the
+    // shortest pieces come first
+    if (impl == kImplKv8Dense && kv8_split)
+      std::stable_sort(pitems.begin() + p->pitem_first[impl], pitems.end(),
+                       [&](const DevPrefixItem& a, const DevPrefixItem& b) {
+                         int32_t a0, a1, b0, b1;
+                         piece_range(groups[a.group], a.split, a0, a1);
+                         piece_range(groups[b.group], b.split, b0, b1);
+                         return (a1 - a0 + kDenseTile - 1) / kDenseTile < (b1 - b0 + kDenseTile - 1) / kDenseTile;
+                       });
     p->pitem_count[impl] = (int32_t)pitems.size() - p->pitem_first[impl];
   }
   }
@@ -1365,7 +1484,8 @@ granikv_status granikv_dispatch(granikv_ctx* c, const granikv_batch* bt, granikv
   grp_np[0] = 0;
   for (int32_t i = 0; i < G; ++i) grp_np[i + 1] = groups[i].n_splits;
   const SuffixCut cut = cut_suffix_runs(B, grp_np.data() + 1, req_group.data(), bt->seq_len, n_scta, n_tail, U,
-                                        U_tail, reqs, si, scta_begin.data());
+                                        U_tail, seg_tiles, kv8_split ? share.data() : nullptr, reqs, si,
+                                        scta_begin.data());
   const int32_t n_si = cut.n_items;
   const int32_t max_parts = cut.max_parts;
   const int64_t rec = cut.records;

@@ -19,7 +19,7 @@
 // half's sum of P once, over vs.  The running maximum m is taken over z.  P carries a factor of 2^7: it
 // is at most 2^15 (m may lag the row's maximum by 2^8, see below), and fp16 keeps its 11 bits down to 2^-21
 // of the largest weight.
-// Roles (15 warps):
+// Roles (15 warps; the 16th only takes part in the block's barriers here):
 //  * warps 0-7, softmax and epilogue: warp w serves TMEM lanes 32*(w%4).. (row r = lane r), all 128
 //    columns of the tiles i with i % 2 == w / 4; the two warps of a row quarter take turns, half a
 //    tile apart.  The running max is a chain over the tiles: the warp of tile i reads the max used
@@ -66,7 +66,7 @@ constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
 constexpr int kWarpConv = 8, kConvWarps = 4;
 constexpr int kPart = kN / kConvWarps;        // tokens of a V tile that one warp converts
 constexpr int kWarpS = 12, kWarpPv = 13, kWarpTmaK = 14;
-constexpr int kThreads = 480;
+constexpr int kThreads = 512;  // one more warp, for the suffix body's producers
 constexpr int kHalf = kN * 128;               // one 64-dim half of an fp16 tile: 16 KB
 constexpr int kTile = 2 * kHalf;              // 32 KB
 constexpr int kCodes = kN * kD;               // a tile's codes: 16 KB
@@ -430,7 +430,7 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
         }
       }
     }
-  } else {
+  } else if (warp < kSoftmaxWarps) {
     // ---------------- softmax warps 0-7: rows of quarter `quad`, tiles of parity `par` ----------------
     const int quad = warp & 3;
     const int par = warp >> 2;

@@ -33,6 +33,8 @@
 #include "mma_util.cuh"
 #include "tc_util.cuh"
 
+#include <type_traits>
+
 namespace granikv {
 namespace k8s {
 namespace {
@@ -41,7 +43,7 @@ constexpr int kD = 128;
 constexpr int kTile = 16;                          // tokens per tile (MMA M)
 constexpr int kStages = 6;
 constexpr int kWarps = 8;                          // consumer warps: KV heads per CTA
-constexpr int kProducers = 4;                      // producer warps: a quarter of a tile's rows each
+constexpr int kProducers = 8;                      // producer warps: two of a tile's rows each
 constexpr int kRowsEach = kTile / kProducers;
 constexpr int kThreads = (kWarps + kProducers) * 32;
 constexpr int kRowMax = kWarps * (kD + 4);         // packed row of eight heads: 1,056 B
@@ -140,7 +142,7 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
   if (n_tok > kSuffixMaxCtaTokens) return;
 
   if (warp >= kWarps) {
-    // ---------------- producers: one packed row per lane (lanes 0-3 K, 4-7 V) -------------
+    // ---------------- producers: one packed row per lane (lanes 0-1 K, 2-3 V) -------------
     const int part = warp - kWarps;
     if (part >= kProducers) return;
     const bool is_v = (lane & (2 * kRowsEach - 1)) >= kRowsEach;
@@ -245,49 +247,67 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
     for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
 
     bool ok = true;
-    for (int t = seg.t0; t < seg.t1; t += kTile, ++tile) {
-      const int st = tile % kStages;
-      const bool landed = mbar_wait_bounded(full_bar(st), (tile / kStages) & 1, abort_flag, p.err, kDevTimeout,
-                                            kWaitLimitNs);
-      if (!__all_sync(0xffffffffu, landed)) {
-        ok = false;
-        break;
-      }
-      const uint32_t kst = sbase + st * kStageBytes;
-      const uint32_t vst = kst + kTileBytes;
+    // V tiles from token t on: one running-max update for both, and their products side by side, so
+    // that a warp has two chains to issue from (two warps a scheduler leave most of a chain's
+    // latency open)
+    auto tiles = [&](auto count, int t) {
+      constexpr int V = decltype(count)::value;
       const int mi = lane >> 3;
-      // the scales of tokens r and r + 8
-      const unsigned char* ksp = smem + st * kStageBytes + r * kRowStride + scale_at;
-      const float ka = *reinterpret_cast<const float*>(ksp), kb = *reinterpret_cast<const float*>(ksp + 8 * kRowStride);
-      const float va = *reinterpret_cast<const float*>(ksp + kTileBytes);
-      const float vb = *reinterpret_cast<const float*>(ksp + kTileBytes + 8 * kRowStride);
-
-      // S^T = K . Q^T, in two accumulation chains
-      float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
-      {
-        const uint32_t at = kst + head_off + ((lane & 7) + (mi & 1) * 8) * kRowStride + (mi >> 1) * 16;
+      const uint32_t frag = head_off + ((lane & 7) + (mi & 1) * 8) * kRowStride + (mi >> 1) * 16;
+      uint32_t at[V];  // this lane's ldmatrix row of each tile
+      float sa[V], sb[V], la[V], lb[V], s[V][4], s2[V][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t w0, w1, w2, w3, a0, a1, a2, a3;
-          ldsm_x4(at + i * 32, w0, w1, w2, w3);
-          e4m3x4_to_f16x4(w0, a0, a2);
-          e4m3x4_to_f16x4(w1, a1, a3);
-          mma_f16_16816(s, a0, a1, a2, a3, qf[4 * i], qf[4 * i + 1]);
-          e4m3x4_to_f16x4(w2, a0, a2);
-          e4m3x4_to_f16x4(w3, a1, a3);
-          mma_f16_16816(s2, a0, a1, a2, a3, qf[4 * i + 2], qf[4 * i + 3]);
+      for (int v = 0; v < V; ++v) {
+        const int st = (tile + v) % kStages;
+        const bool landed = mbar_wait_bounded(full_bar(st), ((tile + v) / kStages) & 1, abort_flag, p.err, kDevTimeout,
+                                              kWaitLimitNs);
+        if (!__all_sync(0xffffffffu, landed)) return false;
+        at[v] = sbase + st * kStageBytes + frag;
+        // the scales of tokens r and r + 8
+        const unsigned char* ksp = smem + st * kStageBytes + r * kRowStride + scale_at;
+        sa[v] = *reinterpret_cast<const float*>(ksp);
+        sb[v] = *reinterpret_cast<const float*>(ksp + 8 * kRowStride);
+        la[v] = *reinterpret_cast<const float*>(ksp + kTileBytes);
+        lb[v] = *reinterpret_cast<const float*>(ksp + kTileBytes + 8 * kRowStride);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[v][e] = s2[v][e] = 0.f;
+      }
+      // S^T = K . Q^T, in two accumulation chains a tile
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[V][4];
+#pragma unroll
+        for (int v = 0; v < V; ++v) ldsm_x4(at[v] + i * 32, w[v][0], w[v][1], w[v][2], w[v][3]);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16x4(w[v][0], a0, a2);
+          e4m3x4_to_f16x4(w[v][1], a1, a3);
+          mma_f16_16816(s[v], a0, a1, a2, a3, qf[4 * i], qf[4 * i + 1]);
+          e4m3x4_to_f16x4(w[v][2], a0, a2);
+          e4m3x4_to_f16x4(w[v][3], a1, a3);
+          mma_f16_16816(s2[v], a0, a1, a2, a3, qf[4 * i + 2], qf[4 * i + 3]);
         }
       }
-      const int rem = seg.t1 - t;  // valid tokens in this tile (may exceed 16)
-      const float la = lg2_approx(va), lb = lg2_approx(vb);
-      // P / vs below uses the very logarithm that P does, so its rounding does not reach the row sum
-      // (the zero row of a token that does not count has scale 0, and adds nothing)
-      const float ia = va > 0.f ? ex2_approx(-la) : 0.f, ib = vb > 0.f ? ex2_approx(-lb) : 0.f;
-      s[0] = r < rem ? (s[0] + s2[0]) * (f0 * ka) + la : -INFINITY;
-      s[1] = r < rem ? (s[1] + s2[1]) * (f1 * ka) + la : -INFINITY;
-      s[2] = r + 8 < rem ? (s[2] + s2[2]) * (f0 * kb) + lb : -INFINITY;
-      s[3] = r + 8 < rem ? (s[3] + s2[3]) * (f1 * kb) + lb : -INFINITY;
-      float mx0 = fmaxf(s[0], s[2]), mx1 = fmaxf(s[1], s[3]);
+      const int rem = seg.t1 - t;  // valid tokens from the first tile on
+      float mx0 = -INFINITY, mx1 = -INFINITY;
+      float ia[V], ib[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float va = la[v], vb = lb[v];
+        la[v] = lg2_approx(va);
+        lb[v] = lg2_approx(vb);
+        // P / vs below uses the very logarithm that P does, so its rounding does not reach the row
+        // sum (the zero row of a token that does not count has scale 0, and adds nothing)
+        ia[v] = va > 0.f ? ex2_approx(-la[v]) : 0.f;
+        ib[v] = vb > 0.f ? ex2_approx(-lb[v]) : 0.f;
+        s[v][0] = v * kTile + r < rem ? (s[v][0] + s2[v][0]) * (f0 * sa[v]) + la[v] : -INFINITY;
+        s[v][1] = v * kTile + r < rem ? (s[v][1] + s2[v][1]) * (f1 * sa[v]) + la[v] : -INFINITY;
+        s[v][2] = v * kTile + r + 8 < rem ? (s[v][2] + s2[v][2]) * (f0 * sb[v]) + lb[v] : -INFINITY;
+        s[v][3] = v * kTile + r + 8 < rem ? (s[v][3] + s2[v][3]) * (f1 * sb[v]) + lb[v] : -INFINITY;
+        mx0 = max3f(mx0, s[v][0], s[v][2]);
+        mx1 = max3f(mx1, s[v][1], s[v][3]);
+      }
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
@@ -309,31 +329,49 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
         m0 = mn0;
         m1 = mn1;
       }
-      const float p0 = ex2_approx(s[0] - mu0 + kShift), p1 = ex2_approx(s[1] - mu1 + kShift);
-      const float p2 = ex2_approx(s[2] - mu0 + kShift), p3 = ex2_approx(s[3] - mu1 + kShift);
-      l0 += p0 * ia + p2 * ib;
-      l1 += p1 * ia + p3 * ib;
-      // P^T in B-operand layout
-      const uint32_t b0 = movmatrix_t(pack_f16(p0, p1));
-      const uint32_t b1 = movmatrix_t(pack_f16(p2, p3));
-      // O^T += V^T . P^T: m-tile mt holds dims 16 mt + 2 r (row r) and 16 mt + 2 r + 1 (row r + 8)
-      {
-        const uint32_t at = vst + head_off + ((lane & 7) + (mi & 1) * 8) * kRowStride + (mi >> 1) * 16;
+      uint32_t b0[V], b1[V];  // P^T in B-operand layout
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t w0, w1, w2, w3, a0, a1, a2, a3;
-          ldsm_x4_t(at + i * 32, w0, w1, w2, w3);
-          e4m3x4_to_f16x4(__byte_perm(w0, 0, 0x3120), a0, a1);
-          e4m3x4_to_f16x4(__byte_perm(w1, 0, 0x3120), a2, a3);
-          mma_f16_16816(o[2 * i], a0, a1, a2, a3, b0, b1);
-          e4m3x4_to_f16x4(__byte_perm(w2, 0, 0x3120), a0, a1);
-          e4m3x4_to_f16x4(__byte_perm(w3, 0, 0x3120), a2, a3);
-          mma_f16_16816(o[2 * i + 1], a0, a1, a2, a3, b0, b1);
+      for (int v = 0; v < V; ++v) {
+        const float p0 = ex2_approx(s[v][0] - mu0 + kShift), p1 = ex2_approx(s[v][1] - mu1 + kShift);
+        const float p2 = ex2_approx(s[v][2] - mu0 + kShift), p3 = ex2_approx(s[v][3] - mu1 + kShift);
+        l0 += p0 * ia[v] + p2 * ib[v];
+        l1 += p1 * ia[v] + p3 * ib[v];
+        b0[v] = movmatrix_t(pack_f16(p0, p1));
+        b1[v] = movmatrix_t(pack_f16(p2, p3));
+      }
+      // O^T += V^T . P^T: m-tile mt holds dims 16 mt + 2 r (row r) and 16 mt + 2 r + 1 (row r + 8)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[V][4];
+#pragma unroll
+        for (int v = 0; v < V; ++v) ldsm_x4_t(at[v] + kTileBytes + i * 32, w[v][0], w[v][1], w[v][2], w[v][3]);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16x4(__byte_perm(w[v][0], 0, 0x3120), a0, a1);
+          e4m3x4_to_f16x4(__byte_perm(w[v][1], 0, 0x3120), a2, a3);
+          mma_f16_16816(o[2 * i], a0, a1, a2, a3, b0[v], b1[v]);
+          e4m3x4_to_f16x4(__byte_perm(w[v][2], 0, 0x3120), a0, a1);
+          e4m3x4_to_f16x4(__byte_perm(w[v][3], 0, 0x3120), a2, a3);
+          mma_f16_16816(o[2 * i + 1], a0, a1, a2, a3, b0[v], b1[v]);
         }
       }
-      // this warp is done reading the stage
+      // this warp is done reading the stages
       __syncwarp();
-      if (lane == 0) mbar_arrive(empty_bar(st));
+      if (lane == 0)
+#pragma unroll
+        for (int v = 0; v < V; ++v) mbar_arrive(empty_bar((tile + v) % kStages));
+      tile += V;
+      return true;
+    };
+    for (int t = seg.t0; ok && t < seg.t1;) {
+      if (seg.t1 - t > kTile) {
+        ok = tiles(std::integral_constant<int, 2>{}, t);
+        t += 2 * kTile;
+      } else {
+        ok = tiles(std::integral_constant<int, 1>{}, t);
+        t += kTile;
+      }
     }
     if (!ok) break;
 
