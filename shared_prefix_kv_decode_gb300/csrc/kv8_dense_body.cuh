@@ -2,10 +2,15 @@
 // (tcgen05/TMEM), head_dim 128, bf16 q.
 //
 // One CTA takes one (prefix group, KV head j, 128-row block, L_p piece), as the 16-bit dense kernel:
-// rows are the group's (request, head-in-group) pairs of KV head j, and for each 128-token tile i
-//     S(i) = Q K(i)^T       (8 tcgen05.mma 128x128x32, kind::f8f6f4: the codes of K as they are)
+// rows are the group's (request, head-in-group) pairs of KV head j.  For each 64-token tile i, one
+// scale block of the slab,
+//     S(i) = Q K(i)^T       (8 tcgen05.mma 128x64x32, kind::f8f6f4: the codes of K as they are, Q from TMEM)
 //     P(i) = 2^(z - m)      (softmax warps; fp16, written back over S(i) in TMEM)
-//     O   += P(i) V(i)      (8 tcgen05.mma 128x128x16, fp16, with A = P(i) read from TMEM)
+//     O   += P(i) V(i)      (4 tcgen05.mma 128x128x16, fp16, with A = P(i) read from TMEM)
+// A tile passes through S, softmax and PV with about 2,700 clocks of latency (products, commits and
+// barrier waits, exponentials), while the tensor core needs 512 for it and the exponential unit 512
+// as well: five tiles in flight (five S/P buffers of 64 columns, O and Q in the rest of TMEM) cover
+// that.  128-token tiles with three buffers, all that fit, took 1,830 clocks for 128 tokens.
 // Number format.  S takes K's codes straight from TMA and q as the sum of two e4m3 values: each row is
 // scaled by a power of two so that its largest element lies in [2^7, 2^8), hi = e4m3(q) and lo =
 // e4m3(q - hi).  bf16 has 8 significant bits and each part 4, so q = hi + lo exactly down to 2^-2, 2^-9
@@ -13,22 +18,22 @@
 // the largest (bf16 itself rounds an element by 2^-9 of its own size).  Two passes at fp8's rate
 // take the time of one in fp16, and no conversion stands before S.  V's codes become fp16 exactly:
 // P in 8 bits would lose the weights.
-// The scales of a slab are those of 64-token blocks counted from its start, so each half of a tile
-// has one K scale ks and one V scale vs: z = s ks + log2 vs (base 2) costs the FMA that the softmax
-// needs anyway, P = 2^(z - m) is p times vs, which is what meets the V codes, and the row sum adds each
-// half's sum of P once, over vs.  The running maximum m is taken over z.  P carries a factor of 2^7: it
-// is at most 2^15 (m may lag the row's maximum by 2^8, see below), and fp16 keeps its 11 bits down to 2^-21
-// of the largest weight.
+// The scales of a slab are those of 64-token blocks counted from its start, so a tile has one K scale
+// ks and one V scale vs: z = s ks + log2 vs (base 2) costs the FMA that the softmax needs anyway, P =
+// 2^(z - m) is p times vs, which is what meets the V codes, and the row sum adds the tile's sum of P
+// once, over vs.  The running maximum m is taken over z.  P carries a factor of 2^7: it is at most 2^15
+// (m may lag the row's maximum by 2^8, see below), and fp16 keeps its 11 bits down to 2^-21 of the
+// largest weight.
 // Roles (15 warps; the 16th only takes part in the block's barriers here):
-//  * warps 0-7, softmax and epilogue: warp w serves TMEM lanes 32*(w%4).. (row r = lane r), all 128
+//  * warps 0-7, softmax and epilogue: warp w serves TMEM lanes 32*(w%4).. (row r = lane r), all 64
 //    columns of the tiles i with i % 2 == w / 4; the two warps of a row quarter take turns, half a
 //    tile apart.  The running max is a chain over the tiles: the warp of tile i reads the max used
 //    for tile i-1 from shared memory, keeps it unless the tile's row max exceeds it by more than
-//    2^8 (then O is rescaled in TMEM), and publishes its own.
-//  * warps 8-11, V conversion: each takes 32 tokens of every V tile.  It loads their codes by TMA into
-//    its own ring of three, turns 16 codes at a time into fp16 and stores them in the
+//    2^8 (then O is rescaled in TMEM), and publishes its own.  First they bring Q into TMEM.
+//  * warps 8-11, V conversion: each takes 32 tokens of every 128 of V.  It loads their codes by TMA into
+//    its own ring of four, turns 16 codes at a time into fp16 and stores them in the
 //    128-byte-swizzled layout that the MMA operand has (rows past the piece's end as zeros).
-//  * warps 12 and 13, the MMAs: one issues S(i), up to three tiles ahead (three S/P buffers in TMEM), the
+//  * warps 12 and 13, the MMAs: one issues S(i), up to five tiles ahead, the
 //    other PV(i), so that neither's waits hold up the other's products.
 //  * warp 14, the TMA loads of K.
 // Every mbarrier wait is bounded in time; on expiry the CTA raises an abort flag, latches an error,
@@ -53,40 +58,38 @@ using k8s::pack_f16;
 
 constexpr int kD = 128;
 constexpr int kM = kDenseRows;                // 128 query rows per CTA
-constexpr int kN = kDenseTile;                // 128 tokens per tile
-static_assert(kN / 4 == kKv8VBox, "a conversion warp's part of a V tile is one box");
-static_assert(kN == 2 * kKv8Block, "each half of a tile is one block of the slab");
-constexpr int kKSlots = 3;                    // slots of the K ring (codes)
+constexpr int kN = kKv8Block;                 // 64 tokens per tile
+constexpr int kPair = kDenseTile;             // 128 tokens: what the K and V rings hold in a slot
+static_assert(kPair == 2 * kN && kPair / 4 == kKv8VBox, "a conversion warp's part of a V slot is one box");
+constexpr int kKSlots = 4;                    // slots of the K ring (codes)
 constexpr int kVSlots = 3;                    // slots of the V ring (fp16)
-constexpr int kCSlots = 3;                    // slots of each conversion warp's ring of V codes
-constexpr int kSBufs = 3;                     // S/P buffers in TMEM
-static_assert(kKSlots == kSBufs && kVSlots == kSBufs, "one commit tells both that a result is there and a slot free");
+constexpr int kCSlots = 4;                    // slots of each conversion warp's ring of V codes
+constexpr int kSBufs = 5;                     // S/P buffers in TMEM
 constexpr int kSoftmaxWarps = 8;
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
 constexpr int kWarpConv = 8, kConvWarps = 4;
-constexpr int kPart = kN / kConvWarps;        // tokens of a V tile that one warp converts
+constexpr int kPart = kPair / kConvWarps;     // tokens of a V slot that one warp converts
 constexpr int kWarpS = 12, kWarpPv = 13, kWarpTmaK = 14;
 constexpr int kThreads = 512;  // one more warp, for the suffix body's producers
-constexpr int kHalf = kN * 128;               // one 64-dim half of an fp16 tile: 16 KB
+constexpr int kHalf = kPair * 128;            // one 64-dim half of an fp16 slot: 16 KB
 constexpr int kTile = 2 * kHalf;              // 32 KB
-constexpr int kCodes = kN * kD;               // a tile's codes: 16 KB
+constexpr int kCodes = kPair * kD;            // a slot's codes: 16 KB
 constexpr int kPartCodes = kPart * kD;        // 4 KB
-constexpr int kQPart = kM * kD;               // hi (or lo) of the Q block: 16 KB
-constexpr int kOffQ = 0;
-constexpr int kOffK = kOffQ + 2 * kQPart;
+constexpr int kOffK = 0;
 constexpr int kOffV = kOffK + kKSlots * kCodes;
 constexpr int kOffCodes = kOffV + kVSlots * kTile;
 constexpr int kOffUnit = kOffCodes + kConvWarps * kCSlots * kPartCodes;  // [kM] power of two that undoes a row's scaling
 constexpr int kOffMPub = kOffUnit + kM * 4;   // [4 quarters][2 tile parities][32 rows] published maxima
 constexpr int kOffBar = kOffMPub + 4 * 2 * 32 * 4;
-constexpr int kBarArea = 448;
+constexpr int kBarArea = 512;
 constexpr int kSmemBytes = kOffBar + kBarArea + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 static_assert(kVSlots * kTile >= kM * kD * 4, "the epilogue stages the fp32 record rows in the V ring");
 static_assert(kKSlots * kCodes >= kM * 8, "the epilogue keeps the rows' record offsets in the K ring");
 static_assert(kConvWarps * kCSlots * kPartCodes >= 4 * kM * 4, "the epilogue's sums and maxima");
-constexpr uint32_t kTmemCols = 512;           // S/P buffers at 0, 128, 256; O at 384
-constexpr uint32_t kColO = 384;
+constexpr uint32_t kTmemCols = 512;           // S/P buffers at 0, 64, 128, 192, 256; Q (hi, lo) at 320; O at 384
+constexpr uint32_t kColQ = kSBufs * kN, kColO = 384;
+static_assert(kColQ + 2 * kD / 4 <= kColO && kColO + kD <= kTmemCols, "TMEM columns");
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;     // log2 of the largest growth tolerated in P
 constexpr float kShift = 7.0f;                // log2 of the factor that P carries
@@ -94,11 +97,13 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 enum : int {
   kBarKFull = 0,                            // [kKSlots] TMA -> MMA
-  kBarCFull = kBarKFull + kKSlots,          // [kConvWarps][kCSlots] TMA -> conversion (codes of V)
+  kBarKEmpty = kBarKFull + kKSlots,         // [kKSlots] MMA (S of the slot's tiles done) -> TMA
+  kBarCFull = kBarKEmpty + kKSlots,         // [kConvWarps][kCSlots] TMA -> conversion (codes of V)
   kBarVFull = kBarCFull + kConvWarps * kCSlots,  // [kVSlots] conversion -> MMA (kConvWarps arrivals)
-  kBarSFull = kBarVFull + kVSlots,          // [kSBufs] S(i) in TMEM -> softmax; K slot free -> TMA
+  kBarVEmpty = kBarVFull + kVSlots,         // [kVSlots] MMA (PV of the slot's tiles done) -> conversion
+  kBarSFull = kBarVEmpty + kVSlots,         // [kSBufs] S(i) in TMEM -> softmax
   kBarPFull = kBarSFull + kSBufs,           // [kSBufs] P(i) in TMEM -> MMA (128 arrivals)
-  kBarPvDone = kBarPFull + kSBufs,          // [kSBufs] PV(i) done -> softmax; V slot free -> conversion
+  kBarPvDone = kBarPFull + kSBufs,          // [kSBufs] PV(i) done -> softmax, and S(i + kSBufs)
   kBarDrain = kBarPvDone + kSBufs,          // [2] all S (all PV) products done -> teardown
   kBarPair = kBarDrain + 2,                 // [4] the two softmax warps of a row quarter, epilogue (64)
   kBarMPub = kBarPair + 4,                  // [4 quarters][2 parities] max of a tile published (32)
@@ -106,13 +111,14 @@ enum : int {
 };
 static_assert(8 * kNumBars + 16 <= kBarArea, "barrier area");
 
-// D[tmem] (+)= A[smem desc] * B[smem desc], kind::f8f6f4, issued by one thread
-__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                        uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] * B[smem desc], kind::f8f6f4 (A: M rows = TMEM lanes, four 8-bit elements per
+// 32-bit column along K), issued by one thread
+__device__ __forceinline__ void umma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -120,6 +126,29 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64
 // kind::f8f6f4), fp32 accumulator, A K-major.
 __host__ __device__ constexpr uint32_t idesc_fmt0_f32(int M, int N, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
+// 16 columns of this warp's TMEM lanes
+__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(a));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int32_t x, int32_t y, uint32_t mbar) {
@@ -149,7 +178,7 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
   const uint32_t raw_u = smem_u32(smem_raw);
   const uint32_t base = (raw_u + 1023u) & ~1023u;
   unsigned char* smem = smem_raw + (base - raw_u);
-  const uint32_t sQ = base + kOffQ, sK = base + kOffK, sV = base + kOffV, sC = base + kOffCodes;
+  const uint32_t sK = base + kOffK, sV = base + kOffV, sC = base + kOffCodes;
   // row sums and maxima for the epilogue, [kind][parity][row], in the codes' place (idle by then)
   float* red = reinterpret_cast<float*>(smem + kOffCodes);
   float* units = reinterpret_cast<float*>(smem + kOffUnit);
@@ -169,20 +198,22 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
   int32_t t0, t1;
   piece_range(gr, it.split, t0, t1);
   const int n_tiles = t1 > t0 ? (t1 - t0 + kN - 1) / kN : 0;
+  const int n_pairs = (n_tiles + 1) / 2;  // ring slots used
   const bool slab_ok = gr.slab_off >= 0 && gr.slab_off + gr.L_p <= p.n_hot && n_tiles > 0;
   const int32_t rbase = it.row_block * kM;
   const int64_t first_slot = gr.slab_off + t0;
 
+  // slot contents: tokens kPair * i .. of the piece
   auto issue_k = [&](int i) {
     const int st = i % kKSlots;
     mbar_arrive_expect_tx(bar(kBarKFull + st), kCodes);
-    tma_load_2d(sK + st * kCodes, tmk, j * kD, (int32_t)(first_slot + (int64_t)i * kN), bar(kBarKFull + st));
+    tma_load_2d(sK + st * kCodes, tmk, j * kD, (int32_t)(first_slot + (int64_t)i * kPair), bar(kBarKFull + st));
   };
-  // conversion warp w's part of V tile i
+  // conversion warp w's part of V's slot contents i
   auto issue_v = [&](int w, int i) {
     const int c = w * kCSlots + i % kCSlots;
     mbar_arrive_expect_tx(bar(kBarCFull + c), kPartCodes);
-    tma_load_2d(sC + c * kPartCodes, tmv, j * kD, (int32_t)(first_slot + (int64_t)i * kN + w * kPart), bar(kBarCFull + c));
+    tma_load_2d(sC + c * kPartCodes, tmv, j * kD, (int32_t)(first_slot + (int64_t)i * kPair + w * kPart), bar(kBarCFull + c));
   };
   const int l2_ahead = p.l2_ahead;
   if (warp == kWarpTmaK && lane == 0) {
@@ -202,8 +233,8 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
     fence_proxy_async_smem();
     grid_dep_wait();  // the slab may have been written by the work before this kernel
     if (slab_ok) {
-      for (int i = 0; i < min(n_tiles, kKSlots); ++i) issue_k(i);
-      for (int i = 0; i < min(n_tiles, kCSlots); ++i)
+      for (int i = 0; i < min(n_pairs, kKSlots); ++i) issue_k(i);
+      for (int i = 0; i < min(n_pairs, kCSlots); ++i)
         for (int w = 0; w < kConvWarps; ++w) issue_v(w, i);
     }
   }
@@ -214,65 +245,61 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
   // q and the records are touched only after the previous kernel in the stream has completed
   grid_dep_wait();
   grid_dep_launch_dependents();
-  // Q rows of this block -> shared memory as hi and lo, K-major with 128-byte swizzle: row r, 16-byte
-  // chunk c lives at r*128 + ((c%8) ^ (r%8))*16 of each; rows past the group are 0.  The 16 lanes that
-  // hold a row, 8 elements each, agree on its power of two.
-  {
-    constexpr int kQIters = (kM * 16 + kThreads - 1) / kThreads;
-    int32_t qoff[kQIters];
-#pragma unroll
-    for (int k = 0; k < kQIters; ++k) {
-      const int idx = tid + k * kThreads;
-      const int32_t row = rbase + (idx >> 4);
-      qoff[k] = -1;
-      if (idx < kM * 16 && row < rows) qoff[k] = p.group_req[gr.req_begin + row / g];
+  // Q: the two softmax warps of a row quarter take half of their rows' dims each, agree on each row's
+  // power of two through shared memory, and split the elements into hi and lo, four to a word; rows
+  // past the group are 0
+  uint32_t qw[32];
+  float* part = reinterpret_cast<float*>(smem + kOffMPub);  // [2][kM], used for the maxima of tiles later
+  const int qrow = (warp & 3) * 32 + lane, qhalf = warp >> 2;
+  if (warp < kSoftmaxWarps) {
+    const int32_t row = rbase + qrow;
+    const bool have = row < rows;
+    const uint4* src = nullptr;
+    if (have) {
+      const int32_t b = p.group_req[gr.req_begin + row / g];
+      src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                           ((int64_t)b * p.n_q + j * g + row % g) * kD + qhalf * (kD / 2));
     }
-    uint4 qv[kQIters];
+    float amax = 0.f;
 #pragma unroll
-    for (int k = 0; k < kQIters; ++k) {
-      const int idx = tid + k * kThreads;
-      const int32_t row = rbase + (idx >> 4);
-      qv[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (qoff[k] >= 0)
-        qv[k] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                               ((int64_t)qoff[k] * p.n_q + j * g + row % g) * kD)[idx & 15];
+    for (int k = 0; k < 8; ++k) {
+      const uint4 x = have ? src[k] : make_uint4(0u, 0u, 0u, 0u);
+      qw[4 * k] = x.x;
+      qw[4 * k + 1] = x.y;
+      qw[4 * k + 2] = x.z;
+      qw[4 * k + 3] = x.w;
     }
 #pragma unroll
-    for (int k = 0; k < kQIters; ++k) {
-      const int idx = tid + k * kThreads;  // 16 lanes of a warp hold one row
-      uint32_t w[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
-      float amax = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) amax = fmaxf(amax, bf16x2_finite_max(w[i]));
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      float unit;
-      const float f = q_factor<7>(amax, unit);
-      uint32_t hi[2], lo[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float a = __uint_as_float(w[2 * i] << 16) * f, b = __uint_as_float(w[2 * i] & 0xffff0000u) * f;
-        const float c = __uint_as_float(w[2 * i + 1] << 16) * f, d = __uint_as_float(w[2 * i + 1] & 0xffff0000u) * f;
-        // an infinity becomes NaN, as the scores it stands in would end
-        hi[i] = f32x4_to_e4m3x4(a + 0.f * a, b + 0.f * b, c + 0.f * c, d + 0.f * d);
-        float h[4];
-        e4m3x4_to_f32x4(hi[i], h);
-        lo[i] = f32x4_to_e4m3x4(a - h[0], b - h[1], c - h[2], d - h[3]);
-      }
-      if (idx < kM * 16) {
-        const int r = idx >> 4, c = idx & 15;
-        const uint32_t at = sQ + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
-        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
-        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + kQPart), "r"(lo[0]), "r"(lo[1]) : "memory");
-        if (c == 0) units[r] = unit;
-      }
-    }
+    for (int k = 0; k < 32; ++k) amax = fmaxf(amax, bf16x2_finite_max(qw[k]));
+    part[qhalf * kM + qrow] = amax;
   }
-  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (warp < kSoftmaxWarps) {
+    float unit;
+    const float f = q_factor<7>(fmaxf(part[qrow], part[kM + qrow]), unit);
+    if (qhalf == 0) units[qrow] = unit;
+    uint32_t hi[16], lo[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float a = __uint_as_float(qw[2 * k] << 16) * f, b = __uint_as_float(qw[2 * k] & 0xffff0000u) * f;
+      const float c = __uint_as_float(qw[2 * k + 1] << 16) * f, d = __uint_as_float(qw[2 * k + 1] & 0xffff0000u) * f;
+      // an infinity becomes NaN, as the scores it stands in would end
+      hi[k] = f32x4_to_e4m3x4(a + 0.f * a, b + 0.f * b, c + 0.f * c, d + 0.f * d);
+      float v[4];
+      e4m3x4_to_f32x4(hi[k], v);
+      lo[k] = f32x4_to_e4m3x4(a - v[0], b - v[1], c - v[2], d - v[3]);
+    }
+    const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColQ + qhalf * 16;
+    tmem_st16(at, hi);
+    tmem_st16(at + 32, lo);
+    tmem_wait_st();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
 
   if (warp >= kWarpConv && warp < kWarpConv + kConvWarps) {
     // ---------------- conversion: codes of V -> fp16 operand tiles ----------------
@@ -289,8 +316,8 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
     // tokens lt and lt + 4 modulo 8 have two swizzles
     const uint32_t lo0 = row_off + ((ch ^ lt) << 4), hi0 = row_off + (((ch + 1) ^ lt) << 4);
     const uint32_t lo1 = row_off + ((ch ^ (lt + 4)) << 4), hi1 = row_off + (((ch + 1) ^ (lt + 4)) << 4);
-    int issued = slab_ok ? min(n_tiles, kCSlots) : 0, seen = 0;
-    for (int i = 0; slab_ok && i < n_tiles; ++i) {
+    int issued = slab_ok ? min(n_pairs, kCSlots) : 0, seen = 0;
+    for (int i = 0; slab_ok && i < n_pairs; ++i) {
       const int c = w * kCSlots + i % kCSlots, st = i % kVSlots;
       bool ok = mbar_wait_bounded(bar(kBarCFull + c), (i / kCSlots) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
       ok = __all_sync(0xffffffffu, ok);
@@ -300,14 +327,14 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
       uint4 x[kPer];
 #pragma unroll
       for (int n = 0; n < kPer; ++n) x[n] = lds128(src + n * 4 * kD);
-      const int valid = t1 - t0 - i * kN - w * kPart;  // tokens of the part in range, or more
+      const int valid = t1 - t0 - i * kPair - w * kPart;  // tokens of the part in range, or more
       if (valid < kPart) {  // 0 * whatever lies past the piece must not reach O
 #pragma unroll
         for (int n = 0; n < kPer; ++n)
           if (lt + 4 * n >= valid) x[n] = make_uint4(0u, 0u, 0u, 0u);
       }
       if (i >= kVSlots) {
-        ok = mbar_wait_bounded(bar(kBarPvDone + st), ((i / kVSlots) - 1) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
+        ok = mbar_wait_bounded(bar(kBarVEmpty + st), ((i / kVSlots) - 1) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
       }
@@ -331,10 +358,10 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
       __syncwarp();  // the warp has stored its part, and read its codes
       if (lane == 0) {
         mbar_arrive(bar(kBarVFull + st));
-        if (i + kCSlots < n_tiles) {
+        if (i + kCSlots < n_pairs) {
           issue_v(w, i + kCSlots);
-          if (l2_ahead > 0 && i + kCSlots + l2_ahead < n_tiles)
-            tma_prefetch_l2_2d(tmv, j * kD, (int32_t)(first_slot + (int64_t)(i + kCSlots + l2_ahead) * kN + w * kPart));
+          if (l2_ahead > 0 && i + kCSlots + l2_ahead < n_pairs)
+            tma_prefetch_l2_2d(tmv, j * kD, (int32_t)(first_slot + (int64_t)(i + kCSlots + l2_ahead) * kPair + w * kPart));
           issued = i + kCSlots + 1;
         }
       }
@@ -354,14 +381,14 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
   } else if (warp == kWarpTmaK) {
     // ---------------- TMA loads of K ----------------
     if (lane == 0) {
-      int issued = slab_ok ? min(n_tiles, kKSlots) : 0;
-      for (int i = issued; slab_ok && i < n_tiles; ++i) {
-        if (!mbar_wait_bounded(bar(kBarSFull + i % kKSlots), ((i / kKSlots) - 1) & 1, abort_flag, p.err, kDevTimeout,
+      int issued = slab_ok ? min(n_pairs, kKSlots) : 0;
+      for (int i = issued; slab_ok && i < n_pairs; ++i) {
+        if (!mbar_wait_bounded(bar(kBarKEmpty + i % kKSlots), ((i / kKSlots) - 1) & 1, abort_flag, p.err, kDevTimeout,
                                kWaitLimitNs))
           break;
         issue_k(i);
-        if (l2_ahead > 0 && i + l2_ahead < n_tiles)
-          tma_prefetch_l2_2d(tmk, j * kD, (int32_t)(first_slot + (int64_t)(i + l2_ahead) * kN));
+        if (l2_ahead > 0 && i + l2_ahead < n_pairs)
+          tma_prefetch_l2_2d(tmk, j * kD, (int32_t)(first_slot + (int64_t)(i + l2_ahead) * kPair));
         issued = i + 1;
       }
       // never leave with a copy in flight
@@ -377,48 +404,67 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
     }
   } else if (warp == kWarpS || warp == kWarpPv) {
     // ---------------- MMA issuers ----------------
-    if (lane == 0 && !*abort_flag) {
+    // The whole warp runs the loop and one elected lane issues: with the operands' descriptors uniform
+    // over the warp, an MMA is issued every 32 clocks; from inside a one-lane branch, every 45, which is
+    // more than these 128x64x32 products take.
+    if (!*abort_flag) {
       constexpr uint32_t idS = idesc_fmt0_f32(kM, kN, false);
       constexpr uint32_t idO = idesc_fmt0_f32(kM, kD, true);
-      auto wait = [&](int b, int i) {
-        return mbar_wait_bounded(bar(b + i % kSBufs), (i / kSBufs) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
+      const bool el = elect_one();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      auto wait = [&](int b, int slots, int i) {
+        const bool ok = mbar_wait_bounded(bar(b + i % slots), (i / slots) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
+        return __all_sync(0xffffffffu, ok) != 0;
       };
       int committed = 0;
       if (warp == kWarpS) {
-        const uint64_t dq0 = smem_desc_sw128(sQ, 16, 1024);
         const uint64_t dk0 = smem_desc_sw128(sK, 16, 1024);
         for (int i = 0; i < n_tiles; ++i) {
-          // S(i) overwrites S(i-3)/P(i-3), whose last reader is PV(i-3)
-          if (i >= kSBufs && !wait(kBarPvDone, i - kSBufs)) break;
-          if (!wait(kBarKFull, i)) break;
+          // S(i) overwrites S(i-5)/P(i-5), whose last reader is PV(i-5)
+          if (i >= kSBufs && !wait(kBarPvDone, kSBufs, i - kSBufs)) break;
+          if ((i & 1) == 0 && !wait(kBarKFull, kKSlots, i >> 1)) break;
           tc_fence_after();
-          const uint32_t dS = tmem + (uint32_t)((i % kSBufs) * kN);
-          const uint64_t dk = dk0 + (uint64_t)(((i % kKSlots) * kCodes) >> 4);
+          const uint32_t dS = tm + (uint32_t)((i % kSBufs) * kN);
+          const int st = (i >> 1) % kKSlots;
+          const uint64_t dk = dk0 + (uint64_t)((st * kCodes + (i & 1) * kN * kD) >> 4);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)  // lo, the smaller, first
-            umma_f8(dS, dq0 + (uint64_t)(((kk < 4 ? kQPart : 0) + (kk & 3) * 32) >> 4), dk + (uint64_t)(((kk & 3) * 32) >> 4),
-                    idS, kk > 0 ? 1u : 0u);
-          umma_commit(bar(kBarSFull + i % kSBufs));
+            if (el)
+              umma_f8_ts(dS, tm + kColQ + (kk < 4 ? 32 : 0) + (kk & 3) * 8, dk + (uint64_t)(((kk & 3) * 32) >> 4), idS,
+                         kk > 0 ? 1u : 0u);
+          if (el) {
+            umma_commit(bar(kBarSFull + i % kSBufs));
+            if (i & 1) umma_commit(bar(kBarKEmpty + st));
+          }
+          __syncwarp();
           committed += 1;
         }
       } else {
-        // V tile as an MN-major B operand: 16 tokens per step (2048 bytes), the two 64-dim halves
+        // V slot as an MN-major B operand: 16 tokens per step (2048 bytes), the two 64-dim halves
         // kHalf apart (leading offset), 8-token groups 1024 bytes apart (stride)
         const uint64_t dv0 = smem_desc_sw128(sV, kHalf, 1024);
         for (int i = 0; i < n_tiles; ++i) {
-          if (!wait(kBarVFull, i) || !wait(kBarPFull, i)) break;
+          if ((i & 1) == 0 && !wait(kBarVFull, kVSlots, i >> 1)) break;
+          if (!wait(kBarPFull, kSBufs, i)) break;
           tc_fence_after();
-          const uint32_t pa = tmem + (uint32_t)((i % kSBufs) * kN);  // P(i): 64 columns, two tokens per column
-          const uint64_t dv = dv0 + (uint64_t)(((i % kVSlots) * kTile) >> 4);
+          const uint32_t pa = tm + (uint32_t)((i % kSBufs) * kN);  // P(i): 32 columns, two tokens per column
+          const int st = (i >> 1) % kVSlots;
+          const uint64_t dv = dv0 + (uint64_t)((st * kTile + (i & 1) * (kN / 16) * 2048) >> 4);
 #pragma unroll
           for (int ks = 0; ks < kN / 16; ++ks)
-            umma_f16_ts(tmem + kColO, pa + (uint32_t)(ks * 8), dv + (uint64_t)((ks * 2048) >> 4), idO, (i > 0 || ks > 0) ? 1u : 0u);
-          umma_commit(bar(kBarPvDone + i % kSBufs));
+            if (el)
+              umma_f16_ts(tm + kColO, pa + (uint32_t)(ks * 8), dv + (uint64_t)((ks * 2048) >> 4), idO,
+                          (i > 0 || ks > 0) ? 1u : 0u);
+          if (el) {
+            umma_commit(bar(kBarPvDone + i % kSBufs));
+            if (i & 1) umma_commit(bar(kBarVEmpty + st));
+          }
+          __syncwarp();
           committed += 1;
         }
       }
-      // drain: every tcgen05 op this thread issued completes before the CTA frees TMEM
-      if (committed > 0) {
+      // drain: every tcgen05 op the elected lane issued completes before the CTA frees TMEM
+      if (committed > 0 && el) {
         const uint32_t drain = bar(kBarDrain + (warp == kWarpS ? 0 : 1));
         umma_commit(drain);
         const uint64_t t_start = globaltimer_ns();
@@ -448,17 +494,13 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
       h = j * g + row % g;
       rec = p.reqs[b].rec_base + it.split;
     }
-    // the scales of tile i's two blocks (the second block's of a tile that ends in its first are
-    // not used: the first's again)
+    // the scales of tile i
     const int64_t scale_at = (int64_t)p.n_kv * kD + 4 * j;
-    float ks[2], vs[2];
+    float ks, vs;
     auto load_scales = [&](int i) {
       const int64_t a = (first_slot + (int64_t)i * kN) * p.kv8_row + scale_at;
-      const int64_t b = a + (t1 - t0 - i * kN > kKv8Block ? kKv8Block * p.kv8_row : 0);
-      ks[0] = *reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.kpool) + a);
-      ks[1] = *reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.kpool) + b);
-      vs[0] = *reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.vpool) + a);
-      vs[1] = *reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.vpool) + b);
+      ks = *reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.kpool) + a);
+      vs = *reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.vpool) + a);
     };
     float m_own = -INFINITY;   // max (of z, base 2) used for this warp's latest tile
     float l = 0.f;             // this warp's share of the row sum, relative to m_own
@@ -467,28 +509,33 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
     if (ok && par < n_tiles) load_scales(par);
     for (int i = par; ok && i < n_tiles; i += 2) {
       const int sb = i % kSBufs;
-      const float ca[2] = {scale * ks[0], scale * ks[1]};
-      const float cb[2] = {lg2_approx(vs[0]), lg2_approx(vs[1])};
+      const float ca = scale * ks, cb = lg2_approx(vs);
       if (i + 2 < n_tiles) load_scales(i + 2);
-      ok = mbar_wait_bounded(bar(kBarSFull + sb), (i / kSBufs) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
+      // the max used for tile i-1, decided by the other warp of the quarter
+      float m_prev = -INFINITY;
+      if (i > 0) {
+        const int pp = (i - 1) & 1;
+        ok = mbar_wait_bounded(bar(kBarMPub + quad * 2 + pp), ((i - 1) >> 1) & 1, abort_flag, p.err, kDevTimeout,
+                               kWaitLimitNs);
+        m_prev = mpub[pp * 32 + lane];
+      }
+      ok = ok && mbar_wait_bounded(bar(kBarSFull + sb), (i / kSBufs) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
       ok = __all_sync(0xffffffffu, ok);  // the TMEM loads below are warp-collective
       if (!ok) break;
       tc_fence_after();
       const int valid = min(kN, t1 - t0 - i * kN);               // tokens of the tile in range
       const uint32_t ts = tmem + lane_off + (uint32_t)(sb * kN);
-      // row max of z over the 128 columns, half by half (the factors are positive); S(i) is read
-      // again below for the exponentials, which keeps the thread's registers within the launch's
-      float mx = -INFINITY;
+      uint32_t u[2][32];
+      GRANIKV_TMEM_LD32(ts, u[0]);
+      GRANIKV_TMEM_LD32(ts + 32, u[1]);
+      tmem_wait_ld();
+      if (valid < kN) {  // masked keys: -inf, so their weight is 0
 #pragma unroll
-      for (int hb = 0; hb < 2; ++hb) {
-        uint32_t u[2][32];
-        GRANIKV_TMEM_LD32(ts + hb * 64, u[0]);
-        GRANIKV_TMEM_LD32(ts + hb * 64 + 32, u[1]);
-        tmem_wait_ld();
-        if (valid < kN) {
-#pragma unroll
-          for (int k = 0; k < 64; ++k) u[k >> 5][k & 31] = 64 * hb + k < valid ? u[k >> 5][k & 31] : 0xff800000u;
-        }
+        for (int k = 0; k < kN; ++k) u[k >> 5][k & 31] = k < valid ? u[k >> 5][k & 31] : 0xff800000u;
+      }
+      // row max of z (the factor is positive)
+      float mx;
+      {
         float t[22], w[7];
         auto sv = [&](int k) { return __uint_as_float(u[k >> 5][k & 31]); };
 #pragma unroll
@@ -496,21 +543,13 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
         t[21] = sv(63);
 #pragma unroll
         for (int k = 0; k < 7; ++k) w[k] = max3f(t[3 * k], t[3 * k + 1], t[3 * k + 2]);
-        const float hm = max3f(max3f(w[0], w[1], w[2]), max3f(w[3], w[4], w[5]), fmaxf(w[6], t[21]));
-        mx = fmaxf(mx, hm * ca[hb] + cb[hb]);
+        mx = max3f(max3f(w[0], w[1], w[2]), max3f(w[3], w[4], w[5]), fmaxf(w[6], t[21])) * ca + cb;
       }
-      // the max used for tile i: that of tile i-1 (decided by the other warp of the quarter),
-      // moved only when this tile's row max exceeds it by more than 2^kRescaleThreshold
+      // the max used for tile i: moved only when this tile's row max exceeds the last one by more
+      // than 2^kRescaleThreshold
       float m_i = mx;
       bool warp_need = false;
-      float m_prev = -INFINITY;
       if (i > 0) {
-        const int pp = (i - 1) & 1;
-        ok = mbar_wait_bounded(bar(kBarMPub + quad * 2 + pp), ((i - 1) >> 1) & 1, abort_flag, p.err, kDevTimeout,
-                               kWaitLimitNs);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        m_prev = mpub[pp * 32 + lane];
         warp_need = __any_sync(0xffffffffu, mx > m_prev + kRescaleThreshold);
         m_i = warp_need ? fmaxf(m_prev, mx) : m_prev;
       }
@@ -526,37 +565,27 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
         if (!ok) break;
         tc_fence_after();
         const float alpha = m_prev == m_i ? 1.f : ex2_approx(m_prev - m_i);
-        uint32_t u[32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t ta = tmem + lane_off + kColO + c * 32;
-          GRANIKV_TMEM_LD32(ta, u);
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t x[16];
+          const uint32_t ta = tmem + lane_off + kColO + c * 16;
+          tmem_ld16(ta, x);
           tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * alpha);
-          GRANIKV_TMEM_ST32(ta, u);
+          for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * alpha);
+          tmem_st16(ta, x);
         }
         tmem_wait_st();
       }
       if (m_own != m_i && m_own != -INFINITY) l *= ex2_approx(m_own - m_i);
       m_own = m_i;
-      // P = 2^(z - m + kShift), packed two per 32-bit column and written over columns [0, 64) of the
-      // S(i) buffer: S columns [64*hb, 64*hb + 64) are in registers before their P goes to
-      // columns [32*hb, 32*hb + 32)
+      // P = 2^(z - m + kShift), packed two per 32-bit column and written over columns [0, 32) of the
+      // S(i) buffer, whose 64 columns are in registers
       const float m_use = m_i == -INFINITY ? 0.f : m_i;
-#pragma unroll
-      for (int hb = 0; hb < 2; ++hb) {
-        const float off = cb[hb] - m_use + kShift;
-        const uint64_t scale2 = f2_pack(ca[hb], ca[hb]), nm2 = f2_pack(off, off);
-        uint64_t acc[2] = {0ull, 0ull};  // packed partial sums of the half (0.0f bit patterns)
-        uint32_t u[2][32];
-        GRANIKV_TMEM_LD32(ts + hb * 64, u[0]);
-        GRANIKV_TMEM_LD32(ts + hb * 64 + 32, u[1]);
-        tmem_wait_ld();
-        if (valid < kN) {  // masked keys: -inf, so their weight is 0
-#pragma unroll
-          for (int k = 0; k < 64; ++k) u[k >> 5][k & 31] = 64 * hb + k < valid ? u[k >> 5][k & 31] : 0xff800000u;
-        }
+      {
+        const float off = cb - m_use + kShift;
+        const uint64_t scale2 = f2_pack(ca, ca), nm2 = f2_pack(off, off);
+        uint64_t acc[2] = {0ull, 0ull};  // packed partial sums (0.0f bit patterns)
         uint32_t pk[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
@@ -569,11 +598,11 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
           acc[k & 1] = f2_add(acc[k & 1], f2_pack(ea, eb));
           pk[k] = pack_f16(ea, eb);
         }
-        GRANIKV_TMEM_ST32(tmem + lane_off + (uint32_t)(sb * kN + hb * 32), pk);
+        GRANIKV_TMEM_ST32(ts, pk);
         float la, lb;
         f2_unpack(f2_add(acc[0], acc[1]), la, lb);
         // over vs, by the very logarithm that P has
-        l += (la + lb) * ex2_approx(-cb[hb]);
+        l += (la + lb) * ex2_approx(-cb);
       }
       tmem_wait_st();
       tc_fence_before();
