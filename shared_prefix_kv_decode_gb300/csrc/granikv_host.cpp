@@ -884,6 +884,7 @@ granikv_status granikv_cold_weigh(granikv_ctx* c, int32_t layer, const void* q, 
   a.n_kv = c->cfg.n_kv;
   a.d = c->cfg.head_dim;
   a.g = c->g;
+  a.num_sms = c->num_sms;
   a.keep = keep;
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c->cfg.head_dim));
   a.err = c->d_err;
@@ -1788,7 +1789,7 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
     if (p->n_sitems <= 0) return cudaSuccess;
     c->n_kernels += 1;
     if (p->suffix_impl == kImplKv8Suffix) return launch_kv8_suffix(a, a.scta_begin, p->n_scta, st, pdl);
-    if (p->suffix_impl == kImplKv8Generic) return launch_kv8_suffix_generic(c->cfg.dtype, a, st);
+    if (p->suffix_impl == kImplKv8Generic) return launch_kv8_generic(c->cfg.dtype, a, 0, 0, true, st);
     return p->suffix_impl == kImplSuffixMma ? launch_suffix_mma(a, a.scta_begin, p->n_scta, st, pdl)
                                             : launch_suffix_generic(c->cfg.dtype, a, st);
   };
@@ -1801,8 +1802,7 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
       c->n_kernels += 1;
     }
     if (r == cudaSuccess && p->pitem_count[kImplKv8Generic] > 0) {
-      r = launch_kv8_prefix_generic(c->cfg.dtype, a, p->pitem_first[kImplKv8Generic], p->pitem_count[kImplKv8Generic],
-                                    st);
+      r = launch_kv8_generic(c->cfg.dtype, a, p->pitem_first[kImplKv8Generic], p->pitem_count[kImplKv8Generic], false, st);
       c->n_kernels += 1;
     }
     if (r == cudaSuccess && p->pitem_count[kImplKv8Dense] > 0) {
@@ -1856,6 +1856,13 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
     c->n_kernels += 1;
     if (e == cudaSuccess) e = launch_merge_k(true);
     return e == cudaErrorNotSupported ? GRANIKV_ERR_UNSUPPORTED : cuda_status(e);
+  }
+  if (p->n_pitems > 0 && p->pitem_count[kImplKv8Generic] == p->n_pitems && p->suffix_impl == kImplKv8Generic) {
+    // CUDA-core prefix and suffix items in one launch, then the merge
+    e = launch_kv8_generic(c->cfg.dtype, a, p->pitem_first[kImplKv8Generic], p->n_pitems, p->n_sitems > 0, s);
+    c->n_kernels += 1;
+    if (e == cudaSuccess) e = launch_merge_k(false);
+    return cuda_status(e);
   }
   const bool one_launch = p->concurrent && p->n_pitems > 0 && n_dense + n_casc == p->n_pitems &&
                           (n_dense == 0 || c->has_tmaps) && p->suffix_impl == kImplSuffixMma && p->n_sitems > 0;

@@ -161,6 +161,7 @@ struct WeighParams {
   float* weight;               // [B, cap]
   int64_t n_slots, n_hot;
   int32_t cap, B, n_q, n_kv, d, g;
+  int32_t num_sms;
   float keep;                  // weight = keep * weight + this step's
   float scale_log2;
   int32_t* err;
@@ -218,9 +219,9 @@ cudaError_t launch_kv8_append(int32_t dtype, const void* k_new, const void* v_ne
                               uint8_t* kpool, uint8_t* vpool, int32_t n_kv, int32_t d, int64_t n_hot,
                               int64_t n_slots, int32_t* err, cudaStream_t s);
 cudaError_t launch_kv8_append_newest(int32_t dtype, const AttnParams& p, cudaStream_t s);
-cudaError_t launch_kv8_prefix_generic(int32_t dtype, const AttnParams& p, int32_t first_item, int32_t n_items,
-                                      cudaStream_t s);
-cudaError_t launch_kv8_suffix_generic(int32_t dtype, const AttnParams& p, cudaStream_t s);
+// CUDA-core attention of n_items prefix items and, with suffix, of the suffix items, in one launch.
+cudaError_t launch_kv8_generic(int32_t dtype, const AttnParams& p, int32_t first_item, int32_t n_items, bool suffix,
+                               cudaStream_t s);
 // Tensor-core path of the 8-bit cache (kernels_kv8_tc.cu): dense prefix items and suffix token-CTAs in
 // one grid (either count may be 0; n_tail as for launch_prefix_suffix_tc), and the suffix alone.
 cudaError_t launch_kv8_step(const AttnParams& p, int32_t first_dense, int32_t n_dense, const CUtensorMap& tmk,

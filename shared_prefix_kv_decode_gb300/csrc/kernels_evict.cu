@@ -8,6 +8,8 @@
 #include "mma_util.cuh"
 #include "tc_util.cuh"
 
+#include <cooperative_groups.h>
+
 #include <type_traits>
 
 namespace granikv {
@@ -25,6 +27,7 @@ struct WeighRows {
   int32_t first[N + 1];  // chunks of the rows before
   int32_t len[N];
   int32_t n, b0;         // rows here; row r is request b0 + r
+  int32_t tokens;        // of a chunk
 };
 
 // Chunk -> (row of the parameter, first token); a chunk that begins past the row's live tokens has n <= 0.
@@ -127,7 +130,10 @@ __global__ void __launch_bounds__(256) weigh_generic_kernel(WeighParams p, const
 // multiplies the scores, and q is brought into fp16's range by a power of two per query head
 // (exact but for elements 2^-28 below the row's largest).
 // The units' sums go to shared memory and are added in KV-head order: the result has one order.
-constexpr int kChunk = 64;          // tokens of a CTA
+// A CTA takes 64, 128 or 256 tokens: its start (length, slots, q, first rows: four trips to memory one
+// after the other) costs about 4 us, so long rows take more tokens a CTA as long as the grid still
+// fills the SMs twice over.
+constexpr int kChunkMin = 64, kChunkMax = 256;
 constexpr int kMaxSums = 40 * 1024; // shared memory for the units' sums
 
 template <bool KV8, int D>
@@ -139,14 +145,16 @@ struct KRows {
 
 template <bool KV8, int D, int N>
 __global__ void __launch_bounds__(256, 2) weigh_mma_kernel(WeighParams p, const __grid_constant__ WeighRows<N> rows) {
-  extern __shared__ float s_sum[];  // [n_kv][kChunk]
-  __shared__ int32_t s_slot[kChunk];
+  extern __shared__ float s_sum[];  // [n_kv][rows.tokens]
+  __shared__ int32_t s_slot[kChunkMax];
+  const int kChunk = rows.tokens;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = lane >> 2, c = lane & 3;
   int32_t b, t0, n;
   chunk_of(rows, p.live_len, blockIdx.x, kChunk, b, t0, n);
   if (n <= 0) return;
-  if (tid < kChunk) {
+  // every place up to the last unit's end has a slot or -1
+  if (tid < (n + 15) / 16 * 16) {
     int32_t slot = -1;
     if (tid < n) {
       slot = p.req_to_slot[(int64_t)b * p.cap + t0 + tid];
@@ -157,7 +165,6 @@ __global__ void __launch_bounds__(256, 2) weigh_mma_kernel(WeighParams p, const 
     }
     s_slot[tid] = slot;
   }
-  __syncthreads();
   const int n_units = (n + 15) / 16 * p.n_kv;
   using Rows = KRows<KV8, D>;
   // the row of a slot (or, for a slot that does not count, zeros)
@@ -255,12 +262,31 @@ __global__ void __launch_bounds__(256, 2) weigh_mma_kernel(WeighParams p, const 
       s_sum[j * kChunk + tile + r + 8] = w1;
     }
   };
-  Rows k0, k1;
-  load_unit(warp, k0);
-  for (int u = warp; u < n_units; u += 16) {
-    load_unit(u + 8, k1);
-    unit(u, k0);
-    if (u + 8 < n_units) {
+  // q of the warp's first units' heads is on its way with the slots
+  if (warp < n_units) load_q(warp % p.n_kv * p.g, (warp % p.n_kv + 1) * p.g);
+  __syncthreads();
+  // rows are requested one unit ahead (16-bit rows: 32 registers a unit) or two (packed rows: 16)
+  if constexpr (KV8) {
+    Rows k0, k1, k2;
+    load_unit(warp, k0);
+    load_unit(warp + 8, k1);
+    for (int u = warp; u < n_units; u += 24) {
+      load_unit(u + 16, k2);
+      unit(u, k0);
+      if (u + 8 >= n_units) break;
+      load_unit(u + 24, k0);
+      unit(u + 8, k1);
+      if (u + 16 >= n_units) break;
+      load_unit(u + 32, k1);
+      unit(u + 16, k2);
+    }
+  } else {
+    Rows k0, k1;
+    load_unit(warp, k0);
+    for (int u = warp; u < n_units; u += 16) {
+      load_unit(u + 8, k1);
+      unit(u, k0);
+      if (u + 8 >= n_units) break;
       load_unit(u + 16, k0);
       unit(u + 8, k1);
     }
@@ -290,7 +316,151 @@ struct EvictRows {
 
 constexpr int kEvictThreads = 1024;
 
-// One CTA per row: a radix selection (four passes of 8 bits) finds the key of the n_evict-th
+// Sum of v over the threads before this one, and over all (block of kEvictThreads); s: 33 words.
+__device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* s, uint32_t& total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t upto = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  __syncthreads();
+  if (lane == 31) s[warp] = upto;
+  __syncthreads();
+  uint32_t x = s[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  total = __shfl_sync(0xffffffffu, x, 31);
+  const uint32_t before = __shfl_sync(0xffffffffu, x, warp ? warp - 1 : 0);
+  return (warp ? before : 0u) + upto - v;
+}
+
+// Rows of up to 8 * 1024 * PER tokens: a cluster of CTAs per row, each with a slice of it in registers
+// (PER tokens a thread: slot and weight).  The whole row is read once and written once; what it costs
+// is latency.  A radix selection in three digits (11, 11 and 10 bits: the first one, sign, exponent
+// and two mantissa bits, already spreads softmax weights over many bins) finds the key of the
+// n_evict-th lightest candidate: each CTA counts its slice in shared memory, and after a cluster
+// barrier adds up the others' counts.  Then every CTA knows how many leave before its slice, and
+// places each token by ballots.  All of a row's tokens are in registers before the barrier that
+// precedes the first write, so the row is closed up in place.  Counts are whole numbers: the result
+// does not depend on the order of the atomics.
+template <int PER, int N>
+__global__ void __launch_bounds__(kEvictThreads, 1)
+    evict_cluster_kernel(const __grid_constant__ EvictRows<N> rows, int32_t row0, int32_t keep_last, int32_t cs,
+                         int32_t* __restrict__ req_to_slot, int32_t* __restrict__ suffix_len,
+                         float* __restrict__ weight, int32_t cap, int32_t* __restrict__ slots_out) {
+  namespace cg = cooperative_groups;
+  constexpr int kBins = 2048;
+  __shared__ uint32_t s_hist[3][kBins];
+  __shared__ uint32_t s_scan[33];
+  __shared__ uint32_t s_cnt[PER * 32];  // tokens of (k, warp): below | equal << 16
+  __shared__ uint32_t s_total, s_prefix;
+  __shared__ int32_t s_left;
+  const EvictRow r = rows.r[blockIdx.x / cs];
+  const int32_t b = row0 + blockIdx.x / cs, rank = blockIdx.x % cs;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0 && rank == 0 && suffix_len) suffix_len[b] = r.len - r.n_evict;
+  if (r.n_evict <= 0) return;  // the whole cluster
+  cg::cluster_group cluster = cg::this_cluster();
+  int32_t* tab = req_to_slot + (int64_t)b * cap;
+  float* wt = weight + (int64_t)b * cap;
+  const int32_t slice = (r.len + cs - 1) / cs;
+  const int32_t p0 = rank * slice + tid, p1 = min(r.len, (rank + 1) * slice);  // slice <= PER * 1024
+  const int32_t c0 = r.first, c1 = r.len - keep_last;                          // candidates
+  float w[PER];
+  int32_t slot[PER];
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int32_t p = p0 + k * kEvictThreads;
+    const bool in = p < p1;
+    w[k] = in ? wt[p] : 0.f;
+    slot[k] = in ? tab[p] : 0;
+  }
+  auto candidate = [&](int k) {
+    const int32_t p = p0 + k * kEvictThreads;
+    return p < p1 && p >= c0 && p < c1;
+  };
+  for (int i = tid; i < 3 * kBins; i += kEvictThreads) (&s_hist[0][0])[i] = 0u;
+  __syncthreads();
+  uint32_t prefix = 0;
+  int32_t left = r.n_evict;
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int sh = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const uint32_t key = weight_key(w[k]);
+      const bool match = pass == 0 || (key >> (sh + bits)) == (prefix >> (sh + bits));
+      if (candidate(k) && match) atomicAdd(&s_hist[pass][(key >> sh) & ((1u << bits) - 1u)], 1u);
+    }
+    cluster.sync();  // (for one CTA, a block barrier)
+    uint32_t a = 0, c = 0;  // the row's counts of bins 2 tid and 2 tid + 1
+    for (int q = 0; q < cs; ++q) {
+      const uint2 x = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&s_hist[pass][2 * tid], q));
+      a += x.x;
+      c += x.y;
+    }
+    uint32_t total;
+    const int32_t before = (int32_t)block_exclusive(a + c, s_scan, total);
+    if (before < left && left <= before + (int32_t)(a + c)) {
+      const bool second = left > before + (int32_t)a;
+      s_prefix = prefix | ((uint32_t)(2 * tid + (second ? 1 : 0)) << sh);
+      s_left = left - before - (second ? (int32_t)a : 0);
+    }
+    __syncthreads();
+    prefix = s_prefix;
+    left = s_left;
+  }
+  // leavers: keys below `prefix`, and the first `left` with that key
+  uint32_t below[PER], equal[PER];  // ballots of this warp's tokens
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const uint32_t key = weight_key(w[k]);
+    below[k] = __ballot_sync(0xffffffffu, candidate(k) && key < prefix);
+    equal[k] = __ballot_sync(0xffffffffu, candidate(k) && key == prefix);
+    if (lane == 0) s_cnt[k * 32 + warp] = (uint32_t)__popc(below[k]) | ((uint32_t)__popc(equal[k]) << 16);
+  }
+  __syncthreads();
+  {
+    uint32_t total;
+    const uint32_t v = tid < PER * 32 ? s_cnt[tid] : 0u;
+    const uint32_t ex = block_exclusive(v, s_scan, total);
+    if (tid < PER * 32) s_cnt[tid] = ex;
+    if (tid == 0) s_total = total;
+  }
+  cluster.sync();  // every slice is in registers and counted
+  int32_t base_b = 0, base_e = 0;
+  for (int q = 0; q < rank; ++q) {
+    const uint32_t x = *cluster.map_shared_rank(&s_total, q);
+    base_b += (int32_t)(x & 0xffffu);
+    base_e += (int32_t)(x >> 16);
+  }
+  const uint32_t lower = (1u << lane) - 1u;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int32_t p = p0 + k * kEvictThreads;
+    if (p >= p1) continue;
+    const uint32_t ex = s_cnt[k * 32 + warp];
+    const int32_t nb = base_b + (int32_t)(ex & 0xffffu) + __popc(below[k] & lower);
+    const int32_t ne = base_e + (int32_t)(ex >> 16) + __popc(equal[k] & lower);
+    const int32_t gone = nb + min(ne, left);  // leavers before this place
+    const bool leaves = ((below[k] >> lane) & 1u) || (((equal[k] >> lane) & 1u) && ne < left);
+    if (leaves) {
+      slots_out[r.out + gone] = slot[k];
+    } else if (gone > 0) {
+      tab[p - gone] = slot[k];
+      wt[p - gone] = w[k];
+    }
+    if (p >= r.len - r.n_evict) wt[p] = 0.f;
+  }
+  cluster.sync();  // no CTA leaves while another reads its counts
+}
+
+// Longer rows.  One CTA per row: a radix selection (four passes of 8 bits) finds the key of the n_evict-th
 // lightest candidate; one pass in place then closes the row up, tile by tile.  A tile's places are
 // read before any is written, and tokens only move towards the row's start, so no place is
 // overwritten before it is read.
@@ -403,38 +573,70 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
   for (int32_t t = r.len - r.n_evict + tid; t < r.len; t += kEvictThreads) wt[t] = 0.f;
 }
 
+template <int PER, int N>
+cudaError_t evict_cluster(const EvictRows<N>& a, int32_t row0, int32_t n, int32_t cs, int32_t keep_last,
+                          int32_t* req_to_slot, int32_t* suffix_len, float* weight, int32_t cap, int32_t* slots_out,
+                          cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(n * cs));
+  cfg.blockDim = dim3(kEvictThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict_cluster_kernel<PER, N>, a, row0, keep_last, cs, req_to_slot, suffix_len, weight,
+                            cap, slots_out);
+}
+
 template <int N>
 cudaError_t evict_n(const EvictRow* rows, int32_t row0, int32_t n, int32_t keep_last, int32_t* req_to_slot,
                     int32_t* suffix_len, float* weight, int32_t cap, int32_t* slots_out, cudaStream_t s) {
   EvictRows<N> a{};
-  for (int32_t i = 0; i < n; ++i) a.r[i] = rows[i];
+  int32_t longest = 1;
+  for (int32_t i = 0; i < n; ++i) {
+    a.r[i] = rows[i];
+    if (rows[i].n_evict > 0 && rows[i].len > longest) longest = rows[i].len;
+  }
+  // the fewest CTAs (a power of two, 8 at most) whose threads hold the longest row at PER tokens each;
+  // two a thread while that is not more than a grid of about two CTAs an SM, else eight or sixteen
+  auto ctas = [&](int per) {
+    int32_t cs = 1;
+    while ((int64_t)cs * per * kEvictThreads < longest) cs *= 2;
+    return cs;
+  };
+  if (ctas(2) <= 8 && n * ctas(2) <= 304)
+    return evict_cluster<2>(a, row0, n, ctas(2), keep_last, req_to_slot, suffix_len, weight, cap, slots_out, s);
+  if (ctas(8) <= 8)
+    return evict_cluster<8>(a, row0, n, ctas(8), keep_last, req_to_slot, suffix_len, weight, cap, slots_out, s);
+  if (ctas(16) <= 8)
+    return evict_cluster<16>(a, row0, n, ctas(16), keep_last, req_to_slot, suffix_len, weight, cap, slots_out, s);
   evict_kernel<N><<<n, kEvictThreads, 0, s>>>(a, row0, keep_last, req_to_slot, suffix_len, weight, cap, slots_out);
   return cudaGetLastError();
+}
+
+template <typename T>
+bool weigh_on_mma(const WeighParams& p) {
+  return std::is_same_v<T, __nv_bfloat16> && (p.d == 128 || p.d == 64) &&
+         (int)sizeof(float) * p.n_kv * kChunkMax <= kMaxSums;
 }
 
 template <typename T, bool KV8, int N>
 cudaError_t weigh_launch(const WeighParams& p, const WeighRows<N>& rows, int32_t chunks, cudaStream_t s) {
   if constexpr (std::is_same_v<T, __nv_bfloat16>) {
-    const int smem = (int)sizeof(float) * p.n_kv * kChunk;
-    if (p.d == 128 && smem <= kMaxSums) {
-      weigh_mma_kernel<KV8, 128, N><<<chunks, 256, smem, s>>>(p, rows);
-      return cudaGetLastError();
-    }
-    if (p.d == 64 && smem <= kMaxSums) {
-      weigh_mma_kernel<KV8, 64, N><<<chunks, 256, smem, s>>>(p, rows);
+    if (weigh_on_mma<T>(p)) {
+      const int smem = (int)sizeof(float) * p.n_kv * rows.tokens;
+      if (p.d == 128) weigh_mma_kernel<KV8, 128, N><<<chunks, 256, smem, s>>>(p, rows);
+      else weigh_mma_kernel<KV8, 64, N><<<chunks, 256, smem, s>>>(p, rows);
       return cudaGetLastError();
     }
   }
   const int smem = (int)sizeof(float) * (kTok * (p.d + 1) + 8 * kTok);
   weigh_generic_kernel<T, KV8, N><<<chunks, 256, smem, s>>>(p, rows);
   return cudaGetLastError();
-}
-
-template <typename T, bool KV8>
-int weigh_tokens(const WeighParams& p) {
-  const bool mma = std::is_same_v<T, __nv_bfloat16> && (p.d == 128 || p.d == 64) &&
-                   (int)sizeof(float) * p.n_kv * kChunk <= kMaxSums;
-  return mma ? kChunk : kTok;
 }
 
 template <typename T, bool KV8, int N>
@@ -445,18 +647,25 @@ cudaError_t weigh_rows(const WeighParams& p, const int32_t* seq_len, int32_t b0,
     rows.first[r] = (int32_t)chunks;
     rows.len[r] = seq_len[b0 + r];
     chunks += (seq_len[b0 + r] + tokens - 1) / tokens;
+    if (chunks > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
   }
-  if (chunks > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
   rows.first[n] = (int32_t)chunks;
   rows.n = n;
   rows.b0 = b0;
+  rows.tokens = tokens;
   return chunks ? weigh_launch<T, KV8, N>(p, rows, (int32_t)chunks, s) : cudaSuccess;
 }
 
 template <typename T, bool KV8>
 cudaError_t weigh_all(const WeighParams& p, const int32_t* seq_len, cudaStream_t s) {
   constexpr int kSmall = 64, kLarge = 1024;
-  const int tokens = weigh_tokens<T, KV8>(p);
+  int tokens = kTok;
+  if (weigh_on_mma<T>(p)) {
+    int64_t total = 0;
+    for (int32_t b = 0; b < p.B; ++b) total += seq_len[b];
+    tokens = kChunkMax;
+    while (tokens > kChunkMin && total < 4LL * p.num_sms * tokens) tokens /= 2;
+  }
   cudaError_t e = cudaSuccess;
   for (int32_t b = 0; b < p.B && e == cudaSuccess;) {
     const int32_t n = p.B - b < kLarge ? p.B - b : kLarge;

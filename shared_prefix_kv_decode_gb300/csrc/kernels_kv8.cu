@@ -13,49 +13,63 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ void latch(int32_t* err, int32_t code) { atomicCAS(err, 0, code); }
 
-// 8 consecutive elements of a 16-byte aligned row.
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// 16 bytes of a row, kept as they came: 8 bf16 or 4 fp32 elements.
+template <typename T>
+struct Piece;
+template <>
+struct Piece<__nv_bfloat16> {
+  static constexpr int kElems = 8;
+  uint4 w;
+  __device__ __forceinline__ float amax() const {
+    return fmaxf(fmaxf(bf16x2_finite_max(w.x), bf16x2_finite_max(w.y)), fmaxf(bf16x2_finite_max(w.z), bf16x2_finite_max(w.w)));
   }
-}
+  __device__ __forceinline__ void store(uint8_t* dst, float inv) const {
+    auto lo = [&](uint32_t x) { return __uint_as_float(x << 16) * inv; };
+    auto hi = [&](uint32_t x) { return __uint_as_float(x & 0xffff0000u) * inv; };
+    *reinterpret_cast<uint2*>(dst) = make_uint2(f32x4_to_e4m3x4(lo(w.x), hi(w.x), lo(w.y), hi(w.y)),
+                                                f32x4_to_e4m3x4(lo(w.z), hi(w.z), lo(w.w), hi(w.w)));
+  }
+};
+template <>
+struct Piece<float> {
+  static constexpr int kElems = 4;
+  uint4 w;
+  __device__ __forceinline__ float amax() const {
+    return fmaxf(fmaxf(finite_abs(__uint_as_float(w.x)), finite_abs(__uint_as_float(w.y))),
+                 fmaxf(finite_abs(__uint_as_float(w.z)), finite_abs(__uint_as_float(w.w))));
+  }
+  __device__ __forceinline__ void store(uint8_t* dst, float inv) const {
+    *reinterpret_cast<uint32_t*>(dst) = f32x4_to_e4m3x4(__uint_as_float(w.x) * inv, __uint_as_float(w.y) * inv,
+                                                        __uint_as_float(w.z) * inv, __uint_as_float(w.w) * inv);
+  }
+};
 
-// One block of kKv8Block slab tokens of one KV head, of K (blockIdx.z = 0) or V: 256 threads hold
-// the block in registers (NCH chunks of 8 elements each), so the rows are read once.
-template <typename T, int NCH>
+// One block of kKv8Block slab tokens of one KV head, of K (blockIdx.z = 0) or V.  The block stays in
+// registers between its amax and its codes (NP 16-byte pieces a thread, all requested at once), so
+// the rows are read once: 3 bytes moved for each bf16 element, bound by HBM.
+template <typename T, int NP>
 __global__ void __launch_bounds__(256) kv8_fill_kernel(const T* __restrict__ k, const T* __restrict__ v, int32_t L_p,
                                                        uint8_t* __restrict__ kpool, uint8_t* __restrict__ vpool,
                                                        int64_t first_slot, int32_t n_kv, int32_t d, int64_t row) {
+  constexpr int E = Piece<T>::kElems;
   __shared__ float s_max[8];
   const int32_t j = blockIdx.y;
   const T* src = blockIdx.z ? v : k;
   uint8_t* pool = blockIdx.z ? vpool : kpool;
   const int32_t t0 = blockIdx.x * kKv8Block;
   const int32_t n = min(kKv8Block, L_p - t0);
-  const int32_t per_row = d / 8;  // chunks of a head's row
-  float x[NCH][8];
-  float amax = 0.f;
+  const int32_t per_row = d / E;  // pieces of a head's row
+  Piece<T> x[NP];
 #pragma unroll
-  for (int c = 0; c < NCH; ++c) {
+  for (int c = 0; c < NP; ++c) {
     const int32_t idx = threadIdx.x + c * 256;
     const int32_t t = idx / per_row;
-    if (t < n) load8(src + ((int64_t)(t0 + t) * n_kv + j) * d + idx % per_row * 8, x[c]);
-    else
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[c][i] = 0.f;
+    x[c].w = t < n ? __ldcs(reinterpret_cast<const uint4*>(src + ((int64_t)(t0 + t) * n_kv + j) * d + idx % per_row * E))
+                   : make_uint4(0u, 0u, 0u, 0u);
   }
+  float amax = 0.f;
 #pragma unroll
-  for (int c = 0; c < NCH; ++c)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, finite_abs(x[c][i]));
+  for (int c = 0; c < NP; ++c) amax = fmaxf(amax, x[c].amax());
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = amax;
@@ -65,13 +79,10 @@ __global__ void __launch_bounds__(256) kv8_fill_kernel(const T* __restrict__ k, 
   const float inv = kv8_inverse(amax), scale = kv8_scale(amax);
   uint8_t* dst = pool + (first_slot + t0) * row;
 #pragma unroll
-  for (int c = 0; c < NCH; ++c) {
+  for (int c = 0; c < NP; ++c) {
     const int32_t idx = threadIdx.x + c * 256;
     const int32_t t = idx / per_row;
-    if (t >= n) continue;
-    const uint32_t lo = f32x4_to_e4m3x4(x[c][0] * inv, x[c][1] * inv, x[c][2] * inv, x[c][3] * inv);
-    const uint32_t hi = f32x4_to_e4m3x4(x[c][4] * inv, x[c][5] * inv, x[c][6] * inv, x[c][7] * inv);
-    *reinterpret_cast<uint2*>(dst + (int64_t)t * row + (int64_t)j * d + idx % per_row * 8) = make_uint2(lo, hi);
+    if (t < n) x[c].store(dst + (int64_t)t * row + (int64_t)j * d + idx % per_row * E, inv);
   }
   for (int32_t t = threadIdx.x; t < n; t += 256)
     *reinterpret_cast<float*>(dst + (int64_t)t * row + (int64_t)n_kv * d + 4 * j) = scale;
@@ -261,32 +272,33 @@ __device__ __forceinline__ void kv8_generic_run(const AttnParams& p, int32_t j, 
   }
 }
 
+// CTAs [0, n_prefix) take prefix items first_item.., the rest (suffix item, KV head, block of kRows of
+// its query heads): one launch, so that short prefixes and suffixes share the SMs.
 template <typename T, int VPL>
-__global__ void __launch_bounds__(256) kv8_prefix_generic_kernel(AttnParams p, int32_t first_item) {
-  const DevPrefixItem it = p.pitems[first_item + blockIdx.x];
-  const DevGroup gr = p.groups[it.group];
-  if (gr.slab_off < 0 || gr.slab_off + gr.L_p > p.n_hot) {
-    if (threadIdx.x == 0) latch(p.err, kDevBadSlab);
+__global__ void __launch_bounds__(256) kv8_generic_kernel(AttnParams p, int32_t first_item, int32_t n_prefix) {
+  if ((int32_t)blockIdx.x < n_prefix) {
+    const DevPrefixItem it = p.pitems[first_item + blockIdx.x];
+    const DevGroup gr = p.groups[it.group];
+    if (gr.slab_off < 0 || gr.slab_off + gr.L_p > p.n_hot) {
+      if (threadIdx.x == 0) latch(p.err, kDevBadSlab);
+      return;
+    }
+    int32_t t0, t1;
+    piece_range(gr, it.split, t0, t1);
+    const int32_t r0 = it.row_block * gr.rows_per_cta;
+    const int n_rows = min(gr.n_req * p.g - r0, kRows);
+    auto req = [&](int r) { return p.group_req[gr.req_begin + (r0 + r) / p.g]; };
+    kv8_generic_run<T, VPL>(
+        p, it.kv_head, t0, t1, n_rows, [&](int32_t t) { return (int32_t)(gr.slab_off + t); },
+        [&](int r) { return (int64_t)req(r) * p.n_q + it.kv_head * p.g + (r0 + r) % p.g; },
+        [&](int r) { return p.reqs[req(r)].rec_base + it.split; });
     return;
   }
-  int32_t t0, t1;
-  piece_range(gr, it.split, t0, t1);
-  const int32_t r0 = it.row_block * gr.rows_per_cta;
-  const int n_rows = min(gr.n_req * p.g - r0, kRows);
-  auto req = [&](int r) { return p.group_req[gr.req_begin + (r0 + r) / p.g]; };
-  kv8_generic_run<T, VPL>(
-      p, it.kv_head, t0, t1, n_rows, [&](int32_t t) { return (int32_t)(gr.slab_off + t); },
-      [&](int r) { return (int64_t)req(r) * p.n_q + it.kv_head * p.g + (r0 + r) % p.g; },
-      [&](int r) { return p.reqs[req(r)].rec_base + it.split; });
-}
-
-// blockIdx.y: KV head and block of kRows of its query heads.
-template <typename T, int VPL>
-__global__ void __launch_bounds__(256) kv8_suffix_generic_kernel(AttnParams p) {
-  DevSuffixItem it = p.sitems[blockIdx.x];
+  const int blocks = (p.g + kRows - 1) / kRows, per = p.n_kv * blocks;
+  const int32_t w = blockIdx.x - n_prefix;
+  DevSuffixItem it = p.sitems[w / per];
   if (p.live_len) it.t1 = max(it.t0, min(it.t1, p.live_len[it.b]));
-  const int blocks = (p.g + kRows - 1) / kRows;
-  const int32_t j = blockIdx.y / blocks, h0 = j * p.g + blockIdx.y % blocks * kRows;
+  const int32_t j = w % per / blocks, h0 = j * p.g + w % blocks * kRows;
   const int n_rows = min(kRows, (j + 1) * p.g - h0);
   kv8_generic_run<T, VPL>(
       p, j, it.t0, it.t1, n_rows,
@@ -320,9 +332,8 @@ cudaError_t fill_t(const T* k, const T* v, int32_t L_p, uint8_t* kpool, uint8_t*
                    int32_t n_kv, int32_t d, cudaStream_t s) {
   const dim3 grid((L_p + kKv8Block - 1) / kKv8Block, n_kv, 2);
   return with_vpl(d, [&](auto vpl) {
-    constexpr int nch = decltype(vpl)::value;  // kKv8Block * d / 8 chunks over 256 threads
-    static_assert(kKv8Block * 32 / 8 == 256, "chunks per thread");
-    kv8_fill_kernel<T, nch><<<grid, 256, 0, s>>>(k, v, L_p, kpool, vpool, first_slot, n_kv, d, kv8_row_bytes(n_kv, d));
+    constexpr int np = kKv8Block * 32 * decltype(vpl)::value / Piece<T>::kElems / 256;  // pieces a thread
+    kv8_fill_kernel<T, np><<<grid, 256, 0, s>>>(k, v, L_p, kpool, vpool, first_slot, n_kv, d, kv8_row_bytes(n_kv, d));
     return cudaGetLastError();
   });
 }
@@ -366,30 +377,18 @@ cudaError_t launch_kv8_append_newest(int32_t dtype, const AttnParams& p, cudaStr
   });
 }
 
-cudaError_t launch_kv8_prefix_generic(int32_t dtype, const AttnParams& p, int32_t first_item, int32_t n_items,
-                                      cudaStream_t s) {
-  if (n_items <= 0) return cudaSuccess;
+cudaError_t launch_kv8_generic(int32_t dtype, const AttnParams& p, int32_t first_item, int32_t n_items, bool suffix,
+                               cudaStream_t s) {
+  const int64_t ctas = n_items + (suffix ? (int64_t)p.n_sitems * p.n_kv * ((p.g + kRows - 1) / kRows) : 0);
+  if (ctas <= 0) return cudaSuccess;
+  if (ctas > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
   const int smem = generic_smem(p.d);
   return with_vpl(p.d, [&](auto vpl) {
     constexpr int n = decltype(vpl)::value;
-    auto kernel = dtype == 1 ? kv8_prefix_generic_kernel<__nv_bfloat16, n> : kv8_prefix_generic_kernel<float, n>;
+    auto kernel = dtype == 1 ? kv8_generic_kernel<__nv_bfloat16, n> : kv8_generic_kernel<float, n>;
     cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<n_items, 256, smem, s>>>(p, first_item);
-    return cudaGetLastError();
-  });
-}
-
-cudaError_t launch_kv8_suffix_generic(int32_t dtype, const AttnParams& p, cudaStream_t s) {
-  if (p.n_sitems <= 0) return cudaSuccess;
-  const int smem = generic_smem(p.d);
-  const dim3 grid(p.n_sitems, p.n_kv * ((p.g + kRows - 1) / kRows));
-  return with_vpl(p.d, [&](auto vpl) {
-    constexpr int n = decltype(vpl)::value;
-    auto kernel = dtype == 1 ? kv8_suffix_generic_kernel<__nv_bfloat16, n> : kv8_suffix_generic_kernel<float, n>;
-    cudaError_t e = allow_smem(kernel, smem);
-    if (e != cudaSuccess) return e;
-    kernel<<<grid, 256, smem, s>>>(p);
+    kernel<<<(unsigned)ctas, 256, smem, s>>>(p, first_item, n_items);
     return cudaGetLastError();
   });
 }

@@ -48,7 +48,8 @@ cudaError_t launch_kv8_step(const AttnParams& p, int32_t first_dense, int32_t n_
   const int32_t groups = (p.n_kv + k8s::kWarps - 1) / k8s::kWarps;
   const int64_t n = (int64_t)n_dense + (int64_t)n_scta * groups;
   if (n <= 0) return cudaSuccess;
-  cudaError_t e = allow_smem(kv8_step_kernel, kSmem);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem_once(kv8_step_kernel, kSmem, allowed);
   if (e != cudaSuccess) return e;
   return launch_kernel(kv8_step_kernel, dim3((unsigned)n), dim3(k8d::kThreads), kSmem, s, pdl, p, first_dense, n_dense,
                        tmk, tmv, cta_begin, n_scta, n_tail);
@@ -56,7 +57,8 @@ cudaError_t launch_kv8_step(const AttnParams& p, int32_t first_dense, int32_t n_
 
 cudaError_t launch_kv8_suffix(const AttnParams& p, const int32_t* cta_begin, int32_t n_scta, cudaStream_t s, bool pdl) {
   if (n_scta <= 0) return cudaSuccess;
-  cudaError_t e = allow_smem(kv8_suffix_kernel, k8s::kSmemBytes);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem_once(kv8_suffix_kernel, k8s::kSmemBytes, allowed);
   if (e != cudaSuccess) return e;
   const dim3 grid(n_scta, (p.n_kv + k8s::kWarps - 1) / k8s::kWarps);
   return launch_kernel(kv8_suffix_kernel, grid, dim3(k8s::kThreads), k8s::kSmemBytes, s, pdl, p, cta_begin);

@@ -217,12 +217,27 @@ def test_evict_weights(cuda_ok, kind):
     _evict_case(rng, lens, out, first, 5, 2504, KINDS[kind](rng))
 
 
-@pytest.mark.parametrize("n", [1, 1000, 1024, 4096, 5000, 20000, 70001])
+@pytest.mark.parametrize("n", [1, 1000, 1024, 2049, 4096, 5000, 16385, 20000, 70001, 131073])
 @pytest.mark.parametrize("share", [0.0, 0.001, 0.5, 1.0])
 def test_evict_lengths(cuda_ok, n, share):
     rng = np.random.default_rng(n)
     out = [max(1 if share else 0, int(n * share)), 0, 1]
     _evict_case(rng, [n, n, n], out, None, 0, n + 5, KINDS["softmax"](rng))
+
+
+@pytest.mark.parametrize("kind", ["equal", "odd", "few"])
+@pytest.mark.parametrize("n", [5000, 40000, 100000, 140000])
+def test_evict_ties_across_slices(cuda_ok, kind, n):
+    """Long rows of few different weights: the ties that leave are the lowest places of the whole row."""
+    rng = np.random.default_rng([n, len(kind)])
+    _evict_case(rng, [n, n - 77, 3], [n // 3, n - 200, 2], [5, 0, 0], 0, n, KINDS[kind](rng))
+
+
+def test_evict_many_middling_rows(cuda_ok):
+    """Enough rows of a few thousand tokens that a thread holds eight of them."""
+    rng = np.random.default_rng(12)
+    lens = [int(x) for x in rng.integers(1500, 5000, 200)]
+    _evict_case(rng, lens, [n // 4 for n in lens], [4] * 200, 32, 5000, KINDS["softmax"](rng))
 
 
 def test_evict_many_rows(cuda_ok):
