@@ -198,22 +198,20 @@ def _check(status: int, where: str):
 
 
 def _ptr(x) -> Optional[int]:
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    if hasattr(x, "data_ptr"):
-        return int(x.data_ptr())
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        if x is None or isinstance(x, int):
+            return x
     raise TypeError(f"expected a device address or a tensor, got {type(x)}")
 
 
 def _stream(s) -> Optional[int]:
-    if s is None:
-        return None
-    if isinstance(s, int):
-        return s or None
-    if hasattr(s, "cuda_stream"):
-        return int(s.cuda_stream) or None
+    try:
+        return s.cuda_stream or None
+    except AttributeError:
+        if s is None or isinstance(s, int):
+            return s or None
     raise TypeError(f"expected a stream handle, got {type(s)}")
 
 

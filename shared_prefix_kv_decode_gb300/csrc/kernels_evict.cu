@@ -120,10 +120,11 @@ __global__ void __launch_bounds__(256) weigh_generic_kernel(WeighParams p, const
 
 // bf16 q, head_dim 64 or 128: one unit is 16 tokens of one KV head, on warp-level tensor cores,
 //     S^T[16 tok x 8 heads] = K[16 tok x d] . Q^T[d x 8]     (d / 16 mma.m16n8k16 for each 8 query heads)
-// A warp takes its tokens' rows straight from global memory into the A operand: the sum over d may
-// be taken in any order, so the lanes of a row take 16-byte pieces of it (whole sectors), and Q^T is
-// loaded in the same order.  K is read once, no shared memory or barrier stands between HBM and the
-// MMAs, and each warp requests its next unit's rows before it computes the present one.
+// The sum over d may be taken in any order, so the lanes of a row take 16-byte pieces of it (whole
+// sectors) that serve as the A operand as they are, and Q^T is loaded in the same order.  Every lane
+// copies its own pieces into shared memory some units ahead (cp.async) and reads them back when their
+// turn comes: K is read once, no lane waits for another, and the bytes in flight are not bound by
+// registers.
 // Of a 16-bit row lane c = lane % 4 holds dims 32 i + 8 c + 0..7 of load i; k-step 2 i + u takes its dims
 // 4 u + {0, 1} and 4 u + {2, 3}.  Of a packed 8-bit row it holds dims 64 i + 16 c + 0..15; k-step
 // 4 i + u takes dims 4 u + {0, 1} and 4 u + {2, 3}, converted to fp16 (exact); the row's scale
@@ -136,16 +137,23 @@ __global__ void __launch_bounds__(256) weigh_generic_kernel(WeighParams p, const
 constexpr int kChunkMin = 64, kChunkMax = 256;
 constexpr int kMaxSums = 40 * 1024; // shared memory for the units' sums
 
+// Two units in shared memory a warp, and as many warps as registers allow: packed rows (224K tokens)
+// 50.8 us with four CTAs an SM, 52.9 with three and three units, 58.9 with two and four; 16-bit rows (30K
+// tokens) 15.3 us with three CTAs.  With the units ahead in registers instead, 58.8 and 15.2 us at best.
 template <bool KV8, int D>
-struct KRows {
-  static constexpr int kLoads = KV8 ? D / 64 : D / 32;
-  uint4 a[kLoads], b[kLoads];  // rows lane / 4 and lane / 4 + 8
-  float sa, sb;                // their scales
+struct WeighUnit {
+  static constexpr int kPieces = KV8 ? D / 64 : D / 32;            // 16-byte pieces of a row a lane
+  static constexpr int kBytes = 2 * kPieces * 512 + (KV8 ? 256 : 0);  // rows lane / 4 and lane / 4 + 8, and their scales
+  static constexpr int kDepth = 2;
+  static constexpr int kRing = 8 * kDepth * kBytes;
+  static constexpr int kBlocks = KV8 ? 4 : 3;
 };
 
 template <bool KV8, int D, int N>
-__global__ void __launch_bounds__(256, 2) weigh_mma_kernel(WeighParams p, const __grid_constant__ WeighRows<N> rows) {
-  extern __shared__ float s_sum[];  // [n_kv][rows.tokens]
+__global__ void __launch_bounds__(256, WeighUnit<KV8, D>::kBlocks) weigh_mma_kernel(WeighParams p, const __grid_constant__ WeighRows<N> rows) {
+  using Unit = WeighUnit<KV8, D>;
+  extern __shared__ __align__(16) unsigned char s_ring[];  // [8 warps][kDepth] units, then the sums
+  float* s_sum = reinterpret_cast<float*>(s_ring + Unit::kRing);  // [n_kv][rows.tokens]
   __shared__ int32_t s_slot[kChunkMax];
   const int kChunk = rows.tokens;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -166,26 +174,25 @@ __global__ void __launch_bounds__(256, 2) weigh_mma_kernel(WeighParams p, const 
     s_slot[tid] = slot;
   }
   const int n_units = (n + 15) / 16 * p.n_kv;
-  using Rows = KRows<KV8, D>;
-  // the row of a slot (or, for a slot that does not count, zeros)
-  auto load_row = [&](int32_t slot, int32_t j, uint4 (&x)[Rows::kLoads], float& scale) {
-    scale = 1.f;
-    if (slot < 0) {
+  const uint32_t ring = smem_u32(s_ring) + warp * (Unit::kDepth * Unit::kBytes);
+  // this lane's pieces of the rows of unit u into stage st (zeros for a slot that does not count)
+  auto load_unit = [&](int u, int st) {
+    if (u < n_units) {
+      const int32_t j = u % p.n_kv, tile = u / p.n_kv * 16;
 #pragma unroll
-      for (int i = 0; i < Rows::kLoads; ++i) x[i] = make_uint4(0u, 0u, 0u, 0u);
-      return;
+      for (int h = 0; h < 2; ++h) {
+        const int32_t slot = s_slot[tile + r + 8 * h];
+        const uint8_t* row = (const uint8_t*)p.kpool + (slot < 0 ? 0 : (int64_t)slot * (KV8 ? p.kv8_row : (int64_t)p.n_kv * D * 2));
+        const uint4* src = reinterpret_cast<const uint4*>(row + (int64_t)j * (KV8 ? D : 2 * D)) + c;
+        const uint32_t dst = ring + st * Unit::kBytes + (h * Unit::kPieces * 32 + lane) * 16;
+#pragma unroll
+        for (int i = 0; i < Unit::kPieces; ++i) cp_async16(dst + i * 512, src + 4 * i, slot < 0 ? 0 : 16);
+        if constexpr (KV8)
+          cp_async4(ring + st * Unit::kBytes + 2 * Unit::kPieces * 512 + (h * 32 + lane) * 4,
+                    row + (int64_t)p.n_kv * D + 4 * j, slot < 0 ? 0 : 4);
+      }
     }
-    const uint8_t* row = (const uint8_t*)p.kpool + (int64_t)slot * (KV8 ? p.kv8_row : (int64_t)p.n_kv * D * 2);
-    const uint4* src = reinterpret_cast<const uint4*>(row + (int64_t)j * (KV8 ? D : 2 * D)) + c;
-#pragma unroll
-    for (int i = 0; i < Rows::kLoads; ++i) x[i] = __ldg(src + 4 * i);
-    if constexpr (KV8) scale = __ldg(reinterpret_cast<const float*>(row + (int64_t)p.n_kv * D) + j);
-  };
-  auto load_unit = [&](int u, Rows& k) {
-    if (u >= n_units) return;
-    const int32_t j = u % p.n_kv, tile = u / p.n_kv * 16;
-    load_row(s_slot[tile + r], j, k.a, k.sa);
-    load_row(s_slot[tile + r + 8], j, k.b, k.sb);
+    cp_async_commit();
   };
   constexpr int kSteps = D / 16;
   uint32_t qf[kSteps][2];
@@ -225,32 +232,43 @@ __global__ void __launch_bounds__(256, 2) weigh_mma_kernel(WeighParams p, const 
     e0 = __shfl_sync(0xffffffffu, minus, 8 * c);
     e1 = __shfl_sync(0xffffffffu, minus, 8 * c + 4);
   };
-  auto unit = [&](int u, const Rows& k) {
+  auto unit = [&](int u, int st) {
     const int32_t j = u % p.n_kv, tile = u / p.n_kv * 16;
+    const unsigned char* mine = s_ring + warp * (Unit::kDepth * Unit::kBytes) + st * Unit::kBytes;
+    const uint4* ka = reinterpret_cast<const uint4*>(mine) + lane;
+    float sa = 1.f, sb = 1.f;
+    if constexpr (KV8) {
+      const float* sc = reinterpret_cast<const float*>(mine + 2 * Unit::kPieces * 512);
+      sa = sc[lane];
+      sb = sc[32 + lane];
+    }
     float w0 = 0.f, w1 = 0.f;
     for (int32_t h0 = j * p.g; h0 < (j + 1) * p.g; h0 += 8) {
       if (have != h0) load_q(h0, (j + 1) * p.g);
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};  // two accumulation chains
 #pragma unroll
-      for (int i = 0; i < Rows::kLoads; ++i) {
-        const uint32_t a[4] = {k.a[i].x, k.a[i].y, k.a[i].z, k.a[i].w}, z[4] = {k.b[i].x, k.b[i].y, k.b[i].z, k.b[i].w};
+      for (int i = 0; i < Unit::kPieces; ++i) {
+        const uint4 x = ka[32 * i], y = ka[32 * (Unit::kPieces + i)];
+        const uint32_t a[4] = {x.x, x.y, x.z, x.w}, z[4] = {y.x, y.y, y.z, y.w};
         if constexpr (KV8) {
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             uint32_t a0, a2, b0, b2;
             e4m3x4_to_f16x4(a[w], a0, a2);
             e4m3x4_to_f16x4(z[w], b0, b2);
-            mma_f16_16816(s, a0, b0, a2, b2, qf[4 * i + w][0], qf[4 * i + w][1]);
+            mma_f16_16816(w & 1 ? s2 : s, a0, b0, a2, b2, qf[4 * i + w][0], qf[4 * i + w][1]);
           }
         } else {
 #pragma unroll
           for (int w = 0; w < 2; ++w)
-            mma_bf16_16816(s, a[2 * w], z[2 * w], a[2 * w + 1], z[2 * w + 1], qf[2 * i + w][0], qf[2 * i + w][1]);
+            mma_bf16_16816(w & 1 ? s2 : s, a[2 * w], z[2 * w], a[2 * w + 1], z[2 * w + 1], qf[2 * i + w][0], qf[2 * i + w][1]);
         }
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] += s2[e];
       // a head without weight (lse -inf, or past the group) adds 2^-inf = 0, whatever its score
-      w0 += (e0 == -INFINITY ? 0.f : exp2f(s[0] * (c0 * k.sa) + e0)) + (e1 == -INFINITY ? 0.f : exp2f(s[1] * (c1 * k.sa) + e1));
-      w1 += (e0 == -INFINITY ? 0.f : exp2f(s[2] * (c0 * k.sb) + e0)) + (e1 == -INFINITY ? 0.f : exp2f(s[3] * (c1 * k.sb) + e1));
+      w0 += (e0 == -INFINITY ? 0.f : exp2f(s[0] * (c0 * sa) + e0)) + (e1 == -INFINITY ? 0.f : exp2f(s[1] * (c1 * sa) + e1));
+      w1 += (e0 == -INFINITY ? 0.f : exp2f(s[2] * (c0 * sb) + e0)) + (e1 == -INFINITY ? 0.f : exp2f(s[3] * (c1 * sb) + e1));
     }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
@@ -265,31 +283,14 @@ __global__ void __launch_bounds__(256, 2) weigh_mma_kernel(WeighParams p, const 
   // q of the warp's first units' heads is on its way with the slots
   if (warp < n_units) load_q(warp % p.n_kv * p.g, (warp % p.n_kv + 1) * p.g);
   __syncthreads();
-  // rows are requested one unit ahead (16-bit rows: 32 registers a unit) or two (packed rows: 16)
-  if constexpr (KV8) {
-    Rows k0, k1, k2;
-    load_unit(warp, k0);
-    load_unit(warp + 8, k1);
-    for (int u = warp; u < n_units; u += 24) {
-      load_unit(u + 16, k2);
-      unit(u, k0);
-      if (u + 8 >= n_units) break;
-      load_unit(u + 24, k0);
-      unit(u + 8, k1);
-      if (u + 16 >= n_units) break;
-      load_unit(u + 32, k1);
-      unit(u + 16, k2);
-    }
-  } else {
-    Rows k0, k1;
-    load_unit(warp, k0);
-    for (int u = warp; u < n_units; u += 16) {
-      load_unit(u + 8, k1);
-      unit(u, k0);
-      if (u + 8 >= n_units) break;
-      load_unit(u + 16, k0);
-      unit(u + 8, k1);
-    }
+#pragma unroll
+  for (int i = 0; i < Unit::kDepth - 1; ++i) load_unit(warp + 8 * i, i);
+  int st = 0;
+  for (int u = warp; u < n_units; u += 8) {
+    load_unit(u + 8 * (Unit::kDepth - 1), (st + Unit::kDepth - 1) % Unit::kDepth);
+    cp_async_wait<Unit::kDepth - 1>();
+    unit(u, st);
+    st = (st + 1) % Unit::kDepth;
   }
   __syncthreads();
   if (tid < n) {
@@ -624,14 +625,21 @@ bool weigh_on_mma(const WeighParams& p) {
          (int)sizeof(float) * p.n_kv * kChunkMax <= kMaxSums;
 }
 
+template <bool KV8, int D, int N>
+cudaError_t weigh_mma(const WeighParams& p, const WeighRows<N>& rows, int32_t chunks, cudaStream_t s) {
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem_once(weigh_mma_kernel<KV8, D, N>, WeighUnit<KV8, D>::kRing + kMaxSums, allowed);
+  if (e != cudaSuccess) return e;
+  const int smem = WeighUnit<KV8, D>::kRing + (int)sizeof(float) * p.n_kv * rows.tokens;
+  weigh_mma_kernel<KV8, D, N><<<chunks, 256, smem, s>>>(p, rows);
+  return cudaGetLastError();
+}
+
 template <typename T, bool KV8, int N>
 cudaError_t weigh_launch(const WeighParams& p, const WeighRows<N>& rows, int32_t chunks, cudaStream_t s) {
   if constexpr (std::is_same_v<T, __nv_bfloat16>) {
     if (weigh_on_mma<T>(p)) {
-      const int smem = (int)sizeof(float) * p.n_kv * rows.tokens;
-      if (p.d == 128) weigh_mma_kernel<KV8, 128, N><<<chunks, 256, smem, s>>>(p, rows);
-      else weigh_mma_kernel<KV8, 64, N><<<chunks, 256, smem, s>>>(p, rows);
-      return cudaGetLastError();
+      return p.d == 128 ? weigh_mma<KV8, 128, N>(p, rows, chunks, s) : weigh_mma<KV8, 64, N>(p, rows, chunks, s);
     }
   }
   const int smem = (int)sizeof(float) * (kTok * (p.d + 1) + 8 * kTok);

@@ -44,19 +44,22 @@ struct Piece<float> {
   }
 };
 
-// One block of kKv8Block slab tokens of one KV head, of K (blockIdx.z = 0) or V.  The block stays in
+// One block of kKv8Block slab tokens of one KV head (the heads of a block are neighbours in the grid, so
+// that its rows are read and written whole at about the same time), of K (blockIdx.y = 0) or V.  The block stays in
 // registers between its amax and its codes (NP 16-byte pieces a thread, all requested at once), so
-// the rows are read once: 3 bytes moved for each bf16 element, bound by HBM.
+// the rows are read once: 3 bytes moved for each bf16 element, bound by HBM and by how many CTAs an SM
+// holds in the meantime (16K tokens of 8 x 128: 25.2 us with five CTAs an SM, 23.1 with six; the
+// floor is 14.9).
 template <typename T, int NP>
-__global__ void __launch_bounds__(256) kv8_fill_kernel(const T* __restrict__ k, const T* __restrict__ v, int32_t L_p,
+__global__ void __launch_bounds__(256, NP <= 4 ? 6 : 1) kv8_fill_kernel(const T* __restrict__ k, const T* __restrict__ v, int32_t L_p,
                                                        uint8_t* __restrict__ kpool, uint8_t* __restrict__ vpool,
                                                        int64_t first_slot, int32_t n_kv, int32_t d, int64_t row) {
   constexpr int E = Piece<T>::kElems;
   __shared__ float s_max[8];
-  const int32_t j = blockIdx.y;
-  const T* src = blockIdx.z ? v : k;
-  uint8_t* pool = blockIdx.z ? vpool : kpool;
-  const int32_t t0 = blockIdx.x * kKv8Block;
+  const int32_t j = blockIdx.x % n_kv;
+  const T* src = blockIdx.y ? v : k;
+  uint8_t* pool = blockIdx.y ? vpool : kpool;
+  const int32_t t0 = blockIdx.x / n_kv * kKv8Block;
   const int32_t n = min(kKv8Block, L_p - t0);
   const int32_t per_row = d / E;  // pieces of a head's row
   Piece<T> x[NP];
@@ -158,8 +161,9 @@ __global__ void __launch_bounds__(256) kv8_append_newest_kernel(AttnParams p) {
 
 // ---- decode attention on CUDA cores -----------------------------------------------------------
 // A CTA takes up to kGenericRows query rows of one KV head and a run of tokens.  Tiles of 32
-// tokens are dequantised into shared memory once for all rows; a warp holds two rows, its lanes
-// are the tile's tokens for the scores and head_dim's columns for the weighted sum.
+// tokens are dequantised into shared memory once for all rows (a thread holds the next tile's codes
+// and scales while it computes this one); a warp holds two rows, its lanes are the tile's tokens for
+// the scores and head_dim's columns for the weighted sum.  Small problems: bound by latency.
 constexpr int kTok = kGenericTile, kRows = kGenericRows;
 
 __host__ __device__ inline int generic_smem(int d) {
@@ -171,11 +175,11 @@ template <typename T, int VPL, typename SlotOf, typename RowOf, typename RecOf>
 __device__ __forceinline__ void kv8_generic_run(const AttnParams& p, int32_t j, int32_t t0, int32_t t1, int n_rows,
                                                 SlotOf slot_of, RowOf row_of, RecOf rec_of) {
   constexpr int d = VPL * 32;
-  extern __shared__ float sm[];
-  float* sK = sm;                    // [kTok][d + 1]
-  float* sV = sK + kTok * (d + 1);   // [kTok][d]
+  extern __shared__ __align__(16) float sm[];
+  float* sV = sm;                    // [kTok][d]
   float* sQ = sV + kTok * d;         // [kRows][d]
-  __shared__ int32_t s_slot[kTok];
+  float* sK = sQ + kRows * d;        // [kTok][d + 1]
+  __shared__ __align__(16) float s_w[8][2][kTok];  // the warps' weights
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < n_rows * d; i += blockDim.x)
     sQ[i] = (float)((const T*)p.q)[row_of(i / d) * d + i % d] * p.scale_log2;
@@ -185,47 +189,54 @@ __device__ __forceinline__ void kv8_generic_run(const AttnParams& p, int32_t j, 
   for (int r = 0; r < 2; ++r)
 #pragma unroll
     for (int i = 0; i < VPL; ++i) acc[r][i] = 0.f;
-  for (int32_t t = t0; t < t1; t += kTok) {
-    __syncthreads();  // the tile before is read
-    if (threadIdx.x < kTok) s_slot[threadIdx.x] = t + threadIdx.x < t1 ? slot_of(t + threadIdx.x) : -1;
-    __syncthreads();
-    for (int i = threadIdx.x; i < kTok * (d / 4); i += blockDim.x) {
-      const int tok = i / (d / 4), c = i % (d / 4) * 4;
-      const int32_t slot = s_slot[tok];
-      float kx[4] = {0.f, 0.f, 0.f, 0.f}, vx[4] = {0.f, 0.f, 0.f, 0.f};
+  // this thread's share of a tile: VPL words of four codes, word i of token (thread + 256 i) / (d / 4)
+  uint32_t kw[VPL], vw[VPL];
+  float ks[VPL], vs[VPL];
+  auto load = [&](int32_t t) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int w = threadIdx.x + 256 * i, tok = w / (d / 4), c = w % (d / 4) * 4;
+      const int32_t slot = t + tok < t1 ? slot_of(t + tok) : -1;
+      kw[i] = vw[i] = 0u;
+      ks[i] = vs[i] = 0.f;
       if (slot >= 0) {
         const uint8_t* kr = (const uint8_t*)p.kpool + (int64_t)slot * p.kv8_row;
         const uint8_t* vr = (const uint8_t*)p.vpool + (int64_t)slot * p.kv8_row;
-        const uint32_t kw = *reinterpret_cast<const uint32_t*>(kr + (int64_t)j * d + c);
-        const uint32_t vw = *reinterpret_cast<const uint32_t*>(vr + (int64_t)j * d + c);
-        const float ks = *reinterpret_cast<const float*>(kr + (int64_t)p.n_kv * d + 4 * j);
-        const float vs = *reinterpret_cast<const float*>(vr + (int64_t)p.n_kv * d + 4 * j);
-        e4m3x4_to_f32x4(kw, kx);
-        e4m3x4_to_f32x4(vw, vx);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          kx[u] *= ks;
-          vx[u] *= vs;
-        }
+        kw[i] = *reinterpret_cast<const uint32_t*>(kr + (int64_t)j * d + c);
+        vw[i] = *reinterpret_cast<const uint32_t*>(vr + (int64_t)j * d + c);
+        ks[i] = *reinterpret_cast<const float*>(kr + (int64_t)p.n_kv * d + 4 * j);
+        vs[i] = *reinterpret_cast<const float*>(vr + (int64_t)p.n_kv * d + 4 * j);
       }
+    }
+  };
+  load(t0);
+  for (int32_t t = t0; t < t1; t += kTok) {
+    __syncthreads();  // the tile before is read
 #pragma unroll
-      for (int u = 0; u < 4; ++u) sK[tok * (d + 1) + c + u] = kx[u];
-      *reinterpret_cast<float4*>(sV + tok * d + c) = make_float4(vx[0], vx[1], vx[2], vx[3]);
+    for (int i = 0; i < VPL; ++i) {
+      const int w = threadIdx.x + 256 * i, tok = w / (d / 4), c = w % (d / 4) * 4;
+      float kx[4], vx[4];
+      e4m3x4_to_f32x4(kw[i], kx);
+      e4m3x4_to_f32x4(vw[i], vx);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) sK[tok * (d + 1) + c + u] = kx[u] * ks[i];
+      *reinterpret_cast<float4*>(sV + tok * d + c) = make_float4(vx[0] * vs[i], vx[1] * vs[i], vx[2] * vs[i], vx[3] * vs[i]);
     }
     __syncthreads();
+    if (t + kTok < t1) load(t + kTok);
     if (r0 >= n_rows) continue;
-    const bool live = s_slot[lane] >= 0;
+    const bool live = t + lane < t1 && slot_of(t + lane) >= 0;
     const float* q0 = sQ + r0 * d;
     const float* q1 = r0 + 1 < n_rows ? q0 + d : q0;
     float s[2] = {0.f, 0.f};
     const float* kr = sK + lane * (d + 1);
-#pragma unroll 8
-    for (int i = 0; i < d; ++i) {
-      const float kv = kr[i];
-      s[0] += q0[i] * kv;
-      s[1] += q1[i] * kv;
+#pragma unroll 4
+    for (int i = 0; i < d; i += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(q0 + i), b = *reinterpret_cast<const float4*>(q1 + i);
+      const float k0 = kr[i], k1 = kr[i + 1], k2 = kr[i + 2], k3 = kr[i + 3];
+      s[0] += a.x * k0 + a.y * k1 + a.z * k2 + a.w * k3;
+      s[1] += b.x * k0 + b.y * k1 + b.z * k2 + b.w * k3;
     }
-    float w[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       if (!live) s[r] = -INFINITY;
@@ -235,8 +246,9 @@ __device__ __forceinline__ void kv8_generic_run(const AttnParams& p, int32_t j, 
       const float mn = fmaxf(m[r], mx);
       const float base = mn == -INFINITY ? 0.f : mn;
       const float a = exp2f(m[r] - base);
-      w[r] = exp2f(s[r] - base);
-      float sum = w[r];
+      const float w = exp2f(s[r] - base);
+      s_w[warp][r][lane] = w;
+      float sum = w;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       l[r] = l[r] * a + sum;
@@ -244,16 +256,21 @@ __device__ __forceinline__ void kv8_generic_run(const AttnParams& p, int32_t j, 
 #pragma unroll
       for (int i = 0; i < VPL; ++i) acc[r][i] *= a;
     }
-    const int n_tok = min(kTok, t1 - t);
-    for (int tok = 0; tok < n_tok; ++tok) {
-      const float w0 = __shfl_sync(0xffffffffu, w[0], tok), w1 = __shfl_sync(0xffffffffu, w[1], tok);
+    __syncwarp();
+    const int n_tok = min(kTok, t1 - t);  // V rows past them hold zeros
+    for (int tok = 0; tok < n_tok; tok += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(&s_w[warp][0][tok]), b = *reinterpret_cast<const float4*>(&s_w[warp][1][tok]);
+      const float wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const float v = sV[tok * d + lane + 32 * i];
-        acc[0][i] += w0 * v;
-        acc[1][i] += w1 * v;
-      }
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          const float v = sV[(tok + u) * d + lane + 32 * i];
+          acc[0][i] += wa[u] * v;
+          acc[1][i] += wb[u] * v;
+        }
     }
+    __syncwarp();  // the weights are read
   }
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
@@ -330,7 +347,9 @@ cudaError_t with_vpl(int32_t d, F f) {
 template <typename T>
 cudaError_t fill_t(const T* k, const T* v, int32_t L_p, uint8_t* kpool, uint8_t* vpool, int64_t first_slot,
                    int32_t n_kv, int32_t d, cudaStream_t s) {
-  const dim3 grid((L_p + kKv8Block - 1) / kKv8Block, n_kv, 2);
+  const int64_t ctas = (int64_t)((L_p + kKv8Block - 1) / kKv8Block) * n_kv;
+  if (ctas > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)ctas, 2);
   return with_vpl(d, [&](auto vpl) {
     constexpr int np = kKv8Block * 32 * decltype(vpl)::value / Piece<T>::kElems / 256;  // pieces a thread
     kv8_fill_kernel<T, np><<<grid, 256, 0, s>>>(k, v, L_p, kpool, vpool, first_slot, n_kv, d, kv8_row_bytes(n_kv, d));
