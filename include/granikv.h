@@ -141,6 +141,8 @@ granikv_status granikv_destroy(granikv_ctx* ctx);
  * tokens: 64 consecutive tokens of a slab, counted from its start (the last block may be
  * shorter), whose rows all hold the block's scale, or one COLD token (page size 1).
  * Those rows and q and o must start on 16-byte boundaries (GRANIKV_ERR_INVALID).
+ * A NaN or an infinity in a head's q, or a NaN in the K that a request attends, makes that head's o
+ * and lse of that request NaN; a NaN in V reaches its own columns of o only.
  * granikv_dispatch, granikv_decode_attention (and its append and static forms),
  * granikv_cold_weigh and the pool calls work on such a context as on any other;
  * granikv_prefill_attention is GRANIKV_ERR_UNSUPPORTED (a prefix is prefilled in 16 bits and its

@@ -888,7 +888,7 @@ granikv_status granikv_cold_weigh(granikv_ctx* c, int32_t layer, const void* q, 
   a.keep = keep;
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c->cfg.head_dim));
   a.err = c->d_err;
-  c->n_kernels += 1;
+  c->n_kernels += (bt->B + kRowsPerLaunch - 1) / kRowsPerLaunch;
   return cuda_status(launch_cold_weigh(c->cfg.dtype, a, bt->seq_len, (cudaStream_t)stream));
 }
 
@@ -919,7 +919,7 @@ granikv_status granikv_cold_evict(granikv_ctx* c, const int32_t* seq_len, const 
   DeviceGuard dg(c->cfg.device);
   cudaError_t e = launch_cold_evict(rows.data(), B, keep_last, req_to_slot, suffix_len, weight, cap, slots_out,
                                     (cudaStream_t)stream);
-  c->n_kernels += 1;
+  c->n_kernels += (B + kRowsPerLaunch - 1) / kRowsPerLaunch;
   return cuda_status(e);
 }
 
@@ -941,7 +941,7 @@ granikv_status granikv_plan_destroy(granikv_plan* p) {
   return GRANIKV_OK;
 }
 
-granikv_status granikv_dispatch(granikv_ctx* c, const granikv_batch* bt, granikv_plan* p) {
+static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, granikv_plan* p) {
   if (!c || !bt || !p || p->ctx != c) return GRANIKV_ERR_INVALID;
   const int32_t B = bt->B;
   if (B <= 0 || B > c->cfg.max_batch || !bt->slab_id || !bt->seq_len || bt->cap < 0)
@@ -1561,6 +1561,16 @@ granikv_status granikv_dispatch(granikv_ctx* c, const granikv_batch* bt, granikv
   p->version++;
   p->valid = true;
   return GRANIKV_OK;
+}
+
+granikv_status granikv_dispatch(granikv_ctx* c, const granikv_batch* bt, granikv_plan* p) {
+  try {
+    return dispatch_impl(c, bt, p);
+  } catch (const std::bad_alloc&) {  // the plan is left invalid, and nothing half made serves the next dispatch
+    p->scratch.groups_cached = p->scratch.pitems_cached = false;
+    p->scratch.tail_key.clear();
+    return GRANIKV_ERR_INVALID;
+  }
 }
 
 granikv_status granikv_plan_num_groups(const granikv_plan* p, int32_t* n) {

@@ -145,6 +145,9 @@ __host__ __device__ inline int64_t kv8_row_bytes(int32_t n_kv, int32_t d) {
   return ((int64_t)n_kv * (d + 4) + 15) / 16 * 16;
 }
 
+// Rows whose counts fit the parameters of one weighing or eviction launch (16 KB of 32).
+constexpr int kRowsPerLaunch = 1024;
+
 // Tokens and weights of one row for the eviction kernel, passed by value.
 struct EvictRow {
   int32_t len, n_evict, first, out;  // tokens; how many leave; first position that may; first place in slots_out

@@ -666,7 +666,7 @@ cudaError_t weigh_rows(const WeighParams& p, const int32_t* seq_len, int32_t b0,
 
 template <typename T, bool KV8>
 cudaError_t weigh_all(const WeighParams& p, const int32_t* seq_len, cudaStream_t s) {
-  constexpr int kSmall = 64, kLarge = 1024;
+  constexpr int kSmall = 64, kLarge = kRowsPerLaunch;
   int tokens = kTok;
   if (weigh_on_mma<T>(p)) {
     int64_t total = 0;
@@ -696,7 +696,7 @@ cudaError_t launch_cold_evict(const EvictRow* rows, int32_t B, int32_t keep_last
                               int32_t* suffix_len, float* weight, int32_t cap, int32_t* slots_out, cudaStream_t s) {
   // the rows' counts travel as a kernel parameter: nothing is staged in memory that two calls (or
   // a captured and an eager one) could share
-  constexpr int kSmall = 64, kLarge = 1024;
+  constexpr int kSmall = 64, kLarge = kRowsPerLaunch;
   cudaError_t e = cudaSuccess;
   for (int32_t b = 0; b < B && e == cudaSuccess;) {
     const int32_t n = B - b < kLarge ? B - b : kLarge;

@@ -406,12 +406,14 @@ __global__ void __launch_bounds__(256, kBlocks) merge_bf16_d128_kernel(AttnParam
     m = M;
   }
   if (!have) return;
-  const float inv = den > 0.f ? 1.f / den : 0.f;
+  // (over the 8-bit cache a row with a NaN among its weights, whose record says +inf, becomes NaN)
+  const bool weight = den > 0.f || (p.kv8_row && den != den);
+  const float inv = weight ? 1.f / den : 0.f;
   __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
   __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
   reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + row * 128)[lane] =
       make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
-  if (lane == 0) p.lse[row] = den > 0.f ? m + logf(den) : -INFINITY;
+  if (lane == 0) p.lse[row] = weight ? m + logf(den) : -INFINITY;
 }
 
 template <int W>

@@ -285,7 +285,7 @@ __device__ __forceinline__ void kv8_generic_run(const AttnParams& p, int32_t j, 
     float* dst = p.rec_o + ((int64_t)rec * p.n_q + h) * d;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) dst[lane + 32 * i] = acc[r][i] * inv;
-    if (lane == 0) p.rec_lse[(int64_t)rec * p.n_q + h] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2;
+    if (lane == 0) p.rec_lse[(int64_t)rec * p.n_q + h] = kv8_record_lse(l[r], (m[r] + log2f(l[r])) * kLn2);
   }
 }
 

@@ -399,8 +399,8 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
     }
     if (lane < 4) {
       float* ldst = p.rec_lse + (int64_t)rec * p.n_q + hq0;
-      if (w0) st_record(ldst, l0 == 0.f ? -INFINITY : (m0 - kShift + log2f(l0)) * kLn2, keep);
-      if (w1) st_record(ldst + 1, l1 == 0.f ? -INFINITY : (m1 - kShift + log2f(l1)) * kLn2, keep);
+      if (w0) st_record(ldst, kv8_record_lse(l0, (m0 - kShift + log2f(l0)) * kLn2), keep);
+      if (w1) st_record(ldst + 1, kv8_record_lse(l1, (m1 - kShift + log2f(l1)) * kLn2), keep);
     }
   }
 }

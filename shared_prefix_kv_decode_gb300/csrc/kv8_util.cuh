@@ -76,6 +76,12 @@ __device__ __forceinline__ void q_to_f16(uint32_t* w, float& unit) {
   for (int i = 0; i < W; ++i) w[i] = bf16x2_to_f16x2(w[i], f);
 }
 
+// A partial row's log-sum-exp as the merge takes it: -inf for a row without weight, +inf for one whose
+// weights hold a NaN (the merge's maximum passes over a NaN; +inf makes the whole row NaN).
+__device__ __forceinline__ float kv8_record_lse(float sum, float lse) {
+  return sum == 0.f ? -INFINITY : sum == sum ? lse : INFINITY;
+}
+
 // |x| for a block's amax: infinities and NaN do not count.
 __device__ __forceinline__ float finite_abs(float x) {
   const float a = fabsf(x);

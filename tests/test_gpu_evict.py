@@ -153,6 +153,36 @@ def test_weigh_empty_head_and_bad_slot(cuda_ok, kv8):
     assert torch.equal(ref[1, keep], w[1, keep])
 
 
+@pytest.mark.parametrize("kv8", [False, True])
+def test_weigh_more_rows_than_one_launch(cuda_ok, kv8):
+    torch, rng = _torch(), np.random.default_rng(6)
+    lens = [int(x) for x in rng.integers(0, 6, 1030)]
+    lens[1023], lens[1024], lens[1029] = 70, 65, 3
+    c = Cold(rng, n_q=8, n_kv=2, d=128, dtype="bf16", lens=lens, kv8=kv8)
+    w = torch.rand(len(lens), c.cap, device="cuda")
+    start = w.clone()
+    kernels, _ = c.ctx.launch_count()
+    c.ctx.cold_weigh(0, c.q, c.lse, c.batch, w, 0.5)
+    c.ctx.sync_status()
+    assert c.ctx.launch_count()[0] == kernels + 2
+    c.check(w, start, 0.5)
+
+
+def test_weigh_bad_query_stays_with_its_row(cuda_ok):
+    """A NaN in one request's q makes its tokens' weights NaN (the last to leave) and changes no other row."""
+    torch, rng = _torch(), np.random.default_rng(7)
+    for kv8 in (False, True):
+        c = Cold(rng, n_q=32, n_kv=8, d=128, dtype="bf16", lens=[100, 40, 70], kv8=kv8)
+        w = torch.zeros(3, c.cap, device="cuda")
+        c.ctx.cold_weigh(0, c.q, c.lse, c.batch, w, 1.0)
+        bad = torch.zeros(3, c.cap, device="cuda")
+        c.q[1, 9, 3] = float("nan")
+        c.ctx.cold_weigh(0, c.q, c.lse, c.batch, bad, 1.0)
+        c.ctx.sync_status()
+        assert torch.isnan(bad[1, :40]).all() and not torch.isnan(bad[1, 40:]).any()
+        assert torch.equal(bad[[0, 2]], w[[0, 2]])
+
+
 def test_weights_of_a_step_sum_to_the_heads(cuda_ok):
     """Weighed with decode's own lse and no prefix, a request's tokens share the n_q heads' weight of 1."""
     torch, gb, rng = _torch(), _gb(), np.random.default_rng(5)

@@ -483,6 +483,91 @@ def test_backends_agree(cuda_ok):
         c.check(*c.decode(), f"backend {backend}")
 
 
+SCHEDULES = {"serial": lambda x: x.set_concurrency(False), "half": lambda x: x.set_concurrency(True, 0.5),
+             "all": lambda x: x.set_concurrency(True, 1.0), "ahead": lambda x: x.set_dense_l2_ahead(4),
+             "unfused": lambda x: x.set_fused_merge(False), "fused": lambda x: x.set_fused_merge(True),
+             "mixed": lambda x: x.set_msat(30), "cascade": lambda x: x.set_msat(10000)}
+
+
+@pytest.mark.parametrize("how", sorted(SCHEDULES))
+def test_decode_schedules(cuda_ok, how):
+    """Every knob of the schedule leaves the result within the same tolerance; `mixed` runs one group
+    on the tensor cores and one on CUDA cores."""
+    rng = np.random.default_rng(22)
+    c = Kv8(rng, n_q=32, n_kv=8, d=128, dtype="bf16", prefixes=[1500, 700], of=[0, 1, 0, 0, -1, 0, 0, 0, 0, 0], lens=[300, 20, 0, 1, 90, 64, 700, 33, 5, 16])
+    SCHEDULES[how](c.ctx)
+    c.check(*c.decode(), how)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("backend", ["dense", "cascade"])
+def test_decode_bad_query_stays_with_its_head(cuda_ok, bad, backend):
+    """A NaN or infinity in one head's q makes that head's row NaN and changes no other."""
+    torch, gb, rng = _torch(), _gb(), np.random.default_rng(23)
+    c = Kv8(rng, n_q=32, n_kv=8, d=128, dtype="bf16", prefixes=[300], of=[0, 0, -1], lens=[20, 0, 70],
+            backend=gb.BACKEND_DENSE if backend == "dense" else gb.BACKEND_CASCADE)
+    o, lse = c.decode()
+    for b, h in ((0, 5), (1, 31), (2, 0)):
+        c.q[b, h, 77] = bad
+    o2, lse2 = c.decode()
+    hit = torch.zeros_like(lse, dtype=torch.bool)
+    hit[0, 5] = hit[1, 31] = hit[2, 0] = True
+    assert torch.equal(torch.isnan(o2).any(dim=2), hit) and torch.isnan(o2[hit]).all() and torch.equal(torch.isnan(lse2), hit)
+    assert torch.equal(o2[~hit], o[~hit]) and torch.equal(lse2[~hit], lse[~hit])
+
+
+@pytest.mark.parametrize("shape", [(32, 8, 128, "bf16"), (8, 2, 64, "f32")])
+@pytest.mark.parametrize("where", ["prefix", "cold"])
+def test_decode_nan_key_reaches_its_readers(cuda_ok, shape, where):
+    """A NaN in one head of one token's K makes that head NaN for the requests that attend the token."""
+    torch = _torch()
+    n_q, n_kv, d, dtype = shape
+
+    def case(edit):
+        return Kv8(np.random.default_rng(26), n_q=n_q, n_kv=n_kv, d=d, dtype=dtype, prefixes=[300], of=[0, -1, 0], lens=[20, 40, 0], edit=edit)
+
+    def edit(kind, k, v):
+        if kind == where and k.shape[0] in (300, 40):
+            k[17, 1, 9] = np.nan
+
+    (o, lse), (o2, lse2) = (case(e).decode() for e in (None, edit))
+    g = n_q // n_kv
+    hit = torch.zeros_like(lse, dtype=torch.bool)
+    hit[[0, 2] if where == "prefix" else [1], g:2 * g] = True
+    assert torch.equal(torch.isnan(lse2), hit) and torch.isnan(o2[hit]).all()
+    assert torch.equal(o2[~hit], o[~hit]) and torch.equal(lse2[~hit], lse[~hit])
+
+
+def test_decode_on_two_streams_at_once(cuda_ok):
+    """One plan, two workspaces, two streams: the results of the calls one after the other."""
+    torch, rng = _torch(), np.random.default_rng(24)
+    c = Kv8(rng, n_q=32, n_kv=8, d=128, dtype="bf16", prefixes=[2000], of=[0] * 8 + [-1], lens=[int(x) for x in rng.integers(0, 400, 8)] + [40])
+    o, lse = c.decode()
+    plan = c.ctx.dispatch(c.batch)
+    n = c.ctx.workspace_size(plan)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [(torch.empty_like(o), torch.empty_like(lse), torch.empty(n, dtype=torch.uint8, device="cuda")) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, (a, b, ws) in zip(streams, outs):
+            c.ctx.decode_attention(0, c.q, c.batch, plan, a, b, ws, n, s)
+    torch.cuda.synchronize()
+    c.ctx.sync_status()
+    for a, b, _ in outs:
+        assert torch.equal(a, o) and torch.equal(b, lse)
+
+
+def test_decode_the_same_slot_twice(cuda_ok):
+    """A slot named twice in a row, and by two rows, counts once for each place."""
+    rng = np.random.default_rng(25)
+    c = Kv8(rng, n_q=32, n_kv=8, d=128, dtype="bf16", prefixes=[90], of=[0, -1, 0], lens=[40, 35, 7])
+    c.table[0, 3], c.table[0, 39], c.table[2, 6] = c.table[0, 4], c.table[0, 4], c.table[1, 20]
+    for x in (c.ck, c.cv):
+        x[0][3] = x[0][39] = x[0][4]
+        x[2][6] = x[1][20]
+    c.check(*c.decode(), "twice")
+
+
 def test_cache_in_8_bits_with_prefix_lifecycle(cuda_ok):
     """GraniKVCache(kv8=True): admission to HOT, fallback to COLD shared by two requests, appends,
     decode with the newest token written by the call."""

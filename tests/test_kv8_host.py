@@ -103,6 +103,60 @@ def test_kv8_dispatch_plans(granikv_lib):
         assert ctx.workspace_size(plan) > 0
 
 
+def _plan_case(rng):
+    n_prefix = int(rng.choice([1, 1, 2, 5, 20]))
+    B = int(rng.choice([1, 2, 7, 40, 200, 1000]))
+    prefixes = [int(np.exp(rng.uniform(0, 11))) for _ in range(n_prefix)]
+    top = np.exp(rng.uniform(0, 9))
+    lens = [int(rng.uniform(0, 40000)) if rng.random() < 0.1 else int(rng.uniform(0, top)) for _ in range(B)]
+    n_q, n_kv = [(8, 8), (32, 8), (40, 8), (64, 8), (16, 4), (8, 1), (6, 2), (24, 12), (32, 16)][int(rng.integers(9))]
+    return prefixes, lens, n_q, n_kv
+
+
+PLANS = [_plan_case(np.random.default_rng(s)) for s in range(120)] + [
+    ([16384], [300] * 8, 32, 8), ([8192], [250], 32, 8), ([16384], [1] * 64, 32, 8), ([100000], [300000, 1], 32, 8),
+    ([100], [200000, 3, 5, 7], 32, 8), ([16384], [100] * 4000, 32, 8), ([500], [0, 1, 2, 3] * 1000, 32, 8)]
+
+
+@pytest.mark.parametrize("group", range(0, len(PLANS), 10))
+@pytest.mark.parametrize("schedule", [(True, 0.0), (True, 0.5), (False, 0.0)])
+def test_plans_cover_every_token_once(granikv_lib, group, schedule):
+    """Head_dim 128: each request's suffix items tile its COLD tokens in order, every item is in one run,
+    a run's tokens fit the kernel's staging (4096), and every group's pieces are there once."""
+    for prefixes, lens, n_q, n_kv in PLANS[group:group + 10]:
+        B = len(lens)
+        ctx = gb.Context(n_layers=1, n_q=n_q, n_kv=n_kv, head_dim=128, dtype=gb.DTYPE_BF16, n_slots=4_000_000, hot_fraction=0.5,
+                         max_batch=B, host_only=True, kv8=True)
+        ctx.set_concurrency(*schedule)
+        slabs = [ctx.hot_alloc(L)[0] for L in prefixes]
+        plan = ctx.dispatch(gb.Batch([slabs[b % len(slabs)] for b in range(B)], lens, 4096, max(lens) + 1))
+        img, groups, sched, runs = plan.image(), plan.groups(), plan.schedule(), plan.suffix_runs()
+        up = lambda x: (x + 15) // 16 * 16
+        at = up(64 * len(groups))
+        at = up(at + 4 * B)
+        reqs = np.frombuffer(img, np.int32, 4 * B, at).reshape(B, 4)
+        at = up(at + 16 * B)
+        n_items = sum(g["n_splits"] * n_kv * -(-g["m_eff"] // 128) for g in groups)
+        assert sched["prefix_ctas"] == n_items
+        items = np.frombuffer(img, np.int32, 4 * n_items, at).reshape(n_items, 4)
+        assert len({tuple(x) for x in items}) == n_items
+        at = up(at + 16 * n_items)
+        n_seg = int((reqs[:, 2] - reqs[:, 1]).sum())
+        seg = np.frombuffer(img, np.int32, 4 * n_seg, at).reshape(n_seg, 4)
+        begin = np.frombuffer(img, np.int32, runs["runs"] + 1, up(at + 16 * n_seg))
+        assert begin[0] == 0 and begin[-1] == n_seg and (np.diff(begin) >= 0).all()
+        spans = {}
+        for b, t0, t1, _ in seg:
+            spans.setdefault(int(b), []).append((int(t0), int(t1)))
+        for b, n in enumerate(lens):
+            edges = spans.get(b, [])
+            assert [e[0] for e in edges] == [0][:len(edges)] + [e[1] for e in edges[:-1]]
+            assert (edges[-1][1] if edges else 0) == n and all(t1 > t0 for t0, t1 in edges)
+        tokens = np.concatenate([[0], np.cumsum(seg[:, 2] - seg[:, 1])])
+        assert (tokens[begin[1:]] - tokens[begin[:-1]]).max(initial=0) <= 4096
+        assert runs["tail_runs"] <= n_items and runs["tail_runs"] <= runs["runs"]
+
+
 @pytest.mark.parametrize("kv8", [False, True])
 def test_weigh_refusals(granikv_lib, kv8):
     ctx = _ctx(kv8=kv8)
