@@ -1871,7 +1871,7 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
     // CUDA-core prefix and suffix items in one launch, then the merge
     e = launch_kv8_generic(c->cfg.dtype, a, p->pitem_first[kImplKv8Generic], p->n_pitems, p->n_sitems > 0, s);
     c->n_kernels += 1;
-    if (e == cudaSuccess) e = launch_merge_k(false);
+    if (e == cudaSuccess) e = launch_merge_k(true);
     return cuda_status(e);
   }
   const bool one_launch = p->concurrent && p->n_pitems > 0 && n_dense + n_casc == p->n_pitems &&

@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(256) merge_kernel(AttnParams p) {
   const int32_t b = (int32_t)(row / p.n_q);
   const int32_t h = (int32_t)(row % p.n_q);
   const DevReq r = p.reqs[b];
+  grid_dep_wait();  // the records are complete once the kernel before this one is
   const float* lse_rec = p.rec_lse + (int64_t)r.rec_base * p.n_q + h;
   float M = -INFINITY;
   for (int32_t i = lane; i < r.n_parts; i += 32) M = fmaxf(M, lse_rec[(int64_t)i * p.n_q]);
@@ -439,31 +440,29 @@ cudaError_t launch_merge_w(const AttnParams& p, cudaStream_t s, bool pdl) {
 }
 
 template <typename T, int VPL>
-cudaError_t launch_merge_vpl(const AttnParams& p, cudaStream_t s) {
+cudaError_t launch_merge_vpl(const AttnParams& p, cudaStream_t s, bool pdl) {
   const int64_t rows = (int64_t)p.B * p.n_q;
-  const int grid = (int)((rows + 7) / 8);
-  merge_kernel<T, VPL><<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_kernel(merge_kernel<T, VPL>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, pdl, p);
 }
 
 template <typename T>
-cudaError_t launch_merge_t(const AttnParams& p, cudaStream_t s) {
+cudaError_t launch_merge_t(const AttnParams& p, cudaStream_t s, bool pdl) {
   switch (p.d / 32) {
-    case 1: return launch_merge_vpl<T, 1>(p, s);
-    case 2: return launch_merge_vpl<T, 2>(p, s);
-    case 3: return launch_merge_vpl<T, 3>(p, s);
-    case 4: return launch_merge_vpl<T, 4>(p, s);
-    case 5: return launch_merge_vpl<T, 5>(p, s);
-    case 6: return launch_merge_vpl<T, 6>(p, s);
-    case 7: return launch_merge_vpl<T, 7>(p, s);
-    case 8: return launch_merge_vpl<T, 8>(p, s);
+    case 1: return launch_merge_vpl<T, 1>(p, s, pdl);
+    case 2: return launch_merge_vpl<T, 2>(p, s, pdl);
+    case 3: return launch_merge_vpl<T, 3>(p, s, pdl);
+    case 4: return launch_merge_vpl<T, 4>(p, s, pdl);
+    case 5: return launch_merge_vpl<T, 5>(p, s, pdl);
+    case 6: return launch_merge_vpl<T, 6>(p, s, pdl);
+    case 7: return launch_merge_vpl<T, 7>(p, s, pdl);
+    case 8: return launch_merge_vpl<T, 8>(p, s, pdl);
     default: return cudaErrorInvalidValue;
   }
 }
 
 cudaError_t launch_merge(int32_t dtype, const AttnParams& p, cudaStream_t s, bool pdl) {
   if (dtype == 1 && p.d == 128) return launch_merge_w<1>(p, s, pdl);
-  return dtype == 1 ? launch_merge_t<__nv_bfloat16>(p, s) : launch_merge_t<float>(p, s);
+  return dtype == 1 ? launch_merge_t<__nv_bfloat16>(p, s, pdl) : launch_merge_t<float>(p, s, pdl);
 }
 
 cudaError_t launch_merge_rows(const AttnParams& p, int32_t warps_per_row, cudaStream_t s, bool pdl) {

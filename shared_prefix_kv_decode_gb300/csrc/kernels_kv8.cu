@@ -3,6 +3,7 @@
 // 256) and either type of q.
 #include "kv8_util.cuh"
 #include "launch_util.cuh"
+#include "tc_util.cuh"
 
 #include <cmath>
 
@@ -160,139 +161,229 @@ __global__ void __launch_bounds__(256) kv8_append_newest_kernel(AttnParams p) {
 }
 
 // ---- decode attention on CUDA cores -----------------------------------------------------------
-// A CTA takes up to kGenericRows query rows of one KV head and a run of tokens.  Tiles of 32
-// tokens are dequantised into shared memory once for all rows (a thread holds the next tile's codes
-// and scales while it computes this one); a warp holds two rows, its lanes are the tile's tokens for
-// the scores and head_dim's columns for the weighted sum.  Small problems: bound by latency.
-constexpr int kTok = kGenericTile, kRows = kGenericRows;
+// A CTA takes up to kGenericRows query rows of one KV head and a run of tokens.  Tiles of 64
+// tokens are unpacked into shared memory once for all rows (a thread holds the next tile's codes
+// and scales while it computes this one).  Warps w and w + 4 hold the same four rows, each over its half
+// of a tile: the lanes are the half's tokens for the scores and head_dim's columns for the weighted
+// sum, and the two join at the end.  A token's scales multiply its score and its weight.
+// Bound by the latency of small problems and by reads of shared memory: four rows a warp use what it
+// reads of K and V four times, and products go two to an instruction where a lane's columns pair up
+// (head_dim a multiple of 64).  fp32, 1,500-token prefix, 48 requests of 8/2 heads of 64 with up to 80 COLD
+// tokens: 22.4 us with two rows a warp and 32-token tiles, 19.9 so, with the merge, at three CTAs an SM.
+constexpr int kRows = kGenericRows;
+constexpr int kTok = 64, kHalfTok = 32;
+constexpr int kWarpRows = 4;
+static_assert(kRows == 4 * kWarpRows && kTok % kGenericTile == 0, "eight warps: four row groups, two halves of a tile");
 
+// floats: V [kTok][d], q [kRows][d], K [kTok][d + 4], weights [8][kTok / 2][kWarpRows], scales [2][kTok]
 __host__ __device__ inline int generic_smem(int d) {
-  return (int)sizeof(float) * (kTok * (d + 1) + kTok * d + kRows * d);
+  return (int)sizeof(float) * (kTok * (d + 4) + kTok * d + kRows * d + 8 * kHalfTok * kWarpRows + 2 * kTok);
 }
 
 // slot_of(t): the token's slot, or -1 for one that does not count.
-template <typename T, int VPL, typename SlotOf, typename RowOf, typename RecOf>
+template <typename T, int VPL, typename SlotOf, typename ReqOf, typename HeadOf, typename RecOf>
 __device__ __forceinline__ void kv8_generic_run(const AttnParams& p, int32_t j, int32_t t0, int32_t t1, int n_rows,
-                                                SlotOf slot_of, RowOf row_of, RecOf rec_of) {
+                                                SlotOf slot_of, ReqOf req_of, HeadOf head_of, RecOf rec_of) {
   constexpr int d = VPL * 32;
+  constexpr int kPer = VPL % 2 ? 1 : 2;  // neighbouring columns a lane takes
+  constexpr int kCols = VPL / kPer;      // column of (i, e): (lane + 32 i) * kPer + e
   extern __shared__ __align__(16) float sm[];
-  float* sV = sm;                    // [kTok][d]
-  float* sQ = sV + kTok * d;         // [kRows][d]
-  float* sK = sQ + kRows * d;        // [kTok][d + 1]
-  __shared__ __align__(16) float s_w[8][2][kTok];  // the warps' weights
+  float* sV = sm;                 // codes
+  float* sQ = sV + kTok * d;
+  float* sK = sQ + kRows * d;     // codes: 16-byte reads of eight tokens cover all banks
+  float4* sW = reinterpret_cast<float4*>(sK + kTok * (d + 4));
+  float* sScale = reinterpret_cast<float*>(sW + 8 * kHalfTok);  // of K (0: the token does not count), of V
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < n_rows * d; i += blockDim.x)
-    sQ[i] = (float)((const T*)p.q)[row_of(i / d) * d + i % d] * p.scale_log2;
-  const int r0 = warp * 2;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, acc[2][VPL];
+  const int r0 = (warp & 3) * kWarpRows, half = warp >> 2;
+  float4* w_mine = sW + warp * kHalfTok;  // weights times the V scale of this warp's four rows, by token
+  for (int i = threadIdx.x; i < kRows * d; i += blockDim.x)
+    sQ[i] = i < n_rows * d ? (float)((const T*)p.q)[((int64_t)req_of(i / d) * p.n_q + head_of(i / d)) * d + i % d] * p.scale_log2 : 0.f;
+  int32_t rec[kWarpRows];  // looked up now, so that the loads finish during the tiles
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
+  for (int r = 0; r < kWarpRows; ++r) rec[r] = half == 0 && r0 + r < n_rows ? rec_of(r0 + r) : -1;
+  float m[kWarpRows], l[kWarpRows], acc[kWarpRows][VPL];
+#pragma unroll
+  for (int r = 0; r < kWarpRows; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) acc[r][i] = 0.f;
-  // this thread's share of a tile: VPL words of four codes, word i of token (thread + 256 i) / (d / 4)
-  uint32_t kw[VPL], vw[VPL];
+  }
+  // this thread's share of a tile: VPL pieces of eight codes, piece i of token (thread + 256 i) / (d / 8)
+  uint2 kw[VPL], vw[VPL];
   float ks[VPL], vs[VPL];
   auto load = [&](int32_t t) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int w = threadIdx.x + 256 * i, tok = w / (d / 4), c = w % (d / 4) * 4;
+      const int w = threadIdx.x + 256 * i, tok = w / (d / 8), c = w % (d / 8) * 8;
       const int32_t slot = t + tok < t1 ? slot_of(t + tok) : -1;
-      kw[i] = vw[i] = 0u;
+      kw[i] = vw[i] = make_uint2(0u, 0u);
       ks[i] = vs[i] = 0.f;
       if (slot >= 0) {
         const uint8_t* kr = (const uint8_t*)p.kpool + (int64_t)slot * p.kv8_row;
         const uint8_t* vr = (const uint8_t*)p.vpool + (int64_t)slot * p.kv8_row;
-        kw[i] = *reinterpret_cast<const uint32_t*>(kr + (int64_t)j * d + c);
-        vw[i] = *reinterpret_cast<const uint32_t*>(vr + (int64_t)j * d + c);
-        ks[i] = *reinterpret_cast<const float*>(kr + (int64_t)p.n_kv * d + 4 * j);
-        vs[i] = *reinterpret_cast<const float*>(vr + (int64_t)p.n_kv * d + 4 * j);
+        kw[i] = *reinterpret_cast<const uint2*>(kr + (int64_t)j * d + c);
+        vw[i] = *reinterpret_cast<const uint2*>(vr + (int64_t)j * d + c);
+        if (c == 0) {
+          ks[i] = *reinterpret_cast<const float*>(kr + (int64_t)p.n_kv * d + 4 * j);
+          vs[i] = *reinterpret_cast<const float*>(vr + (int64_t)p.n_kv * d + 4 * j);
+        }
       }
     }
+  };
+  auto unpack = [](float* dst, uint2 w) {
+    float x[4];
+    e4m3x4_to_f32x4(w.x, x);
+    *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+    e4m3x4_to_f32x4(w.y, x);
+    *reinterpret_cast<float4*>(dst + 4) = make_float4(x[0], x[1], x[2], x[3]);
   };
   load(t0);
   for (int32_t t = t0; t < t1; t += kTok) {
     __syncthreads();  // the tile before is read
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int w = threadIdx.x + 256 * i, tok = w / (d / 4), c = w % (d / 4) * 4;
-      float kx[4], vx[4];
-      e4m3x4_to_f32x4(kw[i], kx);
-      e4m3x4_to_f32x4(vw[i], vx);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) sK[tok * (d + 1) + c + u] = kx[u] * ks[i];
-      *reinterpret_cast<float4*>(sV + tok * d + c) = make_float4(vx[0] * vs[i], vx[1] * vs[i], vx[2] * vs[i], vx[3] * vs[i]);
+      const int w = threadIdx.x + 256 * i, tok = w / (d / 8), c = w % (d / 8) * 8;
+      unpack(sK + tok * (d + 4) + c, kw[i]);
+      unpack(sV + tok * d + c, vw[i]);
+      if (c == 0) {
+        sScale[tok] = ks[i];
+        sScale[kTok + tok] = vs[i];
+      }
     }
     __syncthreads();
     if (t + kTok < t1) load(t + kTok);
-    if (r0 >= n_rows) continue;
-    const bool live = t + lane < t1 && slot_of(t + lane) >= 0;
-    const float* q0 = sQ + r0 * d;
-    const float* q1 = r0 + 1 < n_rows ? q0 + d : q0;
-    float s[2] = {0.f, 0.f};
-    const float* kr = sK + lane * (d + 1);
+    const int first = half * kHalfTok;  // of the warp's tokens in the tile
+    const int n_tok = min(kHalfTok, t1 - t - first);
+    if (r0 >= n_rows || n_tok <= 0) continue;
+    const float k_scale = sScale[first + lane], v_scale = sScale[kTok + first + lane];
+    const ulonglong2* q = reinterpret_cast<const ulonglong2*>(sQ + r0 * d);
+    const ulonglong2* kr = reinterpret_cast<const ulonglong2*>(sK + (first + lane) * (d + 4));
+    uint64_t s2[kWarpRows][2];  // two partial sums each
+#pragma unroll
+    for (int r = 0; r < kWarpRows; ++r) s2[r][0] = s2[r][1] = 0ull;  // 0.0f bit patterns
 #pragma unroll 4
-    for (int i = 0; i < d; i += 4) {
-      const float4 a = *reinterpret_cast<const float4*>(q0 + i), b = *reinterpret_cast<const float4*>(q1 + i);
-      const float k0 = kr[i], k1 = kr[i + 1], k2 = kr[i + 2], k3 = kr[i + 3];
-      s[0] += a.x * k0 + a.y * k1 + a.z * k2 + a.w * k3;
-      s[1] += b.x * k0 + b.y * k1 + b.z * k2 + b.w * k3;
+    for (int i = 0; i < d / 4; ++i) {
+      const ulonglong2 k = kr[i];
+#pragma unroll
+      for (int r = 0; r < kWarpRows; ++r) {
+        const ulonglong2 a = q[r * (d / 4) + i];
+        s2[r][0] = f2_fma(a.x, k.x, s2[r][0]);
+        s2[r][1] = f2_fma(a.y, k.y, s2[r][1]);
+      }
+    }
+    float s[kWarpRows], mx[kWarpRows], w[kWarpRows], sum[kWarpRows];
+#pragma unroll
+    for (int r = 0; r < kWarpRows; ++r) {
+      float x, y;
+      f2_unpack(f2_add(s2[r][0], s2[r][1]), x, y);
+      mx[r] = s[r] = k_scale != 0.f ? (x + y) * k_scale : -INFINITY;  // (a written row's scale is above 0)
     }
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      if (!live) s[r] = -INFINITY;
-      float mx = s[r];
+    for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float mn = fmaxf(m[r], mx);
+      for (int r = 0; r < kWarpRows; ++r) mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], o));
+#pragma unroll
+    for (int r = 0; r < kWarpRows; ++r) {
+      const float mn = fmaxf(m[r], mx[r]);
       const float base = mn == -INFINITY ? 0.f : mn;
       const float a = exp2f(m[r] - base);
-      const float w = exp2f(s[r] - base);
-      s_w[warp][r][lane] = w;
-      float sum = w;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      l[r] = l[r] * a + sum;
+      sum[r] = w[r] = exp2f(s[r] - base);
+      l[r] *= a;
       m[r] = mn;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) acc[r][i] *= a;
     }
-    __syncwarp();
-    const int n_tok = min(kTok, t1 - t);  // V rows past them hold zeros
-    for (int tok = 0; tok < n_tok; tok += 4) {
-      const float4 a = *reinterpret_cast<const float4*>(&s_w[warp][0][tok]), b = *reinterpret_cast<const float4*>(&s_w[warp][1][tok]);
-      const float wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+    w_mine[lane] = make_float4(w[0] * v_scale, w[1] * v_scale, w[2] * v_scale, w[3] * v_scale);
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int r = 0; r < kWarpRows; ++r) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], o);
+#pragma unroll
+    for (int r = 0; r < kWarpRows; ++r) l[r] += sum[r];
+    __syncwarp();
+    const float* v_mine = sV + first * d;
+    if constexpr (kPer == 2) {
+      uint64_t o2[kWarpRows][kCols];
+#pragma unroll
+      for (int r = 0; r < kWarpRows; ++r)
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) o2[r][i] = f2_pack(acc[r][2 * i], acc[r][2 * i + 1]);
+#pragma unroll 4
+      for (int tok = 0; tok < n_tok; ++tok) {
+        const float4 x = w_mine[tok];
+        const uint64_t x2[kWarpRows] = {f2_pack(x.x, x.x), f2_pack(x.y, x.y), f2_pack(x.z, x.z), f2_pack(x.w, x.w)};
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) {
+          const uint64_t v = *reinterpret_cast<const uint64_t*>(v_mine + tok * d + (lane + 32 * i) * 2);
+#pragma unroll
+          for (int r = 0; r < kWarpRows; ++r) o2[r][i] = f2_fma(x2[r], v, o2[r][i]);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < kWarpRows; ++r)
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) f2_unpack(o2[r][i], acc[r][2 * i], acc[r][2 * i + 1]);
+    } else {
+#pragma unroll 4
+      for (int tok = 0; tok < n_tok; ++tok) {
+        const float4 x = w_mine[tok];
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-          const float v = sV[(tok + u) * d + lane + 32 * i];
-          acc[0][i] += wa[u] * v;
-          acc[1][i] += wb[u] * v;
+          const float v = v_mine[tok * d + lane + 32 * i];
+          acc[0][i] += x.x * v;
+          acc[1][i] += x.y * v;
+          acc[2][i] += x.z * v;
+          acc[3][i] += x.w * v;
         }
+      }
     }
     __syncwarp();  // the weights are read
   }
+  // the second halves' states go to shared memory (K and V are read), the first join them
+  __syncthreads();
+  float* other = sV + (warp & 3) * (kWarpRows * (d + 2));  // [kWarpRows][d], then the maxima and sums
+  if (half == 1 && r0 < n_rows) {
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < kWarpRows; ++r) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) other[r * d + i * 32 + lane] = acc[r][i];
+      if (lane == 0) {
+        other[kWarpRows * d + r] = m[r];
+        other[kWarpRows * (d + 1) + r] = l[r];
+      }
+    }
+  }
+  __syncthreads();
+  if (half == 1) return;
+#pragma unroll
+  for (int r = 0; r < kWarpRows; ++r) {
     if (r0 + r >= n_rows) break;
-    const int32_t rec = rec_of(r0 + r);
-    if (rec < 0 || rec >= p.n_records) {
+    if (rec[r] < 0 || rec[r] >= p.n_records) {
       if (lane == 0) latch(p.err, kDevBadRecord);
       continue;
     }
-    const int32_t h = (int32_t)(row_of(r0 + r) % p.n_q);
-    const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
-    float* dst = p.rec_o + ((int64_t)rec * p.n_q + h) * d;
+    const float m1 = other[kWarpRows * d + r], l1 = other[kWarpRows * (d + 1) + r];
+    const float mn = fmaxf(m[r], m1), base = mn == -INFINITY ? 0.f : mn;
+    const float a0 = exp2f(m[r] - base), a1 = exp2f(m1 - base);
+    const float sum = l[r] * a0 + l1 * a1;
+    const int64_t at = (int64_t)rec[r] * p.n_q + head_of(r0 + r);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    float* dst = p.rec_o + at * d;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) dst[lane + 32 * i] = acc[r][i] * inv;
-    if (lane == 0) p.rec_lse[(int64_t)rec * p.n_q + h] = kv8_record_lse(l[r], (m[r] + log2f(l[r])) * kLn2);
+    for (int i = 0; i < kCols; ++i)
+#pragma unroll
+      for (int e = 0; e < kPer; ++e)
+        dst[(lane + 32 * i) * kPer + e] = (acc[r][i * kPer + e] * a0 + other[r * d + (i * kPer + e) * 32 + lane] * a1) * inv;
+    if (lane == 0) p.rec_lse[at] = kv8_record_lse(sum, (mn + log2f(sum)) * kLn2);
   }
 }
 
 // CTAs [0, n_prefix) take prefix items first_item.., the rest (suffix item, KV head, block of kRows of
 // its query heads): one launch, so that short prefixes and suffixes share the SMs.
 template <typename T, int VPL>
-__global__ void __launch_bounds__(256) kv8_generic_kernel(AttnParams p, int32_t first_item, int32_t n_prefix) {
+__global__ void __launch_bounds__(256, VPL <= 2 ? 3 : VPL <= 6 ? 2 : 1) kv8_generic_kernel(AttnParams p, int32_t first_item, int32_t n_prefix) {
+  grid_dep_launch_dependents();  // the merge waits for this grid before it reads a record
   if ((int32_t)blockIdx.x < n_prefix) {
     const DevPrefixItem it = p.pitems[first_item + blockIdx.x];
     const DevGroup gr = p.groups[it.group];
@@ -307,7 +398,7 @@ __global__ void __launch_bounds__(256) kv8_generic_kernel(AttnParams p, int32_t 
     auto req = [&](int r) { return p.group_req[gr.req_begin + (r0 + r) / p.g]; };
     kv8_generic_run<T, VPL>(
         p, it.kv_head, t0, t1, n_rows, [&](int32_t t) { return (int32_t)(gr.slab_off + t); },
-        [&](int r) { return (int64_t)req(r) * p.n_q + it.kv_head * p.g + (r0 + r) % p.g; },
+        req, [&](int r) { return it.kv_head * p.g + (r0 + r) % p.g; },
         [&](int r) { return p.reqs[req(r)].rec_base + it.split; });
     return;
   }
@@ -325,7 +416,7 @@ __global__ void __launch_bounds__(256) kv8_generic_kernel(AttnParams p, int32_t 
         latch(p.err, kDevBadSlot);
         return (int32_t)-1;
       },
-      [&](int r) { return (int64_t)it.b * p.n_q + h0 + r; }, [&](int) { return it.rec; });
+      [&](int) { return it.b; }, [&](int r) { return h0 + r; }, [&](int) { return it.rec; });
 }
 
 // Runs f with VPL = d / 32 as a compile-time constant.
