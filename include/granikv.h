@@ -148,7 +148,8 @@ granikv_status granikv_destroy(granikv_ctx* ctx);
  * granikv_prefill_attention is GRANIKV_ERR_UNSUPPORTED (a prefix is prefilled in 16 bits and its
  * K/V given to granikv_hot_fill), and granikv_set_fused_merge has no effect. ----------------- */
 granikv_status granikv_create_kv8(const granikv_config* cfg, granikv_ctx** out);
-/* Bytes of one slot's row; GRANIKV_ERR_UNSUPPORTED for a head_dim that granikv_create refuses. */
+/* Bytes of one slot's row; GRANIKV_ERR_UNSUPPORTED for a head_dim that granikv_create refuses, and
+ * (as from granikv_create_kv8) for a row of more than 2^24 bytes. */
 granikv_status granikv_kv8_row_bytes(int32_t n_kv, int32_t head_dim, size_t* bytes);
 
 /* ---- HOT pool ("B.10 Cross-pool admission and promotion policy"; "B.8 Multi-prefix

@@ -514,9 +514,12 @@ granikv_status create_impl(const granikv_config* cfg, bool kv8, granikv_ctx** ou
   if (!(fp > 0.0 && fp < 1.0)) return GRANIKV_ERR_INVALID;
   if (cfg->max_slabs < 0 || cfg->max_batch < 0 || cfg->m_sat < 0) return GRANIKV_ERR_INVALID;
 
+  if (kv8 && kv8_row_bytes(cfg->n_kv, cfg->head_dim) > kKv8MaxRow) return GRANIKV_ERR_UNSUPPORTED;
+
   granikv_ctx* c = new (std::nothrow) granikv_ctx();
   if (!c) return GRANIKV_ERR_INVALID;
   c->cfg = *cfg;
+  if (kv8) c->kv8_row = kv8_row_bytes(cfg->n_kv, cfg->head_dim);
   c->cfg.hot_fraction = fp;
   if (c->cfg.max_slabs == 0) c->cfg.max_slabs = kDefaultMaxSlabs;
   if (c->cfg.max_batch == 0) c->cfg.max_batch = kDefaultMaxBatch;
@@ -528,7 +531,6 @@ granikv_status create_impl(const granikv_config* cfg, bool kv8, granikv_ctx** ou
     delete c;
     return GRANIKV_ERR_INVALID;
   }
-  if (kv8) c->kv8_row = kv8_row_bytes(cfg->n_kv, cfg->head_dim);
   if (c->n_hot > 0) c->free_ext.push_back({0, c->n_hot});
   c->slabs.resize(c->cfg.max_slabs);
   c->head = 0;
@@ -633,6 +635,7 @@ granikv_status granikv_create_kv8(const granikv_config* cfg, granikv_ctx** out) 
 granikv_status granikv_kv8_row_bytes(int32_t n_kv, int32_t head_dim, size_t* bytes) {
   if (!bytes || n_kv <= 0) return GRANIKV_ERR_INVALID;
   if (head_dim <= 0 || head_dim % 32 || head_dim > 256) return GRANIKV_ERR_UNSUPPORTED;
+  if (kv8_row_bytes(n_kv, head_dim) > kKv8MaxRow) return GRANIKV_ERR_UNSUPPORTED;
   *bytes = (size_t)kv8_row_bytes(n_kv, head_dim);
   return GRANIKV_OK;
 }

@@ -141,6 +141,7 @@ constexpr int kKv8Block = 64;
 constexpr int kKv8VBox = 32;  // slots of one TMA box of V's codes (dense kernel)
 constexpr float kE4m3Max = 448.0f;
 constexpr float kKv8AmaxMin = 1.2621774483536189e-29f;  // 2^-96: smallest amax a scale is made for
+constexpr int64_t kKv8MaxRow = 1 << 24;  // bytes of a packed row: offsets within a block of 64 fit 32 bits
 __host__ __device__ inline int64_t kv8_row_bytes(int32_t n_kv, int32_t d) {
   return ((int64_t)n_kv * (d + 4) + 15) / 16 * 16;
 }

@@ -10,6 +10,7 @@
 
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <type_traits>
 
 namespace granikv {
@@ -131,15 +132,16 @@ __global__ void __launch_bounds__(256) weigh_generic_kernel(WeighParams p, const
 // multiplies the scores, and q is brought into fp16's range by a power of two per query head
 // (exact but for elements 2^-28 below the row's largest).
 // The units' sums go to shared memory and are added in KV-head order: the result has one order.
-// A CTA takes 64, 128 or 256 tokens: its start (length, slots, q, first rows: four trips to memory one
-// after the other) costs about 4 us, so long rows take more tokens a CTA as long as the grid still
-// fills the SMs twice over.
-constexpr int kChunkMin = 64, kChunkMax = 256;
-constexpr int kMaxSums = 40 * 1024; // shared memory for the units' sums
+// A CTA takes a chunk of 64 to 512 tokens, sized so that all chunks run at once: with 256 tokens a CTA the
+// 877 chunks of 224K tokens made 1.44 waves of 608 CTAs (49.5 us against 47.8), and a CTA's start (length, slots, q, first rows: four
+// trips to memory one after the other) costs about 4 us each time.
+constexpr int kChunkMin = 64, kChunkMax = 512;
+constexpr int kMaxHeads = 64;  // KV heads: the sums of a chunk of kChunkMin tokens take 16 KB
 
-// Two units in shared memory a warp, and as many warps as registers allow: packed rows (224K tokens)
-// 50.8 us with four CTAs an SM, 52.9 with three and three units, 58.9 with two and four; 16-bit rows (30K
-// tokens) 15.3 us with three CTAs.  With the units ahead in registers instead, 58.8 and 15.2 us at best.
+// Two units in shared memory a warp, and as many warps as registers allow: 224K tokens of packed rows
+// 47.8 us (5.0 TB/s of its 237 MB), 30K of 16-bit rows 13.9 us.  Fewer CTAs with deeper rings were
+// slower (224K tokens, on an earlier form: 50.8 us with four CTAs an SM, 52.9 with three and three units,
+// 58.9 with two and four), and so were units ahead in registers (58.8).
 template <bool KV8, int D>
 struct WeighUnit {
   static constexpr int kPieces = KV8 ? D / 64 : D / 32;            // 16-byte pieces of a row a lane
@@ -147,6 +149,8 @@ struct WeighUnit {
   static constexpr int kDepth = 2;
   static constexpr int kRing = 8 * kDepth * kBytes;
   static constexpr int kBlocks = KV8 ? 4 : 3;
+  // shared memory for a chunk's sums that leaves room for kBlocks CTAs an SM
+  static constexpr int kSums = KV8 ? 16 * 1024 : 8 * 1024;
 };
 
 template <bool KV8, int D, int N>
@@ -162,34 +166,47 @@ __global__ void __launch_bounds__(256, WeighUnit<KV8, D>::kBlocks) weigh_mma_ker
   chunk_of(rows, p.live_len, blockIdx.x, kChunk, b, t0, n);
   if (n <= 0) return;
   // every place up to the last unit's end has a slot or -1
-  if (tid < (n + 15) / 16 * 16) {
+  for (int32_t i = tid; i < (n + 15) / 16 * 16; i += 256) {
     int32_t slot = -1;
-    if (tid < n) {
-      slot = p.req_to_slot[(int64_t)b * p.cap + t0 + tid];
+    if (i < n) {
+      slot = p.req_to_slot[(int64_t)b * p.cap + t0 + i];
       if (slot < p.n_hot || slot >= p.n_slots) {
         latch(p.err, kDevBadSlot);
         slot = -1;
       }
     }
-    s_slot[tid] = slot;
+    s_slot[i] = slot;
   }
-  const int n_units = (n + 15) / 16 * p.n_kv;
   const uint32_t ring = smem_u32(s_ring) + warp * (Unit::kDepth * Unit::kBytes);
-  // this lane's pieces of the rows of unit u into stage st (zeros for a slot that does not count)
-  auto load_unit = [&](int u, int st) {
-    if (u < n_units) {
-      const int32_t j = u % p.n_kv, tile = u / p.n_kv * 16;
+  // a warp takes every eighth unit; unit u is KV head j = u % n_kv of the tokens from tile = u / n_kv * 16 on
+  struct Place {
+    int32_t j, tile;
+  };
+  const int32_t step_j = 8 % p.n_kv, step_tile = 8 / p.n_kv * 16;
+  auto next = [&](Place& x) {
+    x.j += step_j;
+    x.tile += step_tile;
+    if (x.j >= p.n_kv) {
+      x.j -= p.n_kv;
+      x.tile += 16;
+    }
+  };
+  const int32_t row_bytes = KV8 ? (int32_t)p.kv8_row : p.n_kv * D * 2;
+  // this lane's pieces of the rows of a unit into stage st (zeros for a slot that does not count)
+  auto load_unit = [&](const Place& x, int st) {
+    if (x.tile < n) {
+      const int32_t j = x.j, tile = x.tile;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int32_t slot = s_slot[tile + r + 8 * h];
-        const uint8_t* row = (const uint8_t*)p.kpool + (slot < 0 ? 0 : (int64_t)slot * (KV8 ? p.kv8_row : (int64_t)p.n_kv * D * 2));
-        const uint4* src = reinterpret_cast<const uint4*>(row + (int64_t)j * (KV8 ? D : 2 * D)) + c;
+        const uint8_t* row = (const uint8_t*)p.kpool + (int64_t)max(slot, 0) * row_bytes;
+        const uint4* src = reinterpret_cast<const uint4*>(row + j * (KV8 ? D : 2 * D)) + c;
         const uint32_t dst = ring + st * Unit::kBytes + (h * Unit::kPieces * 32 + lane) * 16;
 #pragma unroll
         for (int i = 0; i < Unit::kPieces; ++i) cp_async16(dst + i * 512, src + 4 * i, slot < 0 ? 0 : 16);
         if constexpr (KV8)
           cp_async4(ring + st * Unit::kBytes + 2 * Unit::kPieces * 512 + (h * 32 + lane) * 4,
-                    row + (int64_t)p.n_kv * D + 4 * j, slot < 0 ? 0 : 4);
+                    row + p.n_kv * D + 4 * j, slot < 0 ? 0 : 4);
       }
     }
     cp_async_commit();
@@ -232,8 +249,8 @@ __global__ void __launch_bounds__(256, WeighUnit<KV8, D>::kBlocks) weigh_mma_ker
     e0 = __shfl_sync(0xffffffffu, minus, 8 * c);
     e1 = __shfl_sync(0xffffffffu, minus, 8 * c + 4);
   };
-  auto unit = [&](int u, int st) {
-    const int32_t j = u % p.n_kv, tile = u / p.n_kv * 16;
+  auto unit = [&](const Place& x, int st) {
+    const int32_t j = x.j, tile = x.tile;
     const unsigned char* mine = s_ring + warp * (Unit::kDepth * Unit::kBytes) + st * Unit::kBytes;
     const uint4* ka = reinterpret_cast<const uint4*>(mine) + lane;
     float sa = 1.f, sb = 1.f;
@@ -280,24 +297,29 @@ __global__ void __launch_bounds__(256, WeighUnit<KV8, D>::kBlocks) weigh_mma_ker
       s_sum[j * kChunk + tile + r + 8] = w1;
     }
   };
+  Place now{warp % p.n_kv, warp / p.n_kv * 16}, ahead = now;
   // q of the warp's first units' heads is on its way with the slots
-  if (warp < n_units) load_q(warp % p.n_kv * p.g, (warp % p.n_kv + 1) * p.g);
+  if (now.tile < n) load_q(now.j * p.g, (now.j + 1) * p.g);
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < Unit::kDepth - 1; ++i) load_unit(warp + 8 * i, i);
+  for (int i = 0; i < Unit::kDepth - 1; ++i) {
+    load_unit(ahead, i);
+    next(ahead);
+  }
   int st = 0;
-  for (int u = warp; u < n_units; u += 8) {
-    load_unit(u + 8 * (Unit::kDepth - 1), (st + Unit::kDepth - 1) % Unit::kDepth);
+  for (; now.tile < n; next(now)) {
+    load_unit(ahead, (st + Unit::kDepth - 1) % Unit::kDepth);
+    next(ahead);
     cp_async_wait<Unit::kDepth - 1>();
-    unit(u, st);
+    unit(now, st);
     st = (st + 1) % Unit::kDepth;
   }
   __syncthreads();
-  if (tid < n) {
+  for (int32_t i = tid; i < n; i += 256) {
     float w = 0.f;
-    for (int32_t j = 0; j < p.n_kv; ++j) w += s_sum[j * kChunk + tid];
-    if (s_slot[tid] < 0) w = 0.f;
-    float* dst = p.weight + (int64_t)b * p.cap + t0 + tid;
+    for (int32_t j = 0; j < p.n_kv; ++j) w += s_sum[j * kChunk + i];
+    if (s_slot[i] < 0) w = 0.f;
+    float* dst = p.weight + (int64_t)b * p.cap + t0 + i;
     *dst = p.keep != 0.f ? p.keep * *dst + w : w;
   }
 }
@@ -621,14 +643,13 @@ cudaError_t evict_n(const EvictRow* rows, int32_t row0, int32_t n, int32_t keep_
 
 template <typename T>
 bool weigh_on_mma(const WeighParams& p) {
-  return std::is_same_v<T, __nv_bfloat16> && (p.d == 128 || p.d == 64) &&
-         (int)sizeof(float) * p.n_kv * kChunkMax <= kMaxSums;
+  return std::is_same_v<T, __nv_bfloat16> && (p.d == 128 || p.d == 64) && p.n_kv <= kMaxHeads;
 }
 
 template <bool KV8, int D, int N>
 cudaError_t weigh_mma(const WeighParams& p, const WeighRows<N>& rows, int32_t chunks, cudaStream_t s) {
   static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem_once(weigh_mma_kernel<KV8, D, N>, WeighUnit<KV8, D>::kRing + kMaxSums, allowed);
+  cudaError_t e = allow_smem_once(weigh_mma_kernel<KV8, D, N>, WeighUnit<KV8, D>::kRing + 4 * kMaxHeads * kChunkMin, allowed);
   if (e != cudaSuccess) return e;
   const int smem = WeighUnit<KV8, D>::kRing + (int)sizeof(float) * p.n_kv * rows.tokens;
   weigh_mma_kernel<KV8, D, N><<<chunks, 256, smem, s>>>(p, rows);
@@ -669,10 +690,18 @@ cudaError_t weigh_all(const WeighParams& p, const int32_t* seq_len, cudaStream_t
   constexpr int kSmall = 64, kLarge = kRowsPerLaunch;
   int tokens = kTok;
   if (weigh_on_mma<T>(p)) {
-    int64_t total = 0;
-    for (int32_t b = 0; b < p.B; ++b) total += seq_len[b];
-    tokens = kChunkMax;
-    while (tokens > kChunkMin && total < 4LL * p.num_sms * tokens) tokens /= 2;
+    using Unit = WeighUnit<KV8, 128>;
+    const int most = std::max(kChunkMin, std::min(kChunkMax, Unit::kSums / (4 * p.n_kv) / 16 * 16));
+    const int64_t slots = (int64_t)Unit::kBlocks * p.num_sms;
+    // the fewest tokens a chunk, in steps of 16, with which the grid is one wave
+    tokens = kChunkMin;
+    for (int pass = 0; pass < 8 && tokens < most; ++pass) {
+      int64_t chunks = 0;
+      for (int32_t b = 0; b < p.B; ++b) chunks += (seq_len[b] + tokens - 1) / tokens;
+      if (chunks <= slots) break;
+      const int64_t want = (chunks * tokens / slots + 15) / 16 * 16;
+      tokens = (int)std::min<int64_t>(most, std::max<int64_t>(want, tokens + 16));
+    }
   }
   cudaError_t e = cudaSuccess;
   for (int32_t b = 0; b < p.B && e == cudaSuccess;) {

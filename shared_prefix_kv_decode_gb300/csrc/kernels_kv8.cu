@@ -14,66 +14,89 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ void latch(int32_t* err, int32_t code) { atomicCAS(err, 0, code); }
 
-// 16 bytes of a row, kept as they came: 8 bf16 or 4 fp32 elements.
+// 16 bytes of a row, kept as they came: 8 bf16 or 4 fp32 elements.  amax_of: the largest finite magnitude
+// of N pieces.
 template <typename T>
 struct Piece;
 template <>
 struct Piece<__nv_bfloat16> {
   static constexpr int kElems = 8;
   uint4 w;
-  __device__ __forceinline__ float amax() const {
-    return fmaxf(fmaxf(bf16x2_finite_max(w.x), bf16x2_finite_max(w.y)), fmaxf(bf16x2_finite_max(w.z), bf16x2_finite_max(w.w)));
-  }
   __device__ __forceinline__ void store(uint8_t* dst, float inv) const {
-    auto lo = [&](uint32_t x) { return __uint_as_float(x << 16) * inv; };
-    auto hi = [&](uint32_t x) { return __uint_as_float(x & 0xffff0000u) * inv; };
-    *reinterpret_cast<uint2*>(dst) = make_uint2(f32x4_to_e4m3x4(lo(w.x), hi(w.x), lo(w.y), hi(w.y)),
-                                                f32x4_to_e4m3x4(lo(w.z), hi(w.z), lo(w.w), hi(w.w)));
+    const uint64_t inv2 = f2_pack(inv, inv);
+    auto codes = [&](uint32_t x) {
+      float a, b;
+      f2_unpack(f2_mul(f2_pack(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)), inv2), a, b);
+      return (uint32_t)f32x2_to_e4m3x2(a, b);
+    };
+    *reinterpret_cast<uint2*>(dst) = make_uint2(codes(w.x) | codes(w.y) << 16, codes(w.z) | codes(w.w) << 16);
+  }
+  template <int N>
+  __device__ static __forceinline__ float amax_of(const Piece (&x)[N]) {
+    // magnitudes order as their bits do, two to a word; only where one is not finite are they told apart
+    uint32_t m = 0u;
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+      m = __vmaxu2(m, __vmaxu2(x[c].w.x & 0x7fff7fffu, x[c].w.y & 0x7fff7fffu));
+      m = __vmaxu2(m, __vmaxu2(x[c].w.z & 0x7fff7fffu, x[c].w.w & 0x7fff7fffu));
+    }
+    const uint32_t top = max(m & 0xffffu, m >> 16);
+    float amax = __uint_as_float(top << 16);
+    if (top >= 0x7f80u) {
+      amax = 0.f;
+#pragma unroll
+      for (int c = 0; c < N; ++c)
+        amax = fmaxf(amax, fmaxf(fmaxf(bf16x2_finite_max(x[c].w.x), bf16x2_finite_max(x[c].w.y)),
+                                 fmaxf(bf16x2_finite_max(x[c].w.z), bf16x2_finite_max(x[c].w.w))));
+    }
+    return amax;
   }
 };
 template <>
 struct Piece<float> {
   static constexpr int kElems = 4;
   uint4 w;
-  __device__ __forceinline__ float amax() const {
-    return fmaxf(fmaxf(finite_abs(__uint_as_float(w.x)), finite_abs(__uint_as_float(w.y))),
-                 fmaxf(finite_abs(__uint_as_float(w.z)), finite_abs(__uint_as_float(w.w))));
-  }
   __device__ __forceinline__ void store(uint8_t* dst, float inv) const {
     *reinterpret_cast<uint32_t*>(dst) = f32x4_to_e4m3x4(__uint_as_float(w.x) * inv, __uint_as_float(w.y) * inv,
                                                         __uint_as_float(w.z) * inv, __uint_as_float(w.w) * inv);
+  }
+  template <int N>
+  __device__ static __forceinline__ float amax_of(const Piece (&x)[N]) {
+    float amax = 0.f;
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+      amax = fmaxf(amax, fmaxf(fmaxf(finite_abs(__uint_as_float(x[c].w.x)), finite_abs(__uint_as_float(x[c].w.y))),
+                               fmaxf(finite_abs(__uint_as_float(x[c].w.z)), finite_abs(__uint_as_float(x[c].w.w)))));
+    return amax;
   }
 };
 
 // One block of kKv8Block slab tokens of one KV head (the heads of a block are neighbours in the grid, so
 // that its rows are read and written whole at about the same time), of K (blockIdx.y = 0) or V.  The block stays in
-// registers between its amax and its codes (NP 16-byte pieces a thread, all requested at once), so
-// the rows are read once: 3 bytes moved for each bf16 element, bound by HBM and by how many CTAs an SM
-// holds in the meantime (16K tokens of 8 x 128: 25.2 us with five CTAs an SM, 23.1 with six; the
-// floor is 14.9).
-template <typename T, int NP>
-__global__ void __launch_bounds__(256, NP <= 4 ? 6 : 1) kv8_fill_kernel(const T* __restrict__ k, const T* __restrict__ v, int32_t L_p,
-                                                       uint8_t* __restrict__ kpool, uint8_t* __restrict__ vpool,
-                                                       int64_t first_slot, int32_t n_kv, int32_t d, int64_t row) {
-  constexpr int E = Piece<T>::kElems;
+// registers between its amax and its codes (pieces of 16 bytes, all of a thread's requested at once), so
+// the rows are read once: 3 bytes moved for each bf16 element (16K tokens of 8 x 128: 17.5 us at six CTAs an
+// SM; its 100 MB take 14.9).  What it costs beyond HBM is issue: with head_dim at run time, the pieces'
+// places cost two divisions each, the warps issued in 77 % of the cycles, and it took 23.2 us.
+template <typename T, int D>
+__global__ void __launch_bounds__(256, sizeof(T) * D <= 256 ? 6 : 1) kv8_fill_kernel(
+    const T* __restrict__ k, const T* __restrict__ v, int32_t L_p, uint8_t* __restrict__ kpool,
+    uint8_t* __restrict__ vpool, int64_t first_slot, int32_t n_kv) {
+  constexpr int kElems = Piece<T>::kElems;
+  constexpr int kPerRow = D / kElems;              // pieces of a head's row
+  constexpr int kPieces = kKv8Block * kPerRow / 256;  // of a thread
   __shared__ float s_max[8];
   const int32_t j = blockIdx.x % n_kv;
-  const T* src = blockIdx.y ? v : k;
-  uint8_t* pool = blockIdx.y ? vpool : kpool;
   const int32_t t0 = blockIdx.x / n_kv * kKv8Block;
   const int32_t n = min(kKv8Block, L_p - t0);
-  const int32_t per_row = d / E;  // pieces of a head's row
-  Piece<T> x[NP];
+  const T* src = (blockIdx.y ? v : k) + ((int64_t)t0 * n_kv + j) * D;
+  Piece<T> x[kPieces];
 #pragma unroll
-  for (int c = 0; c < NP; ++c) {
-    const int32_t idx = threadIdx.x + c * 256;
-    const int32_t t = idx / per_row;
-    x[c].w = t < n ? __ldcs(reinterpret_cast<const uint4*>(src + ((int64_t)(t0 + t) * n_kv + j) * d + idx % per_row * E))
+  for (int c = 0; c < kPieces; ++c) {
+    const int32_t idx = threadIdx.x + c * 256, t = idx / kPerRow;
+    x[c].w = t < n ? __ldcs(reinterpret_cast<const uint4*>(src + t * (n_kv * D) + idx % kPerRow * kElems))
                    : make_uint4(0u, 0u, 0u, 0u);
   }
-  float amax = 0.f;
-#pragma unroll
-  for (int c = 0; c < NP; ++c) amax = fmaxf(amax, x[c].amax());
+  float amax = Piece<T>::amax_of(x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = amax;
@@ -81,15 +104,14 @@ __global__ void __launch_bounds__(256, NP <= 4 ? 6 : 1) kv8_fill_kernel(const T*
 #pragma unroll
   for (int w = 0; w < 8; ++w) amax = fmaxf(amax, s_max[w]);
   const float inv = kv8_inverse(amax), scale = kv8_scale(amax);
-  uint8_t* dst = pool + (first_slot + t0) * row;
+  const int32_t row = (int32_t)kv8_row_bytes(n_kv, D);
+  uint8_t* dst = (blockIdx.y ? vpool : kpool) + (first_slot + t0) * row;
 #pragma unroll
-  for (int c = 0; c < NP; ++c) {
-    const int32_t idx = threadIdx.x + c * 256;
-    const int32_t t = idx / per_row;
-    if (t < n) x[c].store(dst + (int64_t)t * row + (int64_t)j * d + idx % per_row * E, inv);
+  for (int c = 0; c < kPieces; ++c) {
+    const int32_t idx = threadIdx.x + c * 256, t = idx / kPerRow;
+    if (t < n) x[c].store(dst + t * row + j * D + idx % kPerRow * kElems, inv);
   }
-  for (int32_t t = threadIdx.x; t < n; t += 256)
-    *reinterpret_cast<float*>(dst + (int64_t)t * row + (int64_t)n_kv * d + 4 * j) = scale;
+  for (int32_t t = threadIdx.x; t < n; t += 256) *reinterpret_cast<float*>(dst + t * row + n_kv * D + 4 * j) = scale;
 }
 
 // One warp quantises head j of one K (or V) row into a packed slot: a lane holds VPL consecutive
@@ -442,8 +464,7 @@ cudaError_t fill_t(const T* k, const T* v, int32_t L_p, uint8_t* kpool, uint8_t*
   if (ctas > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)ctas, 2);
   return with_vpl(d, [&](auto vpl) {
-    constexpr int np = kKv8Block * 32 * decltype(vpl)::value / Piece<T>::kElems / 256;  // pieces a thread
-    kv8_fill_kernel<T, np><<<grid, 256, 0, s>>>(k, v, L_p, kpool, vpool, first_slot, n_kv, d, kv8_row_bytes(n_kv, d));
+    kv8_fill_kernel<T, 32 * decltype(vpl)::value><<<grid, 256, 0, s>>>(k, v, L_p, kpool, vpool, first_slot, n_kv);
     return cudaGetLastError();
   });
 }

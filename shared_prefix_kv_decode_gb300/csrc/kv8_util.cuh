@@ -43,6 +43,13 @@ __device__ __forceinline__ uint32_t f32x4_to_e4m3x4(float a, float b, float c, f
   return (uint32_t)f32x2_to_e4m3x2(a, b) | ((uint32_t)f32x2_to_e4m3x2(c, d) << 16);
 }
 
+// Products of two pairs of floats.
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // A query row scaled by a power of two so that its largest finite element lies in [2^kTop, 2^(kTop+1)).
 // In fp16 with kTop = 14: bf16's 8 significant bits fit fp16's 11, so elements down to 2^-31 of the largest stay
 // exact (fp16's last subnormal is 2^-24), smaller ones are off by at most 2^-39 of it.

@@ -76,6 +76,15 @@ def test_row_bytes_refusals(granikv_lib):
         assert _status(gb.kv8_row_bytes, 2, d) == gb.ERR_UNSUPPORTED
 
 
+def test_rows_too_long_are_refused(granikv_lib):
+    assert gb.kv8_row_bytes(2 ** 24 // 260, 256) <= 2 ** 24
+    for n_kv in (2 ** 24 // 260 + 1, 2 ** 30):
+        assert _status(gb.kv8_row_bytes, n_kv, 256) == gb.ERR_UNSUPPORTED
+        with pytest.raises(gb.GranikvError) as e:
+            _ctx(n_q=n_kv, n_kv=n_kv, d=256)
+        assert e.value.status == gb.ERR_UNSUPPORTED
+
+
 def test_kv8_context_refusals(granikv_lib):
     with pytest.raises(gb.GranikvError) as e:
         _ctx(d=80)
