@@ -146,7 +146,12 @@ granikv_status granikv_destroy(granikv_ctx* ctx);
  * granikv_dispatch, granikv_decode_attention (and its append and static forms),
  * granikv_cold_weigh and the pool calls work on such a context as on any other;
  * granikv_prefill_attention is GRANIKV_ERR_UNSUPPORTED (a prefix is prefilled in 16 bits and its
- * K/V given to granikv_hot_fill), and granikv_set_fused_merge has no effect. ----------------- */
+ * K/V given to granikv_hot_fill), and granikv_set_fused_merge has no effect.  Backends: bf16 q with
+ * head_dim 128 -- dense on tcgen05, COLD tokens of up to 8 query heads a KV head on warp-level
+ * tensor cores; every other shape and GRANIKV_BACKEND_CASCADE on CUDA cores.  The dense backend is the
+ * faster one at every batch size, so M_sat is 1 unless it is set.
+ * granikv_decode_attention_append quantises the newest rows into their slots in a launch of its own
+ * before the attention, and granikv_inject_stall applies as it does to the bf16 path. ----------- */
 granikv_status granikv_create_kv8(const granikv_config* cfg, granikv_ctx** out);
 /* Bytes of one slot's row; GRANIKV_ERR_UNSUPPORTED for a head_dim that granikv_create refuses, and
  * (as from granikv_create_kv8) for a row of more than 2^24 bytes. */

@@ -291,7 +291,8 @@ class GraniKVCache:
                 lse: Optional[torch.Tensor] = None):
         """Causal prefill of a HOT prefix in one layer: its K/V ([L_p, n_kv, d], if given) are
         written into the slab, then each of its L_p query tokens (q [L_p, n_q, d]) attends the
-        slab up to itself.  Returns (o [L_p, n_q, d], lse [L_p, n_q])."""
+        slab up to itself.  Returns (o [L_p, n_q, d], lse [L_p, n_q]).  Refused (ERR_UNSUPPORTED)
+        on an 8-bit cache: prefill in 16 bits and give the K/V to admit()."""
         L_p = q.shape[0]
         if o is None:
             o = torch.empty((L_p, self.n_q, self.head_dim), dtype=self.tdtype, device=self.device)
