@@ -10,11 +10,12 @@
 // A tile passes through S, softmax and PV with about 2,900 clocks of latency (products, commits and
 // barrier waits, exponentials), while its products need 564 at the nominal rates and its exponentials 512
 // of the exponential unit: five tiles in flight (five S/P buffers of 64 columns, O and Q in the rest of
-// TMEM) cover that.  Measured, a CTA takes 0.91 us for 128 tokens (1,760 clocks, 64 % of the products'
-// nominal rate; cuBLAS, on products of this size, 0.68 us), with all-zero data and with half the loads
-// alike: what is left is the hand-over between issue, commit and softmax, not memory or power.  With
-// 128-token tiles in three buffers, all that fit, a step of the 32/8-head shape (16K prefix, B = 64) took
-// 32.7 us against 30.6.
+// TMEM) cover that.  A CTA takes 0.88 us for 128 tokens (15 row blocks on one slab, so that HBM is idle).
+// With parts taken out: the loads alone 0.48, loads and products 0.68 (what cuBLAS takes for products of
+// this size), with softmax 0.75; the conversion of V adds the rest, by its traffic through shared memory
+// next to the operands'.  Other splits of TMEM (four S and two P buffers: 0.92; three and four: 1.02),
+// waits that spin instead of suspending (0.87) and one arrival a warp (0.89) are no better.  128-token
+// tiles in three buffers: a step of the 32/8-head shape (16K prefix, B = 64) took 32.7 us against 30.6.
 // Number format.  S takes K's codes straight from TMA and q as the sum of two e4m3 values: each row is
 // scaled by a power of two so that its largest element lies in [2^7, 2^8), hi = e4m3(q) and lo =
 // e4m3(q - hi).  bf16 has 8 significant bits and each part 4, so q = hi + lo exactly down to 2^-2, 2^-9
