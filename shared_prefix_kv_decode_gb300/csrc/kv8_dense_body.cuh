@@ -89,8 +89,6 @@ constexpr int kOffBar = kOffMPub + 4 * 2 * 32 * 4;
 constexpr int kBarArea = 512;
 constexpr int kSmemBytes = kOffBar + kBarArea + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-static_assert(kVSlots * kTile >= kM * kD * 4, "the epilogue stages the fp32 record rows in the V ring");
-static_assert(kKSlots * kCodes >= kM * 8, "the epilogue keeps the rows' record offsets in the K ring");
 static_assert(kConvWarps * kCSlots * kPartCodes >= 4 * kM * 4, "the epilogue's sums and maxima");
 constexpr uint32_t kTmemCols = 512;           // S/P buffers at 0, 64, 128, 192, 256; Q (hi, lo) at 320; O at 384
 constexpr uint32_t kColQ = kSBufs * kN, kColO = 384;
@@ -138,6 +136,23 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
   return p != 0;
+}
+
+// 32 bytes of a record (32-byte aligned), kept in L2 for the merge
+__device__ __forceinline__ void st_record8(float* a, const float (&x)[8], uint64_t pol) {
+  asm volatile("st.global.L2::cache_hint.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8}, %9;" ::"l"(a), "f"(x[0]),
+               "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]), "l"(pol)
+               : "memory");
+}
+// Two bf16 times f -> fp16; four fp16 -> four e4m3 codes (nearest even, NaN kept).
+__device__ __forceinline__ __half2 f16x2_of(uint32_t w, float f) {
+  return __floats2half2_rn(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
+}
+__device__ __forceinline__ uint32_t f16x4_to_e4m3x4(__half2 a, __half2 b) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(*reinterpret_cast<const uint32_t*>(&a)));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(*reinterpret_cast<const uint32_t*>(&b)));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
 // 16 columns of this warp's TMEM lanes
@@ -221,6 +236,17 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
     tma_load_2d(sC + c * kPartCodes, tmv, j * kD, (int32_t)(first_slot + (int64_t)i * kPair + w * kPart), bar(kBarCFull + c));
   };
   const int l2_ahead = p.l2_ahead;
+  // softmax warps: this lane's row (the same for the two warps of a row quarter), its request, head and
+  // record.  The plan is not written by the work before this kernel, so these loads need not wait for it.
+  const int qrow = (warp & 3) * 32 + lane, qhalf = warp >> 2;
+  const int32_t row = rbase + qrow;
+  const bool have = warp < kSoftmaxWarps && row < rows;
+  int32_t req = 0, h = 0, rec = -1;
+  if (have) {
+    req = p.group_req[gr.req_begin + row / g];
+    h = j * g + row % g;
+    rec = p.reqs[req].rec_base + it.split;
+  }
   if (warp == kWarpTmaK && lane == 0) {
     tma_prefetch_desc(tmk);
     tma_prefetch_desc(tmv);
@@ -255,16 +281,18 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
   // past the group are 0
   uint32_t qw[32];
   float* part = reinterpret_cast<float*>(smem + kOffMPub);  // [2][kM], used for the maxima of tiles later
-  const int qrow = (warp & 3) * 32 + lane, qhalf = warp >> 2;
+  // the scales of tile i; a softmax warp's first ones are on their way with its rows
+  const int64_t scale_at = (int64_t)p.n_kv * kD + 4 * j;
+  float ks = 0.f, vs = 0.f;
+  auto load_scales = [&](int i) {
+    const int64_t a = (first_slot + (int64_t)i * kN) * p.kv8_row + scale_at;
+    ks = *reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.kpool) + a);
+    vs = *reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.vpool) + a);
+  };
   if (warp < kSoftmaxWarps) {
-    const int32_t row = rbase + qrow;
-    const bool have = row < rows;
-    const uint4* src = nullptr;
-    if (have) {
-      const int32_t b = p.group_req[gr.req_begin + row / g];
-      src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                           ((int64_t)b * p.n_q + j * g + row % g) * kD + qhalf * (kD / 2));
-    }
+    if (slab_ok && qhalf < n_tiles) load_scales(qhalf);
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                      ((int64_t)req * p.n_q + h) * kD + qhalf * (kD / 2));
     float amax = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -286,16 +314,19 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
     float unit;
     const float f = q_factor<7>(fmaxf(part[qrow], part[kM + qrow]), unit);
     if (qhalf == 0) units[qrow] = unit;
+    // in fp16 pairs: below 2^8 with 8 significant bits they are exact there down to 2^-17
     uint32_t hi[16], lo[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      const float a = __uint_as_float(qw[2 * k] << 16) * f, b = __uint_as_float(qw[2 * k] & 0xffff0000u) * f;
-      const float c = __uint_as_float(qw[2 * k + 1] << 16) * f, d = __uint_as_float(qw[2 * k + 1] & 0xffff0000u) * f;
+      __half2 x = f16x2_of(qw[2 * k], f), y = f16x2_of(qw[2 * k + 1], f);
       // an infinity becomes NaN, as the scores it stands in would end
-      hi[k] = f32x4_to_e4m3x4(a + 0.f * a, b + 0.f * b, c + 0.f * c, d + 0.f * d);
-      float v[4];
-      e4m3x4_to_f32x4(hi[k], v);
-      lo[k] = f32x4_to_e4m3x4(a - v[0], b - v[1], c - v[2], d - v[3]);
+      const __half2 zero = __floats2half2_rn(0.f, 0.f);
+      x = __hfma2(zero, x, x);
+      y = __hfma2(zero, y, y);
+      hi[k] = f16x4_to_e4m3x4(x, y);
+      uint32_t u, v;
+      e4m3x4_to_f16x4(hi[k], u, v);
+      lo[k] = f16x4_to_e4m3x4(__hsub2(x, *reinterpret_cast<__half2*>(&u)), __hsub2(y, *reinterpret_cast<__half2*>(&v)));
     }
     const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColQ + qhalf * 16;
     tmem_st16(at, hi);
@@ -486,32 +517,14 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
     const int quad = warp & 3;
     const int par = warp >> 2;
     const int half = par;                           // the epilogue's column half of O
-    const int r = quad * 32 + lane;                 // row = TMEM lane
+    const int r = qrow;                             // row = TMEM lane
     const uint32_t lane_off = (uint32_t)((quad * 32) << 16);
     const int pair_bar = kBarPair + quad;           // mbarrier of the two warps sharing rows
     float* mpub = reinterpret_cast<float*>(smem + kOffMPub) + quad * 64;  // [tile parity][lane]
     const float scale = p.scale_log2 * units[r];
-    // this row's request, head and record, looked up now so the loads finish during the tiles
-    const int32_t row = rbase + r;
-    int32_t h = 0, rec = -1;
-    if (row < rows) {
-      const int32_t b = p.group_req[gr.req_begin + row / g];
-      h = j * g + row % g;
-      rec = p.reqs[b].rec_base + it.split;
-    }
-    // the scales of tile i
-    const int64_t scale_at = (int64_t)p.n_kv * kD + 4 * j;
-    float ks, vs;
-    auto load_scales = [&](int i) {
-      const int64_t a = (first_slot + (int64_t)i * kN) * p.kv8_row + scale_at;
-      ks = *reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.kpool) + a);
-      vs = *reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.vpool) + a);
-    };
     float m_own = -INFINITY;   // max (of z, base 2) used for this warp's latest tile
     float l = 0.f;             // this warp's share of the row sum, relative to m_own
-    int pair_phase = 0;
     bool ok = !*abort_flag;
-    if (ok && par < n_tiles) load_scales(par);
     for (int i = par; ok && i < n_tiles; i += 2) {
       const int sb = i % kSBufs;
       const float ca = scale * ks, cb = lg2_approx(vs);
@@ -632,8 +645,7 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
       red[2 * kM + par * kM + r] = m_own;
     }
     mbar_arrive(bar(pair_bar));
-    bool pair_ok = mbar_wait_bounded(bar(pair_bar), pair_phase & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
-    ++pair_phase;
+    const bool pair_ok = mbar_wait_bounded(bar(pair_bar), 0, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
     ok = __all_sync(0xffffffffu, pair_ok) && ok && !*abort_flag;
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
@@ -653,44 +665,21 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
       GRANIKV_TMEM_LD32(tmem + lane_off + kColO + half * 64, u[0]);
       GRANIKV_TMEM_LD32(tmem + lane_off + kColO + half * 64 + 32, u[1]);
       tmem_wait_ld();
-      // Stage the normalised half row in shared memory (the K and V rings are idle: every MMA
-      // has completed), 16-byte chunk c of row r at chunk c ^ (r % 32), so that a warp's 32
-      // rows hit all banks; the pair then stores whole 512-byte rows, one per warp instruction.
-      fence_proxy_async_smem();
-      unsigned char* stage = smem + kOffV;
+      // every lane stores its half row, a whole 32-byte sector at a time
+      if (rec >= 0) {
+        const uint64_t keep = l2_policy_keep();
+        float* dst = p.rec_o + ((int64_t)rec * p.n_q + h) * kD + half * 64;
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 8; ++c) {
+          float x[8];
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-          const int chunk = half * 16 + c * 8 + k / 4;
-          *reinterpret_cast<float4*>(stage + r * 512 + ((chunk ^ (r & 31)) << 4)) =
-              make_float4(__uint_as_float(u[c][k]) * inv, __uint_as_float(u[c][k + 1]) * inv,
-                          __uint_as_float(u[c][k + 2]) * inv, __uint_as_float(u[c][k + 3]) * inv);
+          for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(u[c >> 2][(c & 3) * 8 + k]) * inv;
+          st_record8(dst + c * 8, x, keep);
         }
-      if (half == 0) {
-        const float m_fin = m_used == -INFINITY ? 0.f : m_used;
-        const float lse_row = kv8_record_lse(lt, (m_fin - kShift + log2f(lt)) * kLn2);
-        reinterpret_cast<int64_t*>(smem + kOffK)[r] = rec >= 0 ? ((int64_t)rec * p.n_q + h) * kD : -1;
-        if (rec >= 0) st_record(p.rec_lse + (int64_t)rec * p.n_q + h, lse_row, l2_policy_keep());
-      }
-    }
-    // both halves of the quarter's 32 rows are staged (both warps of a pair agree on `ok`, or the
-    // abort flag is up and this wait gives up)
-    mbar_arrive(bar(pair_bar));
-    bool staged = mbar_wait_bounded(bar(pair_bar), pair_phase & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
-    ++pair_phase;
-    staged = __all_sync(0xffffffffu, staged) && ok;
-    if (staged) {
-      const unsigned char* stage = smem + kOffV;
-      const int64_t* sdst = reinterpret_cast<const int64_t*>(smem + kOffK);
-      const uint64_t keep = l2_policy_keep();
-#pragma unroll 4
-      for (int i = 0; i < 16; ++i) {
-        const int rr = quad * 32 + half * 16 + i;
-        const int64_t d = sdst[rr];
-        if (d < 0) continue;
-        const float4 x = *reinterpret_cast<const float4*>(stage + rr * 512 + ((lane ^ (rr & 31)) << 4));
-        st_record4(p.rec_o + d + lane * 4, x, keep);
+        if (half == 0) {
+          const float m_fin = m_used == -INFINITY ? 0.f : m_used;
+          st_record(p.rec_lse + (int64_t)rec * p.n_q + h, kv8_record_lse(lt, (m_fin - kShift + log2f(lt)) * kLn2), keep);
+        }
       }
     }
   }

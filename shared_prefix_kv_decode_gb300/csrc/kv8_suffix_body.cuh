@@ -108,17 +108,21 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
   int32_t* sslot = reinterpret_cast<int32_t*>(smem + kOffSlots);
   DevSuffixItem* sseg = reinterpret_cast<DevSuffixItem*>(smem + kOffSegs);
   const int n_seg = seg_end - seg_begin;
+  // this thread's descriptor (the plan is not written by the work before this kernel)
+  static_assert(kSegSmem <= kThreads, "a descriptor a thread");
+  DevSuffixItem mine{};
+  if (threadIdx.x < min(n_seg, kSegSmem)) mine = p.sitems[seg_begin + threadIdx.x];
   // the token tables, lengths, pools and q are read only after the previous kernel in the
   // stream completed
   grid_dep_wait();
   grid_dep_launch_dependents();
   // a plan made for more tokens than exist yet: each segment ends at its request's live length
-  auto item = [&](int k) {
-    DevSuffixItem it = p.sitems[seg_begin + k];
+  auto live = [&](DevSuffixItem it) {
     if (p.live_len) it.t1 = max(it.t0, min(it.t1, p.live_len[it.b]));
     return it;
   };
-  for (int k = threadIdx.x; k < min(n_seg, kSegSmem); k += blockDim.x) sseg[k] = item(k);
+  auto item = [&](int k) { return live(p.sitems[seg_begin + k]); };
+  if (threadIdx.x < min(n_seg, kSegSmem)) sseg[threadIdx.x] = live(mine);
   if (threadIdx.x == 0) {
     for (int st = 0; st < kStages; ++st) {
       mbar_init(full_bar(st), kProducers);
