@@ -1092,6 +1092,11 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
       if (ctas_for(mid) <= target) hi = mid;
       else lo = mid + 1;
     }
+    // 8-bit cache on CUDA cores: 64 tokens take a CTA about 2 us, another record the merge about 0.25, so
+    // pieces of L tokens shorter than sqrt(8 L) cost the merge more than they save
+    for (int32_t i = 0; i < G; ++i)
+      if (groups[i].impl == kImplKv8Generic)
+        lo = std::max(lo, std::min(max_tiles, (int64_t)std::ceil(std::sqrt(8.0 * (double)groups[i].L_p) / kGenericTile)));
     bool auto_found = false;
     bool kv8_dense = auto_share && c->kv8_row && n_kv <= 8;
     for (int32_t i = 0; i < G; ++i) kv8_dense = kv8_dense && groups[i].impl == kImplKv8Dense;

@@ -215,17 +215,18 @@ __global__ void __launch_bounds__(256) merge_kernel(AttnParams p) {
   for (int k = 0; k < VPL; ++k) acc[k] = 0.f;
   const float* orec = p.rec_o + ((int64_t)r.rec_base * p.n_q + h) * p.d + lane * VPL;
   const int64_t rec_stride = (int64_t)p.n_q * p.d;
+  constexpr int kAhead = VPL <= 4 ? 8 : 4;  // records whose loads are in flight together
   int32_t i = 0;
-  for (; i + 4 <= r.n_parts; i += 4) {
-    float w[4], x[4][VPL];
+  for (; i + kAhead <= r.n_parts; i += kAhead) {
+    float w[kAhead], x[kAhead][VPL];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < kAhead; ++u) {
       w[u] = exp2f((lse_rec[(int64_t)(i + u) * p.n_q] - lse) * kLog2e);
 #pragma unroll
       for (int k = 0; k < VPL; ++k) x[u][k] = orec[(i + u) * rec_stride + k];
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < kAhead; ++u)
 #pragma unroll
       for (int k = 0; k < VPL; ++k) acc[k] += w[u] * x[u][k];
   }
