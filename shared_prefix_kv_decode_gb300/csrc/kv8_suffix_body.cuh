@@ -25,6 +25,9 @@
 // different 16-byte bank groups.  Rows past a segment's end come from a zero row.  Every mbarrier wait is
 // bounded in time; on expiry the CTA raises an abort flag, latches an error, and the producer
 // waits (again bounded) for its copies in flight before the CTA exits.
+// Bound by HBM on scattered rows: 71K tokens (150 MB, 128 requests) alone take 31.6 us with the merge, about
+// 5.8 TB/s once the rings are full; without the conversions the time is the same.  One tile at a time and one
+// producer warp took 48.1.
 #pragma once
 
 #include "internal.h"
