@@ -1807,7 +1807,7 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
     if (p->n_sitems <= 0) return cudaSuccess;
     c->n_kernels += 1;
     if (p->suffix_impl == kImplKv8Suffix) return launch_kv8_suffix(a, a.scta_begin, p->n_scta, st, pdl);
-    if (p->suffix_impl == kImplKv8Generic) return launch_kv8_generic(c->cfg.dtype, a, 0, 0, true, st);
+    if (p->suffix_impl == kImplKv8Generic) return launch_kv8_generic(c->cfg.dtype, a, 0, 0, true, st, false);
     return p->suffix_impl == kImplSuffixMma ? launch_suffix_mma(a, a.scta_begin, p->n_scta, st, pdl)
                                             : launch_suffix_generic(c->cfg.dtype, a, st);
   };
@@ -1820,7 +1820,7 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
       c->n_kernels += 1;
     }
     if (r == cudaSuccess && p->pitem_count[kImplKv8Generic] > 0) {
-      r = launch_kv8_generic(c->cfg.dtype, a, p->pitem_first[kImplKv8Generic], p->pitem_count[kImplKv8Generic], false, st);
+      r = launch_kv8_generic(c->cfg.dtype, a, p->pitem_first[kImplKv8Generic], p->pitem_count[kImplKv8Generic], false, st, false);
       c->n_kernels += 1;
     }
     if (r == cudaSuccess && p->pitem_count[kImplKv8Dense] > 0) {
@@ -1877,7 +1877,7 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
   }
   if (p->n_pitems > 0 && p->pitem_count[kImplKv8Generic] == p->n_pitems && p->suffix_impl == kImplKv8Generic) {
     // CUDA-core prefix and suffix items in one launch, then the merge
-    e = launch_kv8_generic(c->cfg.dtype, a, p->pitem_first[kImplKv8Generic], p->n_pitems, p->n_sitems > 0, s);
+    e = launch_kv8_generic(c->cfg.dtype, a, p->pitem_first[kImplKv8Generic], p->n_pitems, p->n_sitems > 0, s, true);
     c->n_kernels += 1;
     if (e == cudaSuccess) e = launch_merge_k(true);
     return cuda_status(e);

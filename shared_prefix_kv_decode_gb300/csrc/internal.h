@@ -225,7 +225,7 @@ cudaError_t launch_kv8_append(int32_t dtype, const void* k_new, const void* v_ne
 cudaError_t launch_kv8_append_newest(int32_t dtype, const AttnParams& p, cudaStream_t s);
 // CUDA-core attention of n_items prefix items and, with suffix, of the suffix items, in one launch.
 cudaError_t launch_kv8_generic(int32_t dtype, const AttnParams& p, int32_t first_item, int32_t n_items, bool suffix,
-                               cudaStream_t s);
+                               cudaStream_t s, bool pdl);
 // Tensor-core path of the 8-bit cache (kernels_kv8_tc.cu): dense prefix items and suffix token-CTAs in
 // one grid (either count may be 0; n_tail as for launch_prefix_suffix_tc), and the suffix alone.
 cudaError_t launch_kv8_step(const AttnParams& p, int32_t first_dense, int32_t n_dense, const CUtensorMap& tmk,

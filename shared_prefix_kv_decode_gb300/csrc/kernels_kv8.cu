@@ -405,10 +405,12 @@ __device__ __forceinline__ void kv8_generic_run(const AttnParams& p, int32_t j, 
 // its query heads): one launch, so that short prefixes and suffixes share the SMs.
 template <typename T, int VPL>
 __global__ void __launch_bounds__(256, VPL <= 2 ? 3 : VPL <= 6 ? 2 : 1) kv8_generic_kernel(AttnParams p, int32_t first_item, int32_t n_prefix) {
-  grid_dep_launch_dependents();  // the merge waits for this grid before it reads a record
+  // (the plan is not written by the work before this kernel; everything else waits for that work)
   if ((int32_t)blockIdx.x < n_prefix) {
     const DevPrefixItem it = p.pitems[first_item + blockIdx.x];
     const DevGroup gr = p.groups[it.group];
+    grid_dep_wait();
+    grid_dep_launch_dependents();  // the merge waits for this grid before it reads a record
     if (gr.slab_off < 0 || gr.slab_off + gr.L_p > p.n_hot) {
       if (threadIdx.x == 0) latch(p.err, kDevBadSlab);
       return;
@@ -427,6 +429,8 @@ __global__ void __launch_bounds__(256, VPL <= 2 ? 3 : VPL <= 6 ? 2 : 1) kv8_gene
   const int blocks = (p.g + kRows - 1) / kRows, per = p.n_kv * blocks;
   const int32_t w = blockIdx.x - n_prefix;
   DevSuffixItem it = p.sitems[w / per];
+  grid_dep_wait();
+  grid_dep_launch_dependents();
   if (p.live_len) it.t1 = max(it.t0, min(it.t1, p.live_len[it.b]));
   const int32_t j = w % per / blocks, h0 = j * p.g + w % blocks * kRows;
   const int n_rows = min(kRows, (j + 1) * p.g - h0);
@@ -509,7 +513,7 @@ cudaError_t launch_kv8_append_newest(int32_t dtype, const AttnParams& p, cudaStr
 }
 
 cudaError_t launch_kv8_generic(int32_t dtype, const AttnParams& p, int32_t first_item, int32_t n_items, bool suffix,
-                               cudaStream_t s) {
+                               cudaStream_t s, bool pdl) {
   const int64_t ctas = n_items + (suffix ? (int64_t)p.n_sitems * p.n_kv * ((p.g + kRows - 1) / kRows) : 0);
   if (ctas <= 0) return cudaSuccess;
   if (ctas > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
@@ -519,8 +523,7 @@ cudaError_t launch_kv8_generic(int32_t dtype, const AttnParams& p, int32_t first
     auto kernel = dtype == 1 ? kv8_generic_kernel<__nv_bfloat16, n> : kv8_generic_kernel<float, n>;
     cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)ctas, 256, smem, s>>>(p, first_item, n_items);
-    return cudaGetLastError();
+    return launch_kernel(kernel, dim3((unsigned)ctas), dim3(256), (size_t)smem, s, pdl, p, first_item, n_items);
   });
 }
 
