@@ -1092,8 +1092,9 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
       if (ctas_for(mid) <= target) hi = mid;
       else lo = mid + 1;
     }
-    // 8-bit cache on CUDA cores: 64 tokens take a CTA about 2 us, another record the merge about 0.25, so
-    // pieces of L tokens shorter than sqrt(8 L) cost the merge more than they save
+    // 8-bit cache on CUDA cores: with short pieces the merge's records cost more than the pieces save.
+    // At least sqrt(8 L) of L tokens: two prefixes of 34 and 1,995, B = 4 9.7 us, with sqrt(4 L) 10.3, with
+    // sqrt(16 L) 11.0; 8,000 tokens, B = 8 18.5, 21.8 and 20.1
     for (int32_t i = 0; i < G; ++i)
       if (groups[i].impl == kImplKv8Generic)
         lo = std::max(lo, std::min(max_tiles, (int64_t)std::ceil(std::sqrt(8.0 * (double)groups[i].L_p) / kGenericTile)));

@@ -183,228 +183,236 @@ __global__ void __launch_bounds__(256) kv8_append_newest_kernel(AttnParams p) {
 }
 
 // ---- decode attention on CUDA cores -----------------------------------------------------------
-// A CTA takes up to kGenericRows query rows of one KV head and a run of tokens.  Tiles of 64
-// tokens are unpacked into shared memory once for all rows (a thread holds the next tile's codes
-// and scales while it computes this one).  Warps w and w + 4 hold the same four rows, each over its half
-// of a tile: the lanes are the half's tokens for the scores and head_dim's columns for the weighted
-// sum, and the two join at the end.  A token's scales multiply its score and its weight.
-// Bound by the latency of small problems and by reads of shared memory: four rows a warp use what it
-// reads of K and V four times, and products go two to an instruction where a lane's columns pair up
-// (head_dim a multiple of 64).  fp32, 1,500-token prefix, 48 requests of 8/2 heads of 64 with up to 80 COLD
-// tokens: 22.4 us with two rows a warp and 32-token tiles, 19.9 so, with the merge, at three CTAs an SM.
-constexpr int kRows = kGenericRows;
-constexpr int kTok = 64, kHalfTok = 32;
-constexpr int kWarpRows = 4;
-static_assert(kRows == 4 * kWarpRows && kTok % kGenericTile == 0, "eight warps: four row groups, two halves of a tile");
+// A CTA takes up to kGenericRows (16) query rows of one KV head and a run of tokens.  Its warps take the
+// run's 16-token tiles in turn, each all rows of its tiles, with a softmax state of its own; the states
+// join at the end.  A warp unpacks a tile into its own part of shared memory (its lanes hold the next
+// one's codes and scales meanwhile), so nothing in the loop waits for another warp.
+// A lane (x = lane % 8, y = lane / 8) has the scores of tokens x, x + 8 and rows y, y + 4, y + 8, y + 12, then the
+// sums of these rows over columns 4 (x + 8 k) .. + 3: what is read of shared memory serves 8 and 16 products an
+// element.  Products go two to an instruction, with no branch among them.  A token's scales multiply its score
+// and its weight.  Bound by latency in small problems, by issue in large ones.  fp32, 8/2 heads of 64, with the
+// merge: 1,500-token prefix, B = 48 16.5 us; 2,900 tokens, B = 64 26.8; 34 and 1,995 tokens, B = 4 9.7.  (With a warp's
+// lanes as tokens and four rows a warp, reads of shared memory took most of the time: 19.7, 39.0 and 12.5.)
+constexpr int kRows = kGenericRows, kTok = 16, kRowSets = 4;
+static_assert(kRows == 4 * kRowSets, "rows y + 4 i of lanes y");
+__host__ __device__ constexpr int generic_warps(int d) { return d <= 128 ? 8 : 4; }
 
-// floats: V [kTok][d], q [kRows][d], K [kTok][d + 4], weights [8][kTok / 2][kWarpRows], scales [2][kTok]
-__host__ __device__ inline int generic_smem(int d) {
-  return (int)sizeof(float) * (kTok * (d + 4) + kTok * d + kRows * d + 8 * kHalfTok * kWarpRows + 2 * kTok);
+// floats: q [kRows][d + 4]; a warp's K [kTok][d + 4] (then weights [kTok][kRows]) and V [kTok][d] (then, over both, its
+// sums [kRows][d]); the warps' maxima and row sums [warps][2][kRows]
+__host__ __device__ constexpr int generic_warp_floats(int d) { return kTok * (2 * d + 4); }
+__host__ __device__ constexpr int generic_smem(int d) {
+  return (int)sizeof(float) * (kRows * (d + 4) + generic_warps(d) * (generic_warp_floats(d) + 2 * kRows));
 }
 
 // slot_of(t): the token's slot, or -1 for one that does not count.
 template <typename T, int VPL, typename SlotOf, typename ReqOf, typename HeadOf, typename RecOf>
 __device__ __forceinline__ void kv8_generic_run(const AttnParams& p, int32_t j, int32_t t0, int32_t t1, int n_rows,
                                                 SlotOf slot_of, ReqOf req_of, HeadOf head_of, RecOf rec_of) {
-  constexpr int d = VPL * 32;
-  constexpr int kPer = VPL % 2 ? 1 : 2;  // neighbouring columns a lane takes
-  constexpr int kCols = VPL / kPer;      // column of (i, e): (lane + 32 i) * kPer + e
+  constexpr int d = VPL * 32, kWarps = generic_warps(d), kPer = kRows / kWarps;
   extern __shared__ __align__(16) float sm[];
-  float* sV = sm;                 // codes
-  float* sQ = sV + kTok * d;
-  float* sK = sQ + kRows * d;     // codes: 16-byte reads of eight tokens cover all banks
-  float4* sW = reinterpret_cast<float4*>(sK + kTok * (d + 4));
-  float* sScale = reinterpret_cast<float*>(sW + 8 * kHalfTok);  // of K (0: the token does not count), of V
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r0 = (warp & 3) * kWarpRows, half = warp >> 2;
-  float4* w_mine = sW + warp * kHalfTok;  // weights times the V scale of this warp's four rows, by token
-  for (int i = threadIdx.x; i < kRows * d; i += blockDim.x)
-    sQ[i] = i < n_rows * d ? (float)((const T*)p.q)[((int64_t)req_of(i / d) * p.n_q + head_of(i / d)) * d + i % d] * p.scale_log2 : 0.f;
-  int32_t rec[kWarpRows];  // looked up now, so that the loads finish during the tiles
+  const int x = lane & 7, y = lane >> 3;
+  float* sQ = sm;
+  float* sK = sQ + kRows * (d + 4) + warp * generic_warp_floats(d);
+  float* sV = sK + kTok * (d + 4);
+  float4* sP = reinterpret_cast<float4*>(sK);  // [kTok][4]: of lane y's rows
+  float* sState = sQ + kRows * (d + 4) + kWarps * generic_warp_floats(d);  // [warp][max, sum][row]
+  // q, and where the warp's rows go: rows warp, warp + kWarps, ..
+  int32_t rec[kPer];
 #pragma unroll
-  for (int r = 0; r < kWarpRows; ++r) rec[r] = half == 0 && r0 + r < n_rows ? rec_of(r0 + r) : -1;
-  float m[kWarpRows], l[kWarpRows], acc[kWarpRows][VPL];
+  for (int i = 0; i < kPer; ++i) {
+    const int r = warp + i * kWarps;
+    rec[i] = -1;
+    const T* q = nullptr;
+    if (r < n_rows) {
+      rec[i] = rec_of(r);
+      q = (const T*)p.q + ((int64_t)req_of(r) * p.n_q + head_of(r)) * d;
+    }
 #pragma unroll
-  for (int r = 0; r < kWarpRows; ++r) {
-    m[r] = -INFINITY;
-    l[r] = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) acc[r][i] = 0.f;
+    for (int c = 0; c < VPL; ++c) sQ[r * (d + 4) + lane + 32 * c] = q ? (float)q[lane + 32 * c] * p.scale_log2 : 0.f;
   }
-  // this thread's share of a tile: VPL pieces of eight codes, piece i of token (thread + 256 i) / (d / 8)
-  uint2 kw[VPL], vw[VPL];
-  float ks[VPL], vs[VPL];
+  // this lane's share of a tile: VPL pieces of 16 codes, piece i of token (lane + 32 i) / (d / 16), and the K
+  // (lanes below 16) or V scale of token lane % 16 (0 for one that does not count)
+  uint4 kw[VPL], vw[VPL];
+  float scale;
   auto load = [&](int32_t t) {
+    const int32_t mine = t + (lane & 15) < t1 ? slot_of(t + (lane & 15)) : -1;
+    const uint8_t* pool = (const uint8_t*)(lane < 16 ? p.kpool : p.vpool);
+    scale = mine < 0 ? 0.f : *reinterpret_cast<const float*>(pool + (int64_t)mine * p.kv8_row + (int64_t)p.n_kv * d + 4 * j);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int w = threadIdx.x + 256 * i, tok = w / (d / 8), c = w % (d / 8) * 8;
-      const int32_t slot = t + tok < t1 ? slot_of(t + tok) : -1;
-      kw[i] = vw[i] = make_uint2(0u, 0u);
-      ks[i] = vs[i] = 0.f;
+      const int w = lane + 32 * i;
+      const int32_t slot = __shfl_sync(0xffffffffu, mine, w / (d / 16));
+      kw[i] = vw[i] = make_uint4(0u, 0u, 0u, 0u);
       if (slot >= 0) {
-        const uint8_t* kr = (const uint8_t*)p.kpool + (int64_t)slot * p.kv8_row;
-        const uint8_t* vr = (const uint8_t*)p.vpool + (int64_t)slot * p.kv8_row;
-        kw[i] = *reinterpret_cast<const uint2*>(kr + (int64_t)j * d + c);
-        vw[i] = *reinterpret_cast<const uint2*>(vr + (int64_t)j * d + c);
-        if (c == 0) {
-          ks[i] = *reinterpret_cast<const float*>(kr + (int64_t)p.n_kv * d + 4 * j);
-          vs[i] = *reinterpret_cast<const float*>(vr + (int64_t)p.n_kv * d + 4 * j);
-        }
+        const int64_t at = (int64_t)slot * p.kv8_row + (int64_t)j * d + w % (d / 16) * 16;
+        kw[i] = *reinterpret_cast<const uint4*>((const uint8_t*)p.kpool + at);
+        vw[i] = *reinterpret_cast<const uint4*>((const uint8_t*)p.vpool + at);
       }
     }
   };
-  auto unpack = [](float* dst, uint2 w) {
-    float x[4];
-    e4m3x4_to_f32x4(w.x, x);
-    *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
-    e4m3x4_to_f32x4(w.y, x);
-    *reinterpret_cast<float4*>(dst + 4) = make_float4(x[0], x[1], x[2], x[3]);
+  // (the lanes of a store phase start at different pieces of theirs, which spreads them over the banks)
+  auto unpack = [lane](float* dst, const uint4& w) {
+    const bool odd = lane & 1, up = lane & 2;
+    const uint32_t a = odd ? w.y : w.x, b = odd ? w.x : w.y, c = odd ? w.w : w.z, e = odd ? w.z : w.w;
+    const uint32_t u[4] = {up ? c : a, up ? e : b, up ? a : c, up ? b : e};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float f[4];
+      e4m3x4_to_f32x4(u[i], f);
+      *reinterpret_cast<float4*>(dst + 4 * (i ^ (lane & 3))) = make_float4(f[0], f[1], f[2], f[3]);
+    }
   };
-  load(t0);
-  for (int32_t t = t0; t < t1; t += kTok) {
-    __syncthreads();  // the tile before is read
+  // the products, of the row sets that hold rows (y + 4 i for i < 1, 2 or 4), without a branch among them
+  auto with_sets = [&](auto f) {
+    if (n_rows <= 4) f(std::integral_constant<int, 1>{});
+    else if (n_rows <= 8) f(std::integral_constant<int, 2>{});
+    else f(std::integral_constant<int, kRowSets>{});
+  };
+  float m[kRowSets], l[kRowSets];
+  uint64_t o2[kRowSets][VPL][2];  // pairs of columns
+#pragma unroll
+  for (int i = 0; i < kRowSets; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) o2[i][k][0] = o2[i][k][1] = 0ull;  // 0.0f bit patterns
+  }
+  int32_t t = t0 + warp * kTok;
+  if (t < t1) load(t);
+  __syncthreads();  // q
+  for (; t < t1; t += kWarps * kTok) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int w = threadIdx.x + 256 * i, tok = w / (d / 8), c = w % (d / 8) * 8;
+      const int w = lane + 32 * i, tok = w / (d / 16), c = w % (d / 16) * 16;
       unpack(sK + tok * (d + 4) + c, kw[i]);
       unpack(sV + tok * d + c, vw[i]);
-      if (c == 0) {
-        sScale[tok] = ks[i];
-        sScale[kTok + tok] = vs[i];
-      }
     }
-    __syncthreads();
-    if (t + kTok < t1) load(t + kTok);
-    const int first = half * kHalfTok;  // of the warp's tokens in the tile
-    const int n_tok = min(kHalfTok, t1 - t - first);
-    if (r0 >= n_rows || n_tok <= 0) continue;
-    const float k_scale = sScale[first + lane], v_scale = sScale[kTok + first + lane];
-    const ulonglong2* q = reinterpret_cast<const ulonglong2*>(sQ + r0 * d);
-    const ulonglong2* kr = reinterpret_cast<const ulonglong2*>(sK + (first + lane) * (d + 4));
-    uint64_t s2[kWarpRows][2];  // two partial sums each
-#pragma unroll
-    for (int r = 0; r < kWarpRows; ++r) s2[r][0] = s2[r][1] = 0ull;  // 0.0f bit patterns
-#pragma unroll 4
-    for (int i = 0; i < d / 4; ++i) {
-      const ulonglong2 k = kr[i];
-#pragma unroll
-      for (int r = 0; r < kWarpRows; ++r) {
-        const ulonglong2 a = q[r * (d / 4) + i];
-        s2[r][0] = f2_fma(a.x, k.x, s2[r][0]);
-        s2[r][1] = f2_fma(a.y, k.y, s2[r][1]);
-      }
-    }
-    float s[kWarpRows], mx[kWarpRows], w[kWarpRows], sum[kWarpRows];
-#pragma unroll
-    for (int r = 0; r < kWarpRows; ++r) {
-      float x, y;
-      f2_unpack(f2_add(s2[r][0], s2[r][1]), x, y);
-      mx[r] = s[r] = k_scale != 0.f ? (x + y) * k_scale : -INFINITY;  // (a written row's scale is above 0)
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-      for (int r = 0; r < kWarpRows; ++r) mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], o));
-#pragma unroll
-    for (int r = 0; r < kWarpRows; ++r) {
-      const float mn = fmaxf(m[r], mx[r]);
-      const float base = mn == -INFINITY ? 0.f : mn;
-      const float a = exp2f(m[r] - base);
-      sum[r] = w[r] = exp2f(s[r] - base);
-      l[r] *= a;
-      m[r] = mn;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) acc[r][i] *= a;
-    }
-    w_mine[lane] = make_float4(w[0] * v_scale, w[1] * v_scale, w[2] * v_scale, w[3] * v_scale);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-      for (int r = 0; r < kWarpRows; ++r) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], o);
-#pragma unroll
-    for (int r = 0; r < kWarpRows; ++r) l[r] += sum[r];
+    const float ks[2] = {__shfl_sync(0xffffffffu, scale, x), __shfl_sync(0xffffffffu, scale, x + 8)};
+    const float vs[2] = {__shfl_sync(0xffffffffu, scale, x + 16), __shfl_sync(0xffffffffu, scale, x + 24)};
     __syncwarp();
-    const float* v_mine = sV + first * d;
-    if constexpr (kPer == 2) {
-      uint64_t o2[kWarpRows][kCols];
+    if (t + kWarps * kTok < t1) load(t + kWarps * kTok);
+    uint64_t s2[2][kRowSets];
 #pragma unroll
-      for (int r = 0; r < kWarpRows; ++r)
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) o2[r][i] = f2_pack(acc[r][2 * i], acc[r][2 * i + 1]);
+      for (int i = 0; i < kRowSets; ++i) s2[u][i] = 0ull;
+    const ulonglong2* k0 = reinterpret_cast<const ulonglong2*>(sK + x * (d + 4));
+    const ulonglong2* k1 = reinterpret_cast<const ulonglong2*>(sK + (x + 8) * (d + 4));
+    const ulonglong2* q0 = reinterpret_cast<const ulonglong2*>(sQ + y * (d + 4));
+    with_sets([&](auto n) {
 #pragma unroll 4
-      for (int tok = 0; tok < n_tok; ++tok) {
-        const float4 x = w_mine[tok];
-        const uint64_t x2[kWarpRows] = {f2_pack(x.x, x.x), f2_pack(x.y, x.y), f2_pack(x.z, x.z), f2_pack(x.w, x.w)};
+      for (int c = 0; c < d / 4; ++c) {
+        const ulonglong2 a = k0[c], b = k1[c];
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) {
-          const uint64_t v = *reinterpret_cast<const uint64_t*>(v_mine + tok * d + (lane + 32 * i) * 2);
-#pragma unroll
-          for (int r = 0; r < kWarpRows; ++r) o2[r][i] = f2_fma(x2[r], v, o2[r][i]);
+        for (int i = 0; i < n; ++i) {
+          const ulonglong2 q = q0[i * (d + 4) + c];  // (4 rows of d + 4 floats are d + 4 pieces)
+          s2[0][i] = f2_fma(q.y, a.y, f2_fma(q.x, a.x, s2[0][i]));
+          s2[1][i] = f2_fma(q.y, b.y, f2_fma(q.x, b.x, s2[1][i]));
         }
       }
+    });
+    __syncwarp();  // K is read: the weights take its place
+    float w0[kRowSets], w1[kRowSets], alpha[kRowSets];
+    bool moved = false;
 #pragma unroll
-      for (int r = 0; r < kWarpRows; ++r)
+    for (int i = 0; i < kRowSets; ++i) {
+      float lo, hi;
+      f2_unpack(s2[0][i], lo, hi);
+      w0[i] = ks[0] != 0.f ? (lo + hi) * ks[0] : -INFINITY;  // (a written row's scale is above 0)
+      f2_unpack(s2[1][i], lo, hi);
+      w1[i] = ks[1] != 0.f ? (lo + hi) * ks[1] : -INFINITY;
+      float mx = fmaxf(w0[i], w1[i]);
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) f2_unpack(o2[r][i], acc[r][2 * i], acc[r][2 * i + 1]);
-    } else {
-#pragma unroll 4
-      for (int tok = 0; tok < n_tok; ++tok) {
-        const float4 x = w_mine[tok];
+      for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float mn = fmaxf(m[i], mx), base = mn == -INFINITY ? 0.f : mn;
+      alpha[i] = exp2f(m[i] - base);
+      moved = moved || mn != m[i];
+      m[i] = mn;
+      w0[i] = exp2f(w0[i] - base);
+      w1[i] = exp2f(w1[i] - base);
+      l[i] = l[i] * alpha[i] + (w0[i] + w1[i]);  // this lane's tokens; the lanes' sums are added at the end
+    }
+    sP[x * 4 + y] = make_float4(w0[0] * vs[0], w0[1] * vs[0], w0[2] * vs[0], w0[3] * vs[0]);
+    sP[(x + 8) * 4 + y] = make_float4(w1[0] * vs[1], w1[1] * vs[1], w1[2] * vs[1], w1[3] * vs[1]);
+    if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          const float v = v_mine[tok * d + lane + 32 * i];
-          acc[0][i] += x.x * v;
-          acc[1][i] += x.y * v;
-          acc[2][i] += x.z * v;
-          acc[3][i] += x.w * v;
+      for (int i = 0; i < kRowSets; ++i) {
+        const uint64_t a2 = f2_pack(alpha[i], alpha[i]);
+#pragma unroll
+        for (int k = 0; k < VPL; ++k) {
+          o2[i][k][0] = f2_mul(o2[i][k][0], a2);
+          o2[i][k][1] = f2_mul(o2[i][k][1], a2);
         }
       }
     }
-    __syncwarp();  // the weights are read
-  }
-  // the second halves' states go to shared memory (K and V are read), the first join them
-  __syncthreads();
-  float* other = sV + (warp & 3) * (kWarpRows * (d + 2));  // [kWarpRows][d], then the maxima and sums
-  if (half == 1 && r0 < n_rows) {
+    __syncwarp();
+    with_sets([&](auto n) {
+#pragma unroll 4
+      for (int tok = 0; tok < kTok; ++tok) {  // (a token that does not count has weight 0 and V 0)
+        const float4 w = sP[tok * 4 + y];
+        const uint64_t w2[kRowSets] = {f2_pack(w.x, w.x), f2_pack(w.y, w.y), f2_pack(w.z, w.z), f2_pack(w.w, w.w)};
 #pragma unroll
-    for (int r = 0; r < kWarpRows; ++r) {
+        for (int k = 0; k < VPL; ++k) {
+          const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(sV + tok * d + (x + 8 * k) * 4);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) other[r * d + i * 32 + lane] = acc[r][i];
-      if (lane == 0) {
-        other[kWarpRows * d + r] = m[r];
-        other[kWarpRows * (d + 1) + r] = l[r];
+          for (int i = 0; i < n; ++i) {
+            o2[i][k][0] = f2_fma(w2[i], v.x, o2[i][k][0]);
+            o2[i][k][1] = f2_fma(w2[i], v.y, o2[i][k][1]);
+          }
+        }
       }
+    });
+    __syncwarp();  // the tile is read
+  }
+  // the warps' states meet in shared memory, each warp's sums in its own tile's place
+#pragma unroll
+  for (int i = 0; i < kRowSets; ++i) {
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+#pragma unroll
+    for (int k = 0; k < VPL; ++k)
+      *reinterpret_cast<ulonglong2*>(sK + (y + 4 * i) * d + (x + 8 * k) * 4) = make_ulonglong2(o2[i][k][0], o2[i][k][1]);
+    if (x == 0) {
+      sState[warp * 2 * kRows + y + 4 * i] = m[i];
+      sState[warp * 2 * kRows + kRows + y + 4 * i] = l[i];
     }
   }
   __syncthreads();
-  if (half == 1) return;
+  const float* sums = sQ + kRows * (d + 4);
 #pragma unroll
-  for (int r = 0; r < kWarpRows; ++r) {
-    if (r0 + r >= n_rows) break;
-    if (rec[r] < 0 || rec[r] >= p.n_records) {
+  for (int i = 0; i < kPer; ++i) {
+    const int r = warp + i * kWarps;
+    if (r >= n_rows) break;
+    if (rec[i] < 0 || rec[i] >= p.n_records) {
       if (lane == 0) latch(p.err, kDevBadRecord);
       continue;
     }
-    const float m1 = other[kWarpRows * d + r], l1 = other[kWarpRows * (d + 1) + r];
-    const float mn = fmaxf(m[r], m1), base = mn == -INFINITY ? 0.f : mn;
-    const float a0 = exp2f(m[r] - base), a1 = exp2f(m1 - base);
-    const float sum = l[r] * a0 + l1 * a1;
-    const int64_t at = (int64_t)rec[r] * p.n_q + head_of(r0 + r);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    float* dst = p.rec_o + at * d;
+    float top = -INFINITY, total = 0.f, o[VPL];
 #pragma unroll
-    for (int i = 0; i < kCols; ++i)
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sState[w * 2 * kRows + r]);
+    const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
-      for (int e = 0; e < kPer; ++e)
-        dst[(lane + 32 * i) * kPer + e] = (acc[r][i * kPer + e] * a0 + other[r * d + (i * kPer + e) * 32 + lane] * a1) * inv;
-    if (lane == 0) p.rec_lse[at] = kv8_record_lse(sum, (mn + log2f(sum)) * kLn2);
+    for (int c = 0; c < VPL; ++c) o[c] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float a = exp2f(sState[w * 2 * kRows + r] - base);
+      total += sState[w * 2 * kRows + kRows + r] * a;
+#pragma unroll
+      for (int c = 0; c < VPL; ++c) o[c] += sums[w * generic_warp_floats(d) + r * d + lane + 32 * c] * a;
+    }
+    const int64_t at = (int64_t)rec[i] * p.n_q + head_of(r);
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+    for (int c = 0; c < VPL; ++c) p.rec_o[at * d + lane + 32 * c] = o[c] * inv;
+    if (lane == 0) p.rec_lse[at] = kv8_record_lse(total, (base + log2f(total)) * kLn2);
   }
 }
 
 // CTAs [0, n_prefix) take prefix items first_item.., the rest (suffix item, KV head, block of kRows of
 // its query heads): one launch, so that short prefixes and suffixes share the SMs.
 template <typename T, int VPL>
-__global__ void __launch_bounds__(256, VPL <= 2 ? 3 : VPL <= 6 ? 2 : 1) kv8_generic_kernel(AttnParams p, int32_t first_item, int32_t n_prefix) {
+__global__ void __launch_bounds__(generic_warps(32 * VPL) * 32, VPL <= 1 ? 3 : VPL <= 2 ? 2 : 1) kv8_generic_kernel(AttnParams p, int32_t first_item, int32_t n_prefix) {
   // (the plan is not written by the work before this kernel; everything else waits for that work)
   if ((int32_t)blockIdx.x < n_prefix) {
     const DevPrefixItem it = p.pitems[first_item + blockIdx.x];
@@ -523,7 +531,7 @@ cudaError_t launch_kv8_generic(int32_t dtype, const AttnParams& p, int32_t first
     auto kernel = dtype == 1 ? kv8_generic_kernel<__nv_bfloat16, n> : kv8_generic_kernel<float, n>;
     cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
-    return launch_kernel(kernel, dim3((unsigned)ctas), dim3(256), (size_t)smem, s, pdl, p, first_item, n_items);
+    return launch_kernel(kernel, dim3((unsigned)ctas), dim3(generic_warps(32 * n) * 32), (size_t)smem, s, pdl, p, first_item, n_items);
   });
 }
 
