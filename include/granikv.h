@@ -135,9 +135,9 @@ granikv_status granikv_destroy(granikv_ctx* ctx);
  * scales, padding to a multiple of 16 bytes; value = code * scale.  cfg->dtype is the type of q, o
  * and of the K/V rows given to granikv_hot_fill, granikv_cold_append and
  * granikv_decode_attention_append, which quantise them:
- *     scale = max(amax, 2^-96) / 448,   code = e4m3(x * (448 / max(amax, 2^-96))),
- * both in float32, rounded to nearest even and saturated at +-448 (an infinity becomes +-448, a
- * NaN stays one); amax is the largest finite magnitude of the head's elements over a block of
+ *     scale = max(amax, 2^-96) / 448 in float32,   code = e4m3(x * 448 / max(amax, 2^-96)),
+ * the exact quotient rounded once, to nearest even, and saturated at +-448 (an infinity becomes
+ * +-448, a NaN stays one); amax is the largest finite magnitude of the head's elements over a block of
  * tokens: 64 consecutive tokens of a slab, counted from its start (the last block may be
  * shorter), whose rows all hold the block's scale, or one COLD token (page size 1).
  * Those rows and q and o must start on 16-byte boundaries (GRANIKV_ERR_INVALID).

@@ -1,7 +1,8 @@
 """CPU restatements for the 8-bit cache and the eviction of COLD tokens.  TEST INFRASTRUCTURE ONLY.
 
-Quantising follows the definition in float32 (the operations that decide a code are correctly
-rounded, so codes and scales can be compared bit for bit); attention over the cache is that of
+Quantising rounds each exact quotient once (a float64 quotient of float32 values is halfway between two
+codes only if the exact one is: codes have 4 significant bits), so codes and scales can be compared
+bit for bit; attention over the cache is that of
 ``oracle.attention`` on the dequantised values in float64.
 """
 
@@ -32,9 +33,9 @@ _VALUES = e4m3_values()
 
 
 def e4m3_codes(x: np.ndarray) -> np.ndarray:
-    """Nearest code of float32 values: ties to the even code, saturated at +-448, NaN 0x7f."""
-    x = np.asarray(x, dtype=np.float32)
-    a = np.abs(x).astype(np.float64)
+    """Nearest code of values held in float64: ties to the even code, saturated at +-448, NaN 0x7f."""
+    x = np.asarray(x, dtype=np.float64)
+    a = np.abs(x)
     grid = _VALUES[:127]  # the non-negative finite values, ascending
     with np.errstate(invalid="ignore"):
         hi = np.clip(np.searchsorted(grid, a), 1, 126)
@@ -57,7 +58,7 @@ def quantise(x: np.ndarray, block: int) -> Tuple[np.ndarray, np.ndarray]:
         amax[t:t + block] = amax[t:t + block].max(axis=0)
     amax = np.maximum(amax, AMAX_MIN)
     with np.errstate(invalid="ignore", over="ignore"):
-        codes = e4m3_codes(x * (E4M3_MAX / amax)[..., None])
+        codes = e4m3_codes(x.astype(np.float64) * 448.0 / amax.astype(np.float64)[..., None])
     return codes, amax / E4M3_MAX
 
 

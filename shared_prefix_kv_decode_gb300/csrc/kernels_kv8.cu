@@ -22,17 +22,25 @@ template <>
 struct Piece<__nv_bfloat16> {
   static constexpr int kElems = 8;
   uint4 w;
-  __device__ __forceinline__ void store(uint8_t* dst, float inv) const {
-    const uint64_t inv2 = f2_pack(inv, inv);
-    auto codes = [&](uint32_t x) {
+  // (kv8_quotient, two elements to an instruction)
+  __device__ __forceinline__ void store(uint8_t* dst, const Kv8Divisor& by, bool finite) const {
+    const uint64_t f2 = f2_pack(by.minus_f, by.minus_f), inv2 = f2_pack(by.minus_inv, by.minus_inv), a2 = f2_pack(by.a, by.a);
+    auto codes = [&](uint32_t w) {
+      const float x = __uint_as_float(w << 16), y = __uint_as_float(w & 0xffff0000u);
       float a, b;
-      f2_unpack(f2_mul(f2_pack(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)), inv2), a, b);
+      if (finite) {
+        const uint64_t n = f2_mul(f2_pack(x, y), f2), q0 = f2_mul(n, inv2), r = f2_fma(q0, a2, n);
+        f2_unpack(f2_fma(r, inv2, q0), a, b);
+      } else {
+        a = kv8_quotient<__nv_bfloat16>(x, by);
+        b = kv8_quotient<__nv_bfloat16>(y, by);
+      }
       return (uint32_t)f32x2_to_e4m3x2(a, b);
     };
     *reinterpret_cast<uint2*>(dst) = make_uint2(codes(w.x) | codes(w.y) << 16, codes(w.z) | codes(w.w) << 16);
   }
   template <int N>
-  __device__ static __forceinline__ float amax_of(const Piece (&x)[N]) {
+  __device__ static __forceinline__ float amax_of(const Piece (&x)[N], bool& finite) {
     // magnitudes order as their bits do, two to a word; only where one is not finite are they told apart
     uint32_t m = 0u;
 #pragma unroll
@@ -42,7 +50,8 @@ struct Piece<__nv_bfloat16> {
     }
     const uint32_t top = max(m & 0xffffu, m >> 16);
     float amax = __uint_as_float(top << 16);
-    if (top >= 0x7f80u) {
+    finite = top < 0x7f80u;
+    if (!finite) {
       amax = 0.f;
 #pragma unroll
       for (int c = 0; c < N; ++c)
@@ -56,12 +65,12 @@ template <>
 struct Piece<float> {
   static constexpr int kElems = 4;
   uint4 w;
-  __device__ __forceinline__ void store(uint8_t* dst, float inv) const {
-    *reinterpret_cast<uint32_t*>(dst) = f32x4_to_e4m3x4(__uint_as_float(w.x) * inv, __uint_as_float(w.y) * inv,
-                                                        __uint_as_float(w.z) * inv, __uint_as_float(w.w) * inv);
+  __device__ __forceinline__ void store(uint8_t* dst, const Kv8Divisor& by, bool) const {
+    auto q = [&](uint32_t u) { return kv8_quotient<float>(__uint_as_float(u), by); };
+    *reinterpret_cast<uint32_t*>(dst) = f32x4_to_e4m3x4(q(w.x), q(w.y), q(w.z), q(w.w));
   }
   template <int N>
-  __device__ static __forceinline__ float amax_of(const Piece (&x)[N]) {
+  __device__ static __forceinline__ float amax_of(const Piece (&x)[N], bool&) {
     float amax = 0.f;
 #pragma unroll
     for (int c = 0; c < N; ++c)
@@ -74,9 +83,9 @@ struct Piece<float> {
 // One block of kKv8Block slab tokens of one KV head (the heads of a block are neighbours in the grid, so
 // that its rows are read and written whole at about the same time), of K (blockIdx.y = 0) or V.  The block stays in
 // registers between its amax and its codes (pieces of 16 bytes, all of a thread's requested at once), so
-// the rows are read once: 3 bytes moved for each bf16 element (16K tokens of 8 x 128: 17.5 us at six CTAs an
-// SM; its 100 MB take 14.9).  What it costs beyond HBM is issue: with head_dim at run time, the pieces'
-// places cost two divisions each, the warps issued in 77 % of the cycles, and it took 23.2 us.
+// the rows are read once: 3 bytes moved for each bf16 element (16K tokens of 8 x 128: 18.7 us at six CTAs an
+// SM; its 100 MB take 14.9).  What it costs beyond HBM is issue: 17.4 us with one product an element in place of
+// the quotient (which rounds twice), 23.2 with head_dim at run time (two divisions for each piece's place).
 template <typename T, int D>
 __global__ void __launch_bounds__(256, sizeof(T) * D <= 256 ? 6 : 1) kv8_fill_kernel(
     const T* __restrict__ k, const T* __restrict__ v, int32_t L_p, uint8_t* __restrict__ kpool,
@@ -96,20 +105,22 @@ __global__ void __launch_bounds__(256, sizeof(T) * D <= 256 ? 6 : 1) kv8_fill_ke
     x[c].w = t < n ? __ldcs(reinterpret_cast<const uint4*>(src + t * (n_kv * D) + idx % kPerRow * kElems))
                    : make_uint4(0u, 0u, 0u, 0u);
   }
-  float amax = Piece<T>::amax_of(x);
+  bool finite = true;  // this thread's elements
+  float amax = Piece<T>::amax_of(x, finite);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = amax;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < 8; ++w) amax = fmaxf(amax, s_max[w]);
-  const float inv = kv8_inverse(amax), scale = kv8_scale(amax);
+  const Kv8Divisor by = kv8_divisor(amax);
+  const float scale = kv8_scale(amax);
   const int32_t row = (int32_t)kv8_row_bytes(n_kv, D);
   uint8_t* dst = (blockIdx.y ? vpool : kpool) + (first_slot + t0) * row;
 #pragma unroll
   for (int c = 0; c < kPieces; ++c) {
     const int32_t idx = threadIdx.x + c * 256, t = idx / kPerRow;
-    if (t < n) x[c].store(dst + t * row + j * D + idx % kPerRow * kElems, inv);
+    if (t < n) x[c].store(dst + t * row + j * D + idx % kPerRow * kElems, by, finite);
   }
   for (int32_t t = threadIdx.x; t < n; t += 256) *reinterpret_cast<float*>(dst + t * row + n_kv * D + 4 * j) = scale;
 }
@@ -128,16 +139,17 @@ __device__ __forceinline__ void kv8_write_row(const T* __restrict__ src, uint8_t
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const float inv = kv8_inverse(amax);
+  const Kv8Divisor by = kv8_divisor(amax);
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) x[i] = kv8_quotient<T>(x[i], by);
   uint8_t* dst = slot_row + (int64_t)j * d + lane * VPL;
   if constexpr (VPL % 4 == 0) {
 #pragma unroll
     for (int i = 0; i < VPL; i += 4)
-      *reinterpret_cast<uint32_t*>(dst + i) =
-          f32x4_to_e4m3x4(x[i] * inv, x[i + 1] * inv, x[i + 2] * inv, x[i + 3] * inv);
+      *reinterpret_cast<uint32_t*>(dst + i) = f32x4_to_e4m3x4(x[i], x[i + 1], x[i + 2], x[i + 3]);
   } else {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) dst[i] = (uint8_t)f32x2_to_e4m3x2(x[i] * inv, 0.f);
+    for (int i = 0; i < VPL; ++i) dst[i] = (uint8_t)f32x2_to_e4m3x2(x[i], 0.f);
   }
   if (lane == 0) *reinterpret_cast<float*>(slot_row + (int64_t)n_kv * d + 4 * j) = kv8_scale(amax);
 }

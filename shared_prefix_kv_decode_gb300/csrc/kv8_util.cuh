@@ -95,6 +95,41 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a < INFINITY ? a : 0.f;
 }
 __device__ __forceinline__ float kv8_scale(float amax) { return fmaxf(amax, kKv8AmaxMin) / kE4m3Max; }
-__device__ __forceinline__ float kv8_inverse(float amax) { return kE4m3Max / fmaxf(amax, kKv8AmaxMin); }
+
+// x * 448 / amax, such that its conversion to e4m3 is the nearest code of the exact quotient: with a the
+// significand of amax and f = 448 over its power of two (exact), the quotient of x f and a.  One
+// Newton step on the approximate quotient makes it the correctly rounded one of what it divides.
+// bf16: x f is exact (8 + 3 bits), and the exact quotient is either halfway between two codes, then it is
+// q itself, or 2^-13 or more away from that.
+// fp32: x f takes 27 bits, in two parts; the exact quotient may lie closer to a halfway point than
+// fp32 resolves, so q is rounded to odd: of the two neighbours of a quotient that fp32 does not hold, the
+// one with an odd last bit, which lies on its side of every halfway point.
+// An x that is not finite gives itself.
+// (The signs are such that the last sum keeps that of a zero.)
+struct Kv8Divisor {
+  float minus_f, a, minus_inv;
+};
+__device__ __forceinline__ Kv8Divisor kv8_divisor(float amax) {
+  const uint32_t u = __float_as_uint(fmaxf(amax, kKv8AmaxMin));
+  const float a = __uint_as_float((u & 0x7fffffu) | 0x3f800000u);
+  return {-__uint_as_float(((262u - (u >> 23)) << 23) | 0x600000u), a, -1.f / a};  // 1.75 * 2^(8 - exponent)
+}
+template <typename T>
+__device__ __forceinline__ float kv8_quotient(float x, const Kv8Divisor& by);
+template <>
+__device__ __forceinline__ float kv8_quotient<__nv_bfloat16>(float x, const Kv8Divisor& by) {
+  const float n = x * by.minus_f, q0 = n * by.minus_inv, r = fmaf(q0, by.a, n);
+  return r == r ? fmaf(r, by.minus_inv, q0) : x;
+}
+template <>
+__device__ __forceinline__ float kv8_quotient<float>(float x, const Kv8Divisor& by) {
+  const float n = x * by.minus_f, low = fmaf(x, by.minus_f, -n), q0 = n * by.minus_inv;
+  const float r = fmaf(q0, by.a, n) + low;
+  if (!(r == r)) return x;
+  const float q = fmaf(r, by.minus_inv, q0), over = fmaf(q, by.a, n) + low;  // q a - x f
+  uint32_t u = __float_as_uint(q);
+  if (over != 0.f && q != 0.f && !(u & 1u)) u = (over < 0.f) == (q > 0.f) ? u + 1u : u - 1u;
+  return __uint_as_float(u);
+}
 
 }  // namespace granikv

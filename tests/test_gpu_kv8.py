@@ -237,6 +237,52 @@ def test_token_write_is_bit_exact(cuda_ok, n_kv, d, dtype, N):
         assert (rest == 0xFF).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("slab", [False, True])
+def test_write_next_to_halfway_points(cuda_ok, dtype, slab):
+    """Elements on, and a few last places beside, the halfway points of two codes, for many scales."""
+    torch, gb, rng = _torch(), _gb(), np.random.default_rng(27)
+    grid = K8.e4m3_values()[:127]
+    mids = np.concatenate([(grid[:-1] + grid[1:]) / 2, [0.0, 2.0 ** -10, 1e-30]])
+    amax = np.concatenate([2.0 ** rng.uniform(-90, 100, 150), rng.uniform(0.5, 4.0, 300), [2.0 ** -96, 1.0, 3.3e38, 1.75]])
+    if dtype == "bf16":
+        amax = torch.from_numpy(amax.astype(np.float32)).to(torch.bfloat16).float().numpy().astype(np.float64)
+    amax = amax.astype(np.float32)
+    x = (mids[None] * amax[:, None].astype(np.float64) / 448.0).astype(np.float32)
+    step = 1 if dtype == "f32" else 1 << 16
+    u = (x.view(np.int32)[:, None] // step + rng.integers(-3, 4, (len(amax), 7, 1))) * step  # last places of the type
+    x = np.maximum(u, 0).astype(np.int32).view(np.float32).reshape(len(amax), -1)
+    x = np.where(np.isfinite(x), np.minimum(x, amax[:, None]), 0.0) * rng.choice([-1.0, 1.0], x.shape)
+    n, d, block = len(amax), 256, K8.BLOCK if slab else 1
+    heads = np.zeros((n, 4, d), dtype=np.float32)
+    heads[:, :, 0] = amax[:, None]
+    heads[:, :, 1:] = np.pad(x, ((0, 0), (0, 4 * (d - 1) - x.shape[1]))).reshape(n, 4, d - 1)
+    if slab:
+        heads[:, :, 0] = 0.0
+        heads = np.clip(heads / amax[:, None, None], -1, 1).astype(np.float32) * np.float32(1.6171875)
+        heads[::block, :, 0] = 1.6171875
+    c = Kv8(rng, n_q=4, n_kv=4, d=d, dtype=dtype)
+    heads = c.to(heads).float().cpu().numpy()
+    n_slots = n + 40
+    pools = [torch.full((n_slots, c.row), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    n_hot = n + 10 if slab else 10
+    ctx = gb.Context(n_layers=1, n_q=4, n_kv=4, head_dim=d, dtype=c.ctx.dtype, n_slots=n_slots, k_pools=[pools[0]], v_pools=[pools[1]],
+                     hot_fraction=(n_hot + 0.5) / n_slots, kv8=True)
+    if slab:
+        sid, at = ctx.hot_alloc(n)
+        ctx.hot_fill(0, sid, c.to(heads), c.to(heads))
+        slots = np.arange(at, at + n)
+    else:
+        slots = (10 + rng.permutation(n_slots - 10)[:n]).astype(np.int32)
+        ctx.cold_append(0, c.to(heads), c.to(heads), torch.from_numpy(slots).cuda(), n)
+    ctx.sync_status()
+    codes, scales = K8.quantise(heads, block)
+    for pool in pools:
+        got = pool.cpu().numpy()[slots]
+        assert np.array_equal(got[:, : 4 * d].reshape(n, 4, d), codes)
+        assert np.array_equal(got[:, 4 * d : 4 * (d + 4)].copy().view(np.float32), scales)
+
+
 def test_token_write_refuses_bad_slots(cuda_ok):
     torch, gb, rng = _torch(), _gb(), np.random.default_rng(5)
     c = Kv8(rng, n_q=2, n_kv=2, d=64, dtype="bf16", prefixes=[10])
