@@ -241,7 +241,7 @@ __device__ __forceinline__ void kv8_generic_run(const AttnParams& p, int32_t j, 
       q = (const T*)p.q + ((int64_t)req_of(r) * p.n_q + head_of(r)) * d;
     }
 #pragma unroll
-    for (int c = 0; c < VPL; ++c) sQ[r * (d + 4) + lane + 32 * c] = q ? (float)q[lane + 32 * c] * p.scale_log2 : 0.f;
+    for (int c = 0; c < VPL; ++c) sQ[r * (d + 4) + lane + 32 * c] = q ? q_no_inf((float)q[lane + 32 * c]) * p.scale_log2 : 0.f;
   }
   // this lane's share of a tile: VPL pieces of 16 codes, piece i of token (lane + 32 i) / (d / 16), and the K
   // (lanes below 16) or V scale of token lane % 16 (0 for one that does not count)

@@ -318,11 +318,7 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
     uint32_t hi[16], lo[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      __half2 x = f16x2_of(qw[2 * k], f), y = f16x2_of(qw[2 * k + 1], f);
-      // an infinity becomes NaN, as the scores it stands in would end
-      const __half2 zero = __floats2half2_rn(0.f, 0.f);
-      x = __hfma2(zero, x, x);
-      y = __hfma2(zero, y, y);
+      const __half2 x = q_no_inf(f16x2_of(qw[2 * k], f)), y = q_no_inf(f16x2_of(qw[2 * k + 1], f));
       hi[k] = f16x4_to_e4m3x4(x, y);
       uint32_t u, v;
       e4m3x4_to_f16x4(hi[k], u, v);

@@ -246,6 +246,11 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
     load_q(sg + 1);
     float unit;
     q_to_f16<16>(qf, unit);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const __half2 x = q_no_inf(*reinterpret_cast<const __half2*>(&qf[i]));
+      qf[i] = *reinterpret_cast<const uint32_t*>(&x);
+    }
     const float f0 = __shfl_sync(0xffffffffu, unit, 8 * c) * p.scale_log2;
     const float f1 = __shfl_sync(0xffffffffu, unit, 8 * c + 4) * p.scale_log2;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;

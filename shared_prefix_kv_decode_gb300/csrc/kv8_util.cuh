@@ -82,6 +82,10 @@ __device__ __forceinline__ void q_to_f16(uint32_t* w, float& unit) {
 #pragma unroll
   for (int i = 0; i < W; ++i) w[i] = bf16x2_to_f16x2(w[i], f);
 }
+// q as the attention kernels take it: an infinity becomes NaN (0 * inf; a NaN stays one, 0 * x + x is any other x).
+// The scores of an infinity may all be -inf, which looks like a row without keys.
+__device__ __forceinline__ float q_no_inf(float x) { return fmaf(0.f, x, x); }
+__device__ __forceinline__ __half2 q_no_inf(__half2 x) { return __hfma2(__floats2half2_rn(0.f, 0.f), x, x); }
 
 // A partial row's log-sum-exp as the merge takes it: -inf for a row without weight, +inf for one whose
 // weights hold a NaN (the merge's maximum passes over a NaN; +inf makes the whole row NaN).

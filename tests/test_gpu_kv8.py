@@ -648,3 +648,26 @@ def test_cache_in_8_bits_with_prefix_lifecycle(cuda_ok):
     c.cv = [np.concatenate([pv[min(b, 1)], tv[at[b]:at[b + 1]], tv[len(tv) - 3 + b][None]]) for b in range(3)]
     c.q_host = q.double().cpu().numpy()
     c.check(o, lse, "cache")
+
+
+@pytest.mark.parametrize("n_q,n_kv,d,dtype", [(32, 8, 128, "bf16"), (24, 2, 128, "bf16"), (9, 3, 96, "bf16"), (8, 2, 64, "f32")])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("backend", ["dense", "cascade"])
+def test_decode_infinite_query_over_keys_of_one_sign(cuda_ok, n_q, n_kv, d, dtype, bad, backend):
+    """Every K has the same sign in the dimension where q is infinite, so all scores of the head are -inf
+    (or all +inf): its row is NaN all the same, with and without a slab, down to one token."""
+    torch, gb = _torch(), _gb()
+
+    def edit(kind, k, v):
+        k[:, :, 7] = -np.abs(k[:, :, 7]) - 1.0
+
+    c = Kv8(np.random.default_rng([n_q, d]), n_q=n_q, n_kv=n_kv, d=d, dtype=dtype, prefixes=[150], of=[0, -1, -1, 0], lens=[20, 1, 70, 0],
+            edit=edit, backend=gb.BACKEND_DENSE if backend == "dense" else gb.BACKEND_CASCADE)
+    o, lse = c.decode()
+    hit = torch.zeros_like(lse, dtype=torch.bool)
+    for b, h in ((0, 1), (1, 0), (2, n_q - 1), (3, 2)):
+        c.q[b, h, 7] = bad
+        hit[b, h] = True
+    o2, lse2 = c.decode()
+    assert torch.equal(torch.isnan(lse2), hit) and torch.isnan(o2[hit]).all()
+    assert torch.equal(o2[~hit], o[~hit]) and torch.equal(lse2[~hit], lse[~hit])
