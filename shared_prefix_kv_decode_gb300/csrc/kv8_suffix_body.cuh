@@ -7,12 +7,15 @@
 //     O^T[128 x 8]   += V^T[128 x 16 tok] . P^T[16 tok x 8]  (8 mma.m16n8k16, fp16)
 // Number format.  Codes become fp16 exactly (one conversion per pair, on the way from ldmatrix to
 // the MMA); q is brought into fp16's range by a power of two per query head (exact but for elements
-// 2^-31 below the row's largest).  With ks, vs the token's scales and z = s ks + log2 vs (base 2), the running
-// maximum m is taken over z, P = 2^(z - m) is what meets the V codes (p times vs), and the row sum
-// adds P / vs = 2^(s ks - m): scales cost one FMA per score and one per weight, and a token with a
-// small V scale cannot push the weights of the others out of fp16's range.  P carries a factor of
+// 2^-31 below the row's largest).  With ks, vs the token's scales, y = s ks and z = y + log2 vs (base 2), the
+// running maximum m is taken over z and P = 2^(z - m) is what meets the V codes (p times vs), so a token with
+// a small V scale cannot push the weights of the others out of fp16's range.  P carries a factor of
 // 2^14 (it is at most 2^14), so that fp16 keeps its 11 bits down to weights of 2^-28; m, the sums and
 // O are fp32.
+// The row sum adds 2^(y - m + 10).  A scale lies between 2^-104.9 (of zeros) and 2^119.2, so y - m is at most 104.9, and
+// the 4,096 tokens a CTA may have sum to less than 2^127; the heaviest token has y - m of -119.2 or more, so what it
+// adds is a normal number, and a weight down to 2^-40 of it a subnormal one.  (P / vs in place of this exponential
+// would lose the tokens whose P underflows, and with P's factor overflow on 600 zero rows.)
 // ldmatrix moves 16-bit pairs, here two codes: a lane's 4 codes of a row serve one k-step of S^T in
 // a permuted order of head_dim (q is loaded in the same order), and the transposed form gives two
 // tokens x two dims, which one byte permutation turns into the two A registers of O^T's dims 2 r
@@ -62,6 +65,8 @@ static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 static_assert(kRowStride % 128 == 48, "ldmatrix bank groups");
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kShift = 14.f;                     // log2 of the factor that P carries
+constexpr float kSumShift = 10.f;                  // and that the row sum does
+static_assert(kSuffixMaxCtaTokens <= 4096, "the row sum's range");
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // Source of the rows of masked tokens (zero-initialised at module load, never written).
@@ -303,22 +308,18 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
       }
       const int rem = seg.t1 - t;  // valid tokens from the first tile on
       float mx0 = -INFINITY, mx1 = -INFINITY;
-      float ia[V], ib[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float va = la[v], vb = lb[v];
-        la[v] = lg2_approx(va);
-        lb[v] = lg2_approx(vb);
-        // P / vs below uses the very logarithm that P does, so its rounding does not reach the row
-        // sum (the zero row of a token that does not count has scale 0, and adds nothing)
-        ia[v] = va > 0.f ? ex2_approx(-la[v]) : 0.f;
-        ib[v] = vb > 0.f ? ex2_approx(-lb[v]) : 0.f;
-        s[v][0] = v * kTile + r < rem ? (s[v][0] + s2[v][0]) * (f0 * sa[v]) + la[v] : -INFINITY;
-        s[v][1] = v * kTile + r < rem ? (s[v][1] + s2[v][1]) * (f1 * sa[v]) + la[v] : -INFINITY;
-        s[v][2] = v * kTile + r + 8 < rem ? (s[v][2] + s2[v][2]) * (f0 * sb[v]) + lb[v] : -INFINITY;
-        s[v][3] = v * kTile + r + 8 < rem ? (s[v][3] + s2[v][3]) * (f1 * sb[v]) + lb[v] : -INFINITY;
-        mx0 = max3f(mx0, s[v][0], s[v][2]);
-        mx1 = max3f(mx1, s[v][1], s[v][3]);
+        // (the zero row of a token that does not count has scale 0)
+        const bool in_a = v * kTile + r < rem && la[v] != 0.f, in_b = v * kTile + r + 8 < rem && lb[v] != 0.f;
+        la[v] = lg2_approx(la[v]);
+        lb[v] = lg2_approx(lb[v]);
+        s[v][0] = in_a ? (s[v][0] + s2[v][0]) * (f0 * sa[v]) : -INFINITY;
+        s[v][1] = in_a ? (s[v][1] + s2[v][1]) * (f1 * sa[v]) : -INFINITY;
+        s[v][2] = in_b ? (s[v][2] + s2[v][2]) * (f0 * sb[v]) : -INFINITY;
+        s[v][3] = in_b ? (s[v][3] + s2[v][3]) * (f1 * sb[v]) : -INFINITY;
+        mx0 = max3f(mx0, s[v][0] + la[v], s[v][2] + lb[v]);
+        mx1 = max3f(mx1, s[v][1] + la[v], s[v][3] + lb[v]);
       }
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
@@ -328,9 +329,11 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
       const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
       const float mu0 = (mn0 == -INFINITY ? 0.f : mn0), mu1 = (mn1 == -INFINITY ? 0.f : mn1);
       if (__any_sync(0xffffffffu, mn0 != m0 || mn1 != m1)) {
-        const float al0 = ex2_approx(m0 - mu0), al1 = ex2_approx(m1 - mu1);
-        l0 *= al0;
-        l1 *= al1;
+        // (a step of m may pass 2^126, by which O is 0, but not the row sum)
+        const float half0 = ex2_approx(0.5f * (m0 - mu0)), half1 = ex2_approx(0.5f * (m1 - mu1));
+        const float al0 = half0 * half0, al1 = half1 * half1;
+        l0 = l0 * half0 * half0;
+        l1 = l1 * half1 * half1;
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
           o[mt][0] *= al0;
@@ -341,13 +344,17 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
         m0 = mn0;
         m1 = mn1;
       }
+      const float hm0 = 0.5f * (kSumShift - mu0), hm1 = 0.5f * (kSumShift - mu1);
       uint32_t b0[V], b1[V];  // P^T in B-operand layout
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float p0 = ex2_approx(s[v][0] - mu0 + kShift), p1 = ex2_approx(s[v][1] - mu1 + kShift);
-        const float p2 = ex2_approx(s[v][2] - mu0 + kShift), p3 = ex2_approx(s[v][3] - mu1 + kShift);
-        l0 += p0 * ia[v] + p2 * ib[v];
-        l1 += p1 * ia[v] + p3 * ib[v];
+        const float p0 = ex2_approx(s[v][0] + la[v] - mu0 + kShift), p1 = ex2_approx(s[v][1] + la[v] - mu1 + kShift);
+        const float p2 = ex2_approx(s[v][2] + lb[v] - mu0 + kShift), p3 = ex2_approx(s[v][3] + lb[v] - mu1 + kShift);
+        // the row sum's weights as squares of 2^((y - m + kSumShift) / 2), which stays above ex2's smallest result
+        const float e0 = ex2_approx(fmaf(0.5f, s[v][0], hm0)), e1 = ex2_approx(fmaf(0.5f, s[v][1], hm1));
+        const float e2 = ex2_approx(fmaf(0.5f, s[v][2], hm0)), e3 = ex2_approx(fmaf(0.5f, s[v][3], hm1));
+        l0 = fmaf(e2, e2, fmaf(e0, e0, l0));
+        l1 = fmaf(e3, e3, fmaf(e1, e1, l1));
         b0[v] = movmatrix_t(pack_f16(p0, p1));
         b1[v] = movmatrix_t(pack_f16(p2, p3));
       }
@@ -398,8 +405,9 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
       if (lane == 0) latch_err(p.err, kDevBadRecord);
       continue;
     }
-    const float inv0 = l0 == 0.f ? 0.f : 1.f / l0;
-    const float inv1 = l1 == 0.f ? 0.f : 1.f / l1;
+    constexpr float kUnit = 1.f / (float)(1 << (int)(kShift - kSumShift));
+    const float inv0 = l0 == 0.f ? 0.f : kUnit / l0;
+    const float inv1 = l1 == 0.f ? 0.f : kUnit / l1;
     const int hq0 = j * g + h0;
     float* dst0 = p.rec_o + ((int64_t)rec * p.n_q + hq0) * kD + 2 * r;
     const bool w0 = h0 < g, w1 = h0 + 1 < g;
@@ -411,8 +419,8 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
     }
     if (lane < 4) {
       float* ldst = p.rec_lse + (int64_t)rec * p.n_q + hq0;
-      if (w0) st_record(ldst, kv8_record_lse(l0, (m0 - kShift + log2f(l0)) * kLn2), keep);
-      if (w1) st_record(ldst + 1, kv8_record_lse(l1, (m1 - kShift + log2f(l1)) * kLn2), keep);
+      if (w0) st_record(ldst, kv8_record_lse(l0, (m0 - kSumShift + log2f(l0)) * kLn2), keep);
+      if (w1) st_record(ldst + 1, kv8_record_lse(l1, (m1 - kSumShift + log2f(l1)) * kLn2), keep);
     }
   }
 }

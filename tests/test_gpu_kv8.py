@@ -671,3 +671,47 @@ def test_decode_infinite_query_over_keys_of_one_sign(cuda_ok, n_q, n_kv, d, dtyp
     o2, lse2 = c.decode()
     assert torch.equal(torch.isnan(lse2), hit) and torch.isnan(o2[hit]).all()
     assert torch.equal(o2[~hit], o[~hit]) and torch.equal(lse2[~hit], lse[~hit])
+
+
+def test_decode_long_cold_runs_of_zero_values(cuda_ok):
+    """More than 600 COLD tokens of equal weight in one run, their V all zero: o is 0 (or the prefix's share)
+    and lse finite.  The prefix side takes all SMs but two, so the 3,000 tokens make two runs."""
+    def edit(kind, k, v):
+        if kind == "cold":
+            k[:] = 0.0
+            v[:] = 0.0
+    c = Kv8(np.random.default_rng(31), n_q=4, n_kv=1, d=128, dtype="bf16", prefixes=[19200], of=[0, -1], lens=[1500, 1500], edit=edit)
+    c.ctx.set_concurrency(True, 0.99)
+    plan = c.ctx.dispatch(c.batch)
+    assert sum(c.lens) > 600 * plan.suffix_runs()["runs"]
+    o, lse = c.decode(plan)
+    assert not o[1].any()
+    c.check(o, lse, "zero V")
+
+
+def _uneven_v(e, small, where, of):
+    """V of about 2^e, and of `small` 2^-e or nothing in some blocks of a slab or COLD tokens."""
+    def edit(kind, k, v):
+        if kind != of and of != "both":
+            return
+        n, step = k.shape[0], K8.BLOCK if kind == "prefix" else 1
+        at = np.arange(n) // step
+        low = {"first": at <= at[-1] // 2, "last": at > at[-1] // 2, "alternate": at % 2 == 1}[where] if n else np.zeros(0, bool)
+        v[~low] *= np.float32(2.0 ** e)
+        v[low] *= np.float32(small * 2.0 ** -e)
+        k[low] *= np.float32(2.0)
+    return edit
+
+
+UNEVEN = [(32, 8, 128, "bf16"), (16, 2, 128, "bf16"), (24, 2, 128, "bf16"), (8, 2, 64, "f32")]
+
+
+@pytest.mark.parametrize("n_q,n_kv,d,dtype", UNEVEN)
+@pytest.mark.parametrize("e", [20, 62, 100])
+@pytest.mark.parametrize("small", [0.0, 1.0])
+@pytest.mark.parametrize("where", ["first", "last", "alternate"])
+def test_decode_cold_values_far_apart(cuda_ok, n_q, n_kv, d, dtype, e, small, where):
+    """A COLD token keeps its weight in o and lse however small its V is beside the others'."""
+    c = Kv8(np.random.default_rng([e, n_q]), n_q=n_q, n_kv=n_kv, d=d, dtype=dtype, prefixes=[90], of=[-1, -1, -1, 0], lens=[100, 2, 300, 40],
+            edit=_uneven_v(e, small, where, "cold"))
+    c.check(*c.decode(), f"{e} {small} {where}")
