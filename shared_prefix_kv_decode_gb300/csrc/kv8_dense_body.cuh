@@ -26,9 +26,12 @@
 // The scales of a slab are those of 64-token blocks counted from its start, so a tile has one K scale
 // ks and one V scale vs: z = s ks + log2 vs (base 2) costs the FMA that the softmax needs anyway, P =
 // 2^(z - m) is p times vs, which is what meets the V codes, and the row sum adds the tile's sum of P
-// once, over vs.  The running maximum m is taken over z.  P carries a factor of 2^7: it is at most 2^15
-// (m may lag the row's maximum by 2^8, see below), and fp16 keeps its 11 bits down to 2^-21 of the
-// largest weight.
+// once, over vs / v, v the piece's smallest V scale.  The running maximum m is taken over z.  P carries a
+// factor of 2^7: it is at most 2^15 (m may lag the row's maximum by 2^8, see below), and fp16 keeps its 11
+// bits down to 2^-21 of the largest weight.
+// V scales lie between 2^-104.9 (of zeros) and 2^119.2.  Where those of a piece span more than 2^32, a tile's P
+// may underflow while its weights count: the row sum then has a running maximum and exponentials of its own, over
+// s ks alone.  Below that span P reaches weights of 2^-94 of the largest.
 // Roles (15 warps; the 16th only takes part in the block's barriers here):
 //  * warps 0-7, softmax and epilogue: warp w serves TMEM lanes 32*(w%4).. (row r = lane r), all 64
 //    columns of the tiles i with i % 2 == w / 4; the two warps of a row quarter take turns, half a
@@ -89,13 +92,14 @@ constexpr int kOffBar = kOffMPub + 4 * 2 * 32 * 4;
 constexpr int kBarArea = 512;
 constexpr int kSmemBytes = kOffBar + kBarArea + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-static_assert(kConvWarps * kCSlots * kPartCodes >= 4 * kM * 4, "the epilogue's sums and maxima");
+static_assert(kConvWarps * kCSlots * kPartCodes >= 6 * kM * 4, "the epilogue's sums and maxima");
 constexpr uint32_t kTmemCols = 512;           // S/P buffers at 0, 64, 128, 192, 256; Q (hi, lo) at 320; O at 384
 constexpr uint32_t kColQ = kSBufs * kN, kColO = 384;
 static_assert(kColQ + 2 * kD / 4 <= kColO && kColO + kD <= kTmemCols, "TMEM columns");
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;     // log2 of the largest growth tolerated in P
 constexpr float kShift = 7.0f;                // log2 of the factor that P carries
+constexpr uint32_t kWideSpan = 32;            // log2 of a wide span of V scales
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 enum : int {
@@ -199,7 +203,7 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
   const uint32_t base = (raw_u + 1023u) & ~1023u;
   unsigned char* smem = smem_raw + (base - raw_u);
   const uint32_t sK = base + kOffK, sV = base + kOffV, sC = base + kOffCodes;
-  // row sums and maxima for the epilogue, [kind][parity][row], in the codes' place (idle by then)
+  // row sums, exponents and maxima for the epilogue, [kind][parity][row], in the codes' place (idle by then)
   float* red = reinterpret_cast<float*>(smem + kOffCodes);
   float* units = reinterpret_cast<float*>(smem + kOffUnit);
   const uint32_t sBar = base + kOffBar;
@@ -289,8 +293,20 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
     ks = *reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.kpool) + a);
     vs = *reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.vpool) + a);
   };
+  // V scales of the piece's tiles lane, lane + 32, .. as the bits of positive floats, for their span; requested
+  // here and used when the set-up is done
+  constexpr int kSpan = 4;
+  uint32_t v_bits[kSpan] = {};
+  auto v_scale_bits = [&](int i) {
+    return *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.vpool) + (first_slot + (int64_t)i * kN) * p.kv8_row + scale_at);
+  };
   if (warp < kSoftmaxWarps) {
     if (slab_ok && qhalf < n_tiles) load_scales(qhalf);
+    if (slab_ok) {
+#pragma unroll
+      for (int k = 0; k < kSpan; ++k)
+        if (lane + 32 * k < n_tiles) v_bits[k] = v_scale_bits(lane + 32 * k);
+    }
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
                                                       ((int64_t)req * p.n_q + h) * kD + qhalf * (kD / 2));
     float amax = 0.f;
@@ -519,118 +535,150 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
     float* mpub = reinterpret_cast<float*>(smem + kOffMPub) + quad * 64;  // [tile parity][lane]
     const float scale = p.scale_log2 * units[r];
     float m_own = -INFINITY;   // max (of z, base 2) used for this warp's latest tile
-    float l = 0.f;             // this warp's share of the row sum, relative to m_own
+    float l = 0.f;             // this warp's share of the row sum, over 2^(m_own - kShift - least), or, wide, 2^n
+    float n = -INFINITY;
     bool ok = !*abort_flag;
-    for (int i = par; ok && i < n_tiles; i += 2) {
-      const int sb = i % kSBufs;
-      const float ca = scale * ks, cb = lg2_approx(vs);
-      if (i + 2 < n_tiles) load_scales(i + 2);
-      // the max used for tile i-1, decided by the other warp of the quarter
-      float m_prev = -INFINITY;
-      if (i > 0) {
-        const int pp = (i - 1) & 1;
-        ok = mbar_wait_bounded(bar(kBarMPub + quad * 2 + pp), ((i - 1) >> 1) & 1, abort_flag, p.err, kDevTimeout,
-                               kWaitLimitNs);
-        m_prev = mpub[pp * 32 + lane];
-      }
-      ok = ok && mbar_wait_bounded(bar(kBarSFull + sb), (i / kSBufs) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
-      ok = __all_sync(0xffffffffu, ok);  // the TMEM loads below are warp-collective
-      if (!ok) break;
-      tc_fence_after();
-      const int valid = min(kN, t1 - t0 - i * kN);               // tokens of the tile in range
-      const uint32_t ts = tmem + lane_off + (uint32_t)(sb * kN);
-      uint32_t u[2][32];
-      GRANIKV_TMEM_LD32(ts, u[0]);
-      GRANIKV_TMEM_LD32(ts + 32, u[1]);
-      tmem_wait_ld();
-      if (valid < kN) {  // masked keys: -inf, so their weight is 0
+    uint32_t v_min = 0xffffffffu, v_max = 0u;
+    auto span_of = [&](uint32_t x) {
+      v_min = min(v_min, x - 1u);  // (0: no tile there)
+      v_max = max(v_max, x);
+    };
 #pragma unroll
-        for (int k = 0; k < kN; ++k) u[k >> 5][k & 31] = k < valid ? u[k >> 5][k & 31] : 0xff800000u;
-      }
-      // row max of z (the factor is positive)
-      float mx;
-      {
-        float t[22], w[7];
-        auto sv = [&](int k) { return __uint_as_float(u[k >> 5][k & 31]); };
-#pragma unroll
-        for (int k = 0; k < 21; ++k) t[k] = max3f(sv(3 * k), sv(3 * k + 1), sv(3 * k + 2));
-        t[21] = sv(63);
-#pragma unroll
-        for (int k = 0; k < 7; ++k) w[k] = max3f(t[3 * k], t[3 * k + 1], t[3 * k + 2]);
-        mx = max3f(max3f(w[0], w[1], w[2]), max3f(w[3], w[4], w[5]), fmaxf(w[6], t[21])) * ca + cb;
-      }
-      // the max used for tile i: moved only when this tile's row max exceeds the last one by more
-      // than 2^kRescaleThreshold
-      float m_i = mx;
-      bool warp_need = false;
-      if (i > 0) {
-        warp_need = __any_sync(0xffffffffu, mx > m_prev + kRescaleThreshold);
-        m_i = warp_need ? fmaxf(m_prev, mx) : m_prev;
-      }
-      // publish at once, so the warp of tile i+1 is not held up by the rescale below (the slot's
-      // previous value, tile i-2's, was read by that warp before it published tile i-1's)
-      mpub[par * 32 + lane] = m_i;
-      mbar_arrive(bar(kBarMPub + quad * 2 + par));
-      if (warp_need) {
-        // O must hold PV(i-1) before it is rescaled, and PV(i) waits for P(i), written below
-        ok = mbar_wait_bounded(bar(kBarPvDone + (i - 1) % kSBufs), ((i - 1) / kSBufs) & 1, abort_flag, p.err,
-                               kDevTimeout, kWaitLimitNs);
-        ok = __all_sync(0xffffffffu, ok);
+    for (int k = 0; k < kSpan; ++k) span_of(v_bits[k]);
+    for (int i = lane + 32 * kSpan; ok && i < n_tiles; i += 32) span_of(v_scale_bits(i));
+    v_min = __reduce_min_sync(0xffffffffu, v_min) + 1u;
+    const bool wide = __reduce_max_sync(0xffffffffu, v_max) - v_min > kWideSpan << 23;
+    const float least = lg2_approx(__uint_as_float(v_min));  // log2 of the piece's smallest V scale
+    // (a loop for each: in one loop the untaken branch cost 2 % of a 16K prefix)
+    auto all_tiles = [&](auto wide_span) {
+      constexpr bool kWide = decltype(wide_span)::value;
+      for (int i = par; ok && i < n_tiles; i += 2) {
+        const int sb = i % kSBufs;
+        const float ca = scale * ks, cb = lg2_approx(vs);
+        if (i + 2 < n_tiles) load_scales(i + 2);
+        // the max used for tile i-1, decided by the other warp of the quarter
+        float m_prev = -INFINITY;
+        if (i > 0) {
+          const int pp = (i - 1) & 1;
+          ok = mbar_wait_bounded(bar(kBarMPub + quad * 2 + pp), ((i - 1) >> 1) & 1, abort_flag, p.err, kDevTimeout,
+                                 kWaitLimitNs);
+          m_prev = mpub[pp * 32 + lane];
+        }
+        ok = ok && mbar_wait_bounded(bar(kBarSFull + sb), (i / kSBufs) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
+        ok = __all_sync(0xffffffffu, ok);  // the TMEM loads below are warp-collective
         if (!ok) break;
         tc_fence_after();
-        const float alpha = m_prev == m_i ? 1.f : ex2_approx(m_prev - m_i);
-#pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          uint32_t x[16];
-          const uint32_t ta = tmem + lane_off + kColO + c * 16;
-          tmem_ld16(ta, x);
-          tmem_wait_ld();
+        const int valid = min(kN, t1 - t0 - i * kN);               // tokens of the tile in range
+        const uint32_t ts = tmem + lane_off + (uint32_t)(sb * kN);
+        uint32_t u[2][32];
+        GRANIKV_TMEM_LD32(ts, u[0]);
+        GRANIKV_TMEM_LD32(ts + 32, u[1]);
+        tmem_wait_ld();
+        if (valid < kN) {  // masked keys: -inf, so their weight is 0
 #pragma unroll
-          for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * alpha);
-          tmem_st16(ta, x);
+          for (int k = 0; k < kN; ++k) u[k >> 5][k & 31] = k < valid ? u[k >> 5][k & 31] : 0xff800000u;
+        }
+        // row max of z (the factor is positive)
+        float mx;
+        {
+          float t[22], w[7];
+          auto sv = [&](int k) { return __uint_as_float(u[k >> 5][k & 31]); };
+#pragma unroll
+          for (int k = 0; k < 21; ++k) t[k] = max3f(sv(3 * k), sv(3 * k + 1), sv(3 * k + 2));
+          t[21] = sv(63);
+#pragma unroll
+          for (int k = 0; k < 7; ++k) w[k] = max3f(t[3 * k], t[3 * k + 1], t[3 * k + 2]);
+          mx = max3f(max3f(w[0], w[1], w[2]), max3f(w[3], w[4], w[5]), fmaxf(w[6], t[21])) * ca + cb;
+        }
+        // the max used for tile i: moved only when this tile's row max exceeds the last one by more
+        // than 2^kRescaleThreshold
+        float m_i = mx;
+        bool warp_need = false;
+        if (i > 0) {
+          warp_need = __any_sync(0xffffffffu, mx > m_prev + kRescaleThreshold);
+          m_i = warp_need ? fmaxf(m_prev, mx) : m_prev;
+        }
+        // publish at once, so the warp of tile i+1 is not held up by the rescale below (the slot's
+        // previous value, tile i-2's, was read by that warp before it published tile i-1's)
+        mpub[par * 32 + lane] = m_i;
+        mbar_arrive(bar(kBarMPub + quad * 2 + par));
+        if (warp_need) {
+          // O must hold PV(i-1) before it is rescaled, and PV(i) waits for P(i), written below
+          ok = mbar_wait_bounded(bar(kBarPvDone + (i - 1) % kSBufs), ((i - 1) / kSBufs) & 1, abort_flag, p.err,
+                                 kDevTimeout, kWaitLimitNs);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const float alpha = m_prev == m_i ? 1.f : ex2_approx(m_prev - m_i);
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t x[16];
+            const uint32_t ta = tmem + lane_off + kColO + c * 16;
+            tmem_ld16(ta, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * alpha);
+            tmem_st16(ta, x);
+          }
+          tmem_wait_st();
+        }
+        if constexpr (kWide) {  // S(i) once more, for the row sum over its own maximum
+          const float top = fmaxf(n, mx - cb);
+          l *= ex2_approx(n - top);
+          n = top;
+#pragma unroll 1
+          for (int c = 0; c < kN / 16; ++c) {
+            uint32_t x[16];
+            tmem_ld16(ts + c * 16, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) l += c * 16 + k < valid ? ex2_approx(fmaf(__uint_as_float(x[k]), ca, -n)) : 0.f;
+          }
+        } else if (m_own != m_i && m_own != -INFINITY) {
+          l *= ex2_approx(m_own - m_i);
+        }
+        m_own = m_i;
+        // P = 2^(z - m + kShift), packed two per 32-bit column and written over columns [0, 32) of the
+        // S(i) buffer, whose 64 columns are in registers
+        const float m_use = m_i == -INFINITY ? 0.f : m_i;
+        {
+          const float off = cb - m_use + kShift;
+          const uint64_t scale2 = f2_pack(ca, ca), nm2 = f2_pack(off, off);
+          uint64_t acc[2] = {0ull, 0ull};  // packed partial sums (0.0f bit patterns)
+          uint32_t pk[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float sa = __uint_as_float(u[k >> 4][(2 * k) & 31]);
+            const float sb2 = __uint_as_float(u[k >> 4][(2 * k + 1) & 31]);
+            const uint64_t x = f2_fma(f2_pack(sa, sb2), scale2, nm2);
+            float xa, xb;
+            f2_unpack(x, xa, xb);
+            const float ea = ex2_approx(xa), eb = ex2_approx(xb);
+            acc[k & 1] = f2_add(acc[k & 1], f2_pack(ea, eb));
+            pk[k] = pack_f16(ea, eb);
+          }
+          GRANIKV_TMEM_ST32(ts, pk);
+          float la, lb;
+          f2_unpack(f2_add(acc[0], acc[1]), la, lb);
+          // over vs, by the very logarithm that P has
+          if constexpr (!kWide) l += (la + lb) * ex2_approx(least - cb);
         }
         tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(kBarPFull + sb));
       }
-      if (m_own != m_i && m_own != -INFINITY) l *= ex2_approx(m_own - m_i);
-      m_own = m_i;
-      // P = 2^(z - m + kShift), packed two per 32-bit column and written over columns [0, 32) of the
-      // S(i) buffer, whose 64 columns are in registers
-      const float m_use = m_i == -INFINITY ? 0.f : m_i;
-      {
-        const float off = cb - m_use + kShift;
-        const uint64_t scale2 = f2_pack(ca, ca), nm2 = f2_pack(off, off);
-        uint64_t acc[2] = {0ull, 0ull};  // packed partial sums (0.0f bit patterns)
-        uint32_t pk[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const float sa = __uint_as_float(u[k >> 4][(2 * k) & 31]);
-          const float sb2 = __uint_as_float(u[k >> 4][(2 * k + 1) & 31]);
-          const uint64_t x = f2_fma(f2_pack(sa, sb2), scale2, nm2);
-          float xa, xb;
-          f2_unpack(x, xa, xb);
-          const float ea = ex2_approx(xa), eb = ex2_approx(xb);
-          acc[k & 1] = f2_add(acc[k & 1], f2_pack(ea, eb));
-          pk[k] = pack_f16(ea, eb);
-        }
-        GRANIKV_TMEM_ST32(ts, pk);
-        float la, lb;
-        f2_unpack(f2_add(acc[0], acc[1]), la, lb);
-        // over vs, by the very logarithm that P has
-        l += (la + lb) * ex2_approx(-cb);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(bar(kBarPFull + sb));
-    }
-    // epilogue: wait for the last PV, combine the two warps' row sums (each relative to the max
-    // of its own latest tile; the last tile's max is the final one), normalise, write the record
+    };
+    if (wide) all_tiles(std::true_type{});
+    else all_tiles(std::false_type{});
+    // epilogue: wait for the last PV, combine the two warps' row sums (each with its exponent), normalise
+    // (O is relative to the last tile's max), write the record
     if (ok) {
       const int last = n_tiles - 1;
       ok = mbar_wait_bounded(bar(kBarPvDone + last % kSBufs), (last / kSBufs) & 1, abort_flag, p.err, kDevTimeout,
                              kWaitLimitNs);
     }
     ok = __all_sync(0xffffffffu, ok);
-    // swap the row sums and maxima with the other warp at the pair barrier; a warp that left the
+    // swap the row sums, exponents and maxima with the other warp at the pair barrier; a warp that left the
     // tile loop early may stop waiting for published maxima, so its partner's bounded waits give
     // up and both skip the record
     // (the codes' slots, where these go, are idle once the last PV is done; a CTA that gave up may
@@ -638,7 +686,8 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
     const bool safe = ok;
     if (safe) {
       red[par * kM + r] = l;
-      red[2 * kM + par * kM + r] = m_own;
+      red[2 * kM + par * kM + r] = wide ? n : m_own - kShift - least;
+      red[4 * kM + par * kM + r] = m_own;
     }
     mbar_arrive(bar(pair_bar));
     const bool pair_ok = mbar_wait_bounded(bar(pair_bar), 0, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
@@ -646,17 +695,16 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
       tc_fence_after();
-      const float l0 = red[r], l1 = red[kM + r];
-      const float m_used = red[2 * kM + ((n_tiles - 1) & 1) * kM + r];
-      const float m0 = red[2 * kM + r], m1 = red[2 * kM + kM + r];
-      // a warp that had no tile left 0; an equal maximum (both may be -inf or NaN) needs no factor
-      const float lt = (l0 == 0.f ? 0.f : m0 == m_used ? l0 : l0 * ex2_approx(m0 - m_used)) +
-                       (l1 == 0.f ? 0.f : m1 == m_used ? l1 : l1 * ex2_approx(m1 - m_used));
+      const float l0 = red[r], l1 = red[kM + r], e0 = red[2 * kM + r], e1 = red[3 * kM + r];
+      const float m_used = red[4 * kM + ((n_tiles - 1) & 1) * kM + r];
+      const float top = fmaxf(e0, e1);
+      // a warp that had no tile left 0 and -inf
+      const float lt = l0 * ex2_approx(e0 - top) + l1 * ex2_approx(e1 - top);
       if (row < rows && (rec < 0 || rec >= p.n_records)) {
         if (half == 0) atomicCAS(p.err, 0, (int32_t)kDevBadRecord);
         rec = -1;
       }
-      const float inv = lt == 0.f ? 0.f : 1.f / lt;
+      const float inv = 1.f / lt, unit = ex2_approx(m_used - kShift - top);  // (a tile has a valid token)
       uint32_t u[2][32];
       GRANIKV_TMEM_LD32(tmem + lane_off + kColO + half * 64, u[0]);
       GRANIKV_TMEM_LD32(tmem + lane_off + kColO + half * 64 + 32, u[1]);
@@ -669,12 +717,11 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
         for (int c = 0; c < 8; ++c) {
           float x[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(u[c >> 2][(c & 3) * 8 + k]) * inv;
+          for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(u[c >> 2][(c & 3) * 8 + k]) * inv * unit;
           st_record8(dst + c * 8, x, keep);
         }
         if (half == 0) {
-          const float m_fin = m_used == -INFINITY ? 0.f : m_used;
-          st_record(p.rec_lse + (int64_t)rec * p.n_q + h, kv8_record_lse(lt, (m_fin - kShift + log2f(lt)) * kLn2), keep);
+          st_record(p.rec_lse + (int64_t)rec * p.n_q + h, kv8_record_lse(lt, (top + log2f(lt)) * kLn2), keep);
         }
       }
     }

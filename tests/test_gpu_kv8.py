@@ -715,3 +715,59 @@ def test_decode_cold_values_far_apart(cuda_ok, n_q, n_kv, d, dtype, e, small, wh
     c = Kv8(np.random.default_rng([e, n_q]), n_q=n_q, n_kv=n_kv, d=d, dtype=dtype, prefixes=[90], of=[-1, -1, -1, 0], lens=[100, 2, 300, 40],
             edit=_uneven_v(e, small, where, "cold"))
     c.check(*c.decode(), f"{e} {small} {where}")
+
+
+@pytest.mark.parametrize("n_q,n_kv,d,dtype", UNEVEN)
+@pytest.mark.parametrize("e", [20, 62, 100])
+@pytest.mark.parametrize("small", [0.0, 1.0])
+@pytest.mark.parametrize("where", ["first", "last", "alternate"])
+def test_decode_prefix_values_far_apart(cuda_ok, n_q, n_kv, d, dtype, e, small, where):
+    """A slab's token keeps its weight in o and lse however small its block's V is beside the others'; pieces of
+    one tile to many."""
+    c = Kv8(np.random.default_rng([e, n_q, 1]), n_q=n_q, n_kv=n_kv, d=d, dtype=dtype, prefixes=[1100, 300], of=[0, 1, 0, 1], lens=[0, 3, 20, 0],
+            edit=_uneven_v(e, small, where, "prefix"))
+    c.check(*c.decode(), f"{e} {small} {where}")
+
+
+def test_decode_long_prefix_pieces_of_zero_values(cuda_ok):
+    """A piece of 1,064 tokens whose V is all zero and whose first block scores 2^7.65 below the rest, which the
+    kernel's running maximum does not follow: o is 0 and lse finite.  160 requests make 80 CTAs, so that the
+    prefix is one piece.  lse: a score of 128 equal products errs by 128 2^-24 of itself, the sum by L 2^-24, the
+    exponential and logarithm by 2^-20, lse by 2^-23 of itself."""
+    torch = _torch()
+
+    def edit(kind, k, v):
+        k[:64], k[64:] = 0.0, 0.46875
+        v[:] = 0.0
+    c = Kv8(np.random.default_rng(32), n_q=64, n_kv=8, d=128, dtype="bf16", prefixes=[1064], of=[0] * 160, lens=[0] * 160, edit=edit)
+    c.q.fill_(1.0)
+    plan = c.ctx.dispatch(c.batch)
+    assert plan.groups()[0]["n_splits"] == 1
+    o, lse = c.decode(plan)
+    assert not o.any()
+    s = 0.46875 * math.sqrt(128)
+    want = math.log(64 + 1000 * math.exp(s))
+    assert (lse.double() - want).abs().max().item() <= 128 * 2.0 ** -24 * s + 1064 * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -23 * want
+
+
+def test_decode_long_pieces_of_values_far_apart(cuda_ok):
+    """A piece of more than 132 blocks (160 requests of 64 heads make 80 row blocks), V zero but for blocks 129 to
+    131 of about 2^60, K zero: every weight is 1 / 17,000.  Tolerance of o as at the top, all weights equal."""
+    L = 17000
+
+    def edit(kind, k, v):
+        k[:] = 0.0
+        v *= np.float32(2.0 ** 60)
+        v[:129 * 64] = 0.0
+        v[132 * 64:] = 0.0
+    c = Kv8(np.random.default_rng(34), n_q=64, n_kv=1, d=128, dtype="bf16", prefixes=[L], of=[0] * 160, lens=[0] * 160, edit=edit)
+    plan = c.ctx.dispatch(c.batch)
+    assert plan.groups()[0]["n_splits"] <= 2
+    o, lse = c.decode(plan)
+    V = c.pv[0][:, 0]
+    want, A = V.sum(axis=0) / L, np.abs(V).sum(axis=0) / L
+    tol = (L * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -11) * A + 2.0 ** -32 * np.abs(V).max()
+    tol += 2.0 ** -8 * (np.abs(want) + tol)
+    o = o.double().cpu().numpy().reshape(-1, 128)
+    assert (np.abs(o - want) <= tol).all()
+    assert (lse.double() - math.log(L)).abs().max().item() <= L * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -23 * math.log(L)
