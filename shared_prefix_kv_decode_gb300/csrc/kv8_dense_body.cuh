@@ -50,6 +50,8 @@
 
 #include <cuda.h>
 
+#include <cfloat>
+
 #include "internal.h"
 #include "kv8_suffix_body.cuh"
 #include "kv8_util.cuh"
@@ -554,7 +556,8 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
       constexpr bool kWide = decltype(wide_span)::value;
       for (int i = par; ok && i < n_tiles; i += 2) {
         const int sb = i % kSBufs;
-        const float ca = scale * ks, cb = lg2_approx(vs);
+        // (at least the smallest normal number: 0 * -inf of a masked key would be NaN)
+        const float ca = fmaxf(scale * ks, FLT_MIN), cb = lg2_approx(vs);
         if (i + 2 < n_tiles) load_scales(i + 2);
         // the max used for tile i-1, decided by the other warp of the quarter
         float m_prev = -INFINITY;

@@ -771,3 +771,14 @@ def test_decode_long_pieces_of_values_far_apart(cuda_ok):
     o = o.double().cpu().numpy().reshape(-1, 128)
     assert (np.abs(o - want) <= tol).all()
     assert (lse.double() - math.log(L)).abs().max().item() <= L * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -23 * math.log(L)
+
+
+@pytest.mark.parametrize("L_p", [1, 70, 200])
+@pytest.mark.parametrize("size", [2.0 ** -30, 2.0 ** -40, 2.0 ** -100])
+def test_decode_tiny_queries_over_zero_keys(cuda_ok, L_p, size):
+    """All-zero K and a q so small that the product of the scales underflows: the weights are equal, the places
+    past the prefix's end still have none."""
+    def edit(kind, k, v):
+        k[:] = 0.0
+    c = Kv8(np.random.default_rng(33), n_q=32, n_kv=8, d=128, dtype="bf16", prefixes=[L_p], of=[0, 0, -1], lens=[0, 5, 9], q_scale=size, edit=edit)
+    c.check(*c.decode(), f"{L_p} {size}")
