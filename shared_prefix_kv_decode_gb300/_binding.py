@@ -215,16 +215,20 @@ def _stream(s) -> Optional[int]:
     raise TypeError(f"expected a stream handle, got {type(s)}")
 
 
+def _i32_copy(values: Sequence[int]):
+    return (C.c_int32 * len(values))(*[int(v) for v in values])
+
+
 def _i32_array(values: Sequence[int]):
+    """For calls that are done with the array when they return: one of int32_array goes as it is."""
     if isinstance(values, C.Array) and values._type_ is C.c_int32:
         return values
-    arr = (C.c_int32 * len(values))(*[int(v) for v in values])
-    return arr
+    return _i32_copy(values)
 
 
 def int32_array(values: Sequence[int]):
-    """Host int32 array that the calls taking host counts accept as it is (a list is converted at
-    every call)."""
+    """Host int32 array that the calls taking host counts read as it is when they are called (a list
+    is converted at every call).  A Batch copies it."""
     return _i32_array(values)
 
 
@@ -241,8 +245,8 @@ class Batch:
     def __init__(self, slab_id: Sequence[int], seq_len: Sequence[int], req_to_slot, cap: int, seq_len_dev=None):
         if len(slab_id) != len(seq_len):
             raise ValueError("slab_id and seq_len differ in length")
-        self._slab = _i32_array(slab_id)
-        self._len = _i32_array(seq_len)
+        self._slab = _i32_copy(slab_id)
+        self._len = _i32_copy(seq_len)
         self._table = req_to_slot  # keep the tensors alive
         self._live = seq_len_dev
         self.c = _Batch(len(slab_id), C.cast(self._slab, C.POINTER(C.c_int32)),

@@ -210,3 +210,14 @@ def test_evict_refusals(granikv_lib):
 def test_host_arrays_are_taken_as_they_are(granikv_lib):
     a = gb.int32_array([3, 1, 2])
     assert gb.int32_array(a) is a and list(a) == [3, 1, 2]
+
+
+def test_batch_keeps_its_own_counts(granikv_lib):
+    """A batch made from a host array does not follow what the caller writes to the array later."""
+    slabs, lens = gb.int32_array([-1, -1]), gb.int32_array([3, 2])
+    b = gb.Batch(slabs, lens, 4096, 16, 4096)
+    live = b.with_live(8192)
+    slabs[0], lens[0], lens[1] = 5, 17, -4
+    for x in (b, live):
+        assert [x.c.slab_id[i] for i in range(2)] == [-1, -1] and [x.c.seq_len[i] for i in range(2)] == [3, 2]
+    assert _status(_ctx().cold_weigh, 0, 4096, 4096, b, 4096) == gb.ERR_NO_DEVICE
