@@ -200,8 +200,11 @@ class GraniKVCache:
     @property
     def weight(self) -> torch.Tensor:
         """Accumulated attention weight of every place of the token table [max_batch, cap] (fp32),
-        made on first use; a new row's weights are 0."""
+        made on first use, which may not be inside a capture (every replay would zero them); a new
+        row's weights are 0."""
         if self._weight is None:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("use GraniKVCache.weight once before the capture: a graph that makes it zeroes it")
             self._weight = torch.zeros((self.max_batch, self.cap), dtype=torch.float32, device=self.device)
         return self._weight
 

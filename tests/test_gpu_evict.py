@@ -400,3 +400,31 @@ def test_driver_with_a_cold_budget(cuda_ok, kv8, graph):
             # weights in bf16 or fp16 (2^-8 of sum p|v| at most) and the output in bf16 (2^-8 of itself)
             A = np.abs(V[:, h // 4]).max()
             assert np.abs(o[b, h] - ref).max() <= 2.0 ** -8 * (A + np.abs(ref).max()) and abs(lse[b, h] - ref_lse) <= 1e-3
+
+
+def test_weights_are_not_made_inside_a_capture(cuda_ok):
+    """Made while a graph is captured, the weights would be zeroed by every replay: refused, and once they are
+    made the captured weighing accumulates over the replays."""
+    torch, gb = _torch(), _gb()
+    from shared_prefix_kv_decode_gb300 import GraniKVCache
+    rng = np.random.default_rng(13)
+    cache = GraniKVCache(n_layers=1, n_q=8, n_kv=2, head_dim=128, dtype=gb.DTYPE_BF16, n_slots=400, max_batch=2, cap=64)
+    x = torch.from_numpy(_rows(rng, 50, 2, 128, "bf16")).cuda().to(torch.bfloat16)
+    cache.append([30, 20], [x], [x])
+    batch = cache.batch([-1, -1])
+    q = torch.randn(2, 8, 128, device="cuda").to(torch.bfloat16)
+    o, lse = cache.decode(0, q, batch)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="before the capture"):
+        with torch.cuda.graph(g):
+            o.add_(0.0)
+            cache.weigh(0, q, lse, batch)
+    assert not cache.weight.any()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cache.weigh(0, q, lse, batch)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.allclose(cache.weight.sum(dim=1), torch.full((2,), 24.0, device="cuda"), rtol=1e-4)
