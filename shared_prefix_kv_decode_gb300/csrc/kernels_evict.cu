@@ -649,7 +649,7 @@ bool weigh_on_mma(const WeighParams& p) {
 template <bool KV8, int D, int N>
 cudaError_t weigh_mma(const WeighParams& p, const WeighRows<N>& rows, int32_t chunks, cudaStream_t s) {
   static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem_once(weigh_mma_kernel<KV8, D, N>, WeighUnit<KV8, D>::kRing + 4 * kMaxHeads * kChunkMin, allowed);
+  cudaError_t e = allow_smem_once(weigh_mma_kernel<KV8, D, N>, WeighUnit<KV8, D>::kRing + 4 * kMaxHeads * kChunkMin, allowed, 4 * kChunkMax);
   if (e != cudaSuccess) return e;
   const int smem = WeighUnit<KV8, D>::kRing + (int)sizeof(float) * p.n_kv * rows.tokens;
   weigh_mma_kernel<KV8, D, N><<<chunks, 256, smem, s>>>(p, rows);

@@ -41,23 +41,23 @@ inline cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-// Let a kernel be launched with `bytes` of dynamic shared memory on the current device (a no-op up
-// to the 48 KB that need no leave).
+// Let a kernel be launched with `bytes` of dynamic shared memory on the current device.  (The 48 KB that need no
+// leave hold the kernel's static shared memory too: a kernel that has any says how much.)
 template <typename K>
-inline cudaError_t allow_smem(K kernel, int bytes) {
-  if (bytes <= 48 * 1024) return cudaSuccess;
+inline cudaError_t allow_smem(K kernel, int bytes, int static_bytes = 0) {
+  if (bytes + static_bytes <= 48 * 1024) return cudaSuccess;
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 // The same, asked of the driver once per kernel and device; `done` is a bit per device, the caller's
 // static for this kernel and size.
 template <typename K>
-inline cudaError_t allow_smem_once(K kernel, int bytes, std::atomic<uint64_t>& done) {
+inline cudaError_t allow_smem_once(K kernel, int bytes, std::atomic<uint64_t>& done, int static_bytes = 0) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
   if (bit && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
-  e = allow_smem(kernel, bytes);
+  e = allow_smem(kernel, bytes, static_bytes);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }

@@ -428,3 +428,17 @@ def test_weights_are_not_made_inside_a_capture(cuda_ok):
         g.replay()
     torch.cuda.synchronize()
     assert torch.allclose(cache.weight.sum(dim=1), torch.full((2,), 24.0, device="cuda"), rtol=1e-4)
+
+
+@pytest.mark.parametrize("n_q,n_kv", [(8, 2), (32, 8), (24, 2), (7, 1), (64, 64), (65, 65)])
+@pytest.mark.parametrize("kv8", [False, True])
+def test_weigh_bf16_heads_of_64(cuda_ok, n_q, n_kv, kv8):
+    """On tensor cores up to 64 KV heads; one more, on CUDA cores."""
+    torch, rng = _torch(), np.random.default_rng([n_q, n_kv, 64, kv8])
+    c = Cold(rng, n_q=n_q, n_kv=n_kv, d=64, dtype="bf16", lens=[1, 0, 15, 16, 17, 31, 33, 129, 400, 64], kv8=kv8)
+    before = torch.rand(10, c.cap, device="cuda")
+    for keep in (1.0, 0.0):
+        w = before.clone()
+        c.ctx.cold_weigh(0, c.q, c.lse, c.batch, w, keep)
+        c.ctx.sync_status()
+        c.check(w, before, keep, what=f"keep {keep}")
