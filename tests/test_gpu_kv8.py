@@ -782,3 +782,11 @@ def test_decode_tiny_queries_over_zero_keys(cuda_ok, L_p, size):
         k[:] = 0.0
     c = Kv8(np.random.default_rng(33), n_q=32, n_kv=8, d=128, dtype="bf16", prefixes=[L_p], of=[0, 0, -1], lens=[0, 5, 9], q_scale=size, edit=edit)
     c.check(*c.decode(), f"{L_p} {size}")
+
+
+@pytest.mark.parametrize("n_q,n_kv", [(8, 2), (32, 8), (12, 1), (24, 12)])
+def test_decode_bf16_heads_of_64(cuda_ok, n_q, n_kv):
+    rng = np.random.default_rng([n_q, n_kv, 64])
+    c = Kv8(rng, n_q=n_q, n_kv=n_kv, d=64, dtype="bf16", prefixes=[517, 130], of=[0, 1, -1, 0, 0, 1, 0, -1, 0],
+            lens=[5, 33, 70, 0, 1, 16, 200, 17, 64], slots_before=9)
+    c.check(*c.decode(), f"{n_q}/{n_kv}/64/bf16")
