@@ -920,7 +920,7 @@ granikv_status granikv_cold_evict(granikv_ctx* c, const int32_t* seq_len, const 
   if (!has_device(c)) return GRANIKV_ERR_NO_DEVICE;
   if (total == 0 && !suffix_len) return GRANIKV_OK;
   DeviceGuard dg(c->cfg.device);
-  cudaError_t e = launch_cold_evict(rows.data(), B, keep_last, req_to_slot, suffix_len, weight, cap, slots_out,
+  cudaError_t e = launch_cold_evict(rows.data(), B, c->num_sms, keep_last, req_to_slot, suffix_len, weight, cap, slots_out,
                                     (cudaStream_t)stream);
   c->n_kernels += (B + kRowsPerLaunch - 1) / kRowsPerLaunch;
   return cuda_status(e);

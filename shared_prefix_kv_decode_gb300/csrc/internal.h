@@ -235,8 +235,8 @@ cudaError_t launch_kv8_suffix(const AttnParams& p, const int32_t* cta_begin, int
 
 // Eviction (kernels_evict.cu)
 cudaError_t launch_cold_weigh(int32_t dtype, const WeighParams& p, const int32_t* seq_len /*host [B]*/, cudaStream_t s);
-cudaError_t launch_cold_evict(const EvictRow* rows, int32_t B, int32_t keep_last, int32_t* req_to_slot,
-                              int32_t* suffix_len, float* weight, int32_t cap, int32_t* slots_out, cudaStream_t s);
+cudaError_t launch_cold_evict(const EvictRow* rows, int32_t B, int32_t num_sms, int32_t keep_last,
+                              int32_t* req_to_slot, int32_t* suffix_len, float* weight, int32_t cap, int32_t* slots_out, cudaStream_t s);
 
 constexpr int kNumImpl = 8;  // that a prefix group can run on
 

@@ -616,22 +616,25 @@ cudaError_t evict_cluster(const EvictRows<N>& a, int32_t row0, int32_t n, int32_
 }
 
 template <int N>
-cudaError_t evict_n(const EvictRow* rows, int32_t row0, int32_t n, int32_t keep_last, int32_t* req_to_slot,
-                    int32_t* suffix_len, float* weight, int32_t cap, int32_t* slots_out, cudaStream_t s) {
+cudaError_t evict_n(const EvictRow* rows, int32_t row0, int32_t n, int32_t num_sms, int32_t keep_last,
+                    int32_t* req_to_slot, int32_t* suffix_len, float* weight, int32_t cap, int32_t* slots_out, cudaStream_t s) {
   EvictRows<N> a{};
   int32_t longest = 1;
   for (int32_t i = 0; i < n; ++i) {
     a.r[i] = rows[i];
     if (rows[i].n_evict > 0 && rows[i].len > longest) longest = rows[i].len;
   }
-  // the fewest CTAs (a power of two, 8 at most) whose threads hold the longest row at PER tokens each;
-  // two a thread while that is not more than a grid of about two CTAs an SM, else eight or sixteen
+  // the fewest CTAs (a power of two, 8 at most) whose threads hold the longest row at PER tokens each.  Two a
+  // thread where that is one CTA a row, or two or four and all run at once (a CTA's 1,024 threads take an SM), else
+  // eight or sixteen.  With 2 and 8 a thread (us): rows of 2,048, B = 152 6.9 and 9.0, B = 608 25.5 and 33.8; of 4,000,
+  // B = 76 8.0 and 9.4, B = 100 14.9 and 9.5; of 8,000, B = 32 10.1 and 10.0, B = 64 19.3 and 10.2; of 16,000
+  // (clusters of eight), B = 8 13.0 and 11.3
   auto ctas = [&](int per) {
     int32_t cs = 1;
     while ((int64_t)cs * per * kEvictThreads < longest) cs *= 2;
     return cs;
   };
-  if (ctas(2) <= 8 && n * ctas(2) <= 304)
+  if (ctas(2) == 1 || (ctas(2) <= 4 && n * ctas(2) <= num_sms))
     return evict_cluster<2>(a, row0, n, ctas(2), keep_last, req_to_slot, suffix_len, weight, cap, slots_out, s);
   if (ctas(8) <= 8)
     return evict_cluster<8>(a, row0, n, ctas(8), keep_last, req_to_slot, suffix_len, weight, cap, slots_out, s);
@@ -721,16 +724,16 @@ cudaError_t launch_cold_weigh(int32_t dtype, const WeighParams& p, const int32_t
   return p.kv8_row ? weigh_all<float, true>(p, seq_len, s) : weigh_all<float, false>(p, seq_len, s);
 }
 
-cudaError_t launch_cold_evict(const EvictRow* rows, int32_t B, int32_t keep_last, int32_t* req_to_slot,
-                              int32_t* suffix_len, float* weight, int32_t cap, int32_t* slots_out, cudaStream_t s) {
+cudaError_t launch_cold_evict(const EvictRow* rows, int32_t B, int32_t num_sms, int32_t keep_last,
+                              int32_t* req_to_slot, int32_t* suffix_len, float* weight, int32_t cap, int32_t* slots_out, cudaStream_t s) {
   // the rows' counts travel as a kernel parameter: nothing is staged in memory that two calls (or
   // a captured and an eager one) could share
   constexpr int kSmall = 64, kLarge = kRowsPerLaunch;
   cudaError_t e = cudaSuccess;
   for (int32_t b = 0; b < B && e == cudaSuccess;) {
     const int32_t n = B - b < kLarge ? B - b : kLarge;
-    e = n <= kSmall ? evict_n<kSmall>(rows + b, b, n, keep_last, req_to_slot, suffix_len, weight, cap, slots_out, s)
-                    : evict_n<kLarge>(rows + b, b, n, keep_last, req_to_slot, suffix_len, weight, cap, slots_out, s);
+    e = n <= kSmall ? evict_n<kSmall>(rows + b, b, n, num_sms, keep_last, req_to_slot, suffix_len, weight, cap, slots_out, s)
+                    : evict_n<kLarge>(rows + b, b, n, num_sms, keep_last, req_to_slot, suffix_len, weight, cap, slots_out, s);
     b += n;
   }
   return e;

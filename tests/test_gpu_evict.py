@@ -442,3 +442,10 @@ def test_weigh_bf16_heads_of_64(cuda_ok, n_q, n_kv, kv8):
         c.ctx.cold_weigh(0, c.q, c.lse, c.batch, w, keep)
         c.ctx.sync_status()
         c.check(w, before, keep, what=f"keep {keep}")
+
+
+@pytest.mark.parametrize("B,n", [(400, 2048), (76, 4000), (77, 4000), (38, 8000), (39, 8000), (8, 16000)])
+def test_evict_around_one_wave(cuda_ok, B, n):
+    """Rows that take one, two, four or eight CTAs at two tokens a thread, on either side of what 152 SMs run at once."""
+    rng = np.random.default_rng([B, n])
+    _evict_case(rng, [n - b % 5 for b in range(B)], [n // 3 - b for b in range(B)], None, 7, n, KINDS["few" if B % 2 else "softmax"](rng))
