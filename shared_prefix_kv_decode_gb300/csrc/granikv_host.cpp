@@ -1236,8 +1236,9 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
       // set-up for its run (a few us) is left out: the prefix estimate runs about 6 us long on
       // that shape, which covers it; with 4 / 2 / 0 us set aside for it the call took 82.9 /
       // 81.0 / 80.3 us, and at 0 both sides end within 0.4 us of each other.
+      // (an 8-bit cache has tail runs from the common-end plan above only)
       bool all_dense = G > 0 && n_kv <= 8;
-      for (int32_t i = 0; i < G; ++i) all_dense = all_dense && dense_tc(groups[i].impl);
+      for (int32_t i = 0; i < G; ++i) all_dense = all_dense && groups[i].impl == kImplDenseTc;
       if (auto_found && all_dense) {
         const double n_d = (double)ctas_for(lo), n_s = (double)c->num_sms - n_d;
         const double x = (w_s / n_s - prefix_time(lo)) / (1.0 / n_s + 1.0 / n_d);
