@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(256) weigh_generic_kernel(WeighParams p, const
 // 4 u + {0, 1} and 4 u + {2, 3}.  Of a packed 8-bit row it holds dims 64 i + 16 c + 0..15; k-step
 // 4 i + u takes dims 4 u + {0, 1} and 4 u + {2, 3}, converted to fp16 (exact); the row's scale
 // multiplies the scores, and q is brought into fp16's range by a power of two per query head
-// (exact but for elements 2^-28 below the row's largest).
+// (exact but for elements 2^-31 below the row's largest).
 // The units' sums go to shared memory and are added in KV-head order: the result has one order.
 // A CTA takes a chunk of 64 to 512 tokens, sized so that all chunks run at once: with 256 tokens a CTA the
 // 877 chunks of 224K tokens made 1.44 waves of 608 CTAs (49.5 us against 47.8), and a CTA's start (length, slots, q, first rows: four
