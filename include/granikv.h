@@ -157,6 +157,30 @@ granikv_status granikv_create_kv8(const granikv_config* cfg, granikv_ctx** out);
  * (as from granikv_create_kv8) for a row of more than 2^24 bytes. */
 granikv_status granikv_kv8_row_bytes(int32_t n_kv, int32_t head_dim, size_t* bytes);
 
+/* ---- 4-bit cache.  A context made by granikv_create_kv4 keeps K and V as 4-bit floating-point codes
+ * (e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) with an e4m3 scale for each 16 of them and a power
+ * of two for each block of tokens and KV head, in 4.6 bits an element.
+ *
+ * cfg->k_pool and v_pool are then byte pools [n_slots, row_bytes], row_bytes from
+ * granikv_kv4_row_bytes: one slot's row is n_kv * head_dim / 2 bytes of codes (head by head, element
+ * 2 i in the low half of a byte), n_kv * head_dim / 16 e4m3 scales, padding to a multiple of 16 bytes, n_kv
+ * exponent bytes, padding to a multiple of 16 bytes; value = code * scale * 2^(exponent byte - 127).
+ * Rows given to granikv_hot_fill, granikv_cold_append and granikv_decode_attention_append (cfg->dtype) are
+ * quantised: with amax the largest finite magnitude of the head's elements over a block of tokens (64
+ * consecutive tokens of a slab, counted from its start, or one COLD token) and bmax that of 16 elements,
+ *     exponent e: the smallest with amax <= 2688 * 2^e, within [-100, 116];
+ *     scale = the nearest e4m3 value to bmax / (6 * 2^e), at least 2^-9 and at most 448;
+ *     code = the nearest e2m1 value to x / (scale * 2^e), saturated at +-6,
+ * each exact quotient rounded once, ties to even.  An infinity becomes +-6 * scale * 2^e; a NaN makes its 16
+ * elements NaN (their scale is).  Zeros keep their sign.
+ * Everything else is as for granikv_create_kv8: 16-byte alignment of those rows and of q and o; a NaN or an
+ * infinity in a head's q, or a NaN in the K that a request attends, makes that head's o and lse of that
+ * request NaN, a NaN in V reaches its 16 columns of o only; the same calls work, the same are
+ * GRANIKV_ERR_UNSUPPORTED, and the same backends serve the same shapes. ------------------------- */
+granikv_status granikv_create_kv4(const granikv_config* cfg, granikv_ctx** out);
+/* Bytes of one slot's row; GRANIKV_ERR_UNSUPPORTED as from granikv_kv8_row_bytes. */
+granikv_status granikv_kv4_row_bytes(int32_t n_kv, int32_t head_dim, size_t* bytes);
+
 /* ---- HOT pool ("B.10 Cross-pool admission and promotion policy"; "B.8 Multi-prefix
  * sensitivity": first-fit packing of mixed slab sizes; card page: one slab per prefix node).
  * Host only, no device access. ------------------------------------------------------------- */
@@ -179,6 +203,13 @@ granikv_status granikv_hot_stats(granikv_ctx* ctx, int64_t* n_hot, int64_t* larg
  * the prefix's causal attention; the projection that produces K/V is outside the library). */
 granikv_status granikv_hot_fill(granikv_ctx* ctx, int32_t layer, int32_t slab_id,
                                 const void* k, const void* v, granikv_stream_t stream);
+
+/* Tokens [t0, t0 + n) of a slab of one layer as K/V rows ([n, n_kv, head_dim] of the context's dtype,
+ * device, contiguous, 16-byte aligned): a 16- or 32-bit cache's as they are, a packed one's as the values
+ * that codes and scales stand for, rounded once (the 4-bit cache's are exact).  n = 0 is a call that does
+ * nothing; GRANIKV_ERR_INVALID for a range outside the slab. */
+granikv_status granikv_hot_read(granikv_ctx* ctx, int32_t layer, int32_t slab_id, int32_t t0, int32_t n,
+                                void* k, void* v, granikv_stream_t stream);
 
 /* ---- COLD pool ("1 Introduction" and "3 GraniKV": a token-level pool, page size 1, for
  * suffix and decoded tokens; card page: a token-level free list). ------------------------- */
@@ -217,6 +248,12 @@ granikv_status granikv_cold_sync(granikv_ctx* ctx, granikv_stream_t stream);
 granikv_status granikv_cold_append(granikv_ctx* ctx, int32_t layer, const void* k_new,
                                    const void* v_new, const int32_t* slots, int32_t N,
                                    granikv_stream_t stream);
+
+/* K/V of the N tokens at slots[i] (device [N]) of one layer, as granikv_hot_read gives them
+ * ([N, n_kv, head_dim]; a slot may come more than once).  A slot outside [n_hot, n_slots) is a device check
+ * failure; its row of k and v is left as it was. */
+granikv_status granikv_cold_read(granikv_ctx* ctx, int32_t layer, const int32_t* slots, int32_t N, void* k,
+                                 void* v, granikv_stream_t stream);
 
 /* ---- eviction of COLD tokens.  (No counterpart in the paper, whose COLD rows only grow; the
  * token-level pool of "3 GraniKV", page size 1, is what lets single tokens leave.)  The caller

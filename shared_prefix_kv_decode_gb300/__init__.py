@@ -12,13 +12,13 @@ this package is its thin binding.  Build the library with
 from ._binding import (  # noqa: F401
     BACKEND_AUTO, BACKEND_CASCADE, BACKEND_DENSE, BACKEND_NAMES, DTYPE_BF16, DTYPE_F32,
     Batch, Context, DeviceCheckFailed, GranikvError, NoColdSpace, NoHotSpace, Plan,
-    int32_array, kv8_row_bytes, load_library, status_string,
+    int32_array, kv4_row_bytes, kv8_row_bytes, load_library, status_string,
 )
 
 __all__ = [
     "BACKEND_AUTO", "BACKEND_CASCADE", "BACKEND_DENSE", "BACKEND_NAMES", "DTYPE_BF16", "DTYPE_F32",
     "Batch", "Context", "DeviceCheckFailed", "GranikvError", "NoColdSpace", "NoHotSpace", "Plan",
-    "int32_array", "kv8_row_bytes", "load_library", "status_string", "GraniKVCache",
+    "int32_array", "kv4_row_bytes", "kv8_row_bytes", "load_library", "status_string", "GraniKVCache",
 ]
 
 

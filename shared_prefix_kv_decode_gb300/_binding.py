@@ -93,6 +93,8 @@ _SIGNATURES = [
     ("granikv_version", C.c_int32, []),
     ("granikv_create", C.c_int32, [C.POINTER(_Config), C.POINTER(C.c_void_p)]),
     ("granikv_create_kv8", C.c_int32, [C.POINTER(_Config), C.POINTER(C.c_void_p)]),
+    ("granikv_create_kv4", C.c_int32, [C.POINTER(_Config), C.POINTER(C.c_void_p)]),
+    ("granikv_kv4_row_bytes", C.c_int32, [C.c_int32, C.c_int32, C.POINTER(C.c_size_t)]),
     ("granikv_kv8_row_bytes", C.c_int32, [C.c_int32, C.c_int32, C.POINTER(C.c_size_t)]),
     ("granikv_destroy", C.c_int32, [C.c_void_p]),
     ("granikv_hot_alloc", C.c_int32, [C.c_void_p, C.c_int32, C.POINTER(C.c_int32), C.POINTER(C.c_int64)]),
@@ -100,6 +102,10 @@ _SIGNATURES = [
     ("granikv_hot_info", C.c_int32, [C.c_void_p, C.c_int32, C.POINTER(C.c_int64), C.POINTER(C.c_int32)]),
     ("granikv_hot_stats", C.c_int32, [C.c_void_p, C.POINTER(C.c_int64), C.POINTER(C.c_int64)]),
     ("granikv_hot_fill", C.c_int32, [C.c_void_p, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p]),
+    ("granikv_hot_read", C.c_int32, [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p,
+                                     C.c_void_p]),
+    ("granikv_cold_read", C.c_int32, [C.c_void_p, C.c_int32, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p,
+                                      C.c_void_p]),
     ("granikv_cold_alloc", C.c_int32, [C.c_void_p, C.POINTER(C.c_int32), C.c_int32, C.c_void_p,
                                        C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p]),
     ("granikv_cold_free", C.c_int32, [C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p]),
@@ -236,6 +242,13 @@ def kv8_row_bytes(n_kv: int, head_dim: int) -> int:
     """Bytes of one slot of an 8-bit pool (granikv_kv8_row_bytes)."""
     n = C.c_size_t()
     _check(load_library().granikv_kv8_row_bytes(n_kv, head_dim, C.byref(n)), "granikv_kv8_row_bytes")
+    return n.value
+
+
+def kv4_row_bytes(n_kv: int, head_dim: int) -> int:
+    """Bytes of one slot of a 4-bit pool (granikv_kv4_row_bytes)."""
+    n = C.c_size_t()
+    _check(load_library().granikv_kv4_row_bytes(n_kv, head_dim, C.byref(n)), "granikv_kv4_row_bytes")
     return n.value
 
 
@@ -399,8 +412,11 @@ class Context:
                  n_slots: int, k_pools=(), v_pools=(), hot_fraction: float = 0.2,
                  cold_init_order: Optional[Sequence[int]] = None, m_sat: int = 0,
                  max_slabs: int = 0, max_batch: int = 0, device: int = 0, host_only: bool = False,
-                 kv8: bool = False):
-        """kv8: an 8-bit cache (granikv_create_kv8); the pools are then bytes [n_slots, kv8_row_bytes(...)]."""
+                 kv8: bool = False, kv4: bool = False):
+        """kv8: an 8-bit cache (granikv_create_kv8); the pools are then bytes [n_slots, kv8_row_bytes(...)].
+        kv4: a 4-bit one (granikv_create_kv4), [n_slots, kv4_row_bytes(...)]."""
+        if kv8 and kv4:
+            raise ValueError("a cache is kept in 8 bits or in 4")
         self._lib = load_library()
         self._kp = (C.c_void_p * max(1, n_layers))(*[_ptr(p) for p in k_pools]) if k_pools else None
         self._vp = (C.c_void_p * max(1, n_layers))(*[_ptr(p) for p in v_pools]) if v_pools else None
@@ -413,10 +429,12 @@ class Context:
         h = C.c_void_p()
         if kv8:
             _check(self._lib.granikv_create_kv8(C.byref(cfg), C.byref(h)), "granikv_create_kv8")
+        elif kv4:
+            _check(self._lib.granikv_create_kv4(C.byref(cfg), C.byref(h)), "granikv_create_kv4")
         else:
             _check(self._lib.granikv_create(C.byref(cfg), C.byref(h)), "granikv_create")
         self.handle = h
-        self.n_q, self.n_kv, self.head_dim, self.dtype, self.kv8 = n_q, n_kv, head_dim, dtype, kv8
+        self.n_q, self.n_kv, self.head_dim, self.dtype, self.kv8, self.kv4 = n_q, n_kv, head_dim, dtype, kv8, kv4
         self._indexes = []
 
     def index(self) -> Index:
@@ -460,6 +478,11 @@ class Context:
         _check(self._lib.granikv_hot_fill(self.handle, layer, slab_id, _ptr(k), _ptr(v), _stream(stream)),
                "granikv_hot_fill")
 
+    def hot_read(self, layer: int, slab_id: int, t0: int, n: int, k, v, stream=None):
+        """Tokens [t0, t0 + n) of a slab as k, v [n, n_kv, head_dim] of the context's dtype."""
+        _check(self._lib.granikv_hot_read(self.handle, layer, slab_id, t0, n, _ptr(k), _ptr(v), _stream(stream)),
+               "granikv_hot_read")
+
     # COLD pool
     def cold_alloc(self, n_new: Sequence[int], req_to_slot, suffix_len, cap: int, slots_out=None, stream=None):
         arr = _i32_array(n_new)
@@ -485,6 +508,11 @@ class Context:
     def cold_append(self, layer: int, k_new, v_new, slots, N: int, stream=None):
         _check(self._lib.granikv_cold_append(self.handle, layer, _ptr(k_new), _ptr(v_new), _ptr(slots), N,
                                              _stream(stream)), "granikv_cold_append")
+
+    def cold_read(self, layer: int, slots, N: int, k, v, stream=None):
+        """The tokens at COLD slots[0:N] as k, v [N, n_kv, head_dim] of the context's dtype."""
+        _check(self._lib.granikv_cold_read(self.handle, layer, _ptr(slots), N, _ptr(k), _ptr(v), _stream(stream)),
+               "granikv_cold_read")
 
     # eviction of COLD tokens
     def cold_weigh(self, layer: int, q, lse, batch: Batch, weight, keep: float = 1.0, stream=None):

@@ -21,21 +21,26 @@ class GraniKVCache:
     """Per-layer K/V pools [n_slots, n_kv, d], per-request COLD token tables, and a context.
 
     kv8: the pools hold e4m3 codes with fp32 scales, one packed row of bytes a slot
-    (granikv_create_kv8); K and V are still given in `dtype`."""
+    (granikv_create_kv8); K and V are still given in `dtype`.  kv4: 4-bit codes with a scale for each
+    16 and a power of two for each block of tokens (granikv_create_kv4)."""
 
     def __init__(self, *, n_layers: int, n_q: int, n_kv: int, head_dim: int, dtype: int,
                  n_slots: int, max_batch: int, cap: int, hot_fraction: float = 0.2,
                  cold_init_order: Optional[Sequence[int]] = None, m_sat: int = 0,
-                 device: int = 0, max_slabs: int = 0, kv8: bool = False):
+                 device: int = 0, max_slabs: int = 0, kv8: bool = False, kv4: bool = False):
         if not torch.cuda.is_available():
             raise RuntimeError("GraniKVCache needs a CUDA device")
         self.device = torch.device("cuda", device)
         self.tdtype = _TORCH_DTYPE[dtype]
         self.n_layers, self.n_q, self.n_kv, self.head_dim = n_layers, n_q, n_kv, head_dim
         self.dtype, self.n_slots, self.cap, self.max_batch = dtype, n_slots, cap, max_batch
-        self.kv8 = kv8
-        shape = (n_slots, gb.kv8_row_bytes(n_kv, head_dim)) if kv8 else (n_slots, n_kv, head_dim)
-        pool_dtype = torch.uint8 if kv8 else self.tdtype
+        self.kv8, self.kv4 = kv8, kv4
+        if kv8 and kv4:
+            raise ValueError("a cache is kept in 8 bits or in 4")
+        if kv8 or kv4:
+            shape, pool_dtype = (n_slots, (gb.kv8_row_bytes if kv8 else gb.kv4_row_bytes)(n_kv, head_dim)), torch.uint8
+        else:
+            shape, pool_dtype = (n_slots, n_kv, head_dim), self.tdtype
         self.k_pools: List[torch.Tensor] = []
         self.v_pools: List[torch.Tensor] = []
         for _ in range(n_layers):
@@ -44,7 +49,7 @@ class GraniKVCache:
         self.ctx = gb.Context(n_layers=n_layers, n_q=n_q, n_kv=n_kv, head_dim=head_dim, dtype=dtype,
                               n_slots=n_slots, k_pools=self.k_pools, v_pools=self.v_pools,
                               hot_fraction=hot_fraction, cold_init_order=cold_init_order,
-                              m_sat=m_sat, max_batch=max_batch, device=device, max_slabs=max_slabs, kv8=kv8)
+                              m_sat=m_sat, max_batch=max_batch, device=device, max_slabs=max_slabs, kv8=kv8, kv4=kv4)
         self.req_to_slot = torch.zeros((max_batch, cap), dtype=torch.int32, device=self.device)
         self.suffix_len = torch.zeros((max_batch,), dtype=torch.int32, device=self.device)
         self.seq_len_host = [0] * max_batch
@@ -196,6 +201,24 @@ class GraniKVCache:
                                      slots_out, N, s)
         return slots_out[:N]
 
+    def read(self, layer: int, b: int):
+        """K and V of request row b in one layer, [tokens, n_kv, d] each in `dtype`: its HOT prefix, if it was
+        attached to one, then its COLD tokens.  A packed cache gives the values that it holds, so the rows can
+        be handed to another cache."""
+        n = self.seq_len_host[b]
+        pid, shared = self.row_prefix[b] or (-1, 0)
+        slab, L_p = -1, 0
+        if pid >= 0:
+            info = self.index.info(pid)
+            slab, L_p = (info["slab_id"], info["length"]) if info["slab_id"] >= 0 else (-1, 0)
+        k, v = (torch.empty((L_p + n, self.n_kv, self.head_dim), dtype=self.tdtype, device=self.device) for _ in range(2))
+        s = self.stream()
+        if slab >= 0:
+            self.ctx.hot_read(layer, slab, 0, L_p, k, v, s)
+        if n:
+            self.ctx.cold_read(layer, self.req_to_slot[b, :n], n, k[L_p:], v[L_p:], s)
+        return k, v
+
     # eviction of COLD tokens --------------------------------------------------------------
     @property
     def weight(self) -> torch.Tensor:
@@ -295,7 +318,7 @@ class GraniKVCache:
         """Causal prefill of a HOT prefix in one layer: its K/V ([L_p, n_kv, d], if given) are
         written into the slab, then each of its L_p query tokens (q [L_p, n_q, d]) attends the
         slab up to itself.  Returns (o [L_p, n_q, d], lse [L_p, n_q]).  Refused (ERR_UNSUPPORTED)
-        on an 8-bit cache: prefill in 16 bits and give the K/V to admit()."""
+        on an 8- or 4-bit cache: prefill in 16 bits and give the K/V to admit()."""
         L_p = q.shape[0]
         if o is None:
             o = torch.empty((L_p, self.n_q, self.head_dim), dtype=self.tdtype, device=self.device)

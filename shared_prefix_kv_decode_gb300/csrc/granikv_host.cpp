@@ -86,8 +86,9 @@ struct granikv_ctx {
   // TMA descriptors of each layer's K and V pools (dense backend), valid when has_tmaps
   std::vector<CUtensorMap> tmap_k, tmap_v;
   bool has_tmaps = false;
-  // 8-bit cache (granikv_create_kv8): bytes of a slot's packed row, else 0
-  int64_t kv8_row = 0;
+  // 8- or 4-bit cache (granikv_create_kv8, _kv4): bytes of a slot's packed row, and 8 or 4; else 0
+  int64_t packed_row = 0;
+  int32_t packed_bits = 0;
 };
 
 struct granikv_plan {
@@ -169,8 +170,8 @@ bool has_device(const granikv_ctx* c) { return c && !c->cfg.host_only && c->d_ri
 
 // Which prefix implementation serves a group of this shape and backend.
 int32_t prefix_impl_for(const granikv_ctx* c, int32_t backend) {
-  if (c->kv8_row) {
-    const bool dense = backend == GRANIKV_BACKEND_DENSE && c->cfg.dtype == GRANIKV_DTYPE_BF16 &&
+  if (c->packed_row) {
+    const bool dense = c->packed_bits == 8 && backend == GRANIKV_BACKEND_DENSE && c->cfg.dtype == GRANIKV_DTYPE_BF16 &&
                        c->cfg.head_dim == 128 && (c->has_tmaps || c->cfg.host_only);
     return dense ? kImplKv8Dense : kImplKv8Generic;
   }
@@ -192,7 +193,7 @@ bool runs_alone(int32_t impl) { return impl == kImplGeneric || impl == kImplDens
 // Which kernel attends the COLD suffix.
 int32_t suffix_impl_for(const granikv_ctx* c) {
   const bool mma = c->cfg.dtype == GRANIKV_DTYPE_BF16 && c->cfg.head_dim == 128 && c->g <= 8;
-  if (c->kv8_row) return mma ? kImplKv8Suffix : kImplKv8Generic;
+  if (c->packed_row) return mma && c->packed_bits == 8 ? kImplKv8Suffix : kImplKv8Generic;
   return mma ? kImplSuffixMma : kImplGeneric;
 }
 
@@ -502,7 +503,13 @@ int32_t granikv_version(void) { return 100; }
 }  // extern "C"
 
 namespace {
-granikv_status create_impl(const granikv_config* cfg, bool kv8, granikv_ctx** out) {
+// Bytes of a slot's packed row, 0 for a cache of 16 or 32 bits.
+int64_t packed_row_bytes(int32_t bits, int32_t n_kv, int32_t d) {
+  return bits == 8 ? kv8_row_bytes(n_kv, d) : bits == 4 ? kv4_row_bytes(n_kv, d) : 0;
+}
+
+// bits: 8 or 4 for a packed cache, 0 for one of cfg->dtype.
+granikv_status create_impl(const granikv_config* cfg, int32_t bits, granikv_ctx** out) {
   if (!cfg || !out) return GRANIKV_ERR_INVALID;
   *out = nullptr;
   if (cfg->n_layers <= 0 || cfg->n_q <= 0 || cfg->n_kv <= 0 || cfg->n_q % cfg->n_kv)
@@ -514,16 +521,17 @@ granikv_status create_impl(const granikv_config* cfg, bool kv8, granikv_ctx** ou
   if (!(fp > 0.0 && fp < 1.0)) return GRANIKV_ERR_INVALID;
   if (cfg->max_slabs < 0 || cfg->max_batch < 0 || cfg->m_sat < 0) return GRANIKV_ERR_INVALID;
 
-  if (kv8 && kv8_row_bytes(cfg->n_kv, cfg->head_dim) > kKv8MaxRow) return GRANIKV_ERR_UNSUPPORTED;
+  if (packed_row_bytes(bits, cfg->n_kv, cfg->head_dim) > kKv8MaxRow) return GRANIKV_ERR_UNSUPPORTED;
 
   granikv_ctx* c = new (std::nothrow) granikv_ctx();
   if (!c) return GRANIKV_ERR_INVALID;
   c->cfg = *cfg;
-  if (kv8) c->kv8_row = kv8_row_bytes(cfg->n_kv, cfg->head_dim);
+  c->packed_bits = bits;
+  c->packed_row = packed_row_bytes(bits, cfg->n_kv, cfg->head_dim);
   c->cfg.hot_fraction = fp;
   if (c->cfg.max_slabs == 0) c->cfg.max_slabs = kDefaultMaxSlabs;
   if (c->cfg.max_batch == 0) c->cfg.max_batch = kDefaultMaxBatch;
-  c->m_sat = cfg->m_sat ? cfg->m_sat : kv8 ? kDefaultMsatKv8 : kDefaultMsat;
+  c->m_sat = cfg->m_sat ? cfg->m_sat : bits ? kDefaultMsatKv8 : kDefaultMsat;
   c->g = cfg->n_q / cfg->n_kv;
   c->n_hot = (int64_t)std::floor(fp * (double)cfg->n_slots);
   c->n_cold = cfg->n_slots - c->n_hot;
@@ -597,9 +605,9 @@ granikv_status create_impl(const granikv_config* cfg, bool kv8, granikv_ctx** ou
       c->tmap_v.resize(cfg->n_layers);
       bool ok = true;
       for (int32_t l = 0; l < cfg->n_layers && ok; ++l) {
-        if (kv8) {
-          ok = encode_kv8_map(&c->tmap_k[l], c->kpool[l], cfg->n_slots, cfg->n_kv, c->kv8_row, kDenseTile, true) &&
-               encode_kv8_map(&c->tmap_v[l], c->vpool[l], cfg->n_slots, cfg->n_kv, c->kv8_row, kKv8VBox, false);
+        if (bits) {
+          ok = encode_kv8_map(&c->tmap_k[l], c->kpool[l], cfg->n_slots, cfg->n_kv, c->packed_row, kDenseTile, true) &&
+               encode_kv8_map(&c->tmap_v[l], c->vpool[l], cfg->n_slots, cfg->n_kv, c->packed_row, kKv8VBox, false);
           continue;
         }
         ok = ((uintptr_t)c->kpool[l] % 16 == 0) && ((uintptr_t)c->vpool[l] % 16 == 0) &&
@@ -628,16 +636,26 @@ granikv_status create_impl(const granikv_config* cfg, bool kv8, granikv_ctx** ou
 
 extern "C" {
 
-granikv_status granikv_create(const granikv_config* cfg, granikv_ctx** out) { return create_impl(cfg, false, out); }
+granikv_status granikv_create(const granikv_config* cfg, granikv_ctx** out) { return create_impl(cfg, 0, out); }
 
-granikv_status granikv_create_kv8(const granikv_config* cfg, granikv_ctx** out) { return create_impl(cfg, true, out); }
+granikv_status granikv_create_kv8(const granikv_config* cfg, granikv_ctx** out) { return create_impl(cfg, 8, out); }
 
-granikv_status granikv_kv8_row_bytes(int32_t n_kv, int32_t head_dim, size_t* bytes) {
+granikv_status granikv_create_kv4(const granikv_config* cfg, granikv_ctx** out) { return create_impl(cfg, 4, out); }
+
+static granikv_status row_bytes_impl(int32_t bits, int32_t n_kv, int32_t head_dim, size_t* bytes) {
   if (!bytes || n_kv <= 0) return GRANIKV_ERR_INVALID;
   if (head_dim <= 0 || head_dim % 32 || head_dim > 256) return GRANIKV_ERR_UNSUPPORTED;
-  if (kv8_row_bytes(n_kv, head_dim) > kKv8MaxRow) return GRANIKV_ERR_UNSUPPORTED;
-  *bytes = (size_t)kv8_row_bytes(n_kv, head_dim);
+  if (packed_row_bytes(bits, n_kv, head_dim) > kKv8MaxRow) return GRANIKV_ERR_UNSUPPORTED;
+  *bytes = (size_t)packed_row_bytes(bits, n_kv, head_dim);
   return GRANIKV_OK;
+}
+
+granikv_status granikv_kv8_row_bytes(int32_t n_kv, int32_t head_dim, size_t* bytes) {
+  return row_bytes_impl(8, n_kv, head_dim, bytes);
+}
+
+granikv_status granikv_kv4_row_bytes(int32_t n_kv, int32_t head_dim, size_t* bytes) {
+  return row_bytes_impl(4, n_kv, head_dim, bytes);
 }
 
 granikv_status granikv_destroy(granikv_ctx* c) {
@@ -730,14 +748,14 @@ granikv_status granikv_hot_fill(granikv_ctx* c, int32_t layer, int32_t sid, cons
                                 const void* v, granikv_stream_t stream) {
   if (!c || !k || !v || layer < 0 || layer >= c->cfg.n_layers) return GRANIKV_ERR_INVALID;
   if (sid < 0 || sid >= (int32_t)c->slabs.size() || !c->slabs[sid].live) return GRANIKV_ERR_INVALID;
-  if (c->kv8_row && ((uintptr_t)k | (uintptr_t)v) % 16) return GRANIKV_ERR_INVALID;
+  if (c->packed_row && ((uintptr_t)k | (uintptr_t)v) % 16) return GRANIKV_ERR_INVALID;
   if (!has_device(c)) return GRANIKV_ERR_NO_DEVICE;
   DeviceGuard dg(c->cfg.device);
-  if (c->kv8_row) {
+  if (c->packed_row) {
     c->n_kernels += 1;
-    return cuda_status(launch_kv8_fill(c->cfg.dtype, k, v, c->slabs[sid].len, (uint8_t*)c->kpool[layer],
-                                       (uint8_t*)c->vpool[layer], c->slabs[sid].off, c->cfg.n_kv, c->cfg.head_dim,
-                                       (cudaStream_t)stream));
+    const auto fill = c->packed_bits == 4 ? launch_kv4_fill : launch_kv8_fill;
+    return cuda_status(fill(c->cfg.dtype, k, v, c->slabs[sid].len, (uint8_t*)c->kpool[layer], (uint8_t*)c->vpool[layer],
+                            c->slabs[sid].off, c->cfg.n_kv, c->cfg.head_dim, (cudaStream_t)stream));
   }
   size_t row = (size_t)c->cfg.n_kv * c->cfg.head_dim * elem_size(c->cfg.dtype);
   size_t off = (size_t)c->slabs[sid].off * row;
@@ -747,6 +765,48 @@ granikv_status granikv_hot_fill(granikv_ctx* c, int32_t layer, int32_t sid, cons
   if (e == cudaSuccess)
     e = cudaMemcpyAsync((char*)c->vpool[layer] + off, v, bytes, cudaMemcpyDeviceToDevice, s);
   return cuda_status(e);
+}
+
+// ---- rows out of the pools ------------------------------------------------------------------
+
+static granikv_status read_impl(granikv_ctx* c, int32_t layer, const int32_t* slots, int64_t first_slot, int32_t n,
+                                void* k, void* v, granikv_stream_t stream) {
+  DeviceGuard dg(c->cfg.device);
+  ReadParams a{};
+  a.pool[0] = (const uint8_t*)c->kpool[layer];
+  a.pool[1] = (const uint8_t*)c->vpool[layer];
+  a.out[0] = k;
+  a.out[1] = v;
+  a.slots = slots;
+  a.first_slot = first_slot;
+  a.n_hot = c->n_hot;
+  a.n_slots = c->cfg.n_slots;
+  a.row = c->packed_row ? c->packed_row : (int64_t)c->cfg.n_kv * c->cfg.head_dim * elem_size(c->cfg.dtype);
+  a.N = n;
+  a.n_kv = c->cfg.n_kv;
+  a.err = c->d_err;
+  c->n_kernels += 1;
+  return cuda_status(launch_read(c->cfg.dtype, c->packed_bits, c->cfg.head_dim, a, (cudaStream_t)stream));
+}
+
+granikv_status granikv_hot_read(granikv_ctx* c, int32_t layer, int32_t sid, int32_t t0, int32_t n, void* k, void* v,
+                                granikv_stream_t stream) {
+  if (!c || layer < 0 || layer >= c->cfg.n_layers || n < 0 || t0 < 0) return GRANIKV_ERR_INVALID;
+  if (sid < 0 || sid >= (int32_t)c->slabs.size() || !c->slabs[sid].live) return GRANIKV_ERR_INVALID;
+  if ((int64_t)t0 + n > c->slabs[sid].len) return GRANIKV_ERR_INVALID;
+  if (n > 0 && (!k || !v || ((uintptr_t)k | (uintptr_t)v) % 16)) return GRANIKV_ERR_INVALID;
+  if (!has_device(c)) return GRANIKV_ERR_NO_DEVICE;
+  if (n == 0) return GRANIKV_OK;
+  return read_impl(c, layer, nullptr, c->slabs[sid].off + t0, n, k, v, stream);
+}
+
+granikv_status granikv_cold_read(granikv_ctx* c, int32_t layer, const int32_t* slots, int32_t n, void* k, void* v,
+                                 granikv_stream_t stream) {
+  if (!c || layer < 0 || layer >= c->cfg.n_layers || n < 0) return GRANIKV_ERR_INVALID;
+  if (n > 0 && (!slots || !k || !v || ((uintptr_t)k | (uintptr_t)v) % 16)) return GRANIKV_ERR_INVALID;
+  if (!has_device(c)) return GRANIKV_ERR_NO_DEVICE;
+  if (n == 0) return GRANIKV_OK;
+  return read_impl(c, layer, slots, 0, n, k, v, stream);
 }
 
 // ---- COLD pool ------------------------------------------------------------------------------
@@ -837,15 +897,15 @@ granikv_status granikv_cold_append(granikv_ctx* c, int32_t layer, const void* k_
                                    granikv_stream_t stream) {
   if (!c || layer < 0 || layer >= c->cfg.n_layers || N < 0) return GRANIKV_ERR_INVALID;
   if (N > 0 && (!k_new || !v_new || !slots)) return GRANIKV_ERR_INVALID;
-  if (c->kv8_row && ((uintptr_t)k_new | (uintptr_t)v_new) % 16) return GRANIKV_ERR_INVALID;
+  if (c->packed_row && ((uintptr_t)k_new | (uintptr_t)v_new) % 16) return GRANIKV_ERR_INVALID;
   if (!has_device(c)) return GRANIKV_ERR_NO_DEVICE;
   if (N == 0) return GRANIKV_OK;
   DeviceGuard dg(c->cfg.device);
-  if (c->kv8_row) {
+  if (c->packed_row) {
     c->n_kernels += 1;
-    return cuda_status(launch_kv8_append(c->cfg.dtype, k_new, v_new, slots, N, (uint8_t*)c->kpool[layer],
-                                         (uint8_t*)c->vpool[layer], c->cfg.n_kv, c->cfg.head_dim, c->n_hot,
-                                         c->cfg.n_slots, c->d_err, (cudaStream_t)stream));
+    const auto append = c->packed_bits == 4 ? launch_kv4_append : launch_kv8_append;
+    return cuda_status(append(c->cfg.dtype, k_new, v_new, slots, N, (uint8_t*)c->kpool[layer], (uint8_t*)c->vpool[layer],
+                              c->cfg.n_kv, c->cfg.head_dim, c->n_hot, c->cfg.n_slots, c->d_err, (cudaStream_t)stream));
   }
   cudaError_t e = launch_cold_append(c->cfg.dtype, k_new, v_new, slots, N, c->kpool[layer],
                                      c->vpool[layer], (int64_t)c->cfg.n_kv * c->cfg.head_dim,
@@ -875,7 +935,8 @@ granikv_status granikv_cold_weigh(granikv_ctx* c, int32_t layer, const void* q, 
   a.q = q;
   a.lse = lse;
   a.kpool = c->kpool[layer];
-  a.kv8_row = c->kv8_row;
+  a.packed_row = c->packed_row;
+  a.packed_bits = c->packed_bits;
   a.req_to_slot = bt->req_to_slot;
   a.live_len = bt->seq_len_dev;
   a.weight = weight;
@@ -1045,7 +1106,7 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
   // Fused merge when every kernel of the step is a tensor-core kernel; then the suffix may run
   // next to the prefix on its own share of the SMs.
   const bool fast_suffix_pre = token_ctas(suffix_impl_for(c));
-  bool fused = c->fused_merge && !c->kv8_row && (fast_suffix_pre || T_all == 0);
+  bool fused = c->fused_merge && !c->packed_row && (fast_suffix_pre || T_all == 0);
   for (int32_t i = 0; i < G; ++i)
     if (runs_alone(groups[i].impl)) fused = false;
   bool fast_all = fast_suffix_pre || T_all == 0;
@@ -1059,7 +1120,7 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
   int32_t suffix_sms = c->num_sms;  // set after the prefix pieces when the SMs are split
   bool read_ahead = false;          // the split's dense CTAs read ahead into L2 (see below)
   double tail_frac = 0.0;           // share of the suffix work the dense CTAs take after their piece
-  const int64_t seg_tiles = c->kv8_row ? kSegTilesKv8 : kSegTiles;
+  const int64_t seg_tiles = c->packed_row ? kSegTilesKv8 : kSegTiles;
   bool kv8_split = false;           // 8-bit cache: the split and its runs' shares as planned below
   int32_t kv8_main = 0;             // its suffix CTAs
   std::vector<double>& share = w.share;
@@ -1099,7 +1160,7 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
       if (groups[i].impl == kImplKv8Generic)
         lo = std::max(lo, std::min(max_tiles, (int64_t)std::ceil(std::sqrt(8.0 * (double)groups[i].L_p) / kGenericTile)));
     bool auto_found = false;
-    bool kv8_dense = auto_share && c->kv8_row && n_kv <= 8;
+    bool kv8_dense = auto_share && c->packed_row && n_kv <= 8;
     for (int32_t i = 0; i < G; ++i) kv8_dense = kv8_dense && groups[i].impl == kImplKv8Dense;
     if (kv8_dense) {
       // 8-bit cache: every SM works until the end.  With pieces of a given length, dense CTA k is done
@@ -1191,8 +1252,8 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
       // the suffix then bound by the bandwidth HBM gives its random 2 KB row reads (about
       // 5.8 TB/s measured), and the step's bytes bounding either way at about 5.9 TB/s.
       const int64_t head_groups = (n_kv + 7) / 8;
-      const double w_s = (c->kv8_row ? 0.75 : 1.40) * (double)head_groups * (double)T_tiles;
-      const double token_bytes = c->kv8_row ? 2.0 * (double)c->kv8_row : 4.0 * n_kv * c->cfg.head_dim;
+      const double w_s = (c->packed_row ? 0.75 : 1.40) * (double)head_groups * (double)T_tiles;
+      const double token_bytes = c->packed_row ? 2.0 * (double)c->packed_row : 4.0 * n_kv * c->cfg.head_dim;
       const double suffix_bytes = token_bytes * (double)T_all;
       double prefix_bytes = 0.0;
       for (int32_t i = 0; i < G; ++i) prefix_bytes += token_bytes * (double)groups[i].L_p;
@@ -1722,7 +1783,7 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
                                      float* lse, void* ws, size_t ws_bytes, granikv_stream_t stream) {
   if (!c || !bt || !q || !o || !lse || !ws) return GRANIKV_ERR_INVALID;
   if (layer < 0 || layer >= c->cfg.n_layers) return GRANIKV_ERR_INVALID;
-  if (c->kv8_row && ((uintptr_t)q | (uintptr_t)o) % 16) return GRANIKV_ERR_INVALID;
+  if (c->packed_row && ((uintptr_t)q | (uintptr_t)o) % 16) return GRANIKV_ERR_INVALID;
   if (!has_device(c)) return GRANIKV_ERR_NO_DEVICE;
   if ((uintptr_t)ws % 256) return GRANIKV_ERR_INVALID;
   if (!bt->req_to_slot) return GRANIKV_ERR_INVALID;
@@ -1796,7 +1857,8 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
   a.live_len = bt->seq_len_dev;
   a.k_new = k_new;
   a.v_new = v_new;
-  a.kv8_row = c->kv8_row;
+  a.packed_row = c->packed_row;
+  a.packed_bits = c->packed_bits;
   CUtensorMap tmq{};
   a.q_tma = 0;
   if (p->pitem_count[kImplDenseTc] > 0 && c->cfg.dtype == GRANIKV_DTYPE_BF16 && c->cfg.head_dim == 128)
@@ -1805,11 +1867,12 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
   c->last_tickets_bytes = tickets_bytes;
 
   cudaError_t e = cudaSuccess;
+  const auto packed_generic = c->packed_bits == 4 ? launch_kv4_generic : launch_kv8_generic;
   auto launch_suffix = [&](cudaStream_t st, bool pdl) -> cudaError_t {
     if (p->n_sitems <= 0) return cudaSuccess;
     c->n_kernels += 1;
     if (p->suffix_impl == kImplKv8Suffix) return launch_kv8_suffix(a, a.scta_begin, p->n_scta, st, pdl);
-    if (p->suffix_impl == kImplKv8Generic) return launch_kv8_generic(c->cfg.dtype, a, 0, 0, true, st, false);
+    if (p->suffix_impl == kImplKv8Generic) return packed_generic(c->cfg.dtype, a, 0, 0, true, st, false);
     return p->suffix_impl == kImplSuffixMma ? launch_suffix_mma(a, a.scta_begin, p->n_scta, st, pdl)
                                             : launch_suffix_generic(c->cfg.dtype, a, st);
   };
@@ -1822,7 +1885,7 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
       c->n_kernels += 1;
     }
     if (r == cudaSuccess && p->pitem_count[kImplKv8Generic] > 0) {
-      r = launch_kv8_generic(c->cfg.dtype, a, p->pitem_first[kImplKv8Generic], p->pitem_count[kImplKv8Generic], false, st, false);
+      r = packed_generic(c->cfg.dtype, a, p->pitem_first[kImplKv8Generic], p->pitem_count[kImplKv8Generic], false, st, false);
       c->n_kernels += 1;
     }
     if (r == cudaSuccess && p->pitem_count[kImplKv8Dense] > 0) {
@@ -1859,9 +1922,9 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
     if (c->cfg.dtype == GRANIKV_DTYPE_BF16 && c->cfg.head_dim == 128) return launch_merge_rows(a, p->merge_warps, s, pdl);
     return launch_merge(c->cfg.dtype, a, s, pdl);
   };
-  // 8-bit cache: the newest rows are quantised into their slots before anything reads them
-  if (k_new && c->kv8_row) {
-    e = launch_kv8_append_newest(c->cfg.dtype, a, s);
+  // packed cache: the newest rows are quantised into their slots before anything reads them
+  if (k_new && c->packed_row) {
+    e = (c->packed_bits == 4 ? launch_kv4_append_newest : launch_kv8_append_newest)(c->cfg.dtype, a, s);
     c->n_kernels += 1;
     if (e != cudaSuccess) return cuda_status(e);
   }
@@ -1879,7 +1942,7 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
   }
   if (p->n_pitems > 0 && p->pitem_count[kImplKv8Generic] == p->n_pitems && p->suffix_impl == kImplKv8Generic) {
     // CUDA-core prefix and suffix items in one launch, then the merge
-    e = launch_kv8_generic(c->cfg.dtype, a, p->pitem_first[kImplKv8Generic], p->n_pitems, p->n_sitems > 0, s, true);
+    e = packed_generic(c->cfg.dtype, a, p->pitem_first[kImplKv8Generic], p->n_pitems, p->n_sitems > 0, s, true);
     c->n_kernels += 1;
     if (e == cudaSuccess) e = launch_merge_k(true);
     return cuda_status(e);
@@ -1986,7 +2049,7 @@ granikv_status granikv_prefill_attention(granikv_ctx* c, int32_t layer, int32_t 
   if ((k_new == nullptr) != (v_new == nullptr)) return GRANIKV_ERR_INVALID;
   if ((uintptr_t)ws % 256) return GRANIKV_ERR_INVALID;
   if (!has_device(c)) return GRANIKV_ERR_NO_DEVICE;
-  if (c->kv8_row || c->cfg.dtype != GRANIKV_DTYPE_BF16 || c->cfg.head_dim != 128 || !c->has_tmaps)
+  if (c->packed_row || c->cfg.dtype != GRANIKV_DTYPE_BF16 || c->cfg.head_dim != 128 || !c->has_tmaps)
     return GRANIKV_ERR_UNSUPPORTED;
   const int32_t L_p = c->slabs[sid].len;
   const PrefillLayout lay = prefill_layout(c, L_p);

@@ -130,7 +130,8 @@ struct AttnParams {
   const void* v_new;        // here (not the pool) and written to its slot by the suffix CTA
   const int32_t* live_len;  // [B] device token counts that end each request's suffix segments early
                             // (the plan may cover more tokens than exist yet); NULL: the plan's
-  int64_t kv8_row;          // 8-bit cache: bytes of a packed slot row (kv8_row_bytes), else 0
+  int64_t packed_row;       // 8- or 4-bit cache: bytes of a packed slot row (kv8_row_bytes, kv4_row_bytes), else 0
+  int32_t packed_bits;      // 8 or 4, else 0
 };
 
 // ---- 8-bit cache ---------------------------------------------------------------------------
@@ -146,6 +147,21 @@ __host__ __device__ inline int64_t kv8_row_bytes(int32_t n_kv, int32_t d) {
   return ((int64_t)n_kv * (d + 4) + 15) / 16 * 16;
 }
 
+// ---- 4-bit cache ---------------------------------------------------------------------------
+// One slot of a 4-bit pool is one packed row: e2m1 codes [n_kv, d] (two to a byte, the first in the low half),
+// e4m3 scales [n_kv, d / 16], padding to 16 bytes, an exponent byte a KV head, padding to 16 bytes
+// (kv4_util.cuh says what they stand for).  Every row carries its own exponents; the rows of one 64-token
+// block of a slab (kKv8Block) hold the same ones.
+constexpr int kKv4Group = 16;
+constexpr int kKv4ExpMin = -100, kKv4ExpMax = 116;
+__host__ __device__ constexpr int64_t kv4_scales_at(int32_t n_kv, int32_t d) { return (int64_t)n_kv * (d / 2); }
+__host__ __device__ constexpr int64_t kv4_units_at(int32_t n_kv, int32_t d) {
+  return ((int64_t)n_kv * (d / 2 + d / kKv4Group) + 15) / 16 * 16;
+}
+__host__ __device__ constexpr int64_t kv4_row_bytes(int32_t n_kv, int32_t d) {
+  return (kv4_units_at(n_kv, d) + n_kv + 15) / 16 * 16;
+}
+
 // Rows whose counts fit the parameters of one weighing or eviction launch (16 KB of 32).
 constexpr int kRowsPerLaunch = 1024;
 
@@ -158,8 +174,9 @@ struct EvictRow {
 struct WeighParams {
   const void* q;               // [B, n_q, d]
   const float* lse;            // [B, n_q]
-  const void* kpool;           // 16/32-bit rows [n_slots, n_kv, d], or packed 8-bit rows
-  int64_t kv8_row;             // bytes of a packed row, 0 for the 16/32-bit pools
+  const void* kpool;           // 16/32-bit rows [n_slots, n_kv, d], or packed rows
+  int64_t packed_row;          // bytes of a packed row, 0 for the 16/32-bit pools
+  int32_t packed_bits;         // 8 or 4, 0 for the 16/32-bit pools
   const int32_t* req_to_slot;  // [B, cap]
   const int32_t* live_len;     // [B] device
   float* weight;               // [B, cap]
@@ -232,6 +249,28 @@ cudaError_t launch_kv8_step(const AttnParams& p, int32_t first_dense, int32_t n_
                             const CUtensorMap& tmv, const int32_t* cta_begin, int32_t n_scta, int32_t n_tail,
                             cudaStream_t s, bool pdl);
 cudaError_t launch_kv8_suffix(const AttnParams& p, const int32_t* cta_begin, int32_t n_scta, cudaStream_t s, bool pdl);
+
+// 4-bit cache (kernels_kv4.cu): the same calls.
+cudaError_t launch_kv4_fill(int32_t dtype, const void* k, const void* v, int32_t L_p, uint8_t* kpool, uint8_t* vpool,
+                            int64_t first_slot, int32_t n_kv, int32_t d, cudaStream_t s);
+cudaError_t launch_kv4_append(int32_t dtype, const void* k_new, const void* v_new, const int32_t* slots, int32_t N,
+                              uint8_t* kpool, uint8_t* vpool, int32_t n_kv, int32_t d, int64_t n_hot,
+                              int64_t n_slots, int32_t* err, cudaStream_t s);
+cudaError_t launch_kv4_append_newest(int32_t dtype, const AttnParams& p, cudaStream_t s);
+cudaError_t launch_kv4_generic(int32_t dtype, const AttnParams& p, int32_t first_item, int32_t n_items, bool suffix,
+                               cudaStream_t s, bool pdl);
+
+// Rows out of the pools (kernels_read.cu): N rows at slots[i], or from first_slot on where slots is NULL, as
+// [N, n_kv, d] of dtype.  bits: 0 (the pools' rows are of dtype), 8 or 4.
+struct ReadParams {
+  const uint8_t* pool[2];  // K, V
+  void* out[2];
+  const int32_t* slots;
+  int64_t first_slot, n_hot, n_slots, row;  // row: bytes of a slot
+  int32_t N, n_kv;
+  int32_t* err;
+};
+cudaError_t launch_read(int32_t dtype, int32_t bits, int32_t d, const ReadParams& p, cudaStream_t s);
 
 // Eviction (kernels_evict.cu)
 cudaError_t launch_cold_weigh(int32_t dtype, const WeighParams& p, const int32_t* seq_len /*host [B]*/, cudaStream_t s);

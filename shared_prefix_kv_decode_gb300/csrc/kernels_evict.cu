@@ -3,6 +3,7 @@
 //
 // The token-level COLD pool (GraniKV, arXiv:2608.15584, "3 GraniKV": page size 1) lets single
 // tokens leave a request: their table entries close up and their slots go back to the free ring.
+#include "kv4_util.cuh"
 #include "kv8_util.cuh"
 #include "launch_util.cuh"
 #include "mma_util.cuh"
@@ -52,7 +53,7 @@ __device__ __forceinline__ void chunk_of(const WeighRows<N>& rows, const int32_t
 // its heads in order, the warps' sums are added in warp order.
 constexpr int kTok = 32;
 
-template <typename T, bool KV8, int N>
+template <typename T, int BITS, int N>
 __global__ void __launch_bounds__(256) weigh_generic_kernel(WeighParams p, const __grid_constant__ WeighRows<N> rows) {
   extern __shared__ float sm[];
   float* sK = sm;                       // [kTok][d + 1]
@@ -82,8 +83,21 @@ __global__ void __launch_bounds__(256) weigh_generic_kernel(WeighParams p, const
         const int32_t slot = s_slot[tok];
         float x[4] = {0.f, 0.f, 0.f, 0.f};
         if (slot >= 0) {
-          if constexpr (KV8) {
-            const uint8_t* row = (const uint8_t*)p.kpool + (int64_t)slot * p.kv8_row;
+          if constexpr (BITS == 4) {
+            const uint8_t* row = (const uint8_t*)p.kpool + (int64_t)slot * p.packed_row;
+            uint32_t y[4];
+            e2m1x8_to_f16x8(*reinterpret_cast<const uint16_t*>(row + (int64_t)j * (d / 2) + c / 2), y);
+            const uint32_t scale = kv4_scale2(row[kv4_scales_at(p.n_kv, d) + (int64_t)j * (d / kKv4Group) + c / kKv4Group]);
+            const float unit = kv4_unit(row[kv4_units_at(p.n_kv, d) + j]);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t h = f16x2_mul(y[u], scale);
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+              x[2 * u] = f.x * unit;
+              x[2 * u + 1] = f.y * unit;
+            }
+          } else if constexpr (BITS == 8) {
+            const uint8_t* row = (const uint8_t*)p.kpool + (int64_t)slot * p.packed_row;
             e4m3x4_to_f32x4(*reinterpret_cast<const uint32_t*>(row + (int64_t)j * d + c), x);
             const float s = *reinterpret_cast<const float*>(row + (int64_t)p.n_kv * d + 4 * j);
 #pragma unroll
@@ -191,7 +205,7 @@ __global__ void __launch_bounds__(256, WeighUnit<KV8, D>::kBlocks) weigh_mma_ker
       x.tile += 16;
     }
   };
-  const int32_t row_bytes = KV8 ? (int32_t)p.kv8_row : p.n_kv * D * 2;
+  const int32_t row_bytes = KV8 ? (int32_t)p.packed_row : p.n_kv * D * 2;
   // this lane's pieces of the rows of a unit into stage st (zeros for a slot that does not count)
   auto load_unit = [&](const Place& x, int st) {
     if (x.tile < n) {
@@ -659,19 +673,19 @@ cudaError_t weigh_mma(const WeighParams& p, const WeighRows<N>& rows, int32_t ch
   return cudaGetLastError();
 }
 
-template <typename T, bool KV8, int N>
+template <typename T, int BITS, int N>
 cudaError_t weigh_launch(const WeighParams& p, const WeighRows<N>& rows, int32_t chunks, cudaStream_t s) {
-  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+  if constexpr (std::is_same_v<T, __nv_bfloat16> && BITS != 4) {
     if (weigh_on_mma<T>(p)) {
-      return p.d == 128 ? weigh_mma<KV8, 128, N>(p, rows, chunks, s) : weigh_mma<KV8, 64, N>(p, rows, chunks, s);
+      return p.d == 128 ? weigh_mma<BITS == 8, 128, N>(p, rows, chunks, s) : weigh_mma<BITS == 8, 64, N>(p, rows, chunks, s);
     }
   }
   const int smem = (int)sizeof(float) * (kTok * (p.d + 1) + 8 * kTok);
-  weigh_generic_kernel<T, KV8, N><<<chunks, 256, smem, s>>>(p, rows);
+  weigh_generic_kernel<T, BITS, N><<<chunks, 256, smem, s>>>(p, rows);
   return cudaGetLastError();
 }
 
-template <typename T, bool KV8, int N>
+template <typename T, int BITS, int N>
 cudaError_t weigh_rows(const WeighParams& p, const int32_t* seq_len, int32_t b0, int32_t n, int tokens, cudaStream_t s) {
   WeighRows<N> rows;
   int64_t chunks = 0;
@@ -685,15 +699,15 @@ cudaError_t weigh_rows(const WeighParams& p, const int32_t* seq_len, int32_t b0,
   rows.n = n;
   rows.b0 = b0;
   rows.tokens = tokens;
-  return chunks ? weigh_launch<T, KV8, N>(p, rows, (int32_t)chunks, s) : cudaSuccess;
+  return chunks ? weigh_launch<T, BITS, N>(p, rows, (int32_t)chunks, s) : cudaSuccess;
 }
 
-template <typename T, bool KV8>
+template <typename T, int BITS>
 cudaError_t weigh_all(const WeighParams& p, const int32_t* seq_len, cudaStream_t s) {
   constexpr int kSmall = 64, kLarge = kRowsPerLaunch;
   int tokens = kTok;
-  if (weigh_on_mma<T>(p)) {
-    using Unit = WeighUnit<KV8, 128>;
+  if (BITS != 4 && weigh_on_mma<T>(p)) {
+    using Unit = WeighUnit<BITS == 8, 128>;
     const int most = std::max(kChunkMin, std::min(kChunkMax, Unit::kSums / (4 * p.n_kv) / 16 * 16));
     const int64_t slots = (int64_t)Unit::kBlocks * p.num_sms;
     // the fewest tokens a chunk, in steps of 16, with which the grid is one wave
@@ -709,8 +723,8 @@ cudaError_t weigh_all(const WeighParams& p, const int32_t* seq_len, cudaStream_t
   cudaError_t e = cudaSuccess;
   for (int32_t b = 0; b < p.B && e == cudaSuccess;) {
     const int32_t n = p.B - b < kLarge ? p.B - b : kLarge;
-    e = n <= kSmall ? weigh_rows<T, KV8, kSmall>(p, seq_len, b, n, tokens, s)
-                    : weigh_rows<T, KV8, kLarge>(p, seq_len, b, n, tokens, s);
+    e = n <= kSmall ? weigh_rows<T, BITS, kSmall>(p, seq_len, b, n, tokens, s)
+                    : weigh_rows<T, BITS, kLarge>(p, seq_len, b, n, tokens, s);
     b += n;
   }
   return e;
@@ -719,9 +733,11 @@ cudaError_t weigh_all(const WeighParams& p, const int32_t* seq_len, cudaStream_t
 }  // namespace
 
 cudaError_t launch_cold_weigh(int32_t dtype, const WeighParams& p, const int32_t* seq_len, cudaStream_t s) {
-  if (dtype == 1)
-    return p.kv8_row ? weigh_all<__nv_bfloat16, true>(p, seq_len, s) : weigh_all<__nv_bfloat16, false>(p, seq_len, s);
-  return p.kv8_row ? weigh_all<float, true>(p, seq_len, s) : weigh_all<float, false>(p, seq_len, s);
+  auto all = [&](auto t) {
+    using T = decltype(t);
+    return p.packed_bits == 4 ? weigh_all<T, 4>(p, seq_len, s) : p.packed_bits == 8 ? weigh_all<T, 8>(p, seq_len, s) : weigh_all<T, 0>(p, seq_len, s);
+  };
+  return dtype == 1 ? all(__nv_bfloat16{}) : all(0.f);
 }
 
 cudaError_t launch_cold_evict(const EvictRow* rows, int32_t B, int32_t num_sms, int32_t keep_last,

@@ -1,0 +1,112 @@
+// kernels_read.cu -- rows of a pool back as [N, n_kv, d]: of a 16- or 32-bit pool as they are, of a packed one as
+// the values that its codes and scales stand for, rounded once.  (4 bits: exact in bf16 and fp32.)
+#include "kv4_util.cuh"
+#include "launch_util.cuh"
+#include "tc_util.cuh"
+
+#include <type_traits>
+
+namespace granikv {
+namespace {
+
+__device__ __forceinline__ void store16(__nv_bfloat16* dst, const float (&x)[16]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  __stcs(reinterpret_cast<uint4*>(dst), make_uint4(w[0], w[1], w[2], w[3]));
+  __stcs(reinterpret_cast<uint4*>(dst) + 1, make_uint4(w[4], w[5], w[6], w[7]));
+}
+__device__ __forceinline__ void store16(float* dst, const float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    __stcs(reinterpret_cast<float4*>(dst) + i, make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+}
+
+// A thread takes 16 elements of one head of a row.
+template <int BITS, typename T>
+__device__ __forceinline__ void read16(const uint8_t* __restrict__ row, T* __restrict__ dst, int32_t n_kv, int32_t d, int32_t j, int32_t piece) {
+  if constexpr (BITS == 0) {
+    constexpr int kPieces = 16 * sizeof(T) / 16;
+    const uint4* src = reinterpret_cast<const uint4*>(row) + ((int64_t)j * (d / 16) + piece) * kPieces;
+    uint4 w[kPieces];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) w[i] = __ldcs(src + i);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) __stcs(reinterpret_cast<uint4*>(dst) + i, w[i]);
+  } else if constexpr (BITS == 8) {
+    const uint4 w = __ldcs(reinterpret_cast<const uint4*>(row + (int64_t)j * d + piece * 16));
+    const float s = *reinterpret_cast<const float*>(row + (int64_t)n_kv * d + 4 * j);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float f[4];
+      e4m3x4_to_f32x4(u[i], f);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[4 * i + c] = f[c] * s;
+    }
+    store16(dst, x);
+  } else {
+    const uint2 w = __ldcs(reinterpret_cast<const uint2*>(row + (int64_t)j * (d / 2) + piece * 8));
+    const uint32_t b = kv4_scale2(row[kv4_scales_at(n_kv, d) + (int64_t)j * (d / kKv4Group) + piece]);
+    const float t = kv4_unit(row[kv4_units_at(n_kv, d) + j]);
+    float x[16];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t y[4];
+      e2m1x8_to_f16x8(h ? w.y : w.x, y);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t p = f16x2_mul(y[i], b);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p));
+        x[8 * h + 2 * i] = f.x * t;
+        x[8 * h + 2 * i + 1] = f.y * t;
+      }
+    }
+    store16(dst, x);
+  }
+}
+
+template <int BITS, typename T>
+__global__ void __launch_bounds__(256) read_kernel(ReadParams p, int32_t d, int32_t tokens) {
+  const int32_t per_head = d / 16, per_row = p.n_kv * per_head;
+  const uint8_t* pool = blockIdx.y ? p.pool[1] : p.pool[0];
+  T* out = (T*)(blockIdx.y ? p.out[1] : p.out[0]);
+  const int64_t t0 = (int64_t)blockIdx.x * tokens;
+  const int32_t n = (int32_t)min((int64_t)tokens, p.N - t0) * per_row;
+  for (int32_t i = threadIdx.x; i < n; i += 256) {
+    const int32_t t = i / per_row, h = i - t * per_row, j = h / per_head;
+    int64_t slot = p.first_slot + t0 + t;
+    if (p.slots) {
+      slot = p.slots[t0 + t];
+      if (slot < p.n_hot || slot >= p.n_slots) {  // its row is left as it was
+        if (h == 0) atomicCAS(p.err, 0, (int32_t)kDevBadSlot);
+        continue;
+      }
+    }
+    read16<BITS, T>(pool + slot * p.row, out + ((t0 + t) * per_row + h) * 16, p.n_kv, d, j, h - j * per_head);
+  }
+}
+
+template <int BITS>
+cudaError_t read_bits(int32_t dtype, int32_t d, const ReadParams& p, cudaStream_t s) {
+  // as many tokens a CTA as give each thread four pieces or so
+  const int64_t per_row = (int64_t)p.n_kv * (d / 16);
+  if (per_row > INT32_MAX / 2) return cudaErrorInvalidValue;
+  const int32_t tokens = (int32_t)(per_row >= 1024 ? 1 : 1024 / per_row);
+  const dim3 grid((unsigned)(((int64_t)p.N + tokens - 1) / tokens), 2);
+  if (dtype == 1) read_kernel<BITS, __nv_bfloat16><<<grid, 256, 0, s>>>(p, d, tokens);
+  else read_kernel<BITS, float><<<grid, 256, 0, s>>>(p, d, tokens);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_read(int32_t dtype, int32_t bits, int32_t d, const ReadParams& p, cudaStream_t s) {
+  return bits == 8 ? read_bits<8>(dtype, d, p, s) : bits == 4 ? read_bits<4>(dtype, d, p, s) : read_bits<0>(dtype, d, p, s);
+}
+
+}  // namespace granikv

@@ -291,7 +291,7 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
   const int64_t scale_at = (int64_t)p.n_kv * kD + 4 * j;
   float ks = 0.f, vs = 0.f;
   auto load_scales = [&](int i) {
-    const int64_t a = (first_slot + (int64_t)i * kN) * p.kv8_row + scale_at;
+    const int64_t a = (first_slot + (int64_t)i * kN) * p.packed_row + scale_at;
     ks = *reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.kpool) + a);
     vs = *reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.vpool) + a);
   };
@@ -300,7 +300,7 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
   constexpr int kSpan = 4;
   uint32_t v_bits[kSpan] = {};
   auto v_scale_bits = [&](int i) {
-    return *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.vpool) + (first_slot + (int64_t)i * kN) * p.kv8_row + scale_at);
+    return *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.vpool) + (first_slot + (int64_t)i * kN) * p.packed_row + scale_at);
   };
   if (warp < kSoftmaxWarps) {
     if (slab_ok && qhalf < n_tiles) load_scales(qhalf);

@@ -181,7 +181,7 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
         const uint8_t* row = nullptr;
         if (lane < 2 * kRowsEach && t + r < seg.t1) {
           const int32_t slot = sslot[pos + (t - seg.t0) + r];
-          if (slot >= p.n_hot && slot < p.n_slots) row = pool + (int64_t)slot * p.kv8_row;
+          if (slot >= p.n_hot && slot < p.n_slots) row = pool + (int64_t)slot * p.packed_row;
           else latch_err(p.err, kDevBadSlot);
         }
         if (skip0 && n == 0) continue;

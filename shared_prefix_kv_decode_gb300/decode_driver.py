@@ -29,10 +29,10 @@ and is captured again.
 With a COLD budget, every step also weighs the requests' COLD tokens by the attention they
 received in each layer (granikv_cold_weigh, in the captured step too), and before a step a request
 that holds more than the budget gives up its lightest tokens (granikv_cold_evict, but for its last
-`keep_last`), whose slots return to the free ring.  kv8 keeps the pools in 8 bits.
+`keep_last`), whose slots return to the free ring.  kv8 keeps the pools in 8 bits, kv4 in 4.
 
   python -m shared_prefix_kv_decode_gb300.decode_driver [--steps 64] [--layers 2] [--seed 0] [--graph]
-      [--kv8] [--cold-budget N]
+      [--kv8 | --kv4] [--cold-budget N]
 """
 
 from __future__ import annotations
@@ -61,7 +61,7 @@ class DecodeDriver:
     def __init__(self, *, prefix_lens: Sequence[int], n_layers: int = 1, n_q: int = 32, n_kv: int = 8,
                  head_dim: int = 128, max_batch: int = 256, cap: int = 4096, n_slots: int = 1 << 17,
                  seed: int = 0, keep_logical: bool = False, device: int = 0, graph: bool = False,
-                 headroom: int = 16, fused_append: bool = True, kv8: bool = False,
+                 headroom: int = 16, fused_append: bool = True, kv8: bool = False, kv4: bool = False,
                  cold_budget: Optional[int] = None, keep_last: int = 16):
         if cold_budget is not None and not 0 < keep_last <= cold_budget:
             raise ValueError("a COLD budget needs 0 < keep_last <= cold_budget")
@@ -70,7 +70,7 @@ class DecodeDriver:
         self.rng = np.random.default_rng(seed)
         self.keep = keep_logical
         self.cache = GraniKVCache(n_layers=n_layers, n_q=n_q, n_kv=n_kv, head_dim=head_dim, dtype=gb.DTYPE_BF16,
-                                  n_slots=n_slots, max_batch=max_batch, cap=cap, device=device, kv8=kv8)
+                                  n_slots=n_slots, max_batch=max_batch, cap=cap, device=device, kv8=kv8, kv4=kv4)
         self.dev = self.cache.device
         self.ctx = self.cache.ctx
         self.plan = self.ctx.plan()
@@ -348,14 +348,14 @@ class DecodeDriver:
 def run(*, steps: int = 64, n_layers: int = 2, prefix_lens=(16384, 4096), start_batch: int = 48,
         p_arrive: float = 0.25, p_complete: float = 0.02, prompt=(64, 512), seed: int = 0,
         max_batch: int = 256, graph: bool = False, headroom: int = 16, fused_append: bool = True,
-        kv8: bool = False, cold_budget: Optional[int] = None) -> Dict:
+        kv8: bool = False, kv4: bool = False, cold_budget: Optional[int] = None) -> Dict:
     """Seeded arrival/completion schedule: each step, with probability p_arrive a request arrives
     (uniform prefix, uniform prompt length in `prompt`), and every active request completes with
     probability p_complete."""
     sched = np.random.default_rng(seed + 1)
     drv = DecodeDriver(prefix_lens=prefix_lens, n_layers=n_layers, max_batch=max_batch,
                        cap=max(prompt) + steps + headroom + 64, seed=seed, graph=graph, headroom=headroom,
-                       fused_append=fused_append, kv8=kv8, cold_budget=cold_budget)
+                       fused_append=fused_append, kv8=kv8, kv4=kv4, cold_budget=cold_budget)
     for i in range(start_batch):
         drv.arrive(int(sched.integers(len(prefix_lens))), int(sched.integers(prompt[0], prompt[1] + 1)))
     for _ in range(steps):
@@ -372,7 +372,7 @@ def run(*, steps: int = 64, n_layers: int = 2, prefix_lens=(16384, 4096), start_
     disp = [t["dispatch_us"] for t in trace]
     host = [t["host_us"] for t in trace]
     out = {"steps": steps, "layers": n_layers, "graph": graph, "B_min": min(t["B"] for t in trace),
-           "B_max": max(t["B"] for t in trace), "kv8": kv8, "evicted": sum(t["evicted"] for t in trace), "dense_fraction": n_dense / max(1, n_groups),
+           "B_max": max(t["B"] for t in trace), "kv8": kv8, "kv4": kv4, "evicted": sum(t["evicted"] for t in trace), "dense_fraction": n_dense / max(1, n_groups),
            "gpu_us_per_step_median": statistics.median(gpu),
            "host_us_per_step_median": statistics.median(host),
            "host_share_of_step": statistics.median(h / g for h, g in zip(host, gpu)),
@@ -398,12 +398,14 @@ def main(argv=None):
     ap.add_argument("--p-arrive", type=float, default=0.25, help="chance of an arrival per step")
     ap.add_argument("--p-complete", type=float, default=0.02, help="chance per request of completing per step")
     ap.add_argument("--no-fused-append", action="store_true", help="append new K/V with launches of their own")
-    ap.add_argument("--kv8", action="store_true", help="keep the pools in 8 bits")
+    packed = ap.add_mutually_exclusive_group()
+    packed.add_argument("--kv8", action="store_true", help="keep the pools in 8 bits")
+    packed.add_argument("--kv4", action="store_true", help="keep the pools in 4 bits")
     ap.add_argument("--cold-budget", type=int, default=None, help="COLD tokens a request may hold before a step")
     a = ap.parse_args(argv)
     res = run(steps=a.steps, n_layers=a.layers, seed=a.seed, graph=a.graph, headroom=a.headroom,
               p_arrive=a.p_arrive, p_complete=a.p_complete, fused_append=not a.no_fused_append,
-              kv8=a.kv8, cold_budget=a.cold_budget)
+              kv8=a.kv8, kv4=a.kv4, cold_budget=a.cold_budget)
     trace = res.pop("trace")
     if a.trace:
         for i, t in enumerate(trace):

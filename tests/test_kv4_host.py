@@ -1,0 +1,144 @@
+"""CPU checks of the 4-bit cache: the oracle's number format pinned by other means, and the refusals of
+the entry points (checked before any device call)."""
+
+import numpy as np
+import pytest
+
+import oracle.kv4 as K4
+import oracle.kv8 as K8
+from shared_prefix_kv_decode_gb300 import _binding as gb
+
+
+def _ctx(n_q=8, n_kv=2, d=64, dtype=gb.DTYPE_BF16, max_batch=8, **kw):
+    return gb.Context(n_layers=1, n_q=n_q, n_kv=n_kv, head_dim=d, dtype=dtype, n_slots=1000, hot_fraction=0.5,
+                      max_batch=max_batch, host_only=True, **{"kv4": True, **kw})
+
+
+def _status(call, *args):
+    with pytest.raises(gb.GranikvError) as e:
+        call(*args)
+    return e.value.status
+
+
+def test_codes_are_nearest_with_ties_to_even():
+    grid = np.concatenate([K4.E2M1, [8.0]])
+    rng = np.random.default_rng(0)
+    x = np.concatenate([rng.uniform(0, 9, 4000), rng.uniform(0, 0.6, 500), K4.E2M1, (K4.E2M1[:-1] + K4.E2M1[1:]) / 2, [5.0, 1e9, np.inf, 0.0]])
+    codes = K4.e2m1_codes(x)
+    for a, c in zip(x, codes):
+        if a >= 6:
+            assert c == 7
+            continue
+        dist = np.abs(K4.E2M1 - a)
+        best = np.flatnonzero(dist == dist.min())
+        assert c in best and (len(best) == 1 or c % 2 == 0)
+    assert np.array_equal(K4.e2m1_codes(-x), codes | 8)
+    assert (np.diff(grid) > 0).all()
+
+
+@pytest.mark.parametrize("block", [1, K4.BLOCK])
+def test_quantise_by_its_definition(block):
+    """The exponent is the least that holds amax, a scale is within half a step of bmax / 6, and a value within
+    half a step of what it stands for, or at the largest one below it (a scale may be rounded down)."""
+    rng = np.random.default_rng(block)
+    x = (rng.standard_normal((130, 3, 64)) * np.exp2(rng.uniform(-30, 30, (130, 1, 1)))).astype(np.float32)
+    x[5] = 0.0
+    x[7, 1] = 2.0 ** 11 * 1.3125  # exactly 2688: exponent 0
+    x[8, 1] = np.nextafter(np.float32(2688), np.float32(1e9))
+    codes, scale, e = K4.quantise(x, block)
+    unit = np.ldexp(1.0, e.astype(int) - 127)
+    amax = np.abs(x).max(axis=2).astype(np.float64)
+    for t in range(0, 130, block):
+        amax[t:t + block] = amax[t:t + block].max(axis=0)
+    assert (amax <= 2688 * unit).all() and ((amax > 1344 * unit) | (e == 127 + K4.EXP_MIN)).all()
+    if block == 1:
+        assert e[7, 1] == 127 and e[8, 1] == 128
+    b = K8.e4m3_values()[scale]
+    y = np.abs(x).reshape(130, 3, 4, 16).max(axis=3) / (6 * unit[..., None])
+    assert (np.abs(b - y) <= np.maximum(y * 2.0 ** -4, 2.0 ** -9)).all() and (b >= 2.0 ** -9).all()
+    v = K4.values(codes, scale, e).reshape(130, 3, 4, 16)
+    step = np.where(np.abs(v) >= 4 * (b * unit[..., None])[..., None], 2.0, np.where(np.abs(v) >= 2 * (b * unit[..., None])[..., None], 1.0, 0.5))
+    off = np.abs(v - x.reshape(v.shape))
+    one = (b * unit[..., None])[..., None]
+    assert (off <= np.maximum(one * step / 2 * (1 + 1e-12), np.abs(x.reshape(v.shape)) - 6 * one)).all()
+    assert np.array_equal(v.astype(np.float32).astype(np.float64), v)  # exact in fp32
+
+
+def test_quantise_edges():
+    x = np.zeros((2, 2, 32), dtype=np.float32)
+    x[0, 0, :4] = [6.0, -3.0, np.inf, -0.0]
+    x[0, 1, 0], x[0, 1, 20] = np.nan, 12.0
+    x[1, 0] = 3e38
+    x[1, 1] = 1e-40
+    codes, scale, e = K4.quantise(x, 1)
+    assert list(codes[0, 0, :4]) == [7, 13, 7, 8]
+    assert scale[0, 1, 0] == 0x7F and scale[0, 1, 1] != 0x7F and np.isfinite(K4.values(codes, scale, e)[0, 1, 16:]).all()
+    assert np.isnan(K4.values(codes, scale, e)[0, 1, :16]).all()
+    assert e[1, 0] == 127 + K4.EXP_MAX and np.isfinite(K4.values(codes, scale, e)[1, 0].astype(np.float32)).all()
+    assert e[1, 1] == 127 + K4.EXP_MIN and not (codes[1, 1] & 7).any() and (scale[1, 1] == 1).all()
+
+
+@pytest.mark.parametrize("n_kv,d,want", [(8, 128, 592), (1, 32, 48), (3, 96, 192), (2, 64, 96), (5, 256, 736), (1, 128, 96)])
+def test_row_bytes(granikv_lib, n_kv, d, want):
+    assert gb.kv4_row_bytes(n_kv, d) == want == K4.row_bytes(n_kv, d)
+
+
+def test_row_bytes_refusals(granikv_lib):
+    assert _status(gb.kv4_row_bytes, 0, 64) == gb.ERR_INVALID
+    for d in (0, 16, 31, 48, 288):
+        assert _status(gb.kv4_row_bytes, 2, d) == gb.ERR_UNSUPPORTED
+    assert gb.kv4_row_bytes(2 ** 24 // 145 - 1, 256) <= 2 ** 24
+    for n_kv in (2 ** 24 // 145 + 1, 2 ** 30):
+        assert _status(gb.kv4_row_bytes, n_kv, 256) == gb.ERR_UNSUPPORTED
+        with pytest.raises(gb.GranikvError) as e:
+            _ctx(n_q=n_kv, n_kv=n_kv, d=256)
+        assert e.value.status == gb.ERR_UNSUPPORTED
+
+
+def test_kv4_context_refusals(granikv_lib):
+    with pytest.raises(ValueError):
+        _ctx(kv8=True)
+    with pytest.raises(gb.GranikvError) as e:
+        _ctx(d=80)
+    assert e.value.status == gb.ERR_UNSUPPORTED
+    ctx = _ctx()
+    sid, _ = ctx.hot_alloc(100)
+    assert _status(ctx.hot_fill, 0, sid, 4096, 4096 + 8) == gb.ERR_INVALID
+    assert _status(ctx.hot_fill, 0, sid, 4096, 4096) == gb.ERR_NO_DEVICE
+    assert _status(ctx.cold_append, 0, 4098, 4096, 4096, 3) == gb.ERR_INVALID
+    assert _status(ctx.cold_append, 0, 4096, 4096, 4096, 3) == gb.ERR_NO_DEVICE
+    b = gb.Batch([sid], [3], 4096, 16, 4096)
+    assert _status(ctx.decode_attention, 0, 4100, b, None, 4096, 4096, 4096, 1 << 20) == gb.ERR_INVALID
+    assert _status(ctx.decode_attention, 0, 4096, b, None, 4104, 4096, 4096, 1 << 20) == gb.ERR_INVALID
+    assert _status(ctx.decode_attention, 0, 4096, b, None, 4096, 4096, 4096, 1 << 20) == gb.ERR_NO_DEVICE
+    assert _status(ctx.cold_weigh, 0, 4100, 4096, b, 4096) == gb.ERR_INVALID
+    assert _status(ctx.cold_weigh, 0, 4096, 4096, b, 4096) == gb.ERR_NO_DEVICE
+
+
+@pytest.mark.parametrize("kind", [{"kv4": True}, {"kv4": False, "kv8": True}, {"kv4": False}])
+def test_read_refusals(granikv_lib, kind):
+    ctx = _ctx(**kind)
+    sid, _ = ctx.hot_alloc(100)
+    assert _status(ctx.hot_read, 0, sid, 0, 100, 4096, 4096) == gb.ERR_NO_DEVICE
+    assert _status(ctx.hot_read, 0, sid, 100, 0, None, None) == gb.ERR_NO_DEVICE
+    for args in [(1, sid, 0, 5, 4096, 4096), (-1, sid, 0, 5, 4096, 4096), (0, sid + 1, 0, 5, 4096, 4096), (0, -1, 0, 5, 4096, 4096),
+                 (0, sid, -1, 5, 4096, 4096), (0, sid, 0, -1, 4096, 4096), (0, sid, 96, 5, 4096, 4096), (0, sid, 0, 101, 4096, 4096),
+                 (0, sid, 2 ** 31 - 1, 2 ** 31 - 1, 4096, 4096), (0, sid, 0, 5, None, 4096), (0, sid, 0, 5, 4096, None),
+                 (0, sid, 0, 5, 4104, 4096), (0, sid, 0, 5, 4096, 4100)]:
+        assert _status(ctx.hot_read, *args) == gb.ERR_INVALID, args
+    assert _status(ctx.cold_read, 0, 4096, 5, 4096, 4096) == gb.ERR_NO_DEVICE
+    for args in [(1, 4096, 5, 4096, 4096), (0, None, 5, 4096, 4096), (0, 4096, -1, 4096, 4096), (0, 4096, 5, None, 4096),
+                 (0, 4096, 5, 4096, None), (0, 4096, 5, 4098, 4096), (0, 4096, 5, 4096, 4104)]:
+        assert _status(ctx.cold_read, *args) == gb.ERR_INVALID, args
+    ctx.hot_free(sid)
+    assert _status(ctx.hot_read, 0, sid, 0, 1, 4096, 4096) == gb.ERR_INVALID
+
+
+def test_kv4_dispatch_plans(granikv_lib):
+    for d in (64, 128):
+        ctx = _ctx(d=d)
+        sid, _ = ctx.hot_alloc(300)
+        plan = ctx.dispatch(gb.Batch([sid, -1, sid], [5, 40, 0], 4096, 64))
+        (grp,) = plan.groups()
+        assert grp["slab_id"] == sid and grp["n_requests"] == 2 and grp["L_p"] == 300
+        assert ctx.workspace_size(plan) > 0
