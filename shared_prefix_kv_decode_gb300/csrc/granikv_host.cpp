@@ -85,6 +85,7 @@ struct granikv_ctx {
   std::vector<unsigned char> prefill_blob;  // host image of the last prefill call's plan
   // TMA descriptors of each layer's K and V pools (dense backend), valid when has_tmaps
   std::vector<CUtensorMap> tmap_k, tmap_v;
+  std::vector<PackedMaps> packed_maps;  // of a packed cache, in their place
   bool has_tmaps = false;
   // 8- or 4-bit cache (granikv_create_kv8, _kv4): bytes of a slot's packed row, and 8 or 4; else 0
   int64_t packed_row = 0;
@@ -171,9 +172,9 @@ bool has_device(const granikv_ctx* c) { return c && !c->cfg.host_only && c->d_ri
 // Which prefix implementation serves a group of this shape and backend.
 int32_t prefix_impl_for(const granikv_ctx* c, int32_t backend) {
   if (c->packed_row) {
-    const bool dense = c->packed_bits == 8 && backend == GRANIKV_BACKEND_DENSE && c->cfg.dtype == GRANIKV_DTYPE_BF16 &&
+    const bool dense = backend == GRANIKV_BACKEND_DENSE && c->cfg.dtype == GRANIKV_DTYPE_BF16 &&
                        c->cfg.head_dim == 128 && (c->has_tmaps || c->cfg.host_only);
-    return dense ? kImplKv8Dense : kImplKv8Generic;
+    return dense ? kImplPackedDense : kImplPackedGeneric;
   }
   if (c->cfg.dtype == GRANIKV_DTYPE_BF16 && c->cfg.head_dim == 128) {
     if (backend == GRANIKV_BACKEND_DENSE && (c->has_tmaps || c->cfg.host_only)) return kImplDenseTc;
@@ -188,20 +189,20 @@ int32_t prefix_impl_for(const granikv_ctx* c, int32_t backend) {
 
 // Kernels outside the 16-bit tensor-core path: they take no part in the one grid, and their step
 // runs prefix, suffix and merge one after another.
-bool runs_alone(int32_t impl) { return impl == kImplGeneric || impl == kImplDenseTf32 || impl == kImplKv8Generic; }
+bool runs_alone(int32_t impl) { return impl == kImplGeneric || impl == kImplDenseTf32 || impl == kImplPackedGeneric; }
 
 // Which kernel attends the COLD suffix.
 int32_t suffix_impl_for(const granikv_ctx* c) {
   const bool mma = c->cfg.dtype == GRANIKV_DTYPE_BF16 && c->cfg.head_dim == 128 && c->g <= 8;
-  if (c->packed_row) return mma && c->packed_bits == 8 ? kImplKv8Suffix : kImplKv8Generic;
+  if (c->packed_row) return mma ? kImplPackedSuffix : kImplPackedGeneric;
   return mma ? kImplSuffixMma : kImplGeneric;
 }
 
 // The suffix kernels that run one token-CTA per run and group of eight KV heads.
-bool token_ctas(int32_t suffix_impl) { return suffix_impl == kImplSuffixMma || suffix_impl == kImplKv8Suffix; }
+bool token_ctas(int32_t suffix_impl) { return suffix_impl == kImplSuffixMma || suffix_impl == kImplPackedSuffix; }
 
 // The dense prefix kernels of the tensor-core path (16-bit and 8-bit cache).
-bool dense_tc(int32_t impl) { return impl == kImplDenseTc || impl == kImplKv8Dense; }
+bool dense_tc(int32_t impl) { return impl == kImplDenseTc || impl == kImplPackedDense; }
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no link-time libcuda).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -234,15 +235,15 @@ bool encode_pool_map(CUtensorMap* m, void* base, int64_t n_slots, int32_t n_kv) 
   return r == CUDA_SUCCESS;
 }
 
-// An 8-bit pool [n_slots, row bytes] as a byte matrix of its codes (head j at byte 128 j) with boxes
-// of `slots` x one head's 128 codes: with the 128-byte swizzle the operand descriptors expect (K), or
-// stored one row after the other (V, converted before it is an operand).
-bool encode_kv8_map(CUtensorMap* m, void* base, int64_t n_slots, int32_t n_kv, int64_t row, int32_t slots, bool swizzle) {
+// A packed pool [n_slots, row bytes] as a byte matrix of its rows' first `used` bytes with boxes of `slots` x
+// `bytes`: with the 128-byte swizzle the operand descriptors expect (K's codes of 8 bits), or stored one row after
+// the other (what is converted before it is an operand).
+bool encode_packed_map(CUtensorMap* m, void* base, int64_t n_slots, int64_t row, int64_t used, int32_t bytes, int32_t slots, bool swizzle) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)n_kv * 128, (cuuint64_t)n_slots};
+  cuuint64_t dims[2] = {(cuuint64_t)used, (cuuint64_t)n_slots};
   cuuint64_t strides[1] = {(cuuint64_t)row};
-  cuuint32_t box[2] = {128, (cuuint32_t)slots};
+  cuuint32_t box[2] = {(cuuint32_t)bytes, (cuuint32_t)slots};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                    swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -279,7 +280,7 @@ int32_t stream_sub_for(int32_t n_req, int32_t g) {
 int32_t rows_per_cta_for(int32_t impl, int32_t g, int32_t sub) {
   switch (impl) {
     case kImplDenseTc:
-    case kImplKv8Dense: return kDenseRows;
+    case kImplPackedDense: return kDenseRows;
     case kImplDenseTf32: return kDenseTf32Rows;
     case kImplCascadeMma: return kCascadeRows;
     case kImplCascadeStream: return (kCascadeStreamCols * sub / g) * g;
@@ -290,7 +291,7 @@ int32_t rows_per_cta_for(int32_t impl, int32_t g, int32_t sub) {
 int32_t tile_tokens_for(int32_t impl, int32_t sub) {
   switch (impl) {
     case kImplDenseTc:
-    case kImplKv8Dense: return kDenseTile;
+    case kImplPackedDense: return kDenseTile;
     case kImplDenseTf32: return kDenseTf32Tile;
     case kImplCascadeMma: return kCascadeTile;
     case kImplCascadeStream: return kCascadeStreamTile * sub;
@@ -601,13 +602,23 @@ granikv_status create_impl(const granikv_config* cfg, int32_t bits, granikv_ctx*
     if (e == cudaSuccess) e = cudaEventCreateWithFlags(&c->ev_fork, cudaEventDisableTiming);
     if (e == cudaSuccess) e = cudaEventCreateWithFlags(&c->ev_join, cudaEventDisableTiming);
     if (e == cudaSuccess && cfg->dtype == GRANIKV_DTYPE_BF16 && cfg->head_dim == 128 && c->cc_major == 10) {
-      c->tmap_k.resize(cfg->n_layers);
-      c->tmap_v.resize(cfg->n_layers);
+      if (bits) c->packed_maps.resize(cfg->n_layers);
+      else c->tmap_k.resize(cfg->n_layers), c->tmap_v.resize(cfg->n_layers);
       bool ok = true;
       for (int32_t l = 0; l < cfg->n_layers && ok; ++l) {
         if (bits) {
-          ok = encode_kv8_map(&c->tmap_k[l], c->kpool[l], cfg->n_slots, cfg->n_kv, c->packed_row, kDenseTile, true) &&
-               encode_kv8_map(&c->tmap_v[l], c->vpool[l], cfg->n_slots, cfg->n_kv, c->packed_row, kKv8VBox, false);
+          PackedMaps& m = c->packed_maps[l];
+          const int64_t codes = bits == 8 ? (int64_t)cfg->n_kv * 128 : kv4_scales_at(cfg->n_kv, 128);
+          auto encode = [&](CUtensorMap* to, void* pool, int64_t used, int32_t bytes, int32_t slots, bool swizzle) {
+            return encode_packed_map(to, pool, cfg->n_slots, c->packed_row, used, bytes, slots, swizzle);
+          };
+          if (bits == 8) {
+            ok = encode(&m.k, c->kpool[l], codes, 128, kDenseTile, true) && encode(&m.v, c->vpool[l], codes, 128, kKv8VBox, false);
+          } else {
+            const int64_t scales = kv4_units_at(cfg->n_kv, 128);  // (padded to whole boxes)
+            ok = encode(&m.k, c->kpool[l], codes, 64, kKv8VBox, false) && encode(&m.v, c->vpool[l], codes, 64, kKv8VBox, false) &&
+                 encode(&m.ks, c->kpool[l], scales, 16, kKv8VBox, false) && encode(&m.vs, c->vpool[l], scales, 16, kKv8VBox, false);
+          }
           continue;
         }
         ok = ((uintptr_t)c->kpool[l] % 16 == 0) && ((uintptr_t)c->vpool[l] % 16 == 0) &&
@@ -1131,7 +1142,7 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
   //    kernels run one CTA per SM, so their target is one wave over their SMs.
   int64_t target = 2LL * c->num_sms;
   for (int32_t i = 0; i < G; ++i)
-    if (groups[i].impl != kImplGeneric && groups[i].impl != kImplKv8Generic) target = prefix_sms;
+    if (groups[i].impl != kImplGeneric && groups[i].impl != kImplPackedGeneric) target = prefix_sms;
   {
     int64_t max_tiles = 1;
     for (int32_t i = 0; i < G; ++i) {
@@ -1157,11 +1168,11 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
     // At least sqrt(8 L) of L tokens: two prefixes of 34 and 1,995, B = 4 9.7 us, with sqrt(4 L) 10.3, with
     // sqrt(16 L) 11.0; 8,000 tokens, B = 8 18.5, 21.8 and 20.1
     for (int32_t i = 0; i < G; ++i)
-      if (groups[i].impl == kImplKv8Generic)
+      if (groups[i].impl == kImplPackedGeneric)
         lo = std::max(lo, std::min(max_tiles, (int64_t)std::ceil(std::sqrt(8.0 * (double)groups[i].L_p) / kGenericTile)));
     bool auto_found = false;
     bool kv8_dense = auto_share && c->packed_row && n_kv <= 8;
-    for (int32_t i = 0; i < G; ++i) kv8_dense = kv8_dense && groups[i].impl == kImplKv8Dense;
+    for (int32_t i = 0; i < G; ++i) kv8_dense = kv8_dense && groups[i].impl == kImplPackedDense;
     if (kv8_dense) {
       // 8-bit cache: every SM works until the end.  With pieces of a given length, dense CTA k is done
       // at t_k = 5.2 us + 7.3 ns a token and then takes suffix work (3 us for its set-up), the SMs
@@ -1262,7 +1273,7 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
         for (int32_t i = 0; i < G; ++i) {
           const int64_t tile = tile_tokens_for(groups[i].impl, groups[i].sub);
           const double per_token = groups[i].impl == kImplDenseTc ? 0.0078
-                                   : groups[i].impl == kImplKv8Dense ? 0.0078
+                                   : groups[i].impl == kImplPackedDense ? 0.0078
                                    : groups[i].impl == kImplCascadeStream
                                        ? 0.09 * std::min(n_kv, stream_heads(groups[i].sub)) / 8.0
                                        : 0.02;
@@ -1520,7 +1531,7 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
     }
     // the 8-bit dense kernel's first CTAs are those that take suffix runs after their piece: the
     // shortest pieces come first
-    if (impl == kImplKv8Dense && kv8_split)
+    if (impl == kImplPackedDense && kv8_split)
       std::stable_sort(pitems.begin() + p->pitem_first[impl], pitems.end(),
                        [&](const DevPrefixItem& a, const DevPrefixItem& b) {
                          int32_t a0, a1, b0, b1;
@@ -1868,11 +1879,13 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
 
   cudaError_t e = cudaSuccess;
   const auto packed_generic = c->packed_bits == 4 ? launch_kv4_generic : launch_kv8_generic;
+  const auto packed_step = c->packed_bits == 4 ? launch_kv4_step : launch_kv8_step;
+  const auto packed_suffix = c->packed_bits == 4 ? launch_kv4_suffix : launch_kv8_suffix;
   auto launch_suffix = [&](cudaStream_t st, bool pdl) -> cudaError_t {
     if (p->n_sitems <= 0) return cudaSuccess;
     c->n_kernels += 1;
-    if (p->suffix_impl == kImplKv8Suffix) return launch_kv8_suffix(a, a.scta_begin, p->n_scta, st, pdl);
-    if (p->suffix_impl == kImplKv8Generic) return packed_generic(c->cfg.dtype, a, 0, 0, true, st, false);
+    if (p->suffix_impl == kImplPackedSuffix) return packed_suffix(a, a.scta_begin, p->n_scta, st, pdl);
+    if (p->suffix_impl == kImplPackedGeneric) return packed_generic(c->cfg.dtype, a, 0, 0, true, st, false);
     return p->suffix_impl == kImplSuffixMma ? launch_suffix_mma(a, a.scta_begin, p->n_scta, st, pdl)
                                             : launch_suffix_generic(c->cfg.dtype, a, st);
   };
@@ -1884,14 +1897,14 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
       r = launch_prefix_generic(c->cfg.dtype, a, p->pitem_first[kImplGeneric], p->pitem_count[kImplGeneric], st);
       c->n_kernels += 1;
     }
-    if (r == cudaSuccess && p->pitem_count[kImplKv8Generic] > 0) {
-      r = packed_generic(c->cfg.dtype, a, p->pitem_first[kImplKv8Generic], p->pitem_count[kImplKv8Generic], false, st, false);
+    if (r == cudaSuccess && p->pitem_count[kImplPackedGeneric] > 0) {
+      r = packed_generic(c->cfg.dtype, a, p->pitem_first[kImplPackedGeneric], p->pitem_count[kImplPackedGeneric], false, st, false);
       c->n_kernels += 1;
     }
-    if (r == cudaSuccess && p->pitem_count[kImplKv8Dense] > 0) {
+    if (r == cudaSuccess && p->pitem_count[kImplPackedDense] > 0) {
       if (!c->has_tmaps) return cudaErrorNotSupported;
-      r = launch_kv8_step(a, p->pitem_first[kImplKv8Dense], p->pitem_count[kImplKv8Dense], c->tmap_k[layer],
-                          c->tmap_v[layer], a.scta_begin, 0, 0, st, p->pitem_count[kImplKv8Generic] == 0);
+      r = packed_step(a, p->pitem_first[kImplPackedDense], p->pitem_count[kImplPackedDense], c->packed_maps[layer],
+                      a.scta_begin, 0, 0, st, p->pitem_count[kImplPackedGeneric] == 0);
       c->n_kernels += 1;
     }
     if (r == cudaSuccess && p->pitem_count[kImplDenseTf32] > 0) {
@@ -1929,20 +1942,20 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
     if (e != cudaSuccess) return cuda_status(e);
   }
   const int32_t n_dense = p->pitem_count[kImplDenseTc], n_casc = p->pitem_count[kImplCascadeStream];
-  const int32_t n_dense8 = p->pitem_count[kImplKv8Dense];
+  const int32_t n_dense8 = p->pitem_count[kImplPackedDense];
   if (p->concurrent && p->n_pitems > 0 && n_dense8 == p->n_pitems && c->has_tmaps &&
-      p->suffix_impl == kImplKv8Suffix && p->n_sitems > 0) {
+      p->suffix_impl == kImplPackedSuffix && p->n_sitems > 0) {
     // one grid, as below
     const int32_t n_tail = p->n_tail <= n_dense8 ? p->n_tail : 0;
-    e = launch_kv8_step(a, p->pitem_first[kImplKv8Dense], n_dense8, c->tmap_k[layer], c->tmap_v[layer], a.scta_begin,
-                        p->n_scta - n_tail, n_tail, s, true);
+    e = packed_step(a, p->pitem_first[kImplPackedDense], n_dense8, c->packed_maps[layer], a.scta_begin, p->n_scta - n_tail,
+                    n_tail, s, true);
     c->n_kernels += 1;
     if (e == cudaSuccess) e = launch_merge_k(true);
     return e == cudaErrorNotSupported ? GRANIKV_ERR_UNSUPPORTED : cuda_status(e);
   }
-  if (p->n_pitems > 0 && p->pitem_count[kImplKv8Generic] == p->n_pitems && p->suffix_impl == kImplKv8Generic) {
+  if (p->n_pitems > 0 && p->pitem_count[kImplPackedGeneric] == p->n_pitems && p->suffix_impl == kImplPackedGeneric) {
     // CUDA-core prefix and suffix items in one launch, then the merge
-    e = packed_generic(c->cfg.dtype, a, p->pitem_first[kImplKv8Generic], p->n_pitems, p->n_sitems > 0, s, true);
+    e = packed_generic(c->cfg.dtype, a, p->pitem_first[kImplPackedGeneric], p->n_pitems, p->n_sitems > 0, s, true);
     c->n_kernels += 1;
     if (e == cudaSuccess) e = launch_merge_k(true);
     return cuda_status(e);

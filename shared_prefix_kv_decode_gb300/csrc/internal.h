@@ -33,9 +33,9 @@ enum Impl : int32_t {
   kImplSuffixMma = 3, // bf16, head_dim 128, g <= 8: warp-level tensor-core suffix kernel
   kImplCascadeStream = 4,  // bf16, head_dim 128, g <= 128: cascade over whole 2 KB slot rows
   kImplDenseTf32 = 5,      // f32, head_dim % 32 == 0 up to 128: tcgen05 kind::tf32 dense kernel
-  kImplKv8Generic = 6,     // 8-bit cache, any head_dim % 32 == 0 up to 256: CUDA-core kernel
-  kImplKv8Dense = 7,       // 8-bit cache, bf16 q, head_dim 128: tcgen05/TMEM dense kernel
-  kImplKv8Suffix = 8,      // 8-bit cache, bf16 q, head_dim 128, g <= 8: warp-level tensor-core suffix kernel
+  kImplPackedGeneric = 6,  // 8- or 4-bit cache, any head_dim % 32 == 0 up to 256: CUDA-core kernel
+  kImplPackedDense = 7,    // 8- or 4-bit cache, bf16 q, head_dim 128: tcgen05/TMEM dense kernel
+  kImplPackedSuffix = 8,   // 8- or 4-bit cache, bf16 q, head_dim 128, g <= 8: warp-level tensor-core suffix kernel
 };
 
 // Geometry of each prefix kernel: query rows per CTA and tokens per tile.  The planner and the
@@ -139,7 +139,7 @@ struct AttnParams {
 // head, padded to 16 bytes (value = code * scale).  Every row carries its own scales; the rows of
 // one 64-token block of a slab (kKv8Block, counted from the slab's start) hold the same ones.
 constexpr int kKv8Block = 64;
-constexpr int kKv8VBox = 32;  // slots of one TMA box of V's codes (dense kernel)
+constexpr int kKv8VBox = 32;  // slots of one TMA box of V's codes, 4 bits: of all (dense kernel)
 constexpr float kE4m3Max = 448.0f;
 constexpr float kKv8AmaxMin = 1.2621774483536189e-29f;  // 2^-96: smallest amax a scale is made for
 constexpr int64_t kKv8MaxRow = 1 << 24;  // bytes of a packed row: offsets within a block of 64 fit 32 bits
@@ -243,12 +243,17 @@ cudaError_t launch_kv8_append_newest(int32_t dtype, const AttnParams& p, cudaStr
 // CUDA-core attention of n_items prefix items and, with suffix, of the suffix items, in one launch.
 cudaError_t launch_kv8_generic(int32_t dtype, const AttnParams& p, int32_t first_item, int32_t n_items, bool suffix,
                                cudaStream_t s, bool pdl);
-// Tensor-core path of the 8-bit cache (kernels_kv8_tc.cu): dense prefix items and suffix token-CTAs in
-// one grid (either count may be 0; n_tail as for launch_prefix_suffix_tc), and the suffix alone.
-cudaError_t launch_kv8_step(const AttnParams& p, int32_t first_dense, int32_t n_dense, const CUtensorMap& tmk,
-                            const CUtensorMap& tmv, const int32_t* cta_begin, int32_t n_scta, int32_t n_tail,
-                            cudaStream_t s, bool pdl);
+// Tensor-core path of the 8- and 4-bit cache (kernels_kv8_tc.cu, kernels_kv4_tc.cu): dense prefix items and suffix
+// token-CTAs in one grid (either count may be 0; n_tail as for launch_prefix_suffix_tc), and the suffix alone.
+struct PackedMaps {
+  CUtensorMap k, v, ks, vs;  // codes of K and V, their scales (4 bits)
+};
+cudaError_t launch_kv8_step(const AttnParams& p, int32_t first_dense, int32_t n_dense, const PackedMaps& m,
+                            const int32_t* cta_begin, int32_t n_scta, int32_t n_tail, cudaStream_t s, bool pdl);
 cudaError_t launch_kv8_suffix(const AttnParams& p, const int32_t* cta_begin, int32_t n_scta, cudaStream_t s, bool pdl);
+cudaError_t launch_kv4_step(const AttnParams& p, int32_t first_dense, int32_t n_dense, const PackedMaps& m,
+                            const int32_t* cta_begin, int32_t n_scta, int32_t n_tail, cudaStream_t s, bool pdl);
+cudaError_t launch_kv4_suffix(const AttnParams& p, const int32_t* cta_begin, int32_t n_scta, cudaStream_t s, bool pdl);
 
 // 4-bit cache (kernels_kv4.cu): the same calls.
 cudaError_t launch_kv4_fill(int32_t dtype, const void* k, const void* v, int32_t L_p, uint8_t* kpool, uint8_t* vpool,

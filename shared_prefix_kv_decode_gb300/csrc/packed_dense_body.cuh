@@ -1,5 +1,5 @@
-// kv8_dense_body.cuh -- dense prefix backend over the 8-bit cache on the 5th-generation tensor cores
-// (tcgen05/TMEM), head_dim 128, bf16 q.
+// packed_dense_body.cuh -- dense prefix backend over the 8- or 4-bit cache on the 5th-generation tensor cores
+// (tcgen05/TMEM), head_dim 128, bf16 q.  (8 bits first; what 4 bits change stands at the end.)
 //
 // One CTA takes one (prefix group, KV head j, 128-row block, L_p piece), as the 16-bit dense kernel:
 // rows are the group's (request, head-in-group) pairs of KV head j.  For each 64-token tile i, one
@@ -46,6 +46,13 @@
 //  * warp 14, the TMA loads of K.
 // Every mbarrier wait is bounded in time; on expiry the CTA raises an abort flag, latches an error,
 // drains what it issued and frees its TMEM.
+//
+// 4 bits.  An element is code * b * u, b the e4m3 scale of its 16 dims and u the power of two of its block of 64 slab
+// tokens and head, that is, of a tile.  code * b is exact in fp16, so the conversion warps make fp16 operand tiles of
+// K as of V (an fp16x2 conversion and a product for each pair), S is an fp16 product with q in fp16 (scaled by a power of two
+// to [2^14, 2^15): exact down to 2^-31 of the row's largest element), and u takes the place of ks and vs.  A
+// conversion warp's ring holds its 32 tokens' codes and scales of K and V, by four TMA boxes (64 and 16 bytes a
+// token) on one barrier; the K ring has two slots of fp16, filled by four arrivals like V's.
 #pragma once
 
 #include <cuda.h>
@@ -53,27 +60,28 @@
 #include <cfloat>
 
 #include "internal.h"
-#include "kv8_suffix_body.cuh"
+#include "kv4_util.cuh"
 #include "kv8_util.cuh"
 #include "launch_util.cuh"
 #include "mma_util.cuh"
+#include "packed_suffix_body.cuh"
 #include "tc_util.cuh"
 
+#include <type_traits>
+
 namespace granikv {
-namespace k8d {
+namespace pkd {
 namespace {
 
-using k8s::lg2_approx;
-using k8s::pack_f16;
+using pks::lg2_approx;
+using pks::pack_f16;
 
 constexpr int kD = 128;
 constexpr int kM = kDenseRows;                // 128 query rows per CTA
 constexpr int kN = kKv8Block;                 // 64 tokens per tile
 constexpr int kPair = kDenseTile;             // 128 tokens: what the K and V rings hold in a slot
 static_assert(kPair == 2 * kN && kPair / 4 == kKv8VBox, "a conversion warp's part of a V slot is one box");
-constexpr int kKSlots = 4;                    // slots of the K ring (codes)
 constexpr int kVSlots = 3;                    // slots of the V ring (fp16)
-constexpr int kCSlots = 4;                    // slots of each conversion warp's ring of V codes
 constexpr int kSBufs = 5;                     // S/P buffers in TMEM
 constexpr int kSoftmaxWarps = 8;
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
@@ -85,16 +93,53 @@ constexpr int kHalf = kPair * 128;            // one 64-dim half of an fp16 slot
 constexpr int kTile = 2 * kHalf;              // 32 KB
 constexpr int kCodes = kPair * kD;            // a slot's codes: 16 KB
 constexpr int kPartCodes = kPart * kD;        // 4 KB
-constexpr int kOffK = 0;
-constexpr int kOffV = kOffK + kKSlots * kCodes;
-constexpr int kOffCodes = kOffV + kVSlots * kTile;
-constexpr int kOffUnit = kOffCodes + kConvWarps * kCSlots * kPartCodes;  // [kM] power of two that undoes a row's scaling
-constexpr int kOffMPub = kOffUnit + kM * 4;   // [4 quarters][2 tile parities][32 rows] published maxima
-constexpr int kOffBar = kOffMPub + 4 * 2 * 32 * 4;
 constexpr int kBarArea = 512;
-constexpr int kSmemBytes = kOffBar + kBarArea + 1024;  // + alignment slack
-static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-static_assert(kConvWarps * kCSlots * kPartCodes >= 6 * kM * 4, "the epilogue's sums and maxima");
+template <int BITS>
+struct Layout {
+  static constexpr int kKSlots = BITS == 8 ? 4 : 2;       // slots of the K ring (codes, 4 bits: fp16)
+  static constexpr int kKSlotBytes = BITS == 8 ? kCodes : kTile;
+  static constexpr int kCSlots = BITS == 8 ? 4 : 3;       // slots of each conversion warp's ring (V codes, 4 bits: codes and scales of K and V)
+  static constexpr int kHead = kD * BITS / 8;             // bytes of a head's codes
+  static constexpr int kScales = kPart * 16;              // 4 bits: a part's scales, those of two heads a token
+  static constexpr int kOffVc = kPart * (kHead + 16);     // 4 bits: V's codes in a slot
+  static constexpr int kCSlotBytes = BITS == 8 ? kPartCodes : 2 * kOffVc;
+  static constexpr int kOffK = 0;
+  static constexpr int kOffV = kOffK + kKSlots * kKSlotBytes;
+  static constexpr int kOffCodes = kOffV + kVSlots * kTile;
+  static constexpr int kOffUnit = kOffCodes + kConvWarps * kCSlots * kCSlotBytes;  // [kM] power of two that undoes a row's scaling
+  static constexpr int kOffMPub = kOffUnit + kM * 4;      // [4 quarters][2 tile parities][32 rows] published maxima
+  static constexpr int kOffBar = kOffMPub + 4 * 2 * 32 * 4;
+  static constexpr int kSmemBytes = kOffBar + kBarArea + 1024;  // + alignment slack
+  static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+  static_assert(kConvWarps * kCSlots * kCSlotBytes >= 6 * kM * 4, "the epilogue's sums and maxima");
+  // barriers
+  static constexpr int kBarKFull = 0;                            // [kKSlots] TMA (4 bits: conversion, kConvWarps arrivals) -> MMA
+  static constexpr int kBarKEmpty = kBarKFull + kKSlots;         // [kKSlots] MMA (S of the slot's tiles done) -> TMA (conversion)
+  static constexpr int kBarCFull = kBarKEmpty + kKSlots;         // [kConvWarps][kCSlots] TMA -> conversion
+  static constexpr int kBarVFull = kBarCFull + kConvWarps * kCSlots;  // [kVSlots] conversion -> MMA (kConvWarps arrivals)
+  static constexpr int kBarVEmpty = kBarVFull + kVSlots;         // [kVSlots] MMA (PV of the slot's tiles done) -> conversion
+  static constexpr int kBarSFull = kBarVEmpty + kVSlots;         // [kSBufs] S(i) in TMEM -> softmax
+  static constexpr int kBarPFull = kBarSFull + kSBufs;           // [kSBufs] P(i) in TMEM -> MMA (128 arrivals)
+  static constexpr int kBarPvDone = kBarPFull + kSBufs;          // [kSBufs] PV(i) done -> softmax, and S(i + kSBufs)
+  static constexpr int kBarDrain = kBarPvDone + kSBufs;          // [2] all S (all PV) products done -> teardown
+  static constexpr int kBarPair = kBarDrain + 2;                 // [4] the two softmax warps of a row quarter, epilogue (64)
+  static constexpr int kBarMPub = kBarPair + 4;                  // [4 quarters][2 parities] max of a tile published (32)
+  static constexpr int kNumBars = kBarMPub + 8;
+  static_assert(8 * kNumBars + 16 <= kBarArea, "barrier area");
+};
+// The layer's pools as byte matrices [n_slots, row bytes].  8 bits: K in boxes of 128 slots x 128 bytes with the
+// 128-byte swizzle, V in boxes of 32 slots x 128 bytes, row after row.  4 bits: codes in boxes of 32 slots x 64 bytes,
+// scales in boxes of 32 slots x 16 bytes.
+template <int BITS>
+struct Maps;
+template <>
+struct Maps<8> {
+  CUtensorMap k, v;
+};
+template <>
+struct Maps<4> {
+  CUtensorMap k, v, ks, vs;
+};
 constexpr uint32_t kTmemCols = 512;           // S/P buffers at 0, 64, 128, 192, 256; Q (hi, lo) at 320; O at 384
 constexpr uint32_t kColQ = kSBufs * kN, kColO = 384;
 static_assert(kColQ + 2 * kD / 4 <= kColO && kColO + kD <= kTmemCols, "TMEM columns");
@@ -103,22 +148,6 @@ constexpr float kRescaleThreshold = 8.0f;     // log2 of the largest growth tole
 constexpr float kShift = 7.0f;                // log2 of the factor that P carries
 constexpr uint32_t kWideSpan = 32;            // log2 of a wide span of V scales
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
-
-enum : int {
-  kBarKFull = 0,                            // [kKSlots] TMA -> MMA
-  kBarKEmpty = kBarKFull + kKSlots,         // [kKSlots] MMA (S of the slot's tiles done) -> TMA
-  kBarCFull = kBarKEmpty + kKSlots,         // [kConvWarps][kCSlots] TMA -> conversion (codes of V)
-  kBarVFull = kBarCFull + kConvWarps * kCSlots,  // [kVSlots] conversion -> MMA (kConvWarps arrivals)
-  kBarVEmpty = kBarVFull + kVSlots,         // [kVSlots] MMA (PV of the slot's tiles done) -> conversion
-  kBarSFull = kBarVEmpty + kVSlots,         // [kSBufs] S(i) in TMEM -> softmax
-  kBarPFull = kBarSFull + kSBufs,           // [kSBufs] P(i) in TMEM -> MMA (128 arrivals)
-  kBarPvDone = kBarPFull + kSBufs,          // [kSBufs] PV(i) done -> softmax, and S(i + kSBufs)
-  kBarDrain = kBarPvDone + kSBufs,          // [2] all S (all PV) products done -> teardown
-  kBarPair = kBarDrain + 2,                 // [4] the two softmax warps of a row quarter, epilogue (64)
-  kBarMPub = kBarPair + 4,                  // [4 quarters][2 parities] max of a tile published (32)
-  kNumBars = kBarMPub + 8
-};
-static_assert(8 * kNumBars + 16 <= kBarArea, "barrier area");
 
 // D[tmem] (+)= A[tmem] * B[smem desc], kind::f8f6f4 (A: M rows = TMEM lanes, four 8-bit elements per
 // 32-bit column along K), issued by one thread
@@ -191,15 +220,61 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(a));
   return x;
 }
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 x;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(a));
+  return x;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t x;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(a));
+  return x;
+}
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-// Prefix work item `item` (one CTA) on `smem_raw` (at least kSmemBytes), run by kThreads threads.
-// tmk/tmv: the layer's K and V pools as byte matrices [n_slots, row bytes]: K in boxes of 128 slots x
-// 128 bytes with the 128-byte swizzle, V in boxes of 32 slots x 128 bytes, row after row.
-__device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item, const CUtensorMap* tmk,
-                                               const CUtensorMap* tmv, unsigned char* smem_raw) {
+// A conversion lane's address in an fp16 operand tile (128 tokens x 64 dims, 128-byte rows, 128-byte swizzle): 16 dims
+// are two 16-byte chunks of a token's row in 64-dim half lane % 8 / 4.  The lane's tokens are lane / 8 + 4 n.
+struct ConvLane {
+  bool upper;
+  uint32_t lo[2], hi[2];  // chunk offsets of even and odd n: tokens lt and lt + 4 modulo 8 have two swizzles
+  __device__ __forceinline__ ConvLane(int w, int lane) {
+    const int lt = lane >> 3;
+    const uint32_t ch = (lane & 3) * 2;
+    upper = (lane & 7) >= 4;
+    const uint32_t row_off = (uint32_t)w * kPart * 128 + (upper ? kHalf : 0) + (uint32_t)lt * 128;
+#pragma unroll
+    for (int odd = 0; odd < 2; ++odd) {
+      lo[odd] = row_off + ((ch ^ (lt + 4 * odd)) << 4);
+      hi[odd] = row_off + (((ch + 1) ^ (lt + 4 * odd)) << 4);
+    }
+  }
+  // Token lt + 4 n's 16 dims.  Lanes of the upper half store theirs in the other order, so a store instruction
+  // covers all banks.
+  __device__ __forceinline__ void store(uint32_t dst, int n, const uint32_t (&y)[8]) const {
+    const uint32_t a = dst + n * 4 * 128 + lo[n & 1], b = dst + n * 4 * 128 + hi[n & 1];
+    if (upper) {
+      sts128(b, y[4], y[5], y[6], y[7]);
+      sts128(a, y[0], y[1], y[2], y[3]);
+    } else {
+      sts128(a, y[0], y[1], y[2], y[3]);
+      sts128(b, y[4], y[5], y[6], y[7]);
+    }
+  }
+};
+
+// Prefix work item `item` (one CTA) on `smem_raw` (at least Layout<BITS>::kSmemBytes), run by kThreads threads.
+template <int BITS>
+__device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t item, const Maps<BITS>* maps,
+                                                  unsigned char* smem_raw) {
+  using Lay = Layout<BITS>;
+  constexpr int kKSlots = Lay::kKSlots, kCSlots = Lay::kCSlots;
+  constexpr int kOffK = Lay::kOffK, kOffV = Lay::kOffV, kOffCodes = Lay::kOffCodes, kOffUnit = Lay::kOffUnit, kOffMPub = Lay::kOffMPub,
+                kOffBar = Lay::kOffBar;
+  constexpr int kBarKFull = Lay::kBarKFull, kBarKEmpty = Lay::kBarKEmpty, kBarCFull = Lay::kBarCFull, kBarVFull = Lay::kBarVFull,
+                kBarVEmpty = Lay::kBarVEmpty, kBarSFull = Lay::kBarSFull, kBarPFull = Lay::kBarPFull, kBarPvDone = Lay::kBarPvDone,
+                kBarDrain = Lay::kBarDrain, kBarPair = Lay::kBarPair, kBarMPub = Lay::kBarMPub, kNumBars = Lay::kNumBars;
   // 1024-byte alignment for the 128-byte-swizzle atoms
   const uint32_t raw_u = smem_u32(smem_raw);
   const uint32_t base = (raw_u + 1023u) & ~1023u;
@@ -233,13 +308,23 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
   auto issue_k = [&](int i) {
     const int st = i % kKSlots;
     mbar_arrive_expect_tx(bar(kBarKFull + st), kCodes);
-    tma_load_2d(sK + st * kCodes, tmk, j * kD, (int32_t)(first_slot + (int64_t)i * kPair), bar(kBarKFull + st));
+    tma_load_2d(sK + st * kCodes, &maps->k, j * kD, (int32_t)(first_slot + (int64_t)i * kPair), bar(kBarKFull + st));
   };
-  // conversion warp w's part of V's slot contents i
-  auto issue_v = [&](int w, int i) {
+  // conversion warp w's part of V's (4 bits: K's and V's) slot contents i
+  const int32_t scale_x = (int32_t)kv4_scales_at(p.n_kv, kD) + j / 2 * 16;
+  auto issue_c = [&](int w, int i) {
     const int c = w * kCSlots + i % kCSlots;
-    mbar_arrive_expect_tx(bar(kBarCFull + c), kPartCodes);
-    tma_load_2d(sC + c * kPartCodes, tmv, j * kD, (int32_t)(first_slot + (int64_t)i * kPair + w * kPart), bar(kBarCFull + c));
+    const uint32_t dst = sC + c * Lay::kCSlotBytes, full = bar(kBarCFull + c);
+    const int32_t slot = (int32_t)(first_slot + (int64_t)i * kPair + w * kPart);
+    mbar_arrive_expect_tx(full, Lay::kCSlotBytes);
+    if constexpr (BITS == 8) {
+      tma_load_2d(dst, &maps->v, j * kD, slot, full);
+    } else {
+      tma_load_2d(dst, &maps->k, j * Lay::kHead, slot, full);
+      tma_load_2d(dst + kPart * Lay::kHead, &maps->ks, scale_x, slot, full);
+      tma_load_2d(dst + Lay::kOffVc, &maps->v, j * Lay::kHead, slot, full);
+      tma_load_2d(dst + Lay::kOffVc + kPart * Lay::kHead, &maps->vs, scale_x, slot, full);
+    }
   };
   const int l2_ahead = p.l2_ahead;
   // softmax warps: this lane's row (the same for the two warps of a row quarter), its request, head and
@@ -254,11 +339,16 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
     rec = p.reqs[req].rec_base + it.split;
   }
   if (warp == kWarpTmaK && lane == 0) {
-    tma_prefetch_desc(tmk);
-    tma_prefetch_desc(tmv);
+    tma_prefetch_desc(&maps->k);
+    tma_prefetch_desc(&maps->v);
+    if constexpr (BITS == 4) {
+      tma_prefetch_desc(&maps->ks);
+      tma_prefetch_desc(&maps->vs);
+    }
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1u;
       if (i >= kBarVFull && i < kBarVFull + kVSlots) count = kConvWarps;
+      if (BITS == 4 && i >= kBarKFull && i < kBarKFull + kKSlots) count = kConvWarps;
       if (i >= kBarPFull && i < kBarPFull + kSBufs) count = kSoftmaxThreads / 2;
       if (i >= kBarPair && i < kBarPair + 4) count = 64u;
       if (i >= kBarMPub && i < kBarMPub + 8) count = 32u;
@@ -270,9 +360,10 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
     fence_proxy_async_smem();
     grid_dep_wait();  // the slab may have been written by the work before this kernel
     if (slab_ok) {
-      for (int i = 0; i < min(n_pairs, kKSlots); ++i) issue_k(i);
+      if constexpr (BITS == 8)
+        for (int i = 0; i < min(n_pairs, kKSlots); ++i) issue_k(i);
       for (int i = 0; i < min(n_pairs, kCSlots); ++i)
-        for (int w = 0; w < kConvWarps; ++w) issue_v(w, i);
+        for (int w = 0; w < kConvWarps; ++w) issue_c(w, i);
     }
   }
   if (warp == 0) {
@@ -288,19 +379,22 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
   uint32_t qw[32];
   float* part = reinterpret_cast<float*>(smem + kOffMPub);  // [2][kM], used for the maxima of tiles later
   // the scales of tile i; a softmax warp's first ones are on their way with its rows
-  const int64_t scale_at = (int64_t)p.n_kv * kD + 4 * j;
-  float ks = 0.f, vs = 0.f;
+  const int64_t scale_at = BITS == 8 ? (int64_t)p.n_kv * kD + 4 * j : kv4_units_at(p.n_kv, kD) + j;
+  using Scale = std::conditional_t<BITS == 8, float, uint8_t>;  // as it stands in the row
+  Scale ks{}, vs{};
   auto load_scales = [&](int i) {
     const int64_t a = (first_slot + (int64_t)i * kN) * p.packed_row + scale_at;
-    ks = *reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.kpool) + a);
-    vs = *reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.vpool) + a);
+    ks = *reinterpret_cast<const Scale*>(static_cast<const uint8_t*>(p.kpool) + a);
+    vs = *reinterpret_cast<const Scale*>(static_cast<const uint8_t*>(p.vpool) + a);
   };
   // V scales of the piece's tiles lane, lane + 32, .. as the bits of positive floats, for their span; requested
   // here and used when the set-up is done
   constexpr int kSpan = 4;
   uint32_t v_bits[kSpan] = {};
   auto v_scale_bits = [&](int i) {
-    return *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.vpool) + (first_slot + (int64_t)i * kN) * p.packed_row + scale_at);
+    const uint8_t* at = static_cast<const uint8_t*>(p.vpool) + (first_slot + (int64_t)i * kN) * p.packed_row + scale_at;
+    if constexpr (BITS == 8) return *reinterpret_cast<const uint32_t*>(at);
+    else return (uint32_t)*at << 23;
   };
   if (warp < kSoftmaxWarps) {
     if (slab_ok && qhalf < n_tiles) load_scales(qhalf);
@@ -330,8 +424,17 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
   const uint32_t tmem = *tmem_slot;
   if (warp < kSoftmaxWarps) {
     float unit;
-    const float f = q_factor<7>(fmaxf(part[qrow], part[kM + qrow]), unit);
+    const float f = q_factor<BITS == 8 ? 7 : 14>(fmaxf(part[qrow], part[kM + qrow]), unit);
     if (qhalf == 0) units[qrow] = unit;
+    if constexpr (BITS == 4) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const __half2 x = q_no_inf(f16x2_of(qw[k], f));
+        qw[k] = *reinterpret_cast<const uint32_t*>(&x);
+      }
+      GRANIKV_TMEM_ST32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColQ + qhalf * 32, qw);
+      tmem_wait_st();
+    } else {
     // in fp16 pairs: below 2^8 with 8 significant bits they are exact there down to 2^-17
     uint32_t hi[16], lo[16];
 #pragma unroll
@@ -346,72 +449,106 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
     tmem_st16(at, hi);
     tmem_st16(at + 32, lo);
     tmem_wait_st();
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
 
   if (warp >= kWarpConv && warp < kWarpConv + kConvWarps) {
-    // ---------------- conversion: codes of V -> fp16 operand tiles ----------------
-    // lane: dims 16 * (lane % 8) .. of tokens lane / 8 + 4 n of the part, which become two 16-byte chunks
-    // of the token's row in 64-dim half lane % 8 / 4.  Lanes of the upper half store theirs in the other
-    // order, so a store instruction covers all banks.
+    // ---------------- conversion: codes of V (4 bits: of K and V) -> fp16 operand tiles ----------------
+    // lane: dims 16 * (lane % 8) .. of tokens lane / 8 + 4 n of the part
     constexpr int kPer = kPart / 4;
     const int w = warp - kWarpConv;
-    const bool upper = (lane & 7) >= 4;
     const int lt = lane >> 3;
-    const uint32_t src_off = (uint32_t)lt * kD + (lane & 7) * 16;
-    const uint32_t row_off = (uint32_t)w * kPart * 128 + (upper ? kHalf : 0) + (uint32_t)lt * 128;
-    const uint32_t ch = (lane & 3) * 2;
-    // tokens lt and lt + 4 modulo 8 have two swizzles
-    const uint32_t lo0 = row_off + ((ch ^ lt) << 4), hi0 = row_off + (((ch + 1) ^ lt) << 4);
-    const uint32_t lo1 = row_off + ((ch ^ (lt + 4)) << 4), hi1 = row_off + (((ch + 1) ^ (lt + 4)) << 4);
+    const ConvLane cl(w, lane);
     int issued = slab_ok ? min(n_pairs, kCSlots) : 0, seen = 0;
+    auto free_slot = [&](int empty, int slots, int i) {  // the slot for contents i, once its last ones are read
+      const bool ok = i < slots || mbar_wait_bounded(bar(empty + i % slots), ((i / slots) - 1) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
+      return __all_sync(0xffffffffu, ok) != 0;
+    };
     for (int i = 0; slab_ok && i < n_pairs; ++i) {
       const int c = w * kCSlots + i % kCSlots, st = i % kVSlots;
       bool ok = mbar_wait_bounded(bar(kBarCFull + c), (i / kCSlots) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;  // the abort flag is up: every other role leaves as well
       seen = i + 1;
-      const uint32_t src = sC + c * kPartCodes + src_off, dst = sV + st * kTile;
-      uint4 x[kPer];
-#pragma unroll
-      for (int n = 0; n < kPer; ++n) x[n] = lds128(src + n * 4 * kD);
+      const uint32_t src = sC + c * Lay::kCSlotBytes, dst = sV + st * kTile;
       const int valid = t1 - t0 - i * kPair - w * kPart;  // tokens of the part in range, or more
-      if (valid < kPart) {  // 0 * whatever lies past the piece must not reach O
+      if constexpr (BITS == 8) {
+        const uint32_t src_off = (uint32_t)lt * kD + (lane & 7) * 16;
+        uint4 x[kPer];
 #pragma unroll
-        for (int n = 0; n < kPer; ++n)
-          if (lt + 4 * n >= valid) x[n] = make_uint4(0u, 0u, 0u, 0u);
-      }
-      if (i >= kVSlots) {
-        ok = mbar_wait_bounded(bar(kBarVEmpty + st), ((i / kVSlots) - 1) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-      }
+        for (int n = 0; n < kPer; ++n) x[n] = lds128(src + src_off + n * 4 * kD);
+        if (valid < kPart) {  // 0 * whatever lies past the piece must not reach O
 #pragma unroll
-      for (int n = 0; n < kPer; ++n) {
-        uint32_t y[8];
-        e4m3x4_to_f16x4(x[n].x, y[0], y[1]);
-        e4m3x4_to_f16x4(x[n].y, y[2], y[3]);
-        e4m3x4_to_f16x4(x[n].z, y[4], y[5]);
-        e4m3x4_to_f16x4(x[n].w, y[6], y[7]);
-        const uint32_t lo = dst + n * 4 * 128 + (n & 1 ? lo1 : lo0), hi = dst + n * 4 * 128 + (n & 1 ? hi1 : hi0);
-        if (upper) {
-          sts128(hi, y[4], y[5], y[6], y[7]);
-          sts128(lo, y[0], y[1], y[2], y[3]);
-        } else {
-          sts128(lo, y[0], y[1], y[2], y[3]);
-          sts128(hi, y[4], y[5], y[6], y[7]);
+          for (int n = 0; n < kPer; ++n)
+            if (lt + 4 * n >= valid) x[n] = make_uint4(0u, 0u, 0u, 0u);
         }
+        if (!free_slot(kBarVEmpty, kVSlots, i)) break;
+#pragma unroll
+        for (int n = 0; n < kPer; ++n) {
+          uint32_t y[8];
+          e4m3x4_to_f16x4(x[n].x, y[0], y[1]);
+          e4m3x4_to_f16x4(x[n].y, y[2], y[3]);
+          e4m3x4_to_f16x4(x[n].z, y[4], y[5]);
+          e4m3x4_to_f16x4(x[n].w, y[6], y[7]);
+          cl.store(dst, n, y);
+        }
+      } else {
+        uint2 x[kPer];
+        uint32_t b[kPer];
+        auto load = [&](uint32_t from) {
+#pragma unroll
+          for (int n = 0; n < kPer; ++n) {
+            x[n] = lds64(from + (uint32_t)(lt + 4 * n) * Lay::kHead + (lane & 7) * 8);
+            b[n] = lds8(from + kPart * Lay::kHead + (uint32_t)(lt + 4 * n) * 16 + (j & 1) * 8 + (lane & 7));
+          }
+        };
+        auto convert = [&](uint32_t to) {
+#pragma unroll
+          for (int n = 0; n < kPer; ++n) {
+            const uint32_t f = kv4_scale2(b[n]);
+            uint32_t lo[4], hi[4], y[8];
+            e2m1x8_to_f16x8(x[n].x, lo);
+            e2m1x8_to_f16x8(x[n].y, hi);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              y[k] = f16x2_mul(lo[k], f);
+              y[4 + k] = f16x2_mul(hi[k], f);
+            }
+            cl.store(to, n, y);
+          }
+        };
+        load(src);
+        if (!free_slot(kBarKEmpty, kKSlots, i)) break;
+        convert(sK + i % kKSlots * kTile);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarKFull + i % kKSlots));
+        load(src + Lay::kOffVc);
+        if (valid < kPart) {  // 0 * whatever lies past the piece must not reach O
+#pragma unroll
+          for (int n = 0; n < kPer; ++n)
+            if (lt + 4 * n >= valid) {
+              x[n] = make_uint2(0u, 0u);
+              b[n] = 0u;
+            }
+        }
+        if (!free_slot(kBarVEmpty, kVSlots, i)) break;
+        convert(dst);
       }
       fence_proxy_async_smem();
       __syncwarp();  // the warp has stored its part, and read its codes
       if (lane == 0) {
         mbar_arrive(bar(kBarVFull + st));
         if (i + kCSlots < n_pairs) {
-          issue_v(w, i + kCSlots);
-          if (l2_ahead > 0 && i + kCSlots + l2_ahead < n_pairs)
-            tma_prefetch_l2_2d(tmv, j * kD, (int32_t)(first_slot + (int64_t)(i + kCSlots + l2_ahead) * kPair + w * kPart));
+          issue_c(w, i + kCSlots);
+          if (l2_ahead > 0 && i + kCSlots + l2_ahead < n_pairs) {
+            const int32_t slot = (int32_t)(first_slot + (int64_t)(i + kCSlots + l2_ahead) * kPair + w * kPart);
+            tma_prefetch_l2_2d(&maps->v, j * Lay::kHead, slot);
+            if constexpr (BITS == 4) tma_prefetch_l2_2d(&maps->k, j * Lay::kHead, slot);
+          }
           issued = i + kCSlots + 1;
         }
       }
@@ -429,8 +566,8 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
       }
     }
   } else if (warp == kWarpTmaK) {
-    // ---------------- TMA loads of K ----------------
-    if (lane == 0) {
+    // ---------------- TMA loads of K (8 bits) ----------------
+    if (BITS == 8 && lane == 0) {
       int issued = slab_ok ? min(n_pairs, kKSlots) : 0;
       for (int i = issued; slab_ok && i < n_pairs; ++i) {
         if (!mbar_wait_bounded(bar(kBarKEmpty + i % kKSlots), ((i / kKSlots) - 1) & 1, abort_flag, p.err, kDevTimeout,
@@ -438,7 +575,7 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
           break;
         issue_k(i);
         if (l2_ahead > 0 && i + l2_ahead < n_pairs)
-          tma_prefetch_l2_2d(tmk, j * kD, (int32_t)(first_slot + (int64_t)(i + l2_ahead) * kPair));
+          tma_prefetch_l2_2d(&maps->k, j * kD, (int32_t)(first_slot + (int64_t)(i + l2_ahead) * kPair));
         issued = i + 1;
       }
       // never leave with a copy in flight
@@ -476,10 +613,12 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
           tc_fence_after();
           const uint32_t dS = tm + (uint32_t)((i % kSBufs) * kN);
           const int st = (i >> 1) % kKSlots;
-          const uint64_t dk = dk0 + (uint64_t)((st * kCodes + (i & 1) * kN * kD) >> 4);
+          const uint64_t dk = dk0 + (uint64_t)((st * Lay::kKSlotBytes + (i & 1) * kN * 128) >> 4);  // rows of 128 bytes
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)  // lo, the smaller, first
-            if (el)
+          for (int kk = 0; kk < 8; ++kk)  // 8 bits: lo, the smaller, first; 4 bits: 16 dims each, four of a 64-dim half
+            if (el && BITS == 4)
+              umma_f16_ts(dS, tm + kColQ + kk * 8, dk + (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
+            else if (el)
               umma_f8_ts(dS, tm + kColQ + (kk < 4 ? 32 : 0) + (kk & 3) * 8, dk + (uint64_t)(((kk & 3) * 32) >> 4), idS,
                          kk > 0 ? 1u : 0u);
           if (el) {
@@ -550,14 +689,23 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
     for (int i = lane + 32 * kSpan; ok && i < n_tiles; i += 32) span_of(v_scale_bits(i));
     v_min = __reduce_min_sync(0xffffffffu, v_min) + 1u;
     const bool wide = __reduce_max_sync(0xffffffffu, v_max) - v_min > kWideSpan << 23;
-    const float least = lg2_approx(__uint_as_float(v_min));  // log2 of the piece's smallest V scale
+    // log2 of the piece's smallest V scale
+    const float least = BITS == 8 ? lg2_approx(__uint_as_float(v_min)) : (float)((int)(v_min >> 23) - 127);
     // (a loop for each: in one loop the untaken branch cost 2 % of a 16K prefix)
     auto all_tiles = [&](auto wide_span) {
       constexpr bool kWide = decltype(wide_span)::value;
       for (int i = par; ok && i < n_tiles; i += 2) {
         const int sb = i % kSBufs;
         // (at least the smallest normal number: 0 * -inf of a masked key would be NaN)
-        const float ca = fmaxf(scale * ks, FLT_MIN), cb = lg2_approx(vs);
+        float ca, cb;
+        if constexpr (BITS == 8) {
+          ca = scale * ks;
+          cb = lg2_approx(vs);
+        } else {
+          ca = scale * kv4_unit(ks);
+          cb = (float)((int)vs - 127);
+        }
+        ca = fmaxf(ca, FLT_MIN);
         if (i + 2 < n_tiles) load_scales(i + 2);
         // the max used for tile i-1, decided by the other warp of the quarter
         float m_prev = -INFINITY;
@@ -740,5 +888,5 @@ __device__ __forceinline__ void kv8_dense_body(const AttnParams& p, int32_t item
 }
 
 }  // namespace
-}  // namespace k8d
+}  // namespace pkd
 }  // namespace granikv

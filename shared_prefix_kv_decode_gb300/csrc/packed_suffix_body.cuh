@@ -1,11 +1,11 @@
-// kv8_suffix_body.cuh -- COLD suffix partial attention over the 8-bit cache: bulk-copy gather of
+// packed_suffix_body.cuh -- COLD suffix partial attention over the 8- or 4-bit cache: bulk-copy gather of
 // packed rows, warp-level fp16 tensor cores.
 //
 // Shape: head_dim 128, bf16 q, g = n_q/n_kv <= 8.  A consumer warp owns one KV head of one request
 // segment; tokens are the MMA's M dimension, the g query heads its N dimension (8 columns):
 //     S^T[16 tok x 8] = K[16 tok x 128] . Q^T[128 x 8]       (8 mma.m16n8k16, fp16)
 //     O^T[128 x 8]   += V^T[128 x 16 tok] . P^T[16 tok x 8]  (8 mma.m16n8k16, fp16)
-// Number format.  Codes become fp16 exactly (one conversion per pair, on the way from ldmatrix to
+// Number format (8 bits; what 4 bits change stands below).  Codes become fp16 exactly (one conversion per pair, on the way from ldmatrix to
 // the MMA); q is brought into fp16's range by a power of two per query head (exact but for elements
 // 2^-31 below the row's largest).  With ks, vs the token's scales, y = s ks and z = y + log2 vs (base 2), the
 // running maximum m is taken over z and P = 2^(z - m) is what meets the V codes (p times vs), so a token with
@@ -31,9 +31,16 @@
 // Bound by HBM on scattered rows: 71K tokens (150 MB, 128 requests) alone take 31.6 us with the merge, about
 // 5.8 TB/s once the rings are full; without the conversions the time is the same.  One tile at a time and one
 // producer warp took 48.1.
+//
+// 4 bits.  An element is code * b * u, b the e4m3 scale of its 16 dims and u the token's power of two: code * b goes
+// into fp16 exactly (one conversion and one product a pair), u takes the place of the scales ks and vs above, so
+// log2 vs is a whole number.  The 16-bit pairs that ldmatrix moves are four codes: a lane's eight codes of a row serve
+// two k-steps of S^T, and the transposed form gives two tokens x four dims, whose nibbles are paired by shifts.
+// u lies between 2^-100 and 2^116, inside the range that the row sum is made for.
 #pragma once
 
 #include "internal.h"
+#include "kv4_util.cuh"
 #include "kv8_util.cuh"
 #include "launch_util.cuh"
 #include "mma_util.cuh"
@@ -42,27 +49,33 @@
 #include <type_traits>
 
 namespace granikv {
-namespace k8s {
+namespace pks {
 namespace {
 
 constexpr int kD = 128;
 constexpr int kTile = 16;                          // tokens per tile (MMA M)
-constexpr int kStages = 6;
 constexpr int kWarps = 8;                          // consumer warps: KV heads per CTA
 constexpr int kProducers = 8;                      // producer warps: two of a tile's rows each
 constexpr int kRowsEach = kTile / kProducers;
 constexpr int kThreads = (kWarps + kProducers) * 32;
-constexpr int kRowMax = kWarps * (kD + 4);         // packed row of eight heads: 1,056 B
-constexpr int kRowStride = kRowMax + 16;           // 1,072 B: 48 modulo 128
-constexpr int kTileBytes = kTile * kRowStride;
-constexpr int kStageBytes = 2 * kTileBytes;        // K + V: 34,304 B
-constexpr int kOffSlots = kStages * kStageBytes;
-constexpr int kOffSegs = kOffSlots + kSuffixMaxCtaTokens * 4;
 constexpr int kSegSmem = 256;                      // segment descriptors staged in shared memory
-constexpr int kOffBar = kOffSegs + kSegSmem * (int)sizeof(DevSuffixItem);
-constexpr int kSmemBytes = kOffBar + 8 * 2 * kStages + 16;
-static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-static_assert(kRowStride % 128 == 48, "ldmatrix bank groups");
+// Packed rows of eight heads in shared memory, 16 modulo 32 bytes apart: the eight rows that an ldmatrix reads lie in
+// eight different 16-byte bank groups.  8 bits: 1,056 bytes, 4 bits: 592.  The stages fill what shared memory there is.
+template <int BITS>
+struct Layout {
+  static constexpr int kCodes = kD * BITS / 8;     // bytes of a head's codes
+  static constexpr int kRowMax = BITS == 8 ? kWarps * (kD + 4) : (int)kv4_row_bytes(kWarps, kD);
+  static constexpr int kRowStride = kRowMax + (kRowMax % 32 ? 0 : 16);
+  static constexpr int kStages = BITS == 8 ? 6 : 11;
+  static constexpr int kTileBytes = kTile * kRowStride;
+  static constexpr int kStageBytes = 2 * kTileBytes;  // K + V: 34,304 B (8 bits)
+  static constexpr int kOffSlots = kStages * kStageBytes;
+  static constexpr int kOffSegs = kOffSlots + kSuffixMaxCtaTokens * 4;
+  static constexpr int kOffBar = kOffSegs + kSegSmem * (int)sizeof(DevSuffixItem);
+  static constexpr int kSmemBytes = kOffBar + 8 * 2 * kStages + 16;
+  static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+  static_assert(kRowStride % 32 == 16, "ldmatrix bank groups");
+};
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kShift = 14.f;                     // log2 of the factor that P carries
 constexpr float kSumShift = 10.f;                  // and that the row sum does
@@ -70,7 +83,7 @@ static_assert(kSuffixMaxCtaTokens <= 4096, "the row sum's range");
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // Source of the rows of masked tokens (zero-initialised at module load, never written).
-__device__ __align__(128) uint4 g_zero_row[kRowMax / 16];
+__device__ __align__(128) uint4 g_zero_row[Layout<8>::kRowMax / 16];
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t mbar) {
   asm volatile(
@@ -91,11 +104,29 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Two tokens' four codes (lane word of a transposed ldmatrix: token 2 c in the low half) -> for each of the four dims
+// the two tokens' values as fp16x2, times the tokens' scales.
+__device__ __forceinline__ void kv4_transposed(uint32_t w, uint32_t scale2, uint32_t (&y)[4]) {
+  constexpr uint32_t M = 0x0f0f0f0fu;
+  const uint32_t even = (w & M) | ((w >> 12) & ~M), odd = ((w >> 4) & M) | ((w >> 16) & ~M);  // dims 0, 2 and 1, 3 in two bytes
+  e2m1x8_to_f16x8(__byte_perm(even, odd, 0x5140), y);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = f16x2_mul(y[i], scale2);
+}
+// The four e4m3 bytes that sel picks of two words, in pairs, as fp16x2.
+__device__ __forceinline__ void scale_pairs(uint32_t a, uint32_t b, uint32_t sel, uint32_t& lo, uint32_t& hi) {
+  e4m3x4_to_f16x4(__byte_perm(a, b, sel), lo, hi);
+}
+
 // One token-CTA `cta` of the suffix work list, for KV-head group `group`, on `smem` (at least
-// kSmemBytes, 128-byte aligned), run by kThreads or more threads (the extra warps only take
+// Layout<BITS>::kSmemBytes, 128-byte aligned), run by kThreads or more threads (the extra warps only take
 // part in the set-up barriers).
-__device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32_t* __restrict__ cta_begin, int cta,
+template <int BITS>
+__device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const int32_t* __restrict__ cta_begin, int cta,
                                                 int group, unsigned char* smem) {
+  using Lay = Layout<BITS>;
+  constexpr int kStages = Lay::kStages, kTileBytes = Lay::kTileBytes, kStageBytes = Lay::kStageBytes, kRowStride = Lay::kRowStride;
+  constexpr int kOffSlots = Lay::kOffSlots, kOffSegs = Lay::kOffSegs, kOffBar = Lay::kOffBar;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int seg_begin = cta_begin[cta];
@@ -103,8 +134,11 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
   if (seg_begin >= seg_end) return;
   const int j0 = group * kWarps;                      // first KV head of this CTA's group
   const int nh = min(kWarps, p.n_kv - j0);            // heads in the group
-  const uint32_t code_bytes = (uint32_t)nh * kD;
-  const uint32_t scale_bytes = (uint32_t)(nh + 3) / 4 * 16;  // the row is padded to 16 bytes
+  // the parts of a row that the group reads, each from a 16-byte boundary on and of a multiple of 16 bytes
+  const uint32_t code_bytes = (uint32_t)nh * Lay::kCodes;
+  const uint32_t scale_bytes = BITS == 8 ? (uint32_t)(nh + 3) / 4 * 16 : (uint32_t)(nh + 1) / 2 * 16;
+  const uint32_t unit_bytes = BITS == 8 ? 0u : 16u;
+  const uint32_t row_bytes = code_bytes + scale_bytes + unit_bytes;
   const uint32_t sbase = smem_u32(smem);
   auto full_bar = [&](int st) { return sbase + kOffBar + 8 * st; };
   auto empty_bar = [&](int st) { return sbase + kOffBar + 8 * (kStages + st); };
@@ -159,7 +193,9 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
     if (part >= kProducers) return;
     const bool is_v = (lane & (2 * kRowsEach - 1)) >= kRowsEach;
     const uint8_t* pool = static_cast<const uint8_t*>(is_v ? p.vpool : p.kpool);
-    const int64_t code_off = (int64_t)j0 * kD, scale_off = (int64_t)p.n_kv * kD + 4 * j0;
+    const int64_t code_off = (int64_t)j0 * Lay::kCodes;
+    const int64_t scale_off = BITS == 8 ? (int64_t)p.n_kv * kD + 4 * j0 : kv4_scales_at(p.n_kv, kD) + j0 * (kD / kKv4Group);
+    const int64_t unit_off = kv4_units_at(p.n_kv, kD) + j0 / 16 * 16;
     const bool whole = p.n_kv <= kWarps;  // codes and scales are one run of bytes
     const int r = part * kRowsEach + (lane & (kRowsEach - 1));
     int n = 0;    // tiles issued
@@ -185,16 +221,17 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
           else latch_err(p.err, kDevBadSlot);
         }
         if (skip0 && n == 0) continue;
-        if (lane == 0) mbar_arrive_expect_tx(full_bar(st), 2u * kRowsEach * (code_bytes + scale_bytes));
+        if (lane == 0) mbar_arrive_expect_tx(full_bar(st), 2u * kRowsEach * row_bytes);
         __syncwarp();
         if (lane >= 2 * kRowsEach) continue;
         const uint32_t dst = sbase + st * kStageBytes + (is_v ? kTileBytes : 0) + r * kRowStride;
         const uint8_t* zero = reinterpret_cast<const uint8_t*>(g_zero_row);
         if (whole) {
-          bulk_load(dst, row ? row : zero, code_bytes + scale_bytes, full_bar(st));
+          bulk_load(dst, row ? row : zero, row_bytes, full_bar(st));
         } else {
           bulk_load(dst, row ? row + code_off : zero, code_bytes, full_bar(st));
           bulk_load(dst + code_bytes, row ? row + scale_off : zero, scale_bytes, full_bar(st));
+          if constexpr (BITS == 4) bulk_load(dst + code_bytes + scale_bytes, row ? row + unit_off : zero, unit_bytes, full_bar(st));
         }
       }
       pos += seg.t1 - seg.t0;
@@ -222,17 +259,30 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
   const int r = lane >> 2, c = lane & 3;
   const int h0 = 2 * c;  // this thread's two head columns: h0, h0 + 1
   // Q^T as B fragments in the order of the K codes: k-step i takes dims 16 i + 4 c + {0, 1} and {2, 3}
-  // of column r (query head j*g + r); the next segment's rows are loaded one segment ahead
+  // of column r (query head j*g + r), 4 bits: 32 (i / 2) + 8 c + 4 (i % 2) + {0, 1} and {2, 3}; the next segment's rows
+  // are loaded one segment ahead
   uint32_t qn[16];
   auto load_q = [&](int sg) {
     if (sg < n_seg && r < g) {
-      const uint2* qrow = reinterpret_cast<const uint2*>(
-          static_cast<const __nv_bfloat16*>(p.q) + ((int64_t)seg_at(sg).b * p.n_q + j * g + r) * kD);
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + ((int64_t)seg_at(sg).b * p.n_q + j * g + r) * kD;
+      if constexpr (BITS == 8) {
+        const uint2* qrow = reinterpret_cast<const uint2*>(q);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint2 x = qrow[4 * i + c];
-        qn[2 * i] = x.x;
-        qn[2 * i + 1] = x.y;
+        for (int i = 0; i < 8; ++i) {
+          const uint2 x = qrow[4 * i + c];
+          qn[2 * i] = x.x;
+          qn[2 * i + 1] = x.y;
+        }
+      } else {
+        const uint4* qrow = reinterpret_cast<const uint4*>(q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 x = qrow[4 * i + c];
+          qn[4 * i] = x.x;
+          qn[4 * i + 1] = x.y;
+          qn[4 * i + 2] = x.z;
+          qn[4 * i + 3] = x.w;
+        }
       }
     } else {
 #pragma unroll
@@ -240,8 +290,9 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
     }
   };
   load_q(0);
-  const uint32_t head_off = (uint32_t)warp * kD;
-  const uint32_t scale_at = code_bytes + 4 * (uint32_t)warp;
+  const uint32_t head_off = (uint32_t)warp * Lay::kCodes;
+  const uint32_t scale_at = code_bytes + (BITS == 8 ? 4 : kD / kKv4Group) * (uint32_t)warp;
+  const uint32_t unit_at = code_bytes + scale_bytes + (uint32_t)(j0 % 16 + warp);
   int tile = 0;  // tiles consumed so far
   for (int sg = 0; sg < n_seg; ++sg) {
     const DevSuffixItem seg = seg_at(sg);
@@ -273,6 +324,7 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
       const uint32_t frag = head_off + ((lane & 7) + (mi & 1) * 8) * kRowStride + (mi >> 1) * 16;
       uint32_t at[V];  // this lane's ldmatrix row of each tile
       float sa[V], sb[V], la[V], lb[V], s[V][4], s2[V][4];
+      uint2 ka[V], kb[V];  // 4 bits: the K scales of tokens r and r + 8
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int st = (tile + v) % kStages;
@@ -280,30 +332,71 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
                                               kWaitLimitNs);
         if (!__all_sync(0xffffffffu, landed)) return false;
         at[v] = sbase + st * kStageBytes + frag;
-        // the scales of tokens r and r + 8
-        const unsigned char* ksp = smem + st * kStageBytes + r * kRowStride + scale_at;
-        sa[v] = *reinterpret_cast<const float*>(ksp);
-        sb[v] = *reinterpret_cast<const float*>(ksp + 8 * kRowStride);
-        la[v] = *reinterpret_cast<const float*>(ksp + kTileBytes);
-        lb[v] = *reinterpret_cast<const float*>(ksp + kTileBytes + 8 * kRowStride);
+        // the scales (4 bits: units) of tokens r and r + 8
+        if constexpr (BITS == 8) {
+          const unsigned char* ksp = smem + st * kStageBytes + r * kRowStride + scale_at;
+          sa[v] = *reinterpret_cast<const float*>(ksp);
+          sb[v] = *reinterpret_cast<const float*>(ksp + 8 * kRowStride);
+          la[v] = *reinterpret_cast<const float*>(ksp + kTileBytes);
+          lb[v] = *reinterpret_cast<const float*>(ksp + kTileBytes + 8 * kRowStride);
+        } else {
+          const unsigned char* up = smem + st * kStageBytes + r * kRowStride + unit_at;
+          sa[v] = kv4_unit(up[0]);
+          sb[v] = kv4_unit(up[8 * kRowStride]);
+          la[v] = kv4_unit(up[kTileBytes]);
+          lb[v] = kv4_unit(up[kTileBytes + 8 * kRowStride]);
+          const unsigned char* ksp = smem + st * kStageBytes + r * kRowStride + scale_at;
+          ka[v] = *reinterpret_cast<const uint2*>(ksp);
+          kb[v] = *reinterpret_cast<const uint2*>(ksp + 8 * kRowStride);
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[v][e] = s2[v][e] = 0.f;
       }
       // S^T = K . Q^T, in two accumulation chains a tile
+      if constexpr (BITS == 4) {
+        const uint32_t sel = c & 2 ? 0x3311u : 0x2200u;  // of the scales of dims 32 i .., those of this lane's 16, twice
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t w[V][4];
+        for (int i = 0; i < 2; ++i) {
+          uint32_t w[V][4];
 #pragma unroll
-        for (int v = 0; v < V; ++v) ldsm_x4(at[v] + i * 32, w[v][0], w[v][1], w[v][2], w[v][3]);
+          for (int v = 0; v < V; ++v) ldsm_x4(at[v] + i * 32, w[v][0], w[v][1], w[v][2], w[v][3]);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          uint32_t a0, a1, a2, a3;
-          e4m3x4_to_f16x4(w[v][0], a0, a2);
-          e4m3x4_to_f16x4(w[v][1], a1, a3);
-          mma_f16_16816(s[v], a0, a1, a2, a3, qf[4 * i], qf[4 * i + 1]);
-          e4m3x4_to_f16x4(w[v][2], a0, a2);
-          e4m3x4_to_f16x4(w[v][3], a1, a3);
-          mma_f16_16816(s2[v], a0, a1, a2, a3, qf[4 * i + 2], qf[4 * i + 3]);
+          for (int v = 0; v < V; ++v) {
+            uint32_t fa[2], fb[2];
+            scale_pairs(i ? ka[v].y : ka[v].x, 0u, sel, fa[0], fa[1]);
+            scale_pairs(i ? kb[v].y : kb[v].x, 0u, sel, fb[0], fb[1]);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {  // 32 dims
+              uint32_t ya[4], yb[4];
+              e2m1x8_to_f16x8(w[v][2 * u], ya);
+              e2m1x8_to_f16x8(w[v][2 * u + 1], yb);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                ya[k] = f16x2_mul(ya[k], fa[u]);
+                yb[k] = f16x2_mul(yb[k], fb[u]);
+              }
+              const uint32_t* qk = qf + 8 * i + 4 * u;
+              mma_f16_16816(s[v], ya[0], yb[0], ya[1], yb[1], qk[0], qk[1]);
+              mma_f16_16816(s2[v], ya[2], yb[2], ya[3], yb[3], qk[2], qk[3]);
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[V][4];
+#pragma unroll
+          for (int v = 0; v < V; ++v) ldsm_x4(at[v] + i * 32, w[v][0], w[v][1], w[v][2], w[v][3]);
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16x4(w[v][0], a0, a2);
+            e4m3x4_to_f16x4(w[v][1], a1, a3);
+            mma_f16_16816(s[v], a0, a1, a2, a3, qf[4 * i], qf[4 * i + 1]);
+            e4m3x4_to_f16x4(w[v][2], a0, a2);
+            e4m3x4_to_f16x4(w[v][3], a1, a3);
+            mma_f16_16816(s2[v], a0, a1, a2, a3, qf[4 * i + 2], qf[4 * i + 3]);
+          }
         }
       }
       const int rem = seg.t1 - t;  // valid tokens from the first tile on
@@ -312,8 +405,13 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
       for (int v = 0; v < V; ++v) {
         // (the zero row of a token that does not count has scale 0)
         const bool in_a = v * kTile + r < rem && la[v] != 0.f, in_b = v * kTile + r + 8 < rem && lb[v] != 0.f;
-        la[v] = lg2_approx(la[v]);
-        lb[v] = lg2_approx(lb[v]);
+        if constexpr (BITS == 8) {
+          la[v] = lg2_approx(la[v]);
+          lb[v] = lg2_approx(lb[v]);
+        } else {  // (a whole number; whatever it is for a token that does not count)
+          la[v] = (float)((int)(__float_as_uint(la[v]) >> 23) - 127);
+          lb[v] = (float)((int)(__float_as_uint(lb[v]) >> 23) - 127);
+        }
         s[v][0] = in_a ? (s[v][0] + s2[v][0]) * (f0 * sa[v]) : -INFINITY;
         s[v][1] = in_a ? (s[v][1] + s2[v][1]) * (f1 * sa[v]) : -INFINITY;
         s[v][2] = in_b ? (s[v][2] + s2[v][2]) * (f0 * sb[v]) : -INFINITY;
@@ -358,21 +456,49 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
         b0[v] = movmatrix_t(pack_f16(p0, p1));
         b1[v] = movmatrix_t(pack_f16(p2, p3));
       }
-      // O^T += V^T . P^T: m-tile mt holds dims 16 mt + 2 r (row r) and 16 mt + 2 r + 1 (row r + 8)
+      // O^T += V^T . P^T: m-tile mt holds dims 16 mt + 2 r (row r) and 16 mt + 2 r + 1 (row r + 8); 4 bits: dims
+      // 32 (mt / 2) + 4 r + 2 (mt % 2) and the next
+      if constexpr (BITS == 4) {
+        const uint32_t sel = r & 4 ? 0x7351u : 0x6240u;  // of two tokens' scales of 64 dims, those of this lane's 16, side by side
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t w[V][4];
+        for (int i = 0; i < 2; ++i) {
+          uint32_t w[V][4];
 #pragma unroll
-        for (int v = 0; v < V; ++v) ldsm_x4_t(at[v] + kTileBytes + i * 32, w[v][0], w[v][1], w[v][2], w[v][3]);
+          for (int v = 0; v < V; ++v) ldsm_x4_t(at[v] + kTileBytes + i * 32, w[v][0], w[v][1], w[v][2], w[v][3]);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          uint32_t a0, a1, a2, a3;
-          e4m3x4_to_f16x4(__byte_perm(w[v][0], 0, 0x3120), a0, a1);
-          e4m3x4_to_f16x4(__byte_perm(w[v][1], 0, 0x3120), a2, a3);
-          mma_f16_16816(o[2 * i], a0, a1, a2, a3, b0[v], b1[v]);
-          e4m3x4_to_f16x4(__byte_perm(w[v][2], 0, 0x3120), a0, a1);
-          e4m3x4_to_f16x4(__byte_perm(w[v][3], 0, 0x3120), a2, a3);
-          mma_f16_16816(o[2 * i + 1], a0, a1, a2, a3, b0[v], b1[v]);
+          for (int v = 0; v < V; ++v) {
+            // the scales of tokens 2 c, 2 c + 1, 2 c + 8 and 2 c + 9
+            const unsigned char* vsp = smem + ((tile + v) % kStages) * kStageBytes + kTileBytes + 2 * c * kRowStride + scale_at + 4 * i;
+            auto word = [&](int t) { return *reinterpret_cast<const uint32_t*>(vsp + t * kRowStride); };
+            uint32_t fa[2], fb[2];
+            scale_pairs(word(0), word(1), sel, fa[0], fa[1]);
+            scale_pairs(word(8), word(9), sel, fb[0], fb[1]);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {  // 32 dims
+              uint32_t ya[4], yb[4];
+              kv4_transposed(w[v][2 * u], fa[u], ya);
+              kv4_transposed(w[v][2 * u + 1], fb[u], yb);
+              mma_f16_16816(o[4 * i + 2 * u], ya[0], ya[1], yb[0], yb[1], b0[v], b1[v]);
+              mma_f16_16816(o[4 * i + 2 * u + 1], ya[2], ya[3], yb[2], yb[3], b0[v], b1[v]);
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[V][4];
+#pragma unroll
+          for (int v = 0; v < V; ++v) ldsm_x4_t(at[v] + kTileBytes + i * 32, w[v][0], w[v][1], w[v][2], w[v][3]);
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16x4(__byte_perm(w[v][0], 0, 0x3120), a0, a1);
+            e4m3x4_to_f16x4(__byte_perm(w[v][1], 0, 0x3120), a2, a3);
+            mma_f16_16816(o[2 * i], a0, a1, a2, a3, b0[v], b1[v]);
+            e4m3x4_to_f16x4(__byte_perm(w[v][2], 0, 0x3120), a0, a1);
+            e4m3x4_to_f16x4(__byte_perm(w[v][3], 0, 0x3120), a2, a3);
+            mma_f16_16816(o[2 * i + 1], a0, a1, a2, a3, b0[v], b1[v]);
+          }
         }
       }
       // this warp is done reading the stages
@@ -409,13 +535,21 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
     const float inv0 = l0 == 0.f ? 0.f : kUnit / l0;
     const float inv1 = l1 == 0.f ? 0.f : kUnit / l1;
     const int hq0 = j * g + h0;
-    float* dst0 = p.rec_o + ((int64_t)rec * p.n_q + hq0) * kD + 2 * r;
+    float* dst0 = p.rec_o + ((int64_t)rec * p.n_q + hq0) * kD + (BITS == 8 ? 2 : 4) * r;
     const bool w0 = h0 < g, w1 = h0 + 1 < g;
     const uint64_t keep = l2_policy_keep();
+    if constexpr (BITS == 8) {
 #pragma unroll
-    for (int mt = 0; mt < 8; ++mt) {
-      if (w0) st_record2(dst0 + mt * 16, o[mt][0] * inv0, o[mt][2] * inv0, keep);
-      if (w1) st_record2(dst0 + kD + mt * 16, o[mt][1] * inv1, o[mt][3] * inv1, keep);
+      for (int mt = 0; mt < 8; ++mt) {
+        if (w0) st_record2(dst0 + mt * 16, o[mt][0] * inv0, o[mt][2] * inv0, keep);
+        if (w1) st_record2(dst0 + kD + mt * 16, o[mt][1] * inv1, o[mt][3] * inv1, keep);
+      }
+    } else {
+#pragma unroll
+      for (int mt = 0; mt < 8; mt += 2) {
+        if (w0) st_record4(dst0 + mt * 16, make_float4(o[mt][0] * inv0, o[mt][2] * inv0, o[mt + 1][0] * inv0, o[mt + 1][2] * inv0), keep);
+        if (w1) st_record4(dst0 + kD + mt * 16, make_float4(o[mt][1] * inv1, o[mt][3] * inv1, o[mt + 1][1] * inv1, o[mt + 1][3] * inv1), keep);
+      }
     }
     if (lane < 4) {
       float* ldst = p.rec_lse + (int64_t)rec * p.n_q + hq0;
@@ -426,5 +560,5 @@ __device__ __forceinline__ void kv8_suffix_body(const AttnParams& p, const int32
 }
 
 }  // namespace
-}  // namespace k8s
+}  // namespace pks
 }  // namespace granikv
