@@ -75,6 +75,8 @@ namespace {
 
 using pks::lg2_approx;
 using pks::pack_f16;
+using pks::regs_down;
+using pks::regs_up;
 
 constexpr int kD = 128;
 constexpr int kM = kDenseRows;                // 128 query rows per CTA
@@ -85,38 +87,40 @@ constexpr int kVSlots = 3;                    // slots of the V ring (fp16)
 constexpr int kSBufs = 5;                     // S/P buffers in TMEM
 constexpr int kSoftmaxWarps = 8;
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
-constexpr int kWarpConv = 8, kConvWarps = 4;
-constexpr int kPart = kPair / kConvWarps;     // tokens of a V slot that one warp converts
-constexpr int kWarpS = 12, kWarpPv = 13, kWarpTmaK = 14;
-constexpr int kThreads = 512;  // one more warp, for the suffix body's producers
+constexpr int kWarpConv = 8, kParts = 4;
+constexpr int kPart = kPair / kParts;         // tokens of a slot that one warp converts
 constexpr int kHalf = kPair * 128;            // one 64-dim half of an fp16 slot: 16 KB
 constexpr int kTile = 2 * kHalf;              // 32 KB
 constexpr int kCodes = kPair * kD;            // a slot's codes: 16 KB
 constexpr int kPartCodes = kPart * kD;        // 4 KB
-constexpr int kBarArea = 512;
 template <int BITS>
 struct Layout {
+  // 8 bits: kParts warps convert V.  4 bits: as many convert K, before them.  (One more warp, for the suffix body's producers.)
+  static constexpr int kConvWarps = BITS == 8 ? kParts : 2 * kParts;
+  static constexpr int kWarpS = kWarpConv + kConvWarps, kWarpPv = kWarpS + 1, kWarpTmaK = kWarpS + 2;
+  static constexpr int kThreads = (kWarpS + 4) * 32;
+  // 4 bits: 20 warps start with 96 registers; the softmax warps go on with 128, the others with 72
+  static constexpr bool kSplitRegs = BITS == 4;
   static constexpr int kKSlots = BITS == 8 ? 4 : 2;       // slots of the K ring (codes, 4 bits: fp16)
   static constexpr int kKSlotBytes = BITS == 8 ? kCodes : kTile;
-  static constexpr int kCSlots = BITS == 8 ? 4 : 3;       // slots of each conversion warp's ring (V codes, 4 bits: codes and scales of K and V)
+  static constexpr int kCSlots = BITS == 8 ? 4 : 3;       // slots of each conversion warp's ring (codes, 4 bits: and scales)
   static constexpr int kHead = kD * BITS / 8;             // bytes of a head's codes
-  static constexpr int kScales = kPart * 16;              // 4 bits: a part's scales, those of two heads a token
-  static constexpr int kOffVc = kPart * (kHead + 16);     // 4 bits: V's codes in a slot
-  static constexpr int kCSlotBytes = BITS == 8 ? kPartCodes : 2 * kOffVc;
+  static constexpr int kCSlotBytes = BITS == 8 ? kPartCodes : kPart * (kHead + 16);  // (the scales of two heads a token)
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kOffK + kKSlots * kKSlotBytes;
   static constexpr int kOffCodes = kOffV + kVSlots * kTile;
   static constexpr int kOffUnit = kOffCodes + kConvWarps * kCSlots * kCSlotBytes;  // [kM] power of two that undoes a row's scaling
   static constexpr int kOffMPub = kOffUnit + kM * 4;      // [4 quarters][2 tile parities][32 rows] published maxima
   static constexpr int kOffBar = kOffMPub + 4 * 2 * 32 * 4;
+  static constexpr int kBarArea = BITS == 8 ? 512 : 640;
   static constexpr int kSmemBytes = kOffBar + kBarArea + 1024;  // + alignment slack
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
   static_assert(kConvWarps * kCSlots * kCSlotBytes >= 6 * kM * 4, "the epilogue's sums and maxima");
   // barriers
-  static constexpr int kBarKFull = 0;                            // [kKSlots] TMA (4 bits: conversion, kConvWarps arrivals) -> MMA
+  static constexpr int kBarKFull = 0;                            // [kKSlots] TMA (4 bits: conversion, kParts arrivals) -> MMA
   static constexpr int kBarKEmpty = kBarKFull + kKSlots;         // [kKSlots] MMA (S of the slot's tiles done) -> TMA (conversion)
   static constexpr int kBarCFull = kBarKEmpty + kKSlots;         // [kConvWarps][kCSlots] TMA -> conversion
-  static constexpr int kBarVFull = kBarCFull + kConvWarps * kCSlots;  // [kVSlots] conversion -> MMA (kConvWarps arrivals)
+  static constexpr int kBarVFull = kBarCFull + kConvWarps * kCSlots;  // [kVSlots] conversion -> MMA (kParts arrivals)
   static constexpr int kBarVEmpty = kBarVFull + kVSlots;         // [kVSlots] MMA (PV of the slot's tiles done) -> conversion
   static constexpr int kBarSFull = kBarVEmpty + kVSlots;         // [kSBufs] S(i) in TMEM -> softmax
   static constexpr int kBarPFull = kBarSFull + kSBufs;           // [kSBufs] P(i) in TMEM -> MMA (128 arrivals)
@@ -264,12 +268,13 @@ struct ConvLane {
   }
 };
 
-// Prefix work item `item` (one CTA) on `smem_raw` (at least Layout<BITS>::kSmemBytes), run by kThreads threads.
+// Prefix work item `item` (one CTA) on `smem_raw` (at least Layout<BITS>::kSmemBytes), run by Layout<BITS>::kThreads threads.
 template <int BITS>
 __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t item, const Maps<BITS>* maps,
                                                   unsigned char* smem_raw) {
   using Lay = Layout<BITS>;
-  constexpr int kKSlots = Lay::kKSlots, kCSlots = Lay::kCSlots;
+  constexpr int kKSlots = Lay::kKSlots, kCSlots = Lay::kCSlots, kConvWarps = Lay::kConvWarps;
+  constexpr int kWarpS = Lay::kWarpS, kWarpPv = Lay::kWarpPv, kWarpTmaK = Lay::kWarpTmaK;
   constexpr int kOffK = Lay::kOffK, kOffV = Lay::kOffV, kOffCodes = Lay::kOffCodes, kOffUnit = Lay::kOffUnit, kOffMPub = Lay::kOffMPub,
                 kOffBar = Lay::kOffBar;
   constexpr int kBarKFull = Lay::kBarKFull, kBarKEmpty = Lay::kBarKEmpty, kBarCFull = Lay::kBarCFull, kBarVFull = Lay::kBarVFull,
@@ -310,20 +315,18 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     mbar_arrive_expect_tx(bar(kBarKFull + st), kCodes);
     tma_load_2d(sK + st * kCodes, &maps->k, j * kD, (int32_t)(first_slot + (int64_t)i * kPair), bar(kBarKFull + st));
   };
-  // conversion warp w's part of V's (4 bits: K's and V's) slot contents i
+  // conversion warp w's part of V's (4 bits, w < kParts: K's) slot contents i
   const int32_t scale_x = (int32_t)kv4_scales_at(p.n_kv, kD) + j / 2 * 16;
   auto issue_c = [&](int w, int i) {
     const int c = w * kCSlots + i % kCSlots;
     const uint32_t dst = sC + c * Lay::kCSlotBytes, full = bar(kBarCFull + c);
-    const int32_t slot = (int32_t)(first_slot + (int64_t)i * kPair + w * kPart);
+    const int32_t slot = (int32_t)(first_slot + (int64_t)i * kPair + w % kParts * kPart);
     mbar_arrive_expect_tx(full, Lay::kCSlotBytes);
     if constexpr (BITS == 8) {
       tma_load_2d(dst, &maps->v, j * kD, slot, full);
     } else {
-      tma_load_2d(dst, &maps->k, j * Lay::kHead, slot, full);
-      tma_load_2d(dst + kPart * Lay::kHead, &maps->ks, scale_x, slot, full);
-      tma_load_2d(dst + Lay::kOffVc, &maps->v, j * Lay::kHead, slot, full);
-      tma_load_2d(dst + Lay::kOffVc + kPart * Lay::kHead, &maps->vs, scale_x, slot, full);
+      tma_load_2d(dst, w < kParts ? &maps->k : &maps->v, j * Lay::kHead, slot, full);
+      tma_load_2d(dst + kPart * Lay::kHead, w < kParts ? &maps->ks : &maps->vs, scale_x, slot, full);
     }
   };
   const int l2_ahead = p.l2_ahead;
@@ -347,8 +350,8 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     }
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1u;
-      if (i >= kBarVFull && i < kBarVFull + kVSlots) count = kConvWarps;
-      if (BITS == 4 && i >= kBarKFull && i < kBarKFull + kKSlots) count = kConvWarps;
+      if (i >= kBarVFull && i < kBarVFull + kVSlots) count = kParts;
+      if (BITS == 4 && i >= kBarKFull && i < kBarKFull + kKSlots) count = kParts;
       if (i >= kBarPFull && i < kBarPFull + kSBufs) count = kSoftmaxThreads / 2;
       if (i >= kBarPair && i < kBarPair + 4) count = 64u;
       if (i >= kBarMPub && i < kBarMPub + 8) count = 32u;
@@ -455,100 +458,81 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
   __syncthreads();
   tc_fence_after();
 
-  if (warp >= kWarpConv && warp < kWarpConv + kConvWarps) {
+  if (warp >= kSoftmaxWarps) {
+  if constexpr (Lay::kSplitRegs) regs_down<72>();
+  if (warp < kWarpConv + kConvWarps) {
     // ---------------- conversion: codes of V (4 bits: of K and V) -> fp16 operand tiles ----------------
     // lane: dims 16 * (lane % 8) .. of tokens lane / 8 + 4 n of the part
     constexpr int kPer = kPart / 4;
     const int w = warp - kWarpConv;
-    const int lt = lane >> 3;
-    const ConvLane cl(w, lane);
+    const int lt = lane >> 3, part = w % kParts;
+    const bool to_k = BITS == 4 && w < kParts;
+    const ConvLane cl(part, lane);
+    const uint32_t ring = to_k ? sK : sV;
+    const int slots = to_k ? kKSlots : kVSlots, full = to_k ? kBarKFull : kBarVFull, empty = to_k ? kBarKEmpty : kBarVEmpty;
     int issued = slab_ok ? min(n_pairs, kCSlots) : 0, seen = 0;
-    auto free_slot = [&](int empty, int slots, int i) {  // the slot for contents i, once its last ones are read
-      const bool ok = i < slots || mbar_wait_bounded(bar(empty + i % slots), ((i / slots) - 1) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
-      return __all_sync(0xffffffffu, ok) != 0;
-    };
     for (int i = 0; slab_ok && i < n_pairs; ++i) {
-      const int c = w * kCSlots + i % kCSlots, st = i % kVSlots;
+      const int c = w * kCSlots + i % kCSlots, st = i % slots;
       bool ok = mbar_wait_bounded(bar(kBarCFull + c), (i / kCSlots) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;  // the abort flag is up: every other role leaves as well
       seen = i + 1;
-      const uint32_t src = sC + c * Lay::kCSlotBytes, dst = sV + st * kTile;
-      const int valid = t1 - t0 - i * kPair - w * kPart;  // tokens of the part in range, or more
-      if constexpr (BITS == 8) {
-        const uint32_t src_off = (uint32_t)lt * kD + (lane & 7) * 16;
-        uint4 x[kPer];
+      const uint32_t src = sC + c * Lay::kCSlotBytes, dst = ring + st * kTile;
+      const int valid = t1 - t0 - i * kPair - part * kPart;  // tokens of the part in range, or more
+      using Codes = std::conditional_t<BITS == 8, uint4, uint2>;
+      Codes x[kPer];
+      uint32_t b[kPer];  // 4 bits: their scales
 #pragma unroll
-        for (int n = 0; n < kPer; ++n) x[n] = lds128(src + src_off + n * 4 * kD);
-        if (valid < kPart) {  // 0 * whatever lies past the piece must not reach O
-#pragma unroll
-          for (int n = 0; n < kPer; ++n)
-            if (lt + 4 * n >= valid) x[n] = make_uint4(0u, 0u, 0u, 0u);
+      for (int n = 0; n < kPer; ++n) {
+        if constexpr (BITS == 8) {
+          x[n] = lds128(src + (uint32_t)(lt + 4 * n) * kD + (lane & 7) * 16);
+        } else {
+          x[n] = lds64(src + (uint32_t)(lt + 4 * n) * Lay::kHead + (lane & 7) * 8);
+          b[n] = lds8(src + kPart * Lay::kHead + (uint32_t)(lt + 4 * n) * 16 + (j & 1) * 8 + (lane & 7));
         }
-        if (!free_slot(kBarVEmpty, kVSlots, i)) break;
+      }
+      if (valid < kPart) {  // 0 * whatever lies past the piece must not reach O
 #pragma unroll
-        for (int n = 0; n < kPer; ++n) {
-          uint32_t y[8];
+        for (int n = 0; n < kPer; ++n)
+          if (lt + 4 * n >= valid) {
+            x[n] = Codes{};
+            b[n] = 0u;
+          }
+      }
+      if (i >= slots) {
+        ok = mbar_wait_bounded(bar(empty + st), ((i / slots) - 1) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+      }
+#pragma unroll
+      for (int n = 0; n < kPer; ++n) {
+        uint32_t y[8];
+        if constexpr (BITS == 8) {
           e4m3x4_to_f16x4(x[n].x, y[0], y[1]);
           e4m3x4_to_f16x4(x[n].y, y[2], y[3]);
           e4m3x4_to_f16x4(x[n].z, y[4], y[5]);
           e4m3x4_to_f16x4(x[n].w, y[6], y[7]);
-          cl.store(dst, n, y);
-        }
-      } else {
-        uint2 x[kPer];
-        uint32_t b[kPer];
-        auto load = [&](uint32_t from) {
+        } else {
+          const uint32_t f = kv4_scale2(b[n]);
+          uint32_t lo[4], hi[4];
+          e2m1x8_to_f16x8(x[n].x, lo);
+          e2m1x8_to_f16x8(x[n].y, hi);
 #pragma unroll
-          for (int n = 0; n < kPer; ++n) {
-            x[n] = lds64(from + (uint32_t)(lt + 4 * n) * Lay::kHead + (lane & 7) * 8);
-            b[n] = lds8(from + kPart * Lay::kHead + (uint32_t)(lt + 4 * n) * 16 + (j & 1) * 8 + (lane & 7));
+          for (int k = 0; k < 4; ++k) {
+            y[k] = f16x2_mul(lo[k], f);
+            y[4 + k] = f16x2_mul(hi[k], f);
           }
-        };
-        auto convert = [&](uint32_t to) {
-#pragma unroll
-          for (int n = 0; n < kPer; ++n) {
-            const uint32_t f = kv4_scale2(b[n]);
-            uint32_t lo[4], hi[4], y[8];
-            e2m1x8_to_f16x8(x[n].x, lo);
-            e2m1x8_to_f16x8(x[n].y, hi);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              y[k] = f16x2_mul(lo[k], f);
-              y[4 + k] = f16x2_mul(hi[k], f);
-            }
-            cl.store(to, n, y);
-          }
-        };
-        load(src);
-        if (!free_slot(kBarKEmpty, kKSlots, i)) break;
-        convert(sK + i % kKSlots * kTile);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarKFull + i % kKSlots));
-        load(src + Lay::kOffVc);
-        if (valid < kPart) {  // 0 * whatever lies past the piece must not reach O
-#pragma unroll
-          for (int n = 0; n < kPer; ++n)
-            if (lt + 4 * n >= valid) {
-              x[n] = make_uint2(0u, 0u);
-              b[n] = 0u;
-            }
         }
-        if (!free_slot(kBarVEmpty, kVSlots, i)) break;
-        convert(dst);
+        cl.store(dst, n, y);
       }
       fence_proxy_async_smem();
       __syncwarp();  // the warp has stored its part, and read its codes
       if (lane == 0) {
-        mbar_arrive(bar(kBarVFull + st));
+        mbar_arrive(bar(full + st));
         if (i + kCSlots < n_pairs) {
           issue_c(w, i + kCSlots);
-          if (l2_ahead > 0 && i + kCSlots + l2_ahead < n_pairs) {
-            const int32_t slot = (int32_t)(first_slot + (int64_t)(i + kCSlots + l2_ahead) * kPair + w * kPart);
-            tma_prefetch_l2_2d(&maps->v, j * Lay::kHead, slot);
-            if constexpr (BITS == 4) tma_prefetch_l2_2d(&maps->k, j * Lay::kHead, slot);
-          }
+          if (l2_ahead > 0 && i + kCSlots + l2_ahead < n_pairs)
+            tma_prefetch_l2_2d(to_k ? &maps->k : &maps->v, j * Lay::kHead, (int32_t)(first_slot + (int64_t)(i + kCSlots + l2_ahead) * kPair + part * kPart));
           issued = i + kCSlots + 1;
         }
       }
@@ -665,7 +649,13 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
         }
       }
     }
-  } else if (warp < kSoftmaxWarps) {
+  }
+  if constexpr (Lay::kSplitRegs) {
+    __syncwarp();
+    regs_up<96>();
+  }
+  } else {
+    if constexpr (Lay::kSplitRegs) regs_up<128>();
     // ---------------- softmax warps 0-7: rows of quarter `quad`, tiles of parity `par` ----------------
     const int quad = warp & 3;
     const int par = warp >> 2;
@@ -875,6 +865,10 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
           st_record(p.rec_lse + (int64_t)rec * p.n_q + h, kv8_record_lse(lt, (top + log2f(lt)) * kLn2), keep);
         }
       }
+    }
+    if constexpr (Lay::kSplitRegs) {
+      __syncwarp();
+      regs_down<96>();
     }
   }
 

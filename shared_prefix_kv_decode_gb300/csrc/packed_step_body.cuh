@@ -12,13 +12,13 @@ namespace {
 template <int BITS>
 constexpr int kStepSmem = pkd::Layout<BITS>::kSmemBytes > pks::Layout<BITS>::kSmemBytes ? pkd::Layout<BITS>::kSmemBytes
                                                                                        : pks::Layout<BITS>::kSmemBytes;
-static_assert(pks::kThreads <= pkd::kThreads, "the suffix body runs on the dense block size");
+static_assert(pks::kThreads <= pkd::Layout<8>::kThreads && pks::kThreads <= pkd::Layout<4>::kThreads, "the suffix body runs on the dense block size");
 
 // CTAs [0, n_dense) run dense prefix items first_dense.., CTA n_dense + k suffix token-CTA k % n_scta of
 // KV-head group k / n_scta.  Dense CTA c < n_tail then runs suffix token-CTA n_scta + c (one
 // KV-head group only): suffix work the plan gives the dense CTAs for after their prefix piece.
 template <int BITS>
-__global__ void __launch_bounds__(pkd::kThreads, 1)
+__global__ void __launch_bounds__(pkd::Layout<BITS>::kThreads, 1)
     packed_step_kernel(AttnParams p, int32_t first_dense, int32_t n_dense, const __grid_constant__ pkd::Maps<BITS> maps,
                        const int32_t* __restrict__ cta_begin, int32_t n_scta, int32_t n_tail) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
@@ -30,18 +30,18 @@ __global__ void __launch_bounds__(pkd::kThreads, 1)
       // completed and its tensor memory is freed, so its shared memory is free
       __syncthreads();
       fence_proxy_async_smem();
-      pks::packed_suffix_body<BITS>(p, cta_begin, n_scta + c, 0, smem_raw);
+      pks::packed_suffix_body<BITS, pkd::Layout<BITS>::kSplitRegs>(p, cta_begin, n_scta + c, 0, smem_raw);
     }
   } else {
     const int32_t k = c - n_dense;
-    pks::packed_suffix_body<BITS>(p, cta_begin, k % n_scta, k / n_scta, smem_raw);
+    pks::packed_suffix_body<BITS, pkd::Layout<BITS>::kSplitRegs>(p, cta_begin, k % n_scta, k / n_scta, smem_raw);
   }
 }
 
 template <int BITS>
 __global__ void __launch_bounds__(pks::kThreads, 1) packed_suffix_kernel(AttnParams p, const int32_t* __restrict__ cta_begin) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  pks::packed_suffix_body<BITS>(p, cta_begin, blockIdx.x, blockIdx.y, smem_raw);
+  pks::packed_suffix_body<BITS, false>(p, cta_begin, blockIdx.x, blockIdx.y, smem_raw);
 }
 
 template <int BITS>
@@ -54,7 +54,7 @@ cudaError_t launch_packed_step(const AttnParams& p, int32_t first_dense, int32_t
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem_once(packed_step_kernel<BITS>, kStepSmem<BITS>, allowed);
   if (e != cudaSuccess) return e;
-  return launch_kernel(packed_step_kernel<BITS>, dim3((unsigned)n), dim3(pkd::kThreads), kStepSmem<BITS>, s, pdl, p, first_dense,
+  return launch_kernel(packed_step_kernel<BITS>, dim3((unsigned)n), dim3(pkd::Layout<BITS>::kThreads), kStepSmem<BITS>, s, pdl, p, first_dense,
                        n_dense, maps, cta_begin, n_scta, n_tail);
 }
 

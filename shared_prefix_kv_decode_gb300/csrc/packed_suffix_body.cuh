@@ -104,6 +104,16 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Registers a thread of this warpgroup (four warps, all of them here) goes on with.
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Two tokens' four codes (lane word of a transposed ldmatrix: token 2 c in the low half) -> for each of the four dims
 // the two tokens' values as fp16x2, times the tokens' scales.
 __device__ __forceinline__ void kv4_transposed(uint32_t w, uint32_t scale2, uint32_t (&y)[4]) {
@@ -120,8 +130,9 @@ __device__ __forceinline__ void scale_pairs(uint32_t a, uint32_t b, uint32_t sel
 
 // One token-CTA `cta` of the suffix work list, for KV-head group `group`, on `smem` (at least
 // Layout<BITS>::kSmemBytes, 128-byte aligned), run by kThreads or more threads (the extra warps only take
-// part in the set-up barriers).
-template <int BITS>
+// part in the set-up barriers).  kSplitRegs: the block has 20 warps of 96 registers (as the dense body's), of which the
+// consumers go on with 128 and the others with 72.
+template <int BITS, bool kSplitRegs>
 __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const int32_t* __restrict__ cta_begin, int cta,
                                                 int group, unsigned char* smem) {
   using Lay = Layout<BITS>;
@@ -189,6 +200,7 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
 
   if (warp >= kWarps) {
     // ---------------- producers: one packed row per lane (lanes 0-1 K, 2-3 V) -------------
+    if constexpr (kSplitRegs) regs_down<72>();
     const int part = warp - kWarps;
     if (part >= kProducers) return;
     const bool is_v = (lane & (2 * kRowsEach - 1)) >= kRowsEach;
@@ -251,6 +263,7 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
     }
     return;
   }
+  if constexpr (kSplitRegs) regs_up<128>();
   if (warp >= nh) return;  // no CTA-wide barrier is used below
 
   // ---------------- consumers: warp `warp` owns KV head j ----------------
