@@ -609,16 +609,11 @@ granikv_status create_impl(const granikv_config* cfg, int32_t bits, granikv_ctx*
         if (bits) {
           PackedMaps& m = c->packed_maps[l];
           const int64_t codes = bits == 8 ? (int64_t)cfg->n_kv * 128 : kv4_scales_at(cfg->n_kv, 128);
-          auto encode = [&](CUtensorMap* to, void* pool, int64_t used, int32_t bytes, int32_t slots, bool swizzle) {
-            return encode_packed_map(to, pool, cfg->n_slots, c->packed_row, used, bytes, slots, swizzle);
+          auto encode = [&](CUtensorMap* to, void* pool, int32_t bytes, int32_t slots, bool swizzle) {
+            return encode_packed_map(to, pool, cfg->n_slots, c->packed_row, codes, bytes, slots, swizzle);
           };
-          if (bits == 8) {
-            ok = encode(&m.k, c->kpool[l], codes, 128, kDenseTile, true) && encode(&m.v, c->vpool[l], codes, 128, kKv8VBox, false);
-          } else {
-            const int64_t scales = kv4_units_at(cfg->n_kv, 128);  // (padded to whole boxes)
-            ok = encode(&m.k, c->kpool[l], codes, 64, kKv8VBox, false) && encode(&m.v, c->vpool[l], codes, 64, kKv8VBox, false) &&
-                 encode(&m.ks, c->kpool[l], scales, 16, kKv8VBox, false) && encode(&m.vs, c->vpool[l], scales, 16, kKv8VBox, false);
-          }
+          ok = bits == 8 ? encode(&m.k, c->kpool[l], 128, kDenseTile, true) && encode(&m.v, c->vpool[l], 128, kKv8VBox, false)
+                         : encode(&m.k, c->kpool[l], 64, kKv8VBox, false) && encode(&m.v, c->vpool[l], 64, kKv8VBox, false);
           continue;
         }
         ok = ((uintptr_t)c->kpool[l] % 16 == 0) && ((uintptr_t)c->vpool[l] % 16 == 0) &&

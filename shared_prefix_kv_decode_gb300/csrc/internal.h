@@ -246,7 +246,7 @@ cudaError_t launch_kv8_generic(int32_t dtype, const AttnParams& p, int32_t first
 // Tensor-core path of the 8- and 4-bit cache (kernels_kv8_tc.cu, kernels_kv4_tc.cu): dense prefix items and suffix
 // token-CTAs in one grid (either count may be 0; n_tail as for launch_prefix_suffix_tc), and the suffix alone.
 struct PackedMaps {
-  CUtensorMap k, v, ks, vs;  // codes of K and V, their scales (4 bits)
+  CUtensorMap k, v;  // the pools' codes
 };
 cudaError_t launch_kv8_step(const AttnParams& p, int32_t first_dense, int32_t n_dense, const PackedMaps& m,
                             const int32_t* cta_begin, int32_t n_scta, int32_t n_tail, cudaStream_t s, bool pdl);

@@ -51,8 +51,10 @@
 // tokens and head, that is, of a tile.  code * b is exact in fp16, so the conversion warps make fp16 operand tiles of
 // K as of V (an fp16x2 conversion and a product for each pair), S is an fp16 product with q in fp16 (scaled by a power of two
 // to [2^14, 2^15): exact down to 2^-31 of the row's largest element), and u takes the place of ks and vs.  A
-// conversion warp's ring holds its 32 tokens' codes and scales of K and V, by four TMA boxes (64 and 16 bytes a
-// token) on one barrier; the K ring has two slots of fp16, filled by four arrivals like V's.
+// conversion warp's ring holds its 32 tokens' codes, by a TMA box, and scales, 8 bytes a token by cp.async from the warp
+// itself: TMA takes about four clocks for a row of a box, however short, so with the scales in boxes of their own
+// the loads alone took longer (a tile's 2,200 clocks) than everything else.  The K ring has two slots of fp16,
+// filled by four arrivals like V's.
 #pragma once
 
 #include <cuda.h>
@@ -75,6 +77,7 @@ namespace {
 
 using pks::lg2_approx;
 using pks::pack_f16;
+using pks::block_barrier;
 using pks::regs_down;
 using pks::regs_up;
 
@@ -105,7 +108,7 @@ struct Layout {
   static constexpr int kKSlotBytes = BITS == 8 ? kCodes : kTile;
   static constexpr int kCSlots = BITS == 8 ? 4 : 3;       // slots of each conversion warp's ring (codes, 4 bits: and scales)
   static constexpr int kHead = kD * BITS / 8;             // bytes of a head's codes
-  static constexpr int kCSlotBytes = BITS == 8 ? kPartCodes : kPart * (kHead + 16);  // (the scales of two heads a token)
+  static constexpr int kCSlotBytes = BITS == 8 ? kPartCodes : kPart * (kHead + kD / kKv4Group);
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kOffK + kKSlots * kKSlotBytes;
   static constexpr int kOffCodes = kOffV + kVSlots * kTile;
@@ -132,17 +135,9 @@ struct Layout {
   static_assert(8 * kNumBars + 16 <= kBarArea, "barrier area");
 };
 // The layer's pools as byte matrices [n_slots, row bytes].  8 bits: K in boxes of 128 slots x 128 bytes with the
-// 128-byte swizzle, V in boxes of 32 slots x 128 bytes, row after row.  4 bits: codes in boxes of 32 slots x 64 bytes,
-// scales in boxes of 32 slots x 16 bytes.
-template <int BITS>
-struct Maps;
-template <>
-struct Maps<8> {
+// 128-byte swizzle, V in boxes of 32 slots x 128 bytes, row after row.  4 bits: both in boxes of 32 slots x 64 bytes.
+struct Maps {
   CUtensorMap k, v;
-};
-template <>
-struct Maps<4> {
-  CUtensorMap k, v, ks, vs;
 };
 constexpr uint32_t kTmemCols = 512;           // S/P buffers at 0, 64, 128, 192, 256; Q (hi, lo) at 320; O at 384
 constexpr uint32_t kColQ = kSBufs * kN, kColO = 384;
@@ -224,53 +219,46 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(a));
   return x;
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 x;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(a));
-  return x;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-  uint32_t x;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(a));
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t x;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(a));
   return x;
 }
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-// A conversion lane's address in an fp16 operand tile (128 tokens x 64 dims, 128-byte rows, 128-byte swizzle): 16 dims
-// are two 16-byte chunks of a token's row in 64-dim half lane % 8 / 4.  The lane's tokens are lane / 8 + 4 n.
+// A conversion lane's place in an fp16 operand tile (128 tokens x 64 dims a half, 128-byte rows, 128-byte swizzle).  The
+// lanes take 16 bytes of codes each: 16 dims of four tokens, or (4 bits) 32 dims of eight.  A store instruction's
+// eight lanes at a time have to cover eight 16-byte chunks that differ in their place within 128 bytes, which the swizzle
+// XORs with the token's last bits; the lanes of the upper 64 dims, whose chunks have the same places as the lower
+// ones', take the token whose bits differ by one step: 1, or 2 (where the bit 1 already tells two tokens apart).
+// (With the stores of one half in another order, by a branch, a 4-bit tile took 8 % longer.)
+template <int BITS>
 struct ConvLane {
-  bool upper;
-  uint32_t lo[2], hi[2];  // chunk offsets of even and odd n: tokens lt and lt + 4 modulo 8 have two swizzles
-  __device__ __forceinline__ ConvLane(int w, int lane) {
-    const int lt = lane >> 3;
-    const uint32_t ch = (lane & 3) * 2;
-    upper = (lane & 7) >= 4;
-    const uint32_t row_off = (uint32_t)w * kPart * 128 + (upper ? kHalf : 0) + (uint32_t)lt * 128;
-#pragma unroll
-    for (int odd = 0; odd < 2; ++odd) {
-      lo[odd] = row_off + ((ch ^ (lt + 4 * odd)) << 4);
-      hi[odd] = row_off + (((ch + 1) ^ (lt + 4 * odd)) << 4);
-    }
+  static constexpr int kDims = 128 / BITS;             // 16 or 32
+  static constexpr int kLanes = kD / kDims;            // of a token: 8 or 4
+  static constexpr int kStep = 32 / kLanes;            // tokens of a load: 4 or 8
+  static constexpr int kPer = kPart / kStep;           // loads of a part
+  int dim, token;                                      // first dim; token of load 0
+  uint32_t row, ch;                                    // of the operand tile: the row's offset, first chunk
+  __device__ __forceinline__ ConvLane(int part, int lane) {
+    const int c = lane % kLanes;
+    dim = c * kDims;
+    token = (lane / kLanes) ^ (2 * c >= kLanes ? kStep / 4 : 0);
+    row = (uint32_t)(part * kPart + token) * 128 + (2 * c >= kLanes ? kHalf : 0);
+    ch = (uint32_t)(dim % 64 / 8);
   }
-  // Token lt + 4 n's 16 dims.  Lanes of the upper half store theirs in the other order, so a store instruction
-  // covers all banks.
-  __device__ __forceinline__ void store(uint32_t dst, int n, const uint32_t (&y)[8]) const {
-    const uint32_t a = dst + n * 4 * 128 + lo[n & 1], b = dst + n * 4 * 128 + hi[n & 1];
-    if (upper) {
-      sts128(b, y[4], y[5], y[6], y[7]);
-      sts128(a, y[0], y[1], y[2], y[3]);
-    } else {
-      sts128(a, y[0], y[1], y[2], y[3]);
-      sts128(b, y[4], y[5], y[6], y[7]);
-    }
+  // chunk k (8 dims) of load n
+  __device__ __forceinline__ void store(uint32_t tile, int n, int k, uint32_t x, uint32_t y, uint32_t z, uint32_t w) const {
+    const uint32_t swizzle = (uint32_t)(token + n * kStep) & 7u;
+    sts128(tile + row + n * kStep * 128 + (((ch + k) ^ swizzle) << 4), x, y, z, w);
   }
 };
 
 // Prefix work item `item` (one CTA) on `smem_raw` (at least Layout<BITS>::kSmemBytes), run by Layout<BITS>::kThreads threads.
 template <int BITS>
-__device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t item, const Maps<BITS>* maps,
+__device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t item, const Maps* maps,
                                                   unsigned char* smem_raw) {
   using Lay = Layout<BITS>;
   constexpr int kKSlots = Lay::kKSlots, kCSlots = Lay::kCSlots, kConvWarps = Lay::kConvWarps;
@@ -316,18 +304,12 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     tma_load_2d(sK + st * kCodes, &maps->k, j * kD, (int32_t)(first_slot + (int64_t)i * kPair), bar(kBarKFull + st));
   };
   // conversion warp w's part of V's (4 bits, w < kParts: K's) slot contents i
-  const int32_t scale_x = (int32_t)kv4_scales_at(p.n_kv, kD) + j / 2 * 16;
   auto issue_c = [&](int w, int i) {
     const int c = w * kCSlots + i % kCSlots;
     const uint32_t dst = sC + c * Lay::kCSlotBytes, full = bar(kBarCFull + c);
     const int32_t slot = (int32_t)(first_slot + (int64_t)i * kPair + w % kParts * kPart);
-    mbar_arrive_expect_tx(full, Lay::kCSlotBytes);
-    if constexpr (BITS == 8) {
-      tma_load_2d(dst, &maps->v, j * kD, slot, full);
-    } else {
-      tma_load_2d(dst, w < kParts ? &maps->k : &maps->v, j * Lay::kHead, slot, full);
-      tma_load_2d(dst + kPart * Lay::kHead, w < kParts ? &maps->ks : &maps->vs, scale_x, slot, full);
-    }
+    mbar_arrive_expect_tx(full, kPart * Lay::kHead);
+    tma_load_2d(dst, BITS == 4 && w < kParts ? &maps->k : &maps->v, j * Lay::kHead, slot, full);
   };
   const int l2_ahead = p.l2_ahead;
   // softmax warps: this lane's row (the same for the two warps of a row quarter), its request, head and
@@ -344,10 +326,6 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
   if (warp == kWarpTmaK && lane == 0) {
     tma_prefetch_desc(&maps->k);
     tma_prefetch_desc(&maps->v);
-    if constexpr (BITS == 4) {
-      tma_prefetch_desc(&maps->ks);
-      tma_prefetch_desc(&maps->vs);
-    }
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1u;
       if (i >= kBarVFull && i < kBarVFull + kVSlots) count = kParts;
@@ -462,40 +440,53 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
   if constexpr (Lay::kSplitRegs) regs_down<72>();
   if (warp < kWarpConv + kConvWarps) {
     // ---------------- conversion: codes of V (4 bits: of K and V) -> fp16 operand tiles ----------------
-    // lane: dims 16 * (lane % 8) .. of tokens lane / 8 + 4 n of the part
-    constexpr int kPer = kPart / 4;
     const int w = warp - kWarpConv;
-    const int lt = lane >> 3, part = w % kParts;
+    const int part = w % kParts;
     const bool to_k = BITS == 4 && w < kParts;
-    const ConvLane cl(part, lane);
+    using Conv = ConvLane<BITS>;
+    constexpr int kPer = Conv::kPer;
+    const Conv cl(part, lane);
     const uint32_t ring = to_k ? sK : sV;
     const int slots = to_k ? kKSlots : kVSlots, full = to_k ? kBarKFull : kBarVFull, empty = to_k ? kBarKEmpty : kBarVEmpty;
     int issued = slab_ok ? min(n_pairs, kCSlots) : 0, seen = 0;
+    // 4 bits: the scales of contents i, a token a lane (zeros past the piece's end); a group for every i
+    const uint8_t* scale_src = static_cast<const uint8_t*>(to_k ? p.kpool : p.vpool) + (first_slot + part * kPart + lane) * p.packed_row +
+                               kv4_scales_at(p.n_kv, kD) + j * (kD / kKv4Group);
+    auto copy_scales = [&](int i) {
+      if constexpr (BITS == 4) {
+        const uint32_t dst = sC + (w * kCSlots + i % kCSlots) * Lay::kCSlotBytes + kPart * Lay::kHead + lane * 8;
+        const bool in = t0 + i * kPair + part * kPart + lane < t1;
+        if (slab_ok && i < n_pairs) cp_async8(dst, in ? scale_src + (int64_t)i * kPair * p.packed_row : scale_src, in ? 8 : 0);
+        cp_async_commit();
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < kCSlots; ++i) copy_scales(i);
     for (int i = 0; slab_ok && i < n_pairs; ++i) {
       const int c = w * kCSlots + i % kCSlots, st = i % slots;
       bool ok = mbar_wait_bounded(bar(kBarCFull + c), (i / kCSlots) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;  // the abort flag is up: every other role leaves as well
       seen = i + 1;
+      if constexpr (BITS == 4) {
+        cp_async_wait<kCSlots - 1>();
+        __syncwarp();
+      }
       const uint32_t src = sC + c * Lay::kCSlotBytes, dst = ring + st * kTile;
       const int valid = t1 - t0 - i * kPair - part * kPart;  // tokens of the part in range, or more
-      using Codes = std::conditional_t<BITS == 8, uint4, uint2>;
-      Codes x[kPer];
-      uint32_t b[kPer];  // 4 bits: their scales
+      uint4 x[kPer];
+      uint32_t b[kPer];  // 4 bits: their two scales
 #pragma unroll
       for (int n = 0; n < kPer; ++n) {
-        if constexpr (BITS == 8) {
-          x[n] = lds128(src + (uint32_t)(lt + 4 * n) * kD + (lane & 7) * 16);
-        } else {
-          x[n] = lds64(src + (uint32_t)(lt + 4 * n) * Lay::kHead + (lane & 7) * 8);
-          b[n] = lds8(src + kPart * Lay::kHead + (uint32_t)(lt + 4 * n) * 16 + (j & 1) * 8 + (lane & 7));
-        }
+        const uint32_t t = (uint32_t)(cl.token + n * Conv::kStep);
+        x[n] = lds128(src + t * Lay::kHead + cl.dim * BITS / 8);
+        if constexpr (BITS == 4) b[n] = lds16(src + kPart * Lay::kHead + t * 8 + cl.dim / 16);
       }
       if (valid < kPart) {  // 0 * whatever lies past the piece must not reach O
 #pragma unroll
         for (int n = 0; n < kPer; ++n)
-          if (lt + 4 * n >= valid) {
-            x[n] = Codes{};
+          if (cl.token + n * Conv::kStep >= valid) {
+            x[n] = make_uint4(0u, 0u, 0u, 0u);
             b[n] = 0u;
           }
       }
@@ -506,27 +497,28 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
       }
 #pragma unroll
       for (int n = 0; n < kPer; ++n) {
-        uint32_t y[8];
         if constexpr (BITS == 8) {
+          uint32_t y[8];
           e4m3x4_to_f16x4(x[n].x, y[0], y[1]);
           e4m3x4_to_f16x4(x[n].y, y[2], y[3]);
           e4m3x4_to_f16x4(x[n].z, y[4], y[5]);
           e4m3x4_to_f16x4(x[n].w, y[6], y[7]);
+          cl.store(dst, n, 0, y[0], y[1], y[2], y[3]);
+          cl.store(dst, n, 1, y[4], y[5], y[6], y[7]);
         } else {
-          const uint32_t f = kv4_scale2(b[n]);
-          uint32_t lo[4], hi[4];
-          e2m1x8_to_f16x8(x[n].x, lo);
-          e2m1x8_to_f16x8(x[n].y, hi);
+          const uint32_t f = e4m3x2_to_f16x2((uint16_t)b[n]), f2[2] = {__byte_perm(f, f, 0x1010), __byte_perm(f, f, 0x3232)};
+          const uint32_t u[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            y[k] = f16x2_mul(lo[k], f);
-            y[4 + k] = f16x2_mul(hi[k], f);
+            uint32_t y[4];
+            e2m1x8_to_f16x8(u[k], y);
+            cl.store(dst, n, k, f16x2_mul(y[0], f2[k / 2]), f16x2_mul(y[1], f2[k / 2]), f16x2_mul(y[2], f2[k / 2]), f16x2_mul(y[3], f2[k / 2]));
           }
         }
-        cl.store(dst, n, y);
       }
       fence_proxy_async_smem();
       __syncwarp();  // the warp has stored its part, and read its codes
+      copy_scales(i + kCSlots);
       if (lane == 0) {
         mbar_arrive(bar(full + st));
         if (i + kCSlots < n_pairs) {
@@ -538,6 +530,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
       }
     }
     // never leave with a copy in flight
+    if constexpr (BITS == 4) cp_async_wait<0>();
     if (lane == 0) {
       for (int i = seen; i < issued; ++i) {
         const uint64_t t_start = globaltimer_ns();
@@ -651,7 +644,10 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     }
   }
   if constexpr (Lay::kSplitRegs) {
+    // (between the two barriers the softmax warps give back what they took)
     __syncwarp();
+    block_barrier<Lay::kThreads>();
+    block_barrier<Lay::kThreads>();
     regs_up<96>();
   }
   } else {
@@ -868,7 +864,9 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     }
     if constexpr (Lay::kSplitRegs) {
       __syncwarp();
+      block_barrier<Lay::kThreads>();
       regs_down<96>();
+      block_barrier<Lay::kThreads>();
     }
   }
 

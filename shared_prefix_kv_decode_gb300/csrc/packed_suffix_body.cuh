@@ -104,7 +104,10 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Registers a thread of this warpgroup (four warps, all of them here) goes on with.
+// Registers a thread of this warpgroup (four warps, all of them here) goes on with.  regs_up waits for registers that
+// other warps of the block gave up, so no warp may take some back while another still waits for its share: a warpgroup's
+// first change comes right after a barrier of the block, and the next one after another such barrier.  (Idle warps that
+// took theirs back at once left the last softmax warp of their quarter of the SM 16 registers short, for good.)
 template <int N>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -112,6 +115,11 @@ __device__ __forceinline__ void regs_up() {
 template <int N>
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int THREADS>
+__device__ __forceinline__ void block_barrier() {  // of the whole block, from either side of a branch
+  asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
 // Two tokens' four codes (lane word of a transposed ldmatrix: token 2 c in the low half) -> for each of the four dims
