@@ -12,9 +12,7 @@ namespace {
 template <int BITS>
 constexpr int kStepSmem = pkd::Layout<BITS>::kSmemBytes > pks::Layout<BITS>::kSmemBytes ? pkd::Layout<BITS>::kSmemBytes
                                                                                        : pks::Layout<BITS>::kSmemBytes;
-static_assert(pks::Layout<8>::kThreads <= pkd::Layout<8>::kThreads, "the suffix body runs on the dense block size");
-// (and its change of registers is one of the whole block's)
-static_assert(pks::Layout<4>::kThreads == pkd::Layout<4>::kThreads, "the suffix body runs on the dense block size");
+static_assert(pks::kThreads <= pkd::Layout<8>::kThreads && pks::kThreads <= pkd::Layout<4>::kThreads, "the suffix body runs on the dense block size");
 
 // CTAs [0, n_dense) run dense prefix items first_dense.., CTA n_dense + k suffix token-CTA k % n_scta of
 // KV-head group k / n_scta.  Dense CTA c < n_tail then runs suffix token-CTA n_scta + c (one
@@ -32,18 +30,18 @@ __global__ void __launch_bounds__(pkd::Layout<BITS>::kThreads, 1)
       // completed and its tensor memory is freed, so its shared memory is free
       __syncthreads();
       fence_proxy_async_smem();
-      pks::packed_suffix_body<BITS>(p, cta_begin, n_scta + c, 0, smem_raw);
+      pks::packed_suffix_body<BITS, pkd::Layout<BITS>::kSplitRegs>(p, cta_begin, n_scta + c, 0, smem_raw);
     }
   } else {
     const int32_t k = c - n_dense;
-    pks::packed_suffix_body<BITS>(p, cta_begin, k % n_scta, k / n_scta, smem_raw);
+    pks::packed_suffix_body<BITS, pkd::Layout<BITS>::kSplitRegs>(p, cta_begin, k % n_scta, k / n_scta, smem_raw);
   }
 }
 
 template <int BITS>
-__global__ void __launch_bounds__(pks::Layout<BITS>::kThreads, 1) packed_suffix_kernel(AttnParams p, const int32_t* __restrict__ cta_begin) {
+__global__ void __launch_bounds__(pks::kThreads, 1) packed_suffix_kernel(AttnParams p, const int32_t* __restrict__ cta_begin) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  pks::packed_suffix_body<BITS>(p, cta_begin, blockIdx.x, blockIdx.y, smem_raw);
+  pks::packed_suffix_body<BITS, false>(p, cta_begin, blockIdx.x, blockIdx.y, smem_raw);
 }
 
 template <int BITS>
@@ -68,7 +66,7 @@ cudaError_t launch_packed_suffix(const AttnParams& p, const int32_t* cta_begin, 
   cudaError_t e = allow_smem_once(packed_suffix_kernel<BITS>, smem, allowed);
   if (e != cudaSuccess) return e;
   const dim3 grid(n_scta, (p.n_kv + pks::kWarps - 1) / pks::kWarps);
-  return launch_kernel(packed_suffix_kernel<BITS>, grid, dim3(pks::Layout<BITS>::kThreads), smem, s, pdl, p, cta_begin);
+  return launch_kernel(packed_suffix_kernel<BITS>, grid, dim3(pks::kThreads), smem, s, pdl, p, cta_begin);
 }
 
 }  // namespace

@@ -54,34 +54,25 @@ namespace {
 
 constexpr int kD = 128;
 constexpr int kTile = 16;                          // tokens per tile (MMA M)
-constexpr int kWarps = 8;                          // KV heads per CTA
+constexpr int kWarps = 8;                          // consumer warps: KV heads per CTA
+constexpr int kProducers = 8;                      // producer warps: two of a tile's rows each
+constexpr int kRowsEach = kTile / kProducers;
+constexpr int kThreads = (kWarps + kProducers) * 32;
 constexpr int kSegSmem = 256;                      // segment descriptors staged in shared memory
 // Packed rows of eight heads in shared memory, 16 modulo 32 bytes apart: the eight rows that an ldmatrix reads lie in
 // eight different 16-byte bank groups.  8 bits: 1,056 bytes, 4 bits: 592.  The stages fill what shared memory there is.
 template <int BITS>
 struct Layout {
-  // 8 bits: a consumer warp a head, two tiles at a time, and eight producers of two of a tile's rows each.  4 bits: two
-  // consumer warps a head, which take the tiles in turn, and four producers; 20 warps start with 96 registers, of
-  // which the consumers go on with 104 and the producers with 64.
-  static constexpr int kHalves = BITS == 8 ? 1 : 2;
-  static constexpr int kConsumers = kWarps * kHalves;
-  static constexpr int kProducers = BITS == 8 ? 8 : 4;
-  static constexpr int kRowsEach = kTile / kProducers;
-  static constexpr int kThreads = (kConsumers + kProducers) * 32;
-  static constexpr bool kSplitRegs = BITS == 4;
   static constexpr int kCodes = kD * BITS / 8;     // bytes of a head's codes
   static constexpr int kRowMax = BITS == 8 ? kWarps * (kD + 4) : (int)kv4_row_bytes(kWarps, kD);
   static constexpr int kRowStride = kRowMax + (kRowMax % 32 ? 0 : 16);
-  static constexpr int kStages = BITS == 8 ? 6 : 9;
+  static constexpr int kStages = BITS == 8 ? 6 : 11;
   static constexpr int kTileBytes = kTile * kRowStride;
   static constexpr int kStageBytes = 2 * kTileBytes;  // K + V: 34,304 B (8 bits)
-  static constexpr int kState = kHalves == 1 ? 0 : 9 * 512;  // what one warp of a head tells the other: O, m and l of its lanes
-  static constexpr int kOffState = kStages * kStageBytes;
-  static constexpr int kOffSlots = kOffState + kWarps * kState;
+  static constexpr int kOffSlots = kStages * kStageBytes;
   static constexpr int kOffSegs = kOffSlots + kSuffixMaxCtaTokens * 4;
   static constexpr int kOffBar = kOffSegs + kSegSmem * (int)sizeof(DevSuffixItem);
-  static constexpr int kBars = 2 * kStages + (kHalves == 1 ? 0 : 2 * kWarps);
-  static constexpr int kSmemBytes = kOffBar + 8 * kBars + 16;
+  static constexpr int kSmemBytes = kOffBar + 8 * 2 * kStages + 16;
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
   static_assert(kRowStride % 32 == 16, "ldmatrix bank groups");
 };
@@ -147,15 +138,14 @@ __device__ __forceinline__ void scale_pairs(uint32_t a, uint32_t b, uint32_t sel
 
 // One token-CTA `cta` of the suffix work list, for KV-head group `group`, on `smem` (at least
 // Layout<BITS>::kSmemBytes, 128-byte aligned), run by kThreads or more threads (the extra warps only take
-// part in the set-up barriers).
-template <int BITS>
+// part in the set-up barriers).  kSplitRegs: the block has 20 warps of 96 registers (as the dense body's), of which the
+// consumers go on with 128 and the others with 72.
+template <int BITS, bool kSplitRegs>
 __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const int32_t* __restrict__ cta_begin, int cta,
                                                 int group, unsigned char* smem) {
   using Lay = Layout<BITS>;
   constexpr int kStages = Lay::kStages, kTileBytes = Lay::kTileBytes, kStageBytes = Lay::kStageBytes, kRowStride = Lay::kRowStride;
-  constexpr int kOffSlots = Lay::kOffSlots, kOffSegs = Lay::kOffSegs, kOffBar = Lay::kOffBar, kHalves = Lay::kHalves;
-  constexpr int kConsumers = Lay::kConsumers, kProducers = Lay::kProducers, kRowsEach = Lay::kRowsEach;
-  constexpr bool kSplitRegs = Lay::kSplitRegs;
+  constexpr int kOffSlots = Lay::kOffSlots, kOffSegs = Lay::kOffSegs, kOffBar = Lay::kOffBar;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int seg_begin = cta_begin[cta];
@@ -171,10 +161,7 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
   const uint32_t sbase = smem_u32(smem);
   auto full_bar = [&](int st) { return sbase + kOffBar + 8 * st; };
   auto empty_bar = [&](int st) { return sbase + kOffBar + 8 * (kStages + st); };
-  // a head's state has been told (by all lanes of one of its warps), has been read (by all of the other's)
-  auto told_bar = [&](int head) { return sbase + kOffBar + 8 * (2 * kStages + head); };
-  auto read_bar = [&](int head) { return sbase + kOffBar + 8 * (2 * kStages + kWarps + head); };
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffBar + 8 * Lay::kBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffBar + 16 * kStages);
 
   // The slot ids of all of this CTA's tokens (its segments back to back) and its segment
   // descriptors go to shared memory once.  The plan keeps a CTA's tokens within
@@ -183,7 +170,7 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
   DevSuffixItem* sseg = reinterpret_cast<DevSuffixItem*>(smem + kOffSegs);
   const int n_seg = seg_end - seg_begin;
   // this thread's descriptor (the plan is not written by the work before this kernel)
-  static_assert(kSegSmem <= Lay::kThreads, "a descriptor a thread");
+  static_assert(kSegSmem <= kThreads, "a descriptor a thread");
   DevSuffixItem mine{};
   if (threadIdx.x < min(n_seg, kSegSmem)) mine = p.sitems[seg_begin + threadIdx.x];
   // the token tables, lengths, pools and q are read only after the previous kernel in the
@@ -202,10 +189,6 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
       mbar_init(full_bar(st), kProducers);
       mbar_init(empty_bar(st), (uint32_t)nh);
     }
-    for (int head = 0; kHalves > 1 && head < kWarps; ++head) {
-      mbar_init(told_bar(head), 32u);
-      mbar_init(read_bar(head), 32u);
-    }
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -223,10 +206,10 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
   __syncthreads();
   if (n_tok > kSuffixMaxCtaTokens) return;
 
-  if (warp >= kConsumers) {
-    // ---------------- producers: one packed row per lane (8 bits: lanes 0-1 K, 2-3 V) -------------
-    if constexpr (kSplitRegs) regs_down<64>();
-    const int part = warp - kConsumers;
+  if (warp >= kWarps) {
+    // ---------------- producers: one packed row per lane (lanes 0-1 K, 2-3 V) -------------
+    if constexpr (kSplitRegs) regs_down<72>();
+    const int part = warp - kWarps;
     if (part >= kProducers) return;
     const bool is_v = (lane & (2 * kRowsEach - 1)) >= kRowsEach;
     const uint8_t* pool = static_cast<const uint8_t*>(is_v ? p.vpool : p.kpool);
@@ -288,25 +271,23 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
     }
     return;
   }
-  if constexpr (kSplitRegs) regs_up<104>();
-  const int head = warp % kWarps, half = warp / kWarps;
-  if (head >= nh) return;  // no CTA-wide barrier is used below
+  if constexpr (kSplitRegs) regs_up<128>();
+  if (warp >= nh) return;  // no CTA-wide barrier is used below
 
-  // ---------------- consumers: KV head j ----------------
-  const int j = j0 + head;
+  // ---------------- consumers: warp `warp` owns KV head j ----------------
+  const int j = j0 + warp;
   const int g = p.g;
   const int r = lane >> 2, c = lane & 3;
   const int h0 = 2 * c;  // this thread's two head columns: h0, h0 + 1
   // Q^T as B fragments in the order of the K codes: k-step i takes dims 16 i + 4 c + {0, 1} and {2, 3}
   // of column r (query head j*g + r), 4 bits: 32 (i / 2) + 8 c + 4 (i % 2) + {0, 1} and {2, 3}; the next segment's rows
   // are loaded one segment ahead
-  // (4 bits: their lines are asked for, which takes no registers)
   uint32_t qn[16];
-  auto q_row = [&](int sg) { return static_cast<const __nv_bfloat16*>(p.q) + ((int64_t)seg_at(sg).b * p.n_q + j * g + r) * kD; };
   auto load_q = [&](int sg) {
     if (sg < n_seg && r < g) {
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + ((int64_t)seg_at(sg).b * p.n_q + j * g + r) * kD;
       if constexpr (BITS == 8) {
-        const uint2* qrow = reinterpret_cast<const uint2*>(q_row(sg));
+        const uint2* qrow = reinterpret_cast<const uint2*>(q);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint2 x = qrow[4 * i + c];
@@ -314,7 +295,7 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
           qn[2 * i + 1] = x.y;
         }
       } else {
-        const uint4* qrow = reinterpret_cast<const uint4*>(q_row(sg));
+        const uint4* qrow = reinterpret_cast<const uint4*>(q);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint4 x = qrow[4 * i + c];
@@ -329,23 +310,17 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
       for (int i = 0; i < 16; ++i) qn[i] = 0u;
     }
   };
-  auto ask_q = [&](int sg) {  // lane c takes 64 of the row's 256 bytes
-    if (sg < n_seg && r < g) asm volatile("prefetch.global.L1 [%0];" ::"l"(q_row(sg) + 32 * c));
-  };
-  if constexpr (BITS == 8) load_q(0);
-  const uint32_t head_off = (uint32_t)head * Lay::kCodes;
-  const uint32_t scale_at = code_bytes + (BITS == 8 ? 4 : kD / kKv4Group) * (uint32_t)head;
-  const uint32_t unit_at = code_bytes + scale_bytes + (uint32_t)(j0 % 16 + head);
-  int tile = 0;   // the segment's first tile, of all the CTA's
-  int talks = 0;  // segments so far that both warps of a head had tiles of
+  load_q(0);
+  const uint32_t head_off = (uint32_t)warp * Lay::kCodes;
+  const uint32_t scale_at = code_bytes + (BITS == 8 ? 4 : kD / kKv4Group) * (uint32_t)warp;
+  const uint32_t unit_at = code_bytes + scale_bytes + (uint32_t)(j0 % 16 + warp);
+  int tile = 0;  // tiles consumed so far
   for (int sg = 0; sg < n_seg; ++sg) {
     const DevSuffixItem seg = seg_at(sg);
     uint32_t qf[16];
-    if constexpr (BITS == 4) load_q(sg);
 #pragma unroll
     for (int i = 0; i < 16; ++i) qf[i] = qn[i];
-    if constexpr (BITS == 8) load_q(sg + 1);
-    else ask_q(sg + 1);
+    load_q(sg + 1);
     float unit;
     q_to_f16<16>(qf, unit);
 #pragma unroll
@@ -361,19 +336,20 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
     for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
 
     bool ok = true;
-    // V tiles, tile `first` and the next, from token t on: one running-max update for both, and their products side by
-    // side, so that a warp has two chains to issue from (two warps a scheduler leave most of a chain's
+    // V tiles from token t on: one running-max update for both, and their products side by side, so
+    // that a warp has two chains to issue from (two warps a scheduler leave most of a chain's
     // latency open)
-    auto tiles = [&](auto count, int first, int t) {
+    auto tiles = [&](auto count, int t) {
       constexpr int V = decltype(count)::value;
       const int mi = lane >> 3;
       const uint32_t frag = head_off + ((lane & 7) + (mi & 1) * 8) * kRowStride + (mi >> 1) * 16;
       uint32_t at[V];  // this lane's ldmatrix row of each tile
       float sa[V], sb[V], la[V], lb[V], s[V][4], s2[V][4];
+      uint2 ka[V], kb[V];  // 4 bits: the K scales of tokens r and r + 8
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int st = (first + v) % kStages;
-        const bool landed = mbar_wait_bounded(full_bar(st), ((first + v) / kStages) & 1, abort_flag, p.err, kDevTimeout,
+        const int st = (tile + v) % kStages;
+        const bool landed = mbar_wait_bounded(full_bar(st), ((tile + v) / kStages) & 1, abort_flag, p.err, kDevTimeout,
                                               kWaitLimitNs);
         if (!__all_sync(0xffffffffu, landed)) return false;
         at[v] = sbase + st * kStageBytes + frag;
@@ -384,12 +360,15 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
           sb[v] = *reinterpret_cast<const float*>(ksp + 8 * kRowStride);
           la[v] = *reinterpret_cast<const float*>(ksp + kTileBytes);
           lb[v] = *reinterpret_cast<const float*>(ksp + kTileBytes + 8 * kRowStride);
-        } else {  // (K's 16-dim scales are loaded where they are used)
+        } else {
           const unsigned char* up = smem + st * kStageBytes + r * kRowStride + unit_at;
           sa[v] = kv4_unit(up[0]);
           sb[v] = kv4_unit(up[8 * kRowStride]);
           la[v] = kv4_unit(up[kTileBytes]);
           lb[v] = kv4_unit(up[kTileBytes + 8 * kRowStride]);
+          const unsigned char* ksp = smem + st * kStageBytes + r * kRowStride + scale_at;
+          ka[v] = *reinterpret_cast<const uint2*>(ksp);
+          kb[v] = *reinterpret_cast<const uint2*>(ksp + 8 * kRowStride);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[v][e] = s2[v][e] = 0.f;
@@ -405,9 +384,8 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
 #pragma unroll
           for (int v = 0; v < V; ++v) {
             uint32_t fa[2], fb[2];
-            const unsigned char* ksp = smem + ((first + v) % kStages) * kStageBytes + r * kRowStride + scale_at + 4 * i;
-            scale_pairs(*reinterpret_cast<const uint32_t*>(ksp), 0u, sel, fa[0], fa[1]);
-            scale_pairs(*reinterpret_cast<const uint32_t*>(ksp + 8 * kRowStride), 0u, sel, fb[0], fb[1]);
+            scale_pairs(i ? ka[v].y : ka[v].x, 0u, sel, fa[0], fa[1]);
+            scale_pairs(i ? kb[v].y : kb[v].x, 0u, sel, fb[0], fb[1]);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {  // 32 dims
               uint32_t ya[4], yb[4];
@@ -511,7 +489,7 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
 #pragma unroll
           for (int v = 0; v < V; ++v) {
             // the scales of tokens 2 c, 2 c + 1, 2 c + 8 and 2 c + 9
-            const unsigned char* vsp = smem + ((first + v) % kStages) * kStageBytes + kTileBytes + 2 * c * kRowStride + scale_at + 4 * i;
+            const unsigned char* vsp = smem + ((tile + v) % kStages) * kStageBytes + kTileBytes + 2 * c * kRowStride + scale_at + 4 * i;
             auto word = [&](int t) { return *reinterpret_cast<const uint32_t*>(vsp + t * kRowStride); };
             uint32_t fa[2], fb[2];
             scale_pairs(word(0), word(1), sel, fa[0], fa[1]);
@@ -548,59 +526,20 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
       __syncwarp();
       if (lane == 0)
 #pragma unroll
-        for (int v = 0; v < V; ++v) mbar_arrive(empty_bar((first + v) % kStages));
+        for (int v = 0; v < V; ++v) mbar_arrive(empty_bar((tile + v) % kStages));
+      tile += V;
       return true;
     };
-    const int n_t = (seg.t1 - seg.t0 + kTile - 1) / kTile, begin = tile;
-    tile += n_t;
-    bool writer = true;
-    if constexpr (kHalves == 1) {
-      int k = 0;
-      for (; ok && k + 1 < n_t; k += 2) ok = tiles(std::integral_constant<int, 2>{}, begin + k, seg.t0 + k * kTile);
-      if (ok && k < n_t) ok = tiles(std::integral_constant<int, 1>{}, begin + k, seg.t0 + k * kTile);
-      if (!ok) break;
-    } else {
-      // the CTA's even tiles are those of the head's first warp; the warp that has the segment's first tile writes its record
-      writer = half == (begin & 1);
-      for (int k = writer ? 0 : 1; ok && k < n_t; k += 2) ok = tiles(std::integral_constant<int, 1>{}, begin + k, seg.t0 + k * kTile);
-      if (!ok) break;
-      if (n_t > 1) {
-        float4* state = reinterpret_cast<float4*>(smem + Lay::kOffState + head * Lay::kState) + lane;
-        if (!writer) {
-          if (talks > 0) ok = mbar_wait_bounded(read_bar(head), (talks - 1) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
-          if (!__all_sync(0xffffffffu, ok)) break;
-#pragma unroll
-          for (int mt = 0; mt < 8; ++mt) state[32 * mt] = make_float4(o[mt][0], o[mt][1], o[mt][2], o[mt][3]);
-          state[32 * 8] = make_float4(m0, m1, l0, l1);
-          mbar_arrive(told_bar(head));
-        } else {
-          ok = mbar_wait_bounded(told_bar(head), talks & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
-          if (!__all_sync(0xffffffffu, ok)) break;
-          const float4 x = state[32 * 8];
-          const float n0 = fmaxf(m0, x.x), n1 = fmaxf(m1, x.y);
-          const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
-          // (halves of the steps, as above)
-          const float a0 = ex2_approx(0.5f * (m0 - u0)), a1 = ex2_approx(0.5f * (m1 - u1));
-          const float b0 = ex2_approx(0.5f * (x.x - u0)), b1 = ex2_approx(0.5f * (x.y - u1));
-          l0 = l0 * a0 * a0 + x.z * b0 * b0;
-          l1 = l1 * a1 * a1 + x.w * b1 * b1;
-          const float aa0 = a0 * a0, aa1 = a1 * a1, bb0 = b0 * b0, bb1 = b1 * b1;
-#pragma unroll
-          for (int mt = 0; mt < 8; ++mt) {
-            const float4 y = state[32 * mt];
-            o[mt][0] = o[mt][0] * aa0 + y.x * bb0;
-            o[mt][1] = o[mt][1] * aa1 + y.y * bb1;
-            o[mt][2] = o[mt][2] * aa0 + y.z * bb0;
-            o[mt][3] = o[mt][3] * aa1 + y.w * bb1;
-          }
-          mbar_arrive(read_bar(head));
-          m0 = n0;
-          m1 = n1;
-        }
-        ++talks;
+    for (int t = seg.t0; ok && t < seg.t1;) {
+      if (seg.t1 - t > kTile) {
+        ok = tiles(std::integral_constant<int, 2>{}, t);
+        t += 2 * kTile;
+      } else {
+        ok = tiles(std::integral_constant<int, 1>{}, t);
+        t += kTile;
       }
     }
-    if (!writer) continue;
+    if (!ok) break;
 
     // finish the segment: full column sums, normalise, write the record
 #pragma unroll
