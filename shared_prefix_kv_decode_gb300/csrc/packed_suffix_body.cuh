@@ -35,7 +35,7 @@
 // 4 bits.  An element is code * b * u, b the e4m3 scale of its 16 dims and u the token's power of two: code * b goes
 // into fp16 exactly (one conversion and one product a pair), u takes the place of the scales ks and vs above, so
 // log2 vs is a whole number.  The 16-bit pairs that ldmatrix moves are four codes: a lane's eight codes of a row serve
-// two k-steps of S^T, and the transposed form gives two tokens x four dims, whose nibbles are paired by shifts.
+// two k-steps of S^T, and the transposed form gives two tokens x four dims, whose fp16 values are paired by byte permutations.
 // u lies between 2^-100 and 2^116, inside the range that the row sum is made for.
 #pragma once
 
@@ -125,11 +125,10 @@ __device__ __forceinline__ void block_barrier() {  // of the whole block, from e
 // Two tokens' four codes (lane word of a transposed ldmatrix: token 2 c in the low half) -> for each of the four dims
 // the two tokens' values as fp16x2, times the tokens' scales.
 __device__ __forceinline__ void kv4_transposed(uint32_t w, uint32_t scale2, uint32_t (&y)[4]) {
-  constexpr uint32_t M = 0x0f0f0f0fu;
-  const uint32_t even = (w & M) | ((w >> 12) & ~M), odd = ((w >> 4) & M) | ((w >> 16) & ~M);  // dims 0, 2 and 1, 3 in two bytes
-  e2m1x8_to_f16x8(__byte_perm(even, odd, 0x5140), y);
+  uint32_t z[4];
+  e2m1x8_to_f16x8(w, z);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) y[i] = f16x2_mul(y[i], scale2);
+  for (int i = 0; i < 4; ++i) y[i] = f16x2_mul(__byte_perm(z[i / 2], z[2 + i / 2], i & 1 ? 0x7632 : 0x5410), scale2);
 }
 // The four e4m3 bytes that sel picks of two words, in pairs, as fp16x2.
 __device__ __forceinline__ void scale_pairs(uint32_t a, uint32_t b, uint32_t sel, uint32_t& lo, uint32_t& hi) {
@@ -364,8 +363,8 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
           const unsigned char* up = smem + st * kStageBytes + r * kRowStride + unit_at;
           sa[v] = kv4_unit(up[0]);
           sb[v] = kv4_unit(up[8 * kRowStride]);
-          la[v] = kv4_unit(up[kTileBytes]);
-          lb[v] = kv4_unit(up[kTileBytes + 8 * kRowStride]);
+          la[v] = (float)up[kTileBytes];
+          lb[v] = (float)up[kTileBytes + 8 * kRowStride];
           const unsigned char* ksp = smem + st * kStageBytes + r * kRowStride + scale_at;
           ka[v] = *reinterpret_cast<const uint2*>(ksp);
           kb[v] = *reinterpret_cast<const uint2*>(ksp + 8 * kRowStride);
@@ -430,8 +429,8 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
           la[v] = lg2_approx(la[v]);
           lb[v] = lg2_approx(lb[v]);
         } else {  // (a whole number; whatever it is for a token that does not count)
-          la[v] = (float)((int)(__float_as_uint(la[v]) >> 23) - 127);
-          lb[v] = (float)((int)(__float_as_uint(lb[v]) >> 23) - 127);
+          la[v] -= 127.f;
+          lb[v] -= 127.f;
         }
         s[v][0] = in_a ? (s[v][0] + s2[v][0]) * (f0 * sa[v]) : -INFINITY;
         s[v][1] = in_a ? (s[v][1] + s2[v][1]) * (f1 * sa[v]) : -INFINITY;
