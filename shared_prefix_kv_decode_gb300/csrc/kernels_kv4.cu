@@ -10,7 +10,7 @@ namespace {
 // One block of kKv8Block slab tokens of one KV head, of K (blockIdx.y = 0) or V.  A thread holds groups of 16
 // elements in registers between the block's amax and their codes, so the rows are read once: 2.6 bytes moved for
 // each bf16 element.
-template <typename T, int D>
+template <typename T, int D, bool WIDE>
 __global__ void __launch_bounds__(256) kv4_fill_kernel(const T* __restrict__ k, const T* __restrict__ v, int32_t L_p,
                                                        uint8_t* __restrict__ kpool, uint8_t* __restrict__ vpool,
                                                        int64_t first_slot, int32_t n_kv) {
@@ -26,7 +26,7 @@ __global__ void __launch_bounds__(256) kv4_fill_kernel(const T* __restrict__ k, 
 #pragma unroll
   for (int c = 0; c < kPer; ++c) {
     const int32_t idx = threadIdx.x + c * 256, t = idx / kPerRow;
-    if (idx < kGroups && t < n) x[c].load(src + (int64_t)t * (n_kv * D) + idx % kPerRow * kKv4Group);
+    if (idx < kGroups && t < n) x[c].template load<WIDE>(src + (int64_t)t * (n_kv * D) + idx % kPerRow * kKv4Group);
     else x[c].clear();
   }
   float top[kPer], finite[kPer], amax = 0.f;
@@ -73,7 +73,7 @@ __device__ __forceinline__ void kv4_write_row(const T* __restrict__ src, uint8_t
   const int i = threadIdx.x % kTeam;
   const bool mine = slot_row && i < D / kKv4Group;
   Kv4Group<T> x;
-  if (mine) x.load(src + i * kKv4Group);
+  if (mine) x.template load<false>(src + i * kKv4Group);
   else x.clear();
   const float top = x.top(), finite = kv4_finite_top(x, top);
   float amax = finite;
@@ -114,7 +114,9 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const T* __restrict__ k
   }
 }
 
-// Row b of k_new/v_new at the slot of request b's newest token (the fused append's write).
+// Row b of k_new/v_new at the slot of request b's newest token (the fused append's write).  Launched as a dependent of
+// what the stream ran before, and the attention as a dependent of this: its set-up overlaps the writes, and it reads
+// nothing that they change before this grid is done.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv4_append_newest_kernel(AttnParams p) {
   constexpr int kTeam = kv4_team<D>(), kItems = 256 / kTeam;
@@ -122,6 +124,8 @@ __global__ void __launch_bounds__(256) kv4_append_newest_kernel(AttnParams p) {
   uint8_t* at = nullptr;
   const T* src = nullptr;
   int32_t j = 0;
+  grid_dep_launch_dependents();
+  grid_dep_wait();
   if (w < (int64_t)p.B * p.n_kv * 2) {
     const int64_t h = w / 2;
     const int32_t b = (int32_t)(h / p.n_kv);
@@ -145,7 +149,9 @@ cudaError_t fill_t(const T* k, const T* v, int32_t L_p, uint8_t* kpool, uint8_t*
   if (ctas > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)ctas, 2);
   return with_vpl(d, [&](auto vpl) {
-    kv4_fill_kernel<T, 32 * decltype(vpl)::value><<<grid, 256, 0, s>>>(k, v, L_p, kpool, vpool, first_slot, n_kv);
+    constexpr int D = 32 * decltype(vpl)::value;
+    auto kernel = ((uintptr_t)k | (uintptr_t)v) % 32 ? kv4_fill_kernel<T, D, false> : kv4_fill_kernel<T, D, true>;
+    kernel<<<grid, 256, 0, s>>>(k, v, L_p, kpool, vpool, first_slot, n_kv);
     return cudaGetLastError();
   });
 }
@@ -183,9 +189,8 @@ cudaError_t launch_kv4_append_newest(int32_t dtype, const AttnParams& p, cudaStr
   return with_vpl(p.d, [&](auto vpl) {
     constexpr int D = 32 * decltype(vpl)::value, kItems = 256 / kv4_team<D>();
     const unsigned grid = (unsigned)(((int64_t)p.B * p.n_kv * 2 + kItems - 1) / kItems);
-    if (dtype == 1) kv4_append_newest_kernel<__nv_bfloat16, D><<<grid, 256, 0, s>>>(p);
-    else kv4_append_newest_kernel<float, D><<<grid, 256, 0, s>>>(p);
-    return cudaGetLastError();
+    auto kernel = dtype == 1 ? kv4_append_newest_kernel<__nv_bfloat16, D> : kv4_append_newest_kernel<float, D>;
+    return launch_kernel(kernel, dim3(grid), dim3(256), 0, s, true, p);
   });
 }
 

@@ -9,6 +9,18 @@
 namespace granikv {
 namespace {
 
+// WIDE: to a 32-byte boundary, else to a 16-byte one.  (32 bytes in one store: a warp's stores fill whole sectors.  16K
+// tokens of 8 x 128 in 4 bits: 15.0 us, 0.85 of the copy rate)
+template <bool WIDE>
+__device__ __forceinline__ void store32(void* dst, const uint4& a, const uint4& b) {
+  if constexpr (WIDE) {
+    stg32(dst, a, b);
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = a;
+    reinterpret_cast<uint4*>(dst)[1] = b;
+  }
+}
+template <bool WIDE>
 __device__ __forceinline__ void store16(__nv_bfloat16* dst, const float (&x)[16]) {
   uint32_t w[8];
 #pragma unroll
@@ -16,17 +28,17 @@ __device__ __forceinline__ void store16(__nv_bfloat16* dst, const float (&x)[16]
     const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
     w[i] = *reinterpret_cast<const uint32_t*>(&p);
   }
-  __stcs(reinterpret_cast<uint4*>(dst), make_uint4(w[0], w[1], w[2], w[3]));
-  __stcs(reinterpret_cast<uint4*>(dst) + 1, make_uint4(w[4], w[5], w[6], w[7]));
+  store32<WIDE>(dst, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
 }
+template <bool WIDE>
 __device__ __forceinline__ void store16(float* dst, const float (&x)[16]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    __stcs(reinterpret_cast<float4*>(dst) + i, make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+  for (int i = 0; i < 16; i += 8)
+    store32<WIDE>(dst + i, *reinterpret_cast<const uint4*>(x + i), *reinterpret_cast<const uint4*>(x + i + 4));
 }
 
 // A thread takes 16 elements of one head of a row.
-template <int BITS, typename T>
+template <int BITS, typename T, bool WIDE>
 __device__ __forceinline__ void read16(const uint8_t* __restrict__ row, T* __restrict__ dst, int32_t n_kv, int32_t d, int32_t j, int32_t piece) {
   if constexpr (BITS == 0) {
     constexpr int kPieces = 16 * sizeof(T) / 16;
@@ -35,7 +47,7 @@ __device__ __forceinline__ void read16(const uint8_t* __restrict__ row, T* __res
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) w[i] = __ldcs(src + i);
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) __stcs(reinterpret_cast<uint4*>(dst) + i, w[i]);
+    for (int i = 0; i < kPieces; i += 2) store32<WIDE>(reinterpret_cast<uint4*>(dst) + i, w[i], w[i + 1]);
   } else if constexpr (BITS == 8) {
     const uint4 w = __ldcs(reinterpret_cast<const uint4*>(row + (int64_t)j * d + piece * 16));
     const float s = *reinterpret_cast<const float*>(row + (int64_t)n_kv * d + 4 * j);
@@ -48,7 +60,7 @@ __device__ __forceinline__ void read16(const uint8_t* __restrict__ row, T* __res
 #pragma unroll
       for (int c = 0; c < 4; ++c) x[4 * i + c] = f[c] * s;
     }
-    store16(dst, x);
+    store16<WIDE>(dst, x);
   } else {
     const uint2 w = __ldcs(reinterpret_cast<const uint2*>(row + (int64_t)j * (d / 2) + piece * 8));
     const uint32_t b = kv4_scale2(row[kv4_scales_at(n_kv, d) + (int64_t)j * (d / kKv4Group) + piece]);
@@ -66,11 +78,11 @@ __device__ __forceinline__ void read16(const uint8_t* __restrict__ row, T* __res
         x[8 * h + 2 * i + 1] = f.y * t;
       }
     }
-    store16(dst, x);
+    store16<WIDE>(dst, x);
   }
 }
 
-template <int BITS, typename T>
+template <int BITS, typename T, bool WIDE>
 __global__ void __launch_bounds__(256) read_kernel(ReadParams p, int32_t d, int32_t tokens) {
   const int32_t per_head = d / 16, per_row = p.n_kv * per_head;
   const uint8_t* pool = blockIdx.y ? p.pool[1] : p.pool[0];
@@ -87,26 +99,32 @@ __global__ void __launch_bounds__(256) read_kernel(ReadParams p, int32_t d, int3
         continue;
       }
     }
-    read16<BITS, T>(pool + slot * p.row, out + ((t0 + t) * per_row + h) * 16, p.n_kv, d, j, h - j * per_head);
+    read16<BITS, T, WIDE>(pool + slot * p.row, out + ((t0 + t) * per_row + h) * 16, p.n_kv, d, j, h - j * per_head);
   }
 }
 
-template <int BITS>
-cudaError_t read_bits(int32_t dtype, int32_t d, const ReadParams& p, cudaStream_t s) {
-  // as many tokens a CTA as give each thread four pieces or so
+template <int BITS, typename T>
+cudaError_t read_bits(int32_t d, const ReadParams& p, cudaStream_t s) {
+  // Tokens a CTA: four pieces a thread; one, where the CTAs are too few to fill the SMs (64 tokens of 8 x 128 1.8 us, with
+  // four pieces 3.1).
   const int64_t per_row = (int64_t)p.n_kv * (d / 16);
   if (per_row > INT32_MAX / 2) return cudaErrorInvalidValue;
-  const int32_t tokens = (int32_t)(per_row >= 1024 ? 1 : 1024 / per_row);
+  const int64_t pieces = p.N * per_row >= 512 * 1024 ? 1024 : 256;
+  const int32_t tokens = (int32_t)(per_row >= pieces ? 1 : pieces / per_row);
   const dim3 grid((unsigned)(((int64_t)p.N + tokens - 1) / tokens), 2);
-  if (dtype == 1) read_kernel<BITS, __nv_bfloat16><<<grid, 256, 0, s>>>(p, d, tokens);
-  else read_kernel<BITS, float><<<grid, 256, 0, s>>>(p, d, tokens);
+  auto kernel = ((uintptr_t)p.out[0] | (uintptr_t)p.out[1]) % 32 ? read_kernel<BITS, T, false> : read_kernel<BITS, T, true>;
+  kernel<<<grid, 256, 0, s>>>(p, d, tokens);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_read(int32_t dtype, int32_t bits, int32_t d, const ReadParams& p, cudaStream_t s) {
-  return bits == 8 ? read_bits<8>(dtype, d, p, s) : bits == 4 ? read_bits<4>(dtype, d, p, s) : read_bits<0>(dtype, d, p, s);
+  auto of = [&](auto t) {
+    using T = decltype(t);
+    return bits == 8 ? read_bits<8, T>(d, p, s) : bits == 4 ? read_bits<4, T>(d, p, s) : read_bits<0, T>(d, p, s);
+  };
+  return dtype == 1 ? of(__nv_bfloat16{}) : of(0.f);
 }
 
 }  // namespace granikv
