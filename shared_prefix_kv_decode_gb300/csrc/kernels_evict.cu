@@ -144,7 +144,9 @@ __global__ void __launch_bounds__(256) weigh_generic_kernel(WeighParams p, const
 // 4 u + {0, 1} and 4 u + {2, 3}.  Of a packed 8-bit row it holds dims 64 i + 16 c + 0..15; k-step
 // 4 i + u takes dims 4 u + {0, 1} and 4 u + {2, 3}, converted to fp16 (exact); the row's scale
 // multiplies the scores, and q is brought into fp16's range by a power of two per query head
-// (exact but for elements 2^-31 below the row's largest).
+// (exact but for elements 2^-31 below the row's largest).  Of a packed 4-bit row it holds dims D / 4 c and on in one
+// piece of 16 bytes (d 64: 8), with the four bytes that its 16-dim scales are among and the four that the row's unit is; the
+// piece's word w takes k-steps 2 w and 2 w + 1 (dims 8 w + 4 u + {0, 1} and {2, 3}), converted to fp16 times scale (exact).
 // The units' sums go to shared memory and are added in KV-head order: the result has one order.
 // A CTA takes a chunk of 64 to 512 tokens, sized so that all chunks run at once: with 256 tokens a CTA the
 // 877 chunks of 224K tokens made 1.44 waves of 608 CTAs (49.5 us against 47.8), and a CTA's start (length, slots, q, first rows: four
@@ -156,20 +158,23 @@ constexpr int kMaxHeads = 64;  // KV heads: the sums of a chunk of kChunkMin tok
 // 47.8 us (5.0 TB/s of its 237 MB), 30K of 16-bit rows 13.9 us.  Fewer CTAs with deeper rings were
 // slower (224K tokens, on an earlier form: 50.8 us with four CTAs an SM, 52.9 with three and three units,
 // 58.9 with two and four), and so were units ahead in registers (58.8).
-template <bool KV8, int D>
+template <int BITS, int D>
 struct WeighUnit {
-  static constexpr int kPieces = KV8 ? D / 64 : D / 32;            // 16-byte pieces of a row a lane
-  static constexpr int kBytes = 2 * kPieces * 512 + (KV8 ? 256 : 0);  // rows lane / 4 and lane / 4 + 8, and their scales
+  static constexpr bool KV8 = BITS == 8;
+  static constexpr int kPieces = BITS == 4 ? 1 : KV8 ? D / 64 : D / 32;  // 16-byte pieces of a row a lane
+  // rows lane / 4 and lane / 4 + 8, and their scales (4 bits: scales and units)
+  static constexpr int kBytes = 2 * kPieces * 512 + (BITS == 4 ? 512 : KV8 ? 256 : 0);
   static constexpr int kDepth = 2;
   static constexpr int kRing = 8 * kDepth * kBytes;
-  static constexpr int kBlocks = KV8 ? 4 : 3;
+  static constexpr int kBlocks = BITS ? 4 : 3;
   // shared memory for a chunk's sums that leaves room for kBlocks CTAs an SM
-  static constexpr int kSums = KV8 ? 16 * 1024 : 8 * 1024;
+  static constexpr int kSums = BITS ? 16 * 1024 : 8 * 1024;
 };
 
-template <bool KV8, int D, int N>
-__global__ void __launch_bounds__(256, WeighUnit<KV8, D>::kBlocks) weigh_mma_kernel(WeighParams p, const __grid_constant__ WeighRows<N> rows) {
-  using Unit = WeighUnit<KV8, D>;
+template <int BITS, int D, int N>
+__global__ void __launch_bounds__(256, WeighUnit<BITS, D>::kBlocks) weigh_mma_kernel(WeighParams p, const __grid_constant__ WeighRows<N> rows) {
+  using Unit = WeighUnit<BITS, D>;
+  constexpr bool KV8 = BITS == 8, KV4 = BITS == 4;
   extern __shared__ __align__(16) unsigned char s_ring[];  // [8 warps][kDepth] units, then the sums
   float* s_sum = reinterpret_cast<float*>(s_ring + Unit::kRing);  // [n_kv][rows.tokens]
   __shared__ int32_t s_slot[kChunkMax];
@@ -205,7 +210,7 @@ __global__ void __launch_bounds__(256, WeighUnit<KV8, D>::kBlocks) weigh_mma_ker
       x.tile += 16;
     }
   };
-  const int32_t row_bytes = KV8 ? (int32_t)p.packed_row : p.n_kv * D * 2;
+  const int32_t row_bytes = BITS ? (int32_t)p.packed_row : p.n_kv * D * 2;
   // this lane's pieces of the rows of a unit into stage st (zeros for a slot that does not count)
   auto load_unit = [&](const Place& x, int st) {
     if (x.tile < n) {
@@ -214,8 +219,17 @@ __global__ void __launch_bounds__(256, WeighUnit<KV8, D>::kBlocks) weigh_mma_ker
       for (int h = 0; h < 2; ++h) {
         const int32_t slot = s_slot[tile + r + 8 * h];
         const uint8_t* row = (const uint8_t*)p.kpool + (int64_t)max(slot, 0) * row_bytes;
-        const uint4* src = reinterpret_cast<const uint4*>(row + j * (KV8 ? D : 2 * D)) + c;
         const uint32_t dst = ring + st * Unit::kBytes + (h * Unit::kPieces * 32 + lane) * 16;
+        if constexpr (KV4) {
+          const uint8_t* src = row + j * (D / 2) + c * (D / 8);
+          if constexpr (D == 128) cp_async16(dst, src, slot < 0 ? 0 : 16);
+          else cp_async8(dst, src, slot < 0 ? 0 : 8);
+          const uint32_t meta = ring + st * Unit::kBytes + 1024 + (h * 32 + lane) * 8;
+          cp_async4(meta, row + kv4_scales_at(p.n_kv, D) + j * (D / kKv4Group) + (D == 128 ? c / 2 * 4 : 0), slot < 0 ? 0 : 4);
+          cp_async4(meta + 4, row + kv4_units_at(p.n_kv, D) + j / 4 * 4, slot < 0 ? 0 : 4);
+          continue;
+        }
+        const uint4* src = reinterpret_cast<const uint4*>(row + j * (KV8 ? D : 2 * D)) + c;
 #pragma unroll
         for (int i = 0; i < Unit::kPieces; ++i) cp_async16(dst + i * 512, src + 4 * i, slot < 0 ? 0 : 16);
         if constexpr (KV8)
@@ -235,7 +249,19 @@ __global__ void __launch_bounds__(256, WeighUnit<KV8, D>::kBlocks) weigh_mma_ker
     const bool mine = h0 + r < h_end;
     const uint4* src = reinterpret_cast<const uint4*>((const __nv_bfloat16*)p.q + ((int64_t)b * p.n_q + h0 + r) * D);
     float unit = 1.f;  // what one step of the scaled q stands for
-    if constexpr (!KV8) {
+    if constexpr (KV4) {
+      uint32_t w[D / 32][4];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint4 x = mine ? __ldg(src + (D / 32) * c + i) : make_uint4(0u, 0u, 0u, 0u);
+        w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+      }
+      q_to_f16<D / 8>(&w[0][0], unit);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) qf[2 * i + u][0] = w[i][2 * u], qf[2 * i + u][1] = w[i][2 * u + 1];
+    } else if constexpr (!KV8) {
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const uint4 x = mine ? __ldg(src + 4 * i + c) : make_uint4(0u, 0u, 0u, 0u);
@@ -273,6 +299,17 @@ __global__ void __launch_bounds__(256, WeighUnit<KV8, D>::kBlocks) weigh_mma_ker
       sa = sc[lane];
       sb = sc[32 + lane];
     }
+    uint2 ma, mb;  // 4 bits: the rows' scales and units
+    if constexpr (KV4) {
+      const uint2* meta = reinterpret_cast<const uint2*>(mine + 1024) + lane;
+      ma = meta[0];
+      mb = meta[32];
+      sa = kv4_unit(ma.y >> (j % 4 * 8) & 255u);
+      sb = kv4_unit(mb.y >> (j % 4 * 8) & 255u);
+      // this lane's one or two scales in the low bytes
+      ma.x >>= D == 128 ? c % 2 * 16 : c * 8;
+      mb.x >>= D == 128 ? c % 2 * 16 : c * 8;
+    }
     float w0 = 0.f, w1 = 0.f;
     for (int32_t h0 = j * p.g; h0 < (j + 1) * p.g; h0 += 8) {
       if (have != h0) load_q(h0, (j + 1) * p.g);
@@ -281,7 +318,22 @@ __global__ void __launch_bounds__(256, WeighUnit<KV8, D>::kBlocks) weigh_mma_ker
       for (int i = 0; i < Unit::kPieces; ++i) {
         const uint4 x = ka[32 * i], y = ka[32 * (Unit::kPieces + i)];
         const uint32_t a[4] = {x.x, x.y, x.z, x.w}, z[4] = {y.x, y.y, y.z, y.w};
-        if constexpr (KV8) {
+        if constexpr (KV4) {
+#pragma unroll
+          for (int w = 0; w < D / 32; ++w) {
+            const uint32_t fa = kv4_scale2(ma.x >> (w / 2 * 8) & 255u), fb = kv4_scale2(mb.x >> (w / 2 * 8) & 255u);
+            uint32_t ka4[4], kb4[4];
+            e2m1x8_to_f16x8(a[w], ka4);
+            e2m1x8_to_f16x8(z[w], kb4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              ka4[k] = f16x2_mul(ka4[k], fa);
+              kb4[k] = f16x2_mul(kb4[k], fb);
+            }
+            mma_f16_16816(s, ka4[0], kb4[0], ka4[1], kb4[1], qf[2 * w][0], qf[2 * w][1]);
+            mma_f16_16816(s2, ka4[2], kb4[2], ka4[3], kb4[3], qf[2 * w + 1][0], qf[2 * w + 1][1]);
+          }
+        } else if constexpr (KV8) {
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             uint32_t a0, a2, b0, b2;
@@ -663,21 +715,21 @@ bool weigh_on_mma(const WeighParams& p) {
   return std::is_same_v<T, __nv_bfloat16> && (p.d == 128 || p.d == 64) && p.n_kv <= kMaxHeads;
 }
 
-template <bool KV8, int D, int N>
+template <int BITS, int D, int N>
 cudaError_t weigh_mma(const WeighParams& p, const WeighRows<N>& rows, int32_t chunks, cudaStream_t s) {
   static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem_once(weigh_mma_kernel<KV8, D, N>, WeighUnit<KV8, D>::kRing + 4 * kMaxHeads * kChunkMin, allowed, 4 * kChunkMax);
+  cudaError_t e = allow_smem_once(weigh_mma_kernel<BITS, D, N>, WeighUnit<BITS, D>::kRing + 4 * kMaxHeads * kChunkMin, allowed, 4 * kChunkMax);
   if (e != cudaSuccess) return e;
-  const int smem = WeighUnit<KV8, D>::kRing + (int)sizeof(float) * p.n_kv * rows.tokens;
-  weigh_mma_kernel<KV8, D, N><<<chunks, 256, smem, s>>>(p, rows);
+  const int smem = WeighUnit<BITS, D>::kRing + (int)sizeof(float) * p.n_kv * rows.tokens;
+  weigh_mma_kernel<BITS, D, N><<<chunks, 256, smem, s>>>(p, rows);
   return cudaGetLastError();
 }
 
 template <typename T, int BITS, int N>
 cudaError_t weigh_launch(const WeighParams& p, const WeighRows<N>& rows, int32_t chunks, cudaStream_t s) {
-  if constexpr (std::is_same_v<T, __nv_bfloat16> && BITS != 4) {
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
     if (weigh_on_mma<T>(p)) {
-      return p.d == 128 ? weigh_mma<BITS == 8, 128, N>(p, rows, chunks, s) : weigh_mma<BITS == 8, 64, N>(p, rows, chunks, s);
+      return p.d == 128 ? weigh_mma<BITS, 128, N>(p, rows, chunks, s) : weigh_mma<BITS, 64, N>(p, rows, chunks, s);
     }
   }
   const int smem = (int)sizeof(float) * (kTok * (p.d + 1) + 8 * kTok);
@@ -706,8 +758,8 @@ template <typename T, int BITS>
 cudaError_t weigh_all(const WeighParams& p, const int32_t* seq_len, cudaStream_t s) {
   constexpr int kSmall = 64, kLarge = kRowsPerLaunch;
   int tokens = kTok;
-  if (BITS != 4 && weigh_on_mma<T>(p)) {
-    using Unit = WeighUnit<BITS == 8, 128>;
+  if (weigh_on_mma<T>(p)) {
+    using Unit = WeighUnit<BITS, 128>;
     const int most = std::max(kChunkMin, std::min(kChunkMax, Unit::kSums / (4 * p.n_kv) / 16 * 16));
     const int64_t slots = (int64_t)Unit::kBlocks * p.num_sms;
     // the fewest tokens a chunk, in steps of 16, with which the grid is one wave
