@@ -331,6 +331,39 @@ def test_read_leaves_the_rows_of_bad_slots(cuda_ok, kind):
         assert (y[1:4] == 7.0).all() and not (y[[0, 4]] == 7.0).all(dim=2).any()
 
 
+@pytest.mark.parametrize("n_kv,d,dtype", [(8, 128, "bf16"), (2, 64, "f32"), (3, 96, "bf16"), (1, 32, "f32")])
+@pytest.mark.parametrize("kind", ["kv4", "kv8", "plain"])
+def test_rows_on_16_byte_boundaries_only(cuda_ok, n_kv, d, dtype, kind):
+    """Rows and results that start 16 bytes past a 32-byte boundary: the same bytes and values as from one."""
+    torch, rng = _torch(), np.random.default_rng([n_kv, d, 16])
+    L, N = 130, 40
+
+    def once(off):
+        rng = np.random.default_rng(7)
+        ctx, pools, tdt = _pools(L + N + 20, n_kv, d, dtype, L + 5, kind)
+        sid, _ = ctx.hot_alloc(L)
+        step = off // torch.tensor([], dtype=tdt).element_size()
+
+        def place(n):
+            x = torch.empty(n * n_kv * d + step, dtype=tdt, device="cuda")[step:].view(n, n_kv, d)
+            assert x.data_ptr() % 32 == off
+            return x
+        pk, pv, ck, cv = (place(n) for n in (L, L, N, N))
+        for x in (pk, pv, ck, cv):
+            x.copy_(torch.from_numpy(_rows(rng, x.shape[0], n_kv, d, dtype)))
+        slots = torch.from_numpy((L + 5 + rng.permutation(N + 15)[:N]).astype(np.int32)).cuda()
+        ctx.hot_fill(0, sid, pk, pv)
+        ctx.cold_append(0, ck, cv, slots, N)
+        outs = [place(n) for n in (L, L, N, N)]
+        ctx.hot_read(0, sid, 0, L, outs[0], outs[1])
+        ctx.cold_read(0, slots, N, outs[2], outs[3])
+        ctx.sync_status()
+        return [p.clone() for p in pools] + outs
+
+    for a, b in zip(once(0), once(16)):
+        assert torch.equal(a.view(torch.uint8) if a.dtype != torch.uint8 else a, b.contiguous().view(torch.uint8) if b.dtype != torch.uint8 else b)
+
+
 def test_rows_go_through_the_cache_unchanged_the_second_time(cuda_ok):
     """What a COLD token reads back as is held exactly when it is written again."""
     torch, rng = _torch(), np.random.default_rng(6)
@@ -697,6 +730,33 @@ def test_step_of_calls_in_a_graph(cuda_ok):
     c.ctx.sync_status()
 
 
+@pytest.mark.parametrize("B", [1, 8, 64])
+def test_calls_back_to_back_in_a_graph(cuda_ok, B):
+    """Two dozen calls one after the other, replayed again and again (as many prefix CTAs as SMs, and fewer): every one
+    ends, with the result of a single call."""
+    torch, rng = _torch(), np.random.default_rng([B, 41])
+    c = Kv4(rng, n_q=32, n_kv=8, d=128, dtype="bf16", prefixes=[9728], of=[0] * B, lens=[0] * B)
+    o, lse = c.decode()
+    plan = c.ctx.dispatch(c.batch)
+    ws = torch.empty(c.ctx.workspace_size(plan), dtype=torch.uint8, device="cuda")
+    outs = [(torch.zeros_like(o), torch.zeros_like(lse)) for _ in range(24)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    c.ctx.decode_attention(0, c.q, c.batch, plan, *outs[0], ws, ws.numel(), s)
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        for a, b in outs:
+            c.ctx.decode_attention(0, c.q, c.batch, plan, a, b, ws, ws.numel(), s)
+    for _ in range(20):
+        with torch.cuda.stream(s):
+            g.replay()
+    s.synchronize()
+    c.ctx.sync_status()
+    for a, b in outs:
+        assert torch.equal(a, o) and torch.equal(b, lse)
+
+
 def test_decode_far_slots(cuda_ok):
     """Slots whose byte offsets pass 2^32, in slab and COLD pool."""
     torch, gb, rng = _torch(), _gb(), np.random.default_rng(17)
@@ -739,6 +799,16 @@ def test_decode_bad_slot_is_latched(cuda_ok):
     c.table[0, 7] = -3
     with pytest.raises(gb.DeviceCheckFailed):
         c.decode()
+
+
+def test_stalled_wait_is_reported_and_the_context_survives(cuda_ok):
+    gb, rng = _gb(), np.random.default_rng(30)
+    c = Kv4(rng, n_q=32, n_kv=8, d=128, dtype="bf16", prefixes=[300], of=[0, 0, -1], lens=[40, 20, 70])
+    c.check(*c.decode(), "before")
+    c.ctx.inject_stall(True)
+    with pytest.raises(gb.DeviceCheckFailed):
+        c.decode()
+    c.check(*c.decode(), "after")
 
 
 def test_prefill_is_refused_and_static_workspace_serves(cuda_ok):
