@@ -53,8 +53,8 @@
 // to [2^14, 2^15): exact down to 2^-31 of the row's largest element), and u takes the place of ks and vs.  A
 // conversion warp's ring holds its 32 tokens' codes, by a TMA box, and scales, 8 bytes a token by cp.async from the warp
 // itself: TMA takes about four clocks for a row of a box, however short, so with the scales in boxes of their own
-// the loads alone took longer (a tile's 2,200 clocks) than everything else.  The K ring has two slots of fp16,
-// filled by four arrivals like V's.
+// the loads alone took longer (a tile's 2,200 clocks) than everything else.  The K and V rings have five
+// slots of one tile in fp16.
 #pragma once
 
 #include <cuda.h>
@@ -84,17 +84,14 @@ using pks::regs_up;
 constexpr int kD = 128;
 constexpr int kM = kDenseRows;                // 128 query rows per CTA
 constexpr int kN = kKv8Block;                 // 64 tokens per tile
-constexpr int kPair = kDenseTile;             // 128 tokens: what the K and V rings hold in a slot
-static_assert(kPair == 2 * kN && kPair / 4 == kKv8VBox, "a conversion warp's part of a V slot is one box");
-constexpr int kVSlots = 3;                    // slots of the V ring (fp16)
+constexpr int kPair = kDenseTile;             // 128 tokens: what is loaded at a time
+static_assert(kPair == 2 * kN && kPair / 4 == kKv8VBox, "a conversion warp's part is one box");
 constexpr int kSBufs = 5;                     // S/P buffers in TMEM
 constexpr int kSoftmaxWarps = 8;
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
 constexpr int kWarpConv = 8, kParts = 4;
-constexpr int kPart = kPair / kParts;         // tokens of a slot that one warp converts
-constexpr int kHalf = kPair * 128;            // one 64-dim half of an fp16 slot: 16 KB
-constexpr int kTile = 2 * kHalf;              // 32 KB
-constexpr int kCodes = kPair * kD;            // a slot's codes: 16 KB
+constexpr int kPart = kPair / kParts;         // tokens that one warp converts at a time
+constexpr int kCodes = kPair * kD;            // 8 bits: codes of 128 tokens, 16 KB
 constexpr int kPartCodes = kPart * kD;        // 4 KB
 template <int BITS>
 struct Layout {
@@ -104,14 +101,21 @@ struct Layout {
   static constexpr int kThreads = (kWarpS + 4) * 32;
   // 4 bits: 20 warps start with 96 registers; the softmax warps go on with 128, the others with 72
   static constexpr bool kSplitRegs = BITS == 4;
-  static constexpr int kKSlots = BITS == 8 ? 4 : 2;       // slots of the K ring (codes, 4 bits: fp16)
-  static constexpr int kKSlotBytes = BITS == 8 ? kCodes : kTile;
+  // A slot of the fp16 rings holds 128 tokens, which four warps fill, or (4 bits) a tile of 64, filled by the two warps whose
+  // parts it is: what S and PV have read is free a tile earlier
+  static constexpr int kSlotTiles = BITS == 8 ? 2 : 1;
+  static constexpr int kFill = kParts * kSlotTiles / 2;   // warps that fill a slot
+  static constexpr int kHalf = kSlotTiles * kN * 128;     // one 64-dim half of a slot
+  static constexpr int kSlot = 2 * kHalf;                 // 32 KB or 16
+  static constexpr int kVSlots = BITS == 8 ? 3 : 5;       // slots of the V ring (fp16)
+  static constexpr int kKSlots = BITS == 8 ? 4 : 5;       // slots of the K ring (codes of 128 tokens, 4 bits: fp16)
+  static constexpr int kKSlotBytes = BITS == 8 ? kCodes : kSlot;
   static constexpr int kCSlots = BITS == 8 ? 4 : 3;       // slots of each conversion warp's ring (codes, 4 bits: and scales)
   static constexpr int kHead = kD * BITS / 8;             // bytes of a head's codes
   static constexpr int kCSlotBytes = BITS == 8 ? kPartCodes : kPart * (kHead + kD / kKv4Group);
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kOffK + kKSlots * kKSlotBytes;
-  static constexpr int kOffCodes = kOffV + kVSlots * kTile;
+  static constexpr int kOffCodes = kOffV + kVSlots * kSlot;
   static constexpr int kOffUnit = kOffCodes + kConvWarps * kCSlots * kCSlotBytes;  // [kM] power of two that undoes a row's scaling
   static constexpr int kOffMPub = kOffUnit + kM * 4;      // [4 quarters][2 tile parities][32 rows] published maxima
   static constexpr int kOffBar = kOffMPub + 4 * 2 * 32 * 4;
@@ -120,10 +124,10 @@ struct Layout {
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
   static_assert(kConvWarps * kCSlots * kCSlotBytes >= 6 * kM * 4, "the epilogue's sums and maxima");
   // barriers
-  static constexpr int kBarKFull = 0;                            // [kKSlots] TMA (4 bits: conversion, kParts arrivals) -> MMA
+  static constexpr int kBarKFull = 0;                            // [kKSlots] TMA (4 bits: conversion, kFill arrivals) -> MMA
   static constexpr int kBarKEmpty = kBarKFull + kKSlots;         // [kKSlots] MMA (S of the slot's tiles done) -> TMA (conversion)
   static constexpr int kBarCFull = kBarKEmpty + kKSlots;         // [kConvWarps][kCSlots] TMA -> conversion
-  static constexpr int kBarVFull = kBarCFull + kConvWarps * kCSlots;  // [kVSlots] conversion -> MMA (kParts arrivals)
+  static constexpr int kBarVFull = kBarCFull + kConvWarps * kCSlots;  // [kVSlots] conversion -> MMA (kFill arrivals)
   static constexpr int kBarVEmpty = kBarVFull + kVSlots;         // [kVSlots] MMA (PV of the slot's tiles done) -> conversion
   static constexpr int kBarSFull = kBarVEmpty + kVSlots;         // [kSBufs] S(i) in TMEM -> softmax
   static constexpr int kBarPFull = kBarSFull + kSBufs;           // [kSBufs] P(i) in TMEM -> MMA (128 arrivals)
@@ -228,7 +232,7 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-// A conversion lane's place in an fp16 operand tile (128 tokens x 64 dims a half, 128-byte rows, 128-byte swizzle).  The
+// A conversion lane's place in a slot of fp16 operands (two halves of 64 dims, 128-byte rows, 128-byte swizzle).  The
 // lanes take 16 bytes of codes each: 16 dims of four tokens, or (4 bits) 32 dims of eight.  A store instruction's
 // eight lanes at a time have to cover eight 16-byte chunks that differ in their place within 128 bytes, which the swizzle
 // XORs with the token's last bits; the lanes of the upper 64 dims, whose chunks have the same places as the lower
@@ -246,7 +250,7 @@ struct ConvLane {
     const int c = lane % kLanes;
     dim = c * kDims;
     token = (lane / kLanes) ^ (2 * c >= kLanes ? kStep / 4 : 0);
-    row = (uint32_t)(part * kPart + token) * 128 + (2 * c >= kLanes ? kHalf : 0);
+    row = (uint32_t)(part % Layout<BITS>::kFill * kPart + token) * 128 + (2 * c >= kLanes ? Layout<BITS>::kHalf : 0);
     ch = (uint32_t)(dim % 64 / 8);
   }
   // chunk k (8 dims) of load n
@@ -261,7 +265,8 @@ template <int BITS>
 __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t item, const Maps* maps,
                                                   unsigned char* smem_raw) {
   using Lay = Layout<BITS>;
-  constexpr int kKSlots = Lay::kKSlots, kCSlots = Lay::kCSlots, kConvWarps = Lay::kConvWarps;
+  constexpr int kKSlots = Lay::kKSlots, kVSlots = Lay::kVSlots, kCSlots = Lay::kCSlots, kConvWarps = Lay::kConvWarps;
+  constexpr int kSlotTiles = Lay::kSlotTiles, kHalf = Lay::kHalf, kFill = Lay::kFill;
   constexpr int kWarpS = Lay::kWarpS, kWarpPv = Lay::kWarpPv, kWarpTmaK = Lay::kWarpTmaK;
   constexpr int kOffK = Lay::kOffK, kOffV = Lay::kOffV, kOffCodes = Lay::kOffCodes, kOffUnit = Lay::kOffUnit, kOffMPub = Lay::kOffMPub,
                 kOffBar = Lay::kOffBar;
@@ -292,7 +297,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
   int32_t t0, t1;
   piece_range(gr, it.split, t0, t1);
   const int n_tiles = t1 > t0 ? (t1 - t0 + kN - 1) / kN : 0;
-  const int n_pairs = (n_tiles + 1) / 2;  // ring slots used
+  const int n_pairs = (n_tiles + 1) / 2;
   const bool slab_ok = gr.slab_off >= 0 && gr.slab_off + gr.L_p <= p.n_hot && n_tiles > 0;
   const int32_t rbase = it.row_block * kM;
   const int64_t first_slot = gr.slab_off + t0;
@@ -328,8 +333,8 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     tma_prefetch_desc(&maps->v);
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1u;
-      if (i >= kBarVFull && i < kBarVFull + kVSlots) count = kParts;
-      if (BITS == 4 && i >= kBarKFull && i < kBarKFull + kKSlots) count = kParts;
+      if (i >= kBarVFull && i < kBarVFull + kVSlots) count = kFill;
+      if (BITS == 4 && i >= kBarKFull && i < kBarKFull + kKSlots) count = kFill;
       if (i >= kBarPFull && i < kBarPFull + kSBufs) count = kSoftmaxThreads / 2;
       if (i >= kBarPair && i < kBarPair + 4) count = 64u;
       if (i >= kBarMPub && i < kBarMPub + 8) count = 32u;
@@ -463,7 +468,8 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
 #pragma unroll
     for (int i = 0; i < kCSlots; ++i) copy_scales(i);
     for (int i = 0; slab_ok && i < n_pairs; ++i) {
-      const int c = w * kCSlots + i % kCSlots, st = i % slots;
+      const int c = w * kCSlots + i % kCSlots;
+      const int use = BITS == 8 ? i : 2 * i + part / kFill, st = use % slots;  // the slot's use, of all of the ring's
       bool ok = mbar_wait_bounded(bar(kBarCFull + c), (i / kCSlots) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;  // the abort flag is up: every other role leaves as well
@@ -472,7 +478,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
         cp_async_wait<kCSlots - 1>();
         __syncwarp();
       }
-      const uint32_t src = sC + c * Lay::kCSlotBytes, dst = ring + st * kTile;
+      const uint32_t src = sC + c * Lay::kCSlotBytes, dst = ring + st * Lay::kSlot;
       const int valid = t1 - t0 - i * kPair - part * kPart;  // tokens of the part in range, or more
       uint4 x[kPer];
       uint32_t b[kPer];  // 4 bits: their two scales
@@ -490,13 +496,15 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
             b[n] = 0u;
           }
       }
-      if (i >= slots) {
-        ok = mbar_wait_bounded(bar(empty + st), ((i / slots) - 1) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
+      const bool fills = BITS == 8 || use < n_tiles;  // (4 bits: the last two parts may have no tile)
+      if (fills && use >= slots) {
+        ok = mbar_wait_bounded(bar(empty + st), ((use / slots) - 1) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
       }
 #pragma unroll
       for (int n = 0; n < kPer; ++n) {
+        if (!fills) break;
         if constexpr (BITS == 8) {
           uint32_t y[8];
           e4m3x4_to_f16x4(x[n].x, y[0], y[1]);
@@ -520,7 +528,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
       __syncwarp();  // the warp has stored its part, and read its codes
       copy_scales(i + kCSlots);
       if (lane == 0) {
-        mbar_arrive(bar(full + st));
+        if (fills) mbar_arrive(bar(full + st));
         if (i + kCSlots < n_pairs) {
           issue_c(w, i + kCSlots);
           if (l2_ahead > 0 && i + kCSlots + l2_ahead < n_pairs)
@@ -586,11 +594,11 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
         for (int i = 0; i < n_tiles; ++i) {
           // S(i) overwrites S(i-5)/P(i-5), whose last reader is PV(i-5)
           if (i >= kSBufs && !wait(kBarPvDone, kSBufs, i - kSBufs)) break;
-          if ((i & 1) == 0 && !wait(kBarKFull, kKSlots, i >> 1)) break;
+          if (i % kSlotTiles == 0 && !wait(kBarKFull, kKSlots, i / kSlotTiles)) break;
           tc_fence_after();
           const uint32_t dS = tm + (uint32_t)((i % kSBufs) * kN);
-          const int st = (i >> 1) % kKSlots;
-          const uint64_t dk = dk0 + (uint64_t)((st * Lay::kKSlotBytes + (i & 1) * kN * 128) >> 4);  // rows of 128 bytes
+          const int st = i / kSlotTiles % kKSlots;
+          const uint64_t dk = dk0 + (uint64_t)((st * Lay::kKSlotBytes + i % kSlotTiles * kN * 128) >> 4);  // rows of 128 bytes
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)  // 8 bits: lo, the smaller, first; 4 bits: 16 dims each, four of a 64-dim half
             if (el && BITS == 4)
@@ -600,7 +608,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
                          kk > 0 ? 1u : 0u);
           if (el) {
             umma_commit(bar(kBarSFull + i % kSBufs));
-            if (i & 1) umma_commit(bar(kBarKEmpty + st));
+            if (i % kSlotTiles == kSlotTiles - 1) umma_commit(bar(kBarKEmpty + st));
           }
           __syncwarp();
           committed += 1;
@@ -610,12 +618,12 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
         // kHalf apart (leading offset), 8-token groups 1024 bytes apart (stride)
         const uint64_t dv0 = smem_desc_sw128(sV, kHalf, 1024);
         for (int i = 0; i < n_tiles; ++i) {
-          if ((i & 1) == 0 && !wait(kBarVFull, kVSlots, i >> 1)) break;
+          if (i % kSlotTiles == 0 && !wait(kBarVFull, kVSlots, i / kSlotTiles)) break;
           if (!wait(kBarPFull, kSBufs, i)) break;
           tc_fence_after();
           const uint32_t pa = tm + (uint32_t)((i % kSBufs) * kN);  // P(i): 32 columns, two tokens per column
-          const int st = (i >> 1) % kVSlots;
-          const uint64_t dv = dv0 + (uint64_t)((st * kTile + (i & 1) * (kN / 16) * 2048) >> 4);
+          const int st = i / kSlotTiles % kVSlots;
+          const uint64_t dv = dv0 + (uint64_t)((st * Lay::kSlot + i % kSlotTiles * (kN / 16) * 2048) >> 4);
 #pragma unroll
           for (int ks = 0; ks < kN / 16; ++ks)
             if (el)
@@ -623,7 +631,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
                           (i > 0 || ks > 0) ? 1u : 0u);
           if (el) {
             umma_commit(bar(kBarPvDone + i % kSBufs));
-            if (i & 1) umma_commit(bar(kBarVEmpty + st));
+            if (i % kSlotTiles == kSlotTiles - 1) umma_commit(bar(kBarVEmpty + st));
           }
           __syncwarp();
           committed += 1;
