@@ -169,11 +169,16 @@ granikv_status cuda_status(cudaError_t e) { return e == cudaSuccess ? GRANIKV_OK
 
 bool has_device(const granikv_ctx* c) { return c && !c->cfg.host_only && c->d_ring; }
 
+// Whether the tensor-core kernels of the packed caches have this shape (the COLD one up to eight query heads a KV head).
+bool packed_tc(const granikv_config& cfg, int32_t bits) {
+  return cfg.dtype == GRANIKV_DTYPE_BF16 && (cfg.head_dim == 128 || (bits == 4 && cfg.head_dim == 64));
+}
+
 // Which prefix implementation serves a group of this shape and backend.
 int32_t prefix_impl_for(const granikv_ctx* c, int32_t backend) {
   if (c->packed_row) {
-    const bool dense = backend == GRANIKV_BACKEND_DENSE && c->cfg.dtype == GRANIKV_DTYPE_BF16 &&
-                       c->cfg.head_dim == 128 && (c->has_tmaps || c->cfg.host_only);
+    const bool dense = backend == GRANIKV_BACKEND_DENSE && packed_tc(c->cfg, c->packed_bits) &&
+                       (c->has_tmaps || c->cfg.host_only);
     return dense ? kImplPackedDense : kImplPackedGeneric;
   }
   if (c->cfg.dtype == GRANIKV_DTYPE_BF16 && c->cfg.head_dim == 128) {
@@ -193,8 +198,8 @@ bool runs_alone(int32_t impl) { return impl == kImplGeneric || impl == kImplDens
 
 // Which kernel attends the COLD suffix.
 int32_t suffix_impl_for(const granikv_ctx* c) {
+  if (c->packed_row) return packed_tc(c->cfg, c->packed_bits) && c->g <= 8 ? kImplPackedSuffix : kImplPackedGeneric;
   const bool mma = c->cfg.dtype == GRANIKV_DTYPE_BF16 && c->cfg.head_dim == 128 && c->g <= 8;
-  if (c->packed_row) return mma ? kImplPackedSuffix : kImplPackedGeneric;
   return mma ? kImplSuffixMma : kImplGeneric;
 }
 
@@ -601,19 +606,20 @@ granikv_status create_impl(const granikv_config* cfg, int32_t bits, granikv_ctx*
     if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&c->aux, cudaStreamNonBlocking);
     if (e == cudaSuccess) e = cudaEventCreateWithFlags(&c->ev_fork, cudaEventDisableTiming);
     if (e == cudaSuccess) e = cudaEventCreateWithFlags(&c->ev_join, cudaEventDisableTiming);
-    if (e == cudaSuccess && cfg->dtype == GRANIKV_DTYPE_BF16 && cfg->head_dim == 128 && c->cc_major == 10) {
+    const bool tc = bits ? packed_tc(*cfg, bits) : cfg->dtype == GRANIKV_DTYPE_BF16 && cfg->head_dim == 128;
+    if (e == cudaSuccess && tc && c->cc_major == 10) {
       if (bits) c->packed_maps.resize(cfg->n_layers);
       else c->tmap_k.resize(cfg->n_layers), c->tmap_v.resize(cfg->n_layers);
       bool ok = true;
       for (int32_t l = 0; l < cfg->n_layers && ok; ++l) {
         if (bits) {
           PackedMaps& m = c->packed_maps[l];
-          const int64_t codes = bits == 8 ? (int64_t)cfg->n_kv * 128 : kv4_scales_at(cfg->n_kv, 128);
+          const int32_t head = cfg->head_dim * bits / 8;
+          const int64_t codes = (int64_t)cfg->n_kv * head;
           auto encode = [&](CUtensorMap* to, void* pool, int32_t bytes, int32_t slots, bool swizzle) {
             return encode_packed_map(to, pool, cfg->n_slots, c->packed_row, codes, bytes, slots, swizzle);
           };
-          ok = bits == 8 ? encode(&m.k, c->kpool[l], 128, kDenseTile, true) && encode(&m.v, c->vpool[l], 128, kKv8VBox, false)
-                         : encode(&m.k, c->kpool[l], 64, kKv8VBox, false) && encode(&m.v, c->vpool[l], 64, kKv8VBox, false);
+          ok = encode(&m.k, c->kpool[l], head, bits == 8 ? kDenseTile : kKv8VBox, bits == 8) && encode(&m.v, c->vpool[l], head, kKv8VBox, false);
           continue;
         }
         ok = ((uintptr_t)c->kpool[l] % 16 == 0) && ((uintptr_t)c->vpool[l] % 16 == 0) &&

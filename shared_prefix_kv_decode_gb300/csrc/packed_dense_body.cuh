@@ -1,5 +1,5 @@
 // packed_dense_body.cuh -- dense prefix backend over the 8- or 4-bit cache on the 5th-generation tensor cores
-// (tcgen05/TMEM), head_dim 128, bf16 q.  (8 bits first; what 4 bits change stands at the end.)
+// (tcgen05/TMEM), head_dim 128 (4 bits: or 64), bf16 q.  (8 bits first; what 4 bits change stands at the end.)
 //
 // One CTA takes one (prefix group, KV head j, 128-row block, L_p piece), as the 16-bit dense kernel:
 // rows are the group's (request, head-in-group) pairs of KV head j.  For each 64-token tile i, one
@@ -81,7 +81,6 @@ using pks::block_barrier;
 using pks::regs_down;
 using pks::regs_up;
 
-constexpr int kD = 128;
 constexpr int kM = kDenseRows;                // 128 query rows per CTA
 constexpr int kN = kKv8Block;                 // 64 tokens per tile
 constexpr int kPair = kDenseTile;             // 128 tokens: what is loaded at a time
@@ -91,10 +90,9 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
 constexpr int kWarpConv = 8, kParts = 4;
 constexpr int kPart = kPair / kParts;         // tokens that one warp converts at a time
-constexpr int kCodes = kPair * kD;            // 8 bits: codes of 128 tokens, 16 KB
-constexpr int kPartCodes = kPart * kD;        // 4 KB
-template <int BITS>
+template <int BITS, int D>
 struct Layout {
+  static_assert(D == 128 || (BITS == 4 && D == 64), "head_dim");
   // 8 bits: kParts warps convert V.  4 bits: as many convert K, before them.  (One more warp, for the suffix body's producers.)
   static constexpr int kConvWarps = BITS == 8 ? kParts : 2 * kParts;
   static constexpr int kWarpS = kWarpConv + kConvWarps, kWarpPv = kWarpS + 1, kWarpTmaK = kWarpS + 2;
@@ -106,13 +104,14 @@ struct Layout {
   static constexpr int kSlotTiles = BITS == 8 ? 2 : 1;
   static constexpr int kFill = kParts * kSlotTiles / 2;   // warps that fill a slot
   static constexpr int kHalf = kSlotTiles * kN * 128;     // one 64-dim half of a slot
-  static constexpr int kSlot = 2 * kHalf;                 // 32 KB or 16
+  static constexpr int kSlot = D / 64 * kHalf;            // 32 KB or (4 bits) 16, heads of 64: 8
   static constexpr int kVSlots = BITS == 8 ? 3 : 5;       // slots of the V ring (fp16)
   static constexpr int kKSlots = BITS == 8 ? 4 : 5;       // slots of the K ring (codes of 128 tokens, 4 bits: fp16)
-  static constexpr int kKSlotBytes = BITS == 8 ? kCodes : kSlot;
+  static constexpr int kKSlotBytes = BITS == 8 ? kPair * D : kSlot;
   static constexpr int kCSlots = BITS == 8 ? 4 : 3;       // slots of each conversion warp's ring (codes, 4 bits: and scales)
-  static constexpr int kHead = kD * BITS / 8;             // bytes of a head's codes
-  static constexpr int kCSlotBytes = BITS == 8 ? kPartCodes : kPart * (kHead + kD / kKv4Group);
+  static constexpr int kHead = D * BITS / 8;              // bytes of a head's codes
+  static constexpr int kScale = D / kKv4Group;            // 4 bits: of its scales
+  static constexpr int kCSlotBytes = kPart * (kHead + (BITS == 8 ? 0 : kScale));
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kOffK + kKSlots * kKSlotBytes;
   static constexpr int kOffCodes = kOffV + kVSlots * kSlot;
@@ -145,7 +144,7 @@ struct Maps {
 };
 constexpr uint32_t kTmemCols = 512;           // S/P buffers at 0, 64, 128, 192, 256; Q (hi, lo) at 320; O at 384
 constexpr uint32_t kColQ = kSBufs * kN, kColO = 384;
-static_assert(kColQ + 2 * kD / 4 <= kColO && kColO + kD <= kTmemCols, "TMEM columns");
+static_assert(kColQ + 128 / 2 <= kColO && kColO + 128 <= kTmemCols, "TMEM columns");
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;     // log2 of the largest growth tolerated in P
 constexpr float kShift = 7.0f;                // log2 of the factor that P carries
@@ -238,10 +237,11 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 // XORs with the token's last bits; the lanes of the upper 64 dims, whose chunks have the same places as the lower
 // ones', take the token whose bits differ by one step: 1, or 2 (where the bit 1 already tells two tokens apart).
 // (With the stores of one half in another order, by a branch, a 4-bit tile took 8 % longer.)
-template <int BITS>
+template <int BITS, int D>
 struct ConvLane {
+  using Lay = Layout<BITS, D>;
   static constexpr int kDims = 128 / BITS;             // 16 or 32
-  static constexpr int kLanes = kD / kDims;            // of a token: 8 or 4
+  static constexpr int kLanes = D / kDims;             // of a token: 8 or 4, heads of 64: 2
   static constexpr int kStep = 32 / kLanes;            // tokens of a load: 4 or 8
   static constexpr int kPer = kPart / kStep;           // loads of a part
   int dim, token;                                      // first dim; token of load 0
@@ -249,8 +249,8 @@ struct ConvLane {
   __device__ __forceinline__ ConvLane(int part, int lane) {
     const int c = lane % kLanes;
     dim = c * kDims;
-    token = (lane / kLanes) ^ (2 * c >= kLanes ? kStep / 4 : 0);
-    row = (uint32_t)(part % Layout<BITS>::kFill * kPart + token) * 128 + (2 * c >= kLanes ? Layout<BITS>::kHalf : 0);
+    token = (lane / kLanes) ^ (dim >= 64 ? kStep / 4 : 0);
+    row = (uint32_t)(part % Lay::kFill * kPart + token) * 128 + (dim >= 64 ? Lay::kHalf : 0);
     ch = (uint32_t)(dim % 64 / 8);
   }
   // chunk k (8 dims) of load n
@@ -260,11 +260,11 @@ struct ConvLane {
   }
 };
 
-// Prefix work item `item` (one CTA) on `smem_raw` (at least Layout<BITS>::kSmemBytes), run by Layout<BITS>::kThreads threads.
-template <int BITS>
+// Prefix work item `item` (one CTA) on `smem_raw` (at least Layout<BITS, D>::kSmemBytes), run by Layout<BITS, D>::kThreads threads.
+template <int BITS, int D>
 __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t item, const Maps* maps,
                                                   unsigned char* smem_raw) {
-  using Lay = Layout<BITS>;
+  using Lay = Layout<BITS, D>;
   constexpr int kKSlots = Lay::kKSlots, kVSlots = Lay::kVSlots, kCSlots = Lay::kCSlots, kConvWarps = Lay::kConvWarps;
   constexpr int kSlotTiles = Lay::kSlotTiles, kHalf = Lay::kHalf, kFill = Lay::kFill;
   constexpr int kWarpS = Lay::kWarpS, kWarpPv = Lay::kWarpPv, kWarpTmaK = Lay::kWarpTmaK;
@@ -305,8 +305,8 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
   // slot contents: tokens kPair * i .. of the piece
   auto issue_k = [&](int i) {
     const int st = i % kKSlots;
-    mbar_arrive_expect_tx(bar(kBarKFull + st), kCodes);
-    tma_load_2d(sK + st * kCodes, &maps->k, j * kD, (int32_t)(first_slot + (int64_t)i * kPair), bar(kBarKFull + st));
+    mbar_arrive_expect_tx(bar(kBarKFull + st), Lay::kKSlotBytes);
+    tma_load_2d(sK + st * Lay::kKSlotBytes, &maps->k, j * D, (int32_t)(first_slot + (int64_t)i * kPair), bar(kBarKFull + st));
   };
   // conversion warp w's part of V's (4 bits, w < kParts: K's) slot contents i
   auto issue_c = [&](int w, int i) {
@@ -362,10 +362,11 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
   // Q: the two softmax warps of a row quarter take half of their rows' dims each, agree on each row's
   // power of two through shared memory, and split the elements into hi and lo, four to a word; rows
   // past the group are 0
-  uint32_t qw[32];
+  constexpr int kQw = D / 4;  // words of half a row
+  uint32_t qw[kQw];
   float* part = reinterpret_cast<float*>(smem + kOffMPub);  // [2][kM], used for the maxima of tiles later
   // the scales of tile i; a softmax warp's first ones are on their way with its rows
-  const int64_t scale_at = BITS == 8 ? (int64_t)p.n_kv * kD + 4 * j : kv4_units_at(p.n_kv, kD) + j;
+  const int64_t scale_at = BITS == 8 ? (int64_t)p.n_kv * D + 4 * j : kv4_units_at(p.n_kv, D) + j;
   using Scale = std::conditional_t<BITS == 8, float, uint8_t>;  // as it stands in the row
   Scale ks{}, vs{};
   auto load_scales = [&](int i) {
@@ -390,10 +391,10 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
         if (lane + 32 * k < n_tiles) v_bits[k] = v_scale_bits(lane + 32 * k);
     }
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                      ((int64_t)req * p.n_q + h) * kD + qhalf * (kD / 2));
+                                                      ((int64_t)req * p.n_q + h) * D + qhalf * (D / 2));
     float amax = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kQw / 4; ++k) {
       const uint4 x = have ? src[k] : make_uint4(0u, 0u, 0u, 0u);
       qw[4 * k] = x.x;
       qw[4 * k + 1] = x.y;
@@ -401,7 +402,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
       qw[4 * k + 3] = x.w;
     }
 #pragma unroll
-    for (int k = 0; k < 32; ++k) amax = fmaxf(amax, bf16x2_finite_max(qw[k]));
+    for (int k = 0; k < kQw; ++k) amax = fmaxf(amax, bf16x2_finite_max(qw[k]));
     part[qhalf * kM + qrow] = amax;
   }
   tc_fence_before();
@@ -414,11 +415,13 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     if (qhalf == 0) units[qrow] = unit;
     if constexpr (BITS == 4) {
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
+      for (int k = 0; k < kQw; ++k) {
         const __half2 x = q_no_inf(f16x2_of(qw[k], f));
         qw[k] = *reinterpret_cast<const uint32_t*>(&x);
       }
-      GRANIKV_TMEM_ST32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColQ + qhalf * 32, qw);
+      const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColQ + qhalf * kQw;
+      if constexpr (D == 128) GRANIKV_TMEM_ST32(at, qw);
+      else tmem_st16(at, qw);
       tmem_wait_st();
     } else {
     // in fp16 pairs: below 2^8 with 8 significant bits they are exact there down to 2^-17
@@ -448,7 +451,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     const int w = warp - kWarpConv;
     const int part = w % kParts;
     const bool to_k = BITS == 4 && w < kParts;
-    using Conv = ConvLane<BITS>;
+    using Conv = ConvLane<BITS, D>;
     constexpr int kPer = Conv::kPer;
     const Conv cl(part, lane);
     const uint32_t ring = to_k ? sK : sV;
@@ -456,12 +459,16 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     int issued = slab_ok ? min(n_pairs, kCSlots) : 0, seen = 0;
     // 4 bits: the scales of contents i, a token a lane (zeros past the piece's end); a group for every i
     const uint8_t* scale_src = static_cast<const uint8_t*>(to_k ? p.kpool : p.vpool) + (first_slot + part * kPart + lane) * p.packed_row +
-                               kv4_scales_at(p.n_kv, kD) + j * (kD / kKv4Group);
+                               kv4_scales_at(p.n_kv, D) + j * Lay::kScale;
     auto copy_scales = [&](int i) {
       if constexpr (BITS == 4) {
-        const uint32_t dst = sC + (w * kCSlots + i % kCSlots) * Lay::kCSlotBytes + kPart * Lay::kHead + lane * 8;
+        const uint32_t dst = sC + (w * kCSlots + i % kCSlots) * Lay::kCSlotBytes + kPart * Lay::kHead + lane * Lay::kScale;
         const bool in = t0 + i * kPair + part * kPart + lane < t1;
-        if (slab_ok && i < n_pairs) cp_async8(dst, in ? scale_src + (int64_t)i * kPair * p.packed_row : scale_src, in ? 8 : 0);
+        if (slab_ok && i < n_pairs) {
+          const uint8_t* src = in ? scale_src + (int64_t)i * kPair * p.packed_row : scale_src;
+          if constexpr (D == 128) cp_async8(dst, src, in ? 8 : 0);
+          else cp_async4(dst, src, in ? 4 : 0);
+        }
         cp_async_commit();
       }
     };
@@ -486,7 +493,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
       for (int n = 0; n < kPer; ++n) {
         const uint32_t t = (uint32_t)(cl.token + n * Conv::kStep);
         x[n] = lds128(src + t * Lay::kHead + cl.dim * BITS / 8);
-        if constexpr (BITS == 4) b[n] = lds16(src + kPart * Lay::kHead + t * 8 + cl.dim / 16);
+        if constexpr (BITS == 4) b[n] = lds16(src + kPart * Lay::kHead + t * Lay::kScale + cl.dim / 16);
       }
       if (valid < kPart) {  // 0 * whatever lies past the piece must not reach O
 #pragma unroll
@@ -560,7 +567,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
           break;
         issue_k(i);
         if (l2_ahead > 0 && i + l2_ahead < n_pairs)
-          tma_prefetch_l2_2d(&maps->k, j * kD, (int32_t)(first_slot + (int64_t)(i + l2_ahead) * kPair));
+          tma_prefetch_l2_2d(&maps->k, j * D, (int32_t)(first_slot + (int64_t)(i + l2_ahead) * kPair));
         issued = i + 1;
       }
       // never leave with a copy in flight
@@ -581,7 +588,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     // more than these 128x64x32 products take.
     if (!*abort_flag) {
       constexpr uint32_t idS = idesc_fmt0_f32(kM, kN, false);
-      constexpr uint32_t idO = idesc_fmt0_f32(kM, kD, true);
+      constexpr uint32_t idO = idesc_fmt0_f32(kM, D, true);
       const bool el = elect_one();
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       auto wait = [&](int b, int slots, int i) {
@@ -600,7 +607,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
           const int st = i / kSlotTiles % kKSlots;
           const uint64_t dk = dk0 + (uint64_t)((st * Lay::kKSlotBytes + i % kSlotTiles * kN * 128) >> 4);  // rows of 128 bytes
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)  // 8 bits: lo, the smaller, first; 4 bits: 16 dims each, four of a 64-dim half
+          for (int kk = 0; kk < (BITS == 8 ? 8 : D / 16); ++kk)  // 8 bits: lo, the smaller, first; 4 bits: 16 dims each, four of a 64-dim half
             if (el && BITS == 4)
               umma_f16_ts(dS, tm + kColQ + kk * 8, dk + (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
             else if (el)
@@ -756,7 +763,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
           tc_fence_after();
           const float alpha = m_prev == m_i ? 1.f : ex2_approx(m_prev - m_i);
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
+          for (int c = 0; c < D / 16; ++c) {
             uint32_t x[16];
             const uint32_t ta = tmem + lane_off + kColO + c * 16;
             tmem_ld16(ta, x);
@@ -850,16 +857,16 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
         rec = -1;
       }
       const float inv = 1.f / lt, unit = ex2_approx(m_used - kShift - top);  // (a tile has a valid token)
-      uint32_t u[2][32];
-      GRANIKV_TMEM_LD32(tmem + lane_off + kColO + half * 64, u[0]);
-      GRANIKV_TMEM_LD32(tmem + lane_off + kColO + half * 64 + 32, u[1]);
+      uint32_t u[D / 64][32];
+      GRANIKV_TMEM_LD32(tmem + lane_off + kColO + half * (D / 2), u[0]);
+      if constexpr (D == 128) GRANIKV_TMEM_LD32(tmem + lane_off + kColO + half * 64 + 32, u[1]);
       tmem_wait_ld();
       // every lane stores its half row, a whole 32-byte sector at a time
       if (rec >= 0) {
         const uint64_t keep = l2_policy_keep();
-        float* dst = p.rec_o + ((int64_t)rec * p.n_q + h) * kD + half * 64;
+        float* dst = p.rec_o + ((int64_t)rec * p.n_q + h) * D + half * (D / 2);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < D / 16; ++c) {
           float x[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(u[c >> 2][(c & 3) * 8 + k]) * inv * unit;

@@ -1,7 +1,7 @@
 // packed_suffix_body.cuh -- COLD suffix partial attention over the 8- or 4-bit cache: bulk-copy gather of
 // packed rows, warp-level fp16 tensor cores.
 //
-// Shape: head_dim 128, bf16 q, g = n_q/n_kv <= 8.  A consumer warp owns one KV head of one request
+// Shape: head_dim 128 (4 bits: or 64, with half of all sums over it below), bf16 q, g = n_q/n_kv <= 8.  A consumer warp owns one KV head of one request
 // segment; tokens are the MMA's M dimension, the g query heads its N dimension (8 columns):
 //     S^T[16 tok x 8] = K[16 tok x 128] . Q^T[128 x 8]       (8 mma.m16n8k16, fp16)
 //     O^T[128 x 8]   += V^T[128 x 16 tok] . P^T[16 tok x 8]  (8 mma.m16n8k16, fp16)
@@ -52,7 +52,6 @@ namespace granikv {
 namespace pks {
 namespace {
 
-constexpr int kD = 128;
 constexpr int kTile = 16;                          // tokens per tile (MMA M)
 constexpr int kWarps = 8;                          // consumer warps: KV heads per CTA
 constexpr int kProducers = 8;                      // producer warps: two of a tile's rows each
@@ -61,12 +60,13 @@ constexpr int kThreads = (kWarps + kProducers) * 32;
 constexpr int kSegSmem = 256;                      // segment descriptors staged in shared memory
 // Packed rows of eight heads in shared memory, 16 modulo 32 bytes apart: the eight rows that an ldmatrix reads lie in
 // eight different 16-byte bank groups.  8 bits: 1,056 bytes, 4 bits: 592.  The stages fill what shared memory there is.
-template <int BITS>
+template <int BITS, int D>
 struct Layout {
-  static constexpr int kCodes = kD * BITS / 8;     // bytes of a head's codes
-  static constexpr int kRowMax = BITS == 8 ? kWarps * (kD + 4) : (int)kv4_row_bytes(kWarps, kD);
+  static_assert(D == 128 || (BITS == 4 && D == 64), "head_dim");
+  static constexpr int kCodes = D * BITS / 8;      // bytes of a head's codes
+  static constexpr int kRowMax = BITS == 8 ? kWarps * (D + 4) : (int)kv4_row_bytes(kWarps, D);
   static constexpr int kRowStride = kRowMax + (kRowMax % 32 ? 0 : 16);
-  static constexpr int kStages = BITS == 8 ? 6 : 11;
+  static constexpr int kStages = BITS == 8 ? 6 : D == 128 ? 11 : 20;
   static constexpr int kTileBytes = kTile * kRowStride;
   static constexpr int kStageBytes = 2 * kTileBytes;  // K + V: 34,304 B (8 bits)
   static constexpr int kOffSlots = kStages * kStageBytes;
@@ -83,7 +83,7 @@ static_assert(kSuffixMaxCtaTokens <= 4096, "the row sum's range");
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // Source of the rows of masked tokens (zero-initialised at module load, never written).
-__device__ __align__(128) uint4 g_zero_row[Layout<8>::kRowMax / 16];
+__device__ __align__(128) uint4 g_zero_row[Layout<8, 128>::kRowMax / 16];
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t mbar) {
   asm volatile(
@@ -136,13 +136,13 @@ __device__ __forceinline__ void scale_pairs(uint32_t a, uint32_t b, uint32_t sel
 }
 
 // One token-CTA `cta` of the suffix work list, for KV-head group `group`, on `smem` (at least
-// Layout<BITS>::kSmemBytes, 128-byte aligned), run by kThreads or more threads (the extra warps only take
+// Layout<BITS, D>::kSmemBytes, 128-byte aligned), run by kThreads or more threads (the extra warps only take
 // part in the set-up barriers).  kSplitRegs: the block has 20 warps of 96 registers (as the dense body's), of which the
 // consumers go on with 128 and the others with 72.
-template <int BITS, bool kSplitRegs>
+template <int BITS, int D, bool kSplitRegs>
 __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const int32_t* __restrict__ cta_begin, int cta,
                                                 int group, unsigned char* smem) {
-  using Lay = Layout<BITS>;
+  using Lay = Layout<BITS, D>;
   constexpr int kStages = Lay::kStages, kTileBytes = Lay::kTileBytes, kStageBytes = Lay::kStageBytes, kRowStride = Lay::kRowStride;
   constexpr int kOffSlots = Lay::kOffSlots, kOffSegs = Lay::kOffSegs, kOffBar = Lay::kOffBar;
   const int warp = threadIdx.x >> 5;
@@ -154,7 +154,7 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
   const int nh = min(kWarps, p.n_kv - j0);            // heads in the group
   // the parts of a row that the group reads, each from a 16-byte boundary on and of a multiple of 16 bytes
   const uint32_t code_bytes = (uint32_t)nh * Lay::kCodes;
-  const uint32_t scale_bytes = BITS == 8 ? (uint32_t)(nh + 3) / 4 * 16 : (uint32_t)(nh + 1) / 2 * 16;
+  const uint32_t scale_bytes = BITS == 8 ? (uint32_t)(nh + 3) / 4 * 16 : (uint32_t)(nh * (D / kKv4Group) + 15) / 16 * 16;
   const uint32_t unit_bytes = BITS == 8 ? 0u : 16u;
   const uint32_t row_bytes = code_bytes + scale_bytes + unit_bytes;
   const uint32_t sbase = smem_u32(smem);
@@ -213,8 +213,8 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
     const bool is_v = (lane & (2 * kRowsEach - 1)) >= kRowsEach;
     const uint8_t* pool = static_cast<const uint8_t*>(is_v ? p.vpool : p.kpool);
     const int64_t code_off = (int64_t)j0 * Lay::kCodes;
-    const int64_t scale_off = BITS == 8 ? (int64_t)p.n_kv * kD + 4 * j0 : kv4_scales_at(p.n_kv, kD) + j0 * (kD / kKv4Group);
-    const int64_t unit_off = kv4_units_at(p.n_kv, kD) + j0 / 16 * 16;
+    const int64_t scale_off = BITS == 8 ? (int64_t)p.n_kv * D + 4 * j0 : kv4_scales_at(p.n_kv, D) + j0 * (D / kKv4Group);
+    const int64_t unit_off = kv4_units_at(p.n_kv, D) + j0 / 16 * 16;
     const bool whole = p.n_kv <= kWarps;  // codes and scales are one run of bytes
     const int r = part * kRowsEach + (lane & (kRowsEach - 1));
     int n = 0;    // tiles issued
@@ -281,14 +281,15 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
   // Q^T as B fragments in the order of the K codes: k-step i takes dims 16 i + 4 c + {0, 1} and {2, 3}
   // of column r (query head j*g + r), 4 bits: 32 (i / 2) + 8 c + 4 (i % 2) + {0, 1} and {2, 3}; the next segment's rows
   // are loaded one segment ahead
-  uint32_t qn[16];
+  constexpr int kQ = D / 8;  // words
+  uint32_t qn[kQ];
   auto load_q = [&](int sg) {
     if (sg < n_seg && r < g) {
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + ((int64_t)seg_at(sg).b * p.n_q + j * g + r) * kD;
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + ((int64_t)seg_at(sg).b * p.n_q + j * g + r) * D;
       if constexpr (BITS == 8) {
         const uint2* qrow = reinterpret_cast<const uint2*>(q);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kQ / 2; ++i) {
           const uint2 x = qrow[4 * i + c];
           qn[2 * i] = x.x;
           qn[2 * i + 1] = x.y;
@@ -296,7 +297,7 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
       } else {
         const uint4* qrow = reinterpret_cast<const uint4*>(q);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kQ / 4; ++i) {
           const uint4 x = qrow[4 * i + c];
           qn[4 * i] = x.x;
           qn[4 * i + 1] = x.y;
@@ -306,33 +307,34 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) qn[i] = 0u;
+      for (int i = 0; i < kQ; ++i) qn[i] = 0u;
     }
   };
   load_q(0);
   const uint32_t head_off = (uint32_t)warp * Lay::kCodes;
-  const uint32_t scale_at = code_bytes + (BITS == 8 ? 4 : kD / kKv4Group) * (uint32_t)warp;
+  const uint32_t scale_at = code_bytes + (BITS == 8 ? 4 : D / kKv4Group) * (uint32_t)warp;
   const uint32_t unit_at = code_bytes + scale_bytes + (uint32_t)(j0 % 16 + warp);
   int tile = 0;  // tiles consumed so far
   for (int sg = 0; sg < n_seg; ++sg) {
     const DevSuffixItem seg = seg_at(sg);
-    uint32_t qf[16];
+    uint32_t qf[kQ];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) qf[i] = qn[i];
+    for (int i = 0; i < kQ; ++i) qf[i] = qn[i];
     load_q(sg + 1);
     float unit;
-    q_to_f16<16>(qf, unit);
+    q_to_f16<kQ>(qf, unit);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < kQ; ++i) {
       const __half2 x = q_no_inf(*reinterpret_cast<const __half2*>(&qf[i]));
       qf[i] = *reinterpret_cast<const uint32_t*>(&x);
     }
     const float f0 = __shfl_sync(0xffffffffu, unit, 8 * c) * p.scale_log2;
     const float f1 = __shfl_sync(0xffffffffu, unit, 8 * c + 4) * p.scale_log2;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    float o[8][4];
+    constexpr int kTiles = D / 16;  // m-tiles of O^T
+    float o[kTiles][4];
 #pragma unroll
-    for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
+    for (int mt = 0; mt < kTiles; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
 
     bool ok = true;
     // V tiles from token t on: one running-max update for both, and their products side by side, so
@@ -344,7 +346,7 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
       const uint32_t frag = head_off + ((lane & 7) + (mi & 1) * 8) * kRowStride + (mi >> 1) * 16;
       uint32_t at[V];  // this lane's ldmatrix row of each tile
       float sa[V], sb[V], la[V], lb[V], s[V][4], s2[V][4];
-      uint2 ka[V], kb[V];  // 4 bits: the K scales of tokens r and r + 8
+      uint32_t ka[V][D / 64], kb[V][D / 64];  // 4 bits: the K scales of tokens r and r + 8
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int st = (tile + v) % kStages;
@@ -366,8 +368,13 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
           la[v] = (float)up[kTileBytes];
           lb[v] = (float)up[kTileBytes + 8 * kRowStride];
           const unsigned char* ksp = smem + st * kStageBytes + r * kRowStride + scale_at;
-          ka[v] = *reinterpret_cast<const uint2*>(ksp);
-          kb[v] = *reinterpret_cast<const uint2*>(ksp + 8 * kRowStride);
+          if constexpr (D == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(ksp), y = *reinterpret_cast<const uint2*>(ksp + 8 * kRowStride);
+            ka[v][0] = x.x, ka[v][1] = x.y, kb[v][0] = y.x, kb[v][1] = y.y;
+          } else {
+            ka[v][0] = *reinterpret_cast<const uint32_t*>(ksp);
+            kb[v][0] = *reinterpret_cast<const uint32_t*>(ksp + 8 * kRowStride);
+          }
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[v][e] = s2[v][e] = 0.f;
@@ -376,15 +383,15 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
       if constexpr (BITS == 4) {
         const uint32_t sel = c & 2 ? 0x3311u : 0x2200u;  // of the scales of dims 32 i .., those of this lane's 16, twice
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < D / 64; ++i) {
           uint32_t w[V][4];
 #pragma unroll
           for (int v = 0; v < V; ++v) ldsm_x4(at[v] + i * 32, w[v][0], w[v][1], w[v][2], w[v][3]);
 #pragma unroll
           for (int v = 0; v < V; ++v) {
             uint32_t fa[2], fb[2];
-            scale_pairs(i ? ka[v].y : ka[v].x, 0u, sel, fa[0], fa[1]);
-            scale_pairs(i ? kb[v].y : kb[v].x, 0u, sel, fb[0], fb[1]);
+            scale_pairs(ka[v][i], 0u, sel, fa[0], fa[1]);
+            scale_pairs(kb[v][i], 0u, sel, fb[0], fb[1]);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {  // 32 dims
               uint32_t ya[4], yb[4];
@@ -453,7 +460,7 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
         l0 = l0 * half0 * half0;
         l1 = l1 * half1 * half1;
 #pragma unroll
-        for (int mt = 0; mt < 8; ++mt) {
+        for (int mt = 0; mt < kTiles; ++mt) {
           o[mt][0] *= al0;
           o[mt][2] *= al0;
           o[mt][1] *= al1;
@@ -481,7 +488,7 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
       if constexpr (BITS == 4) {
         const uint32_t sel = r & 4 ? 0x7351u : 0x6240u;  // of two tokens' scales of 64 dims, those of this lane's 16, side by side
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < D / 64; ++i) {
           uint32_t w[V][4];
 #pragma unroll
           for (int v = 0; v < V; ++v) ldsm_x4_t(at[v] + kTileBytes + i * 32, w[v][0], w[v][1], w[v][2], w[v][3]);
@@ -555,20 +562,20 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
     const float inv0 = l0 == 0.f ? 0.f : kUnit / l0;
     const float inv1 = l1 == 0.f ? 0.f : kUnit / l1;
     const int hq0 = j * g + h0;
-    float* dst0 = p.rec_o + ((int64_t)rec * p.n_q + hq0) * kD + (BITS == 8 ? 2 : 4) * r;
+    float* dst0 = p.rec_o + ((int64_t)rec * p.n_q + hq0) * D + (BITS == 8 ? 2 : 4) * r;
     const bool w0 = h0 < g, w1 = h0 + 1 < g;
     const uint64_t keep = l2_policy_keep();
     if constexpr (BITS == 8) {
 #pragma unroll
-      for (int mt = 0; mt < 8; ++mt) {
+      for (int mt = 0; mt < kTiles; ++mt) {
         if (w0) st_record2(dst0 + mt * 16, o[mt][0] * inv0, o[mt][2] * inv0, keep);
-        if (w1) st_record2(dst0 + kD + mt * 16, o[mt][1] * inv1, o[mt][3] * inv1, keep);
+        if (w1) st_record2(dst0 + D + mt * 16, o[mt][1] * inv1, o[mt][3] * inv1, keep);
       }
     } else {
 #pragma unroll
-      for (int mt = 0; mt < 8; mt += 2) {
+      for (int mt = 0; mt < kTiles; mt += 2) {
         if (w0) st_record4(dst0 + mt * 16, make_float4(o[mt][0] * inv0, o[mt][2] * inv0, o[mt + 1][0] * inv0, o[mt + 1][2] * inv0), keep);
-        if (w1) st_record4(dst0 + kD + mt * 16, make_float4(o[mt][1] * inv1, o[mt][3] * inv1, o[mt + 1][1] * inv1, o[mt + 1][3] * inv1), keep);
+        if (w1) st_record4(dst0 + D + mt * 16, make_float4(o[mt][1] * inv1, o[mt][3] * inv1, o[mt + 1][1] * inv1, o[mt + 1][3] * inv1), keep);
       }
     }
     if (lane < 4) {

@@ -396,17 +396,19 @@ def test_decode_matches_64_bit(cuda_ok, n_q, n_kv, d, dtype):
 
 
 @pytest.mark.parametrize("L_p", [1, 15, 63, 64, 65, 127, 128, 129, 300, 1000])
-def test_decode_prefix_lengths(cuda_ok, L_p):
-    rng = np.random.default_rng(L_p)
-    c = Kv4(rng, n_q=32, n_kv=8, d=128, dtype="bf16", prefixes=[L_p], of=[0, 0], lens=[0, 3], slots_before=L_p % 7)
+@pytest.mark.parametrize("d", [128, 64])
+def test_decode_prefix_lengths(cuda_ok, L_p, d):
+    rng = np.random.default_rng([L_p, d])
+    c = Kv4(rng, n_q=32, n_kv=8, d=d, dtype="bf16", prefixes=[L_p], of=[0, 0], lens=[0, 3], slots_before=L_p % 7)
     c.check(*c.decode(), f"L_p {L_p}")
 
 
 @pytest.mark.parametrize("L_p", [640, 777, 2048, 5000])
-def test_decode_long_prefix_pieces(cuda_ok, L_p):
+@pytest.mark.parametrize("d", [128, 64])
+def test_decode_long_prefix_pieces(cuda_ok, L_p, d):
     """Few CTAs, so that a piece has many tiles: its rings and buffers come round again and again."""
-    rng = np.random.default_rng(L_p)
-    c = Kv4(rng, n_q=64, n_kv=8, d=128, dtype="bf16", prefixes=[L_p], of=[0] * 160, lens=[0] * 160)
+    rng = np.random.default_rng([L_p, d])
+    c = Kv4(rng, n_q=64, n_kv=8, d=d, dtype="bf16", prefixes=[L_p], of=[0] * 160, lens=[0] * 160)
     assert c.ctx.dispatch(c.batch).groups()[0]["n_splits"] <= 2
     o, lse = c.decode()
     rows = [0, 1, 15, 16, 17, 80, 158, 159]
@@ -417,23 +419,25 @@ def test_decode_long_prefix_pieces(cuda_ok, L_p):
 
 @pytest.mark.parametrize("B", [1, 3, 33, 100])
 @pytest.mark.parametrize("n_q", [8, 40, 64])
-def test_decode_rows_of_a_group(cuda_ok, B, n_q):
+@pytest.mark.parametrize("d", [128, 64])
+def test_decode_rows_of_a_group(cuda_ok, B, n_q, d):
     """From one row a KV head to several row blocks, the group's requests scattered over the batch."""
-    rng = np.random.default_rng([B, n_q])
-    c = Kv4(rng, n_q=n_q, n_kv=8, d=128, dtype="bf16", prefixes=[390, 64], of=[b * 7 % 3 % 2 for b in range(B)],
+    rng = np.random.default_rng([B, n_q, d])
+    c = Kv4(rng, n_q=n_q, n_kv=8, d=d, dtype="bf16", prefixes=[390, 64], of=[b * 7 % 3 % 2 for b in range(B)],
             lens=[int(x) for x in rng.integers(0, 20, B)])
     c.check(*c.decode(), f"B {B} n_q {n_q}")
 
 
 @pytest.mark.parametrize("lens", [[1], [15], [16], [17], [31, 1], [5000], [1, 2, 3, 4, 700, 5], [33] * 50])
-@pytest.mark.parametrize("n_q,n_kv", [(32, 8), (24, 12), (3, 1)])
-def test_decode_cold_lengths(cuda_ok, lens, n_q, n_kv):
+@pytest.mark.parametrize("n_q,n_kv,d", [(32, 8, 128), (24, 12, 128), (3, 1, 128), (32, 8, 64), (36, 9, 64), (10, 5, 64)])
+def test_decode_cold_lengths(cuda_ok, lens, n_q, n_kv, d):
     rng = np.random.default_rng(sum(lens))
-    c = Kv4(rng, n_q=n_q, n_kv=n_kv, d=128, dtype="bf16", of=[-1] * len(lens), lens=lens)
+    c = Kv4(rng, n_q=n_q, n_kv=n_kv, d=d, dtype="bf16", of=[-1] * len(lens), lens=lens)
     c.check(*c.decode(), f"COLD {lens[:4]}")
 
 
-def test_decode_peaked_and_uneven_scales(cuda_ok):
+@pytest.mark.parametrize("d", [128, 64])
+def test_decode_peaked_and_uneven_scales(cuda_ok, d):
     """Scores far apart, and blocks, tokens and groups of 16 whose K or V differ by many powers of two."""
     def edit(kind, k, v):
         n = k.shape[0]
@@ -448,7 +452,7 @@ def test_decode_peaked_and_uneven_scales(cuda_ok):
             k[:, :, c:c + 16] *= np.float32(2.0 ** (-(c // 16) % 5))
             v[:, :, c:c + 16] *= np.float32(2.0 ** ((c // 16) * 3 % 7 - 3))
     rng = np.random.default_rng(11)
-    c = Kv4(rng, n_q=32, n_kv=8, d=128, dtype="bf16", prefixes=[700], of=[0, 0, -1], lens=[100, 0, 300], q_scale=2.0, edit=edit)
+    c = Kv4(rng, n_q=32, n_kv=8, d=d, dtype="bf16", prefixes=[700], of=[0, 0, -1], lens=[100, 0, 300], q_scale=2.0, edit=edit)
     c.check(*c.decode(), "uneven")
 
 
@@ -484,7 +488,7 @@ def test_decode_tiny_queries_over_zero_keys(cuda_ok, L_p, size):
     c.check(*c.decode(), f"{L_p} {size}")
 
 
-@pytest.mark.parametrize("n_q,n_kv,d,dtype", [(16, 4, 128, "bf16"), (8, 2, 64, "f32")])
+@pytest.mark.parametrize("n_q,n_kv,d,dtype", [(16, 4, 128, "bf16"), (8, 2, 64, "f32"), (16, 4, 64, "bf16")])
 @pytest.mark.parametrize("where", ["prefix", "cold"])
 def test_decode_nan_value_stays_with_its_columns(cuda_ok, n_q, n_kv, d, dtype, where):
     """A NaN in one head of one token's V reaches its 16 columns of that head's output of the requests that
@@ -512,7 +516,7 @@ def test_decode_nan_value_stays_with_its_columns(cuda_ok, n_q, n_kv, d, dtype, w
     assert torch.equal(o2[rest], o[rest])
 
 
-@pytest.mark.parametrize("shape", [(32, 8, 128, "bf16"), (8, 2, 64, "f32")])
+@pytest.mark.parametrize("shape", [(32, 8, 128, "bf16"), (8, 2, 64, "f32"), (32, 8, 64, "bf16")])
 @pytest.mark.parametrize("where", ["prefix", "cold"])
 def test_decode_nan_key_reaches_its_readers(cuda_ok, shape, where):
     """A NaN in one head of one token's K makes that head NaN for the requests that attend the token."""
@@ -551,7 +555,7 @@ def test_decode_bad_query_stays_with_its_head(cuda_ok, bad, backend):
     assert torch.equal(o2[~hit], o[~hit]) and torch.equal(lse2[~hit], lse[~hit])
 
 
-@pytest.mark.parametrize("n_q,n_kv,d,dtype", [(32, 8, 128, "bf16"), (24, 2, 128, "bf16"), (9, 3, 96, "bf16"), (8, 2, 64, "f32")])
+@pytest.mark.parametrize("n_q,n_kv,d,dtype", [(32, 8, 128, "bf16"), (24, 2, 128, "bf16"), (9, 3, 96, "bf16"), (8, 2, 64, "f32"), (32, 8, 64, "bf16")])
 @pytest.mark.parametrize("bad", [float("inf"), float("-inf")])
 def test_decode_infinite_query_over_keys_of_one_sign(cuda_ok, n_q, n_kv, d, dtype, bad):
     """Every K has the same sign in the dimension where q is infinite, so all scores of the head are -inf
@@ -586,7 +590,7 @@ def _uneven_v(e, small, where, of):
     return edit
 
 
-UNEVEN = [(32, 8, 128, "bf16"), (24, 2, 128, "bf16"), (8, 2, 64, "f32")]
+UNEVEN = [(32, 8, 128, "bf16"), (24, 2, 128, "bf16"), (8, 2, 64, "f32"), (32, 8, 64, "bf16")]
 
 
 @pytest.mark.parametrize("n_q,n_kv,d,dtype", UNEVEN)
@@ -618,7 +622,7 @@ def test_decode_long_cold_runs_of_zero_values(cuda_ok):
     c.check(o, lse, "zero V")
 
 
-@pytest.mark.parametrize("n_q,n_kv,d,dtype", [(32, 8, 128, "bf16"), (8, 2, 64, "f32"), (6, 3, 128, "bf16"), (5, 5, 96, "bf16"), (24, 12, 128, "bf16")])
+@pytest.mark.parametrize("n_q,n_kv,d,dtype", [(32, 8, 128, "bf16"), (8, 2, 64, "f32"), (6, 3, 128, "bf16"), (5, 5, 96, "bf16"), (24, 12, 128, "bf16"), (32, 8, 64, "bf16")])
 @pytest.mark.parametrize("on_device", [False, True])
 def test_fused_append_equals_append_then_decode(cuda_ok, n_q, n_kv, d, dtype, on_device):
     torch, gb, rng = _torch(), _gb(), np.random.default_rng(15)
@@ -730,12 +734,12 @@ def test_step_of_calls_in_a_graph(cuda_ok):
     c.ctx.sync_status()
 
 
-@pytest.mark.parametrize("B", [1, 8, 64])
-def test_calls_back_to_back_in_a_graph(cuda_ok, B):
+@pytest.mark.parametrize("B,d", [(1, 128), (8, 128), (64, 128), (8, 64)])
+def test_calls_back_to_back_in_a_graph(cuda_ok, B, d):
     """Two dozen calls one after the other, replayed again and again (as many prefix CTAs as SMs, and fewer): every one
     ends, with the result of a single call."""
     torch, rng = _torch(), np.random.default_rng([B, 41])
-    c = Kv4(rng, n_q=32, n_kv=8, d=128, dtype="bf16", prefixes=[9728], of=[0] * B, lens=[0] * B)
+    c = Kv4(rng, n_q=32, n_kv=8, d=d, dtype="bf16", prefixes=[9728], of=[0] * B, lens=[0] * B)
     o, lse = c.decode()
     plan = c.ctx.dispatch(c.batch)
     ws = torch.empty(c.ctx.workspace_size(plan), dtype=torch.uint8, device="cuda")
@@ -834,11 +838,12 @@ SCHEDULES = {"serial": lambda x: x.set_concurrency(False), "half": lambda x: x.s
 
 
 @pytest.mark.parametrize("how", sorted(SCHEDULES))
-def test_decode_schedules(cuda_ok, how):
+@pytest.mark.parametrize("d", [128, 64])
+def test_decode_schedules(cuda_ok, how, d):
     """Every knob of the schedule leaves the result within the same tolerance; `mixed` runs one group
     on the tensor cores and one on CUDA cores."""
     rng = np.random.default_rng(22)
-    c = Kv4(rng, n_q=32, n_kv=8, d=128, dtype="bf16", prefixes=[1500, 700], of=[0, 1, 0, 0, -1, 0, 0, 0, 0, 0], lens=[300, 20, 0, 1, 90, 64, 700, 33, 5, 16])
+    c = Kv4(rng, n_q=32, n_kv=8, d=d, dtype="bf16", prefixes=[1500, 700], of=[0, 1, 0, 0, -1, 0, 0, 0, 0, 0], lens=[300, 20, 0, 1, 90, 64, 700, 33, 5, 16])
     SCHEDULES[how](c.ctx)
     c.check(*c.decode(), how)
 
