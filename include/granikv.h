@@ -176,7 +176,8 @@ granikv_status granikv_kv8_row_bytes(int32_t n_kv, int32_t head_dim, size_t* byt
  * Everything else is as for granikv_create_kv8: 16-byte alignment of those rows and of q and o; a NaN or an
  * infinity in a head's q, or a NaN in the K that a request attends, makes that head's o and lse of that
  * request NaN, a NaN in V reaches its 16 columns of o only; the same calls work, the same are
- * GRANIKV_ERR_UNSUPPORTED, and the same backends serve the same shapes. ------------------------- */
+ * GRANIKV_ERR_UNSUPPORTED, and the same backends serve the same shapes, but that bf16 q with head_dim 64 runs on
+ * tensor cores as well. ------------------------------------------------------------------- */
 granikv_status granikv_create_kv4(const granikv_config* cfg, granikv_ctx** out);
 /* Bytes of one slot's row; GRANIKV_ERR_UNSUPPORTED as from granikv_kv8_row_bytes. */
 granikv_status granikv_kv4_row_bytes(int32_t n_kv, int32_t head_dim, size_t* bytes);

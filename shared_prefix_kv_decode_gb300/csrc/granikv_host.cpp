@@ -33,7 +33,7 @@ constexpr int32_t kDefaultMaxBatch = 4096;
 // at M_eff <= 32 (both are bandwidth-bound there) and falls far behind above, where its
 // warp-level MMAs run out of throughput.
 constexpr int32_t kDefaultMsat = 4;
-// 8-bit cache: the cascade backend is the CUDA-core kernel, so every group goes to the dense one.
+// 8- and 4-bit cache: the cascade backend is the CUDA-core kernel, so every group goes to the dense one.
 constexpr int32_t kDefaultMsatKv8 = 1;
 
 struct Extent {
@@ -134,7 +134,7 @@ struct granikv_plan {
     std::vector<int64_t> tail_key, tail_key_now, sim_heap;
     int64_t tail_len = 0;
     std::vector<char> grp_tail;           // group's last piece is a shorter remainder
-    std::vector<double> share;            // 8-bit cache: what each suffix run's CTA can take
+    std::vector<double> share;            // packed cache: what each suffix run's CTA can take
     struct Class {                        // dense CTAs that are done at t (us)
       double t;
       int64_t n;
@@ -206,7 +206,7 @@ int32_t suffix_impl_for(const granikv_ctx* c) {
 // The suffix kernels that run one token-CTA per run and group of eight KV heads.
 bool token_ctas(int32_t suffix_impl) { return suffix_impl == kImplSuffixMma || suffix_impl == kImplPackedSuffix; }
 
-// The dense prefix kernels of the tensor-core path (16-bit and 8-bit cache).
+// The dense prefix kernels of the tensor-core path (16-bit and packed caches).
 bool dense_tc(int32_t impl) { return impl == kImplDenseTc || impl == kImplPackedDense; }
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no link-time libcuda).
@@ -1133,7 +1133,7 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
   bool read_ahead = false;          // the split's dense CTAs read ahead into L2 (see below)
   double tail_frac = 0.0;           // share of the suffix work the dense CTAs take after their piece
   const int64_t seg_tiles = c->packed_row ? kSegTilesKv8 : kSegTiles;
-  bool kv8_split = false;           // 8-bit cache: the split and its runs' shares as planned below
+  bool kv8_split = false;           // packed cache: the split and its runs' shares as planned below
   int32_t kv8_main = 0;             // its suffix CTAs
   std::vector<double>& share = w.share;
   share.clear();
@@ -1165,7 +1165,7 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
       if (ctas_for(mid) <= target) hi = mid;
       else lo = mid + 1;
     }
-    // 8-bit cache on CUDA cores: with short pieces the merge's records cost more than the pieces save.
+    // packed cache on CUDA cores: with short pieces the merge's records cost more than the pieces save.
     // At least sqrt(8 L) of L tokens: two prefixes of 34 and 1,995, B = 4 9.7 us, with sqrt(4 L) 10.3, with
     // sqrt(16 L) 11.0; 8,000 tokens, B = 8 18.5, 21.8 and 20.1
     for (int32_t i = 0; i < G; ++i)
@@ -1175,7 +1175,8 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
     bool kv8_dense = auto_share && c->packed_row && n_kv <= 8;
     for (int32_t i = 0; i < G; ++i) kv8_dense = kv8_dense && groups[i].impl == kImplPackedDense;
     if (kv8_dense) {
-      // 8-bit cache: every SM works until the end.  With pieces of a given length, dense CTA k is done
+      // Packed cache (measured in 8 bits; in 4 bits a step of a 16K prefix with 64 requests or of eight prefixes gains
+      // nothing from other constants): every SM works until the end.  With pieces of a given length, dense CTA k is done
       // at t_k = 5.2 us + 7.3 ns a token and then takes suffix work (3 us for its set-up), the SMs
       // without a prefix piece take suffix work from the start (4.5 us); a unit of it (16 tokens, or
       // a third of a segment's cost) is 0.57 us.  The common end T makes the parts add up to
@@ -1309,7 +1310,7 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
       // set-up for its run (a few us) is left out: the prefix estimate runs about 6 us long on
       // that shape, which covers it; with 4 / 2 / 0 us set aside for it the call took 82.9 /
       // 81.0 / 80.3 us, and at 0 both sides end within 0.4 us of each other.
-      // (an 8-bit cache has tail runs from the common-end plan above only)
+      // (a packed cache has tail runs from the common-end plan above only)
       bool all_dense = G > 0 && n_kv <= 8;
       for (int32_t i = 0; i < G; ++i) all_dense = all_dense && groups[i].impl == kImplDenseTc;
       if (auto_found && all_dense) {
@@ -1530,7 +1531,7 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
       for (int32_t j = 0; j < n_kv; ++j)
         for (int32_t rb = 0; rb < dg.row_blocks; ++rb) pitems.push_back({i, j, rb, dg.n_splits - 1});
     }
-    // the 8-bit dense kernel's first CTAs are those that take suffix runs after their piece: the
+    // the packed dense kernel's first CTAs are those that take suffix runs after their piece: the
     // shortest pieces come first
     if (impl == kImplPackedDense && kv8_split)
       std::stable_sort(pitems.begin() + p->pitem_first[impl], pitems.end(),

@@ -9,7 +9,9 @@ namespace {
 
 // One block of kKv8Block slab tokens of one KV head, of K (blockIdx.y = 0) or V.  A thread holds groups of 16
 // elements in registers between the block's amax and their codes, so the rows are read once: 2.6 bytes moved for
-// each bf16 element.
+// each bf16 element.  Bound by memory: 16K tokens of 8 x 128 take 18.4 us from bf16 (86 MB, 0.69 of the copy rate) and
+// 25.6 from fp32 (0.88); without the quantising, the same loads and stores of bf16 take 17.3.  (With two
+// loads of 16 bytes in place of one of 32 and a quotient an instruction instead of two: 21.0 us.)
 template <typename T, int D, bool WIDE>
 __global__ void __launch_bounds__(256) kv4_fill_kernel(const T* __restrict__ k, const T* __restrict__ v, int32_t L_p,
                                                        uint8_t* __restrict__ kpool, uint8_t* __restrict__ vpool,
@@ -88,7 +90,7 @@ __device__ __forceinline__ void kv4_write_row(const T* __restrict__ src, uint8_t
   if (i == 0) slot_row[kv4_units_at(n_kv, D) + j] = (uint8_t)byte;
 }
 
-// Rows at slots[i].  Item w is head w / 2 % n_kv of token w / 2 / n_kv, its K (w even) or V.
+// Rows at slots[i]: 16K tokens of 8 x 128 from bf16 20.9 us, from fp32 25.5.  Item w is head w / 2 % n_kv of token w / 2 / n_kv, its K (w even) or V.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv4_append_kernel(const T* __restrict__ k_new, const T* __restrict__ v_new,
                                                          const int32_t* __restrict__ slots, int32_t N,

@@ -50,11 +50,14 @@
 // 4 bits.  An element is code * b * u, b the e4m3 scale of its 16 dims and u the power of two of its block of 64 slab
 // tokens and head, that is, of a tile.  code * b is exact in fp16, so the conversion warps make fp16 operand tiles of
 // K as of V (an fp16x2 conversion and a product for each pair), S is an fp16 product with q in fp16 (scaled by a power of two
-// to [2^14, 2^15): exact down to 2^-31 of the row's largest element), and u takes the place of ks and vs.  A
-// conversion warp's ring holds its 32 tokens' codes, by a TMA box, and scales, 8 bytes a token by cp.async from the warp
-// itself: TMA takes about four clocks for a row of a box, however short, so with the scales in boxes of their own
-// the loads alone took longer (a tile's 2,200 clocks) than everything else.  The K and V rings have five
-// slots of one tile in fp16.
+// to [2^14, 2^15): exact down to 2^-31 of the row's largest element), and u takes the place of ks and vs.  Eight
+// warps convert, four of K and four of V (four for both: 104.9 us where eight take 86.7, see below for the shape).  A
+// warp's ring holds its 32 tokens' codes, by a TMA box, and scales, 8 bytes a token by cp.async from the warp
+// itself.  The K and V rings have five slots of one tile in fp16 (two and three of two tiles: a step of a 16K prefix with 64 requests 37.4 us, so 36.7).
+// What bounds it: an SM quarter issues for two softmax warps and two conversion warps.  480 requests on a slab of 8K
+// (32/8 heads of 128, two waves of CTAs) take 75.6 us, in 8 bits 63.9; of about 1,590 clocks for 128 tokens a softmax
+// warp works 1,200 (8 bits: 965 of 1,395) and waits the rest, a conversion warp works 570.  The loads are not what it
+// waits for: without those of the scales it was no faster.
 #pragma once
 
 #include <cuda.h>
@@ -236,7 +239,7 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 // eight lanes at a time have to cover eight 16-byte chunks that differ in their place within 128 bytes, which the swizzle
 // XORs with the token's last bits; the lanes of the upper 64 dims, whose chunks have the same places as the lower
 // ones', take the token whose bits differ by one step: 1, or 2 (where the bit 1 already tells two tokens apart).
-// (With the stores of one half in another order, by a branch, a 4-bit tile took 8 % longer.)
+// (With the stores of the upper half in another order, by a branch, and scales in TMA boxes: 90.4 us where this takes 76.1.)
 template <int BITS, int D>
 struct ConvLane {
   using Lay = Layout<BITS, D>;
@@ -465,7 +468,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
         const uint32_t dst = sC + (w * kCSlots + i % kCSlots) * Lay::kCSlotBytes + kPart * Lay::kHead + lane * Lay::kScale;
         const bool in = t0 + i * kPair + part * kPart + lane < t1;
         if (slab_ok && i < n_pairs) {
-          const uint8_t* src = in ? scale_src + (int64_t)i * kPair * p.packed_row : scale_src;
+          const uint8_t* src = in ? scale_src + (int64_t)i * kPair * p.packed_row : static_cast<const uint8_t*>(p.kpool);
           if constexpr (D == 128) cp_async8(dst, src, in ? 8 : 0);
           else cp_async4(dst, src, in ? 4 : 0);
         }

@@ -403,6 +403,36 @@ def test_decode_prefix_lengths(cuda_ok, L_p, d):
     c.check(*c.decode(), f"L_p {L_p}")
 
 
+@pytest.mark.parametrize("n_q,n_kv,d,dtype", [(32, 8, 128, "bf16"), (16, 2, 64, "bf16"), (24, 2, 128, "bf16"), (8, 2, 64, "f32")])
+def test_decode_requests_without_keys(cuda_ok, n_q, n_kv, d, dtype):
+    """o = 0 and lse = -inf where a request has no prefix and, by the device's length, no token (by the host's it is
+    refused); the others are not touched by it."""
+    torch, gb = _torch(), _gb()
+    rng = np.random.default_rng([n_q, d])
+    lens = [40, 7, 0, 3]
+    c = Kv4(rng, n_q=n_q, n_kv=n_kv, d=d, dtype=dtype, prefixes=[70], of=[-1, -1, 0, 0], lens=lens)
+    slabs = [-1, -1, c.slabs[0], c.slabs[0]]
+    with pytest.raises(gb.GranikvError):
+        c.ctx.dispatch(gb.Batch(slabs, [40, 0, 0, 3], c.table, c.cap))
+    c.live[1] = 0
+    o, lse = c.decode(batch=gb.Batch(slabs, lens, c.table, c.cap, seq_len_dev=c.live))
+    assert (o[1] == 0).all() and torch.isneginf(lse[1]).all()
+    rows = [0, 2, 3]
+    c.of, c.lens, c.q_host = [c.of[b] for b in rows], [lens[b] for b in rows], c.q_host[rows]
+    c.ck, c.cv, c.cu = ([x[b] for b in rows] for x in (c.ck, c.cv, c.cu))
+    c.check(o[rows], lse[rows], "the others")
+
+
+@pytest.mark.parametrize("L_p", [1, 33, 64, 129])
+@pytest.mark.parametrize("d", [128, 64])
+def test_decode_slab_that_ends_the_pool(cuda_ok, L_p, d):
+    """One slot behind the slab: tiles and boxes reach past the pool."""
+    rng = np.random.default_rng([L_p, d, 1])
+    c = Kv4(rng, n_q=8, n_kv=2, d=d, dtype="bf16", prefixes=[L_p], of=[0], lens=[1], holes=0)
+    assert c.kp.shape[0] == L_p + 1
+    c.check(*c.decode(), f"L_p {L_p}")
+
+
 @pytest.mark.parametrize("L_p", [640, 777, 2048, 5000])
 @pytest.mark.parametrize("d", [128, 64])
 def test_decode_long_prefix_pieces(cuda_ok, L_p, d):
