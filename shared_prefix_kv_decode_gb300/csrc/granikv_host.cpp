@@ -1630,8 +1630,11 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
   // Where the suffix side ends last (Qwen-2.5 shape) it does not help; next to a light suffix
   // side it costs (16K prefix, 256 COLD tokens a request: B = 1 17.7 -> 18.4 us, B = 8 18.9 ->
   // 19.8 us); and with the kernels one after another (eight prefixes) six tiles ahead cost 17 %.
+  // The 4-bit dense kernel's rings hold three contents of codes where the others have four or more, so it always reads
+  // one content (128 tokens) ahead: 128 requests on 16K 77.5 -> 76.7 us, eight prefixes 75.7 -> 74.2 (two contents 76.9 and
+  // 74.3, eight 77.2 and 75.0); 64 requests on 16K 36.8 -> 36.6, one on 8K the same.
   constexpr int32_t kAutoL2Ahead = 2;
-  p->l2_ahead = c->l2_ahead >= 0 ? c->l2_ahead : (concurrent && read_ahead ? kAutoL2Ahead : 0);
+  p->l2_ahead = c->l2_ahead >= 0 ? c->l2_ahead : c->packed_bits == 4 ? 1 : (concurrent && read_ahead ? kAutoL2Ahead : 0);
   p->group_impl.resize(G);
   for (int32_t i = 0; i < G; ++i) p->group_impl[i] = groups[i].impl;
   // this dispatch succeeded: its groups and prefix items may serve the next one

@@ -144,6 +144,17 @@ def test_kv4_dispatch_plans(granikv_lib):
         assert ctx.workspace_size(plan) > 0
 
 
+def test_dense_kernel_reads_ahead(granikv_lib):
+    """One content ahead over the 4-bit cache, unless it is set; none where the others' split does not ask for it."""
+    for kw, want in ((dict(kv4=True), 1), (dict(kv8=True), 0)):
+        ctx = gb.Context(n_layers=1, n_q=32, n_kv=8, head_dim=128, dtype=gb.DTYPE_BF16, n_slots=4000, hot_fraction=0.5, host_only=True, **kw)
+        sid, _ = ctx.hot_alloc(1000)
+        batch = gb.Batch([sid, sid], [0, 0], 4096, 64)
+        assert ctx.dispatch(batch).dense_l2_ahead() == want
+        ctx.set_dense_l2_ahead(0)
+        assert ctx.dispatch(batch).dense_l2_ahead() == 0
+
+
 def _plan_case(rng):
     n_prefix = int(rng.choice([1, 1, 2, 5, 20]))
     B = int(rng.choice([1, 2, 7, 40, 200, 1000]))
