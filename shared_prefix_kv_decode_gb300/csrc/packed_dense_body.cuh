@@ -81,6 +81,7 @@ namespace {
 using pks::lg2_approx;
 using pks::pack_f16;
 using pks::block_barrier;
+using pks::part_barrier;
 using pks::regs_down;
 using pks::regs_up;
 
@@ -347,18 +348,20 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     if (!slab_ok) atomicCAS(p.err, 0, (int32_t)kDevBadSlab);
     mbar_fence_init();
     fence_proxy_async_smem();
-    grid_dep_wait();  // the slab may have been written by the work before this kernel
-    if (slab_ok) {
-      if constexpr (BITS == 8)
+    if constexpr (BITS == 8) {
+      grid_dep_wait();  // the slab may have been written by the work before this kernel
+      if (slab_ok) {
         for (int i = 0; i < min(n_pairs, kKSlots); ++i) issue_k(i);
-      for (int i = 0; i < min(n_pairs, kCSlots); ++i)
-        for (int w = 0; w < kConvWarps; ++w) issue_c(w, i);
+        for (int i = 0; i < min(n_pairs, kCSlots); ++i)
+          for (int w = 0; w < kConvWarps; ++w) issue_c(w, i);
+      }
     }
   }
   if (warp == 0) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
+  if constexpr (BITS == 4) __syncthreads();  // the barriers are ready: the conversion warps go ahead from here
   // q and the records are touched only after the previous kernel in the stream has completed
   grid_dep_wait();
   grid_dep_launch_dependents();
@@ -408,8 +411,14 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     for (int k = 0; k < kQw; ++k) amax = fmaxf(amax, bf16x2_finite_max(qw[k]));
     part[qhalf * kM + qrow] = amax;
   }
+  // 4 bits: K has to be converted before the first product, which q's way to TMEM need not hold up
+  const bool ahead = BITS == 4 && warp >= kWarpConv && warp < kWarpS;
+  auto q_barrier = [&] {
+    if constexpr (BITS == 8) __syncthreads();
+    else if (!ahead) part_barrier<Lay::kThreads - 32 * kConvWarps>();
+  };
   tc_fence_before();
-  __syncthreads();
+  q_barrier();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (warp < kSoftmaxWarps) {
@@ -444,7 +453,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     }
   }
   tc_fence_before();
-  __syncthreads();
+  q_barrier();
   tc_fence_after();
 
   if (warp >= kSoftmaxWarps) {
@@ -475,6 +484,11 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
         cp_async_commit();
       }
     };
+    if constexpr (BITS == 4) {
+      if (lane == 0)
+        for (int i = 0; i < issued; ++i) issue_c(w, i);
+      __syncwarp();
+    }
 #pragma unroll
     for (int i = 0; i < kCSlots; ++i) copy_scales(i);
     for (int i = 0; slab_ok && i < n_pairs; ++i) {

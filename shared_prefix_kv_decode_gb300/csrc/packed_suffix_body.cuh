@@ -126,6 +126,10 @@ template <int THREADS>
 __device__ __forceinline__ void block_barrier() {  // of the whole block, from either side of a branch
   asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
+template <int THREADS>
+__device__ __forceinline__ void part_barrier() {  // of that many of its threads
+  asm volatile("bar.sync 2, %0;" ::"n"(THREADS) : "memory");
+}
 
 // Two tokens' four codes (lane word of a transposed ldmatrix: token 2 c in the low half) -> for each of the four dims
 // the two tokens' values as fp16x2, times the tokens' scales.
