@@ -1175,15 +1175,19 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
     bool kv8_dense = auto_share && c->packed_row && n_kv <= 8;
     for (int32_t i = 0; i < G; ++i) kv8_dense = kv8_dense && groups[i].impl == kImplPackedDense;
     if (kv8_dense) {
-      // Packed cache (measured in 8 bits; in 4 bits a step of a 16K prefix with 64 requests or of eight prefixes gains
-      // nothing from other constants): every SM works until the end.  With pieces of a given length, dense CTA k is done
+      // Packed cache (8 bits, 4 bits below): every SM works until the end.  With pieces of a given length, dense CTA k is done
       // at t_k = 5.2 us + 7.3 ns a token and then takes suffix work (3 us for its set-up), the SMs
       // without a prefix piece take suffix work from the start (4.5 us); a unit of it (16 tokens, or
       // a third of a segment's cost) is 0.57 us.  The common end T makes the parts add up to
       // the step's units; the length with the earliest end is taken, and every run's share is what
       // its CTA can do by then.  Measured on GB300 (CTA end times): Llama shape 26.9 us for 21.3
       // tiles, Qwen shape 65 us for 64.
-      constexpr double kDense = 5.2, kToken = 0.0073, kTail = 3.0, kMain = 4.5, kUnit = 0.57, kMinTail = 6.0;
+      // 4 bits: 10.5 us + 9 ns a token, a unit 0.8 us.  (27 shapes, 8 to 160 requests on 2K to 30K tokens, 32.4 us in the
+      // geometric mean with the constants of 8 bits and 31.7 so: 24 requests on 2K 12.9 -> 12.2, on 16K 22.3 -> 21.5, 160 on 30K
+      // 113.1 -> 110.4, 160 on 8K 58.5 -> 59.4; a 16K prefix with 64 and eight prefixes the same.)
+      const bool four = c->packed_bits == 4;
+      const double kDense = four ? 10.5 : 5.2, kToken = four ? 0.009 : 0.0073, kUnit = four ? 0.8 : 0.57;
+      constexpr double kTail = 3.0, kMain = 4.5, kMinTail = 6.0;
       const int64_t few = (T_tiles + 3) / 4;  // a run for every four tiles at most
       const double units = (double)(T_tiles + seg_tiles * (n_sreq + std::min<int64_t>(few, c->num_sms)));
       using Class = granikv_plan::Scratch::Class;
