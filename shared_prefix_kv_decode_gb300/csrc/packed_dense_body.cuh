@@ -53,11 +53,14 @@
 // to [2^14, 2^15): exact down to 2^-31 of the row's largest element), and u takes the place of ks and vs.  Eight
 // warps convert, four of K and four of V (four for both: 104.9 us where eight take 86.7, see below for the shape).  A
 // warp's ring holds its 32 tokens' codes, by a TMA box, and scales, 8 bytes a token by cp.async from the warp
-// itself.  The K and V rings have five slots of one tile in fp16 (two and three of two tiles: a step of a 16K prefix with 64 requests 37.4 us, so 36.7).
-// What bounds it: an SM quarter issues for two softmax warps and two conversion warps.  480 requests on a slab of 8K
-// (32/8 heads of 128, two waves of CTAs) take 75.6 us, in 8 bits 63.9; of about 1,590 clocks for 128 tokens a softmax
-// warp works 1,200 (8 bits: 965 of 1,395) and waits the rest, a conversion warp works 570.  The loads are not what it
-// waits for: without those of the scales it was no faster.
+// itself.  The K and V rings have five slots of one tile in fp16 (two and three of two tiles: a step of a 16K prefix with
+// 64 requests 37.4 us, so 36.7).
+// The conversion warps go ahead from the first barrier on, beside q's way to TMEM (one request on 8K 11.2 us, so 10.8).
+// What bounds it: the softmax warps' rounds, next to the conversion on the same issue slots and the same shared memory.
+// 480 requests on a slab of 8K (32/8 heads of 128, two waves of CTAs) take 75 us, in 8 bits 64.  With parts taken out: the
+// products 73.6, three quarters of the conversion's products and stores 69.7, both 67.7; the exponentials, the maxima or the row
+// sums 1 to 2 % each, the scales' loads nothing.  Codes and scales of all conversion warps fetched by two warps of their own, in
+// boxes of 128 rows: 77.
 #pragma once
 
 #include <cuda.h>
