@@ -29,9 +29,12 @@
 // once, over vs / v, v the piece's smallest V scale.  The running maximum m is taken over z.  P carries a
 // factor of 2^7: it is at most 2^15 (m may lag the row's maximum by 2^8, see below), and fp16 keeps its 11
 // bits down to 2^-21 of the largest weight.
-// V scales lie between 2^-104.9 (of zeros) and 2^119.2.  Where those of a piece span more than 2^32, a tile's P
-// may underflow while its weights count: the row sum then has a running maximum and exponentials of its own, over
-// s ks alone.  Below that span P reaches weights of 2^-94 of the largest.
+// V scales lie between 2^-104.9 (of zeros) and 2^119.2.  A tile's P is that much smaller than another's of equal weights
+// as its V scale is, and a block's scale may come from a token without weight, so in fp16 the weights that make up the
+// output may vanish beside others.  Where the scales of a piece span more than 2^8, their powers of two therefore go into
+// V's operands, which are bf16 then (a code, or a code times its 4-bit scale, has 4 or 6 significant bits; the piece's largest
+// scale becomes 2^90, what lies 2^216 below it 0), and P has the significand of vs alone: P = 2^(z - m - 8) as the sum of two
+// bf16 values (16 bits, at most 1, down to 2^-118 of the largest weight), over all of S, in twice the products.
 // Roles (15 warps; the 16th only takes part in the block's barriers here):
 //  * warps 0-7, softmax and epilogue: warp w serves TMEM lanes 32*(w%4).. (row r = lane r), all 64
 //    columns of the tiles i with i % 2 == w / 4; the two warps of a row quarter take turns, half a
@@ -155,7 +158,9 @@ static_assert(kColQ + 128 / 2 <= kColO && kColO + 128 <= kTmemCols, "TMEM column
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;     // log2 of the largest growth tolerated in P
 constexpr float kShift = 7.0f;                // log2 of the factor that P carries
-constexpr uint32_t kWideSpan = 32;            // log2 of a wide span of V scales
+constexpr uint32_t kWideSpan = 8;             // log2 of a wide span of V scales
+constexpr float kWideShift = -8.0f;           // there: log2 of P's factor (P <= 1)
+constexpr int kWideTop = 90;                  // and of what the largest V scale's power of two becomes in V's operands
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // D[tmem] (+)= A[tmem] * B[smem desc], kind::f8f6f4 (A: M rows = TMEM lanes, four 8-bit elements per
@@ -191,6 +196,12 @@ __device__ __forceinline__ void st_record8(float* a, const float (&x)[8], uint64
 // Two bf16 times f -> fp16; four fp16 -> four e4m3 codes (nearest even, NaN kept).
 __device__ __forceinline__ __half2 f16x2_of(uint32_t w, float f) {
   return __floats2half2_rn(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
+}
+// Two fp16 times f -> bf16 (exact: see kWideSpan).
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t w, float f) {
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  const __nv_bfloat162 y = __floats2bfloat162_rn(x.x * f, x.y * f);
+  return *reinterpret_cast<const uint32_t*>(&y);
 }
 __device__ __forceinline__ uint32_t f16x4_to_e4m3x4(__half2 a, __half2 b) {
   uint16_t lo, hi;
@@ -383,22 +394,38 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     ks = *reinterpret_cast<const Scale*>(static_cast<const uint8_t*>(p.kpool) + a);
     vs = *reinterpret_cast<const Scale*>(static_cast<const uint8_t*>(p.vpool) + a);
   };
-  // V scales of the piece's tiles lane, lane + 32, .. as the bits of positive floats, for their span; requested
-  // here and used when the set-up is done
-  constexpr int kSpan = 4;
-  uint32_t v_bits[kSpan] = {};
+  // V scales of the piece's tiles as the bits of positive floats: the smallest one's, and, where they span widely, the
+  // biased exponent of the largest (else 0).  The PV warp finds them beside q's way for the warps that wait for that;
+  // the 4-bit conversion warps, which do not, for themselves.
   auto v_scale_bits = [&](int i) {
     const uint8_t* at = static_cast<const uint8_t*>(p.vpool) + (first_slot + (int64_t)i * kN) * p.packed_row + scale_at;
     if constexpr (BITS == 8) return *reinterpret_cast<const uint32_t*>(at);
     else return (uint32_t)*at << 23;
   };
+  auto v_span = [&](uint32_t& lo) {
+    uint32_t hi = 0u;
+    lo = 0xffffffffu;
+    for (int i = lane; slab_ok && i < n_tiles; i += 32) {
+      const uint32_t x = v_scale_bits(i);
+      lo = min(lo, x);
+      hi = max(hi, x);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    return hi > lo && hi - lo > kWideSpan << 23 ? hi >> 23 : 0u;
+  };
+  volatile uint32_t* v_least = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + 8 * kNumBars + 4);
+  volatile uint32_t* v_top = v_least + 2;
+  if (warp == kWarpPv) {
+    uint32_t lo;
+    const uint32_t top = v_span(lo);
+    if (lane == 0) {
+      *v_least = lo;
+      *v_top = top;
+    }
+  }
   if (warp < kSoftmaxWarps) {
     if (slab_ok && qhalf < n_tiles) load_scales(qhalf);
-    if (slab_ok) {
-#pragma unroll
-      for (int k = 0; k < kSpan; ++k)
-        if (lane + 32 * k < n_tiles) v_bits[k] = v_scale_bits(lane + 32 * k);
-    }
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
                                                       ((int64_t)req * p.n_q + h) * D + qhalf * (D / 2));
     float amax = 0.f;
@@ -494,6 +521,16 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     }
 #pragma unroll
     for (int i = 0; i < kCSlots; ++i) copy_scales(i);
+    uint32_t lo;
+    const int wide_top = to_k ? 0 : BITS == 8 ? (int)*v_top : (int)v_span(lo);
+    // wide: what code (times scale) is multiplied by in V's operands, which are bf16 then: the tile's power of two, that of the
+    // piece's largest made 2^kWideTop
+    auto v_size = [&](int tile) {
+      const int e = tile < n_tiles ? (int)(v_scale_bits(tile) >> 23) - wide_top + kWideTop + 127 : 0;
+      return e > 0 ? __uint_as_float((uint32_t)e << 23) : 0.f;
+    };
+    auto all_parts = [&](auto wide_span) {
+    constexpr bool kWide = decltype(wide_span)::value;
     for (int i = 0; slab_ok && i < n_pairs; ++i) {
       const int c = w * kCSlots + i % kCSlots;
       const int use = BITS == 8 ? i : 2 * i + part / kFill, st = use % slots;  // the slot's use, of all of the ring's
@@ -507,21 +544,27 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
       }
       const uint32_t src = sC + c * Lay::kCSlotBytes, dst = ring + st * Lay::kSlot;
       const int valid = t1 - t0 - i * kPair - part * kPart;  // tokens of the part in range, or more
-      uint4 x[kPer];
-      uint32_t b[kPer];  // 4 bits: their two scales
-#pragma unroll
-      for (int n = 0; n < kPer; ++n) {
+      auto codes = [&](int n, uint32_t& b) {  // of load n, and (4 bits) their two scales
         const uint32_t t = (uint32_t)(cl.token + n * Conv::kStep);
-        x[n] = lds128(src + t * Lay::kHead + cl.dim * BITS / 8);
-        if constexpr (BITS == 4) b[n] = lds16(src + kPart * Lay::kHead + t * Lay::kScale + cl.dim / 16);
-      }
-      if (valid < kPart) {  // 0 * whatever lies past the piece must not reach O
+        if constexpr (BITS == 4) b = lds16(src + kPart * Lay::kHead + t * Lay::kScale + cl.dim / 16);
+        return lds128(src + t * Lay::kHead + cl.dim * BITS / 8);
+      };
+      // 0 * whatever lies past the piece must not reach O
+      auto mask = [&](int n, uint4& x, uint32_t& b) {
+        if (cl.token + n * Conv::kStep >= valid) {
+          x = make_uint4(0u, 0u, 0u, 0u);
+          b = 0u;
+        }
+      };
+      uint4 x[kWide ? 1 : kPer];
+      uint32_t b[kWide ? 1 : kPer];
+      if constexpr (!kWide) {
 #pragma unroll
-        for (int n = 0; n < kPer; ++n)
-          if (cl.token + n * Conv::kStep >= valid) {
-            x[n] = make_uint4(0u, 0u, 0u, 0u);
-            b[n] = 0u;
-          }
+        for (int n = 0; n < kPer; ++n) x[n] = codes(n, b[n]);
+        if (valid < kPart) {
+#pragma unroll
+          for (int n = 0; n < kPer; ++n) mask(n, x[n], b[n]);
+        }
       }
       const bool fills = BITS == 8 || use < n_tiles;  // (4 bits: the last two parts may have no tile)
       if (fills && use >= slots) {
@@ -529,26 +572,49 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
       }
-#pragma unroll
-      for (int n = 0; n < kPer; ++n) {
-        if (!fills) break;
+      [[maybe_unused]] float size = 1.f;
+      if constexpr (kWide) size = v_size(2 * i + part / 2);
+      auto put = [&](int n, const uint4& x, uint32_t b) {
         if constexpr (BITS == 8) {
           uint32_t y[8];
-          e4m3x4_to_f16x4(x[n].x, y[0], y[1]);
-          e4m3x4_to_f16x4(x[n].y, y[2], y[3]);
-          e4m3x4_to_f16x4(x[n].z, y[4], y[5]);
-          e4m3x4_to_f16x4(x[n].w, y[6], y[7]);
+          e4m3x4_to_f16x4(x.x, y[0], y[1]);
+          e4m3x4_to_f16x4(x.y, y[2], y[3]);
+          e4m3x4_to_f16x4(x.z, y[4], y[5]);
+          e4m3x4_to_f16x4(x.w, y[6], y[7]);
+          if constexpr (kWide) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = f16x2_to_bf16x2(y[k], size);
+          }
           cl.store(dst, n, 0, y[0], y[1], y[2], y[3]);
           cl.store(dst, n, 1, y[4], y[5], y[6], y[7]);
         } else {
-          const uint32_t f = e4m3x2_to_f16x2((uint16_t)b[n]), f2[2] = {__byte_perm(f, f, 0x1010), __byte_perm(f, f, 0x3232)};
-          const uint32_t u[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+          const uint32_t f = e4m3x2_to_f16x2((uint16_t)b), f2[2] = {__byte_perm(f, f, 0x1010), __byte_perm(f, f, 0x3232)};
+          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t y[4];
             e2m1x8_to_f16x8(u[k], y);
-            cl.store(dst, n, k, f16x2_mul(y[0], f2[k / 2]), f16x2_mul(y[1], f2[k / 2]), f16x2_mul(y[2], f2[k / 2]), f16x2_mul(y[3], f2[k / 2]));
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              y[h] = f16x2_mul(y[h], f2[k / 2]);
+              if constexpr (kWide) y[h] = f16x2_to_bf16x2(y[h], size);
+            }
+            cl.store(dst, n, k, y[0], y[1], y[2], y[3]);
           }
+        }
+      };
+      if constexpr (kWide) {
+#pragma unroll 1
+        for (int n = 0; fills && n < kPer; ++n) {
+          x[0] = codes(n, b[0]);
+          mask(n, x[0], b[0]);
+          put(n, x[0], b[0]);
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < kPer; ++n) {
+          if (!fills) break;
+          put(n, x[n], b[n]);
         }
       }
       fence_proxy_async_smem();
@@ -564,6 +630,10 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
         }
       }
     }
+    };
+    // (a loop for each)
+    if (wide_top) all_parts(std::true_type{});
+    else all_parts(std::false_type{});
     // never leave with a copy in flight
     if constexpr (BITS == 4) cp_async_wait<0>();
     if (lane == 0) {
@@ -608,7 +678,6 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     // more than these 128x64x32 products take.
     if (!*abort_flag) {
       constexpr uint32_t idS = idesc_fmt0_f32(kM, kN, false);
-      constexpr uint32_t idO = idesc_fmt0_f32(kM, D, true);
       const bool el = elect_one();
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       auto wait = [&](int b, int slots, int i) {
@@ -644,6 +713,10 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
         // V slot as an MN-major B operand: 16 tokens per step (2048 bytes), the two 64-dim halves
         // kHalf apart (leading offset), 8-token groups 1024 bytes apart (stride)
         const uint64_t dv0 = smem_desc_sw128(sV, kHalf, 1024);
+        auto all_products = [&](auto wide_span) {
+        constexpr bool kWide = decltype(wide_span)::value;
+        constexpr uint32_t idO = kWide ? idesc_bf16_f32(kM, D, true) : idesc_fmt0_f32(kM, D, true);
+        constexpr int kTerms = kWide ? 2 : 1;  // of P, 8 columns each for 16 tokens
         for (int i = 0; i < n_tiles; ++i) {
           if (i % kSlotTiles == 0 && !wait(kBarVFull, kVSlots, i / kSlotTiles)) break;
           if (!wait(kBarPFull, kSBufs, i)) break;
@@ -652,9 +725,9 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
           const int st = i / kSlotTiles % kVSlots;
           const uint64_t dv = dv0 + (uint64_t)((st * Lay::kSlot + i % kSlotTiles * (kN / 16) * 2048) >> 4);
 #pragma unroll
-          for (int ks = 0; ks < kN / 16; ++ks)
+          for (int ks = 0; ks < kN / 16 * kTerms; ++ks)
             if (el)
-              umma_f16_ts(tm + kColO, pa + (uint32_t)(ks * 8), dv + (uint64_t)((ks * 2048) >> 4), idO,
+              umma_f16_ts(tm + kColO, pa + (uint32_t)(ks * 8), dv + (uint64_t)((ks / kTerms * 2048) >> 4), idO,
                           (i > 0 || ks > 0) ? 1u : 0u);
           if (el) {
             umma_commit(bar(kBarPvDone + i % kSBufs));
@@ -663,6 +736,9 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
           __syncwarp();
           committed += 1;
         }
+        };
+        if (*v_top) all_products(std::true_type{});
+        else all_products(std::false_type{});
       }
       // drain: every tcgen05 op the elected lane issued completes before the CTA frees TMEM
       if (committed > 0 && el) {
@@ -697,21 +773,11 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     float* mpub = reinterpret_cast<float*>(smem + kOffMPub) + quad * 64;  // [tile parity][lane]
     const float scale = p.scale_log2 * units[r];
     float m_own = -INFINITY;   // max (of z, base 2) used for this warp's latest tile
-    float l = 0.f;             // this warp's share of the row sum, over 2^(m_own - kShift - least), or, wide, 2^n
-    float n = -INFINITY;
+    float l = 0.f;             // this warp's share of the row sum, over 2^(m_own - shift - least)
     bool ok = !*abort_flag;
-    uint32_t v_min = 0xffffffffu, v_max = 0u;
-    auto span_of = [&](uint32_t x) {
-      v_min = min(v_min, x - 1u);  // (0: no tile there)
-      v_max = max(v_max, x);
-    };
-#pragma unroll
-    for (int k = 0; k < kSpan; ++k) span_of(v_bits[k]);
-    for (int i = lane + 32 * kSpan; ok && i < n_tiles; i += 32) span_of(v_scale_bits(i));
-    v_min = __reduce_min_sync(0xffffffffu, v_min) + 1u;
-    const bool wide = __reduce_max_sync(0xffffffffu, v_max) - v_min > kWideSpan << 23;
-    // log2 of the piece's smallest V scale
-    const float least = BITS == 8 ? lg2_approx(__uint_as_float(v_min)) : (float)((int)(v_min >> 23) - 127);
+    const int wide_top = (int)*v_top;
+    // log2 of the piece's smallest V scale; wide: P has no power of two of V's scales
+    const float least = wide_top ? 0.f : BITS == 8 ? lg2_approx(__uint_as_float(*v_least)) : (float)((int)(*v_least >> 23) - 127);
     // (a loop for each: in one loop the untaken branch cost 2 % of a 16K prefix)
     auto all_tiles = [&](auto wide_span) {
       constexpr bool kWide = decltype(wide_span)::value;
@@ -721,10 +787,10 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
         float ca, cb;
         if constexpr (BITS == 8) {
           ca = scale * ks;
-          cb = lg2_approx(vs);
+          cb = lg2_approx(kWide ? __uint_as_float((__float_as_uint(vs) & 0x7fffffu) | 0x3f800000u) : vs);
         } else {
           ca = scale * kv4_unit(ks);
-          cb = (float)((int)vs - 127);
+          cb = kWide ? 0.f : (float)((int)vs - 127);
         }
         ca = fmaxf(ca, FLT_MIN);
         if (i + 2 < n_tiles) load_scales(i + 2);
@@ -742,17 +808,28 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
         tc_fence_after();
         const int valid = min(kN, t1 - t0 - i * kN);               // tokens of the tile in range
         const uint32_t ts = tmem + lane_off + (uint32_t)(sb * kN);
-        uint32_t u[2][32];
-        GRANIKV_TMEM_LD32(ts, u[0]);
-        GRANIKV_TMEM_LD32(ts + 32, u[1]);
-        tmem_wait_ld();
-        if (valid < kN) {  // masked keys: -inf, so their weight is 0
-#pragma unroll
-          for (int k = 0; k < kN; ++k) u[k >> 5][k & 31] = k < valid ? u[k >> 5][k & 31] : 0xff800000u;
-        }
-        // row max of z (the factor is positive)
+        // row max of z (the factor is positive); masked keys: -inf, so their weight is 0
+        [[maybe_unused]] uint32_t u[2][32];
         float mx;
-        {
+        if constexpr (kWide) {
+          mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < kN / 16; ++c) {
+            uint32_t x[16];
+            tmem_ld16(ts + c * 16, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) mx = fmaxf(mx, c * 16 + k < valid ? __uint_as_float(x[k]) : -INFINITY);
+          }
+          mx = mx * ca + cb;
+        } else {
+          GRANIKV_TMEM_LD32(ts, u[0]);
+          GRANIKV_TMEM_LD32(ts + 32, u[1]);
+          tmem_wait_ld();
+          if (valid < kN) {
+#pragma unroll
+            for (int k = 0; k < kN; ++k) u[k >> 5][k & 31] = k < valid ? u[k >> 5][k & 31] : 0xff800000u;
+          }
           float t[22], w[7];
           auto sv = [&](int k) { return __uint_as_float(u[k >> 5][k & 31]); };
 #pragma unroll
@@ -794,53 +871,64 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
           }
           tmem_wait_st();
         }
-        if constexpr (kWide) {  // S(i) once more, for the row sum over its own maximum
-          const float top = fmaxf(n, mx - cb);
-          l *= ex2_approx(n - top);
-          n = top;
-#pragma unroll 1
-          for (int c = 0; c < kN / 16; ++c) {
-            uint32_t x[16];
-            tmem_ld16(ts + c * 16, x);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) l += c * 16 + k < valid ? ex2_approx(fmaf(__uint_as_float(x[k]), ca, -n)) : 0.f;
-          }
-        } else if (m_own != m_i && m_own != -INFINITY) {
-          l *= ex2_approx(m_own - m_i);
-        }
+        if (m_own != m_i && m_own != -INFINITY) l *= ex2_approx(m_own - m_i);
         m_own = m_i;
-        // P = 2^(z - m + kShift), packed two per 32-bit column and written over columns [0, 32) of the
-        // S(i) buffer, whose 64 columns are in registers
+        // P = 2^(z - m + shift), packed two per 32-bit column and written over columns [0, 32) of the
+        // S(i) buffer, whose 64 columns are in registers; wide: 16 tokens at a time, the nearest bf16 over the first 8 columns
+        // of their S and what that leaves out over the others
         const float m_use = m_i == -INFINITY ? 0.f : m_i;
         {
-          const float off = cb - m_use + kShift;
-          const uint64_t scale2 = f2_pack(ca, ca), nm2 = f2_pack(off, off);
-          uint64_t acc[2] = {0ull, 0ull};  // packed partial sums (0.0f bit patterns)
-          uint32_t pk[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const float sa = __uint_as_float(u[k >> 4][(2 * k) & 31]);
-            const float sb2 = __uint_as_float(u[k >> 4][(2 * k + 1) & 31]);
-            const uint64_t x = f2_fma(f2_pack(sa, sb2), scale2, nm2);
-            float xa, xb;
-            f2_unpack(x, xa, xb);
-            const float ea = ex2_approx(xa), eb = ex2_approx(xb);
-            acc[k & 1] = f2_add(acc[k & 1], f2_pack(ea, eb));
-            pk[k] = pack_f16(ea, eb);
-          }
-          GRANIKV_TMEM_ST32(ts, pk);
+          const float off = cb - m_use + (kWide ? kWideShift : kShift);
           float la, lb;
-          f2_unpack(f2_add(acc[0], acc[1]), la, lb);
-          // over vs, by the very logarithm that P has
-          if constexpr (!kWide) l += (la + lb) * ex2_approx(least - cb);
+          if constexpr (kWide) {
+            la = lb = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < kN / 16; ++c) {
+              uint32_t x[16];
+              tmem_ld16(ts + c * 16, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int t = c * 16 + 2 * k;
+                const float ea = t < valid ? ex2_approx(fmaf(__uint_as_float(x[2 * k]), ca, off)) : 0.f;
+                const float eb = t + 1 < valid ? ex2_approx(fmaf(__uint_as_float(x[2 * k + 1]), ca, off)) : 0.f;
+                la += ea, lb += eb;
+                const __nv_bfloat162 hi = __floats2bfloat162_rn(ea, eb);
+                const float2 h = __bfloat1622float2(hi);
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(ea - h.x, eb - h.y);
+                x[2 * k] = *reinterpret_cast<const uint32_t*>(&hi);
+                x[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&lo);
+              }
+              const uint32_t parts[16] = {x[0], x[2], x[4], x[6], x[8], x[10], x[12], x[14], x[1], x[3], x[5], x[7], x[9], x[11], x[13], x[15]};
+              tmem_st16(ts + c * 16, parts);
+            }
+          } else {
+            const uint64_t scale2 = f2_pack(ca, ca), nm2 = f2_pack(off, off);
+            uint64_t acc[2] = {0ull, 0ull};  // packed partial sums (0.0f bit patterns)
+            uint32_t pk[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const float sa = __uint_as_float(u[k >> 4][(2 * k) & 31]);
+              const float sb2 = __uint_as_float(u[k >> 4][(2 * k + 1) & 31]);
+              const uint64_t x = f2_fma(f2_pack(sa, sb2), scale2, nm2);
+              float xa, xb;
+              f2_unpack(x, xa, xb);
+              const float ea = ex2_approx(xa), eb = ex2_approx(xb);
+              acc[k & 1] = f2_add(acc[k & 1], f2_pack(ea, eb));
+              pk[k] = pack_f16(ea, eb);
+            }
+            GRANIKV_TMEM_ST32(ts, pk);
+            f2_unpack(f2_add(acc[0], acc[1]), la, lb);
+          }
+          // over vs (wide: its significand), by the very logarithm that P has
+          l += (la + lb) * ex2_approx(least - cb);
         }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(bar(kBarPFull + sb));
       }
     };
-    if (wide) all_tiles(std::true_type{});
+    if (wide_top) all_tiles(std::true_type{});
     else all_tiles(std::false_type{});
     // epilogue: wait for the last PV, combine the two warps' row sums (each with its exponent), normalise
     // (O is relative to the last tile's max), write the record
@@ -856,9 +944,11 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     // (the codes' slots, where these go, are idle once the last PV is done; a CTA that gave up may
     // still have a copy in flight there, and then writes nothing)
     const bool safe = ok;
+    const int top_exp = (int)*v_top;
+    const float shift = top_exp ? kWideShift : kShift;
     if (safe) {
       red[par * kM + r] = l;
-      red[2 * kM + par * kM + r] = wide ? n : m_own - kShift - least;
+      red[2 * kM + par * kM + r] = m_own - shift - least;
       red[4 * kM + par * kM + r] = m_own;
     }
     mbar_arrive(bar(pair_bar));
@@ -876,7 +966,10 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
         if (half == 0) atomicCAS(p.err, 0, (int32_t)kDevBadRecord);
         rec = -1;
       }
-      const float inv = 1.f / lt, unit = ex2_approx(m_used - kShift - top);  // (a tile has a valid token)
+      // (a tile has a valid token); wide: V's operands back to their size, by half of the power of two each
+      const int size = top_exp ? top_exp - 127 - kWideTop : 0, half_size = size >> 1;
+      const float inv = 1.f / lt * __uint_as_float((uint32_t)(127 + half_size) << 23);
+      const float unit = ex2_approx(m_used - shift - top) * __uint_as_float((uint32_t)(127 + size - half_size) << 23);
       uint32_t u[D / 64][32];
       GRANIKV_TMEM_LD32(tmem + lane_off + kColO + half * (D / 2), u[0]);
       if constexpr (D == 128) GRANIKV_TMEM_LD32(tmem + lane_off + kColO + half * 64 + 32, u[1]);

@@ -1,0 +1,124 @@
+"""Decode attention and weighing over the packed caches where scales lie far apart, and calls that follow one another:
+against 64 bits on the values held, without the allowance for weights that vanish beside others.
+
+Tolerance of o, with A = sum_t p_t |v_t| of each column over a request's L keys and x the error of a score: a weight is rounded
+by half a step of fp16 (2^-11; none in fp32 contexts), products and sums are fp32 (L 2^-24), a score's error moves its weight
+by x relative and the sum by as much, the exponential and the merge add 2^-20, all relative to A; then the
+rounding to the type (2^-8 or 2^-24).  x = d 2^-24 sum |q_i k_i| / sqrt(d), and what the 8-bit prefix's two parts of q
+leave out: 2^-17 of the row's largest q for elements below 2^-9 of it."""
+
+import math
+
+import numpy as np
+import pytest
+
+from tests.test_gpu_kv4 import Kv4
+from tests.test_gpu_kv8 import Kv8, _gb, _rows, _torch
+
+pytestmark = pytest.mark.gpu
+
+CACHES = {8: Kv8, 4: Kv4}
+
+
+def _exact(c, b):
+    """o [n_kv, g, d] and lse [n_kv, g] of request b in 64 bits, sum p |v|, and a score's error."""
+    K, V = c.keys(b)[:2]
+    q = c.q_host[b].reshape(c.n_kv, -1, c.d)
+    s = np.einsum("jgd,ljd->jgl", q, K) / math.sqrt(c.d)
+    x = c.d * 2.0 ** -24 * np.einsum("jgd,ljd->jgl", np.abs(q), np.abs(K)).max(axis=2) / math.sqrt(c.d)
+    if isinstance(c, Kv8) and c.of[b] >= 0:
+        top = np.abs(q).max(axis=2, keepdims=True)
+        small = np.where(np.abs(q) < 2.0 ** -9 * top, np.minimum(np.abs(q), 2.0 ** -17 * top), 0.0)
+        x = x + np.einsum("jgd,ljd->jgl", small, np.abs(K)).max(axis=2) / math.sqrt(c.d)
+    m = s.max(axis=2, keepdims=True)
+    p = np.exp(s - m)
+    lse = m[..., 0] + np.log(p.sum(axis=2))
+    p /= p.sum(axis=2, keepdims=True)
+    return np.einsum("jgl,ljd->jgd", p, V), lse, np.einsum("jgl,ljd->jgd", p, np.abs(V)), x, K.shape[0]
+
+
+def _check(c, o, lse, what):
+    bf16 = c.dtype == "bf16"
+    for b in range(len(c.lens)):
+        want, want_lse, A, x, L = _exact(c, b)
+        tol = (L * 2.0 ** -24 + 2 * x[..., None] + 2.0 ** -20 + (2.0 ** -11 if bf16 else 0.0)) * A
+        tol += (2.0 ** -8 if bf16 else 2.0 ** -24) * (np.abs(want) + tol)
+        got = o[b].double().cpu().numpy().reshape(want.shape)
+        err = np.abs(got - want)
+        assert (err <= tol).all(), f"{what} request {b}: o off by {np.nanmax(err / tol)} of its tolerance, NaN {np.isnan(got).any()}"
+        err = np.abs(lse[b].double().cpu().numpy().reshape(want_lse.shape) - want_lse)
+        tol = x + L * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -23 * np.abs(want_lse)
+        assert (err <= tol).all(), f"{what} request {b}: lse off by {np.nanmax(err / tol)} of its tolerance"
+
+
+SHAPES = [(8, 32, 8, 128, "bf16"), (4, 32, 8, 128, "bf16"), (4, 32, 8, 64, "bf16"), (4, 8, 2, 64, "f32"), (8, 9, 3, 96, "bf16")]
+
+
+# ---- values far apart ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bits,n_q,n_kv,d,dtype", SHAPES)
+@pytest.mark.parametrize("e", [6, 9, 16, 24, 33, 45, 100])
+@pytest.mark.parametrize("at", [0, 2, 4])
+def test_values_beside_a_block_with_a_weightless_outlier(cuda_ok, bits, n_q, n_kv, d, dtype, e, at):
+    """One token of a slab block has V of 2^e and no weight (its score is 150 below the others', a weight of 2^-216), the block's
+    others have V 0: the output is made of the other blocks' V alone, however far their scales lie below."""
+    row = 64 * at + 17
+
+    def edit(kind, k, v):
+        k[:, :, 0] = 0.0
+        if kind == "prefix":
+            v[64 * at:64 * at + 64] = 0.0
+            k[row], v[row] = 0.0, np.float32(2.0 ** e)
+            k[row, :, 0] = -54.0
+
+    c = CACHES[bits](np.random.default_rng([bits, d, e]), n_q=n_q, n_kv=n_kv, d=d, dtype=dtype, prefixes=[340], of=[0, 0, -1, 0],
+                     lens=[0, 30, 5, 1], edit=edit)
+    c.q[:, :, 0] = 32.0
+    c.q_host[:, :, 0] = 32.0
+    _check(c, *c.decode(), f"{bits} bits, 2^{e} in block {at}")
+
+
+@pytest.mark.parametrize("bits,n_q,n_kv,d,dtype", SHAPES)
+@pytest.mark.parametrize("low", [-100, -40, 0, 20])
+@pytest.mark.parametrize("span", [7, 9, 30, 80, 106])
+def test_values_of_blocks_far_apart(cuda_ok, bits, n_q, n_kv, d, dtype, low, span):
+    """Blocks of V about 2^low and 2^(low + span) in turn, the large ones with V in the lower half of the dims and zeros in the
+    upper half only: in the upper half the small blocks' V is the whole output.  Many blocks, so that pieces have several.
+    (Sums of 2,000 unnormalised weights times V stay within fp32.)"""
+    if low + span > 106:
+        pytest.skip("V itself would pass fp32")
+    def edit(kind, k, v):
+        if kind == "prefix":
+            at = np.arange(len(v)) // 64 % 2 == 0
+            v *= np.float32(2.0 ** low)
+            v[at] *= np.float32(2.0 ** span)
+            v[at, :, d // 2:] = 0.0
+        else:
+            v *= np.float32(2.0 ** low)
+
+    c = CACHES[bits](np.random.default_rng([bits, d, span]), n_q=n_q, n_kv=n_kv, d=d, dtype=dtype, prefixes=[2000], of=[0, 0, 0],
+                     lens=[0, 3, 40], edit=edit)
+    _check(c, *c.decode(), f"{bits} bits, 2^{low} and 2^{span} above")
+
+
+@pytest.mark.parametrize("bits,d", [(8, 128), (4, 128), (4, 64)])
+@pytest.mark.parametrize("zero", ["first", "last", "most"])
+def test_values_beside_zero_blocks_in_long_pieces(cuda_ok, bits, d, zero):
+    """Pieces of many tiles (160 requests of 64 heads make 80 row blocks) where some blocks' V is all zero."""
+    L = 5000
+
+    def edit(kind, k, v):
+        if zero == "most":
+            v[: 40 * 64], v[42 * 64:] = 0.0, 0.0
+        else:
+            v[slice(0, 64) if zero == "first" else slice(L // 64 * 64, L)] = 0.0
+
+    c = CACHES[bits](np.random.default_rng([bits, d]), n_q=64, n_kv=8, d=d, dtype="bf16", prefixes=[L], of=[0] * 160, lens=[0] * 160, edit=edit)
+    assert c.ctx.dispatch(c.batch).groups()[0]["n_splits"] <= 2
+    o, lse = c.decode()
+    rows = [0, 1, 15, 16, 17, 80, 158, 159]
+    c.of, c.lens, c.q_host = [0] * len(rows), [0] * len(rows), c.q_host[rows]
+    c.ck, c.cv = c.ck[:len(rows)], c.cv[:len(rows)]
+    if bits == 4:
+        c.cu = c.cu[:len(rows)]
+    _check(c, o[rows], lse[rows], f"{bits} bits, zeros {zero}")
