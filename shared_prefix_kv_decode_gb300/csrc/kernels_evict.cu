@@ -350,8 +350,10 @@ __global__ void __launch_bounds__(256, WeighUnit<BITS, D>::kBlocks) weigh_mma_ke
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[e] += s2[e];
       // a head without weight (lse -inf, or past the group) adds 2^-inf = 0, whatever its score
-      w0 += (e0 == -INFINITY ? 0.f : exp2f(s[0] * (c0 * sa) + e0)) + (e1 == -INFINITY ? 0.f : exp2f(s[1] * (c1 * sa) + e1));
-      w1 += (e0 == -INFINITY ? 0.f : exp2f(s[2] * (c0 * sb) + e0)) + (e1 == -INFINITY ? 0.f : exp2f(s[3] * (c1 * sb) + e1));
+      const float a0 = score_factor<BITS>(c0, sa), a1 = score_factor<BITS>(c1, sa);
+      const float b0 = score_factor<BITS>(c0, sb), b1 = score_factor<BITS>(c1, sb);
+      w0 += (e0 == -INFINITY ? 0.f : exp2f(s[0] * a0 + e0)) + (e1 == -INFINITY ? 0.f : exp2f(s[1] * a1 + e1));
+      w1 += (e0 == -INFINITY ? 0.f : exp2f(s[2] * b0 + e0)) + (e1 == -INFINITY ? 0.f : exp2f(s[3] * b1 + e1));
     }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {

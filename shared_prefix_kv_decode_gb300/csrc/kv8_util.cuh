@@ -6,6 +6,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cfloat>
 #include <cstdint>
 
 #include "internal.h"
@@ -86,6 +87,14 @@ __device__ __forceinline__ void q_to_f16(uint32_t* w, float& unit) {
 // The scores of an infinity may all be -inf, which looks like a row without keys.
 __device__ __forceinline__ float q_no_inf(float x) { return fmaf(0.f, x, x); }
 __device__ __forceinline__ __half2 q_no_inf(__half2 x) { return __hfma2(__floats2half2_rn(0.f, 0.f), x, x); }
+// What a score is multiplied by: q's factor times a key's scale (BITS 0: 1), at most the largest number: a score of 0 stays 0
+// where the two pass fp32.  In 4 bits the scale is a power of two, and rounding the product towards zero only does
+// that: the weighing of 200K tokens takes 44.0 us so, with a minimum 44.4, with neither 43.1.
+template <int BITS>
+__device__ __forceinline__ float score_factor(float f, float scale) {
+  if constexpr (BITS == 4) return __fmul_rz(f, scale);
+  else return fminf(f * scale, FLT_MAX);
+}
 
 // A partial row's log-sum-exp as the merge takes it: -inf for a row without weight, +inf for one whose
 // weights hold a NaN (the merge's maximum passes over a NaN; +inf makes the whole row NaN).

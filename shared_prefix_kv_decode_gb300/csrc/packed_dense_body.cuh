@@ -783,7 +783,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
       constexpr bool kWide = decltype(wide_span)::value;
       for (int i = par; ok && i < n_tiles; i += 2) {
         const int sb = i % kSBufs;
-        // (at least the smallest normal number: 0 * -inf of a masked key would be NaN)
+        // (from the smallest normal number to the largest: 0 * -inf of a masked key and inf * 0 of a score would be NaN)
         float ca, cb;
         if constexpr (BITS == 8) {
           ca = scale * ks;
@@ -792,7 +792,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
           ca = scale * kv4_unit(ks);
           cb = kWide ? 0.f : (float)((int)vs - 127);
         }
-        ca = fmaxf(ca, FLT_MIN);
+        ca = fminf(fmaxf(ca, FLT_MIN), FLT_MAX);
         if (i + 2 < n_tiles) load_scales(i + 2);
         // the max used for tile i-1, decided by the other warp of the quarter
         float m_prev = -INFINITY;

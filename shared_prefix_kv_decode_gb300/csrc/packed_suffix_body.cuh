@@ -448,10 +448,10 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
           la[v] -= 127.f;
           lb[v] -= 127.f;
         }
-        s[v][0] = in_a ? (s[v][0] + s2[v][0]) * (f0 * sa[v]) : -INFINITY;
-        s[v][1] = in_a ? (s[v][1] + s2[v][1]) * (f1 * sa[v]) : -INFINITY;
-        s[v][2] = in_b ? (s[v][2] + s2[v][2]) * (f0 * sb[v]) : -INFINITY;
-        s[v][3] = in_b ? (s[v][3] + s2[v][3]) * (f1 * sb[v]) : -INFINITY;
+        s[v][0] = in_a ? (s[v][0] + s2[v][0]) * score_factor<BITS>(f0, sa[v]) : -INFINITY;
+        s[v][1] = in_a ? (s[v][1] + s2[v][1]) * score_factor<BITS>(f1, sa[v]) : -INFINITY;
+        s[v][2] = in_b ? (s[v][2] + s2[v][2]) * score_factor<BITS>(f0, sb[v]) : -INFINITY;
+        s[v][3] = in_b ? (s[v][3] + s2[v][3]) * score_factor<BITS>(f1, sb[v]) : -INFINITY;
         mx0 = max3f(mx0, s[v][0] + la[v], s[v][2] + lb[v]);
         mx1 = max3f(mx1, s[v][1] + la[v], s[v][3] + lb[v]);
       }

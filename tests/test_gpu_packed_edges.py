@@ -122,3 +122,34 @@ def test_values_beside_zero_blocks_in_long_pieces(cuda_ok, bits, d, zero):
     if bits == 4:
         c.cu = c.cu[:len(rows)]
     _check(c, o[rows], lse[rows], f"{bits} bits, zeros {zero}")
+
+
+# ---- factors of scores beyond fp32 --------------------------------------------------------------
+
+@pytest.mark.parametrize("bits,n_q,n_kv,d,dtype", [(8, 32, 8, 128, "bf16"), (4, 32, 8, 128, "bf16"), (4, 32, 8, 64, "bf16"),
+                                                   (8, 24, 2, 128, "bf16"), (4, 24, 2, 128, "bf16"), (4, 8, 2, 64, "f32")])
+@pytest.mark.parametrize("size", [2.0 ** 20, 2.0 ** 60, 2.0 ** 110])
+def test_large_queries_over_large_keys_of_other_dims(cuda_ok, bits, n_q, n_kv, d, dtype, size):
+    """q and K are large, each in dims where the other is zero: all scores are exactly 0, all weights equal, although the
+    product of q's and K's scales may pass fp32."""
+    def edit(kind, k, v):
+        k *= np.float32(size)
+        k[:, :, :16] = 0.0
+
+    c = CACHES[bits](np.random.default_rng([bits, d, 5]), n_q=n_q, n_kv=n_kv, d=d, dtype=dtype, prefixes=[150], of=[0, 0, -1, -1],
+                     lens=[0, 20, 33, 1], edit=edit)
+    c.q[:, :, 16:] = 0.0
+    c.q *= size
+    c.q_host = c.q.double().cpu().numpy()
+    o, lse = c.decode()
+    batch = _gb().Batch([c.slabs[i] if i >= 0 else -1 for i in c.of], c.lens, c.table, c.cap, c.live)
+    weight = _torch().zeros(4, c.cap, device="cuda")
+    c.ctx.cold_weigh(0, c.q, lse, batch, weight, 0.0)
+    c.ctx.sync_status()
+    c.q_host = np.zeros_like(c.q_host)  # (the same scores, with no error)
+    _check(c, o, lse, f"{bits} bits, {size}")
+    for b, n in enumerate(c.lens):
+        keys = n + (150 if c.of[b] >= 0 else 0)
+        # exp(-lse) over n_q heads: lse to its tolerance above, the exponential and the sum 2^-20 and n_q 2^-24
+        tol = n_q / keys * (keys * 2.0 ** -24 + 2.0 ** -19 + 2.0 ** -23 * math.log(keys) + n_q * 2.0 ** -24)
+        assert (weight[b, :n].double() - n_q / keys).abs().max().item() <= tol if n else True
