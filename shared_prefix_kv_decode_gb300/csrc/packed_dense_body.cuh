@@ -773,7 +773,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     float* mpub = reinterpret_cast<float*>(smem + kOffMPub) + quad * 64;  // [tile parity][lane]
     const float scale = p.scale_log2 * units[r];
     float m_own = -INFINITY;   // max (of z, base 2) used for this warp's latest tile
-    float l = 0.f;             // this warp's share of the row sum, over 2^(m_own - shift - least)
+    float l = 0.f;             // this warp's share of the row sum, over 2^(m_own - (shift + least))
     bool ok = !*abort_flag;
     const int wide_top = (int)*v_top;
     // log2 of the piece's smallest V scale; wide: P has no power of two of V's scales
@@ -948,7 +948,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     const float shift = top_exp ? kWideShift : kShift;
     if (safe) {
       red[par * kM + r] = l;
-      red[2 * kM + par * kM + r] = m_own - shift - least;
+      red[2 * kM + par * kM + r] = m_own - (shift + least);
       red[4 * kM + par * kM + r] = m_own;
     }
     mbar_arrive(bar(pair_bar));

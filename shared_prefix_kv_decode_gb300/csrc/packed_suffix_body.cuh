@@ -12,10 +12,13 @@
 // a small V scale cannot push the weights of the others out of fp16's range.  P carries a factor of
 // 2^14 (it is at most 2^14), so that fp16 keeps its 11 bits down to weights of 2^-28; m, the sums and
 // O are fp32.
-// The row sum adds 2^(y - m + 10).  A scale lies between 2^-104.9 (of zeros) and 2^119.2, so y - m is at most 104.9, and
-// the 4,096 tokens a CTA may have sum to less than 2^127; the heaviest token has y - m of -119.2 or more, so what it
-// adds is a normal number, and a weight down to 2^-40 of it a subnormal one.  (P / vs in place of this exponential
-// would lose the tokens whose P underflows, and with P's factor overflow on 600 zero rows.)
+// The row sum adds 2^(y - m - 6).  y - m is about -log2 vs, 6 to 8 for V of size 1, so these terms are near 1 and the
+// exponents near 0, which is what lse's accuracy hangs on: at 2^(y - m + 10) the roundings of exponents and logarithm near 18 put
+// lse of a single token 3.7e-7 off (root mean square), so 0.9e-7.  A scale lies between 2^-104.9 (of zeros) and 2^119.2, so
+// y - m is at most 104.9, and the 4,096 tokens a CTA may have sum to less than 2^127; the heaviest token has y - m of
+// -119.2 or more, so what it adds is a normal number, and a weight down to 2^-23 of it a subnormal one (at V scales 2^17 below the
+// largest, to 2^-40).  (P / vs in place of this exponential would lose the tokens whose P underflows, and with P's factor
+// overflow on 600 zero rows.)
 // ldmatrix moves 16-bit pairs, here two codes: a lane's 4 codes of a row serve one k-step of S^T in
 // a permuted order of head_dim (q is loaded in the same order), and the transposed form gives two
 // tokens x two dims, which one byte permutation turns into the two A registers of O^T's dims 2 r
@@ -36,9 +39,8 @@
 // into fp16 exactly (one conversion and one product a pair), u takes the place of the scales ks and vs above, so
 // log2 vs is a whole number.  The 16-bit pairs that ldmatrix moves are four codes: a lane's eight codes of a row serve
 // two k-steps of S^T, and the transposed form gives two tokens x four dims, whose fp16 values are paired by byte permutations.
-// u lies between 2^-100 and 2^116, inside the range that the row sum is made for.
-// lse of a single token is 2.6e-6 of its size off (fp32 products on CUDA cores: 4e-8): the additions of the matrix
-// instructions, which S goes through; adding up m and log2 l more exactly changes nothing.
+// u lies between 2^-100 and 2^116 and is about 2^-9 for V of size 1: the row sum adds 2^(y - m - 8) (root mean square of lse's
+// error on a single token 1.0e-7; at + 10, 3.8e-7), the heaviest token 2^-124 or more.
 // 11 stages (heads of 64: 20).  128 requests of 550 tokens take 30.2 us (8 bits: 31.5), 16 of 7,500 42.9 (46.5); with
 // every row in L2 those 16 take 40.6, and their loads alone 28.4: bound by the consumers' instructions, with
 // the conversions and the byte permutations that pair V's tokens on the busiest pipe (54 % of its cycles).
@@ -83,7 +85,8 @@ struct Layout {
 };
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kShift = 14.f;                     // log2 of the factor that P carries
-constexpr float kSumShift = 10.f;                  // and that the row sum does
+template <int BITS>
+constexpr float kSumShiftOf = BITS == 8 ? -6.f : -8.f;  // and that the row sum does
 static_assert(kSuffixMaxCtaTokens <= 4096, "the row sum's range");
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -152,6 +155,7 @@ template <int BITS, int D, bool kSplitRegs>
 __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const int32_t* __restrict__ cta_begin, int cta,
                                                 int group, unsigned char* smem) {
   using Lay = Layout<BITS, D>;
+  constexpr float kSumShift = kSumShiftOf<BITS>;
   constexpr int kStages = Lay::kStages, kTileBytes = Lay::kTileBytes, kStageBytes = Lay::kStageBytes, kRowStride = Lay::kRowStride;
   constexpr int kOffSlots = Lay::kOffSlots, kOffSegs = Lay::kOffSegs, kOffBar = Lay::kOffBar;
   const int warp = threadIdx.x >> 5;

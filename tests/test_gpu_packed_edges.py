@@ -153,3 +153,31 @@ def test_large_queries_over_large_keys_of_other_dims(cuda_ok, bits, n_q, n_kv, d
         # exp(-lse) over n_q heads: lse to its tolerance above, the exponential and the sum 2^-20 and n_q 2^-24
         tol = n_q / keys * (keys * 2.0 ** -24 + 2.0 ** -19 + 2.0 ** -23 * math.log(keys) + n_q * 2.0 ** -24)
         assert (weight[b, :n].double() - n_q / keys).abs().max().item() <= tol if n else True
+
+
+# ---- lse of few keys ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bits,d,where", [(8, 128, "cold"), (4, 128, "cold"), (4, 64, "cold"), (4, 128, "prefix"), (4, 64, "prefix")])
+def test_lse_of_one_key_whose_score_is_one_product(cuda_ok, bits, d, where):
+    """One key, and one dim where q and K are not zero: the score takes no addition, and lse is the score.  V is about 1 (its
+    largest 2 to 16).  Bounds of the errors, in base 2.  COLD: the row sum is e^2 with an argument below 2 of e, rounded by 2^-24,
+    twice: 2^-23; the exponential by 2^-22 of e, 1.45 * 2^-21 in the logarithm; that of a sum in [2^-4, 2^4] by 2^-22.  Prefix:
+    three sums below 8 by 2^-22 each, the exponential 1.45 * 2^-22, the logarithm near 7 by 2^-21.  Both: factors of the
+    score and the way to base e, 5 * 2^-24 of lse.  None has a preferred sign: over 1,920 heads their root mean square
+    is that of errors spread evenly up to the bounds, 3^-1/2 of them."""
+    def edit(kind, k, v):
+        x = k[:, :, 5].copy()
+        k[:] = 0.0
+        k[:, :, 5] = x
+
+    B = 60
+    c = CACHES[bits](np.random.default_rng([bits, d, 6]), n_q=32, n_kv=8, d=d, dtype="bf16", prefixes=[1], of=[0 if where == "prefix" else -1] * B,
+                     lens=[0 if where == "prefix" else 1] * B, edit=edit)
+    _, lse = c.decode()
+    want = np.stack([_exact(c, b)[1].reshape(-1) for b in range(B)])
+    err = np.abs(lse.double().cpu().numpy() - want)
+    bounds = [2.0 ** -23, 1.45 * 2.0 ** -21, 2.0 ** -22] if where == "cold" else [2.0 ** -22] * 3 + [1.45 * 2.0 ** -22, 2.0 ** -21]
+    bounds = math.log(2) * np.array(bounds)
+    assert (err <= bounds.sum() + 5 * 2.0 ** -24 * np.abs(want)).all()
+    rms = np.sqrt((bounds ** 2).sum() + (5 * 2.0 ** -24 * want) ** 2)
+    assert math.sqrt((err ** 2).mean()) <= math.sqrt((rms ** 2).mean() / 3), math.sqrt((err ** 2).mean())
