@@ -122,6 +122,7 @@ struct Layout {
   static constexpr int kHead = D * BITS / 8;              // bytes of a head's codes
   static constexpr int kScale = D / kKv4Group;            // 4 bits: of its scales
   static constexpr int kCSlotBytes = kPart * (kHead + (BITS == 8 ? 0 : kScale));
+  static constexpr int kRedBytes = 6 * kM * 4;            // the epilogue's sums, exponents and maxima
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kOffK + kKSlots * kKSlotBytes;
   static constexpr int kOffCodes = kOffV + kVSlots * kSlot;
@@ -131,7 +132,7 @@ struct Layout {
   static constexpr int kBarArea = BITS == 8 ? 512 : 640;
   static constexpr int kSmemBytes = kOffBar + kBarArea + 1024;  // + alignment slack
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-  static_assert(kConvWarps * kCSlots * kCSlotBytes >= 6 * kM * 4, "the epilogue's sums and maxima");
+  static_assert(kFill * kCSlots * kCSlotBytes >= kRedBytes, "the epilogue's sums and maxima lie in rings whose parts fill every content's first tile");
   // barriers
   static constexpr int kBarKFull = 0;                            // [kKSlots] TMA (4 bits: conversion, kFill arrivals) -> MMA
   static constexpr int kBarKEmpty = kBarKFull + kKSlots;         // [kKSlots] MMA (S of the slot's tiles done) -> TMA (conversion)
@@ -296,7 +297,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
   const uint32_t base = (raw_u + 1023u) & ~1023u;
   unsigned char* smem = smem_raw + (base - raw_u);
   const uint32_t sK = base + kOffK, sV = base + kOffV, sC = base + kOffCodes;
-  // row sums, exponents and maxima for the epilogue, [kind][parity][row], in the codes' place (idle by then)
+  // row sums, exponents and maxima for the epilogue, [kind][parity][row], in the first codes' place (idle by then)
   float* red = reinterpret_cast<float*>(smem + kOffCodes);
   float* units = reinterpret_cast<float*>(smem + kOffUnit);
   const uint32_t sBar = base + kOffBar;
@@ -941,8 +942,10 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     // swap the row sums, exponents and maxima with the other warp at the pair barrier; a warp that left the
     // tile loop early may stop waiting for published maxima, so its partner's bounded waits give
     // up and both skip the record
-    // (the codes' slots, where these go, are idle once the last PV is done; a CTA that gave up may
-    // still have a copy in flight there, and then writes nothing)
+    // (they go into the rings of the first kFill conversion warps.  Those have read all their codes once the last PV is done:
+    // their parts belong to the first tile of each content, which some product waited for.  The other parts' last
+    // content may have no tile, and its copies may still be landing.  A CTA that gave up may have copies in flight
+    // in any ring, and writes nothing)
     const bool safe = ok;
     const int top_exp = (int)*v_top;
     const float shift = top_exp ? kWideShift : kShift;
