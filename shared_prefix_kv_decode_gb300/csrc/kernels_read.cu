@@ -1,5 +1,10 @@
 // kernels_read.cu -- rows of a pool back as [N, n_kv, d]: of a 16- or 32-bit pool as they are, of a packed one as
-// the values that its codes and scales stand for, rounded once.  (4 bits: exact in bf16 and fp32.)
+// the values that its codes and scales stand for, rounded once.
+// 4 bits: exact in bf16 and fp32.  8 bits: code times scale in fp32, then to the type, which for bf16 gives what one
+// rounding of the product gives.  A block's scale is a / 448 = a / 7 / 64 with a of 8 significant bits (rounded by 2^-24).  With c the
+// code's 4 bits, c a / 7 differs from a point halfway between two bf16 values (9 bits) by 1 / (2 c a) >= 2^-13 of itself at
+// least, far more than fp32 rounds; or equals it, only if 7 divides a (a point of 9 bits is not 1 or 2 times a), and
+// then scale and product are exact.
 #include "kv4_util.cuh"
 #include "launch_util.cuh"
 #include "tc_util.cuh"

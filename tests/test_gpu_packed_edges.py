@@ -181,3 +181,35 @@ def test_lse_of_one_key_whose_score_is_one_product(cuda_ok, bits, d, where):
     assert (err <= bounds.sum() + 5 * 2.0 ** -24 * np.abs(want)).all()
     rms = np.sqrt((bounds ** 2).sum() + (5 * 2.0 ** -24 * want) ** 2)
     assert math.sqrt((err ** 2).mean()) <= math.sqrt((rms ** 2).mean() / 3), math.sqrt((err ** 2).mean())
+
+
+# ---- reading back -------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("n_kv,d", [(8, 128), (2, 64)])
+def test_8_bit_rows_read_back_as_the_nearest_values(cuda_ok, n_kv, d):
+    """bf16, bit for bit: code times scale rounded once, over every significand that a bf16 block's largest element may have."""
+    torch, gb, rng = _torch(), _gb(), np.random.default_rng([n_kv, d, 8])
+    import oracle.kv8 as K8
+    N = 400
+    rows = torch.from_numpy(_rows(rng, N, n_kv, d, "bf16"))
+    top = (1.0 + (torch.arange(N * n_kv) % 128) / 128.0).view(N, n_kv) * 2.0 ** torch.from_numpy(rng.integers(-20, 20, (N, n_kv))).float()
+    rows = rows / rows.abs().amax(dim=2, keepdim=True) * top[..., None] * 0.99
+    rows[:, :, 3] = top
+    x = rows.to(torch.bfloat16).cuda()
+    pools = [torch.full((2 * N + 10, gb.kv8_row_bytes(n_kv, d)), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    ctx = gb.Context(n_layers=1, n_q=n_kv, n_kv=n_kv, head_dim=d, dtype=gb.DTYPE_BF16, n_slots=2 * N + 10, k_pools=pools[:1], v_pools=pools[1:],
+                     hot_fraction=(N + 5.5) / (2 * N + 10), kv8=True)
+    sid, _ = ctx.hot_alloc(N)
+    ctx.hot_fill(0, sid, x, x)
+    slots = torch.arange(N + 6, 2 * N + 6, dtype=torch.int32, device="cuda")
+    ctx.cold_append(0, x, x, slots, N)
+    for block in (K8.BLOCK, 1):
+        k, v = torch.empty_like(x), torch.empty_like(x)
+        if block == 1:
+            ctx.cold_read(0, slots, N, k, v)
+        else:
+            ctx.hot_read(0, sid, 0, N, k, v)
+        ctx.sync_status()
+        m, e = np.frexp(K8.through_cache(x.float().cpu().numpy(), block))
+        want = np.ldexp(np.rint(m * 256.0), e - 8)
+        assert np.array_equal(k.double().cpu().numpy(), want) and np.array_equal(v.double().cpu().numpy(), want)
