@@ -213,3 +213,39 @@ def test_8_bit_rows_read_back_as_the_nearest_values(cuda_ok, n_kv, d):
         m, e = np.frexp(K8.through_cache(x.float().cpu().numpy(), block))
         want = np.ldexp(np.rint(m * 256.0), e - 8)
         assert np.array_equal(k.double().cpu().numpy(), want) and np.array_equal(v.double().cpu().numpy(), want)
+
+
+# ---- calls that follow one another --------------------------------------------------------------
+
+@pytest.mark.parametrize("bits,n_q,n_kv,d,dtype", [(8, 32, 8, 128, "bf16"), (4, 32, 8, 128, "bf16"), (4, 32, 8, 64, "bf16"), (4, 8, 2, 64, "f32")])
+def test_appends_back_to_back_in_a_graph(cuda_ok, bits, n_q, n_kv, d, dtype):
+    """A dozen calls that each write other rows into the same newest slots and attend them, one after the other on one
+    workspace, with a prefix that fills the SMs, and replayed: every one's result is that of the same call made alone."""
+    torch, rng = _torch(), np.random.default_rng([bits, d, 42])
+    B = 64
+    lens = [int(n) for n in rng.integers(1, 300, B)]
+    c = CACHES[bits](rng, n_q=n_q, n_kv=n_kv, d=d, dtype=dtype, prefixes=[9728 if dtype == "bf16" else 1500], of=[0] * B, lens=lens)
+    plan = c.ctx.dispatch(c.batch)
+    ws = torch.empty(c.ctx.workspace_size(plan), dtype=torch.uint8, device="cuda")
+    calls = [[torch.randn(B, n_kv, d, device="cuda").to(c.tdt) * 2.0 ** (i % 5) for _ in range(2)] for i in range(12)]
+    alone = [c.decode(plan=plan, k_new=k, v_new=v) for k, v in calls]
+    assert not torch.equal(alone[0][0], alone[1][0])
+    outs = [(torch.zeros_like(o), torch.zeros_like(lse)) for o, lse in alone]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        for (k, v), (o, lse) in zip(calls, outs):
+            c.ctx.decode_attention_append(0, c.q, k, v, c.batch, plan, o, lse, ws, ws.numel(), s)
+    for _ in range(15):
+        for o, lse in outs:
+            o.zero_()
+            lse.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            for _ in range(2):
+                g.replay()
+        s.synchronize()
+        for (o, lse), (o1, lse1) in zip(outs, alone):
+            assert torch.equal(o, o1) and torch.equal(lse, lse1)
+    c.ctx.sync_status()
