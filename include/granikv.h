@@ -504,7 +504,9 @@ granikv_status granikv_set_checks(granikv_ctx* ctx, int32_t on);
  * tile, so that CTA's consumers' bounded wait (2 s) expires.  The CTA then raises its abort
  * flag, waits for the copies it did issue, and exits; the call latches
  * GRANIKV_ERR_DEVICE_CHECK (reported by granikv_sync_status), and the context stays usable for
- * the next call.  Applies to one call of the bf16 tensor-core suffix path; 0 cancels it. */
+ * the next call.  Applies to one call of the tensor-core suffix path (bf16 q); 0 cancels it.
+ * on = 2: the same for the tensor-core prefix of an 8- or 4-bit cache: its first CTA's products with V wait
+ * for an arrival that does not come. */
 granikv_status granikv_inject_stall(granikv_ctx* ctx, int32_t on);
 /* Synchronise the stream and report (and clear) the device error word. */
 granikv_status granikv_sync_status(granikv_ctx* ctx, granikv_stream_t stream);

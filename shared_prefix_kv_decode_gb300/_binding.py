@@ -607,10 +607,10 @@ class Context:
     def set_checks(self, on: bool):
         _check(self._lib.granikv_set_checks(self.handle, 1 if on else 0), "granikv_set_checks")
 
-    def inject_stall(self, on: bool = True):
-        """Test hook: the next decode call's first suffix token-CTA withholds its first tile (see
-        granikv_inject_stall in include/granikv.h)."""
-        _check(self._lib.granikv_inject_stall(self.handle, 1 if on else 0), "granikv_inject_stall")
+    def inject_stall(self, on: bool = True, prefix: bool = False):
+        """Test hook: the next decode call's first suffix token-CTA withholds its first tile, or, with prefix, the first
+        prefix CTA of a packed cache an arrival (see granikv_inject_stall in include/granikv.h)."""
+        _check(self._lib.granikv_inject_stall(self.handle, (2 if prefix else 1) if on else 0), "granikv_inject_stall")
 
     def sync_status(self, stream=None):
         _check(self._lib.granikv_sync_status(self.handle, _stream(stream)), "granikv_sync_status")

@@ -2159,7 +2159,7 @@ granikv_status granikv_set_checks(granikv_ctx* c, int32_t on) {
 
 granikv_status granikv_inject_stall(granikv_ctx* c, int32_t on) {
   if (!c) return GRANIKV_ERR_INVALID;
-  c->inject_stall = on ? 1 : 0;
+  c->inject_stall = on == 2 ? 2 : on ? 1 : 0;
   return GRANIKV_OK;
 }
 

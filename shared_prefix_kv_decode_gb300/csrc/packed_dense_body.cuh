@@ -357,6 +357,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
       if (i >= kBarPFull && i < kBarPFull + kSBufs) count = kSoftmaxThreads / 2;
       if (i >= kBarPair && i < kBarPair + 4) count = 64u;
       if (i >= kBarMPub && i < kBarMPub + 8) count = 32u;
+      if (i == kBarVFull && p.inject_stall == 2 && blockIdx.x == 0) count += 1u;  // test hook: an arrival that does not come
       mbar_init(bar(i), count);
     }
     *abort_flag = slab_ok ? 0 : 1;

@@ -234,7 +234,7 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
     int pos = 0;  // position of the current segment's first token in sslot
     bool stop = false;
     // test hook: token-CTA 0 of group 0 withholds its first tile
-    const bool skip0 = p.inject_stall != 0 && cta == 0 && group == 0;
+    const bool skip0 = p.inject_stall == 1 && cta == 0 && group == 0;
     for (int sg = 0; sg < n_seg && !stop; ++sg) {
       const DevSuffixItem seg = seg_at(sg);
       for (int t = seg.t0; t < seg.t1; t += kTile, ++n) {

@@ -157,7 +157,7 @@ __device__ __forceinline__ void suffix_mma_body(const AttnParams& p, const int32
     int pos = 0;    // position of the current segment's first token in sslot
     bool stop = false;
     // test hook: token-CTA 0 of group 0 withholds its first tile
-    const bool skip0 = p.inject_stall != 0 && cta == 0 && group == 0;
+    const bool skip0 = p.inject_stall == 1 && cta == 0 && group == 0;
     const char* new_base =
         fuse_new ? static_cast<const char*>(is_v ? p.v_new : p.k_new) + (int64_t)j0 * kRowBytes : nullptr;
     for (int sg = 0; sg < n_seg && !stop; ++sg) {

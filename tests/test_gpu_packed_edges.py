@@ -249,3 +249,28 @@ def test_appends_back_to_back_in_a_graph(cuda_ok, bits, n_q, n_kv, d, dtype):
         for (o, lse), (o1, lse1) in zip(outs, alone):
             assert torch.equal(o, o1) and torch.equal(lse, lse1)
     c.ctx.sync_status()
+
+
+@pytest.mark.parametrize("bits,d", [(8, 128), (4, 128), (4, 64)])
+@pytest.mark.parametrize("L_p,cold", [(100, 0), (4000, 0), (9728, 300)])
+def test_stalled_prefix_wait_is_reported_and_the_context_survives(cuda_ok, bits, d, L_p, cold):
+    """The first prefix CTA's wait for V runs out (2 s): every role leaves, the CTA goes on to its COLD run, the call is reported, and the
+    next ones give what the one before gave.  Pieces of one tile, of many, and a step with COLD runs behind the prefix."""
+    import time
+    torch, gb, rng = _torch(), _gb(), np.random.default_rng([bits, d, L_p])
+    B = 64 if cold else 3
+    c = CACHES[bits](rng, n_q=32, n_kv=8, d=d, dtype="bf16", prefixes=[L_p], of=[0] * B, lens=[int(n) for n in rng.integers(cold // 3, cold + 1, B)])
+    plan = c.ctx.dispatch(c.batch)
+    o, lse = c.decode(plan)
+    c.ctx.inject_stall(True, prefix=True)
+    t0 = time.perf_counter()
+    with pytest.raises(gb.DeviceCheckFailed):
+        c.decode(plan)
+    waited = time.perf_counter() - t0
+    assert 1.5 <= waited <= 30.0, waited
+    for _ in range(2):
+        o2, lse2 = c.decode(plan)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    c.ctx.inject_stall(True, prefix=True)
+    c.ctx.inject_stall(False)
+    c.decode(plan)
