@@ -143,6 +143,12 @@ granikv_status granikv_destroy(granikv_ctx* ctx);
  * Those rows and q and o must start on 16-byte boundaries (GRANIKV_ERR_INVALID).
  * A NaN or an infinity in a head's q, or a NaN in the K that a request attends, makes that head's o
  * and lse of that request NaN; a NaN in V reaches its own columns of o only.
+ * Accuracy: sums, maxima and lse are fp32.  On the tensor cores (below) q and K meet as they are but for q's
+ * elements far below its row's largest (8 bits, HOT: below 2^-9 of it, off by up to 2^-17 of it; else 2^-31 and 2^-39),
+ * and a key's weight p is rounded where it meets V: to 11 bits; HOT weights below 2^-13 of their piece's largest are off by up to 2^-24
+ * of that (in pieces whose V scales differ by more than 2^8: 16 bits, whatever the scales); COLD weights by up to 2^-38
+ * of max_t p_t |v_t| / |v|, with |v_t| the largest magnitude of token t's head, so that columns of o 2^-27 or more below
+ * the row's largest may lose bits.  On CUDA cores weights are fp32.
  * granikv_dispatch, granikv_decode_attention (and its append and static forms),
  * granikv_cold_weigh and the pool calls work on such a context as on any other;
  * granikv_prefill_attention is GRANIKV_ERR_UNSUPPORTED (a prefix is prefilled in 16 bits and its
@@ -151,7 +157,7 @@ granikv_status granikv_destroy(granikv_ctx* ctx);
  * tensor cores; every other shape and GRANIKV_BACKEND_CASCADE on CUDA cores.  The dense backend is the
  * faster one at every batch size, so M_sat is 1 unless it is set.
  * granikv_decode_attention_append quantises the newest rows into their slots in a launch of its own
- * before the attention, and granikv_inject_stall applies as it does to the bf16 path. ----------- */
+ * before the attention, and granikv_inject_stall applies as it does to the bf16 path, and to the prefix. ----------- */
 granikv_status granikv_create_kv8(const granikv_config* cfg, granikv_ctx** out);
 /* Bytes of one slot's row; GRANIKV_ERR_UNSUPPORTED for a head_dim that granikv_create refuses, and
  * (as from granikv_create_kv8) for a row of more than 2^24 bytes. */
@@ -159,7 +165,8 @@ granikv_status granikv_kv8_row_bytes(int32_t n_kv, int32_t head_dim, size_t* byt
 
 /* ---- 4-bit cache.  A context made by granikv_create_kv4 keeps K and V as 4-bit floating-point codes
  * (e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) with an e4m3 scale for each 16 of them and a power
- * of two for each block of tokens and KV head, in 4.6 bits an element.
+ * of two for each block of tokens and KV head: 4.6 bits an element for eight heads of 128 (granikv_kv4_row_bytes
+ * gives the exact size, with both paddings: one head of 128 takes 6 bits an element, one of 32 takes 12).
  *
  * cfg->k_pool and v_pool are then byte pools [n_slots, row_bytes], row_bytes from
  * granikv_kv4_row_bytes: one slot's row is n_kv * head_dim / 2 bytes of codes (head by head, element

@@ -34,7 +34,7 @@ constexpr int32_t kDefaultMaxBatch = 4096;
 // warp-level MMAs run out of throughput.
 constexpr int32_t kDefaultMsat = 4;
 // 8- and 4-bit cache: the cascade backend is the CUDA-core kernel, so every group goes to the dense one.
-constexpr int32_t kDefaultMsatKv8 = 1;
+constexpr int32_t kDefaultMsatPacked = 1;
 
 struct Extent {
   int64_t off, len;
@@ -366,7 +366,7 @@ constexpr int64_t kSTile = 16;
 constexpr int64_t kSegTiles = 1;
 // 8-bit cache: a tile takes a token-CTA 0.56 us and a segment about 0.95 us more than that (its q, its
 // record, its odd last tile), measured on GB300 over the CTAs of three workloads
-constexpr int64_t kSegTilesKv8 = 3;
+constexpr int64_t kSegTilesPacked = 3;
 
 struct SuffixCut {
   int32_t n_items = 0;         // suffix work items written
@@ -527,7 +527,7 @@ granikv_status create_impl(const granikv_config* cfg, int32_t bits, granikv_ctx*
   if (!(fp > 0.0 && fp < 1.0)) return GRANIKV_ERR_INVALID;
   if (cfg->max_slabs < 0 || cfg->max_batch < 0 || cfg->m_sat < 0) return GRANIKV_ERR_INVALID;
 
-  if (packed_row_bytes(bits, cfg->n_kv, cfg->head_dim) > kKv8MaxRow) return GRANIKV_ERR_UNSUPPORTED;
+  if (packed_row_bytes(bits, cfg->n_kv, cfg->head_dim) > kPackedMaxRow) return GRANIKV_ERR_UNSUPPORTED;
 
   granikv_ctx* c = new (std::nothrow) granikv_ctx();
   if (!c) return GRANIKV_ERR_INVALID;
@@ -537,7 +537,7 @@ granikv_status create_impl(const granikv_config* cfg, int32_t bits, granikv_ctx*
   c->cfg.hot_fraction = fp;
   if (c->cfg.max_slabs == 0) c->cfg.max_slabs = kDefaultMaxSlabs;
   if (c->cfg.max_batch == 0) c->cfg.max_batch = kDefaultMaxBatch;
-  c->m_sat = cfg->m_sat ? cfg->m_sat : bits ? kDefaultMsatKv8 : kDefaultMsat;
+  c->m_sat = cfg->m_sat ? cfg->m_sat : bits ? kDefaultMsatPacked : kDefaultMsat;
   c->g = cfg->n_q / cfg->n_kv;
   c->n_hot = (int64_t)std::floor(fp * (double)cfg->n_slots);
   c->n_cold = cfg->n_slots - c->n_hot;
@@ -619,7 +619,7 @@ granikv_status create_impl(const granikv_config* cfg, int32_t bits, granikv_ctx*
           auto encode = [&](CUtensorMap* to, void* pool, int32_t bytes, int32_t slots, bool swizzle) {
             return encode_packed_map(to, pool, cfg->n_slots, c->packed_row, codes, bytes, slots, swizzle);
           };
-          ok = encode(&m.k, c->kpool[l], head, bits == 8 ? kDenseTile : kKv8VBox, bits == 8) && encode(&m.v, c->vpool[l], head, kKv8VBox, false);
+          ok = encode(&m.k, c->kpool[l], head, bits == 8 ? kDenseTile : kPackedBox, bits == 8) && encode(&m.v, c->vpool[l], head, kPackedBox, false);
           continue;
         }
         ok = ((uintptr_t)c->kpool[l] % 16 == 0) && ((uintptr_t)c->vpool[l] % 16 == 0) &&
@@ -657,7 +657,7 @@ granikv_status granikv_create_kv4(const granikv_config* cfg, granikv_ctx** out) 
 static granikv_status row_bytes_impl(int32_t bits, int32_t n_kv, int32_t head_dim, size_t* bytes) {
   if (!bytes || n_kv <= 0) return GRANIKV_ERR_INVALID;
   if (head_dim <= 0 || head_dim % 32 || head_dim > 256) return GRANIKV_ERR_UNSUPPORTED;
-  if (packed_row_bytes(bits, n_kv, head_dim) > kKv8MaxRow) return GRANIKV_ERR_UNSUPPORTED;
+  if (packed_row_bytes(bits, n_kv, head_dim) > kPackedMaxRow) return GRANIKV_ERR_UNSUPPORTED;
   *bytes = (size_t)packed_row_bytes(bits, n_kv, head_dim);
   return GRANIKV_OK;
 }
@@ -1132,9 +1132,9 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
   int32_t suffix_sms = c->num_sms;  // set after the prefix pieces when the SMs are split
   bool read_ahead = false;          // the split's dense CTAs read ahead into L2 (see below)
   double tail_frac = 0.0;           // share of the suffix work the dense CTAs take after their piece
-  const int64_t seg_tiles = c->packed_row ? kSegTilesKv8 : kSegTiles;
-  bool kv8_split = false;           // packed cache: the split and its runs' shares as planned below
-  int32_t kv8_main = 0;             // its suffix CTAs
+  const int64_t seg_tiles = c->packed_row ? kSegTilesPacked : kSegTiles;
+  bool packed_split = false;           // packed cache: the split and its runs' shares as planned below
+  int32_t packed_main = 0;             // its suffix CTAs
   std::vector<double>& share = w.share;
   share.clear();
 
@@ -1172,9 +1172,9 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
       if (groups[i].impl == kImplPackedGeneric)
         lo = std::max(lo, std::min(max_tiles, (int64_t)std::ceil(std::sqrt(8.0 * (double)groups[i].L_p) / kGenericTile)));
     bool auto_found = false;
-    bool kv8_dense = auto_share && c->packed_row && n_kv <= 8;
-    for (int32_t i = 0; i < G; ++i) kv8_dense = kv8_dense && groups[i].impl == kImplPackedDense;
-    if (kv8_dense) {
+    bool packed_dense = auto_share && c->packed_row && n_kv <= 8;
+    for (int32_t i = 0; i < G; ++i) packed_dense = packed_dense && groups[i].impl == kImplPackedDense;
+    if (packed_dense) {
       // Packed cache (8 bits, 4 bits below): every SM works until the end.  With pieces of a given length, dense CTA k is done
       // at t_k = 5.2 us + 7.3 ns a token and then takes suffix work (3 us for its set-up), the SMs
       // without a prefix piece take suffix work from the start (4.5 us); a unit of it (16 tokens, or
@@ -1239,13 +1239,13 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
       if (best_len > 0) {
         lo = best_len;
         auto_found = true;
-        kv8_main = (int32_t)(c->num_sms - ctas_for(lo));
+        packed_main = (int32_t)(c->num_sms - ctas_for(lo));
         classes_of(lo, cl);
         std::sort(cl.begin(), cl.end(), [](const Class& a, const Class& b) { return a.t < b.t; });
         // few tiles: on the SMs without a prefix piece only
-        for (int32_t k = 0; k < kv8_main && k < few; ++k) share.push_back(std::max(1.0, (best_T - kMain) / kUnit));
-        kv8_main = (int32_t)share.size();
-        if (few > kv8_main)
+        for (int32_t k = 0; k < packed_main && k < few; ++k) share.push_back(std::max(1.0, (best_T - kMain) / kUnit));
+        packed_main = (int32_t)share.size();
+        if (few > packed_main)
           for (const Class& x : cl)
             for (int64_t k = 0; k < x.n; ++k)
               if ((best_T - x.t - kTail) / kUnit >= kMinTail) share.push_back((best_T - x.t - kTail) / kUnit);
@@ -1255,8 +1255,8 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
           top = std::max(top, s);
         }
         // a run's slot ids fit its shared memory; else the equal shares below, on the main CTAs
-        kv8_split = !share.empty() && top / sum * units < 0.9 * (double)(kSuffixMaxCtaTokens / kSTile);
-        if (!kv8_split) auto_found = ctas_for(lo) < c->num_sms;
+        packed_split = !share.empty() && top / sum * units < 0.9 * (double)(kSuffixMaxCtaTokens / kSTile);
+        if (!packed_split) auto_found = ctas_for(lo) < c->num_sms;
       }
     } else if (auto_share) {
       // Automatic split: the piece length whose prefix time (one wave: the longest piece) and
@@ -1449,9 +1449,9 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
   int32_t n_tail = 0;       // of them, the last n_tail are run by the dense CTAs of one grid
   int64_t U = 0;            // tiles plus segment costs, with every cut counted as inside a request
   int64_t U_tail = 0;       // of U, the tail runs' share
-  if (kv8_split) {
+  if (packed_split) {
     n_scta = (int32_t)share.size();
-    n_tail = n_scta - kv8_main;
+    n_tail = n_scta - packed_main;
     U = T + seg_tiles * (n_sreq + n_scta - 1);
   } else if (T > 0) {
     // one wave over the suffix's SMs, with at least kMinCtaTiles tiles per token-CTA (a CTA's
@@ -1506,7 +1506,7 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
     std::vector<int32_t> key_now;
     key_now.reserve((size_t)G * 7 + 2);
     key_now.push_back(n_kv);
-    key_now.push_back(kv8_split ? 1 : 0);
+    key_now.push_back(packed_split ? 1 : 0);
     for (int32_t i = 0; i < G; ++i) {
       const DevGroup& dg = groups[i];
       key_now.insert(key_now.end(), {dg.impl, dg.sub, dg.n_splits, dg.row_blocks, dg.split_len, dg.n_long, w.grp_tail[i]});
@@ -1537,7 +1537,7 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
     }
     // the packed dense kernel's first CTAs are those that take suffix runs after their piece: the
     // shortest pieces come first
-    if (impl == kImplPackedDense && kv8_split)
+    if (impl == kImplPackedDense && packed_split)
       std::stable_sort(pitems.begin() + p->pitem_first[impl], pitems.end(),
                        [&](const DevPrefixItem& a, const DevPrefixItem& b) {
                          int32_t a0, a1, b0, b1;
@@ -1573,7 +1573,7 @@ static granikv_status dispatch_impl(granikv_ctx* c, const granikv_batch* bt, gra
   grp_np[0] = 0;
   for (int32_t i = 0; i < G; ++i) grp_np[i + 1] = groups[i].n_splits;
   const SuffixCut cut = cut_suffix_runs(B, grp_np.data() + 1, req_group.data(), bt->seq_len, n_scta, n_tail, U,
-                                        U_tail, seg_tiles, kv8_split ? share.data() : nullptr, reqs, si,
+                                        U_tail, seg_tiles, packed_split ? share.data() : nullptr, reqs, si,
                                         scta_begin.data());
   const int32_t n_si = cut.n_items;
   const int32_t max_parts = cut.max_parts;
@@ -1951,12 +1951,12 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
     if (e != cudaSuccess) return cuda_status(e);
   }
   const int32_t n_dense = p->pitem_count[kImplDenseTc], n_casc = p->pitem_count[kImplCascadeStream];
-  const int32_t n_dense8 = p->pitem_count[kImplPackedDense];
-  if (p->concurrent && p->n_pitems > 0 && n_dense8 == p->n_pitems && c->has_tmaps &&
+  const int32_t n_packed_dense = p->pitem_count[kImplPackedDense];
+  if (p->concurrent && p->n_pitems > 0 && n_packed_dense == p->n_pitems && c->has_tmaps &&
       p->suffix_impl == kImplPackedSuffix && p->n_sitems > 0) {
     // one grid, as below
-    const int32_t n_tail = p->n_tail <= n_dense8 ? p->n_tail : 0;
-    e = packed_step(a, p->pitem_first[kImplPackedDense], n_dense8, c->packed_maps[layer], a.scta_begin, p->n_scta - n_tail,
+    const int32_t n_tail = p->n_tail <= n_packed_dense ? p->n_tail : 0;
+    e = packed_step(a, p->pitem_first[kImplPackedDense], n_packed_dense, c->packed_maps[layer], a.scta_begin, p->n_scta - n_tail,
                     n_tail, s, true);
     c->n_kernels += 1;
     if (e == cudaSuccess) e = launch_merge_k(true);
@@ -1998,7 +1998,7 @@ granikv_status decode_attention_impl(granikv_ctx* c, int32_t layer, const void* 
   } else {
     e = launch_prefix(s);
     // the suffix kernel follows a prefix kernel of this call, the merge the suffix kernel
-    const bool after_prefix = p->n_pitems > 0 && n_dense + n_casc + n_dense8 > 0;
+    const bool after_prefix = p->n_pitems > 0 && n_dense + n_casc + n_packed_dense > 0;
     if (e == cudaSuccess) e = launch_suffix(s, after_prefix && token_ctas(p->suffix_impl));
     if (e == cudaSuccess && !p->fused) {
       // the merge's stream predecessor is this call's suffix kernel, or its prefix kernel when

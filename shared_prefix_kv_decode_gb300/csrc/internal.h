@@ -34,8 +34,8 @@ enum Impl : int32_t {
   kImplCascadeStream = 4,  // bf16, head_dim 128, g <= 128: cascade over whole 2 KB slot rows
   kImplDenseTf32 = 5,      // f32, head_dim % 32 == 0 up to 128: tcgen05 kind::tf32 dense kernel
   kImplPackedGeneric = 6,  // 8- or 4-bit cache, any head_dim % 32 == 0 up to 256: CUDA-core kernel
-  kImplPackedDense = 7,    // 8- or 4-bit cache, bf16 q, head_dim 128: tcgen05/TMEM dense kernel
-  kImplPackedSuffix = 8,   // 8- or 4-bit cache, bf16 q, head_dim 128, g <= 8: warp-level tensor-core suffix kernel
+  kImplPackedDense = 7,    // 8- or 4-bit cache, bf16 q, head_dim 128 (4 bits: or 64): tcgen05/TMEM dense kernel
+  kImplPackedSuffix = 8,   // the same shapes with g <= 8: warp-level tensor-core suffix kernel
 };
 
 // Geometry of each prefix kernel: query rows per CTA and tokens per tile.  The planner and the
@@ -137,12 +137,12 @@ struct AttnParams {
 // ---- 8-bit cache ---------------------------------------------------------------------------
 // One slot of an 8-bit pool is one packed row: e4m3 codes [n_kv, d], then one fp32 scale a KV
 // head, padded to 16 bytes (value = code * scale).  Every row carries its own scales; the rows of
-// one 64-token block of a slab (kKv8Block, counted from the slab's start) hold the same ones.
-constexpr int kKv8Block = 64;
-constexpr int kKv8VBox = 32;  // slots of one TMA box of V's codes, 4 bits: of all (dense kernel)
+// one 64-token block of a slab (kPackedBlock, counted from the slab's start) hold the same ones.
+constexpr int kPackedBlock = 64;
+constexpr int kPackedBox = 32;  // slots of one TMA box of V's codes (4 bits: and K's) in the dense kernel
 constexpr float kE4m3Max = 448.0f;
 constexpr float kKv8AmaxMin = 1.2621774483536189e-29f;  // 2^-96: smallest amax a scale is made for
-constexpr int64_t kKv8MaxRow = 1 << 24;  // bytes of a packed row: offsets within a block of 64 fit 32 bits
+constexpr int64_t kPackedMaxRow = 1 << 24;  // bytes of a packed row: offsets within a block of 64 fit 32 bits
 __host__ __device__ inline int64_t kv8_row_bytes(int32_t n_kv, int32_t d) {
   return ((int64_t)n_kv * (d + 4) + 15) / 16 * 16;
 }
@@ -151,7 +151,7 @@ __host__ __device__ inline int64_t kv8_row_bytes(int32_t n_kv, int32_t d) {
 // One slot of a 4-bit pool is one packed row: e2m1 codes [n_kv, d] (two to a byte, the first in the low half),
 // e4m3 scales [n_kv, d / 16], padding to 16 bytes, an exponent byte a KV head, padding to 16 bytes
 // (kv4_util.cuh says what they stand for).  Every row carries its own exponents; the rows of one 64-token
-// block of a slab (kKv8Block) hold the same ones.
+// block of a slab (kPackedBlock) hold the same ones.
 constexpr int kKv4Group = 16;
 constexpr int kKv4ExpMin = -100, kKv4ExpMax = 116;
 __host__ __device__ constexpr int64_t kv4_scales_at(int32_t n_kv, int32_t d) { return (int64_t)n_kv * (d / 2); }
@@ -245,8 +245,10 @@ cudaError_t launch_kv8_generic(int32_t dtype, const AttnParams& p, int32_t first
                                cudaStream_t s, bool pdl);
 // Tensor-core path of the 8- and 4-bit cache (kernels_kv8_tc.cu, kernels_kv4_tc.cu): dense prefix items and suffix
 // token-CTAs in one grid (either count may be 0; n_tail as for launch_prefix_suffix_tc), and the suffix alone.
+// A layer's pools as byte matrices of their codes.  8 bits: K in boxes of 128 slots x 128 bytes with the 128-byte
+// swizzle, V in boxes of 32 slots x 128 bytes, row after row.  4 bits: both in boxes of 32 slots x one head's codes.
 struct PackedMaps {
-  CUtensorMap k, v;  // the pools' codes
+  CUtensorMap k, v;
 };
 cudaError_t launch_kv8_step(const AttnParams& p, int32_t first_dense, int32_t n_dense, const PackedMaps& m,
                             const int32_t* cta_begin, int32_t n_scta, int32_t n_tail, cudaStream_t s, bool pdl);

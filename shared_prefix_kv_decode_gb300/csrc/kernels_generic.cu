@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(256, kBlocks) merge_bf16_d128_kernel(AttnParam
     m = M;
   }
   if (!have) return;
-  // (over the 8-bit cache a row with a NaN among its weights, whose record says +inf, becomes NaN)
+  // (over a packed cache a row with a NaN among its weights, whose record says +inf, becomes NaN)
   const bool weight = den > 0.f || (p.packed_row && den != den);
   const float inv = weight ? 1.f / den : 0.f;
   __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);

@@ -7,7 +7,7 @@
 namespace granikv {
 namespace {
 
-// One block of kKv8Block slab tokens of one KV head, of K (blockIdx.y = 0) or V.  A thread holds groups of 16
+// One block of kPackedBlock slab tokens of one KV head, of K (blockIdx.y = 0) or V.  A thread holds groups of 16
 // elements in registers between the block's amax and their codes, so the rows are read once: 2.6 bytes moved for
 // each bf16 element.  Bound by memory: 16K tokens of 8 x 128 take 18.4 us from bf16 (86 MB, 0.69 of the copy rate) and
 // 25.6 from fp32 (0.88); without the quantising, the same loads and stores of bf16 take 17.3.  (With two
@@ -17,12 +17,12 @@ __global__ void __launch_bounds__(256) kv4_fill_kernel(const T* __restrict__ k, 
                                                        uint8_t* __restrict__ kpool, uint8_t* __restrict__ vpool,
                                                        int64_t first_slot, int32_t n_kv) {
   constexpr int kPerRow = D / kKv4Group;                    // groups of a head's row
-  constexpr int kGroups = kKv8Block * kPerRow;              // of the block
+  constexpr int kGroups = kPackedBlock * kPerRow;              // of the block
   constexpr int kPer = (kGroups + 255) / 256;               // of a thread
   __shared__ float s_max[8];
   const int32_t j = blockIdx.x % n_kv;
-  const int32_t t0 = blockIdx.x / n_kv * kKv8Block;
-  const int32_t n = min(kKv8Block, L_p - t0);
+  const int32_t t0 = blockIdx.x / n_kv * kPackedBlock;
+  const int32_t n = min(kPackedBlock, L_p - t0);
   const T* src = (blockIdx.y ? v : k) + ((int64_t)t0 * n_kv + j) * D;
   Kv4Group<T> x[kPer];
 #pragma unroll
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(256) kv4_append_newest_kernel(AttnParams p) {
 template <typename T>
 cudaError_t fill_t(const T* k, const T* v, int32_t L_p, uint8_t* kpool, uint8_t* vpool, int64_t first_slot,
                    int32_t n_kv, int32_t d, cudaStream_t s) {
-  const int64_t ctas = (int64_t)((L_p + kKv8Block - 1) / kKv8Block) * n_kv;
+  const int64_t ctas = (int64_t)((L_p + kPackedBlock - 1) / kPackedBlock) * n_kv;
   if (ctas > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)ctas, 2);
   return with_vpl(d, [&](auto vpl) {

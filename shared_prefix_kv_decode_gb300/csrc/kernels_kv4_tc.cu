@@ -6,7 +6,7 @@ namespace granikv {
 cudaError_t launch_kv4_step(const AttnParams& p, int32_t first_dense, int32_t n_dense, const PackedMaps& m,
                             const int32_t* cta_begin, int32_t n_scta, int32_t n_tail, cudaStream_t s, bool pdl) {
   const auto launch = p.d == 64 ? launch_packed_step<4, 64> : launch_packed_step<4, 128>;
-  return launch(p, first_dense, n_dense, {m.k, m.v}, cta_begin, n_scta, n_tail, s, pdl);
+  return launch(p, first_dense, n_dense, m, cta_begin, n_scta, n_tail, s, pdl);
 }
 
 cudaError_t launch_kv4_suffix(const AttnParams& p, const int32_t* cta_begin, int32_t n_scta, cudaStream_t s, bool pdl) {

@@ -76,7 +76,7 @@ struct Piece<float> {
   }
 };
 
-// One block of kKv8Block slab tokens of one KV head (the heads of a block are neighbours in the grid, so
+// One block of kPackedBlock slab tokens of one KV head (the heads of a block are neighbours in the grid, so
 // that its rows are read and written whole at about the same time), of K (blockIdx.y = 0) or V.  The block stays in
 // registers between its amax and its codes (pieces of 16 bytes, all of a thread's requested at once), so
 // the rows are read once: 3 bytes moved for each bf16 element (16K tokens of 8 x 128: 18.7 us at six CTAs an
@@ -88,11 +88,11 @@ __global__ void __launch_bounds__(256, sizeof(T) * D <= 256 ? 6 : 1) kv8_fill_ke
     uint8_t* __restrict__ vpool, int64_t first_slot, int32_t n_kv) {
   constexpr int kElems = Piece<T>::kElems;
   constexpr int kPerRow = D / kElems;              // pieces of a head's row
-  constexpr int kPieces = kKv8Block * kPerRow / 256;  // of a thread
+  constexpr int kPieces = kPackedBlock * kPerRow / 256;  // of a thread
   __shared__ float s_max[8];
   const int32_t j = blockIdx.x % n_kv;
-  const int32_t t0 = blockIdx.x / n_kv * kKv8Block;
-  const int32_t n = min(kKv8Block, L_p - t0);
+  const int32_t t0 = blockIdx.x / n_kv * kPackedBlock;
+  const int32_t n = min(kPackedBlock, L_p - t0);
   const T* src = (blockIdx.y ? v : k) + ((int64_t)t0 * n_kv + j) * D;
   Piece<T> x[kPieces];
 #pragma unroll
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(256) kv8_append_newest_kernel(AttnParams p) {
 template <typename T>
 cudaError_t fill_t(const T* k, const T* v, int32_t L_p, uint8_t* kpool, uint8_t* vpool, int64_t first_slot,
                    int32_t n_kv, int32_t d, cudaStream_t s) {
-  const int64_t ctas = (int64_t)((L_p + kKv8Block - 1) / kKv8Block) * n_kv;
+  const int64_t ctas = (int64_t)((L_p + kPackedBlock - 1) / kPackedBlock) * n_kv;
   if (ctas > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)ctas, 2);
   return with_vpl(d, [&](auto vpl) {

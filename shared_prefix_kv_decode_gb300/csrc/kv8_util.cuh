@@ -98,7 +98,7 @@ __device__ __forceinline__ float score_factor(float f, float scale) {
 
 // A partial row's log-sum-exp as the merge takes it: -inf for a row without weight, +inf for one whose
 // weights hold a NaN (the merge's maximum passes over a NaN; +inf makes the whole row NaN).
-__device__ __forceinline__ float kv8_record_lse(float sum, float lse) {
+__device__ __forceinline__ float packed_record_lse(float sum, float lse) {
   return sum == 0.f ? -INFINITY : sum == sum ? lse : INFINITY;
 }
 

@@ -34,7 +34,13 @@
 // output may vanish beside others.  Where the scales of a piece span more than 2^8, their powers of two therefore go into
 // V's operands, which are bf16 then (a code, or a code times its 4-bit scale, has 4 or 6 significant bits; the piece's largest
 // scale becomes 2^90, what lies 2^216 below it 0), and P has the significand of vs alone: P = 2^(z - m - 8) as the sum of two
-// bf16 values (16 bits, at most 1, down to 2^-118 of the largest weight), over all of S, in twice the products.
+// bf16 values (16 bits, at most 1, down to 2^-118 of the largest weight), over all of S, in twice the products, with small
+// loops, so that the others' instructions stay close: unrolled as those are they cost every piece 3 to 4 %.  With every
+// eighth block of V zero the step of a 16K prefix with 64 requests takes 56 us (8 bits 51) instead of 35 (31).
+// Elsewhere P is one fp16 value, 11 bits: a weight below 2^-13 of the piece's largest may be off by 2^-24 of that.  The rounding,
+// 2^-12.8 of a weight on average, moves about 2 % of the bf16 results to a neighbour (8e-4 of them in the root mean square, where
+// their own rounding is 1.7e-3): chosen, since a second part would double the products with P and put a subtraction, a
+// conversion and a store more into the rounds that set the pace.
 // Roles (15 warps; the 16th only takes part in the block's barriers here):
 //  * warps 0-7, softmax and epilogue: warp w serves TMEM lanes 32*(w%4).. (row r = lane r), all 64
 //    columns of the tiles i with i % 2 == w / 4; the two warps of a row quarter take turns, half a
@@ -92,9 +98,9 @@ using pks::regs_down;
 using pks::regs_up;
 
 constexpr int kM = kDenseRows;                // 128 query rows per CTA
-constexpr int kN = kKv8Block;                 // 64 tokens per tile
+constexpr int kN = kPackedBlock;              // 64 tokens per tile
 constexpr int kPair = kDenseTile;             // 128 tokens: what is loaded at a time
-static_assert(kPair == 2 * kN && kPair / 4 == kKv8VBox, "a conversion warp's part is one box");
+static_assert(kPair == 2 * kN && kPair / 4 == kPackedBox, "a conversion warp's part is one box");
 constexpr int kSBufs = 5;                     // S/P buffers in TMEM
 constexpr int kSoftmaxWarps = 8;
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
@@ -132,7 +138,8 @@ struct Layout {
   static constexpr int kBarArea = BITS == 8 ? 512 : 640;
   static constexpr int kSmemBytes = kOffBar + kBarArea + 1024;  // + alignment slack
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-  static_assert(kFill * kCSlots * kCSlotBytes >= kRedBytes, "the epilogue's sums and maxima lie in rings whose parts fill every content's first tile");
+  static_assert(kFill * kCSlots * kCSlotBytes >= kRedBytes,
+                "the epilogue's sums and maxima lie in rings whose parts fill every content's first tile");
   // barriers
   static constexpr int kBarKFull = 0;                            // [kKSlots] TMA (4 bits: conversion, kFill arrivals) -> MMA
   static constexpr int kBarKEmpty = kBarKFull + kKSlots;         // [kKSlots] MMA (S of the slot's tiles done) -> TMA (conversion)
@@ -147,11 +154,6 @@ struct Layout {
   static constexpr int kBarMPub = kBarPair + 4;                  // [4 quarters][2 parities] max of a tile published (32)
   static constexpr int kNumBars = kBarMPub + 8;
   static_assert(8 * kNumBars + 16 <= kBarArea, "barrier area");
-};
-// The layer's pools as byte matrices [n_slots, row bytes].  8 bits: K in boxes of 128 slots x 128 bytes with the
-// 128-byte swizzle, V in boxes of 32 slots x 128 bytes, row after row.  4 bits: both in boxes of 32 slots x 64 bytes.
-struct Maps {
-  CUtensorMap k, v;
 };
 constexpr uint32_t kTmemCols = 512;           // S/P buffers at 0, 64, 128, 192, 256; Q (hi, lo) at 320; O at 384
 constexpr uint32_t kColQ = kSBufs * kN, kColO = 384;
@@ -281,7 +283,7 @@ struct ConvLane {
 
 // Prefix work item `item` (one CTA) on `smem_raw` (at least Layout<BITS, D>::kSmemBytes), run by Layout<BITS, D>::kThreads threads.
 template <int BITS, int D>
-__device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t item, const Maps* maps,
+__device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t item, const PackedMaps* maps,
                                                   unsigned char* smem_raw) {
   using Lay = Layout<BITS, D>;
   constexpr int kKSlots = Lay::kKSlots, kVSlots = Lay::kVSlots, kCSlots = Lay::kCSlots, kConvWarps = Lay::kConvWarps;
@@ -302,6 +304,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
   float* units = reinterpret_cast<float*>(smem + kOffUnit);
   const uint32_t sBar = base + kOffBar;
   auto bar = [&](int i) { return sBar + 8u * i; };
+  // after the barriers four words: the abort flag, V's smallest scale, the tensor memory's address, V's wide top
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffBar + 8 * kNumBars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBar + 8 * kNumBars + 8);
 
@@ -468,15 +471,15 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
       else tmem_st16(at, qw);
       tmem_wait_st();
     } else {
-    // in fp16 pairs: below 2^8 with 8 significant bits they are exact there down to 2^-17
-    uint32_t hi[16], lo[16];
+      // in fp16 pairs: below 2^8 with 8 significant bits they are exact there down to 2^-17
+      uint32_t hi[16], lo[16];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const __half2 x = q_no_inf(f16x2_of(qw[2 * k], f)), y = q_no_inf(f16x2_of(qw[2 * k + 1], f));
-      hi[k] = f16x4_to_e4m3x4(x, y);
-      uint32_t u, v;
-      e4m3x4_to_f16x4(hi[k], u, v);
-      lo[k] = f16x4_to_e4m3x4(__hsub2(x, *reinterpret_cast<__half2*>(&u)), __hsub2(y, *reinterpret_cast<__half2*>(&v)));
+      for (int k = 0; k < 16; ++k) {
+        const __half2 x = q_no_inf(f16x2_of(qw[2 * k], f)), y = q_no_inf(f16x2_of(qw[2 * k + 1], f));
+        hi[k] = f16x4_to_e4m3x4(x, y);
+        uint32_t u, v;
+        e4m3x4_to_f16x4(hi[k], u, v);
+        lo[k] = f16x4_to_e4m3x4(__hsub2(x, *reinterpret_cast<__half2*>(&u)), __hsub2(y, *reinterpret_cast<__half2*>(&v)));
     }
     const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColQ + qhalf * 16;
     tmem_st16(at, hi);
@@ -489,280 +492,282 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
   tc_fence_after();
 
   if (warp >= kSoftmaxWarps) {
-  if constexpr (Lay::kSplitRegs) regs_down<72>();
-  if (warp < kWarpConv + kConvWarps) {
-    // ---------------- conversion: codes of V (4 bits: of K and V) -> fp16 operand tiles ----------------
-    const int w = warp - kWarpConv;
-    const int part = w % kParts;
-    const bool to_k = BITS == 4 && w < kParts;
-    using Conv = ConvLane<BITS, D>;
-    constexpr int kPer = Conv::kPer;
-    const Conv cl(part, lane);
-    const uint32_t ring = to_k ? sK : sV;
-    const int slots = to_k ? kKSlots : kVSlots, full = to_k ? kBarKFull : kBarVFull, empty = to_k ? kBarKEmpty : kBarVEmpty;
-    int issued = slab_ok ? min(n_pairs, kCSlots) : 0, seen = 0;
-    // 4 bits: the scales of contents i, a token a lane (zeros past the piece's end); a group for every i
-    const uint8_t* scale_src = static_cast<const uint8_t*>(to_k ? p.kpool : p.vpool) + (first_slot + part * kPart + lane) * p.packed_row +
-                               kv4_scales_at(p.n_kv, D) + j * Lay::kScale;
-    auto copy_scales = [&](int i) {
-      if constexpr (BITS == 4) {
-        const uint32_t dst = sC + (w * kCSlots + i % kCSlots) * Lay::kCSlotBytes + kPart * Lay::kHead + lane * Lay::kScale;
-        const bool in = t0 + i * kPair + part * kPart + lane < t1;
-        if (slab_ok && i < n_pairs) {
-          const uint8_t* src = in ? scale_src + (int64_t)i * kPair * p.packed_row : static_cast<const uint8_t*>(p.kpool);
-          if constexpr (D == 128) cp_async8(dst, src, in ? 8 : 0);
-          else cp_async4(dst, src, in ? 4 : 0);
+    if constexpr (Lay::kSplitRegs) regs_down<72>();
+    if (warp < kWarpConv + kConvWarps) {
+      // ---------------- conversion: codes of V (4 bits: of K and V) -> fp16 operand tiles ----------------
+      const int w = warp - kWarpConv;
+      const int part = w % kParts;
+      const bool to_k = BITS == 4 && w < kParts;
+      using Conv = ConvLane<BITS, D>;
+      constexpr int kPer = Conv::kPer;
+      const Conv cl(part, lane);
+      const uint32_t ring = to_k ? sK : sV;
+      const int slots = to_k ? kKSlots : kVSlots, full = to_k ? kBarKFull : kBarVFull, empty = to_k ? kBarKEmpty : kBarVEmpty;
+      int issued = slab_ok ? min(n_pairs, kCSlots) : 0, seen = 0;
+      // 4 bits: the scales of contents i, a token a lane (zeros past the piece's end); a group for every i
+      const uint8_t* scale_src = static_cast<const uint8_t*>(to_k ? p.kpool : p.vpool) + (first_slot + part * kPart + lane) * p.packed_row +
+                                 kv4_scales_at(p.n_kv, D) + j * Lay::kScale;
+      auto copy_scales = [&](int i) {
+        if constexpr (BITS == 4) {
+          const uint32_t dst = sC + (w * kCSlots + i % kCSlots) * Lay::kCSlotBytes + kPart * Lay::kHead + lane * Lay::kScale;
+          const bool in = t0 + i * kPair + part * kPart + lane < t1;
+          if (slab_ok && i < n_pairs) {
+            const uint8_t* src = in ? scale_src + (int64_t)i * kPair * p.packed_row : static_cast<const uint8_t*>(p.kpool);
+            if constexpr (D == 128) cp_async8(dst, src, in ? 8 : 0);
+            else cp_async4(dst, src, in ? 4 : 0);
+          }
+          cp_async_commit();
         }
-        cp_async_commit();
-      }
-    };
-    if constexpr (BITS == 4) {
-      if (lane == 0)
-        for (int i = 0; i < issued; ++i) issue_c(w, i);
-      __syncwarp();
-    }
-#pragma unroll
-    for (int i = 0; i < kCSlots; ++i) copy_scales(i);
-    uint32_t lo;
-    const int wide_top = to_k ? 0 : BITS == 8 ? (int)*v_top : (int)v_span(lo);
-    // wide: what code (times scale) is multiplied by in V's operands, which are bf16 then: the tile's power of two, that of the
-    // piece's largest made 2^kWideTop
-    auto v_size = [&](int tile) {
-      const int e = tile < n_tiles ? (int)(v_scale_bits(tile) >> 23) - wide_top + kWideTop + 127 : 0;
-      return e > 0 ? __uint_as_float((uint32_t)e << 23) : 0.f;
-    };
-    auto all_parts = [&](auto wide_span) {
-    constexpr bool kWide = decltype(wide_span)::value;
-    for (int i = 0; slab_ok && i < n_pairs; ++i) {
-      const int c = w * kCSlots + i % kCSlots;
-      const int use = BITS == 8 ? i : 2 * i + part / kFill, st = use % slots;  // the slot's use, of all of the ring's
-      bool ok = mbar_wait_bounded(bar(kBarCFull + c), (i / kCSlots) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;  // the abort flag is up: every other role leaves as well
-      seen = i + 1;
+      };
       if constexpr (BITS == 4) {
-        cp_async_wait<kCSlots - 1>();
+        if (lane == 0)
+          for (int i = 0; i < issued; ++i) issue_c(w, i);
         __syncwarp();
       }
-      const uint32_t src = sC + c * Lay::kCSlotBytes, dst = ring + st * Lay::kSlot;
-      const int valid = t1 - t0 - i * kPair - part * kPart;  // tokens of the part in range, or more
-      auto codes = [&](int n, uint32_t& b) {  // of load n, and (4 bits) their two scales
-        const uint32_t t = (uint32_t)(cl.token + n * Conv::kStep);
-        if constexpr (BITS == 4) b = lds16(src + kPart * Lay::kHead + t * Lay::kScale + cl.dim / 16);
-        return lds128(src + t * Lay::kHead + cl.dim * BITS / 8);
+#pragma unroll
+      for (int i = 0; i < kCSlots; ++i) copy_scales(i);
+      uint32_t lo;
+      const int wide_top = to_k ? 0 : BITS == 8 ? (int)*v_top : (int)v_span(lo);
+      // wide: what code (times scale) is multiplied by in V's operands, which are bf16 then: the tile's power of two, that of the
+      // piece's largest made 2^kWideTop
+      auto v_size = [&](int tile) {
+        const int e = tile < n_tiles ? (int)(v_scale_bits(tile) >> 23) - wide_top + kWideTop + 127 : 0;
+        return e > 0 ? __uint_as_float((uint32_t)e << 23) : 0.f;
       };
-      // 0 * whatever lies past the piece must not reach O
-      auto mask = [&](int n, uint4& x, uint32_t& b) {
-        if (cl.token + n * Conv::kStep >= valid) {
-          x = make_uint4(0u, 0u, 0u, 0u);
-          b = 0u;
-        }
-      };
-      uint4 x[kWide ? 1 : kPer];
-      uint32_t b[kWide ? 1 : kPer];
-      if constexpr (!kWide) {
-#pragma unroll
-        for (int n = 0; n < kPer; ++n) x[n] = codes(n, b[n]);
-        if (valid < kPart) {
-#pragma unroll
-          for (int n = 0; n < kPer; ++n) mask(n, x[n], b[n]);
-        }
-      }
-      const bool fills = BITS == 8 || use < n_tiles;  // (4 bits: the last two parts may have no tile)
-      if (fills && use >= slots) {
-        ok = mbar_wait_bounded(bar(empty + st), ((use / slots) - 1) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-      }
-      [[maybe_unused]] float size = 1.f;
-      if constexpr (kWide) size = v_size(2 * i + part / 2);
-      auto put = [&](int n, const uint4& x, uint32_t b) {
-        if constexpr (BITS == 8) {
-          uint32_t y[8];
-          e4m3x4_to_f16x4(x.x, y[0], y[1]);
-          e4m3x4_to_f16x4(x.y, y[2], y[3]);
-          e4m3x4_to_f16x4(x.z, y[4], y[5]);
-          e4m3x4_to_f16x4(x.w, y[6], y[7]);
-          if constexpr (kWide) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = f16x2_to_bf16x2(y[k], size);
-          }
-          cl.store(dst, n, 0, y[0], y[1], y[2], y[3]);
-          cl.store(dst, n, 1, y[4], y[5], y[6], y[7]);
-        } else {
-          const uint32_t f = e4m3x2_to_f16x2((uint16_t)b), f2[2] = {__byte_perm(f, f, 0x1010), __byte_perm(f, f, 0x3232)};
-          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t y[4];
-            e2m1x8_to_f16x8(u[k], y);
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              y[h] = f16x2_mul(y[h], f2[k / 2]);
-              if constexpr (kWide) y[h] = f16x2_to_bf16x2(y[h], size);
-            }
-            cl.store(dst, n, k, y[0], y[1], y[2], y[3]);
-          }
-        }
-      };
-      if constexpr (kWide) {
-#pragma unroll 1
-        for (int n = 0; fills && n < kPer; ++n) {
-          x[0] = codes(n, b[0]);
-          mask(n, x[0], b[0]);
-          put(n, x[0], b[0]);
-        }
-      } else {
-#pragma unroll
-        for (int n = 0; n < kPer; ++n) {
-          if (!fills) break;
-          put(n, x[n], b[n]);
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();  // the warp has stored its part, and read its codes
-      copy_scales(i + kCSlots);
-      if (lane == 0) {
-        if (fills) mbar_arrive(bar(full + st));
-        if (i + kCSlots < n_pairs) {
-          issue_c(w, i + kCSlots);
-          if (l2_ahead > 0 && i + kCSlots + l2_ahead < n_pairs)
-            tma_prefetch_l2_2d(to_k ? &maps->k : &maps->v, j * Lay::kHead, (int32_t)(first_slot + (int64_t)(i + kCSlots + l2_ahead) * kPair + part * kPart));
-          issued = i + kCSlots + 1;
-        }
-      }
-    }
-    };
-    // (a loop for each)
-    if (wide_top) all_parts(std::true_type{});
-    else all_parts(std::false_type{});
-    // never leave with a copy in flight
-    if constexpr (BITS == 4) cp_async_wait<0>();
-    if (lane == 0) {
-      for (int i = seen; i < issued; ++i) {
-        const uint64_t t_start = globaltimer_ns();
-        while (!mbar_try_wait(bar(kBarCFull + w * kCSlots + i % kCSlots), (i / kCSlots) & 1)) {
-          if (globaltimer_ns() - t_start > kWaitLimitNs) {
-            atomicCAS(p.err, 0, kDevTimeout);
-            break;
-          }
-        }
-      }
-    }
-  } else if (warp == kWarpTmaK) {
-    // ---------------- TMA loads of K (8 bits) ----------------
-    if (BITS == 8 && lane == 0) {
-      int issued = slab_ok ? min(n_pairs, kKSlots) : 0;
-      for (int i = issued; slab_ok && i < n_pairs; ++i) {
-        if (!mbar_wait_bounded(bar(kBarKEmpty + i % kKSlots), ((i / kKSlots) - 1) & 1, abort_flag, p.err, kDevTimeout,
-                               kWaitLimitNs))
-          break;
-        issue_k(i);
-        if (l2_ahead > 0 && i + l2_ahead < n_pairs)
-          tma_prefetch_l2_2d(&maps->k, j * D, (int32_t)(first_slot + (int64_t)(i + l2_ahead) * kPair));
-        issued = i + 1;
-      }
-      // never leave with a copy in flight
-      for (int i = max(0, issued - kKSlots); i < issued; ++i) {
-        const uint64_t t_start = globaltimer_ns();
-        while (!mbar_try_wait(bar(kBarKFull + i % kKSlots), (i / kKSlots) & 1)) {
-          if (globaltimer_ns() - t_start > kWaitLimitNs) {
-            atomicCAS(p.err, 0, kDevTimeout);
-            break;
-          }
-        }
-      }
-    }
-  } else if (warp == kWarpS || warp == kWarpPv) {
-    // ---------------- MMA issuers ----------------
-    // The whole warp runs the loop and one elected lane issues: with the operands' descriptors uniform
-    // over the warp, an MMA is issued every 32 clocks; from inside a one-lane branch, every 45, which is
-    // more than these 128x64x32 products take.
-    if (!*abort_flag) {
-      constexpr uint32_t idS = idesc_fmt0_f32(kM, kN, false);
-      const bool el = elect_one();
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      auto wait = [&](int b, int slots, int i) {
-        const bool ok = mbar_wait_bounded(bar(b + i % slots), (i / slots) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
-        return __all_sync(0xffffffffu, ok) != 0;
-      };
-      int committed = 0;
-      if (warp == kWarpS) {
-        const uint64_t dk0 = smem_desc_sw128(sK, 16, 1024);
-        for (int i = 0; i < n_tiles; ++i) {
-          // S(i) overwrites S(i-5)/P(i-5), whose last reader is PV(i-5)
-          if (i >= kSBufs && !wait(kBarPvDone, kSBufs, i - kSBufs)) break;
-          if (i % kSlotTiles == 0 && !wait(kBarKFull, kKSlots, i / kSlotTiles)) break;
-          tc_fence_after();
-          const uint32_t dS = tm + (uint32_t)((i % kSBufs) * kN);
-          const int st = i / kSlotTiles % kKSlots;
-          const uint64_t dk = dk0 + (uint64_t)((st * Lay::kKSlotBytes + i % kSlotTiles * kN * 128) >> 4);  // rows of 128 bytes
-#pragma unroll
-          for (int kk = 0; kk < (BITS == 8 ? 8 : D / 16); ++kk)  // 8 bits: lo, the smaller, first; 4 bits: 16 dims each, four of a 64-dim half
-            if (el && BITS == 4)
-              umma_f16_ts(dS, tm + kColQ + kk * 8, dk + (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
-            else if (el)
-              umma_f8_ts(dS, tm + kColQ + (kk < 4 ? 32 : 0) + (kk & 3) * 8, dk + (uint64_t)(((kk & 3) * 32) >> 4), idS,
-                         kk > 0 ? 1u : 0u);
-          if (el) {
-            umma_commit(bar(kBarSFull + i % kSBufs));
-            if (i % kSlotTiles == kSlotTiles - 1) umma_commit(bar(kBarKEmpty + st));
-          }
-          __syncwarp();
-          committed += 1;
-        }
-      } else {
-        // V slot as an MN-major B operand: 16 tokens per step (2048 bytes), the two 64-dim halves
-        // kHalf apart (leading offset), 8-token groups 1024 bytes apart (stride)
-        const uint64_t dv0 = smem_desc_sw128(sV, kHalf, 1024);
-        auto all_products = [&](auto wide_span) {
+      auto all_parts = [&](auto wide_span) {
         constexpr bool kWide = decltype(wide_span)::value;
-        constexpr uint32_t idO = kWide ? idesc_bf16_f32(kM, D, true) : idesc_fmt0_f32(kM, D, true);
-        constexpr int kTerms = kWide ? 2 : 1;  // of P, 8 columns each for 16 tokens
-        for (int i = 0; i < n_tiles; ++i) {
-          if (i % kSlotTiles == 0 && !wait(kBarVFull, kVSlots, i / kSlotTiles)) break;
-          if (!wait(kBarPFull, kSBufs, i)) break;
-          tc_fence_after();
-          const uint32_t pa = tm + (uint32_t)((i % kSBufs) * kN);  // P(i): 32 columns, two tokens per column
-          const int st = i / kSlotTiles % kVSlots;
-          const uint64_t dv = dv0 + (uint64_t)((st * Lay::kSlot + i % kSlotTiles * (kN / 16) * 2048) >> 4);
-#pragma unroll
-          for (int ks = 0; ks < kN / 16 * kTerms; ++ks)
-            if (el)
-              umma_f16_ts(tm + kColO, pa + (uint32_t)(ks * 8), dv + (uint64_t)((ks / kTerms * 2048) >> 4), idO,
-                          (i > 0 || ks > 0) ? 1u : 0u);
-          if (el) {
-            umma_commit(bar(kBarPvDone + i % kSBufs));
-            if (i % kSlotTiles == kSlotTiles - 1) umma_commit(bar(kBarVEmpty + st));
+        for (int i = 0; slab_ok && i < n_pairs; ++i) {
+          const int c = w * kCSlots + i % kCSlots;
+          const int use = BITS == 8 ? i : 2 * i + part / kFill, st = use % slots;  // the slot's use, of all of the ring's
+          bool ok = mbar_wait_bounded(bar(kBarCFull + c), (i / kCSlots) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;  // the abort flag is up: every other role leaves as well
+          seen = i + 1;
+          if constexpr (BITS == 4) {
+            cp_async_wait<kCSlots - 1>();
+            __syncwarp();
           }
-          __syncwarp();
-          committed += 1;
+          const uint32_t src = sC + c * Lay::kCSlotBytes, dst = ring + st * Lay::kSlot;
+          const int valid = t1 - t0 - i * kPair - part * kPart;  // tokens of the part in range, or more
+          auto codes = [&](int n, uint32_t& b) {  // of load n, and (4 bits) their two scales
+            const uint32_t t = (uint32_t)(cl.token + n * Conv::kStep);
+            if constexpr (BITS == 4) b = lds16(src + kPart * Lay::kHead + t * Lay::kScale + cl.dim / 16);
+            return lds128(src + t * Lay::kHead + cl.dim * BITS / 8);
+          };
+          // 0 * whatever lies past the piece must not reach O
+          auto mask = [&](int n, uint4& x, uint32_t& b) {
+            if (cl.token + n * Conv::kStep >= valid) {
+              x = make_uint4(0u, 0u, 0u, 0u);
+              b = 0u;
+            }
+          };
+          uint4 x[kWide ? 1 : kPer];
+          uint32_t b[kWide ? 1 : kPer];
+          if constexpr (!kWide) {
+#pragma unroll
+            for (int n = 0; n < kPer; ++n) x[n] = codes(n, b[n]);
+            if (valid < kPart) {
+#pragma unroll
+              for (int n = 0; n < kPer; ++n) mask(n, x[n], b[n]);
+            }
+          }
+          const bool fills = BITS == 8 || use < n_tiles;  // (4 bits: the last two parts may have no tile)
+          if (fills && use >= slots) {
+            ok = mbar_wait_bounded(bar(empty + st), ((use / slots) - 1) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+          }
+          [[maybe_unused]] float size = 1.f;
+          if constexpr (kWide) size = v_size(2 * i + part / 2);
+          auto put = [&](int n, const uint4& x, uint32_t b) {
+            if constexpr (BITS == 8) {
+              uint32_t y[8];
+              e4m3x4_to_f16x4(x.x, y[0], y[1]);
+              e4m3x4_to_f16x4(x.y, y[2], y[3]);
+              e4m3x4_to_f16x4(x.z, y[4], y[5]);
+              e4m3x4_to_f16x4(x.w, y[6], y[7]);
+              if constexpr (kWide) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = f16x2_to_bf16x2(y[k], size);
+              }
+              cl.store(dst, n, 0, y[0], y[1], y[2], y[3]);
+              cl.store(dst, n, 1, y[4], y[5], y[6], y[7]);
+            } else {
+              const uint32_t f = e4m3x2_to_f16x2((uint16_t)b), f2[2] = {__byte_perm(f, f, 0x1010), __byte_perm(f, f, 0x3232)};
+              const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t y[4];
+                e2m1x8_to_f16x8(u[k], y);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                  y[h] = f16x2_mul(y[h], f2[k / 2]);
+                  if constexpr (kWide) y[h] = f16x2_to_bf16x2(y[h], size);
+                }
+                cl.store(dst, n, k, y[0], y[1], y[2], y[3]);
+              }
+            }
+          };
+          if constexpr (kWide) {
+#pragma unroll 1
+            for (int n = 0; fills && n < kPer; ++n) {
+              x[0] = codes(n, b[0]);
+              mask(n, x[0], b[0]);
+              put(n, x[0], b[0]);
+            }
+          } else {
+#pragma unroll
+            for (int n = 0; n < kPer; ++n) {
+              if (!fills) break;
+              put(n, x[n], b[n]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();  // the warp has stored its part, and read its codes
+          copy_scales(i + kCSlots);
+          if (lane == 0) {
+            if (fills) mbar_arrive(bar(full + st));
+            if (i + kCSlots < n_pairs) {
+              issue_c(w, i + kCSlots);
+              if (l2_ahead > 0 && i + kCSlots + l2_ahead < n_pairs)
+                tma_prefetch_l2_2d(to_k ? &maps->k : &maps->v, j * Lay::kHead,
+                                   (int32_t)(first_slot + (int64_t)(i + kCSlots + l2_ahead) * kPair + part * kPart));
+              issued = i + kCSlots + 1;
+            }
+          }
         }
-        };
-        if (*v_top) all_products(std::true_type{});
-        else all_products(std::false_type{});
+      };
+      // (a loop for each)
+      if (wide_top) all_parts(std::true_type{});
+      else all_parts(std::false_type{});
+      // never leave with a copy in flight
+      if constexpr (BITS == 4) cp_async_wait<0>();
+      if (lane == 0) {
+        for (int i = seen; i < issued; ++i) {
+          const uint64_t t_start = globaltimer_ns();
+          while (!mbar_try_wait(bar(kBarCFull + w * kCSlots + i % kCSlots), (i / kCSlots) & 1)) {
+            if (globaltimer_ns() - t_start > kWaitLimitNs) {
+              atomicCAS(p.err, 0, kDevTimeout);
+              break;
+            }
+          }
+        }
       }
-      // drain: every tcgen05 op the elected lane issued completes before the CTA frees TMEM
-      if (committed > 0 && el) {
-        const uint32_t drain = bar(kBarDrain + (warp == kWarpS ? 0 : 1));
-        umma_commit(drain);
-        const uint64_t t_start = globaltimer_ns();
-        while (!mbar_try_wait(drain, 0)) {
-          if (globaltimer_ns() - t_start > kWaitLimitNs) {
-            atomicCAS(p.err, 0, kDevTimeout);
+    } else if (warp == kWarpTmaK) {
+      // ---------------- TMA loads of K (8 bits) ----------------
+      if (BITS == 8 && lane == 0) {
+        int issued = slab_ok ? min(n_pairs, kKSlots) : 0;
+        for (int i = issued; slab_ok && i < n_pairs; ++i) {
+          if (!mbar_wait_bounded(bar(kBarKEmpty + i % kKSlots), ((i / kKSlots) - 1) & 1, abort_flag, p.err, kDevTimeout,
+                                 kWaitLimitNs))
             break;
+          issue_k(i);
+          if (l2_ahead > 0 && i + l2_ahead < n_pairs)
+            tma_prefetch_l2_2d(&maps->k, j * D, (int32_t)(first_slot + (int64_t)(i + l2_ahead) * kPair));
+          issued = i + 1;
+        }
+        // never leave with a copy in flight
+        for (int i = max(0, issued - kKSlots); i < issued; ++i) {
+          const uint64_t t_start = globaltimer_ns();
+          while (!mbar_try_wait(bar(kBarKFull + i % kKSlots), (i / kKSlots) & 1)) {
+            if (globaltimer_ns() - t_start > kWaitLimitNs) {
+              atomicCAS(p.err, 0, kDevTimeout);
+              break;
+            }
+          }
+        }
+      }
+    } else if (warp == kWarpS || warp == kWarpPv) {
+      // ---------------- MMA issuers ----------------
+      // The whole warp runs the loop and one elected lane issues: with the operands' descriptors uniform
+      // over the warp, an MMA is issued every 32 clocks; from inside a one-lane branch, every 45, which is
+      // more than these 128x64x32 products take.
+      if (!*abort_flag) {
+        constexpr uint32_t idS = idesc_fmt0_f32(kM, kN, false);
+        const bool el = elect_one();
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        auto wait = [&](int b, int slots, int i) {
+          const bool ok = mbar_wait_bounded(bar(b + i % slots), (i / slots) & 1, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
+          return __all_sync(0xffffffffu, ok) != 0;
+        };
+        int committed = 0;
+        if (warp == kWarpS) {
+          const uint64_t dk0 = smem_desc_sw128(sK, 16, 1024);
+          for (int i = 0; i < n_tiles; ++i) {
+            // S(i) overwrites S(i-5)/P(i-5), whose last reader is PV(i-5)
+            if (i >= kSBufs && !wait(kBarPvDone, kSBufs, i - kSBufs)) break;
+            if (i % kSlotTiles == 0 && !wait(kBarKFull, kKSlots, i / kSlotTiles)) break;
+            tc_fence_after();
+            const uint32_t dS = tm + (uint32_t)((i % kSBufs) * kN);
+            const int st = i / kSlotTiles % kKSlots;
+            const uint64_t dk = dk0 + (uint64_t)((st * Lay::kKSlotBytes + i % kSlotTiles * kN * 128) >> 4);  // rows of 128 bytes
+#pragma unroll
+            // 8 bits: lo, the smaller, first; 4 bits: 16 dims each, four of a 64-dim half
+            for (int kk = 0; kk < (BITS == 8 ? 8 : D / 16); ++kk)
+              if (el && BITS == 4)
+                umma_f16_ts(dS, tm + kColQ + kk * 8, dk + (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
+              else if (el)
+                umma_f8_ts(dS, tm + kColQ + (kk < 4 ? 32 : 0) + (kk & 3) * 8, dk + (uint64_t)(((kk & 3) * 32) >> 4), idS,
+                           kk > 0 ? 1u : 0u);
+            if (el) {
+              umma_commit(bar(kBarSFull + i % kSBufs));
+              if (i % kSlotTiles == kSlotTiles - 1) umma_commit(bar(kBarKEmpty + st));
+            }
+            __syncwarp();
+            committed += 1;
+          }
+        } else {
+          // V slot as an MN-major B operand: 16 tokens per step (2048 bytes), the two 64-dim halves
+          // kHalf apart (leading offset), 8-token groups 1024 bytes apart (stride)
+          const uint64_t dv0 = smem_desc_sw128(sV, kHalf, 1024);
+          auto all_products = [&](auto wide_span) {
+            constexpr bool kWide = decltype(wide_span)::value;
+            constexpr uint32_t idO = kWide ? idesc_bf16_f32(kM, D, true) : idesc_fmt0_f32(kM, D, true);
+            constexpr int kTerms = kWide ? 2 : 1;  // of P, 8 columns each for 16 tokens
+            for (int i = 0; i < n_tiles; ++i) {
+              if (i % kSlotTiles == 0 && !wait(kBarVFull, kVSlots, i / kSlotTiles)) break;
+              if (!wait(kBarPFull, kSBufs, i)) break;
+              tc_fence_after();
+              const uint32_t pa = tm + (uint32_t)((i % kSBufs) * kN);  // P(i): 32 columns, two tokens per column
+              const int st = i / kSlotTiles % kVSlots;
+              const uint64_t dv = dv0 + (uint64_t)((st * Lay::kSlot + i % kSlotTiles * (kN / 16) * 2048) >> 4);
+#pragma unroll
+              for (int ks = 0; ks < kN / 16 * kTerms; ++ks)
+                if (el)
+                  umma_f16_ts(tm + kColO, pa + (uint32_t)(ks * 8), dv + (uint64_t)((ks / kTerms * 2048) >> 4), idO,
+                              (i > 0 || ks > 0) ? 1u : 0u);
+              if (el) {
+                umma_commit(bar(kBarPvDone + i % kSBufs));
+                if (i % kSlotTiles == kSlotTiles - 1) umma_commit(bar(kBarVEmpty + st));
+              }
+              __syncwarp();
+              committed += 1;
+            }
+          };
+          if (*v_top) all_products(std::true_type{});
+          else all_products(std::false_type{});
+        }
+        // drain: every tcgen05 op the elected lane issued completes before the CTA frees TMEM
+        if (committed > 0 && el) {
+          const uint32_t drain = bar(kBarDrain + (warp == kWarpS ? 0 : 1));
+          umma_commit(drain);
+          const uint64_t t_start = globaltimer_ns();
+          while (!mbar_try_wait(drain, 0)) {
+            if (globaltimer_ns() - t_start > kWaitLimitNs) {
+              atomicCAS(p.err, 0, kDevTimeout);
+              break;
+            }
           }
         }
       }
     }
-  }
-  if constexpr (Lay::kSplitRegs) {
-    // (between the two barriers the softmax warps give back what they took)
-    __syncwarp();
-    block_barrier<Lay::kThreads>();
-    block_barrier<Lay::kThreads>();
-    regs_up<96>();
-  }
+    if constexpr (Lay::kSplitRegs) {
+      // (between the two barriers the softmax warps give back what they took)
+      __syncwarp();
+      block_barrier<Lay::kThreads>();
+      block_barrier<Lay::kThreads>();
+      regs_up<96>();
+    }
   } else {
     if constexpr (Lay::kSplitRegs) regs_up<128>();
     // ---------------- softmax warps 0-7: rows of quarter `quad`, tiles of parity `par` ----------------
@@ -901,7 +906,8 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
                 x[2 * k] = *reinterpret_cast<const uint32_t*>(&hi);
                 x[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&lo);
               }
-              const uint32_t parts[16] = {x[0], x[2], x[4], x[6], x[8], x[10], x[12], x[14], x[1], x[3], x[5], x[7], x[9], x[11], x[13], x[15]};
+              const uint32_t parts[16] = {x[0], x[2], x[4], x[6], x[8], x[10], x[12], x[14],
+                                          x[1], x[3], x[5], x[7], x[9], x[11], x[13], x[15]};
               tmem_st16(ts + c * 16, parts);
             }
           } else {
@@ -990,7 +996,7 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
           st_record8(dst + c * 8, x, keep);
         }
         if (half == 0) {
-          st_record(p.rec_lse + (int64_t)rec * p.n_q + h, kv8_record_lse(lt, (top + log2f(lt)) * kLn2), keep);
+          st_record(p.rec_lse + (int64_t)rec * p.n_q + h, packed_record_lse(lt, (top + log2f(lt)) * kLn2), keep);
         }
       }
     }

@@ -294,7 +294,7 @@ __device__ __forceinline__ void packed_generic_run(const AttnParams& p, int32_t 
     const float inv = total == 0.f ? 0.f : 1.f / total;
 #pragma unroll
     for (int c = 0; c < VPL; ++c) p.rec_o[at * d + lane + 32 * c] = o[c] * inv;
-    if (lane == 0) p.rec_lse[at] = kv8_record_lse(total, (base + log2f(total)) * kLn2);
+    if (lane == 0) p.rec_lse[at] = packed_record_lse(total, (base + log2f(total)) * kLn2);
   }
 }
 

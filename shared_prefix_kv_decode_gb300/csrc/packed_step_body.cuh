@@ -19,7 +19,7 @@ static_assert(pks::kThreads <= pkd::Layout<8, 128>::kThreads && pks::kThreads <=
 // KV-head group only): suffix work the plan gives the dense CTAs for after their prefix piece.
 template <int BITS, int D>
 __global__ void __launch_bounds__(pkd::Layout<BITS, D>::kThreads, 1)
-    packed_step_kernel(AttnParams p, int32_t first_dense, int32_t n_dense, const __grid_constant__ pkd::Maps maps,
+    packed_step_kernel(AttnParams p, int32_t first_dense, int32_t n_dense, const __grid_constant__ PackedMaps maps,
                        const int32_t* __restrict__ cta_begin, int32_t n_scta, int32_t n_tail) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
   const int32_t c = (int32_t)blockIdx.x;
@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(pks::kThreads, 1) packed_suffix_kernel(AttnPar
 }
 
 template <int BITS, int D>
-cudaError_t launch_packed_step(const AttnParams& p, int32_t first_dense, int32_t n_dense, const pkd::Maps& maps,
+cudaError_t launch_packed_step(const AttnParams& p, int32_t first_dense, int32_t n_dense, const PackedMaps& maps,
                                const int32_t* cta_begin, int32_t n_scta, int32_t n_tail, cudaStream_t s, bool pdl) {
   const int32_t groups = (p.n_kv + pks::kWarps - 1) / pks::kWarps;
   const int64_t n = (int64_t)n_dense + (int64_t)n_scta * groups;

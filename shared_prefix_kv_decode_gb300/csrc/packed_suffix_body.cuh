@@ -593,8 +593,8 @@ __device__ __forceinline__ void packed_suffix_body(const AttnParams& p, const in
     }
     if (lane < 4) {
       float* ldst = p.rec_lse + (int64_t)rec * p.n_q + hq0;
-      if (w0) st_record(ldst, kv8_record_lse(l0, (m0 - kSumShift + log2f(l0)) * kLn2), keep);
-      if (w1) st_record(ldst + 1, kv8_record_lse(l1, (m1 - kSumShift + log2f(l1)) * kLn2), keep);
+      if (w0) st_record(ldst, packed_record_lse(l0, (m0 - kSumShift + log2f(l0)) * kLn2), keep);
+      if (w1) st_record(ldst + 1, packed_record_lse(l1, (m1 - kSumShift + log2f(l1)) * kLn2), keep);
     }
   }
 }
