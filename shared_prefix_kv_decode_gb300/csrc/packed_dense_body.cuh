@@ -36,7 +36,7 @@
 // scale becomes 2^90, what lies 2^216 below it 0), and P has the significand of vs alone: P = 2^(z - m - 8) as the sum of two
 // bf16 values (16 bits, at most 1, down to 2^-118 of the largest weight), over all of S, in twice the products, with small
 // loops, so that the others' instructions stay close: unrolled as those are they cost every piece 3 to 4 %.  With every
-// eighth block of V zero the step of a 16K prefix with 64 requests takes 56 us (8 bits 51) instead of 35 (31).
+// eighth block of V zero the step of a 16K prefix with 64 requests takes 56 us (8 bits 51) instead of 34 (31).
 // Elsewhere P is one fp16 value, 11 bits: a weight below 2^-13 of the piece's largest may be off by 2^-24 of that.  The rounding,
 // 2^-12.8 of a weight on average, moves about 2 % of the bf16 results to a neighbour (8e-4 of them in the root mean square, where
 // their own rounding is 1.7e-3): chosen, since a second part would double the products with P and put a subtraction, a
@@ -66,8 +66,8 @@
 // 64 requests 37.4 us, so 36.7).
 // The conversion warps go ahead from the first barrier on, beside q's way to TMEM (one request on 8K 11.2 us, so 10.8).
 // What bounds it: the softmax warps' rounds, next to the conversion on the same issue slots and the same shared memory.
-// 480 requests on a slab of 8K (32/8 heads of 128, two waves of CTAs) take 75 us, in 8 bits 64.  With parts taken out: the
-// products 73.6, three quarters of the conversion's products and stores 69.7, both 67.7; the exponentials, the maxima or the row
+// 480 requests on a slab of 8K (32/8 heads of 128, two waves of CTAs) take 73.8 us, in 8 bits 64.  With parts taken out (of 75 us,
+// before wide pieces had loops of their own): the products 73.6, three quarters of the conversion's products and stores 69.7, both 67.7; the exponentials, the maxima or the row
 // sums 1 to 2 % each, the scales' loads nothing.  Codes and scales of all conversion warps fetched by two warps of their own, in
 // boxes of 128 rows: 77.
 #pragma once
@@ -779,15 +779,15 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
     const int pair_bar = kBarPair + quad;           // mbarrier of the two warps sharing rows
     float* mpub = reinterpret_cast<float*>(smem + kOffMPub) + quad * 64;  // [tile parity][lane]
     const float scale = p.scale_log2 * units[r];
-    float m_own = -INFINITY;   // max (of z, base 2) used for this warp's latest tile
-    float l = 0.f;             // this warp's share of the row sum, over 2^(m_own - (shift + least))
-    bool ok = !*abort_flag;
-    const int wide_top = (int)*v_top;
-    // log2 of the piece's smallest V scale; wide: P has no power of two of V's scales
-    const float least = wide_top ? 0.f : BITS == 8 ? lg2_approx(__uint_as_float(*v_least)) : (float)((int)(*v_least >> 23) - 127);
-    // (a loop for each: in one loop the untaken branch cost 2 % of a 16K prefix)
+    // (a loop and an epilogue for each: in one loop the untaken branch cost 2 % of a 16K prefix, with the epilogue in common
+    // heads of 64 took 36.4 us where they take 33.8)
     auto all_tiles = [&](auto wide_span) {
       constexpr bool kWide = decltype(wide_span)::value;
+      float m_own = -INFINITY;   // max (of z, base 2) used for this warp's latest tile
+      float l = 0.f;             // this warp's share of the row sum, over 2^(m_own - (shift + least))
+      bool ok = !*abort_flag;
+      // log2 of the piece's smallest V scale; wide: P has no power of two of V's scales
+      const float least = kWide ? 0.f : BITS == 8 ? lg2_approx(__uint_as_float(*v_least)) : (float)((int)(*v_least >> 23) - 127);
       for (int i = par; ok && i < n_tiles; i += 2) {
         const int sb = i % kSBufs;
         // (from the smallest normal number to the largest: 0 * -inf of a masked key and inf * 0 of a score would be NaN)
@@ -935,71 +935,84 @@ __device__ __forceinline__ void packed_dense_body(const AttnParams& p, int32_t i
         tc_fence_before();
         mbar_arrive(bar(kBarPFull + sb));
       }
-    };
-    if (wide_top) all_tiles(std::true_type{});
-    else all_tiles(std::false_type{});
-    // epilogue: wait for the last PV, combine the two warps' row sums (each with its exponent), normalise
-    // (O is relative to the last tile's max), write the record
-    if (ok) {
-      const int last = n_tiles - 1;
-      ok = mbar_wait_bounded(bar(kBarPvDone + last % kSBufs), (last / kSBufs) & 1, abort_flag, p.err, kDevTimeout,
-                             kWaitLimitNs);
-    }
-    ok = __all_sync(0xffffffffu, ok);
-    // swap the row sums, exponents and maxima with the other warp at the pair barrier; a warp that left the
-    // tile loop early may stop waiting for published maxima, so its partner's bounded waits give
-    // up and both skip the record
-    // (they go into the rings of the first kFill conversion warps.  Those have read all their codes once the last PV is done:
-    // their parts belong to the first tile of each content, which some product waited for.  The other parts' last
-    // content may have no tile, and its copies may still be landing.  A CTA that gave up may have copies in flight
-    // in any ring, and writes nothing)
-    const bool safe = ok;
-    const int top_exp = (int)*v_top;
-    const float shift = top_exp ? kWideShift : kShift;
-    if (safe) {
-      red[par * kM + r] = l;
-      red[2 * kM + par * kM + r] = m_own - (shift + least);
-      red[4 * kM + par * kM + r] = m_own;
-    }
-    mbar_arrive(bar(pair_bar));
-    const bool pair_ok = mbar_wait_bounded(bar(pair_bar), 0, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
-    ok = __all_sync(0xffffffffu, pair_ok) && ok && !*abort_flag;
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok) {
-      tc_fence_after();
-      const float l0 = red[r], l1 = red[kM + r], e0 = red[2 * kM + r], e1 = red[3 * kM + r];
-      const float m_used = red[4 * kM + ((n_tiles - 1) & 1) * kM + r];
-      const float top = fmaxf(e0, e1);
-      // a warp that had no tile left 0 and -inf
-      const float lt = l0 * ex2_approx(e0 - top) + l1 * ex2_approx(e1 - top);
-      if (row < rows && (rec < 0 || rec >= p.n_records)) {
-        if (half == 0) atomicCAS(p.err, 0, (int32_t)kDevBadRecord);
-        rec = -1;
+      // epilogue: wait for the last PV, combine the two warps' row sums (each with its exponent), normalise
+      // (O is relative to the last tile's max), write the record
+      if (ok) {
+        const int last = n_tiles - 1;
+        ok = mbar_wait_bounded(bar(kBarPvDone + last % kSBufs), (last / kSBufs) & 1, abort_flag, p.err, kDevTimeout,
+                               kWaitLimitNs);
       }
-      // (a tile has a valid token); wide: V's operands back to their size, by half of the power of two each
-      const int size = top_exp ? top_exp - 127 - kWideTop : 0, half_size = size >> 1;
-      const float inv = 1.f / lt * __uint_as_float((uint32_t)(127 + half_size) << 23);
-      const float unit = ex2_approx(m_used - shift - top) * __uint_as_float((uint32_t)(127 + size - half_size) << 23);
-      uint32_t u[D / 64][32];
-      GRANIKV_TMEM_LD32(tmem + lane_off + kColO + half * (D / 2), u[0]);
-      if constexpr (D == 128) GRANIKV_TMEM_LD32(tmem + lane_off + kColO + half * 64 + 32, u[1]);
-      tmem_wait_ld();
-      // every lane stores its half row, a whole 32-byte sector at a time
-      if (rec >= 0) {
+      ok = __all_sync(0xffffffffu, ok);
+      // swap the row sums, exponents and maxima with the other warp at the pair barrier; a warp that left the
+      // tile loop early may stop waiting for published maxima, so its partner's bounded waits give
+      // up and both skip the record
+      // (they go into the rings of the first kFill conversion warps.  Those have read all their codes once the last PV is done:
+      // their parts belong to the first tile of each content, which some product waited for.  The other parts' last
+      // content may have no tile, and its copies may still be landing.  A CTA that gave up may have copies in flight
+      // in any ring, and writes nothing)
+      const bool safe = ok;
+      constexpr float shift = kWide ? kWideShift : kShift;
+      if (safe) {
+        red[par * kM + r] = l;
+        red[2 * kM + par * kM + r] = m_own - (shift + least);
+        red[4 * kM + par * kM + r] = m_own;
+      }
+      mbar_arrive(bar(pair_bar));
+      const bool pair_ok = mbar_wait_bounded(bar(pair_bar), 0, abort_flag, p.err, kDevTimeout, kWaitLimitNs);
+      ok = __all_sync(0xffffffffu, pair_ok) && ok && !*abort_flag;
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        tc_fence_after();
+        const float l0 = red[r], l1 = red[kM + r], e0 = red[2 * kM + r], e1 = red[3 * kM + r];
+        const float m_used = red[4 * kM + ((n_tiles - 1) & 1) * kM + r];
+        const float top = fmaxf(e0, e1);
+        // a warp that had no tile left 0 and -inf
+        const float lt = l0 * ex2_approx(e0 - top) + l1 * ex2_approx(e1 - top);
+        if (row < rows && (rec < 0 || rec >= p.n_records)) {
+          if (half == 0) atomicCAS(p.err, 0, (int32_t)kDevBadRecord);
+          rec = -1;
+        }
+        // (a tile has a valid token); wide: V's operands back to their size, by half of the power of two each
+        const int size = kWide ? (int)*v_top - 127 - kWideTop : 0, half_size = size >> 1;
+        const float inv = 1.f / lt * __uint_as_float((uint32_t)(127 + half_size) << 23);
+        const float unit = ex2_approx(m_used - shift - top) * __uint_as_float((uint32_t)(127 + size - half_size) << 23);
+        // every lane stores its half row, a whole 32-byte sector at a time
         const uint64_t keep = l2_policy_keep();
+        const uint32_t cols = tmem + lane_off + kColO + half * (D / 2);
         float* dst = p.rec_o + ((int64_t)rec * p.n_q + h) * D + half * (D / 2);
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
+        auto store8 = [&](const uint32_t* u, int at) {
           float x[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(u[c >> 2][(c & 3) * 8 + k]) * inv * unit;
-          st_record8(dst + c * 8, x, keep);
+          for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(u[k]) * inv * unit;
+          st_record8(dst + at, x, keep);
+        };
+        if constexpr (kWide) {
+#pragma unroll 1
+          for (int c = 0; c < D / 2; c += 16) {
+            uint32_t u[16];
+            tmem_ld16(cols + c, u);
+            tmem_wait_ld();
+            if (rec >= 0) {
+              store8(u, c);
+              store8(u + 8, c + 8);
+            }
+          }
+        } else {
+          uint32_t u[D / 64][32];
+          GRANIKV_TMEM_LD32(cols, u[0]);
+          if constexpr (D == 128) GRANIKV_TMEM_LD32(cols + 32, u[1]);
+          tmem_wait_ld();
+          if (rec >= 0) {
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) store8(u[c >> 2] + (c & 3) * 8, c * 8);
+          }
         }
-        if (half == 0) {
+        if (rec >= 0 && half == 0)
           st_record(p.rec_lse + (int64_t)rec * p.n_q + h, packed_record_lse(lt, (top + log2f(lt)) * kLn2), keep);
-        }
       }
-    }
+    };
+    if (__builtin_expect(*v_top == 0u, 1)) all_tiles(std::false_type{});
+    else all_tiles(std::true_type{});
     if constexpr (Lay::kSplitRegs) {
       __syncwarp();
       block_barrier<Lay::kThreads>();
