@@ -124,6 +124,52 @@ def test_values_beside_zero_blocks_in_long_pieces(cuda_ok, bits, d, zero):
     _check(c, o[rows], lse[rows], f"{bits} bits, zeros {zero}")
 
 
+def _far_apart(kind, k, v):
+    if kind == "prefix":
+        v[64:128] *= np.float32(2.0 ** 40)
+        v[192:] *= np.float32(2.0 ** -40)
+
+
+@pytest.mark.parametrize("bits,d", [(8, 128), (4, 128), (4, 64)])
+@pytest.mark.parametrize("block", [0, 1, 3])
+def test_nan_beside_blocks_far_apart(cuda_ok, bits, d, block):
+    """A NaN in V stays with its columns (4 bits: the 16 of its scale), one in K or q with the heads that meet it."""
+    torch = _torch()
+    t = 64 * block + 9
+
+    def case(edit):
+        return CACHES[bits](np.random.default_rng([bits, d, 9]), n_q=16, n_kv=4, d=d, dtype="bf16", prefixes=[300], of=[0, 0, -1], lens=[0, 20, 7],
+                            edit=lambda kind, k, v: (_far_apart(kind, k, v), edit(kind, k, v)))
+
+    plain = case(lambda kind, k, v: None)
+    o, lse = plain.decode()
+    _check(plain, o, lse, "without")
+
+    def bad(name):
+        def edit(kind, k, v):
+            if kind == "prefix":
+                (k if name == "k" else v)[t, 1, 37] = np.nan
+        return edit
+
+    o2, lse2 = case(bad("v")).decode()
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    hit[:2, 4:8, slice(32, 48) if bits == 4 else 37] = True
+    assert torch.equal(torch.isnan(o2), hit) and not torch.isnan(lse2).any()
+    o2, lse2 = case(bad("k")).decode()
+    hit = torch.zeros_like(lse, dtype=torch.bool)
+    hit[:2, 4:8] = True
+    assert torch.equal(torch.isnan(lse2), hit) and torch.equal(torch.isnan(o2), hit[..., None].expand_as(o2))
+    assert torch.equal(o2[~hit], o[~hit]) and torch.equal(lse2[~hit], lse[~hit])
+    for x in (float("nan"), float("inf"), -float("inf")):
+        c = case(lambda kind, k, v: None)
+        c.q[1, 6, 5] = x
+        o2, lse2 = c.decode()
+        hit = torch.zeros_like(lse, dtype=torch.bool)
+        hit[1, 6] = True
+        assert torch.equal(torch.isnan(lse2), hit) and torch.equal(torch.isnan(o2), hit[..., None].expand_as(o2))
+        assert torch.equal(o2[~hit], o[~hit]) and torch.equal(lse2[~hit], lse[~hit])
+
+
 # ---- factors of scores beyond fp32 --------------------------------------------------------------
 
 @pytest.mark.parametrize("bits,n_q,n_kv,d,dtype", [(8, 32, 8, 128, "bf16"), (4, 32, 8, 128, "bf16"), (4, 32, 8, 64, "bf16"),
